@@ -86,6 +86,94 @@ int moe_gdr_backward(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, co
                      float* dq, float* d_k, float* d_v, float* dbeta, float* dg, float* dS0,
                      void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/* ---------------------------------------------------------------- queries and keys
+ * Root-mean-square norm of every query and key head with the rotation by the token's position
+ * in the same pass ("Fine-Tuning Trillion-Parameter Sparse MoE Models: Challenges and
+ * Engineering Practices", section 5, fuses the normalization coefficients into the
+ * linear-attention kernels): what stands between the projections and moe_gdr_forward.  For
+ * every token t and head h, over the head's D values,
+ *
+ *   n = w * x / sqrt(mean(x^2) + eps)
+ *   (y_a, y_b) = (n_a cos th_i - n_b sin th_i,  n_b cos th_i + n_a sin th_i),
+ *   th_i = positions[t] * inv_freq[i],   0 <= i < rotary_dim / 2,
+ *
+ * where pair i is (a, b) = (i, i + rotary_dim / 2), or (2 i, 2 i + 1) if `interleaved` is not
+ * zero; values from rotary_dim on are normed only.  th_i is formed in 64 bits and reduced to a
+ * fraction of a turn before its sine and cosine are taken in fp32, so far positions lose
+ * nothing.
+ *
+ * Supported (else MOE_ERR_UNSUPPORTED): D a multiple of 8, at most 256; rotary_dim a multiple
+ * of 16, at most D, 0 for no rotation (positions and inv_freq may then be NULL); pointers
+ * 16-byte aligned; strides multiples of 8 values.  eps > 0.  Heads are addressed by strides (in
+ * values), so q and k can be parts of one fused projection row; token t's head h starts at
+ * t * token_stride + h * head_stride.  Input strides may be 0 (broadcast); rows of an output
+ * must not overlap (MOE_ERR_INVALID_ARG).  y may be x, with the same strides, and dx may be x
+ * or dy (of the same type, with the same strides); other overlaps of inputs and outputs give
+ * undefined values. */
+enum moe_dtype {
+  MOE_BF16 = 0,
+  MOE_F32 = 1
+};
+
+typedef struct moe_qk_rows {
+  const void* x;                          /* [N, heads, D] by strides */
+  int64_t x_token_stride, x_head_stride;
+  void* y;                                /* [N, heads, D] by strides */
+  int64_t y_token_stride, y_head_stride;
+  const float* weight;                    /* [D], or [heads, D] if weight_per_head; NULL: ones */
+  int32_t weight_per_head;
+  int32_t heads;
+} moe_qk_rows;
+
+typedef struct moe_qk_grads {
+  const void* x;                          /* the forward's input */
+  int64_t x_token_stride, x_head_stride;
+  const void* dy;                         /* gradient of y, of type dy_dtype */
+  int64_t dy_token_stride, dy_head_stride;
+  void* dx;                               /* overwritten, of x's type */
+  int64_t dx_token_stride, dx_head_stride;
+  const float* weight;
+  float* dweight;                         /* overwritten, shaped as weight; NULL: not wanted */
+  int32_t weight_per_head;
+  int32_t heads;
+} moe_qk_grads;
+
+/* q and k: the two groups of heads, which share the positions (one launch); k may be NULL.
+ * positions [N] int32 (any sign), inv_freq [rotary_dim / 2] fp64, both on the device.  dtype:
+ * the type of x and y (a moe_dtype). */
+int moe_qk_norm_rope(int32_t N, int32_t D, int32_t rotary_dim, int32_t interleaved,
+                     int32_t dtype, float eps, const int32_t* positions, const double* inv_freq,
+                     const moe_qk_rows* q, const moe_qk_rows* k, moe_stream_t stream);
+
+/* Backward: dx and the weight gradients of <dy, y> (two launches; one if no weight gradient is
+ * wanted).  The norm is formed again from x.  dy_dtype: MOE_F32 (what moe_gdr_backward writes)
+ * or dtype.  Deterministic: every reduction runs in a fixed order. */
+size_t moe_qk_norm_rope_backward_workspace_size(int32_t N, int32_t D, int32_t q_heads,
+                                                int32_t k_heads);
+int moe_qk_norm_rope_backward(int32_t N, int32_t D, int32_t rotary_dim, int32_t interleaved,
+                              int32_t dtype, int32_t dy_dtype, float eps,
+                              const int32_t* positions, const double* inv_freq,
+                              const moe_qk_grads* q, const moe_qk_grads* k, void* workspace,
+                              size_t workspace_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- one token
+ * One step of the gated delta rule for B requests, each of one token: the state of request b
+ * is row slot[b] of S [n_slots, H, dv, dk] fp32, updated in place,
+ *
+ *   S <- exp(g) S (I - beta k^ k^T) + beta v k^T,   o = scale * S q^,
+ *
+ * with q, k [B, H, dk], v [B, H, dv], o [B, H, dv] bf16 and beta, g [B, H] fp32 (types, norms
+ * and zero rows as in moe_gdr_forward, whose S_T is a state to go on from).  slot [B] int32, or
+ * NULL: request b has row b (then B <= n_slots).  slot[b] = -1 marks a padding row: it is
+ * skipped and its o left as it was.  Any other value outside [0, n_slots) and every later
+ * request with an earlier one's slot is skipped the same way and reported as MOE_ERR_BAD_INDEX
+ * in *dev_status (may be NULL).  The products are plain fp32; deterministic.  q, k, v, o and S
+ * must be 16-byte aligned, dk and dv in {64, 128}, else MOE_ERR_UNSUPPORTED. */
+int moe_gdr_step(int32_t B, int32_t H, int32_t dk, int32_t dv, const moe_bf16* q,
+                 const moe_bf16* k, const moe_bf16* v, const float* beta, const float* g,
+                 const int32_t* slot, int32_t n_slots, float scale, float* S, moe_bf16* o,
+                 int32_t* dev_status, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -411,7 +411,13 @@ enum moe_kernel_id {
   MOE_KERNEL_DISPATCH_ROUTE_BWD = 13, /* dx from dx_perm and the router path      */
   MOE_KERNEL_GDR_BWD_FACTORS = 14, /* linear attention backward: chunk factors again */
   MOE_KERNEL_GDR_BWD_SCAN = 15, /* linear attention backward: state-gradient scan  */
-  MOE_KERNEL_COUNT = 16
+  MOE_KERNEL_QK_NORM_ROPE = 16, /* norm and rotation of queries and keys          */
+  MOE_KERNEL_QK_NORM_ROPE_BWD = 17, /* its backward (with the weight gradients)   */
+  MOE_KERNEL_GDR_STEP = 18,     /* gated delta rule: one token                    */
+  MOE_KERNEL_GLR_FWD = 19,      /* gated linear recurrence: forward               */
+  MOE_KERNEL_GLR_BWD = 20,      /* gated linear recurrence: backward              */
+  MOE_KERNEL_GLR_STEP = 21,     /* gated linear recurrence: one token             */
+  MOE_KERNEL_COUNT = 22
 };
 int moe_set_kernel_events(int kernel_id, void* event_before, void* event_after);
 long long moe_launch_count(void);

@@ -1,4 +1,4 @@
-"""ctypes binding of libmoe.so (the C ABI in include/moe.h).
+"""ctypes binding of libmoe.so (the C ABI in include/*.h).
 
 Each ``moe_*`` function here has the name and the argument order of the C entry point and
 only marshals arguments: torch tensors become device pointers, the problem becomes a
@@ -22,8 +22,12 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 c_i32 = ctypes.c_int32
+c_i64 = ctypes.c_int64
 c_vp = ctypes.c_void_p
 c_sz = ctypes.c_size_t
+
+MOE_BF16, MOE_F32 = 0, 1          # moe_dtype
+MOE_GLR_ADD, MOE_GLR_MIX = 0, 1   # moe_glr_mode
 
 MOE_OK = 0
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
@@ -53,6 +57,20 @@ class moe_lora_grad(ctypes.Structure):
 
 class moe_ffn_saved(ctypes.Structure):
     _fields_ = [(n, c_vp) for n in ("a_gate", "a_up", "u_gate", "u_up", "u_down")]
+
+
+class moe_qk_rows(ctypes.Structure):
+    _fields_ = [("x", c_vp), ("x_token_stride", c_i64), ("x_head_stride", c_i64),
+                ("y", c_vp), ("y_token_stride", c_i64), ("y_head_stride", c_i64),
+                ("weight", c_vp), ("weight_per_head", c_i32), ("heads", c_i32)]
+
+
+class moe_qk_grads(ctypes.Structure):
+    _fields_ = [("x", c_vp), ("x_token_stride", c_i64), ("x_head_stride", c_i64),
+                ("dy", c_vp), ("dy_token_stride", c_i64), ("dy_head_stride", c_i64),
+                ("dx", c_vp), ("dx_token_stride", c_i64), ("dx_head_stride", c_i64),
+                ("weight", c_vp), ("dweight", c_vp), ("weight_per_head", c_i32),
+                ("heads", c_i32)]
 
 
 _P = ctypes.POINTER(moe_problem)
@@ -110,6 +128,23 @@ _SIGS = {
     "moe_gdr_backward": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp,
                                         c_vp, ctypes.c_float, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
                                         c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "moe_qk_norm_rope": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32, c_i32, ctypes.c_float, c_vp,
+                                        c_vp, ctypes.POINTER(moe_qk_rows),
+                                        ctypes.POINTER(moe_qk_rows), c_vp]),
+    "moe_qk_norm_rope_backward_workspace_size": (c_sz, [c_i32, c_i32, c_i32, c_i32]),
+    "moe_qk_norm_rope_backward": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32,
+                                                 ctypes.c_float, c_vp, c_vp,
+                                                 ctypes.POINTER(moe_qk_grads),
+                                                 ctypes.POINTER(moe_qk_grads), c_vp, c_sz, c_vp]),
+    "moe_gdr_step": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                    c_vp, c_i32, ctypes.c_float, c_vp, c_vp, c_vp, c_vp]),
+    "moe_glr_forward": (ctypes.c_int, [c_i32, c_i32, c_i32, c_vp, c_i32, c_i32, c_vp, c_i64, c_vp,
+                                       c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "moe_glr_backward": (ctypes.c_int, [c_i32, c_i32, c_i32, c_vp, c_i32, c_i32, c_vp, c_i64,
+                                        c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                        c_vp, c_vp]),
+    "moe_glr_step": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp,
+                                    c_i32, c_vp, c_vp, c_vp, c_vp]),
     "moe_set_kernel_events": (ctypes.c_int, [ctypes.c_int, c_vp, c_vp]),
     "moe_launch_count": (ctypes.c_longlong, []),
     "moe_selftest_wait_timeout": (ctypes.c_int, [c_vp, c_i32, c_vp]),
@@ -118,7 +153,8 @@ _SIGS = {
 KERNEL_IDS = {"router_gemm": 0, "topk": 1, "dispatch": 2, "gateup_gemm": 3, "down_gemm": 4,
               "combine": 5, "bwd_dh_gemm": 6, "bwd_dx_gemm": 7, "wgrad": 8, "gdr_chunk": 9,
               "gdr_scan": 10, "gdr_bwd": 11, "combine_bwd": 12, "dispatch_route_bwd": 13,
-              "gdr_bwd_factors": 14, "gdr_bwd_scan": 15}
+              "gdr_bwd_factors": 14, "gdr_bwd_scan": 15, "qk_norm_rope": 16, "qk_norm_rope_bwd": 17,
+              "gdr_step": 18, "glr_fwd": 19, "glr_bwd": 20, "glr_step": 21}
 
 _lib = None
 
@@ -447,6 +483,174 @@ def moe_gdr_backward(B, T, H, dk, dv, q, k, v, beta, g, scale, d_o, dS_T, S_chun
                                   scale, _ptr(d_o), _ptr(dS_T), _ptr(S_chunks), _ptr(W_chunks),
                                   _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(dbeta), _ptr(dg), _ptr(dS0),
                                   wp, wn, _stream(stream)))
+
+
+_DTYPES = {MOE_BF16: torch.bfloat16, MOE_F32: torch.float32}
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _tensor(name, t, dtype, shape, optional=False):
+    """Address of a dense tensor of the current device after a check of its type and shape."""
+    if t is None:
+        _need(optional, f"{name} is missing")
+        return None
+    _need(t.dtype is dtype and t.shape == shape and t.is_contiguous() and _here(t),
+          f"{name}: a contiguous {dtype} tensor of shape {shape} on the current device is wanted, "
+          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _here(t):
+    return t.is_cuda and t.get_device() == torch.cuda.current_device()
+
+
+def _head_rows(name, t, dtype, N, heads, D):
+    """(address, token stride, head stride) of [N, heads, D] values, dense within a head."""
+    _need(t.dtype is dtype and t.shape == (N, heads, D) and t.stride(2) == 1 and _here(t),
+          f"{name}: a {dtype} tensor of shape {(N, heads, D)}, dense in its last dimension, on "
+          f"the current device is wanted, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on "
+          f"{t.device}")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _head_weight(name, w, heads, D):
+    """(address, one row for each head?) of a norm weight or its gradient."""
+    if w is None:
+        return None, 0
+    return _tensor(name, w, torch.float32, (heads, D) if w.dim() == 2 else (D,)), w.dim() == 2
+
+
+def _qk_rows(name, r, dtype, N, D):
+    if r is None:
+        return None
+    heads = r["x"].shape[1]
+    return ctypes.byref(moe_qk_rows(*_head_rows(name + ".x", r["x"], dtype, N, heads, D),
+                                    *_head_rows(name + ".y", r["y"], dtype, N, heads, D),
+                                    *_head_weight(name + ".weight", r.get("weight"), heads, D),
+                                    heads))
+
+
+def _qk_grads(name, r, dtype, dy_dtype, N, D):
+    if r is None:
+        return None
+    heads, w, dw = r["x"].shape[1], r.get("weight"), r.get("dweight")
+    wp, per_head = _head_weight(name + ".weight", w, heads, D)
+    dwp, dw_per_head = _head_weight(name + ".dweight", dw, heads, D)
+    _need(w is None or dw is None or per_head == dw_per_head,
+          f"{name}.dweight has to be shaped as {name}.weight")
+    return ctypes.byref(moe_qk_grads(*_head_rows(name + ".x", r["x"], dtype, N, heads, D),
+                                     *_head_rows(name + ".dy", r["dy"], dy_dtype, N, heads, D),
+                                     *_head_rows(name + ".dx", r["dx"], dtype, N, heads, D),
+                                     wp, dwp, per_head or dw_per_head, heads))
+
+
+def _positions(positions, inv_freq, N, rotary_dim):
+    return (_tensor("positions", positions, torch.int32, (N,), rotary_dim == 0),
+            _tensor("inv_freq", inv_freq, torch.float64, (rotary_dim // 2,), rotary_dim == 0))
+
+
+def moe_qk_norm_rope(N, D, rotary_dim, interleaved, dtype, eps, positions, inv_freq, q, k,
+                     stream=None):
+    """q and k: dicts of x, y [N, heads, D] (any strides over tokens and heads) and weight ([D],
+    [heads, D] or None); k may be None."""
+    dt = _DTYPES[dtype]
+    pp, fp = _positions(positions, inv_freq, N, rotary_dim)
+    _check("moe_qk_norm_rope",
+           lib().moe_qk_norm_rope(N, D, rotary_dim, 1 if interleaved else 0, dtype, eps, pp, fp,
+                                  _qk_rows("q", q, dt, N, D), _qk_rows("k", k, dt, N, D),
+                                  _stream(stream)))
+
+
+def moe_qk_norm_rope_backward_workspace_size(N, D, q_heads, k_heads) -> int:
+    return lib().moe_qk_norm_rope_backward_workspace_size(N, D, q_heads, k_heads)
+
+
+def moe_qk_norm_rope_backward(N, D, rotary_dim, interleaved, dtype, dy_dtype, eps, positions,
+                              inv_freq, q, k, workspace, stream=None):
+    """q and k: dicts of x, dy, dx [N, heads, D] (any strides over tokens and heads), weight and
+    dweight ([D], [heads, D] or None); k may be None."""
+    dt, gt = _DTYPES[dtype], _DTYPES[dy_dtype]
+    pp, fp = _positions(positions, inv_freq, N, rotary_dim)
+    wp, wn = _ws(workspace)
+    _check("moe_qk_norm_rope_backward",
+           lib().moe_qk_norm_rope_backward(N, D, rotary_dim, 1 if interleaved else 0, dtype,
+                                           dy_dtype, eps, pp, fp,
+                                           _qk_grads("q", q, dt, gt, N, D),
+                                           _qk_grads("k", k, dt, gt, N, D), wp, wn,
+                                           _stream(stream)))
+
+
+def moe_gdr_step(B, H, dk, dv, q, k, v, beta, g, slot, n_slots, scale, S, o, dev_status=None,
+                 stream=None):
+    bf, f32 = torch.bfloat16, torch.float32
+    _check("moe_gdr_step",
+           lib().moe_gdr_step(B, H, dk, dv, _tensor("q", q, bf, (B, H, dk)),
+                              _tensor("k", k, bf, (B, H, dk)), _tensor("v", v, bf, (B, H, dv)),
+                              _tensor("beta", beta, f32, (B, H)), _tensor("g", g, f32, (B, H)),
+                              _tensor("slot", slot, torch.int32, (B,), True), n_slots, scale,
+                              _tensor("S", S, f32, (n_slots, H, dv, dk)),
+                              _tensor("o", o, bf, (B, H, dv)), _ptr(dev_status),
+                              _stream(stream)))
+
+
+# ---- gated linear recurrence (include/linear_recurrence.h)
+
+def _rows(name, t, dtype, N, D):
+    """(address, row stride) of N rows of D values."""
+    _need(t.dtype is dtype and t.shape == (N, D) and (D == 1 or t.stride(1) == 1) and _here(t),
+          f"{name}: a {dtype} tensor of shape {(N, D)}, dense in its rows, on the current device "
+          f"is wanted, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t.data_ptr(), t.stride(0)
+
+
+def moe_glr_forward(N, D, n_seq, seq_off, mode, dtype, g, x, h0, h, h_T, h_chunks,
+                    dev_status=None, stream=None):
+    dt, f32 = _DTYPES[dtype], torch.float32
+    _check("moe_glr_forward",
+           lib().moe_glr_forward(N, D, n_seq,
+                                 _tensor("seq_off", seq_off, torch.int32, (n_seq + 1,), True),
+                                 mode, dtype, *_rows("g", g, dt, N, D), *_rows("x", x, dt, N, D),
+                                 _tensor("h0", h0, f32, (n_seq, D), True),
+                                 _tensor("h", h, dt, (N, D)),
+                                 _tensor("h_T", h_T, f32, (n_seq, D), True),
+                                 _tensor("h_chunks", h_chunks, f32, ((N + 63) // 64, D), True),
+                                 _ptr(dev_status), _stream(stream)))
+
+
+def moe_glr_backward(N, D, n_seq, seq_off, mode, dtype, g, x, h0, h_chunks, dh, dh_T, dg, dx, dh0,
+                     dev_status=None, stream=None):
+    """dg and dx need the row strides of g and x."""
+    dt, f32 = _DTYPES[dtype], torch.float32
+    gp, ld_g = _rows("g", g, dt, N, D)
+    xp, ld_x = _rows("x", x, dt, N, D)
+    dgp, ld_dg = _rows("dg", dg, dt, N, D)
+    dxp, ld_dx = _rows("dx", dx, dt, N, D)
+    _need(N == 1 or (ld_g == ld_dg and ld_x == ld_dx),
+          "dg and dx need the row strides of g and x")
+    _check("moe_glr_backward",
+           lib().moe_glr_backward(N, D, n_seq,
+                                  _tensor("seq_off", seq_off, torch.int32, (n_seq + 1,), True),
+                                  mode, dtype, gp, ld_g, xp, ld_x,
+                                  _tensor("h0", h0, f32, (n_seq, D), True),
+                                  _tensor("h_chunks", h_chunks, f32, ((N + 63) // 64, D)),
+                                  _tensor("dh", dh, dt, (N, D)),
+                                  _tensor("dh_T", dh_T, f32, (n_seq, D), True), dgp, dxp,
+                                  _tensor("dh0", dh0, f32, (n_seq, D), True), _ptr(dev_status),
+                                  _stream(stream)))
+
+
+def moe_glr_step(B, D, mode, dtype, g, x, slot, n_slots, state, h, dev_status=None, stream=None):
+    dt = _DTYPES[dtype]
+    _check("moe_glr_step",
+           lib().moe_glr_step(B, D, mode, dtype, *_rows("g", g, dt, B, D),
+                              *_rows("x", x, dt, B, D),
+                              _tensor("slot", slot, torch.int32, (B,), True), n_slots,
+                              _tensor("state", state, torch.float32, (n_slots, D)),
+                              _tensor("h", h, dt, (B, D)), _ptr(dev_status), _stream(stream)))
 
 
 def moe_set_kernel_events(kernel, before, after):
