@@ -27,7 +27,8 @@
  *   h0, h_T, dh_T, dh0 [n_seq, D] fp32: the state before a sequence's first row and after its
  *   last, and their gradients; each may be NULL (zero, or not wanted).  h_T may be h0: the
  *   states are then updated in place.  An empty sequence hands its h0 to h_T.
- * Any D and N, any alignment of the values' own type.  D, the strides and the pointers of the
+ * Any D, N up to 2^30 and n_seq up to 2^24 (else MOE_ERR_UNSUPPORTED), any alignment of the
+ * values' own type.  D, the strides and the pointers of the
  * `dtype` tensors allowing, two channels are moved at a time, which is faster.
  *
  * Precision: states, products and sums are fp32; h, dg and dx are rounded once.  Sequences do

@@ -205,9 +205,16 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# the handle of a device's current stream: torch's own accessor where it has one (a tenth of
+# the time of building a Stream object, which shows in calls of a few microseconds)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _check(name, status):
@@ -488,81 +495,90 @@ def moe_gdr_backward(B, T, H, dk, dv, q, k, v, beta, g, scale, d_o, dS_T, S_chun
 _DTYPES = {MOE_BF16: torch.bfloat16, MOE_F32: torch.float32}
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+def _device():
+    """The current device (none, which no tensor is on, where there is no GPU)."""
+    if torch.cuda.is_initialized() or torch.cuda.is_available():
+        return torch.cuda.current_device()
+    return -2
 
 
-def _tensor(name, t, dtype, shape, optional=False):
-    """Address of a dense tensor of the current device after a check of its type and shape."""
+def _refuse(name, t, wanted):
+    got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}"
+    raise ValueError(f"{name}: {wanted} on the current device is wanted, got {got}")
+
+
+def _tensor(name, t, dtype, shape, dev, optional=False):
+    """Address of a dense tensor of device ``dev`` after a check of its type and shape."""
     if t is None:
-        _need(optional, f"{name} is missing")
-        return None
-    _need(t.dtype is dtype and t.shape == shape and t.is_contiguous() and _here(t),
-          f"{name}: a contiguous {dtype} tensor of shape {shape} on the current device is wanted, "
-          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return None if optional else _refuse(name, t, f"a contiguous {dtype} tensor {shape}")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(name, t, f"a contiguous {dtype} tensor {shape}")
     return t.data_ptr()
 
 
-def _here(t):
-    return t.is_cuda and t.get_device() == torch.cuda.current_device()
+def _status(dev_status, dev):
+    return _tensor("dev_status", dev_status, torch.int32, (1,), dev, True)
 
 
-def _head_rows(name, t, dtype, N, heads, D):
+def _head_rows(name, t, dtype, shape, dev):
     """(address, token stride, head stride) of [N, heads, D] values, dense within a head."""
-    _need(t.dtype is dtype and t.shape == (N, heads, D) and t.stride(2) == 1 and _here(t),
-          f"{name}: a {dtype} tensor of shape {(N, heads, D)}, dense in its last dimension, on "
-          f"the current device is wanted, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on "
-          f"{t.device}")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(name, t, f"a {dtype} tensor {shape}")
+    by_token, by_head, by_value = t.stride()
+    if by_value != 1:
+        _refuse(name, t, f"a {dtype} tensor {shape}, dense in its last dimension,")
+    return t.data_ptr(), by_token, by_head
 
 
-def _head_weight(name, w, heads, D):
+def _head_weight(name, w, heads, D, dev):
     """(address, one row for each head?) of a norm weight or its gradient."""
     if w is None:
         return None, 0
-    return _tensor(name, w, torch.float32, (heads, D) if w.dim() == 2 else (D,)), w.dim() == 2
+    per_head = w.dim() == 2
+    return _tensor(name, w, torch.float32, (heads, D) if per_head else (D,), dev), per_head
 
 
-def _qk_rows(name, r, dtype, N, D):
+def _qk_rows(name, r, dtype, N, D, dev):
     if r is None:
         return None
-    heads = r["x"].shape[1]
-    return ctypes.byref(moe_qk_rows(*_head_rows(name + ".x", r["x"], dtype, N, heads, D),
-                                    *_head_rows(name + ".y", r["y"], dtype, N, heads, D),
-                                    *_head_weight(name + ".weight", r.get("weight"), heads, D),
-                                    heads))
+    x = r["x"]
+    heads = x.shape[1]
+    shape = (N, heads, D)
+    return ctypes.byref(moe_qk_rows(*_head_rows(name + ".x", x, dtype, shape, dev),
+                                    *_head_rows(name + ".y", r["y"], dtype, shape, dev),
+                                    *_head_weight(name + ".weight", r.get("weight"), heads, D,
+                                                  dev), heads))
 
 
-def _qk_grads(name, r, dtype, dy_dtype, N, D):
+def _qk_grads(name, r, dtype, dy_dtype, N, D, dev):
     if r is None:
         return None
-    heads, w, dw = r["x"].shape[1], r.get("weight"), r.get("dweight")
-    wp, per_head = _head_weight(name + ".weight", w, heads, D)
-    dwp, dw_per_head = _head_weight(name + ".dweight", dw, heads, D)
-    _need(w is None or dw is None or per_head == dw_per_head,
-          f"{name}.dweight has to be shaped as {name}.weight")
-    return ctypes.byref(moe_qk_grads(*_head_rows(name + ".x", r["x"], dtype, N, heads, D),
-                                     *_head_rows(name + ".dy", r["dy"], dy_dtype, N, heads, D),
-                                     *_head_rows(name + ".dx", r["dx"], dtype, N, heads, D),
+    x, w, dw = r["x"], r.get("weight"), r.get("dweight")
+    heads = x.shape[1]
+    shape = (N, heads, D)
+    if w is not None and dw is not None and w.shape != dw.shape:
+        _refuse(name + ".dweight", dw, f"a tensor shaped as {name}.weight")
+    wp, per_head = _head_weight(name + ".weight", w, heads, D, dev)
+    dwp, dw_per_head = _head_weight(name + ".dweight", dw, heads, D, dev)
+    return ctypes.byref(moe_qk_grads(*_head_rows(name + ".x", x, dtype, shape, dev),
+                                     *_head_rows(name + ".dy", r["dy"], dy_dtype, shape, dev),
+                                     *_head_rows(name + ".dx", r["dx"], dtype, shape, dev),
                                      wp, dwp, per_head or dw_per_head, heads))
-
-
-def _positions(positions, inv_freq, N, rotary_dim):
-    return (_tensor("positions", positions, torch.int32, (N,), rotary_dim == 0),
-            _tensor("inv_freq", inv_freq, torch.float64, (rotary_dim // 2,), rotary_dim == 0))
 
 
 def moe_qk_norm_rope(N, D, rotary_dim, interleaved, dtype, eps, positions, inv_freq, q, k,
                      stream=None):
     """q and k: dicts of x, y [N, heads, D] (any strides over tokens and heads) and weight ([D],
     [heads, D] or None); k may be None."""
-    dt = _DTYPES[dtype]
-    pp, fp = _positions(positions, inv_freq, N, rotary_dim)
+    dt, dev = _DTYPES[dtype], _device()
     _check("moe_qk_norm_rope",
-           lib().moe_qk_norm_rope(N, D, rotary_dim, 1 if interleaved else 0, dtype, eps, pp, fp,
-                                  _qk_rows("q", q, dt, N, D), _qk_rows("k", k, dt, N, D),
-                                  _stream(stream)))
+           lib().moe_qk_norm_rope(N, D, rotary_dim, 1 if interleaved else 0, dtype, eps,
+                                  _tensor("positions", positions, torch.int32, (N,), dev,
+                                          rotary_dim == 0),
+                                  _tensor("inv_freq", inv_freq, torch.float64,
+                                          (rotary_dim // 2,), dev, rotary_dim == 0),
+                                  _qk_rows("q", q, dt, N, D, dev),
+                                  _qk_rows("k", k, dt, N, D, dev), _stream(stream)))
 
 
 def moe_qk_norm_rope_backward_workspace_size(N, D, q_heads, k_heads) -> int:
@@ -573,84 +589,96 @@ def moe_qk_norm_rope_backward(N, D, rotary_dim, interleaved, dtype, dy_dtype, ep
                               inv_freq, q, k, workspace, stream=None):
     """q and k: dicts of x, dy, dx [N, heads, D] (any strides over tokens and heads), weight and
     dweight ([D], [heads, D] or None); k may be None."""
-    dt, gt = _DTYPES[dtype], _DTYPES[dy_dtype]
-    pp, fp = _positions(positions, inv_freq, N, rotary_dim)
+    dt, gt, dev = _DTYPES[dtype], _DTYPES[dy_dtype], _device()
     wp, wn = _ws(workspace)
     _check("moe_qk_norm_rope_backward",
            lib().moe_qk_norm_rope_backward(N, D, rotary_dim, 1 if interleaved else 0, dtype,
-                                           dy_dtype, eps, pp, fp,
-                                           _qk_grads("q", q, dt, gt, N, D),
-                                           _qk_grads("k", k, dt, gt, N, D), wp, wn,
+                                           dy_dtype, eps,
+                                           _tensor("positions", positions, torch.int32, (N,),
+                                                   dev, rotary_dim == 0),
+                                           _tensor("inv_freq", inv_freq, torch.float64,
+                                                   (rotary_dim // 2,), dev, rotary_dim == 0),
+                                           _qk_grads("q", q, dt, gt, N, D, dev),
+                                           _qk_grads("k", k, dt, gt, N, D, dev), wp, wn,
                                            _stream(stream)))
 
 
 def moe_gdr_step(B, H, dk, dv, q, k, v, beta, g, slot, n_slots, scale, S, o, dev_status=None,
                  stream=None):
-    bf, f32 = torch.bfloat16, torch.float32
+    bf, f32, dev = torch.bfloat16, torch.float32, _device()
     _check("moe_gdr_step",
-           lib().moe_gdr_step(B, H, dk, dv, _tensor("q", q, bf, (B, H, dk)),
-                              _tensor("k", k, bf, (B, H, dk)), _tensor("v", v, bf, (B, H, dv)),
-                              _tensor("beta", beta, f32, (B, H)), _tensor("g", g, f32, (B, H)),
-                              _tensor("slot", slot, torch.int32, (B,), True), n_slots, scale,
-                              _tensor("S", S, f32, (n_slots, H, dv, dk)),
-                              _tensor("o", o, bf, (B, H, dv)), _ptr(dev_status),
+           lib().moe_gdr_step(B, H, dk, dv, _tensor("q", q, bf, (B, H, dk), dev),
+                              _tensor("k", k, bf, (B, H, dk), dev),
+                              _tensor("v", v, bf, (B, H, dv), dev),
+                              _tensor("beta", beta, f32, (B, H), dev),
+                              _tensor("g", g, f32, (B, H), dev),
+                              _tensor("slot", slot, torch.int32, (B,), dev, True), n_slots, scale,
+                              _tensor("S", S, f32, (n_slots, H, dv, dk), dev),
+                              _tensor("o", o, bf, (B, H, dv), dev), _status(dev_status, dev),
                               _stream(stream)))
 
 
 # ---- gated linear recurrence (include/linear_recurrence.h)
 
-def _rows(name, t, dtype, N, D):
-    """(address, row stride) of N rows of D values."""
-    _need(t.dtype is dtype and t.shape == (N, D) and (D == 1 or t.stride(1) == 1) and _here(t),
-          f"{name}: a {dtype} tensor of shape {(N, D)}, dense in its rows, on the current device "
-          f"is wanted, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-    return t.data_ptr(), t.stride(0)
+def _rows(name, t, dtype, shape, dev):
+    """(address, row stride) of rows dense in themselves."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(name, t, f"a {dtype} tensor {shape}")
+    by_row, by_value = t.stride()
+    if by_value != 1 and shape[1] > 1:
+        _refuse(name, t, f"a {dtype} tensor {shape}, dense in its rows,")
+    return t.data_ptr(), by_row
 
 
 def moe_glr_forward(N, D, n_seq, seq_off, mode, dtype, g, x, h0, h, h_T, h_chunks,
                     dev_status=None, stream=None):
-    dt, f32 = _DTYPES[dtype], torch.float32
+    dt, f32, dev = _DTYPES[dtype], torch.float32, _device()
+    rows = (N, D)
     _check("moe_glr_forward",
            lib().moe_glr_forward(N, D, n_seq,
-                                 _tensor("seq_off", seq_off, torch.int32, (n_seq + 1,), True),
-                                 mode, dtype, *_rows("g", g, dt, N, D), *_rows("x", x, dt, N, D),
-                                 _tensor("h0", h0, f32, (n_seq, D), True),
-                                 _tensor("h", h, dt, (N, D)),
-                                 _tensor("h_T", h_T, f32, (n_seq, D), True),
-                                 _tensor("h_chunks", h_chunks, f32, ((N + 63) // 64, D), True),
-                                 _ptr(dev_status), _stream(stream)))
+                                 _tensor("seq_off", seq_off, torch.int32, (n_seq + 1,), dev, True),
+                                 mode, dtype, *_rows("g", g, dt, rows, dev),
+                                 *_rows("x", x, dt, rows, dev),
+                                 _tensor("h0", h0, f32, (n_seq, D), dev, True),
+                                 _tensor("h", h, dt, rows, dev),
+                                 _tensor("h_T", h_T, f32, (n_seq, D), dev, True),
+                                 _tensor("h_chunks", h_chunks, f32, ((N + 63) // 64, D), dev, True),
+                                 _status(dev_status, dev), _stream(stream)))
 
 
 def moe_glr_backward(N, D, n_seq, seq_off, mode, dtype, g, x, h0, h_chunks, dh, dh_T, dg, dx, dh0,
                      dev_status=None, stream=None):
     """dg and dx need the row strides of g and x."""
-    dt, f32 = _DTYPES[dtype], torch.float32
-    gp, ld_g = _rows("g", g, dt, N, D)
-    xp, ld_x = _rows("x", x, dt, N, D)
-    dgp, ld_dg = _rows("dg", dg, dt, N, D)
-    dxp, ld_dx = _rows("dx", dx, dt, N, D)
-    _need(N == 1 or (ld_g == ld_dg and ld_x == ld_dx),
-          "dg and dx need the row strides of g and x")
+    dt, f32, dev = _DTYPES[dtype], torch.float32, _device()
+    rows = (N, D)
+    gp, ld_g = _rows("g", g, dt, rows, dev)
+    xp, ld_x = _rows("x", x, dt, rows, dev)
+    dgp, ld_dg = _rows("dg", dg, dt, rows, dev)
+    dxp, ld_dx = _rows("dx", dx, dt, rows, dev)
+    if N > 1 and (ld_g != ld_dg or ld_x != ld_dx):
+        raise ValueError("dg and dx need the row strides of g and x")
     _check("moe_glr_backward",
            lib().moe_glr_backward(N, D, n_seq,
-                                  _tensor("seq_off", seq_off, torch.int32, (n_seq + 1,), True),
+                                  _tensor("seq_off", seq_off, torch.int32, (n_seq + 1,), dev, True),
                                   mode, dtype, gp, ld_g, xp, ld_x,
-                                  _tensor("h0", h0, f32, (n_seq, D), True),
-                                  _tensor("h_chunks", h_chunks, f32, ((N + 63) // 64, D)),
-                                  _tensor("dh", dh, dt, (N, D)),
-                                  _tensor("dh_T", dh_T, f32, (n_seq, D), True), dgp, dxp,
-                                  _tensor("dh0", dh0, f32, (n_seq, D), True), _ptr(dev_status),
-                                  _stream(stream)))
+                                  _tensor("h0", h0, f32, (n_seq, D), dev, True),
+                                  _tensor("h_chunks", h_chunks, f32, ((N + 63) // 64, D), dev),
+                                  _tensor("dh", dh, dt, rows, dev),
+                                  _tensor("dh_T", dh_T, f32, (n_seq, D), dev, True), dgp, dxp,
+                                  _tensor("dh0", dh0, f32, (n_seq, D), dev, True),
+                                  _status(dev_status, dev), _stream(stream)))
 
 
 def moe_glr_step(B, D, mode, dtype, g, x, slot, n_slots, state, h, dev_status=None, stream=None):
-    dt = _DTYPES[dtype]
+    dt, dev = _DTYPES[dtype], _device()
+    rows = (B, D)
     _check("moe_glr_step",
-           lib().moe_glr_step(B, D, mode, dtype, *_rows("g", g, dt, B, D),
-                              *_rows("x", x, dt, B, D),
-                              _tensor("slot", slot, torch.int32, (B,), True), n_slots,
-                              _tensor("state", state, torch.float32, (n_slots, D)),
-                              _tensor("h", h, dt, (B, D)), _ptr(dev_status), _stream(stream)))
+           lib().moe_glr_step(B, D, mode, dtype, *_rows("g", g, dt, rows, dev),
+                              *_rows("x", x, dt, rows, dev),
+                              _tensor("slot", slot, torch.int32, (B,), dev, True), n_slots,
+                              _tensor("state", state, torch.float32, (n_slots, D), dev),
+                              _tensor("h", h, dt, rows, dev), _status(dev_status, dev),
+                              _stream(stream)))
 
 
 def moe_set_kernel_events(kernel, before, after):
