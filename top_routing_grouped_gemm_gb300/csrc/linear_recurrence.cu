@@ -72,17 +72,28 @@ struct Piece<__nv_bfloat16, 2> {
   }
 };
 
+// exp(g) as 2^(g log2(e)): two instructions.  The product's rounding costs |g| 2^-24 of the
+// result, which matters little where a state is forgotten that fast.  ex2.approx is below the
+// true value by 2.3e-8 on average for small arguments, as long memories have them (measured over
+// [-0.2, 0]: mean -2.3e-8, rms 3.8e-8; the library's expf, of four times the instructions, has
+// -1.6e-9 and 3.1e-8), which would add up over the ~1 / |g| steps that a state lives; the
+// exponent carries log2(1 + 2.3e-8) against it.
+__device__ __forceinline__ float decay_of(float g) {
+  float a;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(fmaf(g, 1.4426950408889634f, 3.3e-8f)));
+  return a;
+}
+
 // 1 - exp(g) for g <= 0, given a = exp(g): near 0, where the difference cancels, the series
-// -g (1 + g/2 + g^2/6 + ...) to g^7 / 8! (1.6e-8 of the sum at the border).
+// -g (1 + g/2 + g^2/6 + ...) to g^5 / 6! (the next term is 4.8e-8 at the border).
 __device__ __forceinline__ float one_minus(float g, float a) {
-  float p = 1.f / 5040.f;
-  p = fmaf(p, g, 1.f / 720.f);
+  float p = 1.f / 720.f;
   p = fmaf(p, g, 1.f / 120.f);
   p = fmaf(p, g, 1.f / 24.f);
   p = fmaf(p, g, 1.f / 6.f);
   p = fmaf(p, g, 0.5f);
   p = fmaf(p, g, 1.f);
-  return g > -0.35f ? -g * p : 1.f - a;
+  return g > -0.25f ? -g * p : 1.f - a;
 }
 
 // ------------------------------------------------------------------ packed sequences
@@ -285,16 +296,24 @@ __device__ __forceinline__ void join(Exchange<CH>& x, int it, const Pair<CH>& mi
       *reinterpret_cast<volatile int*>(&x.abort) = 1;
       report_status(dev_status, MOE_ERR_TIMEOUT);
     }
-    for (int q = 0; q < rank; ++q) follow(state, x.blocks[buf][q][lane]);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) carry[c] = state[c];
-    for (int q = rank; q < cluster; ++q) follow(state, x.blocks[buf][q][lane]);
-    for (int w = 0; w < order; ++w) follow(carry, x.warps[buf][w][lane]);
+    for (int q = 0; q < kMaxCluster; ++q) {
+      if (q == rank)
+#pragma unroll
+        for (int c = 0; c < CH; ++c) carry[c] = state[c];
+      if (q < cluster) follow(state, x.blocks[buf][q][lane]);
+    }
+#pragma unroll
+    for (int w = 0; w < kWarps - 1; ++w)
+      if (w < order) follow(carry, x.warps[buf][w][lane]);
   } else {
-    for (int w = 0; w < order; ++w) follow(state, x.warps[buf][w][lane]);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) carry[c] = state[c];
-    for (int w = order; w < kWarps; ++w) follow(state, x.warps[buf][w][lane]);
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == order)
+#pragma unroll
+        for (int c = 0; c < CH; ++c) carry[c] = state[c];
+      follow(state, x.warps[buf][w][lane]);
+    }
   }
 }
 
@@ -305,7 +324,7 @@ __device__ __forceinline__ void fetch(Piece<T, CH> (&v)[R], const T* base, long 
   const T* at = base + t0 * stride + d;
   if (t0 >= lo && t0 + R <= hi) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) v[r].load(at + r * stride);
+    for (int r = 0; r < R; ++r, at += stride) v[r].load(at);
   } else {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -372,42 +391,37 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_forward_kernel(const Forwa
     }
 
     // the span's pair; a[r], b[r] stay for the second pass
-    float a[R][CH], b[R][CH];
+    float a[R][CH], b[R][CH], h[CH];
     Pair<CH> pair;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const float lg = g[r].get(c), xv = x[r].get(c);
-        a[r][c] = expf(lg);
-        b[r][c] = MIX ? one_minus(lg, a[r][c]) * xv : xv;
-      }
-    if (it + 1 < steps) {
-      fetch(g, p.g, p.ld_g, d, t0 + step, lo, hi);
-      fetch(x, p.x, p.ld_x, d, t0 + step, lo, hi);
-    }
-    if (firsts && p.h0) {
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (firsts >> r & 1)
-#pragma unroll
-          for (int c = 0; c < CH; ++c)
-            b[r][c] = fmaf(a[r][c], p.h0[marks.first[warp * R + r] * D + d + c], b[r][c]);
-    }
 #pragma unroll
     for (int c = 0; c < CH; ++c) pair.A[c] = 1.f, pair.H[c] = 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
+        const float lg = g[r].get(c), xv = x[r].get(c);
+        a[r][c] = decay_of(lg);
+        b[r][c] = MIX ? one_minus(lg, a[r][c]) * xv : xv;
         pair.A[c] *= a[r][c];
-        pair.H[c] = firsts >> r & 1 ? b[r][c] : fmaf(a[r][c], pair.H[c], b[r][c]);
+        pair.H[c] = fmaf(a[r][c], pair.H[c], b[r][c]);
       }
-    if (firsts)
+    if (it + 1 < steps) {
+      fetch(g, p.g, p.ld_g, d, t0 + step, lo, hi);
+      fetch(x, p.x, p.ld_x, d, t0 + step, lo, hi);
+    }
+    if (firsts) {  // again, with the initial states
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          if ((firsts >> r & 1) && p.h0)
+            b[r][c] = fmaf(a[r][c], p.h0[marks.first[warp * R + r] * D + d + c], b[r][c]);
+          pair.H[c] = firsts >> r & 1 ? b[r][c] : fmaf(a[r][c], pair.H[c], b[r][c]);
+        }
 #pragma unroll
       for (int c = 0; c < CH; ++c) pair.A[c] = -1.f;
+    }
 
-    float h[CH];
     join(xch, it, pair, warp, rank, p.cluster, lane, state, h, p.dev_status);
 
     if (p.h_chunks && on && t0 % kChunk == 0 && t0 >= lo && t0 < hi)
@@ -419,7 +433,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_forward_kernel(const Forwa
       for (int r = 0; r < R; ++r) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) h[c] = fmaf(a[r][c], h[c], b[r][c]);
-        if (on) Piece<T, CH>::store(out + r * D, h);
+        if (on) Piece<T, CH>::store(out, h);
+        out += D;
       }
     } else {
 #pragma unroll
@@ -516,33 +531,46 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_backward_kernel(const Back
       return p.dh_T ? p.dh_T[marks.last[warp * R + r] * D + d + c] : 0.f;
     };
 
-    float a[R][CH], om[MIX ? R : 1][CH];  // exp(g), 1 - exp(g)
+    float a[R][CH], om[MIX ? R : 1][CH] = {};  // exp(g), 1 - exp(g)
+    const auto input = [&](int r, int c) { return MIX ? om[r][c] * x[r].get(c) : x[r].get(c); };
     Pair<CH> fwd, rev;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) fwd.A[c] = rev.A[c] = 1.f, fwd.H[c] = rev.H[c] = 0.f;
+    for (int c = 0; c < CH; ++c) fwd.A[c] = 1.f, fwd.H[c] = rev.H[c] = 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const float lg = g[r].get(c);
-        a[r][c] = expf(lg);
+        a[r][c] = decay_of(lg);
         if (MIX) om[r][c] = one_minus(lg, a[r][c]);
-        const float b = MIX ? om[r][c] * x[r].get(c) : x[r].get(c);
-        if (firsts >> r & 1) fwd.H[c] = state_before(r, c);
-        fwd.H[c] = fmaf(a[r][c], fwd.H[c], b);
         fwd.A[c] *= a[r][c];
+        fwd.H[c] = fmaf(a[r][c], fwd.H[c], input(r, c));
       }
 #pragma unroll
     for (int r = R - 1; r >= 0; --r)
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        if (lasts >> r & 1) rev.H[c] = grad_after(r, c);
-        rev.H[c] = a[r][c] * (dh[r].get(c) + rev.H[c]);
-      }
+      for (int c = 0; c < CH; ++c) rev.H[c] = a[r][c] * (dh[r].get(c) + rev.H[c]);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      rev.A[c] = lasts ? -1.f : fwd.A[c];
-      if (firsts) fwd.A[c] = -1.f;
+    for (int c = 0; c < CH; ++c) rev.A[c] = fwd.A[c];
+    if (firsts) {  // again, from the initial states
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          if (firsts >> r & 1) fwd.H[c] = state_before(r, c);
+          fwd.H[c] = fmaf(a[r][c], fwd.H[c], input(r, c));
+          fwd.A[c] = -1.f;
+        }
+    }
+    if (lasts) {  // again, from the final states' gradients
+#pragma unroll
+      for (int r = R - 1; r >= 0; --r)
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          if (lasts >> r & 1) rev.H[c] = grad_after(r, c);
+          rev.H[c] = a[r][c] * (dh[r].get(c) + rev.H[c]);
+          rev.A[c] = -1.f;
+        }
     }
     ahead[it & 1][warp][lane] = fwd;
     Piece<T, CH> g_next[R], x_next[R], dh_next[R];
@@ -555,35 +583,63 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_backward_kernel(const Back
     float h[CH], before[R][CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) h[c] = kept[c];
-    for (int w = 0; w < warp; ++w) follow(h, ahead[it & 1][w][lane]);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int w = 0; w < kWarps - 1; ++w)
+      if (w < warp) follow(h, ahead[it & 1][w][lane]);
+    T* dg = p.dg + (t0 + R - 1) * p.ld_g + d;
+    T* dx = p.dx + (t0 + R - 1) * p.ld_x + d;
+    if (!marked && t0 >= lo && t0 + R <= hi) {
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        if (firsts >> r & 1) h[c] = state_before(r, c);
-        before[r][c] = MIX ? h[c] - x[r].get(c) : h[c];
-        h[c] = fmaf(a[r][c], h[c], MIX ? om[r][c] * x[r].get(c) : x[r].get(c));
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          before[r][c] = MIX ? h[c] - x[r].get(c) : h[c];
+          h[c] = fmaf(a[r][c], h[c], input(r, c));
+        }
+#pragma unroll
+      for (int r = R - 1; r >= 0; --r) {
+        float o_g[CH], o_x[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const float lam = dh[r].get(c) + back[c];
+          back[c] = a[r][c] * lam;
+          o_x[c] = MIX ? om[r][c] * lam : lam;
+          o_g[c] = back[c] * before[r][c];
+        }
+        if (on) {
+          Piece<T, CH>::store(dg, o_g);
+          Piece<T, CH>::store(dx, o_x);
+        }
+        dg -= p.ld_g;
+        dx -= p.ld_x;
       }
-    T* dg = p.dg + t0 * p.ld_g + d;
-    T* dx = p.dx + t0 * p.ld_x + d;
-    const bool whole = !marked && t0 >= lo && t0 + R <= hi;
+    } else {
 #pragma unroll
-    for (int r = R - 1; r >= 0; --r) {
-      float o_g[CH], o_x[CH];
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        if (lasts >> r & 1) back[c] = grad_after(r, c);
-        const float lam = dh[r].get(c) + back[c];
-        back[c] = a[r][c] * lam;
-        o_x[c] = MIX ? om[r][c] * lam : lam;
-        o_g[c] = back[c] * before[r][c];
-      }
-      if (on && (whole || (t0 + r >= lo && t0 + r < hi))) {
-        Piece<T, CH>::store(dg + r * p.ld_g, o_g);
-        Piece<T, CH>::store(dx + r * p.ld_x, o_x);
-        if ((firsts >> r & 1) && p.dh0)
+        for (int c = 0; c < CH; ++c) {
+          if (firsts >> r & 1) h[c] = state_before(r, c);
+          before[r][c] = MIX ? h[c] - x[r].get(c) : h[c];
+          h[c] = fmaf(a[r][c], h[c], input(r, c));
+        }
 #pragma unroll
-          for (int c = 0; c < CH; ++c) p.dh0[marks.first[warp * R + r] * D + d + c] = back[c];
+      for (int r = R - 1; r >= 0; --r) {
+        float o_g[CH], o_x[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          if (lasts >> r & 1) back[c] = grad_after(r, c);
+          const float lam = dh[r].get(c) + back[c];
+          back[c] = a[r][c] * lam;
+          o_x[c] = MIX ? om[r][c] * lam : lam;
+          o_g[c] = back[c] * before[r][c];
+        }
+        if (on && t0 + r >= lo && t0 + r < hi) {
+          Piece<T, CH>::store(dg - (R - 1 - r) * p.ld_g, o_g);
+          Piece<T, CH>::store(dx - (R - 1 - r) * p.ld_x, o_x);
+          if ((firsts >> r & 1) && p.dh0)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) p.dh0[marks.first[warp * R + r] * D + d + c] = back[c];
+        }
       }
     }
     if (marked) __syncthreads();  // the marks are rewritten
