@@ -243,6 +243,10 @@ GLR = [
     (9000, 10, [4000, 0, None], False, F32, True),
     (700, 1030, 7, False, BF, True),
     (1300, 2050, [600, None], True, BF, False),
+    (100, 8, [30, None], True, BF, True),
+    (200, 4, 1, False, F32, True),
+    (4100, 328, [2000, None, 0], True, BF, True),
+    (3001, 100, 1, True, F32, False),
 ]
 
 
@@ -299,11 +303,14 @@ def majorants(g, x, off, h0, mix):
     return M, E
 
 
+# values between the end of a row of g and x and the next: rows on 16-byte boundaries where D
+# allows it, dense, and rows on the boundaries of a value alone
+@pytest.mark.parametrize("wide", [8, 0, 5])
 @pytest.mark.parametrize("case", GLR, ids=[f"{c[0]}x{c[1]}" for c in GLR])
-def test_recurrence(case):
+def test_recurrence(case, wide):
     N, D, lengths, mix, dtype, _ = case
     pad = 0 if isinstance(lengths, int) else 3
-    i = glr_inputs(case, pad=pad, wide=5 if D % 2 else 6)
+    i = glr_inputs(case, pad=pad, wide=wide)
     h, h_T, chunks = run_glr(case, i)
     g, x, h0 = f64(i["g"])[:N], f64(i["x"])[:N], f64(i["h0"])
     ref, ref_T = SM.gated_recurrence(g, x, i["off"], h0, mix)
@@ -321,11 +328,12 @@ def test_recurrence(case):
             close(chunks[c // 64], ref[c - 1], E[c - 1], F32, f"chunk {c}")
 
 
+@pytest.mark.parametrize("wide", [8, 0, 5])
 @pytest.mark.parametrize("case", GLR, ids=[f"{c[0]}x{c[1]}" for c in GLR])
-def test_recurrence_backward(case):
+def test_recurrence_backward(case, wide):
     N, D, lengths, mix, dtype, with_h0 = case
     pad = 0 if isinstance(lengths, int) else 3
-    i = glr_inputs(case, seed=1, pad=pad, wide=5 if D % 2 else 6)
+    i = glr_inputs(case, seed=1, pad=pad, wide=wide)
     _, _, chunks = run_glr(case, i)
     dh = torch.randn((i["rows"], D), generator=i["gen"]).to(dtype).cuda()
     dh_T = torch.randn((i["S"], D), generator=i["gen"]).cuda() if with_h0 else None
@@ -376,7 +384,7 @@ def test_recurrence_backward(case):
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_recurrence_states_in_place_and_prefill_in_parts(dtype):
     """h_T over h0, a long prompt in three calls, against one call; then the same bits again."""
-    N, D = 900, 130
+    N, D = 900, 136
     whole = (N, D, 1, False, dtype, True)
     i = glr_inputs(whole, seed=2)
     h, h_T, _ = run_glr(whole, i)
@@ -397,7 +405,7 @@ def test_recurrence_states_in_place_and_prefill_in_parts(dtype):
 def test_recurrence_sequences_do_not_see_each_other(dtype, bad):
     """A NaN or infinity in one sequence (its inputs, decays, state, padding) leaves the values
     and gradients of the others as they are without it."""
-    case = (700, 70, [130, 200, 0, 70, None], True, dtype, True)
+    case = (700, 72, [130, 200, 0, 70, None], True, dtype, True)
     N, D = case[0], case[1]
     outs = []
     for poisoned in (False, True):

@@ -57,6 +57,23 @@ int encode_map_mnmajor(CUtensorMap* map, const void* base, uint64_t mn_extent, u
   return encode3d(map, base, dims, strides, box);
 }
 
+// rows of `cols` values (bf16 or fp32), ld values apart, read in boxes of box_cols x box_rows as
+// they lie (no swizzle); what a box has outside the tensor reads as zero.
+int encode_map_rows(CUtensorMap* map, const void* base, bool fp32, uint64_t cols, uint64_t rows,
+                    uint64_t ld, uint32_t box_cols, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return MOE_ERR_CUDA;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {ld * (fp32 ? 4 : 2)};
+  const cuuint32_t box[2] = {box_cols, box_rows}, estr[2] = {1, 1};
+  const CUresult r =
+      fn(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+}
+
 int num_sms() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;

@@ -15,7 +15,13 @@ namespace {
 
 constexpr int kChunk = 64;      // rows between the kept states
 constexpr int kWarps = 8;       // warps of a scan block
+constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;  // blocks of a cluster (the portable limit)
+constexpr int kForwardRows = 16;  // rows of a warp in a tile
+constexpr int kBackwardRows = 8;
+constexpr int kForwardStages = 2;   // tiles in shared memory
+constexpr int kBackwardStages = 3;  // (one is still read while the next but one arrives)
+constexpr int kBounds = 1024;   // bounds of sequences that a block keeps in shared memory
 
 __device__ __forceinline__ float ld(const float* p, long long i) { return p[i]; }
 __device__ __forceinline__ float ld(const __nv_bfloat16* p, long long i) {
@@ -30,47 +36,20 @@ __device__ __forceinline__ void st(__nv_bfloat16* p, long long i, float v) {
 //
 // CH channels of one row: two bf16 (4 bytes), one bf16 (rows that are not 4-byte aligned) or
 // one fp32; a warp covers 32 CH neighbouring channels.
-template <typename T, int CH>
-struct Piece;
+__device__ __forceinline__ float get(const uint32_t& bits, int c, __nv_bfloat16) {
+  return __uint_as_float(c ? bits & 0xffff0000u : bits << 16);
+}
+__device__ __forceinline__ float get(const uint32_t& bits, int, float) {
+  return __uint_as_float(bits);
+}
 
-template <>
-struct Piece<float, 1> {
-  float bits;
-  __device__ __forceinline__ void load(const float* p) { bits = __ldcs(p); }
-  __device__ __forceinline__ void clear() { bits = 0.f; }
-  __device__ __forceinline__ float get(int) const { return bits; }
-  static __device__ __forceinline__ void store(float* p, const float (&v)[1]) { __stcs(p, v[0]); }
-};
-
-template <>
-struct Piece<__nv_bfloat16, 1> {
-  unsigned short bits;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    bits = __ldcs(reinterpret_cast<const unsigned short*>(p));
-  }
-  __device__ __forceinline__ void clear() { bits = 0; }
-  __device__ __forceinline__ float get(int) const {
-    return __uint_as_float(static_cast<unsigned>(bits) << 16);
-  }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[1]) {
-    *p = __float2bfloat16_rn(v[0]);
-  }
-};
-
-template <>
-struct Piece<__nv_bfloat16, 2> {
-  unsigned bits;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    bits = __ldcs(reinterpret_cast<const unsigned*>(p));
-  }
-  __device__ __forceinline__ void clear() { bits = 0; }
-  __device__ __forceinline__ float get(int c) const {
-    return __uint_as_float(c ? bits & 0xffff0000u : bits << 16);
-  }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[2]) {
-    __stcs(reinterpret_cast<unsigned*>(p), pack_bf16x2(v[0], v[1]));
-  }
-};
+__device__ __forceinline__ void put(float* p, const float (&v)[1]) { __stcs(p, v[0]); }
+__device__ __forceinline__ void put(__nv_bfloat16* p, const float (&v)[1]) {
+  *p = __float2bfloat16_rn(v[0]);
+}
+__device__ __forceinline__ void put(__nv_bfloat16* p, const float (&v)[2]) {
+  __stcs(reinterpret_cast<unsigned*>(p), pack_bf16x2(v[0], v[1]));
+}
 
 // exp(g) as 2^(g log2(e)): two instructions.  The product's rounding costs |g| 2^-24 of the
 // result, which matters little where a state is forgotten that fast.  ex2.approx is below the
@@ -205,8 +184,9 @@ struct Walker {
 // in the order of the recurrence.  A is -1 for a span in which a sequence begins: what came
 // before is then not used at all, not even multiplied by zero.
 
+// (Aligned for the vector store that carries it.)
 template <int CH>
-struct Pair {
+struct alignas(8 * CH) Pair {
   float A[CH], H[CH];
 };
 
@@ -225,6 +205,13 @@ __device__ __forceinline__ void append(Pair<CH>& s, const Pair<CH>& p) {
   }
 }
 
+// Reports a wait that ran out.  The rest of the launch goes on without waiting (its results are
+// then wrong), so every barrier still gets all its threads.
+__device__ __forceinline__ void give_up(int* abort, int* dev_status) {
+  *reinterpret_cast<volatile int*>(abort) = 1;
+  report_status(dev_status, MOE_ERR_TIMEOUT);
+}
+
 // What the warps of a block and the blocks of a cluster exchange, double-buffered by the parity
 // of the step.  A block writes step n + 2 over step n only after it has every block's pair of
 // step n + 1, and a block publishes that only when all its warps have read step n.
@@ -236,8 +223,9 @@ struct Exchange {
   int abort;
 };
 
-template <int CH>
-__device__ __forceinline__ void exchange_init(Exchange<CH>& x, int cluster) {
+template <int CH, typename Tiles>
+__device__ __forceinline__ void exchange_init(Exchange<CH>& x, int cluster, const Tiles& tiles) {
+  tiles.init();
   if (threadIdx.x == 0) {
     mbar_init(&x.full[0], 1);
     mbar_init(&x.full[1], 1);
@@ -273,18 +261,18 @@ __device__ __forceinline__ void publish(Exchange<CH>& x, int buf, const Pair<CH>
 }
 
 // Joins the pairs of step `it`: `carry` becomes the state in front of this warp's span, `state`
-// goes on over the whole step.  `order` is the warp's place in the order of the recurrence.  The
-// wait is bounded: when it runs out the rest of the launch goes on without waiting (its results
-// are then wrong, and reported), so every barrier still gets all its threads.
-template <int CH>
+// goes on over the whole step.  `order` is the warp's place in the order of the recurrence.  At
+// `meet` all warps have read the step's tile once.
+template <int CH, typename Meet>
 __device__ __forceinline__ void join(Exchange<CH>& x, int it, const Pair<CH>& mine, int order,
                                      int rank, int cluster, int lane, float (&state)[CH],
-                                     float (&carry)[CH], int* dev_status) {
+                                     float (&carry)[CH], int* dev_status, Meet meet) {
   const int buf = it & 1;
   x.warps[buf][order][lane] = mine;
   if (cluster > 1 && threadIdx.x == 0)
     mbar_arrive_expect_tx(&x.full[buf], cluster * 32 * sizeof(Pair<CH>));
   __syncthreads();
+  meet();
   if (cluster > 1) {
     if (order == 0) {
       Pair<CH> sum = mine;
@@ -292,10 +280,7 @@ __device__ __forceinline__ void join(Exchange<CH>& x, int it, const Pair<CH>& mi
       for (int w = 1; w < kWarps; ++w) append(sum, x.warps[buf][w][lane]);
       publish(x, buf, sum, rank, cluster, lane);
     }
-    if (!mbar_wait(&x.full[buf], (it >> 1) & 1, &x.abort)) {
-      *reinterpret_cast<volatile int*>(&x.abort) = 1;
-      report_status(dev_status, MOE_ERR_TIMEOUT);
-    }
+    if (!mbar_wait(&x.full[buf], (it >> 1) & 1, &x.abort)) give_up(&x.abort, dev_status);
 #pragma unroll
     for (int q = 0; q < kMaxCluster; ++q) {
       if (q == rank)
@@ -317,27 +302,80 @@ __device__ __forceinline__ void join(Exchange<CH>& x, int it, const Pair<CH>& mi
   }
 }
 
-// R rows from row t0 at channel d; rows outside [lo, hi) as zeros.
-template <typename T, int CH, int R>
-__device__ __forceinline__ void fetch(Piece<T, CH> (&v)[R], const T* base, long long stride, int d,
-                                      int t0, int lo, int hi) {
-  const T* at = base + t0 * stride + d;
-  if (t0 >= lo && t0 + R <= hi) {
-#pragma unroll
-    for (int r = 0; r < R; ++r, at += stride) v[r].load(at);
-  } else {
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      v[r].clear();
-      if (t0 + r >= lo && t0 + r < hi) v[r].load(at + r * stride);
-    }
+// ------------------------------------------------------------------ tiles in shared memory
+//
+// STAGES tiles of ARRAYS inputs, each [ROWS][32] words: the word of a lane holds its CH channels.
+// Where rows begin on 16-byte boundaries, one thread has TMA copy whole tiles two steps ahead
+// (ASYNC); elsewhere each warp copies its rows through registers when they are asked for.
+template <int ARRAYS, int STAGES, int ROWS, bool ASYNC>
+struct Tiles {
+  uint32_t* words;
+  uint64_t* full;  // [STAGES] barriers (ASYNC)
+
+  __device__ __forceinline__ uint32_t* at(int stage, int array) const {
+    return words + (stage * ARRAYS + array) * ROWS * 32;
   }
+
+  __device__ __forceinline__ void init() const {
+    if (ASYNC && threadIdx.x == 0)
+      for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
+  }
+
+  // One thread: the copies of step `it`, the tile at row t0 of the strip at channel d0.
+  __device__ __forceinline__ void load(int it, const CUtensorMap* maps, int d0, int t0) const {
+    const int stage = it % STAGES;
+    mbar_arrive_expect_tx(&full[stage], ARRAYS * ROWS * 128);
+    const uint64_t policy = l2_policy_evict_first();
+    for (int i = 0; i < ARRAYS; ++i) tma_load_2d(at(stage, i), &maps[i], &full[stage], d0, t0, policy);
+  }
+
+  __device__ __forceinline__ bool wait(int it, volatile int* abort) const {
+    return mbar_wait(&full[it % STAGES], (it / STAGES) & 1, abort);
+  }
+
+  // After a launch that gave up: the copies still in flight (again with a limit).
+  __device__ __forceinline__ void drain(int steps, volatile int* abort) const {
+    if (!*abort || threadIdx.x != 0) return;
+    int never = 0;
+    for (int it = max(0, steps - STAGES); it < steps; ++it) wait(it, &never);
+  }
+};
+
+// R rows of one warp from row t0, those outside [lo, hi) as zeros; words[r 32] is row r's.
+template <int R, typename T>
+__device__ __forceinline__ void copy_rows(uint32_t* words, const T* base, long long stride, int t0,
+                                          int lo, int hi, bool on) {
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    uint32_t bits = 0;
+    if (on && t0 + r >= lo && t0 + r < hi) {
+      const T v = base[(t0 + r) * stride];
+      memcpy(&bits, &v, sizeof v);
+    }
+    words[r * 32] = bits;
+  }
+}
+
+// Dynamic shared memory from its first 128-byte boundary on, as TMA wants it (the launch asks for
+// kAlign bytes more).
+constexpr int kAlign = 128;
+__device__ __forceinline__ uint32_t* aligned_128(uint32_t* p) {
+  return p + (((smem_u32(p) + 127u) & ~127u) - smem_u32(p)) / 4;
+}
+
+// The bounds of the sequences, from shared memory where they fit.
+__device__ __forceinline__ Packed near(const Packed& q, int* bounds) {
+  if (!q.off || q.n_seq >= kBounds) return q;
+  for (int i = threadIdx.x; i <= q.n_seq; i += kThreads) bounds[i] = q.off[i];
+  __syncthreads();
+  return {q.N, q.n_seq, bounds, q.len};
 }
 
 // ------------------------------------------------------------------ forward
 
 template <typename T>
 struct ForwardArgs {
+  CUtensorMap maps[2];  // g, x (ASYNC)
   Packed seq;
   int D, parts, cluster;
   const T *g, *x;
@@ -348,46 +386,69 @@ struct ForwardArgs {
   int* dev_status;
 };
 
-template <typename T, int CH, bool MIX>
-__global__ void __launch_bounds__(32 * kWarps, 2) glr_forward_kernel(const ForwardArgs<T> p) {
-  constexpr int R = 16, ROWS = kWarps * R;
+template <typename T, int CH, bool MIX, bool ASYNC>
+__global__ void __launch_bounds__(kThreads, 2)
+    glr_forward_kernel(const __grid_constant__ ForwardArgs<T> p) {
+  constexpr int R = kForwardRows, ROWS = kWarps * R;
+  extern __shared__ uint32_t dynamic[];
+  uint32_t* ring = aligned_128(dynamic);
+  __shared__ uint64_t full[kForwardStages];
   __shared__ Exchange<CH> xch;
   __shared__ Marks<ROWS> marks;
+  __shared__ int bounds[kBounds];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = blockIdx.x % p.cluster, part = blockIdx.x / p.cluster;
-  const int d0 = (blockIdx.y * 32 + lane) * CH;
-  const bool on = d0 < p.D;
-  const int d = on ? d0 : p.D - CH;  // lanes past the last channel load it too
+  const int d = (blockIdx.y * 32 + lane) * CH;
+  const bool on = d < p.D;
   const long long D = p.D;
   if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seq, p.dev_status);
-  const int lo = part_begin(p.seq, part, p.parts), hi = part_begin(p.seq, part + 1, p.parts);
-
-  if (p.seq.off && p.h_T && on)  // empty sequences hand their state on
-    for (int s = blockIdx.x * kWarps + warp; s < p.seq.n_seq; s += gridDim.x * kWarps)
-      if (bound_of(p.seq, s) >= bound_of(p.seq, s + 1))
-#pragma unroll
-        for (int c = 0; c < CH; ++c) p.h_T[s * D + d + c] = p.h0 ? p.h0[s * D + d + c] : 0.f;
+  const Packed seq = near(p.seq, bounds);
+  const int lo = part_begin(seq, part, p.parts), hi = part_begin(seq, part + 1, p.parts);
 
   const int base = lo / ROWS * ROWS, step = ROWS * p.cluster;
   const int steps = hi > lo ? (hi - base + step - 1) / step : 0;
-  Piece<T, CH> g[R], x[R];
+  const Tiles<2, kForwardStages, ROWS, ASYNC> tiles{ring, full};
+  const auto load = [&](int it) {  // one thread
+    if (it < steps)
+      tiles.load(it, p.maps, blockIdx.y * 32 * CH, base + (it * p.cluster + rank) * ROWS);
+  };
+  exchange_init(xch, p.cluster, tiles);
+  if (ASYNC && threadIdx.x == 0)
+    for (int it = 0; it < kForwardStages; ++it) load(it);
+
+  if (seq.off && p.h_T && on)  // empty sequences hand their state on
+    for (int s = blockIdx.x * kWarps + warp; s < seq.n_seq; s += gridDim.x * kWarps)
+      if (bound_of(seq, s) >= bound_of(seq, s + 1))
+#pragma unroll
+        for (int c = 0; c < CH; ++c) p.h_T[s * D + d + c] = p.h0 ? p.h0[s * D + d + c] : 0.f;
+
   Walker<false, ROWS> walk;
-  walk.start(p.seq);
+  walk.start(seq);
   float state[CH] = {};
-  if (steps) {
-    fetch(g, p.g, p.ld_g, d, base + rank * ROWS + warp * R, lo, hi);
-    fetch(x, p.x, p.ld_x, d, base + rank * ROWS + warp * R, lo, hi);
-  }
-  exchange_init(xch, p.cluster);
   for (int it = 0; it < steps; ++it) {
     const int tile = base + (it * p.cluster + rank) * ROWS, t0 = tile + warp * R;
     unsigned firsts = 0, lasts = 0;
-    const bool marked = walk.mark(p.seq, tile, marks);
+    const bool marked = walk.mark(seq, tile, marks);
     if (marked) {
       __syncthreads();
       const int mine = warp * R + (lane & (R - 1));
       firsts = __ballot_sync(~0u, marks.first[mine] >= 0) & ((1u << R) - 1);
       lasts = __ballot_sync(~0u, marks.last[mine] >= 0) & ((1u << R) - 1);
+    }
+    uint32_t* raw_g = tiles.at(it % kForwardStages, 0) + warp * R * 32 + lane;
+    uint32_t* raw_x = tiles.at(it % kForwardStages, 1) + warp * R * 32 + lane;
+    const bool whole = t0 >= lo && t0 + R <= hi;
+    if (ASYNC) {
+      if (!tiles.wait(it, &xch.abort)) give_up(&xch.abort, p.dev_status);
+      if (!whole) {  // rows of others and padding: the state goes through
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (t0 + r < lo || t0 + r >= hi) raw_g[r * 32] = raw_x[r * 32] = 0;
+        fence_proxy_async_smem();  // TMA writes these words next
+      }
+    } else {
+      copy_rows<R>(raw_g, p.g + d, p.ld_g, t0, lo, hi, on);
+      copy_rows<R>(raw_x, p.x + d, p.ld_x, t0, lo, hi, on);
     }
 
     // the span's pair; a[r], b[r] stay for the second pass
@@ -396,25 +457,23 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_forward_kernel(const Forwa
 #pragma unroll
     for (int c = 0; c < CH; ++c) pair.A[c] = 1.f, pair.H[c] = 0.f;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r) {
+      const uint32_t wg = raw_g[r * 32], wx = raw_x[r * 32];
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const float lg = g[r].get(c), xv = x[r].get(c);
+        const float lg = get(wg, c, T()), xv = get(wx, c, T());
         a[r][c] = decay_of(lg);
         b[r][c] = MIX ? one_minus(lg, a[r][c]) * xv : xv;
         pair.A[c] *= a[r][c];
         pair.H[c] = fmaf(a[r][c], pair.H[c], b[r][c]);
       }
-    if (it + 1 < steps) {
-      fetch(g, p.g, p.ld_g, d, t0 + step, lo, hi);
-      fetch(x, p.x, p.ld_x, d, t0 + step, lo, hi);
     }
     if (firsts) {  // again, with the initial states
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          if ((firsts >> r & 1) && p.h0)
+          if ((firsts >> r & 1) && p.h0 && on)
             b[r][c] = fmaf(a[r][c], p.h0[marks.first[warp * R + r] * D + d + c], b[r][c]);
           pair.H[c] = firsts >> r & 1 ? b[r][c] : fmaf(a[r][c], pair.H[c], b[r][c]);
         }
@@ -422,18 +481,20 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_forward_kernel(const Forwa
       for (int c = 0; c < CH; ++c) pair.A[c] = -1.f;
     }
 
-    join(xch, it, pair, warp, rank, p.cluster, lane, state, h, p.dev_status);
+    join(xch, it, pair, warp, rank, p.cluster, lane, state, h, p.dev_status, [&] {
+      if (ASYNC && threadIdx.x == 0) load(it + kForwardStages);  // over the tile just read
+    });
 
     if (p.h_chunks && on && t0 % kChunk == 0 && t0 >= lo && t0 < hi)
 #pragma unroll
       for (int c = 0; c < CH; ++c) p.h_chunks[t0 / kChunk * D + d + c] = firsts & 1 ? 0.f : h[c];
     T* out = p.h + t0 * D + d;
-    if (!marked && t0 >= lo && t0 + R <= hi) {
+    if (!marked && whole) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) h[c] = fmaf(a[r][c], h[c], b[r][c]);
-        if (on) Piece<T, CH>::store(out, h);
+        if (on) put(out, h);
         out += D;
       }
     } else {
@@ -443,7 +504,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_forward_kernel(const Forwa
         for (int c = 0; c < CH; ++c)
           h[c] = firsts >> r & 1 ? b[r][c] : fmaf(a[r][c], h[c], b[r][c]);
         if (on && t0 + r >= lo && t0 + r < hi) {
-          Piece<T, CH>::store(out + r * D, h);
+          put(out + r * D, h);
           if ((lasts >> r & 1) && p.h_T)
 #pragma unroll
             for (int c = 0; c < CH; ++c) p.h_T[marks.last[warp * R + r] * D + d + c] = h[c];
@@ -452,6 +513,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_forward_kernel(const Forwa
     }
     if (marked) __syncthreads();  // the marks are rewritten
   }
+  if (ASYNC) tiles.drain(steps, &xch.abort);
   if (p.cluster > 1) cluster_sync();  // no block leaves while another may still write to it
 }
 
@@ -464,6 +526,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_forward_kernel(const Forwa
 
 template <typename T>
 struct BackwardArgs {
+  CUtensorMap maps[3];  // g, x, dh (ASYNC)
   Packed seq;
   int D, parts, cluster;
   const T *g, *x, *dh;
@@ -474,65 +537,93 @@ struct BackwardArgs {
   int* dev_status;
 };
 
-template <typename T, int CH, bool MIX>
-__global__ void __launch_bounds__(32 * kWarps, 2) glr_backward_kernel(const BackwardArgs<T> p) {
-  constexpr int R = 8, ROWS = kWarps * R;
+template <typename T, int CH, bool MIX, bool ASYNC>
+__global__ void __launch_bounds__(kThreads, 2)
+    glr_backward_kernel(const __grid_constant__ BackwardArgs<T> p) {
+  constexpr int R = kBackwardRows, ROWS = kWarps * R;
   static_assert(ROWS == kChunk, "a tile begins at a kept state");
+  extern __shared__ uint32_t dynamic[];
+  uint32_t* ring = aligned_128(dynamic);
+  __shared__ uint64_t full[kBackwardStages];
   __shared__ Exchange<CH> xch;
   __shared__ Pair<CH> ahead[2][kWarps][32];  // the forward pairs of the warps
   __shared__ Marks<ROWS> marks;
+  __shared__ int bounds[kBounds];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = blockIdx.x % p.cluster, part = blockIdx.x / p.cluster;
-  const int d0 = (blockIdx.y * 32 + lane) * CH;
-  const bool on = d0 < p.D;
-  const int d = on ? d0 : p.D - CH;
+  const int d = (blockIdx.y * 32 + lane) * CH;
+  const bool on = d < p.D;
   const long long D = p.D;
   if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seq, p.dev_status);
-  const int lo = part_begin(p.seq, part, p.parts), hi = part_begin(p.seq, part + 1, p.parts);
-
-  if (p.seq.off && p.dh0 && on)  // empty sequences hand their gradient on
-    for (int s = blockIdx.x * kWarps + warp; s < p.seq.n_seq; s += gridDim.x * kWarps)
-      if (bound_of(p.seq, s) >= bound_of(p.seq, s + 1))
-#pragma unroll
-        for (int c = 0; c < CH; ++c) p.dh0[s * D + d + c] = p.dh_T ? p.dh_T[s * D + d + c] : 0.f;
+  const Packed seq = near(p.seq, bounds);
+  const int lo = part_begin(seq, part, p.parts), hi = part_begin(seq, part + 1, p.parts);
 
   const int top = (hi + ROWS - 1) / ROWS * ROWS, step = ROWS * p.cluster;
   const int steps = hi > lo ? (top - lo / ROWS * ROWS + step - 1) / step : 0;
-  Piece<T, CH> g[R], x[R], dh[R];
-  float kept[CH] = {};
-  const auto fetch_tile = [&](Piece<T, CH>(&gt)[R], Piece<T, CH>(&xt)[R], Piece<T, CH>(&dt)[R],
-                              float(&kt)[CH], int tile) {
-    fetch(gt, p.g, p.ld_g, d, tile + warp * R, lo, hi);
-    fetch(xt, p.x, p.ld_x, d, tile + warp * R, lo, hi);
-    fetch(dt, p.dh, D, d, tile + warp * R, lo, hi);
-    if (tile >= 0 && tile < hi)
-#pragma unroll
-      for (int c = 0; c < CH; ++c) kt[c] = p.h_chunks[tile / kChunk * D + d + c];
+  const Tiles<3, kBackwardStages, ROWS, ASYNC> tiles{ring, full};
+  const auto load = [&](int it) {  // one thread
+    if (it < steps)
+      tiles.load(it, p.maps, blockIdx.y * 32 * CH, top - (it * p.cluster + rank + 1) * ROWS);
   };
+  exchange_init(xch, p.cluster, tiles);
+  if (ASYNC && threadIdx.x == 0)
+    for (int it = 0; it < kBackwardStages - 1; ++it) load(it);
+  const auto kept_state = [&](int it, float(&k)[CH]) {
+    const int tile = top - (it * p.cluster + rank + 1) * ROWS;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      k[c] = on && it < steps && tile >= 0 ? p.h_chunks[tile / kChunk * D + d + c] : 0.f;
+  };
+
+  if (seq.off && p.dh0 && on)  // empty sequences hand their gradient on
+    for (int s = blockIdx.x * kWarps + warp; s < seq.n_seq; s += gridDim.x * kWarps)
+      if (bound_of(seq, s) >= bound_of(seq, s + 1))
+#pragma unroll
+        for (int c = 0; c < CH; ++c) p.dh0[s * D + d + c] = p.dh_T ? p.dh_T[s * D + d + c] : 0.f;
+
   Walker<true, ROWS> walk;
-  walk.start(p.seq);
-  float state[CH] = {};
-  if (steps) fetch_tile(g, x, dh, kept, top - (rank + 1) * ROWS);
-  exchange_init(xch, p.cluster);
+  walk.start(seq);
+  float state[CH] = {}, kept[CH];
+  kept_state(0, kept);
   for (int it = 0; it < steps; ++it) {
     const int tile = top - (it * p.cluster + rank + 1) * ROWS, t0 = tile + warp * R;
     unsigned firsts = 0, lasts = 0;
-    const bool marked = walk.mark(p.seq, tile, marks);
+    const bool marked = walk.mark(seq, tile, marks);
     if (marked) {
       __syncthreads();
       const int mine = warp * R + (lane & (R - 1));
       firsts = __ballot_sync(~0u, marks.first[mine] >= 0) & ((1u << R) - 1);
       lasts = __ballot_sync(~0u, marks.last[mine] >= 0) & ((1u << R) - 1);
     }
+    uint32_t* raw[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) raw[i] = tiles.at(it % kBackwardStages, i) + warp * R * 32 + lane;
+    const bool whole = t0 >= lo && t0 + R <= hi;
+    if (ASYNC) {
+      if (!tiles.wait(it, &xch.abort)) give_up(&xch.abort, p.dev_status);
+      if (!whole) {  // rows of others and padding: state and gradient go through
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (t0 + r < lo || t0 + r >= hi)
+            raw[0][r * 32] = raw[1][r * 32] = raw[2][r * 32] = 0;
+        fence_proxy_async_smem();  // TMA writes these words next
+      }
+    } else {
+      copy_rows<R>(raw[0], p.g + d, p.ld_g, t0, lo, hi, on);
+      copy_rows<R>(raw[1], p.x + d, p.ld_x, t0, lo, hi, on);
+      copy_rows<R>(raw[2], p.dh + d, D, t0, lo, hi, on);
+    }
+    const auto x = [&](int r, int c) { return get(raw[1][r * 32], c, T()); };
+    const auto dh = [&](int r, int c) { return get(raw[2][r * 32], c, T()); };
     const auto state_before = [&](int r, int c) {  // of the sequence that begins in row r
-      return p.h0 ? p.h0[marks.first[warp * R + r] * D + d + c] : 0.f;
+      return on && p.h0 ? p.h0[marks.first[warp * R + r] * D + d + c] : 0.f;
     };
     const auto grad_after = [&](int r, int c) {  // of the sequence that ends in row r
-      return p.dh_T ? p.dh_T[marks.last[warp * R + r] * D + d + c] : 0.f;
+      return on && p.dh_T ? p.dh_T[marks.last[warp * R + r] * D + d + c] : 0.f;
     };
 
     float a[R][CH], om[MIX ? R : 1][CH] = {};  // exp(g), 1 - exp(g)
-    const auto input = [&](int r, int c) { return MIX ? om[r][c] * x[r].get(c) : x[r].get(c); };
+    const auto input = [&](int r, int c) { return MIX ? om[r][c] * x(r, c) : x(r, c); };
     Pair<CH> fwd, rev;
 #pragma unroll
     for (int c = 0; c < CH; ++c) fwd.A[c] = 1.f, fwd.H[c] = rev.H[c] = 0.f;
@@ -540,7 +631,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_backward_kernel(const Back
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const float lg = g[r].get(c);
+        const float lg = get(raw[0][r * 32], c, T());
         a[r][c] = decay_of(lg);
         if (MIX) om[r][c] = one_minus(lg, a[r][c]);
         fwd.A[c] *= a[r][c];
@@ -549,7 +640,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_backward_kernel(const Back
 #pragma unroll
     for (int r = R - 1; r >= 0; --r)
 #pragma unroll
-      for (int c = 0; c < CH; ++c) rev.H[c] = a[r][c] * (dh[r].get(c) + rev.H[c]);
+      for (int c = 0; c < CH; ++c) rev.H[c] = a[r][c] * (dh(r, c) + rev.H[c]);
 #pragma unroll
     for (int c = 0; c < CH; ++c) rev.A[c] = fwd.A[c];
     if (firsts) {  // again, from the initial states
@@ -568,17 +659,18 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_backward_kernel(const Back
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           if (lasts >> r & 1) rev.H[c] = grad_after(r, c);
-          rev.H[c] = a[r][c] * (dh[r].get(c) + rev.H[c]);
+          rev.H[c] = a[r][c] * (dh(r, c) + rev.H[c]);
           rev.A[c] = -1.f;
         }
     }
     ahead[it & 1][warp][lane] = fwd;
-    Piece<T, CH> g_next[R], x_next[R], dh_next[R];
-    float kept_next[CH] = {};
-    if (it + 1 < steps) fetch_tile(g_next, x_next, dh_next, kept_next, tile - step);
+    float kept_next[CH];
+    kept_state(it + 1, kept_next);
 
     float back[CH];
-    join(xch, it, rev, kWarps - 1 - warp, rank, p.cluster, lane, state, back, p.dev_status);
+    join(xch, it, rev, kWarps - 1 - warp, rank, p.cluster, lane, state, back, p.dev_status, [&] {
+      if (ASYNC && threadIdx.x == 0) load(it + kBackwardStages - 1);  // over the step before's tile
+    });
 
     float h[CH], before[R][CH];
 #pragma unroll
@@ -588,12 +680,12 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_backward_kernel(const Back
       if (w < warp) follow(h, ahead[it & 1][w][lane]);
     T* dg = p.dg + (t0 + R - 1) * p.ld_g + d;
     T* dx = p.dx + (t0 + R - 1) * p.ld_x + d;
-    if (!marked && t0 >= lo && t0 + R <= hi) {
+    if (!marked && whole) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          before[r][c] = MIX ? h[c] - x[r].get(c) : h[c];
+          before[r][c] = MIX ? h[c] - x(r, c) : h[c];
           h[c] = fmaf(a[r][c], h[c], input(r, c));
         }
 #pragma unroll
@@ -601,14 +693,14 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_backward_kernel(const Back
         float o_g[CH], o_x[CH];
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          const float lam = dh[r].get(c) + back[c];
+          const float lam = dh(r, c) + back[c];
           back[c] = a[r][c] * lam;
           o_x[c] = MIX ? om[r][c] * lam : lam;
           o_g[c] = back[c] * before[r][c];
         }
         if (on) {
-          Piece<T, CH>::store(dg, o_g);
-          Piece<T, CH>::store(dx, o_x);
+          put(dg, o_g);
+          put(dx, o_x);
         }
         dg -= p.ld_g;
         dx -= p.ld_x;
@@ -619,7 +711,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_backward_kernel(const Back
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           if (firsts >> r & 1) h[c] = state_before(r, c);
-          before[r][c] = MIX ? h[c] - x[r].get(c) : h[c];
+          before[r][c] = MIX ? h[c] - x(r, c) : h[c];
           h[c] = fmaf(a[r][c], h[c], input(r, c));
         }
 #pragma unroll
@@ -628,14 +720,14 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_backward_kernel(const Back
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           if (lasts >> r & 1) back[c] = grad_after(r, c);
-          const float lam = dh[r].get(c) + back[c];
+          const float lam = dh(r, c) + back[c];
           back[c] = a[r][c] * lam;
           o_x[c] = MIX ? om[r][c] * lam : lam;
           o_g[c] = back[c] * before[r][c];
         }
         if (on && t0 + r >= lo && t0 + r < hi) {
-          Piece<T, CH>::store(dg - (R - 1 - r) * p.ld_g, o_g);
-          Piece<T, CH>::store(dx - (R - 1 - r) * p.ld_x, o_x);
+          put(dg - (R - 1 - r) * p.ld_g, o_g);
+          put(dx - (R - 1 - r) * p.ld_x, o_x);
           if ((firsts >> r & 1) && p.dh0)
 #pragma unroll
             for (int c = 0; c < CH; ++c) p.dh0[marks.first[warp * R + r] * D + d + c] = back[c];
@@ -644,10 +736,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_backward_kernel(const Back
     }
     if (marked) __syncthreads();  // the marks are rewritten
 #pragma unroll
-    for (int r = 0; r < R; ++r) g[r] = g_next[r], x[r] = x_next[r], dh[r] = dh_next[r];
-#pragma unroll
     for (int c = 0; c < CH; ++c) kept[c] = kept_next[c];
   }
+  if (ASYNC) tiles.drain(steps, &xch.abort);
   if (p.cluster > 1) cluster_sync();  // no block leaves while another may still write to it
 }
 
@@ -701,11 +792,16 @@ Grid grid_of(int N, int D, int n_seq, int width, int rows) {
   return g;
 }
 
+// Launches KERNEL with `ring` bytes of shared memory beside its own.
 template <typename Args>
-int launch(void (*kernel)(Args), const Grid& g, const Args& args, cudaStream_t stream) {
+int launch(void (*kernel)(Args), const Grid& g, int ring, const Args& args, cudaStream_t stream) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring) !=
+      cudaSuccess)
+    return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(g.cluster * g.parts, g.strips);
-  cfg.blockDim = dim3(32 * kWarps);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = ring;
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -716,21 +812,27 @@ int launch(void (*kernel)(Args), const Grid& g, const Args& args, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// Calls f(T{}, channels per lane, mode) for the call's type: two bf16 channels per lane where
-// every row of every tensor is 4-byte aligned, else one.
+// Calls f(T{}, channels per lane, mode, ASYNC) for the call's type.  Tensors whose rows all begin
+// on 16-byte boundaries (and do not share one row) are copied by TMA.
 template <typename F>
-int dispatch(int D, int mode, int dtype, std::initializer_list<const void*> ptrs,
+int dispatch(int mode, int dtype, std::initializer_list<const void*> ptrs,
              std::initializer_list<long long> strides, F f) {
   using std::integral_constant;
-  const auto with_mode = [&](auto type, auto ch) {
-    return mode == MOE_GLR_MIX ? f(type, ch, std::true_type{}) : f(type, ch, std::false_type{});
+  using One = integral_constant<int, 1>;
+  using Two = integral_constant<int, 2>;
+  const int size = dtype == MOE_F32 ? 4 : 2;
+  bool aligned = true;
+  for (const void* q : ptrs) aligned = aligned && !misaligned(q, 16);
+  for (long long s : strides) aligned = aligned && s > 0 && s * size % 16 == 0;
+  const auto with_mode = [&](auto type, auto ch, auto async) {
+    return mode == MOE_GLR_MIX ? f(type, ch, std::true_type{}, async)
+                               : f(type, ch, std::false_type{}, async);
   };
-  if (dtype == MOE_F32) return with_mode(float{}, integral_constant<int, 1>{});
-  bool two = D % 2 == 0;
-  for (const void* q : ptrs) two = two && !misaligned(q, 4);
-  for (long long s : strides) two = two && s % 2 == 0;
-  return two ? with_mode(__nv_bfloat16{}, integral_constant<int, 2>{})
-             : with_mode(__nv_bfloat16{}, integral_constant<int, 1>{});
+  if (dtype == MOE_F32)
+    return aligned ? with_mode(float{}, One{}, std::true_type{})
+                   : with_mode(float{}, One{}, std::false_type{});
+  return aligned ? with_mode(__nv_bfloat16{}, Two{}, std::true_type{})
+                 : with_mode(__nv_bfloat16{}, One{}, std::false_type{});
 }
 
 }  // namespace
@@ -761,14 +863,20 @@ int moe_glr_forward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off,
   const Packed seq{N, n_seq, seq_off, seq_off ? 0 : N / n_seq};
   mark_before(MOE_KERNEL_GLR_FWD, stream);
   const int e = dispatch(
-      D, mode, dtype, {g, x, h}, {ld_g, ld_x, D}, [&](auto type, auto ch, auto mix) {
+      mode, dtype, {g, x, h}, {ld_g, ld_x, D}, [&](auto type, auto ch, auto mix, auto async) {
         using T = decltype(type);
-        constexpr int CH = decltype(ch)::value;
-        const Grid gr = grid_of(N, D, n_seq, 32 * CH, 16 * kWarps);
-        const ForwardArgs<T> a{seq,  D,    gr.parts, gr.cluster, static_cast<const T*>(g),
-                               static_cast<const T*>(x), ld_g,   ld_x, h0, static_cast<T*>(h),
-                               h_T,  h_chunks, dev_status};
-        return launch(glr_forward_kernel<T, CH, decltype(mix)::value>, gr, a, stream);
+        constexpr int CH = decltype(ch)::value, ROWS = kForwardRows * kWarps;
+        constexpr bool ASYNC = decltype(async)::value, F32 = sizeof(T) == 4;
+        const Grid gr = grid_of(N, D, n_seq, 32 * CH, ROWS);
+        ForwardArgs<T> a{{}, seq, D, gr.parts, gr.cluster, static_cast<const T*>(g),
+                         static_cast<const T*>(x), ld_g, ld_x, h0, static_cast<T*>(h), h_T,
+                         h_chunks, dev_status};
+        if (ASYNC) {
+          if (int err = encode_map_rows(&a.maps[0], g, F32, D, N, ld_g, 32 * CH, ROWS)) return err;
+          if (int err = encode_map_rows(&a.maps[1], x, F32, D, N, ld_x, 32 * CH, ROWS)) return err;
+        }
+        return launch(glr_forward_kernel<T, CH, decltype(mix)::value, ASYNC>, gr,
+                      kForwardStages * 2 * ROWS * 128 + kAlign, a, stream);
       });
   mark_after(MOE_KERNEL_GLR_FWD, stream);
   count_launches(1);
@@ -786,15 +894,25 @@ int moe_glr_backward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off
   const Packed seq{N, n_seq, seq_off, seq_off ? 0 : N / n_seq};
   mark_before(MOE_KERNEL_GLR_BWD, stream);
   const int e = dispatch(
-      D, mode, dtype, {g, x, dh, dg, dx}, {ld_g, ld_x, D}, [&](auto type, auto ch, auto mix) {
+      mode, dtype, {g, x, dh, dg, dx}, {ld_g, ld_x, D},
+      [&](auto type, auto ch, auto mix, auto async) {
         using T = decltype(type);
         constexpr int CH = decltype(ch)::value;
+        constexpr bool ASYNC = decltype(async)::value, F32 = sizeof(T) == 4;
         const Grid gr = grid_of(N, D, n_seq, 32 * CH, kChunk);
-        const BackwardArgs<T> a{seq, D, gr.parts, gr.cluster, static_cast<const T*>(g),
-                                static_cast<const T*>(x), static_cast<const T*>(dh), ld_g, ld_x,
-                                h0, h_chunks, dh_T, static_cast<T*>(dg), static_cast<T*>(dx), dh0,
-                                dev_status};
-        return launch(glr_backward_kernel<T, CH, decltype(mix)::value>, gr, a, stream);
+        BackwardArgs<T> a{{}, seq, D, gr.parts, gr.cluster, static_cast<const T*>(g),
+                          static_cast<const T*>(x), static_cast<const T*>(dh), ld_g, ld_x, h0,
+                          h_chunks, dh_T, static_cast<T*>(dg), static_cast<T*>(dx), dh0,
+                          dev_status};
+        if (ASYNC) {
+          const void* in[3] = {g, x, dh};
+          const long long ld[3] = {ld_g, ld_x, D};
+          for (int i = 0; i < 3; ++i)
+            if (int err = encode_map_rows(&a.maps[i], in[i], F32, D, N, ld[i], 32 * CH, kChunk))
+              return err;
+        }
+        return launch(glr_backward_kernel<T, CH, decltype(mix)::value, ASYNC>, gr,
+                      kBackwardStages * 3 * kChunk * 128 + kAlign, a, stream);
       });
   mark_after(MOE_KERNEL_GLR_BWD, stream);
   count_launches(1);

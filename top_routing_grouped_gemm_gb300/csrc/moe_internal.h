@@ -122,6 +122,8 @@ int encode_map_kmajor(CUtensorMap* map, const void* base, uint64_t k_extent, uin
                       uint64_t groups, uint32_t box_rows);
 int encode_map_mnmajor(CUtensorMap* map, const void* base, uint64_t mn_extent,
                        uint64_t k_rows, uint64_t groups);
+int encode_map_rows(CUtensorMap* map, const void* base, bool fp32, uint64_t cols, uint64_t rows,
+                    uint64_t ld, uint32_t box_cols, uint32_t box_rows);
 int num_sms();
 
 // Kernel launchers (gemm_fwd.cu).  Return cudaError_t as int.
