@@ -14,14 +14,13 @@ namespace moe {
 namespace {
 
 constexpr int kChunk = 64;      // rows between the kept states
-constexpr int kWarps = 8;       // warps of a scan block
-constexpr int kThreads = 32 * kWarps;
+constexpr int kWarps = 8;       // warps of a scan block, beside the one that joins
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kRows = 8;        // rows of a warp in a tile
+constexpr int kTile = kWarps * kRows;
+constexpr int kStages = 3;      // tiles in shared memory
 constexpr int kMaxCluster = 8;  // blocks of a cluster (the portable limit)
-constexpr int kForwardRows = 16;  // rows of a warp in a tile
-constexpr int kBackwardRows = 8;
-constexpr int kForwardStages = 2;   // tiles in shared memory
-constexpr int kBackwardStages = 3;  // (one is still read while the next but one arrives)
-constexpr int kBounds = 1024;   // bounds of sequences that a block keeps in shared memory
+constexpr int kBounds = 512;    // bounds of sequences that a block keeps in shared memory
 
 __device__ __forceinline__ float ld(const float* p, long long i) { return p[i]; }
 __device__ __forceinline__ float ld(const __nv_bfloat16* p, long long i) {
@@ -96,93 +95,106 @@ __device__ __forceinline__ void check_offsets(const Packed& q, int* dev_status) 
   if (__syncthreads_or(bad) && threadIdx.x == 0) atomicCAS(dev_status, 0, MOE_ERR_BAD_INDEX);
 }
 
-// First row of part p of `parts`: the start of the first sequence that begins at or after row
-// p N / parts.  Whole sequences go to one part, and every block finds the same cuts.
-__device__ __forceinline__ int part_begin(const Packed& q, int p, int parts) {
-  if (p == 0) return 0;
-  if (p == parts) return bound_of(q, q.n_seq);
+// Part p of `parts` begins with the first sequence that begins at or after row p N / parts: its
+// index (off only) and its first row.  Whole sequences go to one part, and every block finds the
+// same cuts.  Called by whole blocks.
+struct Cut {
+  int seq, row;
+};
+
+__device__ __forceinline__ Cut part_begin(const Packed& q, int p, int parts) {
+  if (p == 0) return {0, 0};
+  if (p == parts) return {q.n_seq, bound_of(q, q.n_seq)};
   const int target = static_cast<int>(static_cast<long long>(p) * q.N / parts);
-  if (!q.off) return min((target + q.len - 1) / q.len, q.n_seq) * q.len;
+  if (!q.off) {
+    const int s = min((target + q.len - 1) / q.len, q.n_seq);
+    return {s, s * q.len};
+  }
   int before = 0;
   for (int s = 0; s < q.n_seq; s += blockDim.x) {
     const int i = s + threadIdx.x;
     before += __syncthreads_count(i < q.n_seq && q.off[i] < target);
   }
-  return bound_of(q, before);
+  return {before, bound_of(q, before)};
 }
 
-// Sequences that begin and end in the rows [t0, t0 + ROWS) of a tile: first[r], last[r] = the
-// sequence whose first or last row is t0 + r, else -1.
-template <int ROWS>
+// What begins and ends in the kRows rows of a warp: bit r of firsts and lasts for row r, and the
+// sequences (one warp's own words of shared memory).
 struct Marks {
-  int first[ROWS], last[ROWS];
+  int first[kRows], last[kRows];
 };
 
-// Walks the bounds of the sequences beside tiles that come in ascending (DOWN: descending)
-// order.  The state is the same in all threads of the block.
-template <bool DOWN, int ROWS>
+// Walks the bounds of the sequences beside a warp's rows, which come in ascending (DOWN:
+// descending) order.  The state is the same in all lanes.
+template <bool DOWN>
 struct Walker {
   int cursor;  // bounds passed (DOWN: bounds left)
   int next;    // the nearest bound that is not passed
 
-  __device__ __forceinline__ void start(const Packed& q) {
-    cursor = DOWN ? q.n_seq + 1 : 0;
-    next = DOWN ? 0x7fffffff : -1;
+  __device__ __forceinline__ void start(const Cut& from) {
+    cursor = DOWN ? from.seq + 1 : from.seq;
+    next = from.row;
   }
 
-  // Whether a sequence begins or ends in the tile at t0; then the marks are written, and the
-  // block has to meet before it reads them, and again before the next call.
-  __device__ __forceinline__ bool mark(const Packed& q, int t0, Marks<ROWS>& m) {
+  __device__ __forceinline__ void mark(const Packed& q, int t0, int lane, Marks& m,
+                                       unsigned& firsts, unsigned& lasts) {
+    firsts = lasts = 0;
     if (!q.off) {
-      // the first multiple of len that is not before the tile
-      const long long at = t0 <= 0 ? 0 : (static_cast<long long>(t0) + q.len - 1) / q.len * q.len;
-      if (at > t0 + ROWS) return false;
-    } else if (DOWN ? next < t0 : next > t0 + ROWS) {
-      return false;
+      // the first multiple of len that is not before the rows
+      if (t0 > 0 && (t0 + q.len - 1ll) / q.len * q.len > t0 + kRows) return;
+      __syncwarp();  // the words may still be read
+      const int t = t0 + lane;
+      const bool bound = lane <= kRows && t >= 0 && t <= q.N && t % q.len == 0;
+      const bool first = bound && lane < kRows && t < q.N, last = bound && lane > 0 && t > 0;
+      if (first) m.first[lane] = t / q.len;
+      if (last) m.last[lane - 1] = t / q.len - 1;
+      firsts = __ballot_sync(~0u, first);
+      lasts = __ballot_sync(~0u, last) >> 1;
+      __syncwarp();
+      return;
     }
-    for (int r = threadIdx.x; r < ROWS; r += blockDim.x) m.first[r] = m.last[r] = -1;
-    __syncthreads();
-    if (!q.off) {
-      for (int r = threadIdx.x; r <= ROWS; r += blockDim.x) {
-        const int t = t0 + r;
-        if (t >= 0 && t <= q.N && t % q.len == 0) {
-          if (r < ROWS && t < q.N) m.first[r] = t / q.len;
-          if (r > 0 && t > 0) m.last[r - 1] = t / q.len - 1;
-        }
-      }
-      return true;
-    }
+    if (DOWN ? next < t0 : next > t0 + kRows) return;
+    __syncwarp();
     while (true) {
-      const int j = DOWN ? cursor - 1 - static_cast<int>(threadIdx.x)
-                         : cursor + static_cast<int>(threadIdx.x);
+      const int j = DOWN ? cursor - 1 - lane : cursor + lane;
       bool passed = false;
+      unsigned first = 0, last = 0;
       if (j >= 0 && j <= q.n_seq) {
-        const int b = bound_of(q, j);
-        if (b >= t0 && b < t0 + ROWS && j < q.n_seq && bound_of(q, j + 1) > b) m.first[b - t0] = j;
-        if (b > t0 && b <= t0 + ROWS && j > 0 && bound_of(q, j - 1) < b) m.last[b - t0 - 1] = j - 1;
-        passed = DOWN ? b > t0 : b < t0 + ROWS;
+        const int b = bound_of(q, j), r = b - t0;
+        if (r >= 0 && r < kRows && j < q.n_seq && bound_of(q, j + 1) > b) {
+          m.first[r] = j;
+          first = 1u << r;
+        }
+        if (r > 0 && r <= kRows && j > 0 && bound_of(q, j - 1) < b) {
+          m.last[r - 1] = j - 1;
+          last = 1u << (r - 1);
+        }
+        passed = DOWN ? r > 0 : r < kRows;
       }
-      const int n = __syncthreads_count(passed);
+      firsts |= __reduce_or_sync(~0u, first);
+      lasts |= __reduce_or_sync(~0u, last);
+      const int n = __popc(__ballot_sync(~0u, passed));
       cursor += DOWN ? -n : n;
-      if (n < static_cast<int>(blockDim.x)) break;
+      if (n < 32) break;
     }
     if (DOWN)
       next = cursor > 0 ? bound_of(q, cursor - 1) : -0x7fffffff;
     else
       next = cursor <= q.n_seq ? bound_of(q, cursor) : 0x7fffffff;
-    return true;
+    __syncwarp();
   }
 };
 
 // ------------------------------------------------------------------ joining spans of time
 //
 // h -> a h + b is associative in pairs (A, H): h -> A h + H.  The time axis is cut into tiles of
-// 8 warps x R rows; the blocks of a cluster take neighbouring tiles, cluster after cluster of
-// them.  Each warp runs its R rows twice in registers: once for their pair, and, when the pairs
-// before it are known, once more from the state that these give.  Pairs are joined within a
-// block through shared memory and within the cluster through distributed shared memory, always
-// in the order of the recurrence.  A is -1 for a span in which a sequence begins: what came
-// before is then not used at all, not even multiplied by zero.
+// 8 warps x kRows rows; the blocks of a cluster take neighbouring tiles, cluster after cluster of
+// them.  Each warp runs its rows twice in registers: once for their pair, and, when the pairs
+// before it are known, once more from the state that these give.  A ninth warp joins the pairs,
+// always in the order of the recurrence: over the warps, over the blocks of the cluster (through
+// distributed shared memory) and from step to step; meanwhile the others form the pairs of the
+// next tile.  A is -1 for a span in which a sequence begins: what came before is then not used at
+// all, not even multiplied by zero.
 
 // (Aligned for the vector store that carries it.)
 template <int CH>
@@ -205,30 +217,49 @@ __device__ __forceinline__ void append(Pair<CH>& s, const Pair<CH>& p) {
   }
 }
 
-// Reports a wait that ran out.  The rest of the launch goes on without waiting (its results are
-// then wrong), so every barrier still gets all its threads.
-__device__ __forceinline__ void give_up(int* abort, int* dev_status) {
-  *reinterpret_cast<volatile int*>(abort) = 1;
-  report_status(dev_status, MOE_ERR_TIMEOUT);
-}
-
 // What the warps of a block and the blocks of a cluster exchange, double-buffered by the parity
-// of the step.  A block writes step n + 2 over step n only after it has every block's pair of
-// step n + 1, and a block publishes that only when all its warps have read step n.
-template <int CH>
+// of the step.  A warp forms its pair of step n + 2 after it has its state of step n, which the
+// joining warp gives when it has read the pairs of step n; and that warp joins step n + 2 when
+// every warp has formed its pair, after using its state of step n.  A block sends its pair of
+// step n + 2 when it has every block's of step n + 1, and a block sends that after it has read
+// all of step n.
+template <int CH, int PAIRS>
 struct Exchange {
-  Pair<CH> warps[2][kWarps][32];
+  Pair<CH> warps[2][PAIRS][kWarps][32];
   Pair<CH> blocks[2][kMaxCluster][32];
-  uint64_t full[2];
+  float states[2][PAIRS][kWarps][32 * CH];
+  uint64_t formed[2], joined[2], received[2];
+  uint64_t loaded[kStages], freed[kStages];  // tiles
   int abort;
 };
 
-template <int CH, typename Tiles>
-__device__ __forceinline__ void exchange_init(Exchange<CH>& x, int cluster, const Tiles& tiles) {
-  tiles.init();
+// Waits, with a limit.  When it runs out the rest of the launch goes on without waiting (its
+// results are then wrong, and reported).
+__device__ __forceinline__ void wait_for(uint64_t* bar, int n, int* abort, int* dev_status) {
+  if (!mbar_wait(bar, n & 1, abort)) {
+    *reinterpret_cast<volatile int*>(abort) = 1;
+    report_status(dev_status, MOE_ERR_TIMEOUT);
+  }
+}
+
+// One lane's arrival for its warp.
+__device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+template <typename X>
+__device__ __forceinline__ void exchange_init(X& x, int cluster) {
   if (threadIdx.x == 0) {
-    mbar_init(&x.full[0], 1);
-    mbar_init(&x.full[1], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&x.formed[i], kWarps);
+      mbar_init(&x.joined[i], 1);
+      mbar_init(&x.received[i], 1);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&x.loaded[i], 1);
+      mbar_init(&x.freed[i], kWarps);
+    }
     x.abort = 0;
     fence_barrier_init();
   }
@@ -236,14 +267,13 @@ __device__ __forceinline__ void exchange_init(Exchange<CH>& x, int cluster, cons
   if (cluster > 1) cluster_sync();  // every block runs, its barriers set, before one writes there
 }
 
-// Sends a warp's joined pair to every block of the cluster (itself too), where it counts towards
-// the barrier of the step.
+// Sends a block's pair to every block of the cluster (itself too), where it counts towards the
+// barrier of the step.
 template <int CH>
-__device__ __forceinline__ void publish(Exchange<CH>& x, int buf, const Pair<CH>& p, int rank,
-                                        int cluster, int lane) {
+__device__ __forceinline__ void publish(Pair<CH>* slot, uint64_t* received, const Pair<CH>& p,
+                                        int cluster) {
   for (int q = 0; q < cluster; ++q) {
-    const uint32_t to = cluster_addr(&x.blocks[buf][rank][lane], q);
-    const uint32_t bar = cluster_addr(&x.full[buf], q);
+    const uint32_t to = cluster_addr(slot, q), bar = cluster_addr(received, q);
     if constexpr (CH == 2)
       asm volatile(
           "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, "
@@ -260,27 +290,23 @@ __device__ __forceinline__ void publish(Exchange<CH>& x, int buf, const Pair<CH>
   }
 }
 
-// Joins the pairs of step `it`: `carry` becomes the state in front of this warp's span, `state`
-// goes on over the whole step.  `order` is the warp's place in the order of the recurrence.  At
-// `meet` all warps have read the step's tile once.
-template <int CH, typename Meet>
-__device__ __forceinline__ void join(Exchange<CH>& x, int it, const Pair<CH>& mine, int order,
-                                     int rank, int cluster, int lane, float (&state)[CH],
-                                     float (&carry)[CH], int* dev_status, Meet meet) {
+// The joining warp's part of a step: `pairs` (order w is at warps[PAIR][DOWN ? 7 - w : w]) give
+// every warp its state in states[PAIR] and move `state` over the whole step.
+template <bool DOWN, int PAIR, int CH, int PAIRS>
+__device__ __forceinline__ void join(Exchange<CH, PAIRS>& x, int it, int rank, int cluster,
+                                     int lane, float (&state)[CH], int* dev_status) {
   const int buf = it & 1;
-  x.warps[buf][order][lane] = mine;
-  if (cluster > 1 && threadIdx.x == 0)
-    mbar_arrive_expect_tx(&x.full[buf], cluster * 32 * sizeof(Pair<CH>));
-  __syncthreads();
-  meet();
-  if (cluster > 1) {
-    if (order == 0) {
-      Pair<CH> sum = mine;
+  Pair<CH> pairs[kWarps];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) append(sum, x.warps[buf][w][lane]);
-      publish(x, buf, sum, rank, cluster, lane);
-    }
-    if (!mbar_wait(&x.full[buf], (it >> 1) & 1, &x.abort)) give_up(&x.abort, dev_status);
+  for (int w = 0; w < kWarps; ++w) pairs[w] = x.warps[buf][PAIR][DOWN ? kWarps - 1 - w : w][lane];
+  float carry[CH];
+  if (cluster > 1) {
+    Pair<CH> sum = pairs[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) append(sum, pairs[w]);
+    if (lane == 0) mbar_arrive_expect_tx(&x.received[buf], cluster * 32 * sizeof(Pair<CH>));
+    publish(&x.blocks[buf][rank][lane], &x.received[buf], sum, cluster);
+    wait_for(&x.received[buf], it >> 1, &x.abort, dev_status);
 #pragma unroll
     for (int q = 0; q < kMaxCluster; ++q) {
       if (q == rank)
@@ -288,65 +314,57 @@ __device__ __forceinline__ void join(Exchange<CH>& x, int it, const Pair<CH>& mi
         for (int c = 0; c < CH; ++c) carry[c] = state[c];
       if (q < cluster) follow(state, x.blocks[buf][q][lane]);
     }
-#pragma unroll
-    for (int w = 0; w < kWarps - 1; ++w)
-      if (w < order) follow(carry, x.warps[buf][w][lane]);
   } else {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == order)
-#pragma unroll
-        for (int c = 0; c < CH; ++c) carry[c] = state[c];
-      follow(state, x.warps[buf][w][lane]);
-    }
+    for (int c = 0; c < CH; ++c) carry[c] = state[c];
   }
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    float* to = &x.states[buf][PAIR][DOWN ? kWarps - 1 - w : w][lane * CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) to[c] = carry[c];
+    follow(carry, pairs[w]);
+  }
+  if (cluster == 1)
+#pragma unroll
+    for (int c = 0; c < CH; ++c) state[c] = carry[c];
 }
 
 // ------------------------------------------------------------------ tiles in shared memory
 //
-// STAGES tiles of ARRAYS inputs, each [ROWS][32] words: the word of a lane holds its CH channels.
-// Where rows begin on 16-byte boundaries, one thread has TMA copy whole tiles two steps ahead
-// (ASYNC); elsewhere each warp copies its rows through registers when they are asked for.
-template <int ARRAYS, int STAGES, int ROWS, bool ASYNC>
-struct Tiles {
-  uint32_t* words;
-  uint64_t* full;  // [STAGES] barriers (ASYNC)
+// kStages tiles of ARRAYS inputs, each [kTile][32] words: the word of a lane holds its CH
+// channels.  Where rows begin on 16-byte boundaries, the joining warp has TMA copy whole tiles
+// ahead (ASYNC); elsewhere each warp copies its rows through registers when they are asked for.
+template <int ARRAYS>
+__device__ __forceinline__ uint32_t* tile_at(uint32_t* ring, int it, int array) {
+  return ring + (it % kStages * ARRAYS + array) * kTile * 32;
+}
 
-  __device__ __forceinline__ uint32_t* at(int stage, int array) const {
-    return words + (stage * ARRAYS + array) * ROWS * 32;
-  }
+// One thread: the copies of step `it`, the tile at row t0 of the strip at channel d0.
+template <int ARRAYS>
+__device__ __forceinline__ void load_tile(uint32_t* ring, uint64_t* loaded, const CUtensorMap* maps,
+                                          int it, int d0, int t0) {
+  uint64_t* bar = &loaded[it % kStages];
+  mbar_arrive_expect_tx(bar, ARRAYS * kTile * 128);
+  const uint64_t policy = l2_policy_evict_first();
+  for (int i = 0; i < ARRAYS; ++i)
+    tma_load_2d(tile_at<ARRAYS>(ring, it, i), &maps[i], bar, d0, t0, policy);
+}
 
-  __device__ __forceinline__ void init() const {
-    if (ASYNC && threadIdx.x == 0)
-      for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
-  }
+// One thread, after a launch that gave up: the copies still in flight (again with a limit).
+__device__ __forceinline__ void drain(uint64_t* loaded, int steps, volatile int* abort) {
+  if (!*abort) return;
+  int never = 0;
+  for (int it = max(0, steps - kStages); it < steps; ++it)
+    mbar_wait(&loaded[it % kStages], (it / kStages) & 1, &never);
+}
 
-  // One thread: the copies of step `it`, the tile at row t0 of the strip at channel d0.
-  __device__ __forceinline__ void load(int it, const CUtensorMap* maps, int d0, int t0) const {
-    const int stage = it % STAGES;
-    mbar_arrive_expect_tx(&full[stage], ARRAYS * ROWS * 128);
-    const uint64_t policy = l2_policy_evict_first();
-    for (int i = 0; i < ARRAYS; ++i) tma_load_2d(at(stage, i), &maps[i], &full[stage], d0, t0, policy);
-  }
-
-  __device__ __forceinline__ bool wait(int it, volatile int* abort) const {
-    return mbar_wait(&full[it % STAGES], (it / STAGES) & 1, abort);
-  }
-
-  // After a launch that gave up: the copies still in flight (again with a limit).
-  __device__ __forceinline__ void drain(int steps, volatile int* abort) const {
-    if (!*abort || threadIdx.x != 0) return;
-    int never = 0;
-    for (int it = max(0, steps - STAGES); it < steps; ++it) wait(it, &never);
-  }
-};
-
-// R rows of one warp from row t0, those outside [lo, hi) as zeros; words[r 32] is row r's.
-template <int R, typename T>
+// A warp's rows from row t0, those outside [lo, hi) as zeros; words[r 32] is row r's.
+template <typename T>
 __device__ __forceinline__ void copy_rows(uint32_t* words, const T* base, long long stride, int t0,
                                           int lo, int hi, bool on) {
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
+  for (int r = 0; r < kRows; ++r) {
     uint32_t bits = 0;
     if (on && t0 + r >= lo && t0 + r < hi) {
       const T v = base[(t0 + r) * stride];
@@ -371,6 +389,16 @@ __device__ __forceinline__ Packed near(const Packed& q, int* bounds) {
   return {q.N, q.n_seq, bounds, q.len};
 }
 
+// to = from for the sequences without rows, from null: zero (a part of them for each warp).
+template <int CH>
+__device__ __forceinline__ void hand_on_empty(const Packed& q, const float* from, float* to,
+                                              long long D, int d, int warp) {
+  for (int s = blockIdx.x * kWarps + warp; s < q.n_seq; s += gridDim.x * kWarps)
+    if (bound_of(q, s) >= bound_of(q, s + 1))
+#pragma unroll
+      for (int c = 0; c < CH; ++c) to[s * D + d + c] = from ? from[s * D + d + c] : 0.f;
+}
+
 // ------------------------------------------------------------------ forward
 
 template <typename T>
@@ -389,12 +417,10 @@ struct ForwardArgs {
 template <typename T, int CH, bool MIX, bool ASYNC>
 __global__ void __launch_bounds__(kThreads, 2)
     glr_forward_kernel(const __grid_constant__ ForwardArgs<T> p) {
-  constexpr int R = kForwardRows, ROWS = kWarps * R;
   extern __shared__ uint32_t dynamic[];
   uint32_t* ring = aligned_128(dynamic);
-  __shared__ uint64_t full[kForwardStages];
-  __shared__ Exchange<CH> xch;
-  __shared__ Marks<ROWS> marks;
+  __shared__ Exchange<CH, 1> xch;
+  __shared__ Marks marks[2][kWarps];
   __shared__ int bounds[kBounds];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = blockIdx.x % p.cluster, part = blockIdx.x / p.cluster;
@@ -403,117 +429,130 @@ __global__ void __launch_bounds__(kThreads, 2)
   const long long D = p.D;
   if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seq, p.dev_status);
   const Packed seq = near(p.seq, bounds);
-  const int lo = part_begin(seq, part, p.parts), hi = part_begin(seq, part + 1, p.parts);
-
-  const int base = lo / ROWS * ROWS, step = ROWS * p.cluster;
+  const Cut from = part_begin(seq, part, p.parts);
+  const int lo = from.row, hi = part_begin(seq, part + 1, p.parts).row;
+  const int base = lo / kTile * kTile, step = kTile * p.cluster;
   const int steps = hi > lo ? (hi - base + step - 1) / step : 0;
-  const Tiles<2, kForwardStages, ROWS, ASYNC> tiles{ring, full};
-  const auto load = [&](int it) {  // one thread
-    if (it < steps)
-      tiles.load(it, p.maps, blockIdx.y * 32 * CH, base + (it * p.cluster + rank) * ROWS);
-  };
-  exchange_init(xch, p.cluster, tiles);
-  if (ASYNC && threadIdx.x == 0)
-    for (int it = 0; it < kForwardStages; ++it) load(it);
+  const auto tile_row = [&](int it) { return base + (it * p.cluster + rank) * kTile; };
+  exchange_init(xch, p.cluster);
 
-  if (seq.off && p.h_T && on)  // empty sequences hand their state on
-    for (int s = blockIdx.x * kWarps + warp; s < seq.n_seq; s += gridDim.x * kWarps)
-      if (bound_of(seq, s) >= bound_of(seq, s + 1))
-#pragma unroll
-        for (int c = 0; c < CH; ++c) p.h_T[s * D + d + c] = p.h0 ? p.h0[s * D + d + c] : 0.f;
-
-  Walker<false, ROWS> walk;
-  walk.start(seq);
-  float state[CH] = {};
-  for (int it = 0; it < steps; ++it) {
-    const int tile = base + (it * p.cluster + rank) * ROWS, t0 = tile + warp * R;
-    unsigned firsts = 0, lasts = 0;
-    const bool marked = walk.mark(seq, tile, marks);
-    if (marked) {
-      __syncthreads();
-      const int mine = warp * R + (lane & (R - 1));
-      firsts = __ballot_sync(~0u, marks.first[mine] >= 0) & ((1u << R) - 1);
-      lasts = __ballot_sync(~0u, marks.last[mine] >= 0) & ((1u << R) - 1);
+  if (warp == kWarps) {  // the joining warp
+    const auto load = [&](int it) {
+      if (ASYNC && lane == 0 && it < steps)
+        load_tile<2>(ring, xch.loaded, p.maps, it, blockIdx.y * 32 * CH, tile_row(it));
+    };
+    for (int it = 0; it < kStages; ++it) load(it);
+    float state[CH] = {};
+    for (int it = 0; it < steps; ++it) {
+      wait_for(&xch.formed[it & 1], it >> 1, &xch.abort, p.dev_status);
+      load(it + kStages);  // every warp has read this step's tile
+      join<false, 0>(xch, it, rank, p.cluster, lane, state, p.dev_status);
+      arrive_warp(&xch.joined[it & 1], lane);
     }
-    uint32_t* raw_g = tiles.at(it % kForwardStages, 0) + warp * R * 32 + lane;
-    uint32_t* raw_x = tiles.at(it % kForwardStages, 1) + warp * R * 32 + lane;
-    const bool whole = t0 >= lo && t0 + R <= hi;
-    if (ASYNC) {
-      if (!tiles.wait(it, &xch.abort)) give_up(&xch.abort, p.dev_status);
-      if (!whole) {  // rows of others and padding: the state goes through
+    if (ASYNC && lane == 0) drain(xch.loaded, steps, &xch.abort);
+  } else {
+    if (seq.off && p.h_T && on) hand_on_empty<CH>(seq, p.h0, p.h_T, D, d, warp);
+    struct Span {
+      float a[kRows][CH], b[kRows][CH];
+      unsigned firsts, lasts;
+    };
+    Walker<false> walk;
+    walk.start(from);
+
+    // the pair of the span of step `it`
+    const auto form = [&](int it, Span& s) {
+      const int t0 = tile_row(it) + warp * kRows;
+      const Marks& m = marks[it & 1][warp];
+      walk.mark(seq, t0, lane, marks[it & 1][warp], s.firsts, s.lasts);
+      uint32_t* g = tile_at<2>(ring, it, 0) + warp * kRows * 32 + lane;
+      uint32_t* x = tile_at<2>(ring, it, 1) + warp * kRows * 32 + lane;
+      if (ASYNC) {
+        wait_for(&xch.loaded[it % kStages], it / kStages, &xch.abort, p.dev_status);
+        if (t0 < lo || t0 + kRows > hi) {  // rows of others and padding: the state goes through
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-          if (t0 + r < lo || t0 + r >= hi) raw_g[r * 32] = raw_x[r * 32] = 0;
-        fence_proxy_async_smem();  // TMA writes these words next
+          for (int r = 0; r < kRows; ++r)
+            if (t0 + r < lo || t0 + r >= hi) g[r * 32] = x[r * 32] = 0;
+          fence_proxy_async_smem();  // TMA writes these words next
+        }
+      } else {
+        copy_rows(g, p.g + d, p.ld_g, t0, lo, hi, on);
+        copy_rows(x, p.x + d, p.ld_x, t0, lo, hi, on);
       }
-    } else {
-      copy_rows<R>(raw_g, p.g + d, p.ld_g, t0, lo, hi, on);
-      copy_rows<R>(raw_x, p.x + d, p.ld_x, t0, lo, hi, on);
-    }
-
-    // the span's pair; a[r], b[r] stay for the second pass
-    float a[R][CH], b[R][CH], h[CH];
-    Pair<CH> pair;
+      Pair<CH> pair;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) pair.A[c] = 1.f, pair.H[c] = 0.f;
+      for (int c = 0; c < CH; ++c) pair.A[c] = 1.f, pair.H[c] = 0.f;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const uint32_t wg = raw_g[r * 32], wx = raw_x[r * 32];
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const float lg = get(wg, c, T()), xv = get(wx, c, T());
-        a[r][c] = decay_of(lg);
-        b[r][c] = MIX ? one_minus(lg, a[r][c]) * xv : xv;
-        pair.A[c] *= a[r][c];
-        pair.H[c] = fmaf(a[r][c], pair.H[c], b[r][c]);
-      }
-    }
-    if (firsts) {  // again, with the initial states
-#pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int r = 0; r < kRows; ++r) {
+        const uint32_t wg = g[r * 32], wx = x[r * 32];
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          if ((firsts >> r & 1) && p.h0 && on)
-            b[r][c] = fmaf(a[r][c], p.h0[marks.first[warp * R + r] * D + d + c], b[r][c]);
-          pair.H[c] = firsts >> r & 1 ? b[r][c] : fmaf(a[r][c], pair.H[c], b[r][c]);
+          const float lg = get(wg, c, T()), xv = get(wx, c, T());
+          s.a[r][c] = decay_of(lg);
+          s.b[r][c] = MIX ? one_minus(lg, s.a[r][c]) * xv : xv;
+          pair.A[c] *= s.a[r][c];
+          pair.H[c] = fmaf(s.a[r][c], pair.H[c], s.b[r][c]);
         }
-#pragma unroll
-      for (int c = 0; c < CH; ++c) pair.A[c] = -1.f;
-    }
-
-    join(xch, it, pair, warp, rank, p.cluster, lane, state, h, p.dev_status, [&] {
-      if (ASYNC && threadIdx.x == 0) load(it + kForwardStages);  // over the tile just read
-    });
-
-    if (p.h_chunks && on && t0 % kChunk == 0 && t0 >= lo && t0 < hi)
-#pragma unroll
-      for (int c = 0; c < CH; ++c) p.h_chunks[t0 / kChunk * D + d + c] = firsts & 1 ? 0.f : h[c];
-    T* out = p.h + t0 * D + d;
-    if (!marked && whole) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-#pragma unroll
-        for (int c = 0; c < CH; ++c) h[c] = fmaf(a[r][c], h[c], b[r][c]);
-        if (on) put(out, h);
-        out += D;
       }
-    } else {
+      if (s.firsts) {  // again, with the initial states
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            if ((s.firsts >> r & 1) && p.h0 && on)
+              s.b[r][c] = fmaf(s.a[r][c], p.h0[m.first[r] * D + d + c], s.b[r][c]);
+            pair.H[c] = s.firsts >> r & 1 ? s.b[r][c] : fmaf(s.a[r][c], pair.H[c], s.b[r][c]);
+            pair.A[c] = -1.f;
+          }
+      }
+      xch.warps[it & 1][0][warp][lane] = pair;
+      arrive_warp(&xch.formed[it & 1], lane);
+    };
+
+    // the rows of step `it` from the state in front of them
+    const auto finish = [&](int it, Span& s) {
+      const int t0 = tile_row(it) + warp * kRows;
+      const Marks& m = marks[it & 1][warp];
+      wait_for(&xch.joined[it & 1], it >> 1, &xch.abort, p.dev_status);
+      float h[CH];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) h[c] = xch.states[it & 1][0][warp][lane * CH + c];
+      if (p.h_chunks && on && t0 % kChunk == 0 && t0 >= lo && t0 < hi)
 #pragma unroll
         for (int c = 0; c < CH; ++c)
-          h[c] = firsts >> r & 1 ? b[r][c] : fmaf(a[r][c], h[c], b[r][c]);
-        if (on && t0 + r >= lo && t0 + r < hi) {
-          put(out + r * D, h);
-          if ((lasts >> r & 1) && p.h_T)
+          p.h_chunks[t0 / kChunk * D + d + c] = s.firsts & 1 ? 0.f : h[c];
+      T* out = p.h + t0 * D + d;
+      if (!(s.firsts | s.lasts) && t0 >= lo && t0 + kRows <= hi) {
 #pragma unroll
-            for (int c = 0; c < CH; ++c) p.h_T[marks.last[warp * R + r] * D + d + c] = h[c];
+        for (int r = 0; r < kRows; ++r, out += D) {
+#pragma unroll
+          for (int c = 0; c < CH; ++c) h[c] = fmaf(s.a[r][c], h[c], s.b[r][c]);
+          if (on) put(out, h);
+        }
+        return;
+      }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r, out += D) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+          h[c] = s.firsts >> r & 1 ? s.b[r][c] : fmaf(s.a[r][c], h[c], s.b[r][c]);
+        if (on && t0 + r >= lo && t0 + r < hi) {
+          put(out, h);
+          if ((s.lasts >> r & 1) && p.h_T)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) p.h_T[m.last[r] * D + d + c] = h[c];
         }
       }
+    };
+
+    Span even, odd;
+    for (int it = -1; it < steps; it += 2) {
+      if (it + 1 < steps) form(it + 1, even);
+      if (it >= 0) finish(it, odd);
+      if (it + 2 < steps) form(it + 2, odd);
+      if (it + 1 < steps) finish(it + 1, even);
     }
-    if (marked) __syncthreads();  // the marks are rewritten
   }
-  if (ASYNC) tiles.drain(steps, &xch.abort);
+  __syncwarp();
   if (p.cluster > 1) cluster_sync();  // no block leaves while another may still write to it
 }
 
@@ -522,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // lam_t = dh_t + back_t, back_{t-1} = a_t lam_t runs the same scan with time reversed: pairs
 // (A, H) of back over a span, the last row first.  A tile is one 64-row piece between kept
 // states, so the states in front of its rows are formed again from the kept one within the
-// block, beside the pairs of the gradient.
+// block, by pairs of their own.
 
 template <typename T>
 struct BackwardArgs {
@@ -540,14 +579,11 @@ struct BackwardArgs {
 template <typename T, int CH, bool MIX, bool ASYNC>
 __global__ void __launch_bounds__(kThreads, 2)
     glr_backward_kernel(const __grid_constant__ BackwardArgs<T> p) {
-  constexpr int R = kBackwardRows, ROWS = kWarps * R;
-  static_assert(ROWS == kChunk, "a tile begins at a kept state");
+  static_assert(kTile == kChunk, "a tile begins at a kept state");
   extern __shared__ uint32_t dynamic[];
   uint32_t* ring = aligned_128(dynamic);
-  __shared__ uint64_t full[kBackwardStages];
-  __shared__ Exchange<CH> xch;
-  __shared__ Pair<CH> ahead[2][kWarps][32];  // the forward pairs of the warps
-  __shared__ Marks<ROWS> marks;
+  __shared__ Exchange<CH, 2> xch;  // the gradient's pairs, the state's
+  __shared__ Marks marks[2][kWarps];
   __shared__ int bounds[kBounds];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = blockIdx.x % p.cluster, part = blockIdx.x / p.cluster;
@@ -556,189 +592,201 @@ __global__ void __launch_bounds__(kThreads, 2)
   const long long D = p.D;
   if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seq, p.dev_status);
   const Packed seq = near(p.seq, bounds);
-  const int lo = part_begin(seq, part, p.parts), hi = part_begin(seq, part + 1, p.parts);
+  const Cut until = part_begin(seq, part + 1, p.parts);
+  const int lo = part_begin(seq, part, p.parts).row, hi = until.row;
+  const int top = (hi + kTile - 1) / kTile * kTile, step = kTile * p.cluster;
+  const int steps = hi > lo ? (top - lo / kTile * kTile + step - 1) / step : 0;
+  const auto tile_row = [&](int it) { return top - (it * p.cluster + rank + 1) * kTile; };
+  exchange_init(xch, p.cluster);
 
-  const int top = (hi + ROWS - 1) / ROWS * ROWS, step = ROWS * p.cluster;
-  const int steps = hi > lo ? (top - lo / ROWS * ROWS + step - 1) / step : 0;
-  const Tiles<3, kBackwardStages, ROWS, ASYNC> tiles{ring, full};
-  const auto load = [&](int it) {  // one thread
-    if (it < steps)
-      tiles.load(it, p.maps, blockIdx.y * 32 * CH, top - (it * p.cluster + rank + 1) * ROWS);
-  };
-  exchange_init(xch, p.cluster, tiles);
-  if (ASYNC && threadIdx.x == 0)
-    for (int it = 0; it < kBackwardStages - 1; ++it) load(it);
-  const auto kept_state = [&](int it, float(&k)[CH]) {
-    const int tile = top - (it * p.cluster + rank + 1) * ROWS;
+  if (warp == kWarps) {  // the joining warp
+    const auto load = [&](int it) {
+      if (ASYNC && lane == 0 && it < steps)
+        load_tile<3>(ring, xch.loaded, p.maps, it, blockIdx.y * 32 * CH, tile_row(it));
+    };
+    const auto kept_state = [&](int it, float(&k)[CH]) {
+      const int tile = tile_row(it);
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-      k[c] = on && it < steps && tile >= 0 ? p.h_chunks[tile / kChunk * D + d + c] : 0.f;
-  };
-
-  if (seq.off && p.dh0 && on)  // empty sequences hand their gradient on
-    for (int s = blockIdx.x * kWarps + warp; s < seq.n_seq; s += gridDim.x * kWarps)
-      if (bound_of(seq, s) >= bound_of(seq, s + 1))
-#pragma unroll
-        for (int c = 0; c < CH; ++c) p.dh0[s * D + d + c] = p.dh_T ? p.dh_T[s * D + d + c] : 0.f;
-
-  Walker<true, ROWS> walk;
-  walk.start(seq);
-  float state[CH] = {}, kept[CH];
-  kept_state(0, kept);
-  for (int it = 0; it < steps; ++it) {
-    const int tile = top - (it * p.cluster + rank + 1) * ROWS, t0 = tile + warp * R;
-    unsigned firsts = 0, lasts = 0;
-    const bool marked = walk.mark(seq, tile, marks);
-    if (marked) {
-      __syncthreads();
-      const int mine = warp * R + (lane & (R - 1));
-      firsts = __ballot_sync(~0u, marks.first[mine] >= 0) & ((1u << R) - 1);
-      lasts = __ballot_sync(~0u, marks.last[mine] >= 0) & ((1u << R) - 1);
-    }
-    uint32_t* raw[3];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) raw[i] = tiles.at(it % kBackwardStages, i) + warp * R * 32 + lane;
-    const bool whole = t0 >= lo && t0 + R <= hi;
-    if (ASYNC) {
-      if (!tiles.wait(it, &xch.abort)) give_up(&xch.abort, p.dev_status);
-      if (!whole) {  // rows of others and padding: state and gradient go through
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          if (t0 + r < lo || t0 + r >= hi)
-            raw[0][r * 32] = raw[1][r * 32] = raw[2][r * 32] = 0;
-        fence_proxy_async_smem();  // TMA writes these words next
+      for (int c = 0; c < CH; ++c)
+        k[c] = on && it < steps && tile >= 0 ? p.h_chunks[tile / kChunk * D + d + c] : 0.f;
+    };
+    for (int it = 0; it < kStages; ++it) load(it);
+    float state[CH] = {}, kept[CH];
+    kept_state(0, kept);
+    for (int it = 0; it < steps; ++it) {
+      wait_for(&xch.formed[it & 1], it >> 1, &xch.abort, p.dev_status);
+      join<false, 1>(xch, it, 0, 1, lane, kept, p.dev_status);
+      kept_state(it + 1, kept);
+      join<true, 0>(xch, it, rank, p.cluster, lane, state, p.dev_status);
+      arrive_warp(&xch.joined[it & 1], lane);
+      if (ASYNC && it > 0) {  // the step before has been read for the second time
+        wait_for(&xch.freed[(it - 1) % kStages], (it - 1) / kStages, &xch.abort, p.dev_status);
+        load(it - 1 + kStages);
       }
-    } else {
-      copy_rows<R>(raw[0], p.g + d, p.ld_g, t0, lo, hi, on);
-      copy_rows<R>(raw[1], p.x + d, p.ld_x, t0, lo, hi, on);
-      copy_rows<R>(raw[2], p.dh + d, D, t0, lo, hi, on);
     }
-    const auto x = [&](int r, int c) { return get(raw[1][r * 32], c, T()); };
-    const auto dh = [&](int r, int c) { return get(raw[2][r * 32], c, T()); };
-    const auto state_before = [&](int r, int c) {  // of the sequence that begins in row r
-      return on && p.h0 ? p.h0[marks.first[warp * R + r] * D + d + c] : 0.f;
+    if (ASYNC && lane == 0) drain(xch.loaded, steps, &xch.abort);
+  } else {
+    if (seq.off && p.dh0 && on) hand_on_empty<CH>(seq, p.dh_T, p.dh0, D, d, warp);
+    struct Span {
+      float a[kRows][CH], om[MIX ? kRows : 1][CH];  // exp(g), 1 - exp(g)
+      unsigned firsts, lasts;
     };
-    const auto grad_after = [&](int r, int c) {  // of the sequence that ends in row r
-      return on && p.dh_T ? p.dh_T[marks.last[warp * R + r] * D + d + c] : 0.f;
+    Walker<true> walk;
+    walk.start(until);
+    const auto words = [&](int it, int array) {
+      return tile_at<3>(ring, it, array) + warp * kRows * 32 + lane;
+    };
+    const auto state_before = [&](const Marks& m, int r, int c) {  // where a sequence begins
+      return on && p.h0 ? p.h0[m.first[r] * D + d + c] : 0.f;
+    };
+    const auto grad_after = [&](const Marks& m, int r, int c) {  // where a sequence ends
+      return on && p.dh_T ? p.dh_T[m.last[r] * D + d + c] : 0.f;
     };
 
-    float a[R][CH], om[MIX ? R : 1][CH] = {};  // exp(g), 1 - exp(g)
-    const auto input = [&](int r, int c) { return MIX ? om[r][c] * x(r, c) : x(r, c); };
-    Pair<CH> fwd, rev;
+    // the pairs of the span of step `it`
+    const auto form = [&](int it, Span& s) {
+      const int t0 = tile_row(it) + warp * kRows;
+      const Marks& m = marks[it & 1][warp];
+      walk.mark(seq, t0, lane, marks[it & 1][warp], s.firsts, s.lasts);
+      uint32_t *g = words(it, 0), *x = words(it, 1), *dh = words(it, 2);
+      if (ASYNC) {
+        wait_for(&xch.loaded[it % kStages], it / kStages, &xch.abort, p.dev_status);
+        if (t0 < lo || t0 + kRows > hi) {  // rows of others and padding: all goes through
 #pragma unroll
-    for (int c = 0; c < CH; ++c) fwd.A[c] = 1.f, fwd.H[c] = rev.H[c] = 0.f;
+          for (int r = 0; r < kRows; ++r)
+            if (t0 + r < lo || t0 + r >= hi) g[r * 32] = x[r * 32] = dh[r * 32] = 0;
+          fence_proxy_async_smem();  // TMA writes these words next
+        }
+      } else {
+        copy_rows(g, p.g + d, p.ld_g, t0, lo, hi, on);
+        copy_rows(x, p.x + d, p.ld_x, t0, lo, hi, on);
+        copy_rows(dh, p.dh + d, D, t0, lo, hi, on);
+      }
+      const auto input = [&](int r, int c) {
+        const float xv = get(x[r * 32], c, T());
+        return MIX ? s.om[MIX ? r : 0][c] * xv : xv;
+      };
+      Pair<CH> fwd, rev;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+      for (int c = 0; c < CH; ++c) fwd.A[c] = 1.f, fwd.H[c] = rev.H[c] = 0.f;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const float lg = get(g[r * 32], c, T());
+          s.a[r][c] = decay_of(lg);
+          if (MIX) s.om[MIX ? r : 0][c] = one_minus(lg, s.a[r][c]);
+          fwd.A[c] *= s.a[r][c];
+          fwd.H[c] = fmaf(s.a[r][c], fwd.H[c], input(r, c));
+        }
+#pragma unroll
+      for (int r = kRows - 1; r >= 0; --r)
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+          rev.H[c] = s.a[r][c] * (get(dh[r * 32], c, T()) + rev.H[c]);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) rev.A[c] = fwd.A[c];
+      if (s.firsts) {  // again, from the initial states
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            if (s.firsts >> r & 1) fwd.H[c] = state_before(m, r, c);
+            fwd.H[c] = fmaf(s.a[r][c], fwd.H[c], input(r, c));
+            fwd.A[c] = -1.f;
+          }
+      }
+      if (s.lasts) {  // again, from the final states' gradients
+#pragma unroll
+        for (int r = kRows - 1; r >= 0; --r)
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            if (s.lasts >> r & 1) rev.H[c] = grad_after(m, r, c);
+            rev.H[c] = s.a[r][c] * (get(dh[r * 32], c, T()) + rev.H[c]);
+            rev.A[c] = -1.f;
+          }
+      }
+      xch.warps[it & 1][0][warp][lane] = rev;
+      xch.warps[it & 1][1][warp][lane] = fwd;
+      arrive_warp(&xch.formed[it & 1], lane);
+    };
+
+    // the gradients of step `it`
+    const auto finish = [&](int it, Span& s) {
+      const int t0 = tile_row(it) + warp * kRows;
+      const Marks& m = marks[it & 1][warp];
+      const uint32_t *x = words(it, 1), *dh = words(it, 2);
+      wait_for(&xch.joined[it & 1], it >> 1, &xch.abort, p.dev_status);
+      float back[CH], h[CH], before[kRows][CH];
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const float lg = get(raw[0][r * 32], c, T());
-        a[r][c] = decay_of(lg);
-        if (MIX) om[r][c] = one_minus(lg, a[r][c]);
-        fwd.A[c] *= a[r][c];
-        fwd.H[c] = fmaf(a[r][c], fwd.H[c], input(r, c));
+        back[c] = xch.states[it & 1][0][warp][lane * CH + c];
+        h[c] = xch.states[it & 1][1][warp][lane * CH + c];
       }
+      const auto advance = [&](int r, int c) {
+        const float xv = get(x[r * 32], c, T());
+        before[r][c] = MIX ? h[c] - xv : h[c];
+        h[c] = fmaf(s.a[r][c], h[c], MIX ? s.om[MIX ? r : 0][c] * xv : xv);
+      };
+      T* dg = p.dg + (t0 + kRows - 1) * p.ld_g + d;
+      T* dx = p.dx + (t0 + kRows - 1) * p.ld_x + d;
+      float o_g[CH], o_x[CH];
+      const auto retreat = [&](int r, int c) {
+        const float lam = get(dh[r * 32], c, T()) + back[c];
+        back[c] = s.a[r][c] * lam;
+        o_x[c] = MIX ? s.om[MIX ? r : 0][c] * lam : lam;
+        o_g[c] = back[c] * before[r][c];
+      };
+      if (!(s.firsts | s.lasts) && t0 >= lo && t0 + kRows <= hi) {
 #pragma unroll
-    for (int r = R - 1; r >= 0; --r)
+        for (int r = 0; r < kRows; ++r)
 #pragma unroll
-      for (int c = 0; c < CH; ++c) rev.H[c] = a[r][c] * (dh(r, c) + rev.H[c]);
+          for (int c = 0; c < CH; ++c) advance(r, c);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) rev.A[c] = fwd.A[c];
-    if (firsts) {  // again, from the initial states
+        for (int r = kRows - 1; r >= 0; --r, dg -= p.ld_g, dx -= p.ld_x) {
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          if (firsts >> r & 1) fwd.H[c] = state_before(r, c);
-          fwd.H[c] = fmaf(a[r][c], fwd.H[c], input(r, c));
-          fwd.A[c] = -1.f;
+          for (int c = 0; c < CH; ++c) retreat(r, c);
+          if (on) {
+            put(dg, o_g);
+            put(dx, o_x);
+          }
         }
-    }
-    if (lasts) {  // again, from the final states' gradients
+      } else {
 #pragma unroll
-      for (int r = R - 1; r >= 0; --r)
+        for (int r = 0; r < kRows; ++r)
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          if (lasts >> r & 1) rev.H[c] = grad_after(r, c);
-          rev.H[c] = a[r][c] * (dh(r, c) + rev.H[c]);
-          rev.A[c] = -1.f;
+          for (int c = 0; c < CH; ++c) {
+            if (s.firsts >> r & 1) h[c] = state_before(m, r, c);
+            advance(r, c);
+          }
+#pragma unroll
+        for (int r = kRows - 1; r >= 0; --r, dg -= p.ld_g, dx -= p.ld_x) {
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            if (s.lasts >> r & 1) back[c] = grad_after(m, r, c);
+            retreat(r, c);
+          }
+          if (on && t0 + r >= lo && t0 + r < hi) {
+            put(dg, o_g);
+            put(dx, o_x);
+            if ((s.firsts >> r & 1) && p.dh0)
+#pragma unroll
+              for (int c = 0; c < CH; ++c) p.dh0[m.first[r] * D + d + c] = back[c];
+          }
         }
-    }
-    ahead[it & 1][warp][lane] = fwd;
-    float kept_next[CH];
-    kept_state(it + 1, kept_next);
+      }
+      if (ASYNC) arrive_warp(&xch.freed[it % kStages], lane);
+    };
 
-    float back[CH];
-    join(xch, it, rev, kWarps - 1 - warp, rank, p.cluster, lane, state, back, p.dev_status, [&] {
-      if (ASYNC && threadIdx.x == 0) load(it + kBackwardStages - 1);  // over the step before's tile
-    });
-
-    float h[CH], before[R][CH];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) h[c] = kept[c];
-#pragma unroll
-    for (int w = 0; w < kWarps - 1; ++w)
-      if (w < warp) follow(h, ahead[it & 1][w][lane]);
-    T* dg = p.dg + (t0 + R - 1) * p.ld_g + d;
-    T* dx = p.dx + (t0 + R - 1) * p.ld_x + d;
-    if (!marked && whole) {
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          before[r][c] = MIX ? h[c] - x(r, c) : h[c];
-          h[c] = fmaf(a[r][c], h[c], input(r, c));
-        }
-#pragma unroll
-      for (int r = R - 1; r >= 0; --r) {
-        float o_g[CH], o_x[CH];
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const float lam = dh(r, c) + back[c];
-          back[c] = a[r][c] * lam;
-          o_x[c] = MIX ? om[r][c] * lam : lam;
-          o_g[c] = back[c] * before[r][c];
-        }
-        if (on) {
-          put(dg, o_g);
-          put(dx, o_x);
-        }
-        dg -= p.ld_g;
-        dx -= p.ld_x;
-      }
-    } else {
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          if (firsts >> r & 1) h[c] = state_before(r, c);
-          before[r][c] = MIX ? h[c] - x(r, c) : h[c];
-          h[c] = fmaf(a[r][c], h[c], input(r, c));
-        }
-#pragma unroll
-      for (int r = R - 1; r >= 0; --r) {
-        float o_g[CH], o_x[CH];
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          if (lasts >> r & 1) back[c] = grad_after(r, c);
-          const float lam = dh(r, c) + back[c];
-          back[c] = a[r][c] * lam;
-          o_x[c] = MIX ? om[r][c] * lam : lam;
-          o_g[c] = back[c] * before[r][c];
-        }
-        if (on && t0 + r >= lo && t0 + r < hi) {
-          put(dg - (R - 1 - r) * p.ld_g, o_g);
-          put(dx - (R - 1 - r) * p.ld_x, o_x);
-          if ((firsts >> r & 1) && p.dh0)
-#pragma unroll
-            for (int c = 0; c < CH; ++c) p.dh0[marks.first[warp * R + r] * D + d + c] = back[c];
-        }
-      }
+    Span even, odd;
+    for (int it = -1; it < steps; it += 2) {
+      if (it + 1 < steps) form(it + 1, even);
+      if (it >= 0) finish(it, odd);
+      if (it + 2 < steps) form(it + 2, odd);
+      if (it + 1 < steps) finish(it + 1, even);
     }
-    if (marked) __syncthreads();  // the marks are rewritten
-#pragma unroll
-    for (int c = 0; c < CH; ++c) kept[c] = kept_next[c];
   }
-  if (ASYNC) tiles.drain(steps, &xch.abort);
+  __syncwarp();
   if (p.cluster > 1) cluster_sync();  // no block leaves while another may still write to it
 }
 
@@ -782,11 +830,11 @@ struct Grid {
   int strips, cluster, parts;
 };
 
-Grid grid_of(int N, int D, int n_seq, int width, int rows) {
+Grid grid_of(int N, int D, int n_seq, int width) {
   Grid g;
   g.strips = (D + width - 1) / width;
   const int want = 2 * num_sms();  // two blocks of 8 warps on every SM
-  const int tiles = (N + rows - 1) / rows;
+  const int tiles = (N + kTile - 1) / kTile;
   g.cluster = std::max(1, std::min({kMaxCluster, tiles, want / g.strips}));
   g.parts = std::max(1, std::min({n_seq, tiles, want / (g.strips * g.cluster)}));
   return g;
@@ -865,18 +913,18 @@ int moe_glr_forward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off,
   const int e = dispatch(
       mode, dtype, {g, x, h}, {ld_g, ld_x, D}, [&](auto type, auto ch, auto mix, auto async) {
         using T = decltype(type);
-        constexpr int CH = decltype(ch)::value, ROWS = kForwardRows * kWarps;
+        constexpr int CH = decltype(ch)::value;
         constexpr bool ASYNC = decltype(async)::value, F32 = sizeof(T) == 4;
-        const Grid gr = grid_of(N, D, n_seq, 32 * CH, ROWS);
+        const Grid gr = grid_of(N, D, n_seq, 32 * CH);
         ForwardArgs<T> a{{}, seq, D, gr.parts, gr.cluster, static_cast<const T*>(g),
                          static_cast<const T*>(x), ld_g, ld_x, h0, static_cast<T*>(h), h_T,
                          h_chunks, dev_status};
         if (ASYNC) {
-          if (int err = encode_map_rows(&a.maps[0], g, F32, D, N, ld_g, 32 * CH, ROWS)) return err;
-          if (int err = encode_map_rows(&a.maps[1], x, F32, D, N, ld_x, 32 * CH, ROWS)) return err;
+          if (int err = encode_map_rows(&a.maps[0], g, F32, D, N, ld_g, 32 * CH, kTile)) return err;
+          if (int err = encode_map_rows(&a.maps[1], x, F32, D, N, ld_x, 32 * CH, kTile)) return err;
         }
         return launch(glr_forward_kernel<T, CH, decltype(mix)::value, ASYNC>, gr,
-                      kForwardStages * 2 * ROWS * 128 + kAlign, a, stream);
+                      kStages * 2 * kTile * 128 + kAlign, a, stream);
       });
   mark_after(MOE_KERNEL_GLR_FWD, stream);
   count_launches(1);
@@ -899,7 +947,7 @@ int moe_glr_backward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off
         using T = decltype(type);
         constexpr int CH = decltype(ch)::value;
         constexpr bool ASYNC = decltype(async)::value, F32 = sizeof(T) == 4;
-        const Grid gr = grid_of(N, D, n_seq, 32 * CH, kChunk);
+        const Grid gr = grid_of(N, D, n_seq, 32 * CH);
         BackwardArgs<T> a{{}, seq, D, gr.parts, gr.cluster, static_cast<const T*>(g),
                           static_cast<const T*>(x), static_cast<const T*>(dh), ld_g, ld_x, h0,
                           h_chunks, dh_T, static_cast<T*>(dg), static_cast<T*>(dx), dh0,
@@ -908,11 +956,11 @@ int moe_glr_backward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off
           const void* in[3] = {g, x, dh};
           const long long ld[3] = {ld_g, ld_x, D};
           for (int i = 0; i < 3; ++i)
-            if (int err = encode_map_rows(&a.maps[i], in[i], F32, D, N, ld[i], 32 * CH, kChunk))
+            if (int err = encode_map_rows(&a.maps[i], in[i], F32, D, N, ld[i], 32 * CH, kTile))
               return err;
         }
         return launch(glr_backward_kernel<T, CH, decltype(mix)::value, ASYNC>, gr,
-                      kBackwardStages * 3 * kChunk * 128 + kAlign, a, stream);
+                      kStages * 3 * kTile * 128 + kAlign, a, stream);
       });
   mark_after(MOE_KERNEL_GLR_BWD, stream);
   count_launches(1);
