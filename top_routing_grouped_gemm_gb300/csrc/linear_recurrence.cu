@@ -14,8 +14,8 @@ namespace moe {
 namespace {
 
 constexpr int kChunk = 64;      // rows between the kept states
-constexpr int kWarps = 8;       // warps of a scan block, beside the one that joins
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kWarps = 8;       // warps of a scan block, beside two that join what these form
+constexpr int kThreads = 32 * (kWarps + 2);
 constexpr int kRows = 8;        // rows of a warp in a tile
 constexpr int kTile = kWarps * kRows;
 constexpr int kStages = 3;      // tiles in shared memory
@@ -31,22 +31,92 @@ __device__ __forceinline__ void st(__nv_bfloat16* p, long long i, float v) {
   p[i] = __float2bfloat16_rn(v);
 }
 
-// ------------------------------------------------------------------ what a lane moves at once
+// ------------------------------------------------------------------ what a lane works on
 //
-// CH channels of one row: two bf16 (4 bytes), one bf16 (rows that are not 4-byte aligned) or
-// one fp32; a warp covers 32 CH neighbouring channels.
-__device__ __forceinline__ float get(const uint32_t& bits, int c, __nv_bfloat16) {
-  return __uint_as_float(c ? bits & 0xffff0000u : bits << 16);
-}
-__device__ __forceinline__ float get(const uint32_t& bits, int, float) {
-  return __uint_as_float(bits);
+// CH channels of one row: two bf16 (one 4-byte word), one bf16 (rows that are not 16-byte
+// aligned) or one fp32; a warp covers 32 CH neighbouring channels.  Two channels are worked on by
+// packed fp32 instructions, which halve the issue slots that bound these kernels.
+template <int CH>
+struct Vec;
+
+template <>
+struct Vec<1> {
+  float v;
+  __device__ __forceinline__ float operator[](int) const { return v; }
+};
+
+template <>
+struct Vec<2> {
+  unsigned long long v;
+  __device__ __forceinline__ float operator[](int c) const {
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+    return c ? hi : lo;
+  }
+};
+
+__device__ __forceinline__ Vec<2> pack(float lo, float hi) {
+  Vec<2> r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
 }
 
-__device__ __forceinline__ void put(float* p, const float (&v)[1]) { __stcs(p, v[0]); }
-__device__ __forceinline__ void put(__nv_bfloat16* p, const float (&v)[1]) {
-  *p = __float2bfloat16_rn(v[0]);
+template <int CH>
+__device__ __forceinline__ Vec<CH> all(float f) {
+  if constexpr (CH == 2)
+    return pack(f, f);
+  else
+    return {f};
 }
-__device__ __forceinline__ void put(__nv_bfloat16* p, const float (&v)[2]) {
+
+__device__ __forceinline__ Vec<1> fma(Vec<1> a, Vec<1> b, Vec<1> c) { return {fmaf(a.v, b.v, c.v)}; }
+__device__ __forceinline__ Vec<1> operator*(Vec<1> a, Vec<1> b) { return {a.v * b.v}; }
+__device__ __forceinline__ Vec<1> operator+(Vec<1> a, Vec<1> b) { return {a.v + b.v}; }
+__device__ __forceinline__ Vec<2> fma(Vec<2> a, Vec<2> b, Vec<2> c) {
+  Vec<2> r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ Vec<2> operator*(Vec<2> a, Vec<2> b) {
+  Vec<2> r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Vec<2> operator+(Vec<2> a, Vec<2> b) {
+  Vec<2> r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+template <int CH>
+__device__ __forceinline__ Vec<CH> operator-(Vec<CH> a, Vec<CH> b) {
+  return fma(b, all<CH>(-1.f), a);
+}
+
+// The channels of a word of shared memory, of global memory, and back.
+template <typename T, int CH>
+__device__ __forceinline__ Vec<CH> of_word(uint32_t bits) {
+  if constexpr (CH == 2)
+    return pack(__uint_as_float(bits << 16), __uint_as_float(bits & 0xffff0000u));
+  else
+    return {__uint_as_float(sizeof(T) == 4 ? bits : bits << 16)};
+}
+
+template <int CH>
+__device__ __forceinline__ Vec<CH> read(const float* p) {
+  if constexpr (CH == 2)
+    return pack(p[0], p[1]);
+  else
+    return {p[0]};
+}
+template <int CH>
+__device__ __forceinline__ void write(float* p, Vec<CH> v) {
+#pragma unroll
+  for (int c = 0; c < CH; ++c) p[c] = v[c];
+}
+
+__device__ __forceinline__ void put(float* p, Vec<1> v) { __stcs(p, v.v); }
+__device__ __forceinline__ void put(__nv_bfloat16* p, Vec<1> v) { *p = __float2bfloat16_rn(v.v); }
+__device__ __forceinline__ void put(__nv_bfloat16* p, Vec<2> v) {
   __stcs(reinterpret_cast<unsigned*>(p), pack_bf16x2(v[0], v[1]));
 }
 
@@ -56,22 +126,35 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, const float (&v)[2]) {
 // [-0.2, 0]: mean -2.3e-8, rms 3.8e-8; the library's expf, of four times the instructions, has
 // -1.6e-9 and 3.1e-8), which would add up over the ~1 / |g| steps that a state lives; the
 // exponent carries log2(1 + 2.3e-8) against it.
-__device__ __forceinline__ float decay_of(float g) {
+__device__ __forceinline__ float exp2_approx(float t) {
   float a;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(fmaf(g, 1.4426950408889634f, 3.3e-8f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(t));
   return a;
+}
+template <int CH>
+__device__ __forceinline__ Vec<CH> decay_of(Vec<CH> g) {
+  const Vec<CH> t = fma(g, all<CH>(1.4426950408889634f), all<CH>(3.3e-8f));
+  if constexpr (CH == 2)
+    return pack(exp2_approx(t[0]), exp2_approx(t[1]));
+  else
+    return {exp2_approx(t[0])};
 }
 
 // 1 - exp(g) for g <= 0, given a = exp(g): near 0, where the difference cancels, the series
 // -g (1 + g/2 + g^2/6 + ...) to g^5 / 6! (the next term is 4.8e-8 at the border).
-__device__ __forceinline__ float one_minus(float g, float a) {
-  float p = 1.f / 720.f;
-  p = fmaf(p, g, 1.f / 120.f);
-  p = fmaf(p, g, 1.f / 24.f);
-  p = fmaf(p, g, 1.f / 6.f);
-  p = fmaf(p, g, 0.5f);
-  p = fmaf(p, g, 1.f);
-  return g > -0.25f ? -g * p : 1.f - a;
+template <int CH>
+__device__ __forceinline__ Vec<CH> one_minus(Vec<CH> g, Vec<CH> a) {
+  Vec<CH> p = fma(all<CH>(-1.f / 720.f), g, all<CH>(-1.f / 120.f));
+  p = fma(p, g, all<CH>(-1.f / 24.f));
+  p = fma(p, g, all<CH>(-1.f / 6.f));
+  p = fma(p, g, all<CH>(-0.5f));
+  p = fma(p, g, all<CH>(-1.f));
+  p = p * g;
+  const Vec<CH> far = all<CH>(1.f) - a;
+  if constexpr (CH == 2)
+    return pack(g[0] > -0.25f ? p[0] : far[0], g[1] > -0.25f ? p[1] : far[1]);
+  else
+    return {g[0] > -0.25f ? p[0] : far[0]};
 }
 
 // ------------------------------------------------------------------ packed sequences
@@ -118,8 +201,8 @@ __device__ __forceinline__ Cut part_begin(const Packed& q, int p, int parts) {
   return {before, bound_of(q, before)};
 }
 
-// What begins and ends in the kRows rows of a warp: bit r of firsts and lasts for row r, and the
-// sequences (one warp's own words of shared memory).
+// The sequences that begin and end in the kRows rows of a warp (in shared memory; the walker's
+// masks say which rows).
 struct Marks {
   int first[kRows], last[kRows];
 };
@@ -141,7 +224,7 @@ struct Walker {
     firsts = lasts = 0;
     if (!q.off) {
       // the first multiple of len that is not before the rows
-      if (t0 > 0 && (t0 + q.len - 1ll) / q.len * q.len > t0 + kRows) return;
+      if (t0 > 0 && (t0 + q.len - 1u) / q.len * q.len > static_cast<unsigned>(t0 + kRows)) return;
       __syncwarp();  // the words may still be read
       const int t = t0 + lane;
       const bool bound = lane <= kRows && t >= 0 && t <= q.N && t % q.len == 0;
@@ -190,7 +273,7 @@ struct Walker {
 // h -> a h + b is associative in pairs (A, H): h -> A h + H.  The time axis is cut into tiles of
 // 8 warps x kRows rows; the blocks of a cluster take neighbouring tiles, cluster after cluster of
 // them.  Each warp runs its rows twice in registers: once for their pair, and, when the pairs
-// before it are known, once more from the state that these give.  A ninth warp joins the pairs,
+// before it are known, once more from the state that these give.  Two more warps join the pairs,
 // always in the order of the recurrence: over the warps, over the blocks of the cluster (through
 // distributed shared memory) and from step to step; meanwhile the others form the pairs of the
 // next tile.  A is -1 for a span in which a sequence begins: what came before is then not used at
@@ -199,44 +282,57 @@ struct Walker {
 // (Aligned for the vector store that carries it.)
 template <int CH>
 struct alignas(8 * CH) Pair {
-  float A[CH], H[CH];
+  Vec<CH> A, H;
+  __device__ __forceinline__ bool cut() const { return A[0] < 0.f; }  // of all channels alike
 };
 
 template <int CH>
-__device__ __forceinline__ void follow(float (&h)[CH], const Pair<CH>& p) {
-#pragma unroll
-  for (int c = 0; c < CH; ++c) h[c] = p.A[c] < 0.f ? p.H[c] : fmaf(p.A[c], h[c], p.H[c]);
+__device__ __forceinline__ void follow(Vec<CH>& h, const Pair<CH>& p) {
+  const Vec<CH> on = fma(p.A, h, p.H);
+  h = p.cut() ? p.H : on;
 }
 
 template <int CH>
 __device__ __forceinline__ void append(Pair<CH>& s, const Pair<CH>& p) {
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    s.H[c] = p.A[c] < 0.f ? p.H[c] : fmaf(p.A[c], s.H[c], p.H[c]);
-    s.A[c] = fminf(p.A[c], s.A[c]) < 0.f ? -1.f : s.A[c] * p.A[c];
-  }
+  const Vec<CH> A = s.A * p.A;
+  s.A = s.cut() || p.cut() ? all<CH>(-1.f) : A;
+  follow(s.H, p);
 }
 
-// What the warps of a block and the blocks of a cluster exchange, double-buffered by the parity
-// of the step.  A warp forms its pair of step n + 2 after it has its state of step n, which the
-// joining warp gives when it has read the pairs of step n; and that warp joins step n + 2 when
-// every warp has formed its pair, after using its state of step n.  A block sends its pair of
-// step n + 2 when it has every block's of step n + 1, and a block sends that after it has read
-// all of step n.
+// What the warps of a block and the blocks of a cluster exchange.  Step n uses the buffers n % 2
+// between the warps of a block.  A warp forms its pair of step n + 2 after it has used what the
+// joining warps gave it for step n, and they go to step n + 2 when every warp has formed its pair.
+// Between blocks it uses the buffers n % 4: a block sends its pair of step n + 4 when its warps
+// have used step n + 2, for which it had every block's pair; each block sent that when its warps
+// had used step n.
 template <int CH, int PAIRS>
 struct Exchange {
   Pair<CH> warps[2][PAIRS][kWarps][32];
-  Pair<CH> blocks[2][kMaxCluster][32];
-  float states[2][PAIRS][kWarps][32 * CH];
-  uint64_t formed[2], joined[2], received[2];
+  Pair<CH> blocks[4][kMaxCluster][32];
+  Vec<CH> state[2][32];  // in front of the block's tile
+  Marks marks[2][kWarps];
+  uint64_t formed[2], joined[2], received[4];
   uint64_t loaded[kStages], freed[kStages];  // tiles
   int abort;
 };
 
+// Position in the ring of tiles, and the parity of its current use.
+struct Turn {
+  int at = 0;
+  unsigned use = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == kStages) at = 0, use ^= 1;
+  }
+};
+
 // Waits, with a limit.  When it runs out the rest of the launch goes on without waiting (its
 // results are then wrong, and reported).
-__device__ __forceinline__ void wait_for(uint64_t* bar, int n, int* abort, int* dev_status) {
-  if (!mbar_wait(bar, n & 1, abort)) {
+__device__ __forceinline__ void wait_for(uint64_t* bar, unsigned parity, int* abort,
+                                         int* dev_status) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)  // mostly soon over, without a look at the clock
+    if (mbar_try_wait(bar, parity)) return;
+  if (!mbar_wait(bar, parity, abort)) {
     *reinterpret_cast<volatile int*>(abort) = 1;
     report_status(dev_status, MOE_ERR_TIMEOUT);
   }
@@ -248,14 +344,14 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-template <typename X>
-__device__ __forceinline__ void exchange_init(X& x, int cluster) {
+template <int CH, int PAIRS>
+__device__ __forceinline__ void exchange_init(Exchange<CH, PAIRS>& x, int cluster) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&x.formed[i], kWarps);
-      mbar_init(&x.joined[i], 1);
-      mbar_init(&x.received[i], 1);
+      mbar_init(&x.joined[i], 2);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&x.received[i], 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&x.loaded[i], 1);
       mbar_init(&x.freed[i], kWarps);
@@ -267,96 +363,94 @@ __device__ __forceinline__ void exchange_init(X& x, int cluster) {
   if (cluster > 1) cluster_sync();  // every block runs, its barriers set, before one writes there
 }
 
-// Sends a block's pair to every block of the cluster (itself too), where it counts towards the
-// barrier of the step.
-template <int CH>
-__device__ __forceinline__ void publish(Pair<CH>* slot, uint64_t* received, const Pair<CH>& p,
-                                        int cluster) {
-  for (int q = 0; q < cluster; ++q) {
-    const uint32_t to = cluster_addr(slot, q), bar = cluster_addr(received, q);
-    if constexpr (CH == 2)
-      asm volatile(
-          "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, "
-          "[%5];" ::"r"(to),
-          "r"(__float_as_uint(p.A[0])), "r"(__float_as_uint(p.A[1])), "r"(__float_as_uint(p.H[0])),
-          "r"(__float_as_uint(p.H[1])), "r"(bar)
-          : "memory");
-    else
-      asm volatile(
-          "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::
-              "r"(to),
-          "r"(__float_as_uint(p.A[0])), "r"(__float_as_uint(p.H[0])), "r"(bar)
-          : "memory");
-  }
-}
-
-// The joining warp's part of a step: `pairs` (order w is at warps[PAIR][DOWN ? 7 - w : w]) give
-// every warp its state in states[PAIR] and move `state` over the whole step.
-template <bool DOWN, int PAIR, int CH, int PAIRS>
-__device__ __forceinline__ void join(Exchange<CH, PAIRS>& x, int it, int rank, int cluster,
-                                     int lane, float (&state)[CH], int* dev_status) {
-  const int buf = it & 1;
+// Two warps join.  This is the first one's part of step `it`: the pairs of the block's warps (in
+// the order of the recurrence) become the pairs of all that comes before them in the tile; the
+// whole tile's is sent to every block of the cluster, this one too, where its bytes count towards
+// the barrier of the step.
+template <bool DOWN, int CH, int PAIRS>
+__device__ __forceinline__ void join_warps(Exchange<CH, PAIRS>& x, int it, int rank, int cluster,
+                                           int lane) {
   Pair<CH> pairs[kWarps];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) pairs[w] = x.warps[buf][PAIR][DOWN ? kWarps - 1 - w : w][lane];
-  float carry[CH];
-  if (cluster > 1) {
-    Pair<CH> sum = pairs[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) append(sum, pairs[w]);
-    if (lane == 0) mbar_arrive_expect_tx(&x.received[buf], cluster * 32 * sizeof(Pair<CH>));
-    publish(&x.blocks[buf][rank][lane], &x.received[buf], sum, cluster);
-    wait_for(&x.received[buf], it >> 1, &x.abort, dev_status);
-#pragma unroll
-    for (int q = 0; q < kMaxCluster; ++q) {
-      if (q == rank)
-#pragma unroll
-        for (int c = 0; c < CH; ++c) carry[c] = state[c];
-      if (q < cluster) follow(state, x.blocks[buf][q][lane]);
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) carry[c] = state[c];
-  }
+  for (int w = 0; w < kWarps; ++w) pairs[w] = x.warps[it & 1][0][DOWN ? kWarps - 1 - w : w][lane];
+  Pair<CH> sum{all<CH>(1.f), all<CH>(0.f)};
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    float* to = &x.states[buf][PAIR][DOWN ? kWarps - 1 - w : w][lane * CH];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) to[c] = carry[c];
-    follow(carry, pairs[w]);
+    x.warps[it & 1][0][DOWN ? kWarps - 1 - w : w][lane] = sum;
+    if (w == 0)
+      sum = pairs[0];
+    else
+      append(sum, pairs[w]);
   }
-  if (cluster == 1)
+  Pair<CH>* slot = &x.blocks[it & 3][rank][lane];
+  uint64_t* received = &x.received[it & 3];
+  if (cluster == 1) {
+    *slot = sum;
+    arrive_warp(received, lane);
+  } else {
+    if (lane == 0) mbar_arrive_expect_tx(received, cluster * 32 * sizeof(Pair<CH>));
+    for (int q = 0; q < cluster; ++q) {
+      const uint32_t to = cluster_addr(slot, q), bar = cluster_addr(received, q);
+      if constexpr (CH == 2)
+        asm volatile(
+            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::
+                "r"(to),
+            "l"(sum.A.v), "l"(sum.H.v), "r"(bar)
+            : "memory");
+      else
+        asm volatile(
+            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::
+                "r"(to),
+            "r"(__float_as_uint(sum.A.v)), "r"(__float_as_uint(sum.H.v)), "r"(bar)
+            : "memory");
+    }
+  }
+  arrive_warp(&x.joined[it & 1], lane);
+}
+
+// The second one's: the state in front of this block's tile, from `state` in front of the step's
+// first tile, which moves on over the whole step.
+template <int CH, int PAIRS>
+__device__ __forceinline__ void join_blocks(Exchange<CH, PAIRS>& x, int it, int rank, int cluster,
+                                            int lane, Vec<CH>& state, int* dev_status) {
+  wait_for(&x.received[it & 3], it >> 2 & 1, &x.abort, dev_status);
+  Vec<CH> mine = state;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) state[c] = carry[c];
+  for (int q = 0; q < kMaxCluster; ++q) {
+    if (q == rank) mine = state;
+    if (q < cluster) follow(state, x.blocks[it & 3][q][lane]);
+  }
+  x.state[it & 1][lane] = mine;
+  arrive_warp(&x.joined[it & 1], lane);
 }
 
 // ------------------------------------------------------------------ tiles in shared memory
 //
-// kStages tiles of ARRAYS inputs, each [kTile][32] words: the word of a lane holds its CH
-// channels.  Where rows begin on 16-byte boundaries, the joining warp has TMA copy whole tiles
-// ahead (ASYNC); elsewhere each warp copies its rows through registers when they are asked for.
+// kStages tiles of ARRAYS inputs, each [kTile][32] words: the word of a lane holds its CH channels.
+// Where rows begin on 16-byte boundaries, TMA copies whole tiles ahead (ASYNC); elsewhere each
+// warp copies its rows through registers when they are asked for.
 template <int ARRAYS>
-__device__ __forceinline__ uint32_t* tile_at(uint32_t* ring, int it, int array) {
-  return ring + (it % kStages * ARRAYS + array) * kTile * 32;
+__device__ __forceinline__ uint32_t* tile_at(uint32_t* ring, int stage, int array) {
+  return ring + (stage * ARRAYS + array) * kTile * 32;
 }
 
 // One thread: the copies of step `it`, the tile at row t0 of the strip at channel d0.
 template <int ARRAYS>
 __device__ __forceinline__ void load_tile(uint32_t* ring, uint64_t* loaded, const CUtensorMap* maps,
                                           int it, int d0, int t0) {
-  uint64_t* bar = &loaded[it % kStages];
-  mbar_arrive_expect_tx(bar, ARRAYS * kTile * 128);
+  const int stage = it % kStages;
+  mbar_arrive_expect_tx(&loaded[stage], ARRAYS * kTile * 128);
   const uint64_t policy = l2_policy_evict_first();
   for (int i = 0; i < ARRAYS; ++i)
-    tma_load_2d(tile_at<ARRAYS>(ring, it, i), &maps[i], bar, d0, t0, policy);
+    tma_load_2d(tile_at<ARRAYS>(ring, stage, i), &maps[i], &loaded[stage], d0, t0, policy);
 }
 
-// One thread, after a launch that gave up: the copies still in flight (again with a limit).
-__device__ __forceinline__ void drain(uint64_t* loaded, int steps, volatile int* abort) {
-  if (!*abort) return;
+// The same thread at the end: no copy is in flight when the block goes, not even in a launch that
+// gave up (again with a limit).
+__device__ __forceinline__ void drain(uint64_t* loaded, int steps) {
   int never = 0;
   for (int it = max(0, steps - kStages); it < steps; ++it)
-    mbar_wait(&loaded[it % kStages], (it / kStages) & 1, &never);
+    mbar_wait(&loaded[it % kStages], it / kStages & 1, &never);
 }
 
 // A warp's rows from row t0, those outside [lo, hi) as zeros; words[r 32] is row r's.
@@ -384,7 +478,7 @@ __device__ __forceinline__ uint32_t* aligned_128(uint32_t* p) {
 // The bounds of the sequences, from shared memory where they fit.
 __device__ __forceinline__ Packed near(const Packed& q, int* bounds) {
   if (!q.off || q.n_seq >= kBounds) return q;
-  for (int i = threadIdx.x; i <= q.n_seq; i += kThreads) bounds[i] = q.off[i];
+  for (int i = threadIdx.x; i <= q.n_seq; i += blockDim.x) bounds[i] = q.off[i];
   __syncthreads();
   return {q.N, q.n_seq, bounds, q.len};
 }
@@ -395,8 +489,7 @@ __device__ __forceinline__ void hand_on_empty(const Packed& q, const float* from
                                               long long D, int d, int warp) {
   for (int s = blockIdx.x * kWarps + warp; s < q.n_seq; s += gridDim.x * kWarps)
     if (bound_of(q, s) >= bound_of(q, s + 1))
-#pragma unroll
-      for (int c = 0; c < CH; ++c) to[s * D + d + c] = from ? from[s * D + d + c] : 0.f;
+      write(to + s * D + d, from ? read<CH>(from + s * D + d) : all<CH>(0.f));
 }
 
 // ------------------------------------------------------------------ forward
@@ -417,10 +510,10 @@ struct ForwardArgs {
 template <typename T, int CH, bool MIX, bool ASYNC>
 __global__ void __launch_bounds__(kThreads, 2)
     glr_forward_kernel(const __grid_constant__ ForwardArgs<T> p) {
+  static_assert(kTile == kChunk, "a tile begins at a kept state");
   extern __shared__ uint32_t dynamic[];
   uint32_t* ring = aligned_128(dynamic);
   __shared__ Exchange<CH, 1> xch;
-  __shared__ Marks marks[2][kWarps];
   __shared__ int bounds[kBounds];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = blockIdx.x % p.cluster, part = blockIdx.x / p.cluster;
@@ -436,38 +529,40 @@ __global__ void __launch_bounds__(kThreads, 2)
   const auto tile_row = [&](int it) { return base + (it * p.cluster + rank) * kTile; };
   exchange_init(xch, p.cluster);
 
-  if (warp == kWarps) {  // the joining warp
+  if (warp == kWarps) {  // joins the warps, and has the tiles loaded
     const auto load = [&](int it) {
       if (ASYNC && lane == 0 && it < steps)
         load_tile<2>(ring, xch.loaded, p.maps, it, blockIdx.y * 32 * CH, tile_row(it));
     };
     for (int it = 0; it < kStages; ++it) load(it);
-    float state[CH] = {};
     for (int it = 0; it < steps; ++it) {
-      wait_for(&xch.formed[it & 1], it >> 1, &xch.abort, p.dev_status);
-      load(it + kStages);  // every warp has read this step's tile
-      join<false, 0>(xch, it, rank, p.cluster, lane, state, p.dev_status);
-      arrive_warp(&xch.joined[it & 1], lane);
+      wait_for(&xch.formed[it & 1], it >> 1 & 1, &xch.abort, p.dev_status);
+      join_warps<false>(xch, it, rank, p.cluster, lane);
+      load(it + kStages);  // over the tile that every warp has read
     }
-    if (ASYNC && lane == 0) drain(xch.loaded, steps, &xch.abort);
+    if (ASYNC && lane == 0) drain(xch.loaded, steps);
+  } else if (warp > kWarps) {  // joins the blocks
+    Vec<CH> state = all<CH>(0.f);
+    for (int it = 0; it < steps; ++it)
+      join_blocks(xch, it, rank, p.cluster, lane, state, p.dev_status);
   } else {
     if (seq.off && p.h_T && on) hand_on_empty<CH>(seq, p.h0, p.h_T, D, d, warp);
     struct Span {
-      float a[kRows][CH], b[kRows][CH];
+      Vec<CH> a[kRows], b[kRows];  // the rows' decays and inputs
       unsigned firsts, lasts;
     };
     Walker<false> walk;
     walk.start(from);
 
     // the pair of the span of step `it`
-    const auto form = [&](int it, Span& s) {
+    const auto form = [&](int it, int buf, Span& s) {
       const int t0 = tile_row(it) + warp * kRows;
-      const Marks& m = marks[it & 1][warp];
-      walk.mark(seq, t0, lane, marks[it & 1][warp], s.firsts, s.lasts);
-      uint32_t* g = tile_at<2>(ring, it, 0) + warp * kRows * 32 + lane;
-      uint32_t* x = tile_at<2>(ring, it, 1) + warp * kRows * 32 + lane;
+      Marks& m = xch.marks[buf][warp];
+      walk.mark(seq, t0, lane, m, s.firsts, s.lasts);
+      uint32_t* g = tile_at<2>(ring, it % kStages, 0) + warp * kRows * 32 + lane;
+      uint32_t* x = tile_at<2>(ring, it % kStages, 1) + warp * kRows * 32 + lane;
       if (ASYNC) {
-        wait_for(&xch.loaded[it % kStages], it / kStages, &xch.abort, p.dev_status);
+        wait_for(&xch.loaded[it % kStages], it / kStages & 1, &xch.abort, p.dev_status);
         if (t0 < lo || t0 + kRows > hi) {  // rows of others and padding: the state goes through
 #pragma unroll
           for (int r = 0; r < kRows; ++r)
@@ -478,78 +573,66 @@ __global__ void __launch_bounds__(kThreads, 2)
         copy_rows(g, p.g + d, p.ld_g, t0, lo, hi, on);
         copy_rows(x, p.x + d, p.ld_x, t0, lo, hi, on);
       }
-      Pair<CH> pair;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) pair.A[c] = 1.f, pair.H[c] = 0.f;
+      Pair<CH> pair{all<CH>(1.f), all<CH>(0.f)};
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
-        const uint32_t wg = g[r * 32], wx = x[r * 32];
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const float lg = get(wg, c, T()), xv = get(wx, c, T());
-          s.a[r][c] = decay_of(lg);
-          s.b[r][c] = MIX ? one_minus(lg, s.a[r][c]) * xv : xv;
-          pair.A[c] *= s.a[r][c];
-          pair.H[c] = fmaf(s.a[r][c], pair.H[c], s.b[r][c]);
-        }
+        const Vec<CH> lg = of_word<T, CH>(g[r * 32]);
+        s.b[r] = of_word<T, CH>(x[r * 32]);
+        s.a[r] = decay_of(lg);
+        if constexpr (MIX) s.b[r] = one_minus(lg, s.a[r]) * s.b[r];
+        pair.A = pair.A * s.a[r];
+        pair.H = fma(s.a[r], pair.H, s.b[r]);
       }
       if (s.firsts) {  // again, with the initial states
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-#pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            if ((s.firsts >> r & 1) && p.h0 && on)
-              s.b[r][c] = fmaf(s.a[r][c], p.h0[m.first[r] * D + d + c], s.b[r][c]);
-            pair.H[c] = s.firsts >> r & 1 ? s.b[r][c] : fmaf(s.a[r][c], pair.H[c], s.b[r][c]);
-            pair.A[c] = -1.f;
-          }
+        for (int r = 0; r < kRows; ++r) {
+          if ((s.firsts >> r & 1) && p.h0 && on)
+            s.b[r] = fma(s.a[r], read<CH>(p.h0 + m.first[r] * D + d), s.b[r]);
+          const Vec<CH> next = fma(s.a[r], pair.H, s.b[r]);
+          pair.H = s.firsts >> r & 1 ? s.b[r] : next;
+        }
+        pair.A = all<CH>(-1.f);
       }
-      xch.warps[it & 1][0][warp][lane] = pair;
-      arrive_warp(&xch.formed[it & 1], lane);
+      xch.warps[buf][0][warp][lane] = pair;
+      arrive_warp(&xch.formed[buf], lane);
     };
 
     // the rows of step `it` from the state in front of them
-    const auto finish = [&](int it, Span& s) {
+    const auto finish = [&](int it, int buf, Span& s) {
       const int t0 = tile_row(it) + warp * kRows;
-      const Marks& m = marks[it & 1][warp];
-      wait_for(&xch.joined[it & 1], it >> 1, &xch.abort, p.dev_status);
-      float h[CH];
-#pragma unroll
-      for (int c = 0; c < CH; ++c) h[c] = xch.states[it & 1][0][warp][lane * CH + c];
-      if (p.h_chunks && on && t0 % kChunk == 0 && t0 >= lo && t0 < hi)
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-          p.h_chunks[t0 / kChunk * D + d + c] = s.firsts & 1 ? 0.f : h[c];
-      T* out = p.h + t0 * D + d;
+      const Marks& m = xch.marks[buf][warp];
+      wait_for(&xch.joined[buf], it >> 1 & 1, &xch.abort, p.dev_status);
+      Vec<CH> h = xch.state[buf][lane];
+      follow(h, xch.warps[buf][0][warp][lane]);
+      if (warp == 0 && p.h_chunks && on && t0 >= lo && t0 < hi)  // kTile == kChunk
+        write(p.h_chunks + t0 / kChunk * D + d, s.firsts & 1 ? all<CH>(0.f) : h);
+      T* to = p.h + t0 * D + d;
       if (!(s.firsts | s.lasts) && t0 >= lo && t0 + kRows <= hi) {
 #pragma unroll
-        for (int r = 0; r < kRows; ++r, out += D) {
-#pragma unroll
-          for (int c = 0; c < CH; ++c) h[c] = fmaf(s.a[r][c], h[c], s.b[r][c]);
-          if (on) put(out, h);
+        for (int r = 0; r < kRows; ++r, to += D) {
+          h = fma(s.a[r], h, s.b[r]);
+          if (on) put(to, h);
         }
-        return;
-      }
+      } else {
 #pragma unroll
-      for (int r = 0; r < kRows; ++r, out += D) {
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-          h[c] = s.firsts >> r & 1 ? s.b[r][c] : fmaf(s.a[r][c], h[c], s.b[r][c]);
-        if (on && t0 + r >= lo && t0 + r < hi) {
-          put(out, h);
-          if ((s.lasts >> r & 1) && p.h_T)
-#pragma unroll
-            for (int c = 0; c < CH; ++c) p.h_T[m.last[r] * D + d + c] = h[c];
+        for (int r = 0; r < kRows; ++r, to += D) {
+          const Vec<CH> next = fma(s.a[r], h, s.b[r]);
+          h = s.firsts >> r & 1 ? s.b[r] : next;
+          if (on && t0 + r >= lo && t0 + r < hi) {
+            put(to, h);
+            if ((s.lasts >> r & 1) && p.h_T) write(p.h_T + m.last[r] * D + d, h);
+          }
         }
       }
     };
 
+    // always one step's pairs ahead of the states
     Span even, odd;
     for (int it = -1; it < steps; it += 2) {
-      if (it + 1 < steps) form(it + 1, even);
-      if (it >= 0) finish(it, odd);
-      if (it + 2 < steps) form(it + 2, odd);
-      if (it + 1 < steps) finish(it + 1, even);
+      if (it + 1 < steps) form(it + 1, 0, even);
+      if (it >= 0) finish(it, 1, odd);
+      if (it + 2 < steps) form(it + 2, 1, odd);
+      if (it + 1 < steps) finish(it + 1, 0, even);
     }
   }
   __syncwarp();
@@ -582,8 +665,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   static_assert(kTile == kChunk, "a tile begins at a kept state");
   extern __shared__ uint32_t dynamic[];
   uint32_t* ring = aligned_128(dynamic);
-  __shared__ Exchange<CH, 2> xch;  // the gradient's pairs, the state's
-  __shared__ Marks marks[2][kWarps];
+  // the gradient's pairs, the state's
+  __shared__ Exchange<CH, 2> xch;
   __shared__ int bounds[kBounds];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = blockIdx.x % p.cluster, part = blockIdx.x / p.cluster;
@@ -599,58 +682,73 @@ __global__ void __launch_bounds__(kThreads, 2)
   const auto tile_row = [&](int it) { return top - (it * p.cluster + rank + 1) * kTile; };
   exchange_init(xch, p.cluster);
 
-  if (warp == kWarps) {  // the joining warp
+  if (warp == kWarps) {  // joins the gradient's pairs of the warps, and has the tiles loaded
     const auto load = [&](int it) {
       if (ASYNC && lane == 0 && it < steps)
         load_tile<3>(ring, xch.loaded, p.maps, it, blockIdx.y * 32 * CH, tile_row(it));
     };
-    const auto kept_state = [&](int it, float(&k)[CH]) {
-      const int tile = tile_row(it);
-#pragma unroll
-      for (int c = 0; c < CH; ++c)
-        k[c] = on && it < steps && tile >= 0 ? p.h_chunks[tile / kChunk * D + d + c] : 0.f;
-    };
     for (int it = 0; it < kStages; ++it) load(it);
-    float state[CH] = {}, kept[CH];
-    kept_state(0, kept);
     for (int it = 0; it < steps; ++it) {
-      wait_for(&xch.formed[it & 1], it >> 1, &xch.abort, p.dev_status);
-      join<false, 1>(xch, it, 0, 1, lane, kept, p.dev_status);
-      kept_state(it + 1, kept);
-      join<true, 0>(xch, it, rank, p.cluster, lane, state, p.dev_status);
-      arrive_warp(&xch.joined[it & 1], lane);
+      wait_for(&xch.formed[it & 1], it >> 1 & 1, &xch.abort, p.dev_status);
+      join_warps<true>(xch, it, rank, p.cluster, lane);
       if (ASYNC && it > 0) {  // the step before has been read for the second time
-        wait_for(&xch.freed[(it - 1) % kStages], (it - 1) / kStages, &xch.abort, p.dev_status);
+        wait_for(&xch.freed[(it - 1) % kStages], (it - 1) / kStages & 1, &xch.abort, p.dev_status);
         load(it - 1 + kStages);
       }
     }
-    if (ASYNC && lane == 0) drain(xch.loaded, steps, &xch.abort);
+    if (ASYNC && lane == 0) drain(xch.loaded, steps);
+  } else if (warp > kWarps) {  // joins the state's pairs of the warps, and the blocks
+    const auto kept_state = [&](int it) {
+      const int tile = tile_row(it);
+      return on && it < steps && tile >= 0 ? read<CH>(p.h_chunks + tile / kChunk * D + d)
+                                           : all<CH>(0.f);
+    };
+    Vec<CH> state = all<CH>(0.f), kept = kept_state(0);
+    for (int it = 0; it < steps; ++it) {
+      wait_for(&xch.formed[it & 1], it >> 1 & 1, &xch.abort, p.dev_status);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {  // the state in front of each warp's rows, as A
+        const Pair<CH> pair = xch.warps[it & 1][1][w][lane];
+        xch.warps[it & 1][1][w][lane].A = kept;
+        follow(kept, pair);
+      }
+      kept = kept_state(it + 1);
+      join_blocks(xch, it, rank, p.cluster, lane, state, p.dev_status);
+    }
   } else {
     if (seq.off && p.dh0 && on) hand_on_empty<CH>(seq, p.dh_T, p.dh0, D, d, warp);
-    struct Span {
-      float a[kRows][CH], om[MIX ? kRows : 1][CH];  // exp(g), 1 - exp(g)
-      unsigned firsts, lasts;
-    };
     Walker<true> walk;
     walk.start(until);
-    const auto words = [&](int it, int array) {
-      return tile_at<3>(ring, it, array) + warp * kRows * 32 + lane;
+    const auto state_before = [&](const Marks& m, int r) {  // where a sequence begins
+      return on && p.h0 ? read<CH>(p.h0 + m.first[r] * D + d) : all<CH>(0.f);
     };
-    const auto state_before = [&](const Marks& m, int r, int c) {  // where a sequence begins
-      return on && p.h0 ? p.h0[m.first[r] * D + d + c] : 0.f;
+    const auto grad_after = [&](const Marks& m, int r) {  // where a sequence ends
+      return on && p.dh_T ? read<CH>(p.dh_T + m.last[r] * D + d) : all<CH>(0.f);
     };
-    const auto grad_after = [&](const Marks& m, int r, int c) {  // where a sequence ends
-      return on && p.dh_T ? p.dh_T[m.last[r] * D + d + c] : 0.f;
+    // exp(g) of the rows, and 1 - exp(g) where it is needed
+    const auto gates = [&](const uint32_t* g, Vec<CH>(&a)[kRows], Vec<CH>(&om)[MIX ? kRows : 1]) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const Vec<CH> lg = of_word<T, CH>(g[r * 32]);
+        a[r] = decay_of(lg);
+        if constexpr (MIX) om[r] = one_minus(lg, a[r]);
+      }
     };
 
     // the pairs of the span of step `it`
-    const auto form = [&](int it, Span& s) {
+    struct Masks {
+      unsigned firsts, lasts;
+    };
+    Turn form_tile, tile;
+    const auto form = [&](int it, int buf, Masks& s) {
       const int t0 = tile_row(it) + warp * kRows;
-      const Marks& m = marks[it & 1][warp];
-      walk.mark(seq, t0, lane, marks[it & 1][warp], s.firsts, s.lasts);
-      uint32_t *g = words(it, 0), *x = words(it, 1), *dh = words(it, 2);
+      Marks& m = xch.marks[buf][warp];
+      walk.mark(seq, t0, lane, m, s.firsts, s.lasts);
+      uint32_t *g = tile_at<3>(ring, form_tile.at, 0) + warp * kRows * 32 + lane,
+               *x = tile_at<3>(ring, form_tile.at, 1) + warp * kRows * 32 + lane,
+               *dh = tile_at<3>(ring, form_tile.at, 2) + warp * kRows * 32 + lane;
       if (ASYNC) {
-        wait_for(&xch.loaded[it % kStages], it / kStages, &xch.abort, p.dev_status);
+        wait_for(&xch.loaded[form_tile.at], form_tile.use, &xch.abort, p.dev_status);
         if (t0 < lo || t0 + kRows > hi) {  // rows of others and padding: all goes through
 #pragma unroll
           for (int r = 0; r < kRows; ++r)
@@ -662,90 +760,85 @@ __global__ void __launch_bounds__(kThreads, 2)
         copy_rows(x, p.x + d, p.ld_x, t0, lo, hi, on);
         copy_rows(dh, p.dh + d, D, t0, lo, hi, on);
       }
-      const auto input = [&](int r, int c) {
-        const float xv = get(x[r * 32], c, T());
-        return MIX ? s.om[MIX ? r : 0][c] * xv : xv;
+      Vec<CH> a[kRows], om[MIX ? kRows : 1];
+      gates(g, a, om);
+      const auto input = [&](int r) {
+        const Vec<CH> xv = of_word<T, CH>(x[r * 32]);
+        if constexpr (MIX)
+          return om[r] * xv;
+        else
+          return xv;
       };
-      Pair<CH> fwd, rev;
+      Pair<CH> fwd{all<CH>(1.f), all<CH>(0.f)}, rev = fwd;
 #pragma unroll
-      for (int c = 0; c < CH; ++c) fwd.A[c] = 1.f, fwd.H[c] = rev.H[c] = 0.f;
+      for (int r = 0; r < kRows; ++r) {
+        fwd.A = fwd.A * a[r];
+        fwd.H = fma(a[r], fwd.H, input(r));
+      }
 #pragma unroll
-      for (int r = 0; r < kRows; ++r)
+      for (int r = kRows - 1; r >= 0; --r) rev.H = a[r] * (of_word<T, CH>(dh[r * 32]) + rev.H);
+      rev.A = fwd.A;
+      if (const unsigned firsts = s.firsts) {  // again, from the initial states
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const float lg = get(g[r * 32], c, T());
-          s.a[r][c] = decay_of(lg);
-          if (MIX) s.om[MIX ? r : 0][c] = one_minus(lg, s.a[r][c]);
-          fwd.A[c] *= s.a[r][c];
-          fwd.H[c] = fmaf(s.a[r][c], fwd.H[c], input(r, c));
+        for (int r = 0; r < kRows; ++r) {
+          if (firsts >> r & 1) fwd.H = state_before(m, r);
+          fwd.H = fma(a[r], fwd.H, input(r));
         }
-#pragma unroll
-      for (int r = kRows - 1; r >= 0; --r)
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-          rev.H[c] = s.a[r][c] * (get(dh[r * 32], c, T()) + rev.H[c]);
-#pragma unroll
-      for (int c = 0; c < CH; ++c) rev.A[c] = fwd.A[c];
-      if (s.firsts) {  // again, from the initial states
-#pragma unroll
-        for (int r = 0; r < kRows; ++r)
-#pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            if (s.firsts >> r & 1) fwd.H[c] = state_before(m, r, c);
-            fwd.H[c] = fmaf(s.a[r][c], fwd.H[c], input(r, c));
-            fwd.A[c] = -1.f;
-          }
+        fwd.A = all<CH>(-1.f);
       }
-      if (s.lasts) {  // again, from the final states' gradients
+      if (const unsigned lasts = s.lasts) {  // again, from the final states' gradients
 #pragma unroll
-        for (int r = kRows - 1; r >= 0; --r)
-#pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            if (s.lasts >> r & 1) rev.H[c] = grad_after(m, r, c);
-            rev.H[c] = s.a[r][c] * (get(dh[r * 32], c, T()) + rev.H[c]);
-            rev.A[c] = -1.f;
-          }
+        for (int r = kRows - 1; r >= 0; --r) {
+          if (lasts >> r & 1) rev.H = grad_after(m, r);
+          rev.H = a[r] * (of_word<T, CH>(dh[r * 32]) + rev.H);
+        }
+        rev.A = all<CH>(-1.f);
       }
-      xch.warps[it & 1][0][warp][lane] = rev;
-      xch.warps[it & 1][1][warp][lane] = fwd;
-      arrive_warp(&xch.formed[it & 1], lane);
+      xch.warps[buf][0][warp][lane] = rev;
+      xch.warps[buf][1][warp][lane] = fwd;
+      arrive_warp(&xch.formed[buf], lane);
+      form_tile.next();
     };
 
     // the gradients of step `it`
-    const auto finish = [&](int it, Span& s) {
+    const auto finish = [&](int it, int buf, const Masks& s) {
       const int t0 = tile_row(it) + warp * kRows;
-      const Marks& m = marks[it & 1][warp];
-      const uint32_t *x = words(it, 1), *dh = words(it, 2);
-      wait_for(&xch.joined[it & 1], it >> 1, &xch.abort, p.dev_status);
-      float back[CH], h[CH], before[kRows][CH];
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        back[c] = xch.states[it & 1][0][warp][lane * CH + c];
-        h[c] = xch.states[it & 1][1][warp][lane * CH + c];
-      }
-      const auto advance = [&](int r, int c) {
-        const float xv = get(x[r * 32], c, T());
-        before[r][c] = MIX ? h[c] - xv : h[c];
-        h[c] = fmaf(s.a[r][c], h[c], MIX ? s.om[MIX ? r : 0][c] * xv : xv);
+      const Marks& m = xch.marks[buf][warp];
+      const unsigned firsts = s.firsts, lasts = s.lasts;
+      const uint32_t *g = tile_at<3>(ring, tile.at, 0) + warp * kRows * 32 + lane,
+                     *x = tile_at<3>(ring, tile.at, 1) + warp * kRows * 32 + lane,
+                     *dh = tile_at<3>(ring, tile.at, 2) + warp * kRows * 32 + lane;
+      Vec<CH> a[kRows], om[MIX ? kRows : 1];
+      gates(g, a, om);
+      wait_for(&xch.joined[buf], it >> 1 & 1, &xch.abort, p.dev_status);
+      Vec<CH> back = xch.state[buf][lane], h = xch.warps[buf][1][warp][lane].A;
+      follow(back, xch.warps[buf][0][warp][lane]);
+      Vec<CH> before[kRows], o_g, o_x;
+      const auto advance = [&](int r) {
+        const Vec<CH> xv = of_word<T, CH>(x[r * 32]);
+        if constexpr (MIX) {
+          before[r] = h - xv;
+          h = fma(a[r], h, om[r] * xv);
+        } else {
+          before[r] = h;
+          h = fma(a[r], h, xv);
+        }
+      };
+      const auto retreat = [&](int r) {
+        const Vec<CH> lam = of_word<T, CH>(dh[r * 32]) + back;
+        back = a[r] * lam;
+        o_x = lam;
+        if constexpr (MIX) o_x = om[r] * lam;
+        o_g = back * before[r];
       };
       T* dg = p.dg + (t0 + kRows - 1) * p.ld_g + d;
       T* dx = p.dx + (t0 + kRows - 1) * p.ld_x + d;
-      float o_g[CH], o_x[CH];
-      const auto retreat = [&](int r, int c) {
-        const float lam = get(dh[r * 32], c, T()) + back[c];
-        back[c] = s.a[r][c] * lam;
-        o_x[c] = MIX ? s.om[MIX ? r : 0][c] * lam : lam;
-        o_g[c] = back[c] * before[r][c];
-      };
-      if (!(s.firsts | s.lasts) && t0 >= lo && t0 + kRows <= hi) {
+      if (!(firsts | lasts) && t0 >= lo && t0 + kRows <= hi) {
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-#pragma unroll
-          for (int c = 0; c < CH; ++c) advance(r, c);
+        for (int r = 0; r < kRows; ++r) advance(r);
 #pragma unroll
         for (int r = kRows - 1; r >= 0; --r, dg -= p.ld_g, dx -= p.ld_x) {
-#pragma unroll
-          for (int c = 0; c < CH; ++c) retreat(r, c);
+          retreat(r);
           if (on) {
             put(dg, o_g);
             put(dx, o_x);
@@ -753,37 +846,32 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       } else {
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-#pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            if (s.firsts >> r & 1) h[c] = state_before(m, r, c);
-            advance(r, c);
-          }
+        for (int r = 0; r < kRows; ++r) {
+          if (firsts >> r & 1) h = state_before(m, r);
+          advance(r);
+        }
 #pragma unroll
         for (int r = kRows - 1; r >= 0; --r, dg -= p.ld_g, dx -= p.ld_x) {
-#pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            if (s.lasts >> r & 1) back[c] = grad_after(m, r, c);
-            retreat(r, c);
-          }
+          if (lasts >> r & 1) back = grad_after(m, r);
+          retreat(r);
           if (on && t0 + r >= lo && t0 + r < hi) {
             put(dg, o_g);
             put(dx, o_x);
-            if ((s.firsts >> r & 1) && p.dh0)
-#pragma unroll
-              for (int c = 0; c < CH; ++c) p.dh0[m.first[r] * D + d + c] = back[c];
+            if ((firsts >> r & 1) && p.dh0) write(p.dh0 + m.first[r] * D + d, back);
           }
         }
       }
-      if (ASYNC) arrive_warp(&xch.freed[it % kStages], lane);
+      if (ASYNC) arrive_warp(&xch.freed[tile.at], lane);
+      tile.next();
     };
 
-    Span even, odd;
+    // always one step's pairs ahead of the states
+    Masks even, odd;
     for (int it = -1; it < steps; it += 2) {
-      if (it + 1 < steps) form(it + 1, even);
-      if (it >= 0) finish(it, odd);
-      if (it + 2 < steps) form(it + 2, odd);
-      if (it + 1 < steps) finish(it + 1, even);
+      if (it + 1 < steps) form(it + 1, 0, even);
+      if (it >= 0) finish(it, 1, odd);
+      if (it + 2 < steps) form(it + 2, 1, odd);
+      if (it + 1 < steps) finish(it + 1, 0, even);
     }
   }
   __syncwarp();
@@ -842,7 +930,8 @@ Grid grid_of(int N, int D, int n_seq, int width) {
 
 // Launches KERNEL with `ring` bytes of shared memory beside its own.
 template <typename Args>
-int launch(void (*kernel)(Args), const Grid& g, int ring, const Args& args, cudaStream_t stream) {
+int launch(void (*kernel)(Args), const Grid& g, int ring, const Args& args,
+           cudaStream_t stream) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring) !=
       cudaSuccess)
     return MOE_ERR_CUDA;
