@@ -1,8 +1,13 @@
 // Norm of query and key heads with the rotation by position, forward and backward
 // (include/linear_attention.h has the formulas).
 #include <math.h>
+#include <stdlib.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "moe_internal.h"
+#include "ptx.cuh"
 
 #include "../../include/linear_attention.h"
 
@@ -10,6 +15,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxD = 256;
+constexpr int kSms = 152;  // of the GPU that the cuts are made for
 
 // One group of heads (q or k) as the kernels see it.
 struct Side {
@@ -22,157 +28,343 @@ struct Side {
   int heads;
 };
 
-__device__ __forceinline__ float ld(const float* p, long long i) { return p[i]; }
-__device__ __forceinline__ float ld(const __nv_bfloat16* p, long long i) {
-  return __bfloat162float(p[i]);
+// Eight consecutive values of a row: what a lane holds.
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
-__device__ __forceinline__ void st(float* p, long long i, float v) { p[i] = v; }
-__device__ __forceinline__ void st(__nv_bfloat16* p, long long i, float v) {
-  p[i] = __float2bfloat16_rn(v);
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                 pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
 }
 
-// cos and sin of pos * inv_freq: the angle in turns, in 64 bits, less its whole turns; what is
-// left (at most half a turn) is exact to 2^-25 of a turn in fp32.
-__device__ __forceinline__ float2 cos_sin(int pos, double inv_freq) {
-  double turns = static_cast<double>(pos) * (inv_freq * 0.15915494309189533577);
-  turns -= rint(turns);
+// A block takes kHeads (a launch's choice) heads of a range of tokens, in tiles of kTokens.  L
+// lanes hold a row (a token's head), 8 values each, and always the same head, so that its weight
+// stays in registers and its weight gradient gathers there.  The block forms the tile's sines
+// and cosines once, in shared memory, for all its heads.
+constexpr int kThreads = 256;
+constexpr int kTokens = 16;
+constexpr int kPairs = kMaxD / 2;
+
+struct Shape {
+  int N, D, rot, interleaved, heads_per_block, tokens_per_block;
+  float eps;
+  const int* pos;
+  const double* inv_freq;
+};
+
+// The angle of pair i at position pos in turns, modulo 1, as a 64-bit fraction: frequency (turns a
+// token, the same fraction) times pos in whole numbers, which wraps as turns do.  Exact but for the
+// frequency's own rounding (2^-53 of it, times pos), at any position; a product in 64-bit floating
+// point would be as exact, at a thirtieth of the rate on this GPU.
+__device__ __forceinline__ unsigned long long fraction_of(double inv_freq) {
+  double f = inv_freq * 0.15915494309189533577;
+  f -= floor(f);
+  return static_cast<unsigned long long>(f * 18446744073709551616.0);
+}
+
+// cos and sin of it from its upper 32 bits (half of 2^-32 of a turn off at most; 2^-25 after the
+// conversion to fp32 for angles of a quarter of a turn and more).
+__device__ __forceinline__ float2 cos_sin(unsigned long long fraction, int pos) {
+  const unsigned long long turns = fraction * static_cast<unsigned long long>(static_cast<long long>(pos));
   float2 cs;
-  sincospif(2.f * static_cast<float>(turns), &cs.y, &cs.x);
+  sincospif(static_cast<float>(static_cast<int>(turns >> 32)) * 4.656612873077393e-10f, &cs.y, &cs.x);
   return cs;
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Tile of cosines and sines.  A lane rotates `per` = 8 pairs (halves: its values are one half of
+// them) or 4 (neighbours); pair i belongs to the lanes' place i / per.  Two pairs make a float4,
+// and the float4s of neighbouring places are neighbours, so that lanes read without conflicts.
+__device__ __forceinline__ void fill_angles(float4* table, const unsigned long long* fractions,
+                                            const Shape& s, long long t0, long long hi) {
+  const int half = s.rot / 2, per = s.interleaved ? 4 : 8, places = half / per;
+  const int n = static_cast<int>(min(static_cast<long long>(kTokens), hi - t0)) * half;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int t = i / half, pair = i % half, in = pair % per;
+    reinterpret_cast<float2*>(table)[2 * (t * (half / 2) + in / 2 * places + pair / per) + in % 2] =
+        cos_sin(fractions[pair], s.pos[t0 + t]);
+  }
+}
+
+// y = R(th) n (BACK: R(-th) n) for the 8 values of a lane; `turns` says whether it has a rotated
+// pair, `low` whether its values are the first members of the pairs (halves).
+template <bool BACK>
+__device__ __forceinline__ void rotate(float (&v)[8], const float4* table, const Shape& s, int t,
+                                       int sub, int partner, bool turns, bool low) {
+  if (s.rot == 0) return;
+  const int half = s.rot / 2;
+  if (s.interleaved) {
+    if (!turns) return;
+    const float4* cs = table + t * (half / 2) + sub;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    for (int c = 0; c < 2; ++c) {
+      const float4 w = cs[c * (half / 4)];
+      const float cosv[2] = {w.x, w.z}, sinv[2] = {BACK ? -w.y : w.y, BACK ? -w.w : w.w};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float a = v[4 * c + 2 * e], b = v[4 * c + 2 * e + 1];
+        v[4 * c + 2 * e] = a * cosv[e] - b * sinv[e];
+        v[4 * c + 2 * e + 1] = b * cosv[e] + a * sinv[e];
+      }
+    }
+    return;
+  }
+  // the first members need -sin times the second ones, the second +sin times the first
+  const float sign = low == BACK ? 1.f : -1.f;
+  const float4* cs = table + t * (half / 2) + (low ? sub : sub - half / 8);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const float p0 = __shfl_sync(~0u, v[2 * c], partner);
+    const float p1 = __shfl_sync(~0u, v[2 * c + 1], partner);
+    if (turns) {
+      const float4 w = cs[c * (half / 8)];
+      v[2 * c] = fmaf(sign * w.y, p0, v[2 * c] * w.x);
+      v[2 * c + 1] = fmaf(sign * w.w, p1, v[2 * c + 1] * w.z);
+    }
+  }
+}
+
+template <int L>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
 
-// One warp per (token, head).
-template <typename T>
-__global__ void __launch_bounds__(256) rope_forward_kernel(int N, int D, int rot, int interleaved,
-                                                           float eps, const int* pos,
-                                                           const double* inv_freq, Side q, Side k) {
-  __shared__ float rows[8][kMaxD];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int heads = q.heads + k.heads;
-  const long long r = static_cast<long long>(blockIdx.x) * 8 + warp;
-  if (r >= static_cast<long long>(N) * heads) return;
-  const int t = static_cast<int>(r / heads);
-  int h = static_cast<int>(r % heads);
-  const Side& s = h < q.heads ? q : k;
-  if (h >= q.heads) h -= q.heads;
-  const T* x = static_cast<const T*>(s.x) + t * s.x_ts + h * s.x_hs;
-  T* y = static_cast<T*>(s.out) + t * s.o_ts + h * s.o_hs;
-  float* n = rows[warp];
-  float sum = 0.f;
-  for (int i = lane; i < D; i += 32) {
-    n[i] = ld(x, i);
-    sum += n[i] * n[i];
-  }
-  const float rstd = rsqrtf(warp_sum(sum) / D + eps);
-  for (int i = lane; i < D; i += 32)
-    n[i] *= rstd * (s.weight ? s.weight[static_cast<long long>(h) * s.w_hs + i] : 1.f);
-  __syncwarp();
-  for (int i = lane; i < rot / 2; i += 32) {
-    const int a = interleaved ? 2 * i : i, b = interleaved ? 2 * i + 1 : i + rot / 2;
-    const float2 cs = cos_sin(pos[t], inv_freq[i]);
-    st(y, a, n[a] * cs.x - n[b] * cs.y);
-    st(y, b, n[b] * cs.x + n[a] * cs.y);
-  }
-  for (int i = rot + lane; i < D; i += 32) st(y, i, n[i]);
-}
+// What a lane has to do.
+template <int L>
+struct Lane {
+  int sub, partner;       // its place in the row, and the lane with the other halves of its pairs
+  int head, slot;         // head of all heads; which tokens of a tile (slot, slot + stride, ...)
+  int stride;
+  bool in, turns, low;    // has values; rotates them; they are first members
 
-// Blocks (split, head): each of the 8 warps takes every 8th token of the split, so the weight
-// gradient of a head gathers in registers; partial [splits][heads][D] holds the blocks' sums.
-template <typename T, typename G>
-__global__ void __launch_bounds__(256) rope_backward_kernel(int N, int D, int rot, int interleaved,
-                                                            float eps, const int* pos,
-                                                            const double* inv_freq, Side q, Side k,
-                                                            int per_split, float* partial) {
-  __shared__ float rows[8][kMaxD];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.y;
-  const Side& s = c < q.heads ? q : k;
-  const int h = c < q.heads ? c : c - q.heads;
-  const long long lo = static_cast<long long>(blockIdx.x) * per_split;
-  const long long hi = min(lo + per_split, static_cast<long long>(N));
-  float* n = rows[warp];
-  float w[kMaxD / 32], dw[kMaxD / 32];
-#pragma unroll
-  for (int j = 0; j < kMaxD / 32; ++j) {
-    const int i = lane + 32 * j;
-    w[j] = i < D && s.weight ? s.weight[static_cast<long long>(h) * s.w_hs + i] : 1.f;
-    dw[j] = 0.f;
+  __device__ __forceinline__ Lane(const Shape& s, int heads) {
+    const int group = threadIdx.x / L;
+    sub = threadIdx.x % L;
+    slot = group / s.heads_per_block;
+    stride = kThreads / L / s.heads_per_block;
+    head = blockIdx.y * s.heads_per_block + group % s.heads_per_block;
+    in = slot < stride && head < heads && sub * 8 < s.D;
+    if (slot >= stride || head >= heads) slot = kTokens, head = heads - 1;
+    const int half = s.rot / 16;  // lanes of the first members
+    turns = sub * 8 < s.rot;
+    low = sub < half;
+    const int other = !turns ? sub : low ? sub + half : sub - half;
+    partner = (threadIdx.x & 31 & ~(L - 1)) + (s.interleaved ? sub : other);
   }
-  for (long long t = lo + warp; t < hi; t += 8) {
-    const T* x = static_cast<const T*>(s.x) + t * s.x_ts + h * s.x_hs;
-    const G* dy = static_cast<const G*>(s.dy) + t * s.dy_ts + h * s.dy_hs;
-    T* dx = static_cast<T*>(s.out) + t * s.o_ts + h * s.o_hs;
-    for (int i = lane; i < rot / 2; i += 32) {
-      const int a = interleaved ? 2 * i : i, b = interleaved ? 2 * i + 1 : i + rot / 2;
-      const float2 cs = cos_sin(pos[t], inv_freq[i]);
-      const float da = ld(dy, a), db = ld(dy, b);
-      n[a] = da * cs.x + db * cs.y;
-      n[b] = db * cs.x - da * cs.y;
-    }
-    for (int i = rot + lane; i < D; i += 32) n[i] = ld(dy, i);
-    float xv[kMaxD / 32], sum = 0.f;
+};
+
+template <typename T, int L>
+__global__ void __launch_bounds__(kThreads, 4)
+    rope_forward_kernel(const Shape s, const Side q, const Side k) {
+  extern __shared__ float4 table[];  // [2][kTokens][rot / 4]
+  __shared__ unsigned long long fractions[kPairs];
+  for (int i = threadIdx.x; i < s.rot / 2; i += kThreads) fractions[i] = fraction_of(s.inv_freq[i]);
+  const Lane<L> me(s, q.heads + k.heads);
+  const Side& side = me.head < q.heads ? q : k;
+  const int h = me.head < q.heads ? me.head : me.head - q.heads;
+  float w[8];
 #pragma unroll
-    for (int j = 0; j < kMaxD / 32; ++j) {
-      const int i = lane + 32 * j;
-      xv[j] = i < D ? ld(x, i) : 0.f;
-      sum += xv[j] * xv[j];
-    }
-    const float rstd = rsqrtf(warp_sum(sum) / D + eps);
-    __syncwarp();
-    float dot = 0.f;
+  for (int e = 0; e < 8; ++e)
+    w[e] = me.in && side.weight ? side.weight[static_cast<long long>(h) * side.w_hs + me.sub * 8 + e] : 1.f;
+  const T* x = static_cast<const T*>(side.x) + h * side.x_hs + me.sub * 8;
+  T* y = static_cast<T*>(side.out) + h * side.o_hs + me.sub * 8;
+  const long long lo = static_cast<long long>(blockIdx.x) * s.tokens_per_block;
+  const long long hi = min(lo + s.tokens_per_block, static_cast<long long>(s.N));
+  const float inv_D = 1.f / s.D;
+  __syncthreads();
+  int buf = 0;
+  for (long long t0 = lo; t0 < hi; t0 += kTokens, buf ^= 1) {
+    float4* angles = table + buf * kTokens * (s.rot / 4);
+    if (s.rot) fill_angles(angles, fractions, s, t0, hi);
+    __syncthreads();  // (the other buffer's readers are done when they come here again)
+    const int n = static_cast<int>(min(static_cast<long long>(kTokens), hi - t0));
+    for (int t = 0; t < n; t += 2 * me.stride) {  // the same for all lanes: they shuffle
+      float v[2][8];
+      bool row[2];
 #pragma unroll
-    for (int j = 0; j < kMaxD / 32; ++j) {
-      const int i = lane + 32 * j;
-      if (i < D) {
-        xv[j] *= rstd;
-        dw[j] += n[i] * xv[j];
-        dot += n[i] * w[j] * xv[j];
+      for (int u = 0; u < 2; ++u) {
+        const int at = t + me.slot + u * me.stride;
+        row[u] = me.in && at < n;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
+        if (row[u]) load8(x + (t0 + at) * side.x_ts, v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int at = t + me.slot + u * me.stride;
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(v[u][e], v[u][e], sum);
+        const float rstd = rsqrtf(fmaf(row_sum<L>(sum), inv_D, s.eps));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[u][e] *= rstd * w[e];
+        rotate<false>(v[u], angles, s, row[u] ? at : 0, me.sub, me.partner, me.turns, me.low);
+        if (row[u]) store8(y + (t0 + at) * side.o_ts, v[u]);
       }
     }
-    dot = warp_sum(dot) / D;
-#pragma unroll
-    for (int j = 0; j < kMaxD / 32; ++j) {
-      const int i = lane + 32 * j;
-      if (i < D) st(dx, i, rstd * (n[i] * w[j] - xv[j] * dot));
-    }
-    __syncwarp();
-  }
-  if (!partial) return;
-#pragma unroll
-  for (int j = 0; j < kMaxD / 32; ++j)
-    if (lane + 32 * j < D) n[lane + 32 * j] = dw[j];
-  __syncthreads();
-  for (int i = threadIdx.x; i < D; i += 256) {
-    float sum = 0.f;
-    for (int v = 0; v < 8; ++v) sum += rows[v][i];
-    partial[(static_cast<long long>(blockIdx.x) * gridDim.y + c) * D + i] = sum;
   }
 }
 
-// dweight from the blocks' sums: one thread per value, the splits (and, for a shared row, the
-// heads) in order.
-__global__ void rope_dweight_kernel(const float* partial, int splits, int heads, int D,
-                                    int first_head, int n_heads, int per_head, float* dweight) {
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= (per_head ? n_heads : 1) * D) return;
-  const int h0 = per_head ? i / D : 0, h1 = per_head ? h0 + 1 : n_heads;
+// partial: [blocks][2][D] (the shared weights of q and k) or [gridDim.x][heads][D] (a row for each
+// head), the sums of the block's rows; null: not wanted.
+template <typename T, typename G, int L>
+__global__ void __launch_bounds__(kThreads, 3)
+    rope_backward_kernel(const Shape s, const Side q, const Side k, float* partial) {
+  extern __shared__ float4 table[];  // [2][kTokens][rot / 4]
+  __shared__ unsigned long long fractions[kPairs];
+  __shared__ float sums[kThreads / L][L * 8];
+  for (int i = threadIdx.x; i < s.rot / 2; i += kThreads) fractions[i] = fraction_of(s.inv_freq[i]);
+  const int heads = q.heads + k.heads;
+  const Lane<L> me(s, heads);
+  const Side& side = me.head < q.heads ? q : k;
+  const int h = me.head < q.heads ? me.head : me.head - q.heads;
+  float w[8], dw[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    w[e] = me.in && side.weight ? side.weight[static_cast<long long>(h) * side.w_hs + me.sub * 8 + e] : 1.f;
+    dw[e] = 0.f;
+  }
+  const T* x = static_cast<const T*>(side.x) + h * side.x_hs + me.sub * 8;
+  const G* dy = static_cast<const G*>(side.dy) + h * side.dy_hs + me.sub * 8;
+  T* dx = static_cast<T*>(side.out) + h * side.o_hs + me.sub * 8;
+  const long long lo = static_cast<long long>(blockIdx.x) * s.tokens_per_block;
+  const long long hi = min(lo + s.tokens_per_block, static_cast<long long>(s.N));
+  const float inv_D = 1.f / s.D;
+  __syncthreads();
+  int buf = 0;
+  for (long long t0 = lo; t0 < hi; t0 += kTokens, buf ^= 1) {
+    float4* angles = table + buf * kTokens * (s.rot / 4);
+    if (s.rot) fill_angles(angles, fractions, s, t0, hi);
+    __syncthreads();
+    const int n = static_cast<int>(min(static_cast<long long>(kTokens), hi - t0));
+    for (int t = 0; t < n; t += 2 * me.stride) {
+      float v[2][8], d[2][8];
+      bool row[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int at = t + me.slot + u * me.stride;
+        row[u] = me.in && at < n;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[u][e] = d[u][e] = 0.f;
+        if (row[u]) {
+          load8(x + (t0 + at) * side.x_ts, v[u]);
+          load8(dy + (t0 + at) * side.dy_ts, d[u]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int at = t + me.slot + u * me.stride;
+        rotate<true>(d[u], angles, s, row[u] ? at : 0, me.sub, me.partner, me.turns, me.low);
+        // both sums of the row at once: u = w dn; mean(u x^) = rstd mean(u x)
+        float sum = 0.f, dot = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          sum = fmaf(v[u][e], v[u][e], sum);
+          dot = fmaf(d[u][e] * w[e], v[u][e], dot);
+        }
+        const float rstd = rsqrtf(fmaf(row_sum<L>(sum), inv_D, s.eps));
+        const float c = row_sum<L>(dot) * inv_D * rstd * rstd;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dw[e] = fmaf(d[u][e], v[u][e] * rstd, dw[e]);
+          d[u][e] = rstd * fmaf(-c, v[u][e], d[u][e] * w[e]);
+        }
+        if (row[u]) store8(dx + (t0 + at) * side.o_ts, d[u]);
+      }
+    }
+  }
+  if (!partial) return;
+  const int group = threadIdx.x / L;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sums[group][me.sub * 8 + e] = dw[e];
+  __syncthreads();
+  const int groups = kThreads / L / s.heads_per_block * s.heads_per_block;
+  const int first = blockIdx.y * s.heads_per_block;
+  if (q.w_hs || k.w_hs) {  // a row for each head: its groups, every heads_per_block'th
+    for (int i = threadIdx.x; i < s.heads_per_block * s.D; i += kThreads) {
+      const int head = i / s.D, e = i % s.D;
+      if (first + head >= heads) continue;
+      float sum = 0.f;
+      for (int g = head; g < groups; g += s.heads_per_block) sum += sums[g][e];
+      partial[(static_cast<long long>(blockIdx.x) * heads + first + head) * s.D + e] = sum;
+    }
+  } else {
+    for (int i = threadIdx.x; i < 2 * s.D; i += kThreads) {
+      const int of_k = i / s.D, e = i % s.D;
+      float sum = 0.f;
+      for (int g = 0; g < groups; ++g) {
+        const int head = first + g % s.heads_per_block;
+        if (head < heads && (head >= q.heads) == of_k) sum += sums[g][e];
+      }
+      partial[(static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 * s.D + i] = sum;
+    }
+  }
+}
+
+// dweight from the blocks' sums: output row b of D values is the sum of rows b + j + i `step` of
+// partial, j < inner, i < outer.  32 columns to a block; its 32 warps take every 32nd row each and
+// are then added in order.
+__global__ void __launch_bounds__(1024)
+    rope_dweight_kernel(const float* partial, int outer, int inner, int step, int D,
+                        float* dweight) {
+  __shared__ float sums[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i = blockIdx.x * 32 + lane;
+  const float* from = partial + static_cast<long long>(blockIdx.y) * D + i;
   float sum = 0.f;
-  for (int s = 0; s < splits; ++s)
-    for (int h = h0; h < h1; ++h)
-      sum += partial[(static_cast<long long>(s) * heads + first_head + h) * D + i % D];
-  dweight[i] = sum;
+  if (i < D)
+#pragma unroll 4
+    for (int r = warp; r < outer * inner; r += 32)
+      sum += from[(static_cast<long long>(r / inner) * step + r % inner) * D];
+  sums[warp][lane] = sum;
+  __syncthreads();
+  if (warp) return;
+#pragma unroll
+  for (int v = 1; v < 32; ++v) sum += sums[v][lane];
+  if (i < D) dweight[static_cast<long long>(blockIdx.y) * D + i] = sum;
 }
 
 // ------------------------------------------------------------------------ host side
 
-int per_split_of(int N) { return N <= 64 * 64 ? 64 : (N + 63) / 64; }
-int splits_of(int N) { return (N + per_split_of(N) - 1) / per_split_of(N); }
+// Lanes of a row: 8 values each, a power of two of them that divides a warp; heads of less than 64
+// values leave some idle.
+int lanes_of(int D) { return D > 128 ? 32 : D > 64 ? 16 : 8; }
+
+// The heads in equal parts, as many to a block as its lanes hold rows of one token, and the tokens
+// in as many parts as fill the GPU (4 blocks to an SM), or fewer if there are fewer tokens.
+struct Cuts {
+  int heads_per_block, head_parts, tokens_per_block, token_parts;
+};
+
+Cuts cuts_of(int N, int D, int heads) {
+  Cuts c;
+  const int rows = kThreads / lanes_of(D);
+  c.head_parts = (heads + rows - 1) / rows;
+  c.heads_per_block = (heads + c.head_parts - 1) / c.head_parts;
+  c.head_parts = (heads + c.heads_per_block - 1) / c.heads_per_block;
+  const int at_once = rows / c.heads_per_block;  // tokens
+  const long long parts = std::max(1, 4 * kSms / c.head_parts);
+  const long long per = (N + parts - 1) / parts;
+  c.tokens_per_block = static_cast<int>((per + at_once - 1) / at_once * at_once);
+  c.token_parts = static_cast<int>((static_cast<long long>(N) + c.tokens_per_block - 1) / c.tokens_per_block);
+  return c;
+}
 
 bool bad_align(const void* p) { return reinterpret_cast<uintptr_t>(p) & 15u; }
 
@@ -228,8 +420,22 @@ int side_of(int N, int D, const moe_qk_grads* r, Side* s) {
   return MOE_OK;
 }
 
+// Rows of the partial sums: two for each block, or one for each head and part of the tokens.
 size_t backward_ws(int N, int D, int q_heads, int k_heads) {
-  return up256(static_cast<size_t>(splits_of(N)) * (q_heads + k_heads) * D * 4);
+  const Cuts c = cuts_of(N, D, q_heads + k_heads);
+  return up256(static_cast<size_t>(c.token_parts) *
+               std::max(2 * c.head_parts, q_heads + k_heads) * D * 4);
+}
+
+// Calls f(lanes) for the width of the heads.
+template <typename F>
+void with_lanes(int D, F f) {
+  if (lanes_of(D) == 32)
+    f(std::integral_constant<int, 32>{});
+  else if (lanes_of(D) == 16)
+    f(std::integral_constant<int, 16>{});
+  else
+    f(std::integral_constant<int, 8>{});
 }
 
 }  // namespace
@@ -248,16 +454,19 @@ int moe_qk_norm_rope(int32_t N, int32_t D, int32_t rotary_dim, int32_t interleav
   if (int e = side_of(N, D, q, &sq)) return e;
   if (k)
     if (int e = side_of(N, D, k, &sk)) return e;
-  const long long rows = static_cast<long long>(N) * (sq.heads + sk.heads);
-  if ((rows + 7) / 8 > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
-  const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
+  const Cuts c = cuts_of(N, D, sq.heads + sk.heads);
+  const Shape s{N, D, rotary_dim, interleaved != 0, c.heads_per_block, c.tokens_per_block, eps,
+                positions, inv_freq};
+  const dim3 grid(c.token_parts, c.head_parts);
+  const int smem = 2 * kTokens * rotary_dim * 4;
   mark_before(MOE_KERNEL_QK_NORM_ROPE, stream);
-  if (dtype == MOE_BF16)
-    rope_forward_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(
-        N, D, rotary_dim, interleaved, eps, positions, inv_freq, sq, sk);
-  else
-    rope_forward_kernel<float><<<grid, 256, 0, stream>>>(N, D, rotary_dim, interleaved, eps,
-                                                         positions, inv_freq, sq, sk);
+  with_lanes(D, [&](auto lanes) {
+    constexpr int L = decltype(lanes)::value;
+    if (dtype == MOE_BF16)
+      rope_forward_kernel<__nv_bfloat16, L><<<grid, kThreads, smem, stream>>>(s, sq, sk);
+    else
+      rope_forward_kernel<float, L><<<grid, kThreads, smem, stream>>>(s, sq, sk);
+  });
   const cudaError_t err = cudaGetLastError();
   mark_after(MOE_KERNEL_QK_NORM_ROPE, stream);
   count_launches(1);
@@ -290,27 +499,36 @@ int moe_qk_norm_rope_backward(int32_t N, int32_t D, int32_t rotary_dim, int32_t 
     if (bad_align(workspace)) return MOE_ERR_UNSUPPORTED;
     partial = static_cast<float*>(workspace);
   }
-  const dim3 grid(splits_of(N), heads);
-  const int per = per_split_of(N);
+  const Cuts c = cuts_of(N, D, heads);
+  const Shape s{N, D, rotary_dim, interleaved != 0, c.heads_per_block, c.tokens_per_block, eps,
+                positions, inv_freq};
+  const dim3 grid(c.token_parts, c.head_parts);
+  const int smem = 2 * kTokens * rotary_dim * 4;
   mark_before(MOE_KERNEL_QK_NORM_ROPE_BWD, stream);
-  if (dtype == MOE_F32)
-    rope_backward_kernel<float, float><<<grid, 256, 0, stream>>>(
-        N, D, rotary_dim, interleaved, eps, positions, inv_freq, sq, sk, per, partial);
-  else if (dy_dtype == MOE_F32)
-    rope_backward_kernel<__nv_bfloat16, float><<<grid, 256, 0, stream>>>(
-        N, D, rotary_dim, interleaved, eps, positions, inv_freq, sq, sk, per, partial);
-  else
-    rope_backward_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 256, 0, stream>>>(
-        N, D, rotary_dim, interleaved, eps, positions, inv_freq, sq, sk, per, partial);
+  with_lanes(D, [&](auto lanes) {
+    constexpr int L = decltype(lanes)::value;
+    using B = __nv_bfloat16;
+    if (dtype == MOE_F32)
+      rope_backward_kernel<float, float, L><<<grid, kThreads, smem, stream>>>(s, sq, sk, partial);
+    else if (dy_dtype == MOE_F32)
+      rope_backward_kernel<B, float, L><<<grid, kThreads, smem, stream>>>(s, sq, sk, partial);
+    else
+      rope_backward_kernel<B, B, L><<<grid, kThreads, smem, stream>>>(s, sq, sk, partial);
+  });
   int launches = 1;
-  const auto reduce = [&](float* dw, int first, int n, int per_head) {
-    const int values = (per_head ? n : 1) * D;
-    rope_dweight_kernel<<<(values + 127) / 128, 128, 0, stream>>>(partial, grid.x, heads, D, first,
-                                                                  n, per_head, dw);
+  // rows of partial: two for each block, or, if either side has a weight for each head, one for
+  // each head (a shared weight's are then added over its heads)
+  const bool by_head = sq.w_hs || sk.w_hs;
+  const auto reduce = [&](float* dw, int side, int first, int n, bool per_head) {
+    const dim3 blocks((D + 31) / 32, per_head ? n : 1);
+    const float* from = partial + static_cast<size_t>(by_head ? first : side) * D;
+    const int outer = by_head ? c.token_parts : c.token_parts * c.head_parts;
+    rope_dweight_kernel<<<blocks, 1024, 0, stream>>>(from, outer, by_head && !per_head ? n : 1,
+                                                     by_head ? heads : 2, D, dw);
     ++launches;
   };
-  if (q->dweight) reduce(q->dweight, 0, sq.heads, q->weight_per_head != 0);
-  if (k && k->dweight) reduce(k->dweight, sq.heads, sk.heads, k->weight_per_head != 0);
+  if (q->dweight) reduce(q->dweight, 0, 0, sq.heads, q->weight_per_head != 0);
+  if (k && k->dweight) reduce(k->dweight, 1, sq.heads, sk.heads, k->weight_per_head != 0);
   const cudaError_t err = cudaGetLastError();
   mark_after(MOE_KERNEL_QK_NORM_ROPE_BWD, stream);
   count_launches(launches);
