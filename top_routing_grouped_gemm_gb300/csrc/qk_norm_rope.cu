@@ -28,37 +28,57 @@ struct Side {
   int heads;
 };
 
-// Eight consecutive values of a row: what a lane holds.
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// A lane holds two quads of a row (a token's head): with halves paired, values 4 j .. 4 j + 3 of
+// the first half and their partners in the second, so that a rotation stays within the lane; with
+// neighbours paired, and for the values that are not rotated, eight consecutive ones.
+template <typename T>
+struct Raw;  // as loaded
+
+template <>
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p, int far) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p + far));
   }
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+
+template <>
+struct Raw<__nv_bfloat16> {
+  uint2 a, b;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int far) {
+    a = __ldcs(reinterpret_cast<const uint2*>(p));
+    b = __ldcs(reinterpret_cast<const uint2*>(p + far));
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+
+__device__ __forceinline__ void store(float* p, int far, const float (&v)[8]) {
   __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+  __stcs(reinterpret_cast<float4*>(p + far), make_float4(v[4], v[5], v[6], v[7]));
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                 pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+__device__ __forceinline__ void store(__nv_bfloat16* p, int far, const float (&v)[8]) {
+  __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])));
+  __stcs(reinterpret_cast<uint2*>(p + far),
+         make_uint2(pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
 }
 
-// A block takes kHeads (a launch's choice) heads of a range of tokens, in tiles of kTokens.  L
-// lanes hold a row (a token's head), 8 values each, and always the same head, so that its weight
-// stays in registers and its weight gradient gathers there.  The block forms the tile's sines
-// and cosines once, in shared memory, for all its heads.
+// A block takes some heads of a range of tokens, in tiles of kTokens.  L lanes hold a row, and
+// always the same head, so that its weight stays in registers and its weight gradient gathers
+// there.  The block forms the tile's sines and cosines once, in shared memory, for all its heads.
 constexpr int kThreads = 256;
 constexpr int kTokens = 16;
-constexpr int kPairs = kMaxD / 2;
+constexpr int kForwardBlocks = 4, kBackwardBlocks = 2;  // to an SM
 
 struct Shape {
   int N, D, rot, interleaved, heads_per_block, tokens_per_block;
@@ -67,73 +87,86 @@ struct Shape {
   const double* inv_freq;
 };
 
-// The angle of pair i at position pos in turns, modulo 1, as a 64-bit fraction: frequency (turns a
-// token, the same fraction) times pos in whole numbers, which wraps as turns do.  Exact but for the
-// frequency's own rounding (2^-53 of it, times pos), at any position; a product in 64-bit floating
-// point would be as exact, at a thirtieth of the rate on this GPU.
-__device__ __forceinline__ unsigned long long fraction_of(double inv_freq) {
-  double f = inv_freq * 0.15915494309189533577;
-  f -= floor(f);
-  return static_cast<unsigned long long>(f * 18446744073709551616.0);
-}
+// The tile's angles.  A thread keeps one pair: its frequency in turns a token, as a 64-bit fraction
+// of a turn.  Times the position in whole numbers that wraps as turns do, so the angle is exact but
+// for the frequency's own rounding (2^-53 of it, times the position), at any position; a product in
+// 64-bit floating point would be as exact, at a thirtieth of the rate on this GPU.  The upper 32
+// bits go on to the sine and cosine in fp32.  A lane rotates four pairs: place j holds pairs
+// 4 j .. 4 j + 3 as two float4 (cos, sin, cos, sin), the first ones of all places before the
+// second ones, so that the lanes of a row read without conflicts.
+struct Angles {
+  unsigned long long fraction;
+  int pair, token, step, to;  // its pair, first token, tokens between, and place in a token's table
 
-// cos and sin of it from its upper 32 bits (half of 2^-32 of a turn off at most; 2^-25 after the
-// conversion to fp32 for angles of a quarter of a turn and more).
-__device__ __forceinline__ float2 cos_sin(unsigned long long fraction, int pos) {
-  const unsigned long long turns = fraction * static_cast<unsigned long long>(static_cast<long long>(pos));
-  float2 cs;
-  sincospif(static_cast<float>(static_cast<int>(turns >> 32)) * 4.656612873077393e-10f, &cs.y, &cs.x);
-  return cs;
-}
-
-// Tile of cosines and sines.  A lane rotates `per` = 8 pairs (halves: its values are one half of
-// them) or 4 (neighbours); pair i belongs to the lanes' place i / per.  Two pairs make a float4,
-// and the float4s of neighbouring places are neighbours, so that lanes read without conflicts.
-__device__ __forceinline__ void fill_angles(float4* table, const unsigned long long* fractions,
-                                            const Shape& s, long long t0, long long hi) {
-  const int half = s.rot / 2, per = s.interleaved ? 4 : 8, places = half / per;
-  const int n = static_cast<int>(min(static_cast<long long>(kTokens), hi - t0)) * half;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int t = i / half, pair = i % half, in = pair % per;
-    reinterpret_cast<float2*>(table)[2 * (t * (half / 2) + in / 2 * places + pair / per) + in % 2] =
-        cos_sin(fractions[pair], s.pos[t0 + t]);
+  __device__ __forceinline__ explicit Angles(const Shape& s) {
+    const int half = s.rot / 2;
+    step = kThreads / max(half, 1);
+    token = threadIdx.x / max(half, 1);
+    pair = threadIdx.x - token * half;
+    to = (pair % 4 / 2 * (half / 4) + pair / 4) * 2 + pair % 2;
+    if (token >= step || half == 0) token = kTokens;
+    if (token == kTokens) return;
+    double f = s.inv_freq[pair] * 0.15915494309189533577;
+    f -= floor(f);
+    fraction = static_cast<unsigned long long>(f * 18446744073709551616.0);
   }
-}
 
-// y = R(th) n (BACK: R(-th) n) for the 8 values of a lane; `turns` says whether it has a rotated
-// pair, `low` whether its values are the first members of the pairs (halves).
+  __device__ __forceinline__ void fill(float4* table, const Shape& s, long long t0, int n) const {
+    for (int t = token; t < n; t += step) {
+      const long long pos = s.pos[t0 + t];
+      const int turns = static_cast<int>(fraction * static_cast<unsigned long long>(pos) >> 32);
+      float2 cs;
+      sincospif(static_cast<float>(turns) * 4.656612873077393e-10f, &cs.y, &cs.x);  // 2^-31
+      reinterpret_cast<float2*>(table)[t * (s.rot / 2) + to] = cs;
+    }
+  }
+};
+
+// What a lane has to do.
+template <int L>
+struct Lane {
+  int near, far;     // its first quad, and the second from there
+  int place;         // of its pairs in a token's table
+  int head, slot;    // head of all heads; tokens slot, slot + stride, ... of a tile
+  int stride;
+  bool in, turns;    // has values; rotates them
+
+  __device__ __forceinline__ Lane(const Shape& s, int heads) {
+    const int group = threadIdx.x / L;
+    place = threadIdx.x % L;
+    stride = kThreads / L / s.heads_per_block;
+    slot = group / s.heads_per_block;
+    head = blockIdx.y * s.heads_per_block + group % s.heads_per_block;
+    in = place * 8 < s.D;
+    if (slot >= stride || head >= heads) slot = kTokens, head = heads - 1;
+    turns = place * 8 < s.rot;
+    const bool halves = turns && !s.interleaved;
+    near = in ? place * (halves ? 4 : 8) : 0;
+    far = halves ? s.rot / 2 : 4;
+  }
+};
+
+// R(th) v, or R(-th) v (BACK).
 template <bool BACK>
 __device__ __forceinline__ void rotate(float (&v)[8], const float4* table, const Shape& s, int t,
-                                       int sub, int partner, bool turns, bool low) {
-  if (s.rot == 0) return;
-  const int half = s.rot / 2;
-  if (s.interleaved) {
-    if (!turns) return;
-    const float4* cs = table + t * (half / 2) + sub;
+                                       int place) {
+  const float4* cs = table + t * (s.rot / 4) + place;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const float4 w = cs[c * (half / 4)];
-      const float cosv[2] = {w.x, w.z}, sinv[2] = {BACK ? -w.y : w.y, BACK ? -w.w : w.w};
+  for (int c = 0; c < 2; ++c) {
+    const float4 w = cs[c * (s.rot / 8)];
+    const float cosv[2] = {w.x, w.z}, sinv[2] = {BACK ? -w.y : w.y, BACK ? -w.w : w.w};
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float a = v[4 * c + 2 * e], b = v[4 * c + 2 * e + 1];
-        v[4 * c + 2 * e] = a * cosv[e] - b * sinv[e];
-        v[4 * c + 2 * e + 1] = b * cosv[e] + a * sinv[e];
+    for (int e = 0; e < 2; ++e) {
+      const int i = 2 * c + e;
+      if (s.interleaved) {
+        const float x0 = v[2 * i], x1 = v[2 * i + 1];
+        v[2 * i] = x0 * cosv[e] - x1 * sinv[e];
+        v[2 * i + 1] = x1 * cosv[e] + x0 * sinv[e];
+      } else {
+        const float x0 = v[i], x1 = v[i + 4];
+        v[i] = x0 * cosv[e] - x1 * sinv[e];
+        v[i + 4] = x1 * cosv[e] + x0 * sinv[e];
       }
-    }
-    return;
-  }
-  // the first members need -sin times the second ones, the second +sin times the first
-  const float sign = low == BACK ? 1.f : -1.f;
-  const float4* cs = table + t * (half / 2) + (low ? sub : sub - half / 8);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const float p0 = __shfl_sync(~0u, v[2 * c], partner);
-    const float p1 = __shfl_sync(~0u, v[2 * c + 1], partner);
-    if (turns) {
-      const float4 w = cs[c * (half / 8)];
-      v[2 * c] = fmaf(sign * w.y, p0, v[2 * c] * w.x);
-      v[2 * c + 1] = fmaf(sign * w.w, p1, v[2 * c + 1] * w.z);
     }
   }
 }
@@ -145,77 +178,66 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// What a lane has to do.
 template <int L>
-struct Lane {
-  int sub, partner;       // its place in the row, and the lane with the other halves of its pairs
-  int head, slot;         // head of all heads; which tokens of a tile (slot, slot + stride, ...)
-  int stride;
-  bool in, turns, low;    // has values; rotates them; they are first members
+__device__ __forceinline__ void load_weight(const Side& side, int h, const Lane<L>& me, float (&w)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    w[e] = side.weight ? side.weight[static_cast<long long>(h) * side.w_hs + me.near +
+                                     (e < 4 ? e : me.far + e - 4)]
+                       : 1.f;
+}
 
-  __device__ __forceinline__ Lane(const Shape& s, int heads) {
-    const int group = threadIdx.x / L;
-    sub = threadIdx.x % L;
-    slot = group / s.heads_per_block;
-    stride = kThreads / L / s.heads_per_block;
-    head = blockIdx.y * s.heads_per_block + group % s.heads_per_block;
-    in = slot < stride && head < heads && sub * 8 < s.D;
-    if (slot >= stride || head >= heads) slot = kTokens, head = heads - 1;
-    const int half = s.rot / 16;  // lanes of the first members
-    turns = sub * 8 < s.rot;
-    low = sub < half;
-    const int other = !turns ? sub : low ? sub + half : sub - half;
-    partner = (threadIdx.x & 31 & ~(L - 1)) + (s.interleaved ? sub : other);
-  }
-};
+// Lanes past the row's end (a width that is no power of two) add nothing.
+template <int L>
+__device__ __forceinline__ void trim(float (&v)[8], const Shape& s, const Lane<L>& me) {
+  if (s.D != 8 * L && !me.in)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+}
 
 template <typename T, int L>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kForwardBlocks)
     rope_forward_kernel(const Shape s, const Side q, const Side k) {
+  constexpr int U = 4;  // rows that a lane has on their way
   extern __shared__ float4 table[];  // [2][kTokens][rot / 4]
-  __shared__ unsigned long long fractions[kPairs];
-  for (int i = threadIdx.x; i < s.rot / 2; i += kThreads) fractions[i] = fraction_of(s.inv_freq[i]);
+  const Angles angles(s);
   const Lane<L> me(s, q.heads + k.heads);
   const Side& side = me.head < q.heads ? q : k;
   const int h = me.head < q.heads ? me.head : me.head - q.heads;
   float w[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    w[e] = me.in && side.weight ? side.weight[static_cast<long long>(h) * side.w_hs + me.sub * 8 + e] : 1.f;
-  const T* x = static_cast<const T*>(side.x) + h * side.x_hs + me.sub * 8;
-  T* y = static_cast<T*>(side.out) + h * side.o_hs + me.sub * 8;
+  load_weight(side, h, me, w);
+  const T* x = static_cast<const T*>(side.x) + h * side.x_hs + me.near;
+  T* y = static_cast<T*>(side.out) + h * side.o_hs + me.near;
   const long long lo = static_cast<long long>(blockIdx.x) * s.tokens_per_block;
   const long long hi = min(lo + s.tokens_per_block, static_cast<long long>(s.N));
   const float inv_D = 1.f / s.D;
-  __syncthreads();
   int buf = 0;
   for (long long t0 = lo; t0 < hi; t0 += kTokens, buf ^= 1) {
-    float4* angles = table + buf * kTokens * (s.rot / 4);
-    if (s.rot) fill_angles(angles, fractions, s, t0, hi);
-    __syncthreads();  // (the other buffer's readers are done when they come here again)
+    float4* now = table + buf * kTokens * (s.rot / 4);
     const int n = static_cast<int>(min(static_cast<long long>(kTokens), hi - t0));
-    for (int t = 0; t < n; t += 2 * me.stride) {  // the same for all lanes: they shuffle
-      float v[2][8];
-      bool row[2];
+    angles.fill(now, s, t0, n);
+    __syncthreads();  // (the other buffer's readers are done when they come here again)
+    for (int t = 0; t < n; t += U * me.stride) {  // the same for all lanes: they shuffle
+      const int first = t + me.slot;
+      Raw<T> raw[U];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int at = t + me.slot + u * me.stride;
-        row[u] = me.in && at < n;
+      for (int u = 0; u < U; ++u)  // past the last row: that row again
+        raw[u].load(x + (t0 + min(first + u * me.stride, n - 1)) * side.x_ts, me.far);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
-        if (row[u]) load8(x + (t0 + at) * side.x_ts, v[u]);
-      }
+      for (int u = 0; u < U; ++u) {
+        const int at = first + u * me.stride;
+        float v[8], sum = 0.f;
+        raw[u].get(v);
+        trim(v, s, me);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int at = t + me.slot + u * me.stride;
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(v[u][e], v[u][e], sum);
+        for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
         const float rstd = rsqrtf(fmaf(row_sum<L>(sum), inv_D, s.eps));
+        if (at < n && me.in) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[u][e] *= rstd * w[e];
-        rotate<false>(v[u], angles, s, row[u] ? at : 0, me.sub, me.partner, me.turns, me.low);
-        if (row[u]) store8(y + (t0 + at) * side.o_ts, v[u]);
+          for (int e = 0; e < 8; ++e) v[e] *= rstd * w[e];
+          if (me.turns) rotate<false>(v, now, s, at, me.place);
+          store(y + (t0 + at) * side.o_ts, me.far, v);
+        }
       }
     }
   }
@@ -224,75 +246,74 @@ __global__ void __launch_bounds__(kThreads, 4)
 // partial: [blocks][2][D] (the shared weights of q and k) or [gridDim.x][heads][D] (a row for each
 // head), the sums of the block's rows; null: not wanted.
 template <typename T, typename G, int L>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, kBackwardBlocks)
     rope_backward_kernel(const Shape s, const Side q, const Side k, float* partial) {
+  constexpr int U = 4;
   extern __shared__ float4 table[];  // [2][kTokens][rot / 4]
-  __shared__ unsigned long long fractions[kPairs];
   __shared__ float sums[kThreads / L][L * 8];
-  for (int i = threadIdx.x; i < s.rot / 2; i += kThreads) fractions[i] = fraction_of(s.inv_freq[i]);
+  const Angles angles(s);
   const int heads = q.heads + k.heads;
   const Lane<L> me(s, heads);
   const Side& side = me.head < q.heads ? q : k;
   const int h = me.head < q.heads ? me.head : me.head - q.heads;
-  float w[8], dw[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    w[e] = me.in && side.weight ? side.weight[static_cast<long long>(h) * side.w_hs + me.sub * 8 + e] : 1.f;
-    dw[e] = 0.f;
-  }
-  const T* x = static_cast<const T*>(side.x) + h * side.x_hs + me.sub * 8;
-  const G* dy = static_cast<const G*>(side.dy) + h * side.dy_hs + me.sub * 8;
-  T* dx = static_cast<T*>(side.out) + h * side.o_hs + me.sub * 8;
+  float w[8], dw[8] = {};
+  load_weight(side, h, me, w);
+  const T* x = static_cast<const T*>(side.x) + h * side.x_hs + me.near;
+  const G* dy = static_cast<const G*>(side.dy) + h * side.dy_hs + me.near;
+  T* dx = static_cast<T*>(side.out) + h * side.o_hs + me.near;
   const long long lo = static_cast<long long>(blockIdx.x) * s.tokens_per_block;
   const long long hi = min(lo + s.tokens_per_block, static_cast<long long>(s.N));
   const float inv_D = 1.f / s.D;
-  __syncthreads();
   int buf = 0;
   for (long long t0 = lo; t0 < hi; t0 += kTokens, buf ^= 1) {
-    float4* angles = table + buf * kTokens * (s.rot / 4);
-    if (s.rot) fill_angles(angles, fractions, s, t0, hi);
-    __syncthreads();
+    float4* now = table + buf * kTokens * (s.rot / 4);
     const int n = static_cast<int>(min(static_cast<long long>(kTokens), hi - t0));
-    for (int t = 0; t < n; t += 2 * me.stride) {
-      float v[2][8], d[2][8];
-      bool row[2];
+    angles.fill(now, s, t0, n);
+    __syncthreads();
+    for (int t = 0; t < n; t += U * me.stride) {
+      const int first = t + me.slot;
+      Raw<T> raw[U];
+      Raw<G> raw_d[U];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int at = t + me.slot + u * me.stride;
-        row[u] = me.in && at < n;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[u][e] = d[u][e] = 0.f;
-        if (row[u]) {
-          load8(x + (t0 + at) * side.x_ts, v[u]);
-          load8(dy + (t0 + at) * side.dy_ts, d[u]);
-        }
+      for (int u = 0; u < U; ++u) {
+        const long long at = t0 + min(first + u * me.stride, n - 1);
+        raw[u].load(x + at * side.x_ts, me.far);
+        raw_d[u].load(dy + at * side.dy_ts, me.far);
       }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int at = t + me.slot + u * me.stride;
-        rotate<true>(d[u], angles, s, row[u] ? at : 0, me.sub, me.partner, me.turns, me.low);
+      for (int u = 0; u < U; ++u) {
+        const int at = first + u * me.stride;
+        float v[8], d[8];
+        raw[u].get(v);
+        raw_d[u].get(d);
+        trim(v, s, me);
+        if (me.turns) rotate<true>(d, now, s, min(at, n - 1), me.place);
         // both sums of the row at once: u = w dn; mean(u x^) = rstd mean(u x)
         float sum = 0.f, dot = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          sum = fmaf(v[u][e], v[u][e], sum);
-          dot = fmaf(d[u][e] * w[e], v[u][e], dot);
+          sum = fmaf(v[e], v[e], sum);
+          dot = fmaf(d[e] * w[e], v[e], dot);
         }
+        if (s.D != 8 * L && !me.in) dot = 0.f;
         const float rstd = rsqrtf(fmaf(row_sum<L>(sum), inv_D, s.eps));
         const float c = row_sum<L>(dot) * inv_D * rstd * rstd;
+        if (at < n && me.in) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          dw[e] = fmaf(d[u][e], v[u][e] * rstd, dw[e]);
-          d[u][e] = rstd * fmaf(-c, v[u][e], d[u][e] * w[e]);
+          for (int e = 0; e < 8; ++e) {
+            dw[e] = fmaf(d[e], v[e] * rstd, dw[e]);
+            d[e] = rstd * fmaf(-c, v[e], d[e] * w[e]);
+          }
+          store(dx + (t0 + at) * side.o_ts, me.far, d);
         }
-        if (row[u]) store8(dx + (t0 + at) * side.o_ts, d[u]);
       }
     }
   }
   if (!partial) return;
   const int group = threadIdx.x / L;
+  if (me.in)
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sums[group][me.sub * 8 + e] = dw[e];
+    for (int e = 0; e < 8; ++e) sums[group][me.near + (e < 4 ? e : me.far + e - 4)] = dw[e];
   __syncthreads();
   const int groups = kThreads / L / s.heads_per_block * s.heads_per_block;
   const int first = blockIdx.y * s.heads_per_block;
@@ -347,19 +368,19 @@ __global__ void __launch_bounds__(1024)
 int lanes_of(int D) { return D > 128 ? 32 : D > 64 ? 16 : 8; }
 
 // The heads in equal parts, as many to a block as its lanes hold rows of one token, and the tokens
-// in as many parts as fill the GPU (4 blocks to an SM), or fewer if there are fewer tokens.
+// in as many parts as fill the GPU once, or fewer if there are fewer tokens.
 struct Cuts {
   int heads_per_block, head_parts, tokens_per_block, token_parts;
 };
 
-Cuts cuts_of(int N, int D, int heads) {
+Cuts cuts_of(int N, int D, int heads, int blocks_per_sm) {
   Cuts c;
   const int rows = kThreads / lanes_of(D);
   c.head_parts = (heads + rows - 1) / rows;
   c.heads_per_block = (heads + c.head_parts - 1) / c.head_parts;
   c.head_parts = (heads + c.heads_per_block - 1) / c.heads_per_block;
   const int at_once = rows / c.heads_per_block;  // tokens
-  const long long parts = std::max(1, 4 * kSms / c.head_parts);
+  const long long parts = std::max(1, blocks_per_sm * kSms / c.head_parts);
   const long long per = (N + parts - 1) / parts;
   c.tokens_per_block = static_cast<int>((per + at_once - 1) / at_once * at_once);
   c.token_parts = static_cast<int>((static_cast<long long>(N) + c.tokens_per_block - 1) / c.tokens_per_block);
@@ -422,7 +443,7 @@ int side_of(int N, int D, const moe_qk_grads* r, Side* s) {
 
 // Rows of the partial sums: two for each block, or one for each head and part of the tokens.
 size_t backward_ws(int N, int D, int q_heads, int k_heads) {
-  const Cuts c = cuts_of(N, D, q_heads + k_heads);
+  const Cuts c = cuts_of(N, D, q_heads + k_heads, kBackwardBlocks);
   return up256(static_cast<size_t>(c.token_parts) *
                std::max(2 * c.head_parts, q_heads + k_heads) * D * 4);
 }
@@ -454,7 +475,7 @@ int moe_qk_norm_rope(int32_t N, int32_t D, int32_t rotary_dim, int32_t interleav
   if (int e = side_of(N, D, q, &sq)) return e;
   if (k)
     if (int e = side_of(N, D, k, &sk)) return e;
-  const Cuts c = cuts_of(N, D, sq.heads + sk.heads);
+  const Cuts c = cuts_of(N, D, sq.heads + sk.heads, kForwardBlocks);
   const Shape s{N, D, rotary_dim, interleaved != 0, c.heads_per_block, c.tokens_per_block, eps,
                 positions, inv_freq};
   const dim3 grid(c.token_parts, c.head_parts);
@@ -499,7 +520,7 @@ int moe_qk_norm_rope_backward(int32_t N, int32_t D, int32_t rotary_dim, int32_t 
     if (bad_align(workspace)) return MOE_ERR_UNSUPPORTED;
     partial = static_cast<float*>(workspace);
   }
-  const Cuts c = cuts_of(N, D, heads);
+  const Cuts c = cuts_of(N, D, heads, kBackwardBlocks);
   const Shape s{N, D, rotary_dim, interleaved != 0, c.heads_per_block, c.tokens_per_block, eps,
                 positions, inv_freq};
   const dim3 grid(c.token_parts, c.head_parts);
