@@ -5,20 +5,24 @@
 
 namespace moe {
 
-// Row of the pool for request b, or -1 to skip it: a padding row (-1), a row out of range, or
-// one that an earlier request of the batch has already named (two blocks would race on its
-// state); the last two are reported.  Called by whole blocks, every thread with the same b.
+// Whether an earlier request of the batch has already named request b's row: two blocks would race
+// on its state.  That is reported.  Called by whole blocks, every thread with the same b.
+__device__ __forceinline__ bool named_before(int b, int row, const int* slot, int* dev_status) {
+  int bad = 0;
+  for (int i = threadIdx.x; i < b; i += blockDim.x) bad |= slot[i] == row;
+  bad = __syncthreads_or(bad);
+  if (bad && threadIdx.x == 0 && dev_status) atomicCAS(dev_status, 0, MOE_ERR_BAD_INDEX);
+  return bad;
+}
+
+// Row of the pool for request b, or -1 to skip it: a padding row (-1), or one that is out of range
+// or was named before, which is reported.  Called by whole blocks, every thread with the same b.
 __device__ __forceinline__ int claimed_slot(int b, const int* slot, int n_slots,
                                             int* dev_status) {
   if (!slot) return b;
   const int row = slot[b];
-  if (row == -1) return -1;
-  int bad = row < 0 || row >= n_slots;
-  if (!bad)
-    for (int i = threadIdx.x; i < b; i += blockDim.x) bad |= slot[i] == row;
-  bad = __syncthreads_or(bad);
-  if (!bad) return row;
-  if (threadIdx.x == 0 && dev_status) atomicCAS(dev_status, 0, MOE_ERR_BAD_INDEX);
+  if (row >= 0 && row < n_slots) return named_before(b, row, slot, dev_status) ? -1 : row;
+  if (row != -1 && threadIdx.x == 0 && dev_status) atomicCAS(dev_status, 0, MOE_ERR_BAD_INDEX);
   return -1;
 }
 
