@@ -863,13 +863,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       tile.next();
     };
 
-    // always one step's pairs ahead of the states
-    Masks even, odd;
-    for (int it = -1; it < steps; it += 2) {
-      if (it + 1 < steps) form(it + 1, 0, even);
-      if (it >= 0) finish(it, 1, odd);
-      if (it + 2 < steps) form(it + 2, 1, odd);
-      if (it + 1 < steps) finish(it + 1, 0, even);
+    // always one step's pairs ahead of the states (one copy of the code: with two, it no longer
+    // fits the instruction cache)
+    Masks now{}, next{};
+    for (int it = -1; it < steps; ++it) {
+      if (it + 1 < steps) form(it + 1, (it + 1) & 1, next);
+      if (it >= 0) finish(it, it & 1, now);
+      now = next;
     }
   }
   __syncwarp();
