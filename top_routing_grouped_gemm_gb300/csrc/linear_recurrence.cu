@@ -2,6 +2,7 @@
 // (include/linear_recurrence.h has the formulas).
 #include <algorithm>
 #include <initializer_list>
+#include <mutex>
 #include <type_traits>
 
 #include "moe_internal.h"
@@ -19,7 +20,7 @@ constexpr int kThreads = 32 * (kWarps + 2);
 constexpr int kRows = 8;        // rows of a warp in a tile
 constexpr int kTile = kWarps * kRows;
 constexpr int kStages = 3;      // tiles in shared memory
-constexpr int kMaxCluster = 8;  // blocks of a cluster (the portable limit)
+constexpr int kMaxCluster = 16;  // blocks of a cluster
 constexpr int kBounds = 512;    // bounds of sequences that a block keeps in shared memory
 
 __device__ __forceinline__ float ld(const float* p, long long i) { return p[i]; }
@@ -304,11 +305,10 @@ __device__ __forceinline__ void append(Pair<CH>& s, const Pair<CH>& p) {
 // joining warps gave it for step n, and they go to step n + 2 when every warp has formed its pair.
 // Between blocks it uses the buffers n % 4: a block sends its pair of step n + 4 when its warps
 // have used step n + 2, for which it had every block's pair; each block sent that when its warps
-// had used step n.
+// had used step n.  (Those are in dynamic shared memory, behind the tiles: [4][cluster][32].)
 template <int CH, int PAIRS>
 struct Exchange {
   Pair<CH> warps[2][PAIRS][kWarps][32];
-  Pair<CH> blocks[4][kMaxCluster][32];
   Vec<CH> state[2][32];  // in front of the block's tile
   Marks marks[2][kWarps];
   uint64_t formed[2], joined[2], received[4];
@@ -365,8 +365,8 @@ __device__ __forceinline__ void exchange_init(Exchange<CH, PAIRS>& x) {
 // whole tile's is sent to every block of the cluster, this one too, where its bytes count towards
 // the barrier of the step.
 template <bool DOWN, int CH, int PAIRS>
-__device__ __forceinline__ void join_warps(Exchange<CH, PAIRS>& x, int it, int rank, int cluster,
-                                           int lane) {
+__device__ __forceinline__ void join_warps(Exchange<CH, PAIRS>& x, Pair<CH>* blocks, int it,
+                                           int rank, int cluster, int lane) {
   Pair<CH> pairs[kWarps];
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) pairs[w] = x.warps[it & 1][0][DOWN ? kWarps - 1 - w : w][lane];
@@ -379,7 +379,7 @@ __device__ __forceinline__ void join_warps(Exchange<CH, PAIRS>& x, int it, int r
     else
       append(sum, pairs[w]);
   }
-  Pair<CH>* slot = &x.blocks[it & 3][rank][lane];
+  Pair<CH>* slot = &blocks[((it & 3) * cluster + rank) * 32 + lane];
   uint64_t* received = &x.received[it & 3];
   if (cluster == 1) {
     *slot = sum;
@@ -408,14 +408,16 @@ __device__ __forceinline__ void join_warps(Exchange<CH, PAIRS>& x, int it, int r
 // The second one's: the state in front of this block's tile, from `state` in front of the step's
 // first tile, which moves on over the whole step.
 template <int CH, int PAIRS>
-__device__ __forceinline__ void join_blocks(Exchange<CH, PAIRS>& x, int it, int rank, int cluster,
-                                            int lane, Vec<CH>& state, int* dev_status) {
+__device__ __forceinline__ void join_blocks(Exchange<CH, PAIRS>& x, const Pair<CH>* blocks, int it,
+                                            int rank, int cluster, int lane, Vec<CH>& state,
+                                            int* dev_status) {
   wait_for(&x.received[it & 3], it >> 2 & 1, &x.abort, dev_status);
   Vec<CH> mine = state;
-#pragma unroll
-  for (int q = 0; q < kMaxCluster; ++q) {
+  const Pair<CH>* pairs = &blocks[(it & 3) * cluster * 32 + lane];
+#pragma unroll 4
+  for (int q = 0; q < cluster; ++q) {
     if (q == rank) mine = state;
-    if (q < cluster) follow(state, x.blocks[it & 3][q][lane]);
+    follow(state, pairs[q * 32]);
   }
   x.state[it & 1][lane] = mine;
   arrive_warp(&x.joined[it & 1], lane);
@@ -510,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   static_assert(kTile == kChunk, "a tile begins at a kept state");
   extern __shared__ uint32_t dynamic[];
   uint32_t* ring = aligned_128(dynamic);
+  Pair<CH>* blocks = reinterpret_cast<Pair<CH>*>(ring + kStages * 2 * kTile * 32);
   __shared__ Exchange<CH, 1> xch;
   __shared__ int bounds[kBounds];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -535,14 +538,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int it = 0; it < kStages; ++it) load(it);
     for (int it = 0; it < steps; ++it) {
       wait_for(&xch.formed[it & 1], it >> 1 & 1, &xch.abort, p.dev_status);
-      join_warps<false>(xch, it, rank, p.cluster, lane);
+      join_warps<false>(xch, blocks, it, rank, p.cluster, lane);
       load(it + kStages);  // over the tile that every warp has read
     }
     if (ASYNC && lane == 0) drain(xch.loaded, steps);
   } else if (warp > kWarps) {  // joins the blocks
     Vec<CH> state = all<CH>(0.f);
     for (int it = 0; it < steps; ++it)
-      join_blocks(xch, it, rank, p.cluster, lane, state, p.dev_status);
+      join_blocks(xch, blocks, it, rank, p.cluster, lane, state, p.dev_status);
   } else {
     if (seq.off && p.h_T && on) hand_on_empty<CH>(seq, p.h0, p.h_T, D, d, warp);
     struct Span {
@@ -663,6 +666,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   static_assert(kTile == kChunk, "a tile begins at a kept state");
   extern __shared__ uint32_t dynamic[];
   uint32_t* ring = aligned_128(dynamic);
+  Pair<CH>* blocks = reinterpret_cast<Pair<CH>*>(ring + kStages * 3 * kTile * 32);
   // the gradient's pairs, the state's
   __shared__ Exchange<CH, 2> xch;
   __shared__ int bounds[kBounds];
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int it = 0; it < kStages; ++it) load(it);
     for (int it = 0; it < steps; ++it) {
       wait_for(&xch.formed[it & 1], it >> 1 & 1, &xch.abort, p.dev_status);
-      join_warps<true>(xch, it, rank, p.cluster, lane);
+      join_warps<true>(xch, blocks, it, rank, p.cluster, lane);
       if (ASYNC && it > 0) {  // the step before has been read for the second time
         wait_for(&xch.freed[(it - 1) % kStages], (it - 1) / kStages & 1, &xch.abort, p.dev_status);
         load(it - 1 + kStages);
@@ -712,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         follow(kept, pair);
       }
       kept = kept_state(it + 1);
-      join_blocks(xch, it, rank, p.cluster, lane, state, p.dev_status);
+      join_blocks(xch, blocks, it, rank, p.cluster, lane, state, p.dev_status);
     }
   } else {
     if (seq.off && p.dh0 && on) hand_on_empty<CH>(seq, p.dh_T, p.dh0, D, d, warp);
@@ -912,40 +916,81 @@ int check_rows(int N, int D, int n_seq, const int* seq_off, int mode, int dtype,
   return MOE_OK;
 }
 
-// Blocks of a scan: strips of `width` channels, each a row of clusters over time.
-struct Grid {
-  int strips, cluster, parts;
-};
-
-Grid grid_of(int N, int D, int n_seq, int width) {
-  Grid g;
-  g.strips = (D + width - 1) / width;
-  const int want = 2 * num_sms();  // two blocks of 8 warps on every SM
-  const int tiles = (N + kTile - 1) / kTile;
-  g.cluster = std::max(1, std::min({kMaxCluster, tiles, want / g.strips}));
-  g.parts = std::max(1, std::min({n_seq, tiles, want / (g.strips * g.cluster)}));
-  return g;
+// Dynamic shared memory of a scan of `arrays` inputs with clusters of the given size.
+template <int CH>
+int dynamic_bytes(int arrays, int cluster) {
+  return kAlign + kStages * arrays * kTile * 128 + 4 * cluster * 32 * static_cast<int>(sizeof(Pair<CH>));
 }
 
-// Launches KERNEL with `ring` bytes of shared memory beside its own.
-template <typename Args>
-int launch(void (*kernel)(Args), const Grid& g, int ring, const Args& args,
-           cudaStream_t stream) {
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring) !=
-      cudaSuccess)
-    return MOE_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(g.cluster * g.parts, g.strips);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = ring;
-  cfg.stream = stream;
+cudaLaunchAttribute cluster_of(int c) {
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = g.cluster;
+  attr.val.clusterDim.x = c;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  return attr;
+}
+
+// A cluster beyond what the GPU has room for beside the others would wait for a second round (40
+// strips of clusters of 7, where 38 fit, took half as long again as clusters of 6), so the driver
+// is asked how many clusters of each size run at once, for each kernel and device the first time.
+struct Room {
+  int clusters[kMaxCluster + 1] = {};
+  cudaError_t err = cudaErrorUnknown;
+};
+
+template <auto KERNEL, int CH, int ARRAYS>
+const Room* room_for() {
+  static Room rooms[64];
+  static std::once_flag once[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  std::call_once(once[dev], [&] {
+    Room& r = rooms[dev];
+    r.err = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 dynamic_bytes<CH>(ARRAYS, kMaxCluster));
+    if (r.err == cudaSuccess)
+      r.err = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    for (int c = 1; c <= kMaxCluster && r.err == cudaSuccess; ++c) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(c);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = dynamic_bytes<CH>(ARRAYS, c);
+      cudaLaunchAttribute attr = cluster_of(c);
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      r.err = cudaOccupancyMaxActiveClusters(&r.clusters[c], KERNEL, &cfg);
+    }
+  });
+  return rooms[dev].err == cudaSuccess ? &rooms[dev] : nullptr;
+}
+
+// Launches KERNEL in as large clusters as can all run at once, up to 8 blocks; where these leave
+// room, sequences are parted.  Larger clusters (whose exchanges take longer) only where they put
+// more blocks to work: few channels in few sequences (65536 x 64, one sequence: 107 us in clusters
+// of 8, 63 us of 16; 65536 x 512, 24 sequences: 51 us of 8 and 89 us of 16).
+template <auto KERNEL, int CH, int ARRAYS, typename Args>
+int launch(int N, int D, int n_seq, Args& args, cudaStream_t stream) {
+  const Room* room = room_for<KERNEL, CH, ARRAYS>();
+  if (!room) return MOE_ERR_CUDA;
+  const int strips = (D + 32 * CH - 1) / (32 * CH), tiles = (N + kTile - 1) / kTile;
+  const auto parts = [&](int c) {
+    return std::max(1, std::min({n_seq, tiles, room->clusters[c] / strips}));
+  };
+  int cluster = 1;
+  for (int c = 2; c <= std::min(kMaxCluster, tiles); ++c)
+    if (room->clusters[c] >= strips && (c <= 8 || c * parts(c) > cluster * parts(cluster)))
+      cluster = c;
+  args.cluster = cluster;
+  args.parts = parts(cluster);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster * args.parts, strips);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = dynamic_bytes<CH>(ARRAYS, cluster);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = cluster_of(cluster);
   cfg.attrs = &attr;
-  cfg.numAttrs = g.cluster > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, KERNEL, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 // Calls f(T{}, channels per lane, mode, ASYNC) for the call's type.  Tensors whose rows all begin
@@ -1003,16 +1048,14 @@ int moe_glr_forward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off,
         using T = decltype(type);
         constexpr int CH = decltype(ch)::value;
         constexpr bool ASYNC = decltype(async)::value, F32 = sizeof(T) == 4;
-        const Grid gr = grid_of(N, D, n_seq, 32 * CH);
-        ForwardArgs<T> a{{}, seq, D, gr.parts, gr.cluster, static_cast<const T*>(g),
-                         static_cast<const T*>(x), ld_g, ld_x, h0, static_cast<T*>(h), h_T,
+        ForwardArgs<T> a{{}, seq, D, 1, 1, static_cast<const T*>(g), static_cast<const T*>(x), ld_g, ld_x, h0, static_cast<T*>(h), h_T,
                          h_chunks, dev_status};
         if (ASYNC) {
           if (int err = encode_map_rows(&a.maps[0], g, F32, D, N, ld_g, 32 * CH, kTile)) return err;
           if (int err = encode_map_rows(&a.maps[1], x, F32, D, N, ld_x, 32 * CH, kTile)) return err;
         }
-        return launch(glr_forward_kernel<T, CH, decltype(mix)::value, ASYNC>, gr,
-                      kStages * 2 * kTile * 128 + kAlign, a, stream);
+        return launch<glr_forward_kernel<T, CH, decltype(mix)::value, ASYNC>, CH, 2>(N, D, n_seq, a,
+                                                                                      stream);
       });
   mark_after(MOE_KERNEL_GLR_FWD, stream);
   count_launches(1);
@@ -1035,8 +1078,7 @@ int moe_glr_backward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off
         using T = decltype(type);
         constexpr int CH = decltype(ch)::value;
         constexpr bool ASYNC = decltype(async)::value, F32 = sizeof(T) == 4;
-        const Grid gr = grid_of(N, D, n_seq, 32 * CH);
-        BackwardArgs<T> a{{}, seq, D, gr.parts, gr.cluster, static_cast<const T*>(g),
+        BackwardArgs<T> a{{}, seq, D, 1, 1, static_cast<const T*>(g),
                           static_cast<const T*>(x), static_cast<const T*>(dh), ld_g, ld_x, h0,
                           h_chunks, dh_T, static_cast<T*>(dg), static_cast<T*>(dx), dh0,
                           dev_status};
@@ -1047,8 +1089,8 @@ int moe_glr_backward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off
             if (int err = encode_map_rows(&a.maps[i], in[i], F32, D, N, ld[i], 32 * CH, kTile))
               return err;
         }
-        return launch(glr_backward_kernel<T, CH, decltype(mix)::value, ASYNC>, gr,
-                      kStages * 3 * kTile * 128 + kAlign, a, stream);
+        return launch<glr_backward_kernel<T, CH, decltype(mix)::value, ASYNC>, CH, 3>(N, D, n_seq, a,
+                                                                                       stream);
       });
   mark_after(MOE_KERNEL_GLR_BWD, stream);
   count_launches(1);
