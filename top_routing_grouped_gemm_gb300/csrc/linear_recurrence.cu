@@ -23,15 +23,6 @@ constexpr int kStages = 3;      // tiles in shared memory
 constexpr int kMaxCluster = 16;  // blocks of a cluster
 constexpr int kBounds = 512;    // bounds of sequences that a block keeps in shared memory
 
-__device__ __forceinline__ float ld(const float* p, long long i) { return p[i]; }
-__device__ __forceinline__ float ld(const __nv_bfloat16* p, long long i) {
-  return __bfloat162float(p[i]);
-}
-__device__ __forceinline__ void st(float* p, long long i, float v) { p[i] = v; }
-__device__ __forceinline__ void st(__nv_bfloat16* p, long long i, float v) {
-  p[i] = __float2bfloat16_rn(v);
-}
-
 // ------------------------------------------------------------------ what a lane works on
 //
 // CH channels of one row: two bf16 (one 4-byte word), one bf16 (rows that are not 16-byte
@@ -881,18 +872,63 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (p.cluster > 1) cluster_sync();  // no block leaves while another may still write to it
 }
 
-template <typename T, bool MIX>
-__global__ void __launch_bounds__(128)
+// ------------------------------------------------------------------ one token
+
+// Four channels of a row, or one.
+__device__ __forceinline__ void get(const float* p, float (&v)[4]) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+}
+__device__ __forceinline__ void get(const __nv_bfloat16* p, float (&v)[4]) {
+  const uint2 a = *reinterpret_cast<const uint2*>(p);
+  v[0] = __uint_as_float(a.x << 16), v[1] = __uint_as_float(a.x & 0xffff0000u);
+  v[2] = __uint_as_float(a.y << 16), v[3] = __uint_as_float(a.y & 0xffff0000u);
+}
+__device__ __forceinline__ void get(const float* p, float (&v)[1]) { v[0] = *p; }
+__device__ __forceinline__ void get(const __nv_bfloat16* p, float (&v)[1]) {
+  v[0] = __bfloat162float(*p);
+}
+__device__ __forceinline__ void set(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void set(__nv_bfloat16* p, const float (&v)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+__device__ __forceinline__ void set(float* p, const float (&v)[1]) { *p = v[0]; }
+__device__ __forceinline__ void set(__nv_bfloat16* p, const float (&v)[1]) {
+  *p = __float2bfloat16_rn(v[0]);
+}
+
+// V channels to a thread.  Gates and inputs are on their way while the request's row is looked up,
+// and the state while the requests before it are searched for the same row.
+constexpr int kStepThreads = 128;
+
+template <typename T, bool MIX, int V>
+__global__ void __launch_bounds__(kStepThreads)
     glr_step_kernel(int D, const T* g, long long ld_g, const T* x, long long ld_x,
                     const int* slot, int n_slots, float* state, T* h, int* dev_status) {
-  const int b = blockIdx.y, d = blockIdx.x * 128 + threadIdx.x;
-  const int row = claimed_slot(b, slot, n_slots, dev_status);
-  if (row < 0 || d >= D) return;
-  float* s = state + static_cast<long long>(row) * D + d;
-  const float lg = ld(g, b * ld_g + d), xv = ld(x, b * ld_x + d);
-  const float now = fmaf(expf(lg), *s, MIX ? -expm1f(lg) * xv : xv);
-  *s = now;
-  st(h, static_cast<long long>(b) * D + d, now);
+  const int b = blockIdx.y, d = (blockIdx.x * kStepThreads + threadIdx.x) * V;
+  const bool on = d < D;
+  const int row = slot ? slot[b] : b;
+  float lg[V], xv[V], s[V];
+  if (on) {
+    get(g + b * ld_g + d, lg);
+    get(x + b * ld_x + d, xv);
+  }
+  if (row < 0 || row >= n_slots) {
+    if (row != -1 && threadIdx.x == 0 && dev_status) atomicCAS(dev_status, 0, MOE_ERR_BAD_INDEX);
+    return;
+  }
+  float* at = state + static_cast<long long>(row) * D + d;
+  if (on) get(at, s);
+  if ((slot && named_before(b, row, slot, dev_status)) || !on) return;
+#pragma unroll
+  for (int c = 0; c < V; ++c) {
+    const float a = expf(lg[c]);
+    s[c] = fmaf(a, s[c], MIX ? one_minus(lg[c], a) * xv[c] : xv[c]);
+  }
+  set(at, s);
+  set(h + static_cast<long long>(b) * D + d, s);
 }
 
 // ------------------------------------------------------------------------ host side
@@ -1019,19 +1055,6 @@ int dispatch(int mode, int dtype, std::initializer_list<const void*> ptrs,
 }  // namespace
 }  // namespace moe
 
-#define GLR_LAUNCH(KERNEL, GRID, BLOCK, ...)                                        \
-  do {                                                                              \
-    if (dtype == MOE_BF16) {                                                        \
-      using T = __nv_bfloat16;                                                      \
-      if (mode == MOE_GLR_MIX) KERNEL<T, true><<<GRID, BLOCK, 0, stream>>>(__VA_ARGS__); \
-      else KERNEL<T, false><<<GRID, BLOCK, 0, stream>>>(__VA_ARGS__);               \
-    } else {                                                                        \
-      using T = float;                                                              \
-      if (mode == MOE_GLR_MIX) KERNEL<T, true><<<GRID, BLOCK, 0, stream>>>(__VA_ARGS__); \
-      else KERNEL<T, false><<<GRID, BLOCK, 0, stream>>>(__VA_ARGS__);               \
-    }                                                                               \
-  } while (0)
-
 extern "C" {
 
 using namespace moe;
@@ -1103,11 +1126,36 @@ int moe_glr_step(int32_t B, int32_t D, int32_t mode, int32_t dtype, const void* 
   if (int e = check_rows(B, D, 1, nullptr, mode, dtype, g, ld_g, x, ld_x, h, false)) return e;
   if (!state || n_slots <= 0 || (!slot && B > n_slots)) return MOE_ERR_INVALID_ARG;
   if (B > 65535) return MOE_ERR_UNSUPPORTED;
-  const dim3 grid((D + 127) / 128, B);
+  // four channels to a thread where every row begins on the boundary of four values (64 requests x
+  // 4096 channels, bf16: 4.5 us with one, 3.8 us with four; 512 requests: 12.8 and 6.8)
+  const int size = dtype == MOE_BF16 ? 2 : 4;
+  const bool four = D % 4 == 0 && ld_g % 4 == 0 && ld_x % 4 == 0 && !misaligned(g, 4 * size) &&
+                    !misaligned(x, 4 * size) && !misaligned(h, 4 * size) && !misaligned(state, 16);
+  const int width = kStepThreads * (four ? 4 : 1);
+  const dim3 grid((D + width - 1) / width, B);
   mark_before(MOE_KERNEL_GLR_STEP, stream);
-  GLR_LAUNCH(glr_step_kernel, grid, 128, D, static_cast<const T*>(g), ld_g,
-             static_cast<const T*>(x), ld_x, slot, n_slots, state, static_cast<T*>(h),
-             dev_status);
+  const auto run = [&](auto type, auto mix, auto v) {
+    using T = decltype(type);
+    glr_step_kernel<T, decltype(mix)::value, decltype(v)::value><<<grid, kStepThreads, 0, stream>>>(
+        D, static_cast<const T*>(g), ld_g, static_cast<const T*>(x), ld_x, slot, n_slots, state,
+        static_cast<T*>(h), dev_status);
+  };
+  const auto with_width = [&](auto type, auto mix) {
+    if (four)
+      run(type, mix, std::integral_constant<int, 4>{});
+    else
+      run(type, mix, std::integral_constant<int, 1>{});
+  };
+  const auto with_mode = [&](auto type) {
+    if (mode == MOE_GLR_MIX)
+      with_width(type, std::true_type{});
+    else
+      with_width(type, std::false_type{});
+  };
+  if (dtype == MOE_BF16)
+    with_mode(__nv_bfloat16{});
+  else
+    with_mode(float{});
   const cudaError_t err = cudaGetLastError();
   mark_after(MOE_KERNEL_GLR_STEP, stream);
   count_launches(1);

@@ -73,15 +73,16 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, int far, const float (&v
          make_uint2(pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
 }
 
-// A block takes some heads of a range of tokens, in tiles of kTokens.  L lanes hold a row, and
+// A block takes some heads of a range of tokens, in tiles.  L lanes hold a row, and
 // always the same head, so that its weight stays in registers and its weight gradient gathers
 // there.  The block forms the tile's sines and cosines once, in shared memory, for all its heads.
 constexpr int kThreads = 256;
-constexpr int kTokens = 16;
+constexpr int kRows = 4;  // rows that a lane has on their way
+constexpr int kIdle = 1 << 20;  // a token that no tile has
 constexpr int kForwardBlocks = 4, kBackwardBlocks = 2;  // to an SM
 
 struct Shape {
-  int N, D, rot, interleaved, heads_per_block, tokens_per_block;
+  int N, D, rot, interleaved, heads_per_block, tokens_per_block, tile;
   float eps;
   const int* pos;
   const double* inv_freq;
@@ -104,8 +105,10 @@ struct Angles {
     token = threadIdx.x / max(half, 1);
     pair = threadIdx.x - token * half;
     to = (pair % 4 / 2 * (half / 4) + pair / 4) * 2 + pair % 2;
-    if (token >= step || half == 0) token = kTokens;
-    if (token == kTokens) return;
+    if (token >= step || half == 0) {
+      token = kIdle;
+      return;
+    }
     double f = s.inv_freq[pair] * 0.15915494309189533577;
     f -= floor(f);
     fraction = static_cast<unsigned long long>(f * 18446744073709551616.0);
@@ -138,7 +141,7 @@ struct Lane {
     slot = group / s.heads_per_block;
     head = blockIdx.y * s.heads_per_block + group % s.heads_per_block;
     in = place * 8 < s.D;
-    if (slot >= stride || head >= heads) slot = kTokens, head = heads - 1;
+    if (slot >= stride || head >= heads) slot = kIdle, head = heads - 1;
     turns = place * 8 < s.rot;
     const bool halves = turns && !s.interleaved;
     near = in ? place * (halves ? 4 : 8) : 0;
@@ -198,8 +201,7 @@ __device__ __forceinline__ void trim(float (&v)[8], const Shape& s, const Lane<L
 template <typename T, int L>
 __global__ void __launch_bounds__(kThreads, kForwardBlocks)
     rope_forward_kernel(const Shape s, const Side q, const Side k) {
-  constexpr int U = 4;  // rows that a lane has on their way
-  extern __shared__ float4 table[];  // [2][kTokens][rot / 4]
+  extern __shared__ float4 table[];  // [2][tile][rot / 4]
   const Angles angles(s);
   const Lane<L> me(s, q.heads + k.heads);
   const Side& side = me.head < q.heads ? q : k;
@@ -212,19 +214,19 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
   const long long hi = min(lo + s.tokens_per_block, static_cast<long long>(s.N));
   const float inv_D = 1.f / s.D;
   int buf = 0;
-  for (long long t0 = lo; t0 < hi; t0 += kTokens, buf ^= 1) {
-    float4* now = table + buf * kTokens * (s.rot / 4);
-    const int n = static_cast<int>(min(static_cast<long long>(kTokens), hi - t0));
+  for (long long t0 = lo; t0 < hi; t0 += s.tile, buf ^= 1) {
+    float4* now = table + buf * s.tile * (s.rot / 4);
+    const int n = static_cast<int>(min(static_cast<long long>(s.tile), hi - t0));
     angles.fill(now, s, t0, n);
     __syncthreads();  // (the other buffer's readers are done when they come here again)
-    for (int t = 0; t < n; t += U * me.stride) {  // the same for all lanes: they shuffle
+    for (int t = 0; t < n; t += kRows * me.stride) {  // the same for all lanes: they shuffle
       const int first = t + me.slot;
-      Raw<T> raw[U];
+      Raw<T> raw[kRows];
 #pragma unroll
-      for (int u = 0; u < U; ++u)  // past the last row: that row again
+      for (int u = 0; u < kRows; ++u)  // past the last row: that row again
         raw[u].load(x + (t0 + min(first + u * me.stride, n - 1)) * side.x_ts, me.far);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
+      for (int u = 0; u < kRows; ++u) {
         const int at = first + u * me.stride;
         float v[8], sum = 0.f;
         raw[u].get(v);
@@ -248,8 +250,7 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
 template <typename T, typename G, int L>
 __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
     rope_backward_kernel(const Shape s, const Side q, const Side k, float* partial) {
-  constexpr int U = 4;
-  extern __shared__ float4 table[];  // [2][kTokens][rot / 4]
+  extern __shared__ float4 table[];  // [2][tile][rot / 4]
   __shared__ float sums[kThreads / L][L * 8];
   const Angles angles(s);
   const int heads = q.heads + k.heads;
@@ -265,23 +266,23 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
   const long long hi = min(lo + s.tokens_per_block, static_cast<long long>(s.N));
   const float inv_D = 1.f / s.D;
   int buf = 0;
-  for (long long t0 = lo; t0 < hi; t0 += kTokens, buf ^= 1) {
-    float4* now = table + buf * kTokens * (s.rot / 4);
-    const int n = static_cast<int>(min(static_cast<long long>(kTokens), hi - t0));
+  for (long long t0 = lo; t0 < hi; t0 += s.tile, buf ^= 1) {
+    float4* now = table + buf * s.tile * (s.rot / 4);
+    const int n = static_cast<int>(min(static_cast<long long>(s.tile), hi - t0));
     angles.fill(now, s, t0, n);
     __syncthreads();
-    for (int t = 0; t < n; t += U * me.stride) {
+    for (int t = 0; t < n; t += kRows * me.stride) {
       const int first = t + me.slot;
-      Raw<T> raw[U];
-      Raw<G> raw_d[U];
+      Raw<T> raw[kRows];
+      Raw<G> raw_d[kRows];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
+      for (int u = 0; u < kRows; ++u) {
         const long long at = t0 + min(first + u * me.stride, n - 1);
         raw[u].load(x + at * side.x_ts, me.far);
         raw_d[u].load(dy + at * side.dy_ts, me.far);
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
+      for (int u = 0; u < kRows; ++u) {
         const int at = first + u * me.stride;
         float v[8], d[8];
         raw[u].get(v);
@@ -367,22 +368,47 @@ __global__ void __launch_bounds__(1024)
 // values leave some idle.
 int lanes_of(int D) { return D > 128 ? 32 : D > 64 ? 16 : 8; }
 
-// The heads in equal parts, as many to a block as its lanes hold rows of one token, and the tokens
-// in as many parts as fill the GPU once, or fewer if there are fewer tokens.
+// Heads of a block: what leaves fewest lanes idle (of a block's lanes, and of the last part's
+// heads), against the angles that each part of the heads forms anew.  In instructions a row, about
+// 90 for each lane and 50 for each pair's angle.  (16 + 4 heads of 80, 16 rows to a block: two parts
+// of 10 heads leave 3 / 8 of the lanes idle, four of 5 leave 1 / 16; the backward of 31250 tokens
+// in bf16 takes 144 and 123 us.)
+int heads_of_block(int D, int heads) {
+  const int lanes = lanes_of(D), rows = kThreads / lanes;
+  int best = 1;
+  double least = 1e30;
+  for (int h = 1; h <= std::min(heads, rows); ++h) {
+    const int parts = (heads + h - 1) / h;
+    const double busy = static_cast<double>(rows / h * h) / rows * heads / (parts * h);
+    const double cost = lanes * 90.0 / busy + D / 2 * 50.0 / h;
+    if (cost <= least) least = cost, best = h;
+  }
+  return best;
+}
+
+// The heads in parts, and the tokens in as many parts as fill the GPU once, or fewer if there are
+// fewer tokens.
+// A tile is what a block's lanes take in a few rounds of kRows rows each, or less where its angles
+// would not fit 32 KB twice.
 struct Cuts {
-  int heads_per_block, head_parts, tokens_per_block, token_parts;
+  int heads_per_block, head_parts, tokens_per_block, token_parts, at_once;
+
+  int tile(int rot) const {
+    const int round = kRows * at_once, fit = rot ? 4096 / rot : round;
+    if (round <= fit) return round * std::max(1, std::min(16, fit) / round);
+    return std::max(at_once, fit / at_once * at_once);
+  }
 };
 
 Cuts cuts_of(int N, int D, int heads, int blocks_per_sm) {
   Cuts c;
   const int rows = kThreads / lanes_of(D);
-  c.head_parts = (heads + rows - 1) / rows;
-  c.heads_per_block = (heads + c.head_parts - 1) / c.head_parts;
+  c.heads_per_block = heads_of_block(D, heads);
   c.head_parts = (heads + c.heads_per_block - 1) / c.heads_per_block;
-  const int at_once = rows / c.heads_per_block;  // tokens
+  c.at_once = rows / c.heads_per_block;  // tokens
   const long long parts = std::max(1, blocks_per_sm * kSms / c.head_parts);
   const long long per = (N + parts - 1) / parts;
-  c.tokens_per_block = static_cast<int>((per + at_once - 1) / at_once * at_once);
+  c.tokens_per_block = static_cast<int>((per + c.at_once - 1) / c.at_once * c.at_once);
   c.token_parts = static_cast<int>((static_cast<long long>(N) + c.tokens_per_block - 1) / c.tokens_per_block);
   return c;
 }
@@ -476,10 +502,10 @@ int moe_qk_norm_rope(int32_t N, int32_t D, int32_t rotary_dim, int32_t interleav
   if (k)
     if (int e = side_of(N, D, k, &sk)) return e;
   const Cuts c = cuts_of(N, D, sq.heads + sk.heads, kForwardBlocks);
-  const Shape s{N, D, rotary_dim, interleaved != 0, c.heads_per_block, c.tokens_per_block, eps,
-                positions, inv_freq};
+  const Shape s{N, D, rotary_dim, interleaved != 0, c.heads_per_block, c.tokens_per_block,
+                c.tile(rotary_dim), eps, positions, inv_freq};
   const dim3 grid(c.token_parts, c.head_parts);
-  const int smem = 2 * kTokens * rotary_dim * 4;
+  const int smem = 2 * s.tile * rotary_dim * 4;
   mark_before(MOE_KERNEL_QK_NORM_ROPE, stream);
   with_lanes(D, [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
@@ -521,10 +547,10 @@ int moe_qk_norm_rope_backward(int32_t N, int32_t D, int32_t rotary_dim, int32_t 
     partial = static_cast<float*>(workspace);
   }
   const Cuts c = cuts_of(N, D, heads, kBackwardBlocks);
-  const Shape s{N, D, rotary_dim, interleaved != 0, c.heads_per_block, c.tokens_per_block, eps,
-                positions, inv_freq};
+  const Shape s{N, D, rotary_dim, interleaved != 0, c.heads_per_block, c.tokens_per_block,
+                c.tile(rotary_dim), eps, positions, inv_freq};
   const dim3 grid(c.token_parts, c.head_parts);
-  const int smem = 2 * kTokens * rotary_dim * 4;
+  const int smem = 2 * s.tile * rotary_dim * 4;
   mark_before(MOE_KERNEL_QK_NORM_ROPE_BWD, stream);
   with_lanes(D, [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;

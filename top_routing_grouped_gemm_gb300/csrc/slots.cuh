@@ -15,15 +15,4 @@ __device__ __forceinline__ bool named_before(int b, int row, const int* slot, in
   return bad;
 }
 
-// Row of the pool for request b, or -1 to skip it: a padding row (-1), or one that is out of range
-// or was named before, which is reported.  Called by whole blocks, every thread with the same b.
-__device__ __forceinline__ int claimed_slot(int b, const int* slot, int n_slots,
-                                            int* dev_status) {
-  if (!slot) return b;
-  const int row = slot[b];
-  if (row >= 0 && row < n_slots) return named_before(b, row, slot, dev_status) ? -1 : row;
-  if (row != -1 && threadIdx.x == 0 && dev_status) atomicCAS(dev_status, 0, MOE_ERR_BAD_INDEX);
-  return -1;
-}
-
 }  // namespace moe
