@@ -103,8 +103,8 @@ int moe_gdr_backward(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, co
  * nothing.
  *
  * Supported (else MOE_ERR_UNSUPPORTED): D a multiple of 8, at most 256; rotary_dim a multiple
- * of 16, at most D, 0 for no rotation (positions and inv_freq may then be NULL); pointers
- * 16-byte aligned; strides multiples of 8 values.  eps > 0.  Heads are addressed by strides (in
+ * of 16, at most D, 0 for no rotation (positions and inv_freq may then be NULL); at most 4096
+ * heads in a group and 2^30 tokens; pointers 16-byte aligned; strides multiples of 8 values.  eps > 0.  Heads are addressed by strides (in
  * values), so q and k can be parts of one fused projection row; token t's head h starts at
  * t * token_stride + h * head_stride.  Input strides may be 0 (broadcast); rows of an output
  * must not overlap (MOE_ERR_INVALID_ARG).  y may be x, with the same strides, and dx may be x

@@ -28,8 +28,11 @@
  *   last, and their gradients; each may be NULL (zero, or not wanted).  h_T may be h0: the
  *   states are then updated in place.  An empty sequence hands its h0 to h_T.
  * Any D, N up to 2^30 and n_seq up to 2^24 (else MOE_ERR_UNSUPPORTED), any alignment of the
- * values' own type.  D, the strides and the pointers of the
- * `dtype` tensors allowing, two channels are moved at a time, which is faster.
+ * values' own type; where the rows of all `dtype` tensors begin on 16-byte boundaries they are
+ * copied by TMA, which is faster.  Apart from h_T over h0, outputs may not overlap inputs.
+ *
+ * Waits inside the kernels are bounded; one that runs out ends the waiting of that launch, whose
+ * outputs are then wrong, and is reported as MOE_ERR_TIMEOUT in *dev_status.
  *
  * Precision: states, products and sums are fp32; h, dg and dx are rounded once.  Sequences do
  * not see each other: infinities or NaN in one leave the others alone.  Deterministic: the
@@ -61,8 +64,8 @@ int moe_glr_forward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off,
                     moe_stream_t stream);
 
 /* Backward: gradients of <dh, h> + <dh_T, h_T>.  h_chunks: the forward's (required); h_{t-1} is
- * formed again from it in fp32.  dg and dx have the strides of g and x (ld >= D).  dh0 may be
- * dh_T. */
+ * formed again from it in fp32.  dg and dx have the strides of g and x (ld >= D).  No output may
+ * overlap an input. */
 int moe_glr_backward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off, int32_t mode,
                      int32_t dtype, const void* g, int64_t ld_g, const void* x, int64_t ld_x,
                      const float* h0, const float* h_chunks, const void* dh, const float* dh_T,
@@ -71,8 +74,9 @@ int moe_glr_backward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off
 /* One token for each of B requests: the state of request b is row slot[b] of state
  * [n_slots, D] fp32, updated in place; its h [B, D] is also written in `dtype`.  g, x: B rows,
  * ld_g and ld_x apart.  slot as in moe_gdr_step: NULL for b itself, -1 for a padding row
- * (skipped, its h left as it was), anything else out of range and later requests with an
- * earlier one's slot skipped and reported as MOE_ERR_BAD_INDEX. */
+ * (skipped, its h left as it was), anything else out of range and later requests with an earlier
+ * one's slot skipped and reported as MOE_ERR_BAD_INDEX.  B up to 65535 (else
+ * MOE_ERR_UNSUPPORTED). */
 int moe_glr_step(int32_t B, int32_t D, int32_t mode, int32_t dtype, const void* g, int64_t ld_g,
                  const void* x, int64_t ld_x, const int32_t* slot, int32_t n_slots, float* state,
                  void* h, int32_t* dev_status, moe_stream_t stream);

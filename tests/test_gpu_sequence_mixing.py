@@ -247,6 +247,12 @@ GLR = [
     (200, 4, 1, False, F32, True),
     (4100, 328, [2000, None, 0], True, BF, True),
     (3001, 100, 1, True, F32, False),
+    # sequences of one and three rows; runs of empty ones; more of them than a block keeps bounds of
+    (300, 72, 300, True, BF, True),
+    (303, 72, 101, False, F32, True),
+    (200, 72, [0] * 40 + [5] + [0] * 70 + [None] + [0] * 33 + [3], True, BF, True),
+    (2000, 68, [n % 4 for n in range(900)] + [None, 0], False, F32, True),
+    (5000, 64, [n % 7 for n in range(1300)] + [None, 0], True, BF, True),
 ]
 
 
@@ -446,6 +452,58 @@ def test_recurrence_reports_bad_offsets():
                             g, x, None, h, torch.empty((3, D)).cuda(), None, status)
         assert int(status) == 6, off
         assert (guard[0] == 3).all() and (guard[-1] == 3).all()
+
+
+def test_recurrence_past_2_to_31_values():
+    """300000 x 8192 values: the last rows, states and gradients of the last of three sequences
+    (what is 600 steps back has decayed by e^-60 or more)."""
+    N, D, tail = 300000, 8192, 600
+    assert N * D > 1 << 31
+    torch.manual_seed(12)
+    row = lambda n: torch.randn((n, D), device="cuda").to(BF)  # noqa: E731
+    g = -0.1 - torch.rand((1, D), device="cuda").to(BF)
+    x, dh = (row(1000).repeat(N // 1000, 1) for _ in range(2))
+    off = torch.tensor([0, 1000, 150001, N - 5], dtype=torch.int32).cuda()
+    h, dg, dx = (torch.full((N, D), 7.0, dtype=BF, device="cuda") for _ in range(3))
+    h_T, chunks = torch.empty((3, D), device="cuda"), torch.empty(((N + 63) // 64, D), device="cuda")
+    gs = g.expand(N, D).contiguous()
+    args = (N, D, 3, off, moe.MOE_GLR_ADD, moe.MOE_BF16, gs, x)
+    moe.moe_glr_forward(*args, None, h, h_T, chunks)
+    moe.moe_glr_backward(*args, None, chunks, dh, None, dg, dx, None)
+    torch.cuda.synchronize()
+    lo, hi = N - 5 - tail, N - 5
+    gt, xt, dt = f64(gs[lo:hi]), f64(x[lo:hi]), f64(dh[lo:hi])
+    ref, ref_T = SM.gated_recurrence(gt, xt, [0, tail], None)
+    _, E = majorants(gt, xt, [0, tail], None, False)
+    keep = slice(tail - 50, tail)
+    close(h[lo:hi][keep], ref[keep], E[keep], BF, "h")
+    close(h_T[2], ref_T[0], E[-1], F32, "h_T")
+    back = SM.gated_recurrence_backward(gt, xt, [0, tail], dt)
+    for got, want in ((dx, back["dx"]), (dg, back["dg"])):
+        # sums of at most ~10 terms that matter, each through at most 30 roundings of its step
+        size = np.abs(want[keep]) + 30.0
+        close(got[lo:hi][keep], want[keep], 400 * size, BF)
+    for t in (h, dg, dx):
+        assert (t[hi:] == 7.0).all()
+
+
+def test_norm_rope_past_2_to_31_values():
+    N, H, D = 40000, 512, 128
+    assert N * H * D > 1 << 31
+    gen = torch.Generator().manual_seed(13)
+    x = torch.randn((N, 1, D), generator=gen).to(BF).cuda().expand(N, H, D)
+    y = torch.empty((N, H, D), dtype=BF, device="cuda")
+    freq = (1e6 ** -(torch.arange(0, D, 2, dtype=torch.float64) / D)).cuda()
+    pos = torch.arange(N, dtype=torch.int32).cuda()
+    w = torch.rand(D, generator=gen).cuda()
+    moe.moe_qk_norm_rope(N, D, D, False, moe.MOE_BF16, 1e-6, pos, freq,
+                         dict(x=x, y=y, weight=w), None)
+    torch.cuda.synchronize()
+    t = [0, N // 2, N - 1]
+    n = SM.qk_norm_rope(f64(x[t, :1]), f64(w), None, None, 0, False, 1e-6)
+    ref = SM.qk_norm_rope(f64(x[t, :1]), f64(w), f64(pos[t]), f64(freq), D, False, 1e-6)
+    for head in (0, 255, H - 1):
+        close(y[t, head:head + 1], ref, rope_count(D) * pair_sums(n, D, False), BF)
 
 
 # ---------------------------------------------------------------- single tokens

@@ -645,7 +645,7 @@ struct BackwardArgs {
   int D, parts, cluster;
   const T *g, *x, *dh;
   long long ld_g, ld_x;
-  const float *h0, *h_chunks, *dh_T;  // dh_T may be dh0
+  const float *h0, *h_chunks, *dh_T;
   T *dg, *dx;
   float* dh0;
   int* dev_status;

@@ -429,7 +429,7 @@ int check_common(int N, int D, int rot, int dtype, float eps, const void* pos, c
     return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
   if (rot > 0 && (!pos || !freq)) return MOE_ERR_INVALID_ARG;
-  if (D % 8 || D > kMaxD || rot % 16) return MOE_ERR_UNSUPPORTED;
+  if (D % 8 || D > kMaxD || rot % 16 || N > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
