@@ -27,8 +27,8 @@
  *   h0, h_T, dh_T, dh0 [n_seq, D] fp32: the state before a sequence's first row and after its
  *   last, and their gradients; each may be NULL (zero, or not wanted).  h_T may be h0: the
  *   states are then updated in place.  An empty sequence hands its h0 to h_T.
- * Any D, N up to 2^30 and n_seq up to 2^24 (else MOE_ERR_UNSUPPORTED), any alignment of the
- * values' own type; where the rows of all `dtype` tensors begin on 16-byte boundaries they are
+ * D up to 2^20, N up to 2^30 and n_seq up to 2^24 (else MOE_ERR_UNSUPPORTED), any alignment of
+ * the values' own type; where the rows of all `dtype` tensors begin on 16-byte boundaries they are
  * copied by TMA, which is faster.  Apart from h_T over h0, outputs may not overlap inputs.
  *
  * Waits inside the kernels are bounded; one that runs out ends the waiting of that launch, whose

@@ -7,6 +7,10 @@ itself.  Each check bounds the fp32 error of every value by U times a count of t
 that reach it, weighted with the sizes of the terms they act on (sums of absolute values, formed
 in 64 bits beside the oracle), plus the last rounding."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -800,3 +804,96 @@ def test_captured_and_replayed_on_another_stream():
         chain(b)
         torch.cuda.synchronize()
         assert all(torch.equal(b[n], t) for n, t in got.items())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N, D, lengths", [(4, 392, [4]), (700, 136, [300, 0, 395]),
+                                           (4099, 320, [4099])])
+def test_training_passes_back_to_back_on_two_states(N, D, lengths, dtype):
+    """Passes that follow one another without a wait, on two states in turn: every pass of a state
+    has the bits of its first one, and the inputs stay as they were."""
+    i, other = (glr_inputs((N, D, lengths, True, dtype, True), seed=s) for s in (3, 4))
+    states = []
+    for v in (i, other):
+        gen = torch.Generator().manual_seed(5)
+        states.append(dict(v, dh=torch.randn((N, D), generator=gen).to(dtype).cuda(),
+                           dh_T=torch.randn((len(lengths), D), generator=gen).cuda()))
+
+    def run(s):
+        e = lambda *n, dt=F32: torch.zeros(n, dtype=dt, device="cuda")  # noqa: E731
+        n_seq = len(lengths)
+        out = dict(h=e(N, D, dt=dtype), h_T=e(n_seq, D), chunks=e((N + 63) // 64, D),
+                   dg=e(N, D, dt=dtype), dx=e(N, D, dt=dtype), dh0=e(n_seq, D))
+        off, head = offsets_arg(s), (moe.MOE_GLR_MIX, CODE[dtype])
+        g, x = s["g"][:, :D].contiguous(), s["x"][:, :D].contiguous()
+        h0 = s["h0"]
+
+        def call():
+            moe.moe_glr_forward(N, D, n_seq, off, *head, g, x, h0, out["h"], out["h_T"],
+                                out["chunks"])
+            moe.moe_glr_backward(N, D, n_seq, off, *head, g, x, h0, out["chunks"], s["dh"],
+                                 s["dh_T"], out["dg"], out["dx"], out["dh0"])
+
+        return call, out, dict(g=g, x=x, h0=h0, dh=s["dh"], dh_T=s["dh_T"])
+
+    runs = [run(s) for s in states]
+    kept = [{n: t.clone() for n, t in r[2].items()} for r in runs]
+    first = []
+    for call, out, _ in runs:
+        call()
+        first.append({n: t.clone() for n, t in out.items()})
+    for _ in range(10):
+        for call, _, _ in runs:
+            call()
+    for (_, out, ins), want, before in zip(runs, first, kept):
+        assert all(torch.equal(out[n], want[n]) for n in out)
+        assert all(torch.equal(ins[n], before[n]) for n in ins)
+
+
+FIRST_CALL = """
+import torch
+from top_routing_grouped_gemm_gb300 import moe
+N, H, D, B = 130, 2, 64, 3
+f, dev = moe.MOE_F32, "cuda"
+r = lambda *s: torch.randn(s, device=dev)
+x, y, dx, w, dw = r(N, H, D), r(N, H, D), r(N, H, D), r(D), r(D)
+pos = torch.arange(N, dtype=torch.int32, device=dev)
+freq = 1e4 ** -(torch.arange(0, D, 2, dtype=torch.float64, device=dev) / D)
+ws = torch.empty(1 << 22, dtype=torch.uint8, device=dev)
+g, v, h, dh, dg, dv = -r(N, 128).abs(), r(N, 128), r(N, 128), r(N, 128), r(N, 128), r(N, 128)
+c, h_T, st, hs = r(3, 128), r(1, 128), r(B, 128), r(B, 128)
+bf = lambda *s: r(*s).bfloat16()
+q, k, vv, o, S = bf(B, H, D), bf(B, H, D), bf(B, H, D), bf(B, H, D), r(B, H, D, D)
+beta, gg = torch.sigmoid(r(B, H)), -r(B, H).abs()
+def calls():
+    moe.moe_qk_norm_rope(N, D, D, False, f, 1e-6, pos, freq, dict(x=x, y=y, weight=w), None)
+    moe.moe_qk_norm_rope_backward(N, D, D, False, f, f, 1e-6, pos, freq,
+                                  dict(x=x, dy=y, dx=dx, weight=w, dweight=dw), None, ws)
+    moe.moe_glr_forward(N, 128, 1, None, 1, f, g, v, None, h, h_T, c)
+    moe.moe_glr_backward(N, 128, 1, None, 1, f, g, v, None, c, dh, None, dg, dv, None)
+    moe.moe_glr_step(B, 128, 1, f, g[:B], v[:B], None, B, st, hs)
+    moe.moe_gdr_step(B, H, D, D, q, k, vv, beta, gg, None, B, 0.125, S, o)
+outs = (y, dx, dw, h, h_T, c, dg, dv, st, hs, S, o)
+start = [t.clone() for t in (st, S)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    calls()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in outs]
+st.copy_(start[0]); S.copy_(start[1])
+calls()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, outs))
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_are_captured():
+    """What the library prepares on first use (kernel attributes, the room for clusters) may be
+    prepared while a stream is captured: in a process of its own, whose first calls are a graph."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    got = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True,
+                         text=True, timeout=300)
+    assert got.returncode == 0 and "same" in got.stdout, got.stderr[-2000:]

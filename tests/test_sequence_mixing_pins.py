@@ -263,3 +263,42 @@ def test_binding_refuses_tensors_that_are_not_what_the_call_says():
     q, s = torch.zeros((4, 2, 64), dtype=bf), torch.zeros((4, 2))
     with pytest.raises(ValueError):
         moe.moe_gdr_step(4, 2, 64, 64, q, q, q, s, s, None, 4, 0.1, torch.zeros((4, 2, 64, 64)), q)
+
+
+def test_binding_refuses_missing_tensors():
+    """None where a call cannot do without a tensor raises like any other tensor that is not what
+    the call says."""
+    z, f = torch.zeros((4, 8)), moe.MOE_F32
+    x = torch.zeros((4, 2, 64))
+    freq, pos = torch.ones(32, dtype=torch.float64), torch.arange(4, dtype=torch.int32)
+    calls = [lambda: moe.moe_glr_forward(4, 8, 1, None, 0, f, None, z, None, z, None, None),
+             lambda: moe.moe_glr_forward(4, 8, 1, None, 0, f, z, z, None, None, None, None),
+             lambda: moe.moe_glr_backward(4, 8, 1, None, 0, f, z, z, None, z[:1], z, None, None, z,
+                                          None),
+             lambda: moe.moe_glr_step(4, 8, 0, f, z, None, None, 4, z, z),
+             lambda: moe.moe_qk_norm_rope(4, 64, 64, False, f, 1e-6, pos, freq,
+                                          dict(x=None, y=x), None),
+             lambda: moe.moe_qk_norm_rope(4, 64, 64, False, f, 1e-6, pos, freq,
+                                          dict(x=x[:, 0], y=x), None),
+             lambda: moe.moe_qk_norm_rope_backward(4, 64, 64, False, f, f, 1e-6, pos, freq,
+                                                   dict(x=None, dy=x, dx=x), None, None)]
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_recurrence_refuses_more_channels_than_a_launch_has_strips():
+    for over in (dict(D=(1 << 20) + 1, ld_g=1 << 21, ld_x=1 << 21),
+                 dict(D=1 << 30, ld_g=1 << 30, ld_x=1 << 30)):
+        assert glr(**over) == UNSUPPORTED
+        assert glr(backward=True, **over) == UNSUPPORTED
+    assert moe.lib().moe_glr_step(4, (1 << 20) + 1, 0, 0, FAKE, 1 << 21, FAKE, 1 << 21, FAKE, 4,
+                                  FAKE, FAKE, None, None) == UNSUPPORTED
+
+
+def test_workspace_size_of_sizes_that_are_refused():
+    big = 2 ** 31 - 1
+    for N, D, q, k in ((4, 64, big, big), (4, 64, 4097, 1), (4, 64, 1, 4097), (4, 264, 1, 1),
+                       (big, 64, 1, 1)):
+        assert moe.moe_qk_norm_rope_backward_workspace_size(N, D, q, k) == 0
+    assert moe.moe_qk_norm_rope_backward_workspace_size(1 << 30, 256, 4096, 4096) > 0

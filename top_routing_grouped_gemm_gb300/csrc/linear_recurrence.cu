@@ -962,7 +962,7 @@ int check_rows(int N, int D, int n_seq, const int* seq_off, int mode, int dtype,
   const int size = dtype == MOE_BF16 ? 2 : 4;
   if (misaligned(g, size) || misaligned(x, size) || misaligned(out, size))
     return MOE_ERR_UNSUPPORTED;
-  if (n_seq > (1 << 24) || N > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+  if (n_seq > (1 << 24) || N > (1 << 30) || D > (1 << 20)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

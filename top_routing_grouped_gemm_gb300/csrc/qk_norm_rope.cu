@@ -14,7 +14,7 @@
 namespace moe {
 namespace {
 
-constexpr int kMaxD = 256;
+constexpr int kMaxD = 256, kMaxHeads = 4096;
 constexpr int kSms = 152;  // of the GPU that the cuts are made for
 
 // One group of heads (q or k) as the kernels see it.
@@ -447,7 +447,7 @@ int check_rows(const void* p, long long ts, long long hs) {
 
 int check_heads(int N, int heads, const float* weight) {
   if (heads <= 0) return MOE_ERR_INVALID_ARG;
-  if (heads > 4096 || bad_align(weight)) return MOE_ERR_UNSUPPORTED;
+  if (heads > kMaxHeads || bad_align(weight)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -529,7 +529,9 @@ int moe_qk_norm_rope(int32_t N, int32_t D, int32_t rotary_dim, int32_t interleav
 
 size_t moe_qk_norm_rope_backward_workspace_size(int32_t N, int32_t D, int32_t q_heads,
                                                 int32_t k_heads) {
-  if (N <= 0 || D <= 0 || q_heads <= 0 || k_heads < 0) return 0;
+  if (N <= 0 || N > (1 << 30) || D <= 0 || D > kMaxD || q_heads <= 0 || q_heads > kMaxHeads ||
+      k_heads < 0 || k_heads > kMaxHeads)
+    return 0;
   return backward_ws(N, D, q_heads, k_heads);
 }
 

@@ -522,12 +522,18 @@ def _status(dev_status, dev):
 
 def _head_rows(name, t, dtype, shape, dev):
     """(address, token stride, head stride) of [N, heads, D] values, dense within a head."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _refuse(name, t, f"a {dtype} tensor {shape}")
     by_token, by_head, by_value = t.stride()
     if by_value != 1:
         _refuse(name, t, f"a {dtype} tensor {shape}, dense in its last dimension,")
     return t.data_ptr(), by_token, by_head
+
+
+def _heads(name, x, dtype):
+    if x is None or x.dim() != 3:
+        _refuse(name, x, f"a {dtype} tensor [N, heads, D]")
+    return x.shape[1]
 
 
 def _head_weight(name, w, heads, D, dev):
@@ -542,7 +548,7 @@ def _qk_rows(name, r, dtype, N, D, dev):
     if r is None:
         return None
     x = r["x"]
-    heads = x.shape[1]
+    heads = _heads(name + ".x", x, dtype)
     shape = (N, heads, D)
     return ctypes.byref(moe_qk_rows(*_head_rows(name + ".x", x, dtype, shape, dev),
                                     *_head_rows(name + ".y", r["y"], dtype, shape, dev),
@@ -554,7 +560,7 @@ def _qk_grads(name, r, dtype, dy_dtype, N, D, dev):
     if r is None:
         return None
     x, w, dw = r["x"], r.get("weight"), r.get("dweight")
-    heads = x.shape[1]
+    heads = _heads(name + ".x", x, dtype)
     shape = (N, heads, D)
     if w is not None and dw is not None and w.shape != dw.shape:
         _refuse(name + ".dweight", dw, f"a tensor shaped as {name}.weight")
@@ -622,7 +628,7 @@ def moe_gdr_step(B, H, dk, dv, q, k, v, beta, g, slot, n_slots, scale, S, o, dev
 
 def _rows(name, t, dtype, shape, dev):
     """(address, row stride) of rows dense in themselves."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _refuse(name, t, f"a {dtype} tensor {shape}")
     by_row, by_value = t.stride()
     if by_value != 1 and shape[1] > 1:
