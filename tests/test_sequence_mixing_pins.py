@@ -302,3 +302,32 @@ def test_workspace_size_of_sizes_that_are_refused():
                        (big, 64, 1, 1)):
         assert moe.moe_qk_norm_rope_backward_workspace_size(N, D, q, k) == 0
     assert moe.moe_qk_norm_rope_backward_workspace_size(1 << 30, 256, 4096, 4096) > 0
+
+
+def test_packed_heads_are_the_structures():
+    """The bytes that the binding hands over are the C structures, field by field."""
+    for form, kind in ((moe._QK_ROWS, moe.moe_qk_rows), (moe._QK_GRADS, moe.moe_qk_grads)):
+        values = tuple(range(1, len(kind._fields_) + 1))
+        assert form.size == ctypes.sizeof(kind)
+        assert form.pack(*values) == bytes(kind(*values))
+
+
+def test_binding_refuses_heads_that_do_not_agree():
+    x, y = torch.zeros((4, 2, 64)), torch.zeros((4, 3, 64))
+    for r in (dict(x=x, y=y), dict(x=x, y=None), dict(x=x.transpose(1, 2), y=x),
+              dict(x=x, y=x.bfloat16()), dict(x=x, y=x, weight=torch.ones(63)),
+              dict(x=x, y=x, weight=torch.ones(3, 64)),
+              dict(x=x, y=torch.zeros((4, 2, 128))[..., ::2])):
+        with pytest.raises(ValueError):
+            moe._qk_rows("q", r, torch.float32, 4, 64, -1)
+        r = dict(r, dy=x, dx=r["y"])
+        with pytest.raises(ValueError):
+            moe._qk_grads("q", r, torch.float32, torch.float32, 4, 64, -1)
+    for w, dw in ((torch.ones(64), torch.ones(2, 64)), (None, torch.ones(65))):
+        with pytest.raises(ValueError):
+            moe._qk_grads("q", dict(x=x, dy=x, dx=x, weight=w, dweight=dw), torch.float32,
+                          torch.float32, 4, 64, -1)
+    kind = moe.moe_qk_rows.from_buffer_copy(
+        moe._qk_rows("q", dict(x=y[:, 1:], y=x, weight=torch.ones(2, 64)), torch.float32, 4, 64, -1))
+    assert (kind.x, kind.x_token_stride, kind.x_head_stride) == (y.data_ptr() + 256, 192, 64)
+    assert (kind.y_token_stride, kind.weight_per_head, kind.heads) == (128, 1, 2)

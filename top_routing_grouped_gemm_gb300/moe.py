@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -129,13 +130,11 @@ _SIGS = {
                                         c_vp, ctypes.c_float, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
                                         c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
     "moe_qk_norm_rope": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32, c_i32, ctypes.c_float, c_vp,
-                                        c_vp, ctypes.POINTER(moe_qk_rows),
-                                        ctypes.POINTER(moe_qk_rows), c_vp]),
+                                        c_vp, c_vp, c_vp, c_vp]),
     "moe_qk_norm_rope_backward_workspace_size": (c_sz, [c_i32, c_i32, c_i32, c_i32]),
     "moe_qk_norm_rope_backward": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32,
-                                                 ctypes.c_float, c_vp, c_vp,
-                                                 ctypes.POINTER(moe_qk_grads),
-                                                 ctypes.POINTER(moe_qk_grads), c_vp, c_sz, c_vp]),
+                                                 ctypes.c_float, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                                 c_sz, c_vp]),
     "moe_gdr_step": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp,
                                     c_vp, c_i32, ctypes.c_float, c_vp, c_vp, c_vp, c_vp]),
     "moe_glr_forward": (ctypes.c_int, [c_i32, c_i32, c_i32, c_vp, c_i32, c_i32, c_vp, c_i64, c_vp,
@@ -495,11 +494,19 @@ def moe_gdr_backward(B, T, H, dk, dv, q, k, v, beta, g, scale, d_o, dS_T, S_chun
 _DTYPES = {MOE_BF16: torch.bfloat16, MOE_F32: torch.float32}
 
 
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _device():
     """The current device (none, which no tensor is on, where there is no GPU)."""
-    if torch.cuda.is_initialized() or torch.cuda.is_available():
-        return torch.cuda.current_device()
-    return -2
+    if torch.cuda.is_initialized():
+        return _get_device()
+    return torch.cuda.current_device() if torch.cuda.is_available() else -2
+
+
+def _stream_of(stream, dev):
+    """The stream's handle, by default the current one of the current device ``dev``."""
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _refuse(name, t, wanted):
@@ -520,56 +527,67 @@ def _status(dev_status, dev):
     return _tensor("dev_status", dev_status, torch.int32, (1,), dev, True)
 
 
-def _head_rows(name, t, dtype, shape, dev):
-    """(address, token stride, head stride) of [N, heads, D] values, dense within a head."""
-    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        _refuse(name, t, f"a {dtype} tensor {shape}")
-    by_token, by_head, by_value = t.stride()
-    if by_value != 1:
-        _refuse(name, t, f"a {dtype} tensor {shape}, dense in its last dimension,")
-    return t.data_ptr(), by_token, by_head
+def _is_rows(t, dtype, shape, dev):
+    return t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == dev
 
 
-def _heads(name, x, dtype):
-    if x is None or x.dim() != 3:
-        _refuse(name, x, f"a {dtype} tensor [N, heads, D]")
-    return x.shape[1]
+def _refuse_head_rows(name, t, dtype, N, D):
+    _refuse(name, t, f"a {dtype} tensor [{N}, heads, {D}] (of x's heads), dense in its last dimension,")
 
 
 def _head_weight(name, w, heads, D, dev):
     """(address, one row for each head?) of a norm weight or its gradient."""
     if w is None:
-        return None, 0
+        return 0, 0
     per_head = w.dim() == 2
     return _tensor(name, w, torch.float32, (heads, D) if per_head else (D,), dev), per_head
+
+
+# moe_qk_rows and moe_qk_grads as bytes (a sixth of the time of building the ctypes structures,
+# which shows in calls of a few microseconds)
+_QK_ROWS = struct.Struct("PqqPqqPii")
+_QK_GRADS = struct.Struct("PqqPqqPqqPPii")
 
 
 def _qk_rows(name, r, dtype, N, D, dev):
     if r is None:
         return None
-    x = r["x"]
-    heads = _heads(name + ".x", x, dtype)
+    x, y = r["x"], r["y"]
+    heads = x.shape[1] if x is not None and x.dim() == 3 else 0
     shape = (N, heads, D)
-    return ctypes.byref(moe_qk_rows(*_head_rows(name + ".x", x, dtype, shape, dev),
-                                    *_head_rows(name + ".y", r["y"], dtype, shape, dev),
-                                    *_head_weight(name + ".weight", r.get("weight"), heads, D,
-                                                  dev), heads))
+    if not _is_rows(x, dtype, shape, dev):
+        _refuse_head_rows(name + ".x", x, dtype, N, D)
+    if not _is_rows(y, dtype, shape, dev):
+        _refuse_head_rows(name + ".y", y, dtype, N, D)
+    x_token, x_head, x_value = x.stride()
+    y_token, y_head, y_value = y.stride()
+    if x_value != 1:
+        _refuse_head_rows(name + ".x", x, dtype, N, D)
+    if y_value != 1:
+        _refuse_head_rows(name + ".y", y, dtype, N, D)
+    weight, per_head = _head_weight(name + ".weight", r.get("weight"), heads, D, dev)
+    return _QK_ROWS.pack(x.data_ptr(), x_token, x_head, y.data_ptr(), y_token, y_head, weight,
+                         per_head, heads)
 
 
 def _qk_grads(name, r, dtype, dy_dtype, N, D, dev):
     if r is None:
         return None
     x, w, dw = r["x"], r.get("weight"), r.get("dweight")
-    heads = _heads(name + ".x", x, dtype)
-    shape = (N, heads, D)
+    heads = x.shape[1] if x is not None and x.dim() == 3 else 0
+    shape, at = (N, heads, D), []
+    for part, t, dt in ((".x", x, dtype), (".dy", r["dy"], dy_dtype), (".dx", r["dx"], dtype)):
+        if not _is_rows(t, dt, shape, dev):
+            _refuse_head_rows(name + part, t, dt, N, D)
+        by_token, by_head, by_value = t.stride()
+        if by_value != 1:
+            _refuse_head_rows(name + part, t, dt, N, D)
+        at += t.data_ptr(), by_token, by_head
     if w is not None and dw is not None and w.shape != dw.shape:
         _refuse(name + ".dweight", dw, f"a tensor shaped as {name}.weight")
     wp, per_head = _head_weight(name + ".weight", w, heads, D, dev)
     dwp, dw_per_head = _head_weight(name + ".dweight", dw, heads, D, dev)
-    return ctypes.byref(moe_qk_grads(*_head_rows(name + ".x", x, dtype, shape, dev),
-                                     *_head_rows(name + ".dy", r["dy"], dy_dtype, shape, dev),
-                                     *_head_rows(name + ".dx", r["dx"], dtype, shape, dev),
-                                     wp, dwp, per_head or dw_per_head, heads))
+    return _QK_GRADS.pack(*at, wp, dwp, per_head or dw_per_head, heads)
 
 
 def moe_qk_norm_rope(N, D, rotary_dim, interleaved, dtype, eps, positions, inv_freq, q, k,
@@ -584,7 +602,7 @@ def moe_qk_norm_rope(N, D, rotary_dim, interleaved, dtype, eps, positions, inv_f
                                   _tensor("inv_freq", inv_freq, torch.float64,
                                           (rotary_dim // 2,), dev, rotary_dim == 0),
                                   _qk_rows("q", q, dt, N, D, dev),
-                                  _qk_rows("k", k, dt, N, D, dev), _stream(stream)))
+                                  _qk_rows("k", k, dt, N, D, dev), _stream_of(stream, dev)))
 
 
 def moe_qk_norm_rope_backward_workspace_size(N, D, q_heads, k_heads) -> int:
@@ -606,7 +624,7 @@ def moe_qk_norm_rope_backward(N, D, rotary_dim, interleaved, dtype, dy_dtype, ep
                                                    (rotary_dim // 2,), dev, rotary_dim == 0),
                                            _qk_grads("q", q, dt, gt, N, D, dev),
                                            _qk_grads("k", k, dt, gt, N, D, dev), wp, wn,
-                                           _stream(stream)))
+                                           _stream_of(stream, dev)))
 
 
 def moe_gdr_step(B, H, dk, dv, q, k, v, beta, g, slot, n_slots, scale, S, o, dev_status=None,
@@ -621,14 +639,14 @@ def moe_gdr_step(B, H, dk, dv, q, k, v, beta, g, slot, n_slots, scale, S, o, dev
                               _tensor("slot", slot, torch.int32, (B,), dev, True), n_slots, scale,
                               _tensor("S", S, f32, (n_slots, H, dv, dk), dev),
                               _tensor("o", o, bf, (B, H, dv), dev), _status(dev_status, dev),
-                              _stream(stream)))
+                              _stream_of(stream, dev)))
 
 
 # ---- gated linear recurrence (include/linear_recurrence.h)
 
 def _rows(name, t, dtype, shape, dev):
     """(address, row stride) of rows dense in themselves."""
-    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+    if not _is_rows(t, dtype, shape, dev):
         _refuse(name, t, f"a {dtype} tensor {shape}")
     by_row, by_value = t.stride()
     if by_value != 1 and shape[1] > 1:
@@ -649,7 +667,7 @@ def moe_glr_forward(N, D, n_seq, seq_off, mode, dtype, g, x, h0, h, h_T, h_chunk
                                  _tensor("h", h, dt, rows, dev),
                                  _tensor("h_T", h_T, f32, (n_seq, D), dev, True),
                                  _tensor("h_chunks", h_chunks, f32, ((N + 63) // 64, D), dev, True),
-                                 _status(dev_status, dev), _stream(stream)))
+                                 _status(dev_status, dev), _stream_of(stream, dev)))
 
 
 def moe_glr_backward(N, D, n_seq, seq_off, mode, dtype, g, x, h0, h_chunks, dh, dh_T, dg, dx, dh0,
@@ -672,7 +690,7 @@ def moe_glr_backward(N, D, n_seq, seq_off, mode, dtype, g, x, h0, h_chunks, dh, 
                                   _tensor("dh", dh, dt, rows, dev),
                                   _tensor("dh_T", dh_T, f32, (n_seq, D), dev, True), dgp, dxp,
                                   _tensor("dh0", dh0, f32, (n_seq, D), dev, True),
-                                  _status(dev_status, dev), _stream(stream)))
+                                  _status(dev_status, dev), _stream_of(stream, dev)))
 
 
 def moe_glr_step(B, D, mode, dtype, g, x, slot, n_slots, state, h, dev_status=None, stream=None):
@@ -684,7 +702,7 @@ def moe_glr_step(B, D, mode, dtype, g, x, slot, n_slots, state, h, dev_status=No
                               _tensor("slot", slot, torch.int32, (B,), dev, True), n_slots,
                               _tensor("state", state, torch.float32, (n_slots, D), dev),
                               _tensor("h", h, dt, rows, dev), _status(dev_status, dev),
-                              _stream(stream)))
+                              _stream_of(stream, dev)))
 
 
 def moe_set_kernel_events(kernel, before, after):
