@@ -63,6 +63,13 @@ ROPE = [
 ]
 
 
+# every width of a head: rows take as many lanes as they have values for, several rows to a warp,
+# with other heads and layouts beside them
+WIDTHS = [(41 + D // 8, 1 + D // 8 % 5, D // 8 % 4, D, D // 16 * 16 if D % 3 else D // 32 * 16,
+           D // 8 % 2 == 0, ("shared", "per_head", None)[D // 8 % 3], (BF, F32)[D // 24 % 2],
+           ("fused", "dense", "head_major")[D // 16 % 3]) for D in range(8, 257, 8)]
+
+
 def rope_inputs(case, seed=0):
     N, hq, hk, D, rot, inter, weight, dtype, layout = case
     gen = torch.Generator().manual_seed(seed)
@@ -159,6 +166,12 @@ def test_norm_rope_backward(case, dy32):
         close(s["dweight"], ref, (2 * count + rows) * each, F32, "dweight")
         # the sum itself is split over blocks and warps, so far fewer roundings reach it
         assert relerr(f64(s["dweight"]), ref) <= 2e-5
+
+
+@pytest.mark.parametrize("case", WIDTHS, ids=[str(c[3]) for c in WIDTHS])
+def test_norm_rope_of_every_width(case):
+    test_norm_rope(case)
+    test_norm_rope_backward(case, case[3] % 16 == 0)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])

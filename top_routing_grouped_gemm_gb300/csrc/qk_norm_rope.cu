@@ -73,11 +73,18 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, int far, const float (&v
          make_uint2(pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
 }
 
-// A block takes some heads of a range of tokens, in tiles.  L lanes hold a row, and
-// always the same head, so that its weight stays in registers and its weight gradient gathers
-// there.  The block forms the tile's sines and cosines once, in shared memory, for all its heads.
+// A block takes some heads of a range of tokens, in tiles.  D / 8 neighbouring lanes of a warp hold a
+// row, as many rows as the warp has room for, and always the same head, so that its weight stays in
+// registers and its weight gradient gathers there.  (On a power of two of lanes, rows of 80 values
+// leave 6 of 16 idle: 62500 tokens x 20 heads of 80 bf16 took 130 us so, 86 us now.)  The
+// block forms the tile's sines and cosines once, in shared memory, for all its heads.
 constexpr int kThreads = 256;
-constexpr int kRows = 4;  // rows that a lane has on their way
+// Rows of 8 values that a lane has on their way; the forward, which shares the registers among more
+// blocks, has fewer of them in fp32 (9765 tokens x 40 heads x 128 took 69.3 us with four, 66.4 us with
+// two).
+constexpr int kRows = 4;
+template <typename T>
+constexpr int kForwardRows = sizeof(T) == 4 ? 2 : kRows;
 constexpr int kIdle = 1 << 20;  // a token that no tile has
 constexpr int kForwardBlocks = 4, kBackwardBlocks = 2;  // to an SM
 
@@ -125,35 +132,53 @@ struct Angles {
   }
 };
 
-// What a lane has to do.
-template <int L>
+// What a lane has to do.  The lanes of a row are L = D / 8 of them (FULL), or L is the least power of
+// two that is not less.
+template <int L, bool FULL>
 struct Lane {
   int near, far;     // its first quad, and the second from there
-  int place;         // of its pairs in a token's table
+  int place, lanes;  // among the lanes of its row
   int head, slot;    // head of all heads; tokens slot, slot + stride, ... of a tile
-  int stride;
-  bool in, turns;    // has values; rotates them
+  int group, stride;
+  bool turns;        // rotates its values
 
   __device__ __forceinline__ Lane(const Shape& s, int heads) {
-    const int group = threadIdx.x / L;
-    place = threadIdx.x % L;
-    stride = kThreads / L / s.heads_per_block;
+    lanes = FULL ? L : s.D / 8;
+    const int lane = threadIdx.x & 31, per_warp = 32 / lanes, row = lane / lanes;
+    place = lane - row * lanes;
+    group = threadIdx.x / 32 * per_warp + row;
+    stride = kThreads / 32 * per_warp / s.heads_per_block;
     slot = group / s.heads_per_block;
     head = blockIdx.y * s.heads_per_block + group % s.heads_per_block;
-    in = place * 8 < s.D;
-    if (slot >= stride || head >= heads) slot = kIdle, head = heads - 1;
+    // lanes without a row read what another row's lanes read
+    if (row >= per_warp || slot >= stride || head >= heads)
+      slot = kIdle, head = heads - 1, group = -1;
     turns = place * 8 < s.rot;
     const bool halves = turns && !s.interleaved;
-    near = in ? place * (halves ? 4 : 8) : 0;
+    near = place * (halves ? 4 : 8);
     far = halves ? s.rot / 2 : 4;
+  }
+
+  // The sum over the row's lanes.
+  __device__ __forceinline__ float row_sum(float v) const {
+    if constexpr (FULL) {
+#pragma unroll
+      for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+      return v;
+    } else {
+#pragma unroll
+      for (int o = L / 2; o; o >>= 1) {  // the first o lanes get those behind them
+        const float behind = __shfl_down_sync(~0u, v, o);
+        if (place + o < lanes) v += behind;
+      }
+      return __shfl_sync(~0u, v, (threadIdx.x & 31) - place);
+    }
   }
 };
 
 // R(th) v, or R(-th) v (BACK).
 template <bool BACK>
-__device__ __forceinline__ void rotate(float (&v)[8], const float4* table, const Shape& s, int t,
-                                       int place) {
-  const float4* cs = table + t * (s.rot / 4) + place;
+__device__ __forceinline__ void rotate(float (&v)[8], const float4* cs, const Shape& s) {
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const float4 w = cs[c * (s.rot / 8)];
@@ -174,15 +199,9 @@ __device__ __forceinline__ void rotate(float (&v)[8], const float4* table, const
   }
 }
 
-template <int L>
-__device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-  for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  return v;
-}
-
-template <int L>
-__device__ __forceinline__ void load_weight(const Side& side, int h, const Lane<L>& me, float (&w)[8]) {
+template <int L, bool FULL>
+__device__ __forceinline__ void load_weight(const Side& side, int h, const Lane<L, FULL>& me,
+                                            float (&w)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     w[e] = side.weight ? side.weight[static_cast<long long>(h) * side.w_hs + me.near +
@@ -190,59 +209,56 @@ __device__ __forceinline__ void load_weight(const Side& side, int h, const Lane<
                        : 1.f;
 }
 
-// Lanes past the row's end (a width that is no power of two) add nothing.
-template <int L>
-__device__ __forceinline__ void trim(float (&v)[8], const Shape& s, const Lane<L>& me) {
-  if (s.D != 8 * L && !me.in)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
-}
-
-// Every row is read and written once: 32768 tokens x 32 heads x 128 bf16 take 93.6 us, 0.86 of the
-// rate of a plain copy, with 69 % of the issue slots used.  Two or three rows on their way instead
-// of kRows, and three or five blocks to an SM instead of kForwardBlocks, take 99 to 105 us; partners
-// in other lanes, with shuffles, and blocks in several waves took 131 us.
-template <typename T, int L>
+// Every row is read and written once: 32768 tokens x 32 heads x 128 bf16 take 91.3 us, 0.88 of the
+// rate of a plain copy (94 us with addresses from each row's index, which cost instructions that
+// these 64-bit steps do not).  Two or three rows on their way instead of four, and three or five blocks
+// to an SM instead of kForwardBlocks, take 5 to 12 % longer; partners in other lanes, with shuffles,
+// and blocks in several waves took 131 us.
+template <typename T, int L, bool FULL>
 __global__ void __launch_bounds__(kThreads, kForwardBlocks)
     rope_forward_kernel(const Shape s, const Side q, const Side k) {
   extern __shared__ float4 table[];  // [2][tile][rot / 4]
   const Angles angles(s);
-  const Lane<L> me(s, q.heads + k.heads);
+  const Lane<L, FULL> me(s, q.heads + k.heads);
   const Side& side = me.head < q.heads ? q : k;
   const int h = me.head < q.heads ? me.head : me.head - q.heads;
   float w[8];
   load_weight(side, h, me, w);
   const T* x = static_cast<const T*>(side.x) + h * side.x_hs + me.near;
   T* y = static_cast<T*>(side.out) + h * side.o_hs + me.near;
-  const long long lo = static_cast<long long>(blockIdx.x) * s.tokens_per_block;
-  const long long hi = min(lo + s.tokens_per_block, static_cast<long long>(s.N));
+  const long long x_step = me.stride * side.x_ts, o_step = me.stride * side.o_ts;
+  const int cs_step = me.stride * (s.rot / 4);
+  const int lo = blockIdx.x * s.tokens_per_block, hi = min(lo + s.tokens_per_block, s.N);
   const float inv_D = 1.f / s.D;
   int buf = 0;
-  for (long long t0 = lo; t0 < hi; t0 += s.tile, buf ^= 1) {
-    float4* now = table + buf * s.tile * (s.rot / 4);
-    const int n = static_cast<int>(min(static_cast<long long>(s.tile), hi - t0));
-    angles.fill(now, s, t0, n);
+  for (int t0 = lo; t0 < hi; t0 += s.tile, buf ^= 1) {
+    const int n = min(s.tile, hi - t0);
+    const float4* cs = table + buf * s.tile * (s.rot / 4);
+    angles.fill(table + buf * s.tile * (s.rot / 4), s, t0, n);
     __syncthreads();  // (the other buffer's readers are done when they come here again)
-    for (int t = 0; t < n; t += kRows * me.stride) {  // the same for all lanes: they shuffle
-      const int first = t + me.slot;
-      Raw<T> raw[kRows];
+    const T* from = x + (t0 + min(me.slot, n - 1)) * side.x_ts;
+    T* to = y + (t0 + me.slot) * side.o_ts;
+    cs += me.slot * (s.rot / 4) + me.place;
+    // the same number of rounds for all lanes: they shuffle
+    for (int left = n - me.slot, round = 0; round < n; round += kForwardRows<T> * me.stride) {
+      Raw<T> raw[kForwardRows<T>];
 #pragma unroll
-      for (int u = 0; u < kRows; ++u)  // past the last row: that row again
-        raw[u].load(x + (t0 + min(first + u * me.stride, n - 1)) * side.x_ts, me.far);
+      for (int u = 0; u < kForwardRows<T>; ++u) {
+        raw[u].load(from, me.far);
+        if (left > (u + 1) * me.stride) from += x_step;  // past the last row: that row again
+      }
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) {
-        const int at = first + u * me.stride;
+      for (int u = 0; u < kForwardRows<T>; ++u, left -= me.stride, to += o_step, cs += cs_step) {
         float v[8], sum = 0.f;
         raw[u].get(v);
-        trim(v, s, me);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
-        const float rstd = rsqrtf(fmaf(row_sum<L>(sum), inv_D, s.eps));
-        if (at < n && me.in) {
+        const float rstd = rsqrtf(fmaf(me.row_sum(sum), inv_D, s.eps));
+        if (left > 0) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] *= rstd * w[e];
-          if (me.turns) rotate<false>(v, now, s, at, me.place);
-          store(y + (t0 + at) * side.o_ts, me.far, v);
+          if (me.turns) rotate<false>(v, cs, s);
+          store(to, me.far, v);
         }
       }
     }
@@ -254,14 +270,14 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
 // gradients stay in registers over all of a block's tokens, and no atomic orders their sums.
 // partial: [blocks][2][D] (the shared weights of q and k) or [gridDim.x][heads][D] (a row for each
 // head), the sums of the block's rows; null: not wanted.
-template <typename T, typename G, int L>
+template <typename T, typename G, int L, bool FULL>
 __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
     rope_backward_kernel(const Shape s, const Side q, const Side k, float* partial) {
   extern __shared__ float4 table[];  // [2][tile][rot / 4]
-  __shared__ float sums[kThreads / L][L * 8];
+  __shared__ float sums[kThreads * 8];  // [group][D]
   const Angles angles(s);
   const int heads = q.heads + k.heads;
-  const Lane<L> me(s, heads);
+  const Lane<L, FULL> me(s, heads);
   const Side& side = me.head < q.heads ? q : k;
   const int h = me.head < q.heads ? me.head : me.head - q.heads;
   float w[8], dw[8] = {};
@@ -294,8 +310,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
         float v[8], d[8];
         raw[u].get(v);
         raw_d[u].get(d);
-        trim(v, s, me);
-        if (me.turns) rotate<true>(d, now, s, min(at, n - 1), me.place);
+        if (me.turns) rotate<true>(d, now + min(at, n - 1) * (s.rot / 4) + me.place, s);
         // both sums of the row at once: u = w dn; mean(u x^) = rstd mean(u x)
         float sum = 0.f, dot = 0.f;
 #pragma unroll
@@ -303,10 +318,9 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
           sum = fmaf(v[e], v[e], sum);
           dot = fmaf(d[e] * w[e], v[e], dot);
         }
-        if (s.D != 8 * L && !me.in) dot = 0.f;
-        const float rstd = rsqrtf(fmaf(row_sum<L>(sum), inv_D, s.eps));
-        const float c = row_sum<L>(dot) * inv_D * rstd * rstd;
-        if (at < n && me.in) {
+        const float rstd = rsqrtf(fmaf(me.row_sum(sum), inv_D, s.eps));
+        const float c = me.row_sum(dot) * inv_D * rstd * rstd;
+        if (at < n) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             dw[e] = fmaf(d[e], v[e] * rstd, dw[e]);
@@ -318,19 +332,18 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
     }
   }
   if (!partial) return;
-  const int group = threadIdx.x / L;
-  if (me.in)
+  if (me.group >= 0)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sums[group][me.near + (e < 4 ? e : me.far + e - 4)] = dw[e];
+    for (int e = 0; e < 8; ++e) sums[me.group * s.D + me.near + (e < 4 ? e : me.far + e - 4)] = dw[e];
   __syncthreads();
-  const int groups = kThreads / L / s.heads_per_block * s.heads_per_block;
+  const int groups = me.stride * s.heads_per_block;
   const int first = blockIdx.y * s.heads_per_block;
   if (q.w_hs || k.w_hs) {  // a row for each head: its groups, every heads_per_block'th
     for (int i = threadIdx.x; i < s.heads_per_block * s.D; i += kThreads) {
       const int head = i / s.D, e = i % s.D;
       if (first + head >= heads) continue;
       float sum = 0.f;
-      for (int g = head; g < groups; g += s.heads_per_block) sum += sums[g][e];
+      for (int g = head; g < groups; g += s.heads_per_block) sum += sums[g * s.D + e];
       partial[(static_cast<long long>(blockIdx.x) * heads + first + head) * s.D + e] = sum;
     }
   } else {
@@ -339,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
       float sum = 0.f;
       for (int g = 0; g < groups; ++g) {
         const int head = first + g % s.heads_per_block;
-        if (head < heads && (head >= q.heads) == of_k) sum += sums[g][e];
+        if (head < heads && (head >= q.heads) == of_k) sum += sums[g * s.D + e];
       }
       partial[(static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 * s.D + i] = sum;
     }
@@ -371,23 +384,22 @@ __global__ void __launch_bounds__(1024)
 
 // ------------------------------------------------------------------------ host side
 
-// Lanes of a row: 8 values each, a power of two of them that divides a warp; heads of less than 64
-// values leave some idle.
-int lanes_of(int D) { return D > 128 ? 32 : D > 64 ? 16 : 8; }
+// Rows that a block has at once: 8 values to a lane.
+int rows_of(int D) { return kThreads / 32 * (32 / (D / 8)); }
 
 // Heads of a block: what leaves fewest lanes idle (of a block's lanes, and of the last part's
 // heads), against the angles that each part of the heads forms anew.  In instructions a row, about
-// 90 for each lane and 50 for each pair's angle.  (16 + 4 heads of 80, 16 rows to a block: two parts
-// of 10 heads leave 3 / 8 of the lanes idle, four of 5 leave 1 / 16; the backward of 31250 tokens
-// in bf16 takes 144 and 123 us.)
+// 90 for each lane and 50 for each pair's angle.  (16 + 4 heads of 96, 16 rows to a block: two parts
+// of 10 heads leave 3 / 8 of the lanes idle, four of 5 leave 1 / 16; the backward of 26041 tokens
+// in bf16 takes 125 and 108 us.)
 int heads_of_block(int D, int heads) {
-  const int lanes = lanes_of(D), rows = kThreads / lanes;
+  const int rows = rows_of(D);
   int best = 1;
   double least = 1e30;
   for (int h = 1; h <= std::min(heads, rows); ++h) {
     const int parts = (heads + h - 1) / h;
     const double busy = static_cast<double>(rows / h * h) / rows * heads / (parts * h);
-    const double cost = lanes * 90.0 / busy + D / 2 * 50.0 / h;
+    const double cost = 90.0 * kThreads / rows / busy + D / 2 * 50.0 / h;
     if (cost <= least) least = cost, best = h;
   }
   return best;
@@ -409,7 +421,7 @@ struct Cuts {
 
 Cuts cuts_of(int N, int D, int heads, int blocks_per_sm) {
   Cuts c;
-  const int rows = kThreads / lanes_of(D);
+  const int rows = rows_of(D);
   c.heads_per_block = heads_of_block(D, heads);
   c.head_parts = (heads + c.heads_per_block - 1) / c.heads_per_block;
   c.at_once = rows / c.heads_per_block;  // tokens
@@ -481,15 +493,22 @@ size_t backward_ws(int N, int D, int q_heads, int k_heads) {
                std::max(2 * c.head_parts, q_heads + k_heads) * D * 4);
 }
 
-// Calls f(lanes) for the width of the heads.
+// Calls f(L, FULL) for the lanes of a row.
 template <typename F>
 void with_lanes(int D, F f) {
-  if (lanes_of(D) == 32)
-    f(std::integral_constant<int, 32>{});
-  else if (lanes_of(D) == 16)
-    f(std::integral_constant<int, 16>{});
+  const int lanes = D / 8;
+  const auto with = [&](auto L) {
+    if (lanes == L)
+      f(L, std::true_type{});
+    else
+      f(L, std::false_type{});
+  };
+  if (lanes > 16)
+    with(std::integral_constant<int, 32>{});
+  else if (lanes > 8)
+    with(std::integral_constant<int, 16>{});
   else
-    f(std::integral_constant<int, 8>{});
+    with(std::integral_constant<int, 8>{});
 }
 
 }  // namespace
@@ -514,12 +533,13 @@ int moe_qk_norm_rope(int32_t N, int32_t D, int32_t rotary_dim, int32_t interleav
   const dim3 grid(c.token_parts, c.head_parts);
   const int smem = 2 * s.tile * rotary_dim * 4;
   mark_before(MOE_KERNEL_QK_NORM_ROPE, stream);
-  with_lanes(D, [&](auto lanes) {
+  with_lanes(D, [&](auto lanes, auto full) {
     constexpr int L = decltype(lanes)::value;
+    constexpr bool FULL = decltype(full)::value;
     if (dtype == MOE_BF16)
-      rope_forward_kernel<__nv_bfloat16, L><<<grid, kThreads, smem, stream>>>(s, sq, sk);
+      rope_forward_kernel<__nv_bfloat16, L, FULL><<<grid, kThreads, smem, stream>>>(s, sq, sk);
     else
-      rope_forward_kernel<float, L><<<grid, kThreads, smem, stream>>>(s, sq, sk);
+      rope_forward_kernel<float, L, FULL><<<grid, kThreads, smem, stream>>>(s, sq, sk);
   });
   const cudaError_t err = cudaGetLastError();
   mark_after(MOE_KERNEL_QK_NORM_ROPE, stream);
@@ -561,15 +581,16 @@ int moe_qk_norm_rope_backward(int32_t N, int32_t D, int32_t rotary_dim, int32_t 
   const dim3 grid(c.token_parts, c.head_parts);
   const int smem = 2 * s.tile * rotary_dim * 4;
   mark_before(MOE_KERNEL_QK_NORM_ROPE_BWD, stream);
-  with_lanes(D, [&](auto lanes) {
+  with_lanes(D, [&](auto lanes, auto full) {
     constexpr int L = decltype(lanes)::value;
+    constexpr bool FULL = decltype(full)::value;
     using B = __nv_bfloat16;
     if (dtype == MOE_F32)
-      rope_backward_kernel<float, float, L><<<grid, kThreads, smem, stream>>>(s, sq, sk, partial);
+      rope_backward_kernel<float, float, L, FULL><<<grid, kThreads, smem, stream>>>(s, sq, sk, partial);
     else if (dy_dtype == MOE_F32)
-      rope_backward_kernel<B, float, L><<<grid, kThreads, smem, stream>>>(s, sq, sk, partial);
+      rope_backward_kernel<B, float, L, FULL><<<grid, kThreads, smem, stream>>>(s, sq, sk, partial);
     else
-      rope_backward_kernel<B, B, L><<<grid, kThreads, smem, stream>>>(s, sq, sk, partial);
+      rope_backward_kernel<B, B, L, FULL><<<grid, kThreads, smem, stream>>>(s, sq, sk, partial);
   });
   int launches = 1;
   // rows of partial: two for each block, or, if either side has a weight for each head, one for
