@@ -164,10 +164,10 @@ __device__ __forceinline__ int bound_of(const Packed& q, int j) {
 // Reports offsets that break the rules (one block of the grid calls this).
 __device__ __forceinline__ void check_offsets(const Packed& q, int* dev_status) {
   if (!q.off || !dev_status) return;
-  int bad = threadIdx.x == 0 && q.off[0] != 0;
+  bool bad = q.off[0] != 0;
   for (int s = threadIdx.x; s < q.n_seq; s += blockDim.x)
     bad |= q.off[s] > q.off[s + 1] || q.off[s] < 0 || q.off[s + 1] > q.N;
-  if (__syncthreads_or(bad) && threadIdx.x == 0) atomicCAS(dev_status, 0, MOE_ERR_BAD_INDEX);
+  if (bad) atomicCAS(dev_status, 0, MOE_ERR_BAD_INDEX);
 }
 
 // Part p of `parts` begins with the first sequence that begins at or after row p N / parts: its
@@ -289,6 +289,16 @@ __device__ __forceinline__ void append(Pair<CH>& s, const Pair<CH>& p) {
   const Vec<CH> A = s.A * p.A;
   s.A = s.cut() || p.cut() ? all<CH>(-1.f) : A;
   follow(s.H, p);
+}
+
+// The clusters' barriers wait for no memory: the first one orders the set-up of the mbarriers, which has
+// a fence of its own, the last one nothing (waiting for the copies and stores in flight there cost 1 us
+// of a launch).
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // What the warps of a block and the blocks of a cluster exchange.  Step n uses the buffers n % 2
@@ -518,8 +528,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int d = (blockIdx.y * 32 + lane) * CH;
   const bool on = d < p.D;
   const long long D = p.D;
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seq, p.dev_status);
+  exchange_init(xch);
+  if (p.cluster > 1) cluster_arrive();  // (its way there and back, while the bounds come)
   const Packed seq = near(p.seq, bounds);
+  if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(seq, p.dev_status);
   const Cut from = part_begin(seq, part, p.parts);
   const int lo = from.row, hi = part_begin(seq, part + 1, p.parts).row;
   const int base = lo / kTile * kTile, step = kTile * p.cluster;
@@ -529,11 +541,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (ASYNC && lane == 0 && it < steps)
       load_tile<2>(ring, xch.loaded, p.maps, it, blockIdx.y * 32 * CH, tile_row(it));
   };
-  exchange_init(xch);
-  if (p.cluster > 1) cluster_sync();  // every block runs, its barriers set, before one sends
+  if (warp == kWarps)
+    for (int it = 0; it < kStages; ++it) load(it);
+  if (p.cluster > 1) cluster_wait();  // every block runs, its barriers set, before one sends
 
   if (warp == kWarps) {  // joins the warps, and has the tiles loaded
-    for (int it = 0; it < kStages; ++it) load(it);
     for (int it = 0; it < steps; ++it) {
       wait_for(&xch.formed[it & 1], it >> 1 & 1, &xch.abort, p.dev_status);
       join_warps<false>(xch, blocks, it, rank, p.cluster, lane);
@@ -635,7 +647,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   __syncwarp();
-  if (p.cluster > 1) cluster_sync();  // no block leaves while another may still write to it
+  if (p.cluster > 1) {  // no block leaves while another may still write to it
+    cluster_arrive();
+    cluster_wait();
+  }
 }
 
 // ------------------------------------------------------------------ backward
@@ -679,8 +694,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int d = (blockIdx.y * 32 + lane) * CH;
   const bool on = d < p.D;
   const long long D = p.D;
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seq, p.dev_status);
+  exchange_init(xch);
+  if (p.cluster > 1) cluster_arrive();  // (its way there and back, while the bounds come)
   const Packed seq = near(p.seq, bounds);
+  if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(seq, p.dev_status);
   const Cut until = part_begin(seq, part + 1, p.parts);
   const int lo = part_begin(seq, part, p.parts).row, hi = until.row;
   const int top = (hi + kTile - 1) / kTile * kTile, step = kTile * p.cluster;
@@ -690,11 +707,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (ASYNC && lane == 0 && it < steps)
       load_tile<3>(ring, xch.loaded, p.maps, it, blockIdx.y * 32 * CH, tile_row(it));
   };
-  exchange_init(xch);
-  if (p.cluster > 1) cluster_sync();  // every block runs, its barriers set, before one sends
+  if (warp == kWarps)
+    for (int it = 0; it < kStages; ++it) load(it);
+  if (p.cluster > 1) cluster_wait();  // every block runs, its barriers set, before one sends
 
   if (warp == kWarps) {  // joins the gradient's pairs of the warps, and has the tiles loaded
-    for (int it = 0; it < kStages; ++it) load(it);
     for (int it = 0; it < steps; ++it) {
       wait_for(&xch.formed[it & 1], it >> 1 & 1, &xch.abort, p.dev_status);
       join_warps<true>(xch, blocks, it, rank, p.cluster, lane);
@@ -751,6 +768,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int t0 = tile_row(it) + warp * kRows;
       Marks& m = xch.marks[buf][warp];
       walk.mark(seq, t0, lane, m, s.firsts, s.lasts);
+      Vec<CH> early_s = all<CH>(0.f), early_g = early_s;
+      if (s.firsts) early_s = state_before(m, __ffs(s.firsts) - 1);
+      if (s.lasts) early_g = grad_after(m, 31 - __clz(s.lasts));
       uint32_t *g = tile_at<3>(ring, form_tile.at, 0) + warp * kRows * 32 + lane,
                *x = tile_at<3>(ring, form_tile.at, 1) + warp * kRows * 32 + lane,
                *dh = tile_at<3>(ring, form_tile.at, 2) + warp * kRows * 32 + lane;
@@ -788,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (const unsigned firsts = s.firsts) {  // again, from the initial states
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-          if (firsts >> r & 1) fwd.H = state_before(m, r);
+          if (firsts >> r & 1) fwd.H = firsts & ((1 << r) - 1) ? state_before(m, r) : early_s;
           fwd.H = fma(a[r], fwd.H, input(r));
         }
         fwd.A = all<CH>(-1.f);
@@ -796,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (const unsigned lasts = s.lasts) {  // again, from the final states' gradients
 #pragma unroll
         for (int r = kRows - 1; r >= 0; --r) {
-          if (lasts >> r & 1) rev.H = grad_after(m, r);
+          if (lasts >> r & 1) rev.H = lasts >> r > 1 ? grad_after(m, r) : early_g;
           rev.H = a[r] * (of_word<T, CH>(dh[r * 32]) + rev.H);
         }
         rev.A = all<CH>(-1.f);
@@ -882,7 +902,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   __syncwarp();
-  if (p.cluster > 1) cluster_sync();  // no block leaves while another may still write to it
+  if (p.cluster > 1) {  // no block leaves while another may still write to it
+    cluster_arrive();
+    cluster_wait();
+  }
 }
 
 // ------------------------------------------------------------------ one token
