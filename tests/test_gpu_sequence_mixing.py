@@ -863,6 +863,75 @@ def test_training_passes_back_to_back_on_two_states(N, D, lengths, dtype):
         assert all(torch.equal(ins[n], before[n]) for n in ins)
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_keep_the_order_of_their_stream(captured):
+    """Launches are set up while the kernels before them end; what they read and write is still in
+    the stream's order, among themselves and with other kernels: a long chain in which every call
+    uses what the one before it wrote, and writes what that one read, has the bits of the same chain
+    with a wait after every call."""
+    B, H, D, N = 3, 2, 64, 300
+    f, W = moe.MOE_F32, 2 * 64
+    gen = torch.Generator().manual_seed(21)
+    freq = (1e4 ** -(torch.arange(0, D, 2, dtype=torch.float64) / D)).cuda()
+    pos = torch.arange(N, dtype=torch.int32).cuda()
+    w = torch.rand(D, generator=gen).cuda() + 0.5
+    r = lambda *s: torch.randn(s, generator=gen).cuda()  # noqa: E731
+    first = dict(x=r(N, H, D), y=r(N, H, D), g=-r(N, W).abs(), h=r(N, W), h_T=r(1, W),
+                 c=r((N + 63) // 64, W), dg=r(N, W), dx=r(N, H, D), dw=r(D), st=r(4, W),
+                 hs=r(2, W), S=r(B, H, D, D), q=r(B, H, D).to(BF), k=r(B, H, D).to(BF),
+                 v=r(B, H, D).to(BF), o=r(B, H, D).to(BF), o2=r(B, H, D).to(BF),
+                 beta=torch.sigmoid(r(B, H)), gg=-r(B, H).abs())
+    ws = torch.empty(moe.moe_qk_norm_rope_backward_workspace_size(N, D, H, 0), dtype=torch.uint8,
+                     device="cuda")
+
+    def chain(b, wait):
+        x, y, dx = b["x"], b["y"], b["dx"]
+        calls = [
+            lambda: moe.moe_qk_norm_rope(N, D, D, False, f, 1e-6, pos, freq,
+                                         dict(x=x, y=y, weight=w), None),
+            lambda: moe.moe_glr_forward(N, W, 1, None, 1, f, b["g"], y.view(N, W), b["h_T"], b["h"],
+                                        b["h_T"], b["c"]),
+            lambda: moe.moe_glr_backward(N, W, 1, None, 1, f, b["g"], y.view(N, W), None, b["c"],
+                                         b["h"], b["h_T"], b["dg"], dx.view(N, W), None),
+            lambda: moe.moe_qk_norm_rope_backward(N, D, D, False, f, f, 1e-6, pos, freq,
+                                                  dict(x=x, dy=dx, dx=y, weight=w,
+                                                       dweight=b["dw"]), None, ws),
+            lambda: x.add_(y, alpha=0.01),
+            lambda: b["dg"].clamp_(max=0),
+            lambda: moe.moe_glr_step(2, W, 1, f, b["dg"][:2], x.view(N, W)[:2], None, 4, b["st"],
+                                     b["hs"]),
+            lambda: moe.moe_gdr_step(B, H, D, D, b["q"], b["k"], b["v"], b["beta"], b["gg"], None, B,
+                                     0.125, b["S"], b["o"]),
+            lambda: moe.moe_gdr_step(B, H, D, D, b["o"], b["k"], b["v"], b["beta"], b["gg"], None, B,
+                                     0.125, b["S"], b["o2"]),
+            lambda: b["q"].copy_(b["o2"]).add_(1),
+            lambda: b["v"].copy_(b["o"]).sub_(1),
+            lambda: b["g"].copy_(b["dg"]).sub_(0.1),
+        ]
+        for _ in range(12):
+            for call in calls:
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+
+    want = {n: t.clone() for n, t in first.items()}
+    chain(want, True)
+    torch.cuda.synchronize()
+    got = {n: t.clone() for n, t in first.items()}
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            chain(got, False)
+        for n, t in first.items():
+            got[n].copy_(t)
+        graph.replay()
+    else:
+        chain(got, False)
+    torch.cuda.synchronize()
+    for n in got:
+        assert torch.equal(got[n].view(torch.int16), want[n].view(torch.int16)), n
+
+
 FIRST_CALL = """
 import torch
 from top_routing_grouped_gemm_gb300 import moe

@@ -1,5 +1,6 @@
 // One token of the gated delta rule for a batch of requests (include/linear_attention.h).
 #include "moe_internal.h"
+#include "overlap.cuh"
 #include "slots.cuh"
 
 #include "../../include/linear_attention.h"
@@ -63,6 +64,7 @@ __global__ void __launch_bounds__(kThreads)
   const int lane = threadIdx.x & 31, place = threadIdx.x % W;
   const int first = part * kBlockRows + threadIdx.x / W * kRows;  // value row
 
+  after_previous();
   const int row = slot ? slot[b] : b;
   float qv[4], kv[4];
   load4(q + bh * DK + place * 4, qv);
@@ -135,14 +137,11 @@ extern "C" int moe_gdr_step(int32_t B, int32_t H, int32_t dk, int32_t dv, const 
   mark_before(MOE_KERNEL_GDR_STEP, stream);
   const auto launch = [&](auto kernel, int lanes) {
     const int parts = dv / (kThreads / lanes * kRows);
-    kernel<<<static_cast<unsigned>(B) * H * parts, kThreads, 0, stream>>>(
-        H, dv, q_, k_, v_, beta, g, slot, n_slots, scale, S, o_, dev_status);
+    return launch_behind(kernel, dim3(static_cast<unsigned>(B) * H * parts), kThreads, 0, stream, H, dv,
+                         q_, k_, v_, beta, g, slot, n_slots, scale, S, o_, dev_status);
   };
-  if (dk == 128)
-    launch(gdr_step_kernel<128>, 32);
-  else
-    launch(gdr_step_kernel<64>, 16);
-  const cudaError_t err = cudaGetLastError();
+  const cudaError_t err =
+      dk == 128 ? launch(gdr_step_kernel<128>, 32) : launch(gdr_step_kernel<64>, 16);
   mark_after(MOE_KERNEL_GDR_STEP, stream);
   count_launches(1);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

@@ -6,6 +6,7 @@
 #include <type_traits>
 
 #include "moe_internal.h"
+#include "overlap.cuh"
 #include "ptx.cuh"
 #include "slots.cuh"
 
@@ -530,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const long long D = p.D;
   exchange_init(xch);
   if (p.cluster > 1) cluster_arrive();  // (its way there and back, while the bounds come)
+  after_previous();
   const Packed seq = near(p.seq, bounds);
   if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(seq, p.dev_status);
   const Cut from = part_begin(seq, part, p.parts);
@@ -696,6 +698,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const long long D = p.D;
   exchange_init(xch);
   if (p.cluster > 1) cluster_arrive();  // (its way there and back, while the bounds come)
+  after_previous();
   const Packed seq = near(p.seq, bounds);
   if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(seq, p.dev_status);
   const Cut until = part_begin(seq, part + 1, p.parts);
@@ -946,6 +949,7 @@ __global__ void __launch_bounds__(kStepThreads)
                     const int* slot, int n_slots, float* state, T* h, int* dev_status) {
   const int b = blockIdx.y, d = (blockIdx.x * kStepThreads + threadIdx.x) * V;
   const bool on = d < D;
+  after_previous();
   const int row = slot ? slot[b] : b;
   float lg[V], xv[V], s[V];
   if (on) {
@@ -1060,9 +1064,9 @@ int launch(int N, int D, int n_seq, Args& args, cudaStream_t stream) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = dynamic_bytes<CH>(ARRAYS, cluster);
   cfg.stream = stream;
-  cudaLaunchAttribute attr = cluster_of(cluster);
-  cfg.attrs = &attr;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  cudaLaunchAttribute attrs[2] = {behind_previous(), cluster_of(cluster)};
+  cfg.attrs = attrs;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, KERNEL, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -1171,11 +1175,12 @@ int moe_glr_step(int32_t B, int32_t D, int32_t mode, int32_t dtype, const void* 
   const int width = kStepThreads * (four ? 4 : 1);
   const dim3 grid((D + width - 1) / width, B);
   mark_before(MOE_KERNEL_GLR_STEP, stream);
+  cudaError_t err = cudaSuccess;
   const auto run = [&](auto type, auto mix, auto v) {
     using T = decltype(type);
-    glr_step_kernel<T, decltype(mix)::value, decltype(v)::value><<<grid, kStepThreads, 0, stream>>>(
-        D, static_cast<const T*>(g), ld_g, static_cast<const T*>(x), ld_x, slot, n_slots, state,
-        static_cast<T*>(h), dev_status);
+    err = launch_behind(glr_step_kernel<T, decltype(mix)::value, decltype(v)::value>, grid, kStepThreads,
+                        0, stream, D, static_cast<const T*>(g), ld_g, static_cast<const T*>(x), ld_x,
+                        slot, n_slots, state, static_cast<T*>(h), dev_status);
   };
   const auto with_width = [&](auto type, auto mix) {
     if (four)
@@ -1193,7 +1198,6 @@ int moe_glr_step(int32_t B, int32_t D, int32_t mode, int32_t dtype, const void* 
     with_mode(__nv_bfloat16{});
   else
     with_mode(float{});
-  const cudaError_t err = cudaGetLastError();
   mark_after(MOE_KERNEL_GLR_STEP, stream);
   count_launches(1);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

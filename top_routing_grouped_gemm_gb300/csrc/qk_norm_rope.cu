@@ -7,6 +7,7 @@
 #include <type_traits>
 
 #include "moe_internal.h"
+#include "overlap.cuh"
 #include "ptx.cuh"
 
 #include "../../include/linear_attention.h"
@@ -218,6 +219,7 @@ template <typename T, int L, bool FULL>
 __global__ void __launch_bounds__(kThreads, kForwardBlocks)
     rope_forward_kernel(const Shape s, const Side q, const Side k) {
   extern __shared__ float4 table[];  // [2][tile][rot / 4]
+  after_previous();
   const Angles angles(s);
   const Lane<L, FULL> me(s, q.heads + k.heads);
   const Side& side = me.head < q.heads ? q : k;
@@ -275,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
     rope_backward_kernel(const Shape s, const Side q, const Side k, float* partial) {
   extern __shared__ float4 table[];  // [2][tile][rot / 4]
   __shared__ float sums[kThreads * 8];  // [group][D]
+  after_previous();
   const Angles angles(s);
   const int heads = q.heads + k.heads;
   const Lane<L, FULL> me(s, heads);
@@ -359,16 +362,27 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks)
   }
 }
 
-// dweight from the blocks' sums: output row b of D values is the sum of rows b + j + i `step` of
-// partial, j < inner, i < outer.  32 columns to a block; its 32 warps take every 32nd row each and
-// are then added in order.
+// The weight gradients of one side from the blocks' sums: row b of its `rows` (of D values) is the sum
+// of rows b + j + i `step` of `from`, j < inner, i < outer.
+struct Sums {
+  const float* from;
+  float* dweight;
+  int rows, outer, inner;
+};
+
+// 32 columns of one row, of q or of k, to a block; its 32 warps take every 32nd of the rows to add each
+// and are then added in order.
 __global__ void __launch_bounds__(1024)
-    rope_dweight_kernel(const float* partial, int outer, int inner, int step, int D,
-                        float* dweight) {
+    rope_dweight_kernel(const Sums q, const Sums k, int step, int D) {
   __shared__ float sums[32][33];
+  after_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane;
-  const float* from = partial + static_cast<long long>(blockIdx.y) * D + i;
+  const bool of_k = static_cast<int>(blockIdx.y) >= q.rows;
+  const Sums& side = of_k ? k : q;
+  const long long row = blockIdx.y - (of_k ? q.rows : 0);
+  const float* from = side.from + row * D + i;
+  const int outer = side.outer, inner = side.inner;
   float sum = 0.f;
   if (i < D)
 #pragma unroll 4
@@ -379,7 +393,7 @@ __global__ void __launch_bounds__(1024)
   if (warp) return;
 #pragma unroll
   for (int v = 1; v < 32; ++v) sum += sums[v][lane];
-  if (i < D) dweight[static_cast<long long>(blockIdx.y) * D + i] = sum;
+  if (i < D) side.dweight[row * D + i] = sum;
 }
 
 // ------------------------------------------------------------------------ host side
@@ -533,15 +547,17 @@ int moe_qk_norm_rope(int32_t N, int32_t D, int32_t rotary_dim, int32_t interleav
   const dim3 grid(c.token_parts, c.head_parts);
   const int smem = 2 * s.tile * rotary_dim * 4;
   mark_before(MOE_KERNEL_QK_NORM_ROPE, stream);
+  cudaError_t err = cudaSuccess;
   with_lanes(D, [&](auto lanes, auto full) {
     constexpr int L = decltype(lanes)::value;
     constexpr bool FULL = decltype(full)::value;
     if (dtype == MOE_BF16)
-      rope_forward_kernel<__nv_bfloat16, L, FULL><<<grid, kThreads, smem, stream>>>(s, sq, sk);
+      err = launch_behind(rope_forward_kernel<__nv_bfloat16, L, FULL>, grid, kThreads, smem, stream,
+                          s, sq, sk);
     else
-      rope_forward_kernel<float, L, FULL><<<grid, kThreads, smem, stream>>>(s, sq, sk);
+      err = launch_behind(rope_forward_kernel<float, L, FULL>, grid, kThreads, smem, stream,
+                          s, sq, sk);
   });
-  const cudaError_t err = cudaGetLastError();
   mark_after(MOE_KERNEL_QK_NORM_ROPE, stream);
   count_launches(1);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -581,34 +597,39 @@ int moe_qk_norm_rope_backward(int32_t N, int32_t D, int32_t rotary_dim, int32_t 
   const dim3 grid(c.token_parts, c.head_parts);
   const int smem = 2 * s.tile * rotary_dim * 4;
   mark_before(MOE_KERNEL_QK_NORM_ROPE_BWD, stream);
+  cudaError_t err = cudaSuccess;
   with_lanes(D, [&](auto lanes, auto full) {
     constexpr int L = decltype(lanes)::value;
     constexpr bool FULL = decltype(full)::value;
     using B = __nv_bfloat16;
     if (dtype == MOE_F32)
-      rope_backward_kernel<float, float, L, FULL><<<grid, kThreads, smem, stream>>>(s, sq, sk, partial);
+      err = launch_behind(rope_backward_kernel<float, float, L, FULL>, grid, kThreads, smem, stream,
+                          s, sq, sk, partial);
     else if (dy_dtype == MOE_F32)
-      rope_backward_kernel<B, float, L, FULL><<<grid, kThreads, smem, stream>>>(s, sq, sk, partial);
+      err = launch_behind(rope_backward_kernel<B, float, L, FULL>, grid, kThreads, smem, stream,
+                          s, sq, sk, partial);
     else
-      rope_backward_kernel<B, B, L, FULL><<<grid, kThreads, smem, stream>>>(s, sq, sk, partial);
+      err = launch_behind(rope_backward_kernel<B, B, L, FULL>, grid, kThreads, smem, stream,
+                          s, sq, sk, partial);
   });
-  int launches = 1;
-  // rows of partial: two for each block, or, if either side has a weight for each head, one for
-  // each head (a shared weight's are then added over its heads)
-  const bool by_head = sq.w_hs || sk.w_hs;
-  const auto reduce = [&](float* dw, int side, int first, int n, bool per_head) {
-    const dim3 blocks((D + 31) / 32, per_head ? n : 1);
-    const float* from = partial + static_cast<size_t>(by_head ? first : side) * D;
-    const int outer = by_head ? c.token_parts : c.token_parts * c.head_parts;
-    rope_dweight_kernel<<<blocks, 1024, 0, stream>>>(from, outer, by_head && !per_head ? n : 1,
-                                                     by_head ? heads : 2, D, dw);
-    ++launches;
-  };
-  if (q->dweight) reduce(q->dweight, 0, 0, sq.heads, q->weight_per_head != 0);
-  if (k && k->dweight) reduce(k->dweight, 1, sq.heads, sk.heads, k->weight_per_head != 0);
-  const cudaError_t err = cudaGetLastError();
+  if (weights) {
+    // rows of partial: two for each block, or, if either side has a weight for each head, one for
+    // each head (a shared weight's are then added over its heads)
+    const bool by_head = sq.w_hs || sk.w_hs;
+    const auto sums = [&](const moe_qk_grads* side, int place, int first_head) {
+      if (!side || !side->dweight) return Sums{};
+      return Sums{partial + static_cast<size_t>(by_head ? first_head : place) * D, side->dweight,
+                  side->weight_per_head ? side->heads : 1,
+                  by_head ? c.token_parts : c.token_parts * c.head_parts,
+                  by_head && !side->weight_per_head ? side->heads : 1};
+    };
+    const Sums of_q = sums(q, 0, 0), of_k = sums(k, 1, sq.heads);
+    if (err == cudaSuccess)
+      err = launch_behind(rope_dweight_kernel, dim3((D + 31) / 32, of_q.rows + of_k.rows), 1024, 0,
+                          stream, of_q, of_k, by_head ? heads : 2, D);
+  }
   mark_after(MOE_KERNEL_QK_NORM_ROPE_BWD, stream);
-  count_launches(launches);
+  count_launches(weights ? 2 : 1);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
