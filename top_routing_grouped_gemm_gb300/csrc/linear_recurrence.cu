@@ -26,8 +26,8 @@ constexpr int kBounds = 512;    // bounds of sequences that a block keeps in sha
 
 // ------------------------------------------------------------------ what a lane works on
 //
-// CH channels of one row: two bf16 (one 4-byte word), one bf16 (rows that are not 16-byte
-// aligned) or one fp32; a warp covers 32 CH neighbouring channels.  Two channels are worked on by
+// CH channels of one row: two bf16 (one 4-byte word), one bf16 (rows that do not begin on 4-byte
+// boundaries) or one fp32; a warp covers 32 CH neighbouring channels.  Two channels are worked on by
 // packed fp32 instructions, which halve the issue slots that bound these kernels.
 template <int CH>
 struct Vec;
@@ -455,15 +455,20 @@ __device__ __forceinline__ void drain(uint64_t* loaded, int steps) {
 }
 
 // A warp's rows from row t0, those outside [lo, hi) as zeros; words[r 32] is row r's.
-template <typename T>
+template <int CH, typename T>
 __device__ __forceinline__ void copy_rows(uint32_t* words, const T* base, long long stride, int t0,
                                           int lo, int hi, bool on) {
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     uint32_t bits = 0;
     if (on && t0 + r >= lo && t0 + r < hi) {
-      const T v = base[(t0 + r) * stride];
-      memcpy(&bits, &v, sizeof v);
+      const T* from = base + (t0 + r) * stride;
+      if constexpr (CH * sizeof(T) == 4) {
+        bits = __ldg(reinterpret_cast<const uint32_t*>(from));
+      } else {
+        const T v = *from;
+        memcpy(&bits, &v, sizeof v);
+      }
     }
     words[r * 32] = bits;
   }
@@ -495,12 +500,12 @@ __device__ __forceinline__ void hand_on_empty(const Packed& q, const float* from
 
 // ------------------------------------------------------------------ forward
 //
-// g and x are read once and h is written once.  32768 x 2048 bf16 take 72.5 us, 0.83 of the rate of
-// a plain copy (16276 x 2048 fp32 64.8 us, 0.92): what holds the bf16 form back is waiting, between
+// g and x are read once and h is written once.  32768 x 2048 bf16 take 70.2 us, 0.86 of the rate of
+// a plain copy (16276 x 2048 fp32 63.9 us, 0.94): what holds the bf16 form back is waiting, between
 // instructions (two channels to unpack and gate for each word) and for the other blocks, with 50 %
-// of the issue slots used.  24 sequences in as many rows take 83 us, as tiles with bounds go through
-// a path of their own.  16 rows to a warp, without the pairs of the next tile in between, take 70 us
-// and 90 us.
+// of the issue slots used.  24 sequences in as many rows take 82 us, as tiles with bounds go through
+// a path of their own.  (16 rows to a warp, without the pairs of the next tile in between, took 69.6 us
+// where this form then took 72.6, but 90 us where it took 83 with 24 sequences.)
 
 template <typename T>
 struct ForwardArgs {
@@ -583,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           fence_proxy_async_smem();  // TMA writes these words next
         }
       } else {
-        copy_rows(g, p.g + d, p.ld_g, t0, lo, hi, on);
-        copy_rows(x, p.x + d, p.ld_x, t0, lo, hi, on);
+        copy_rows<CH>(g, p.g + d, p.ld_g, t0, lo, hi, on);
+        copy_rows<CH>(x, p.x + d, p.ld_x, t0, lo, hi, on);
       }
       Pair<CH> pair{all<CH>(1.f), all<CH>(0.f)};
 #pragma unroll
@@ -663,10 +668,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 // block, by pairs of their own.
 //
 // g, x and dh are read once and dg and dx are written once.  8192 x 4096 bf16 in 6 sequences, mixed,
-// take 81 us after the forward's 45 us (126.5 us together, 0.63 of a copy's rate), bound by
-// instructions: 63 % of the issue slots, 75 % of the busiest scheduler's.  The gates are formed
+// take 79 us after the forward's 45 us (123.7 us together, 0.65 of a copy's rate), bound by
+// instructions: 66 % of the issue slots, 79 % of the busiest scheduler's.  The gates are formed
 // twice; holding them in registers until the pairs are known leaves no room for the overlap of two
-// tiles and takes 130 us in all.
+// tiles (4 us more).
 
 template <typename T>
 struct BackwardArgs {
@@ -786,9 +791,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           fence_proxy_async_smem();  // TMA writes these words next
         }
       } else {
-        copy_rows(g, p.g + d, p.ld_g, t0, lo, hi, on);
-        copy_rows(x, p.x + d, p.ld_x, t0, lo, hi, on);
-        copy_rows(dh, p.dh + d, D, t0, lo, hi, on);
+        copy_rows<CH>(g, p.g + d, p.ld_g, t0, lo, hi, on);
+        copy_rows<CH>(x, p.x + d, p.ld_x, t0, lo, hi, on);
+        copy_rows<CH>(dh, p.dh + d, D, t0, lo, hi, on);
       }
       Vec<CH> a[kRows], om[MIX ? kRows : 1];
       gates(g, a, om);
@@ -938,8 +943,9 @@ __device__ __forceinline__ void set(__nv_bfloat16* p, const float (&v)[1]) {
   *p = __float2bfloat16_rn(v[0]);
 }
 
-// V channels to a thread; 64 requests x 4096 channels take 3.6 us, a launch and two dependent round
-// trips to memory, 512 requests 6.9 us (0.64 of a copy's rate).  Gates and inputs are on their way while the request's row is looked up,
+// V channels to a thread; 64 requests x 4096 channels take 1.8 us in a graph of such steps, two
+// dependent round trips to memory, 512 requests 6.6 us (0.66 of a copy's rate).  Gates and inputs are
+// on their way while the request's row is looked up,
 // and the state while the requests before it are searched for the same row.
 constexpr int kStepThreads = 128;
 
@@ -1071,7 +1077,8 @@ int launch(int N, int D, int n_seq, Args& args, cudaStream_t stream) {
 }
 
 // Calls f(T{}, channels per lane, mode, ASYNC) for the call's type.  Tensors whose rows all begin
-// on 16-byte boundaries (and do not share one row) are copied by TMA.
+// on 16-byte boundaries (and do not share one row) are copied by TMA; a lane has two bf16 where they
+// all begin on 4-byte boundaries (8191 x 2046, forward: 62 us with one, 37 us with two).
 template <typename F>
 int dispatch(int mode, int dtype, std::initializer_list<const void*> ptrs,
              std::initializer_list<long long> strides, F f) {
@@ -1079,9 +1086,9 @@ int dispatch(int mode, int dtype, std::initializer_list<const void*> ptrs,
   using One = integral_constant<int, 1>;
   using Two = integral_constant<int, 2>;
   const int size = dtype == MOE_F32 ? 4 : 2;
-  bool aligned = true;
-  for (const void* q : ptrs) aligned = aligned && !misaligned(q, 16);
-  for (long long s : strides) aligned = aligned && s > 0 && s * size % 16 == 0;
+  bool aligned = true, even = true;
+  for (const void* q : ptrs) aligned = aligned && !misaligned(q, 16), even = even && !misaligned(q, 4);
+  for (long long s : strides) aligned = aligned && s > 0 && s * size % 16 == 0, even = even && s % 2 == 0;
   const auto with_mode = [&](auto type, auto ch, auto async) {
     return mode == MOE_GLR_MIX ? f(type, ch, std::true_type{}, async)
                                : f(type, ch, std::false_type{}, async);
@@ -1089,8 +1096,9 @@ int dispatch(int mode, int dtype, std::initializer_list<const void*> ptrs,
   if (dtype == MOE_F32)
     return aligned ? with_mode(float{}, One{}, std::true_type{})
                    : with_mode(float{}, One{}, std::false_type{});
-  return aligned ? with_mode(__nv_bfloat16{}, Two{}, std::true_type{})
-                 : with_mode(__nv_bfloat16{}, One{}, std::false_type{});
+  if (aligned) return with_mode(__nv_bfloat16{}, Two{}, std::true_type{});
+  return even ? with_mode(__nv_bfloat16{}, Two{}, std::false_type{})
+              : with_mode(__nv_bfloat16{}, One{}, std::false_type{});
 }
 
 }  // namespace

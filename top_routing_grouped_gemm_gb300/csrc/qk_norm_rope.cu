@@ -210,9 +210,9 @@ __device__ __forceinline__ void load_weight(const Side& side, int h, const Lane<
                        : 1.f;
 }
 
-// Every row is read and written once: 32768 tokens x 32 heads x 128 bf16 take 91.3 us, 0.88 of the
-// rate of a plain copy (94 us with addresses from each row's index, which cost instructions that
-// these 64-bit steps do not).  Two or three rows on their way instead of four, and three or five blocks
+// Every row is read and written once: 32768 tokens x 32 heads x 128 bf16 take 89.8 us, 0.89 of the
+// rate of a plain copy, with 63 % of the issue slots used (2.5 us more with addresses from each row's
+// index, which cost instructions that these 64-bit steps do not).  Two or three rows on their way instead of four, and three or five blocks
 // to an SM instead of kForwardBlocks, take 5 to 12 % longer; partners in other lanes, with shuffles,
 // and blocks in several waves took 131 us.
 template <typename T, int L, bool FULL>
@@ -267,8 +267,8 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks)
   }
 }
 
-// x and dy are read once and dx is written once; with dy in fp32 the same rows take 179 us, 0.89 of
-// the rate of a copy (fewer rows on their way or more blocks to an SM: 187 to 199 us).  The weights'
+// x and dy are read once and dx is written once; with dy in fp32 the same rows take 173.5 us, 0.93
+// of the rate of a copy (fewer rows on their way or more blocks to an SM: 5 to 11 % longer).  The weights'
 // gradients stay in registers over all of a block's tokens, and no atomic orders their sums.
 // partial: [blocks][2][D] (the shared weights of q and k) or [gridDim.x][heads][D] (a row for each
 // head), the sums of the block's rows; null: not wanted.
