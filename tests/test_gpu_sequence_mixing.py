@@ -525,6 +525,44 @@ def test_norm_rope_past_2_to_31_values():
 
 # ---------------------------------------------------------------- single tokens
 
+@pytest.mark.parametrize("D, few, dtype", [(1 << 20, 64, BF), ((1 << 20) - 1, 63, BF),
+                                           ((1 << 20) - 3, 63, F32)])
+def test_recurrence_of_the_most_channels(D, few, dtype):
+    """More strips of channels than the GPU has places for, so blocks come in many rounds.  Channels
+    do not see each other: the first and the last of them have the bits that a call with these few
+    alone gives, which the tests above check value by value."""
+    N = 67
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    r = lambda *n: torch.randn(n, generator=gen, device="cuda")  # noqa: E731
+    g = torch.nn.functional.logsigmoid(r(N, D) + 3).to(dtype)
+    x, dh, h0, dh_T = r(N, D).to(dtype), r(N, D).to(dtype), r(2, D), r(2, D)
+    off = torch.tensor([0, 30, N], dtype=torch.int32, device="cuda")
+
+    def run(part):
+        i = [t[:, part].contiguous() for t in (g, x, dh, h0, dh_T)]
+        d = i[0].shape[1]
+        h, dg, dx = (torch.empty((N, d), dtype=dtype, device="cuda") for _ in range(3))
+        h_T, dh0, chunks = (torch.empty((2, d), device="cuda") for _ in range(3))
+        moe.moe_glr_forward(N, d, 2, off, 1, CODE[dtype], i[0], i[1], i[3], h, h_T, chunks)
+        moe.moe_glr_backward(N, d, 2, off, 1, CODE[dtype], i[0], i[1], i[3], chunks, i[2], i[4], dg,
+                             dx, dh0)
+        return h, h_T, chunks, dg, dx, dh0
+
+    every = run(slice(0, D))
+    for part in (slice(0, few), slice(D - few, D)):
+        for got, want in zip(every, run(part)):
+            assert torch.equal(got[:, part], want)
+
+
+@pytest.mark.parametrize("case", [(3, 4096, 0, 8, 0, False, "per_head", BF, "dense"),
+                                  (2, 4000, 96, 24, 16, True, "shared", F32, "fused"),
+                                  (5, 1000, 1000, 64, 64, False, "per_head", BF, "head_major")],
+                         ids=["8", "24", "64"])
+def test_norm_rope_of_many_heads(case):
+    test_norm_rope(case)
+    test_norm_rope_backward(case, True)
+
+
 @pytest.mark.parametrize("mix", [False, True])
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("B, D, n_slots, slots", [(1, 1, 1, False), (5, 33, 5, False),

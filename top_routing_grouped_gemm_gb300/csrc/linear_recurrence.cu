@@ -1044,7 +1044,7 @@ const Room* room_for() {
       r.err = cudaOccupancyMaxActiveClusters(&r.clusters[c], KERNEL, &cfg);
     }
   });
-  return rooms[dev].err == cudaSuccess ? &rooms[dev] : nullptr;
+  return launched(rooms[dev].err) == cudaSuccess ? &rooms[dev] : nullptr;
 }
 
 // Launches KERNEL in as large clusters as can all run at once, up to 8 blocks; where these leave
@@ -1073,7 +1073,7 @@ int launch(int N, int D, int n_seq, Args& args, cudaStream_t stream) {
   cudaLaunchAttribute attrs[2] = {behind_previous(), cluster_of(cluster)};
   cfg.attrs = attrs;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, KERNEL, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launched(cudaLaunchKernelEx(&cfg, KERNEL, args)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 // Calls f(T{}, channels per lane, mode, ASYNC) for the call's type.  Tensors whose rows all begin

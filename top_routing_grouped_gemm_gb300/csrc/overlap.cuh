@@ -24,6 +24,12 @@ inline cudaLaunchAttribute behind_previous() {
   return attr;
 }
 
+// A launch's own error, which is not left behind for a later call to find.
+inline cudaError_t launched(cudaError_t err) {
+  if (err != cudaSuccess) cudaGetLastError();
+  return err;
+}
+
 template <typename... Params, typename... Args>
 cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, int smem,
                           cudaStream_t stream, Args... args) {
@@ -35,7 +41,7 @@ cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, int
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+  return launched(cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...));
 }
 
 }  // namespace moe
