@@ -148,7 +148,7 @@ int moe_qk_norm_rope(int32_t N, int32_t D, int32_t rotary_dim, int32_t interleav
 /* Backward: dx and the weight gradients of <dy, y> (two launches; one if no weight gradient is
  * wanted).  The norm is formed again from x.  dy_dtype: MOE_F32 (what moe_gdr_backward writes)
  * or dtype.  Deterministic: every reduction runs in a fixed order.  The size is 0 where D or the
- * numbers of rows or heads are beyond the limits. */
+ * numbers of rows or heads are not supported. */
 size_t moe_qk_norm_rope_backward_workspace_size(int32_t N, int32_t D, int32_t q_heads,
                                                 int32_t k_heads);
 int moe_qk_norm_rope_backward(int32_t N, int32_t D, int32_t rotary_dim, int32_t interleaved,

@@ -565,8 +565,8 @@ int moe_qk_norm_rope(int32_t N, int32_t D, int32_t rotary_dim, int32_t interleav
 
 size_t moe_qk_norm_rope_backward_workspace_size(int32_t N, int32_t D, int32_t q_heads,
                                                 int32_t k_heads) {
-  if (N <= 0 || N > (1 << 30) || D <= 0 || D > kMaxD || q_heads <= 0 || q_heads > kMaxHeads ||
-      k_heads < 0 || k_heads > kMaxHeads)
+  if (N <= 0 || N > (1 << 30) || D <= 0 || D > kMaxD || D % 8 || q_heads <= 0 ||
+      q_heads > kMaxHeads || k_heads < 0 || k_heads > kMaxHeads)
     return 0;
   return backward_ws(N, D, q_heads, k_heads);
 }
