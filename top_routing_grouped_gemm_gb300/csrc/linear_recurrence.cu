@@ -338,6 +338,16 @@ __device__ __forceinline__ void wait_for(uint64_t* bar, unsigned parity, int* ab
   }
 }
 
+// The same for a barrier that other blocks of the cluster complete: what they wrote is acquired at
+// their scope.
+__device__ __forceinline__ void wait_for_cluster(uint64_t* bar, unsigned parity, int* abort,
+                                                 int* dev_status) {
+  if (!mbar_wait_cluster(bar, parity, abort)) {
+    *reinterpret_cast<volatile int*>(abort) = 1;
+    report_status(dev_status, MOE_ERR_TIMEOUT);
+  }
+}
+
 // One lane's arrival for its warp.
 __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
   __syncwarp();
@@ -413,7 +423,7 @@ template <int CH, int PAIRS>
 __device__ __forceinline__ void join_blocks(Exchange<CH, PAIRS>& x, const Pair<CH>* blocks, int it,
                                             int rank, int cluster, int lane, Vec<CH>& state,
                                             int* dev_status) {
-  wait_for(&x.received[it & 3], it >> 2 & 1, &x.abort, dev_status);
+  wait_for_cluster(&x.received[it & 3], it >> 2 & 1, &x.abort, dev_status);
   Vec<CH> mine = state;
   const Pair<CH>* pairs = &blocks[(it & 3) * cluster * 32 + lane];
 #pragma unroll 4
