@@ -33,3 +33,14 @@ def test_barriers_that_other_blocks_complete_are_waited_for_at_cluster_scope():
     waits = [w for w in waits if "wait" in w]
     assert waits == ["wait_for_cluster"]
     assert "mbar_wait_cluster(" in body(code, "void wait_for_cluster(")
+
+
+def test_warps_converge_before_the_clusters_barriers():
+    """barrier.cluster in its .aligned form is for warps whose threads run it together; before the
+    first wait one thread of a warp has copied tiles on its own."""
+    code = source("linear_recurrence.cu")
+    for name in ("cluster_arrive", "cluster_wait"):
+        text = body(code, f"void {name}(")
+        assert text.index("__syncwarp();") < text.index("barrier.cluster.")
+    # and nothing goes around the two
+    assert len(re.findall(r"barrier\.cluster\.(?:arrive|wait)", code)) == 2

@@ -294,11 +294,13 @@ __device__ __forceinline__ void append(Pair<CH>& s, const Pair<CH>& p) {
 
 // The clusters' barriers wait for no memory: the first one orders the set-up of the mbarriers, which has
 // a fence of its own, the last one nothing (waiting for the copies and stores in flight there cost 1 us
-// of a launch).
+// of a launch).  A warp's threads, one of which may have copied tiles on its own, come there together.
 __device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -663,7 +665,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (it + 1 < steps) finish(it + 1, 0, even);
     }
   }
-  __syncwarp();
   if (p.cluster > 1) {  // no block leaves while another may still write to it
     cluster_arrive();
     cluster_wait();
@@ -919,7 +920,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       now = next;
     }
   }
-  __syncwarp();
   if (p.cluster > 1) {  // no block leaves while another may still write to it
     cluster_arrive();
     cluster_wait();
