@@ -44,3 +44,13 @@ def test_warps_converge_before_the_clusters_barriers():
         assert text.index("__syncwarp();") < text.index("barrier.cluster.")
     # and nothing goes around the two
     assert len(re.findall(r"barrier\.cluster\.(?:arrive|wait)", code)) == 2
+
+
+def test_kernels_set_up_early_read_through_the_coherent_path():
+    """A kernel that is set up while the one before it ends is alive while its inputs may still be
+    written, which loads of data that is read-only for a kernel's life (ld.global.nc) rule out."""
+    early = [f for f in sorted(os.listdir(B.CSRC)) if '#include "overlap.cuh"' in source(f)]
+    assert {"gdr_step.cu", "linear_recurrence.cu", "qk_norm_rope.cu"} <= set(early)
+    for name in early:
+        code = source(name)
+        assert not re.search(r"__ldg\b|\.nc\b|__restrict__", code), name

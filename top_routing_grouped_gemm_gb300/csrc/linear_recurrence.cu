@@ -466,7 +466,8 @@ __device__ __forceinline__ void drain(uint64_t* loaded, int steps) {
     mbar_wait(&loaded[it % kStages], it / kStages & 1, &never);
 }
 
-// A warp's rows from row t0, those outside [lo, hi) as zeros; words[r 32] is row r's.
+// A warp's rows from row t0, those outside [lo, hi) as zeros; words[r 32] is row r's.  (Plain loads: the
+// kernel is alive before the one in front of it has ended, which may still write these rows then.)
 template <int CH, typename T>
 __device__ __forceinline__ void copy_rows(uint32_t* words, const T* base, long long stride, int t0,
                                           int lo, int hi, bool on) {
@@ -476,7 +477,7 @@ __device__ __forceinline__ void copy_rows(uint32_t* words, const T* base, long l
     if (on && t0 + r >= lo && t0 + r < hi) {
       const T* from = base + (t0 + r) * stride;
       if constexpr (CH * sizeof(T) == 4) {
-        bits = __ldg(reinterpret_cast<const uint32_t*>(from));
+        bits = *reinterpret_cast<const uint32_t*>(from);
       } else {
         const T v = *from;
         memcpy(&bits, &v, sizeof v);

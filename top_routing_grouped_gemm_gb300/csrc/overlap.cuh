@@ -2,10 +2,12 @@
 //
 // A kernel launched so begins with after_previous(), before it reads or writes memory of the caller's:
 // there it waits until the kernel before it has ended and its writes are seen, so the stream's order
-// holds as ever; what is saved is the launch itself (0.4 us of a one-token step of 2.3 us in a graph;
-// calls one after the other: 8192 x 4096 recurrence forward + backward 129 -> 124 us, norm + rotation's
-// backward of 32768 x 32 x 128 185 -> 174 us).  No kernel lets the next one in before its own blocks
-// end: those took the first places that came free, unevenly (124 -> 128 us).
+// holds as ever, for plain loads (what is read-only for a kernel's whole life is another matter: no
+// __ldg and no restricted pointers here).  What is saved is the launch itself (0.4 us of a one-token
+// step of 2.3 us in a graph; calls one after the other: 8192 x 4096 recurrence forward + backward
+// 129 -> 124 us, norm + rotation's backward of 32768 x 32 x 128 185 -> 174 us).  No kernel lets the
+// next one in before its own blocks end: those took the first places that came free, unevenly
+// (124 -> 128 us).
 #pragma once
 
 #include <cuda_runtime.h>
