@@ -31,8 +31,9 @@
  * the values' own type; where the rows of all `dtype` tensors begin on 16-byte boundaries they are
  * copied by TMA, which is faster.  Apart from h_T over h0, outputs may not overlap inputs.
  *
- * Waits inside the kernels are bounded; one that runs out ends the waiting of that launch, whose
- * outputs are then wrong, and is reported as MOE_ERR_TIMEOUT in *dev_status.
+ * Waits inside the kernels are bounded; one that runs out ends that launch early, its outputs then
+ * being incomplete, and is reported as MOE_ERR_TIMEOUT in *dev_status.  Nothing of it is under way
+ * any more when it has ended.
  *
  * Precision: states, products and sums are fp32; h, dg and dx are rounded once.  Sequences do
  * not see each other: infinities or NaN in one leave the others alone.  Deterministic: the
@@ -80,6 +81,12 @@ int moe_glr_backward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off
 int moe_glr_step(int32_t B, int32_t D, int32_t mode, int32_t dtype, const void* g, int64_t ld_g,
                  const void* x, int64_t ld_x, const int32_t* slot, int32_t n_slots, float* state,
                  void* h, int32_t* dev_status, moe_stream_t stream);
+
+/* Self-test of those waits.  After it, launches of moe_glr_forward and moe_glr_backward by the
+ * calling thread wait limit_ms (1..2000) at most, and warp `warp` (0..9) of the blocks of rank `rank`
+ * in their clusters leaves at step `step` as if a wait of its own had run out; every such launch ends
+ * on its own and reports MOE_ERR_TIMEOUT.  limit_ms = 0 ends the self-test. */
+int moe_selftest_recurrence_waits(int32_t limit_ms, int32_t rank, int32_t warp, int32_t step);
 
 #ifdef __cplusplus
 }

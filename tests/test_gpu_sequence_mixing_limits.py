@@ -59,3 +59,71 @@ def test_calls_off_16_byte_boundaries_keep_the_order_of_their_stream(dtype, D, w
     torch.cuda.synchronize()
     for n in got:
         assert torch.equal(got[n].view(torch.int16), want[n].view(torch.int16)), n
+
+
+@pytest.fixture
+def impatient():
+    """Ends the self-test of the waits whatever the test does."""
+    yield
+    moe.moe_selftest_recurrence_waits(0)
+
+
+def training_pass(N, D, dtype, n_seq, seed):
+    """(forward, backward, outputs) of one pass over sequences of equal length."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    g, x, dh = torch.nn.functional.logsigmoid(r(N, D) + 3).to(dtype), r(N, D).to(dtype), r(N, D).to(dtype)
+    h0, dh_T = r(n_seq, D), r(n_seq, D)
+    out = dict(h=torch.zeros_like(g), h_T=torch.zeros_like(h0), dg=torch.zeros_like(g),
+               dx=torch.zeros_like(g), dh0=torch.zeros_like(h0),
+               chunks=torch.zeros(((N + 63) // 64, D), device="cuda"))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    head = (N, D, n_seq, None, moe.MOE_GLR_MIX, CODE[dtype], g, x, h0)
+    return (lambda: moe.moe_glr_forward(*head, out["h"], out["h_T"], out["chunks"], status),
+            lambda: moe.moe_glr_backward(*head, out["chunks"], dh, dh_T, out["dg"], out["dx"],
+                                         out["dh0"], status), out, status)
+
+
+# rows, channels, type, sequences: clusters of 16 and of 8 blocks, single blocks, two sequences to a
+# part; with TMA and without
+@pytest.mark.parametrize("N, D, dtype, n_seq", [(9000, 64, BF, 1), (6000, 1024, F32, 1),
+                                                (5000, 8 * 2048, BF, 1), (60, 40, F32, 1),
+                                                (8000, 512, BF, 40), (7000, 62, BF, 1),
+                                                (4000, 33, F32, 4)])
+def test_scans_that_give_up_end_by_themselves_and_harm_nobody(N, D, dtype, n_seq, impatient):
+    """One warp of a cluster leaves early, in every role and at several steps; all that wait for it
+    run out of patience.  The launch ends, says so, and what runs beside it and after it has its
+    bits."""
+    forward, backward, out, status = training_pass(N, D, dtype, n_seq, 1)
+    o_forward, o_backward, o_out, o_status = training_pass(3000, 520, F32, 3, 2)
+    forward(), backward(), o_forward(), o_backward()
+    want, o_want = ({n: t.clone() for n, t in o.items()} for o in (out, o_out))
+    torch.cuda.synchronize()
+    assert int(status) == 0 and int(o_status) == 0
+    side = torch.cuda.Stream()
+    tries = [(0, 0, 0), (1, 7, 1), (0, 8, 0), (2, 8, 1), (0, 9, 0), (3, 9, 2), (1, 8, 3), (0, 4, 2)]
+    for call in (forward, backward):
+        gave_up = 0
+        for rank, warp, step in tries:
+            status.zero_()
+            for t in o_out.values():
+                t.zero_()
+            torch.cuda.synchronize()
+            moe.moe_selftest_recurrence_waits(4, rank, warp, step)
+            call()
+            moe.moe_selftest_recurrence_waits(0)
+            with torch.cuda.stream(side):
+                o_forward(), o_backward()
+            torch.cuda.synchronize()
+            assert int(status) in (0, 5)  # MOE_ERR_TIMEOUT where there is such a block and step
+            gave_up += int(status) == 5
+            assert int(o_status) == 0
+            assert all(torch.equal(o_out[n], o_want[n]) for n in o_want)
+        assert gave_up >= 2
+    status.zero_()
+    for t in out.values():
+        t.zero_()
+    forward(), backward()
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    assert all(torch.equal(out[n], want[n]) for n in want)

@@ -28,3 +28,10 @@ def test_workspace_size_of_widths_that_are_refused():
     assert got.stdout.strip() == str([0] * len(widths))
     assert all(moe.moe_qk_norm_rope_backward_workspace_size(8, D, 4, 1) > 0
                for D in range(8, 257, 8))
+
+
+def test_selftest_of_the_recurrences_waits_refuses():
+    for args in ((-1, 0, 0, 0), (2001, 0, 0, 0), (5, 0, 0, -1)):
+        assert moe.lib().moe_selftest_recurrence_waits(*args) == 1
+    assert moe.lib().moe_selftest_recurrence_waits(5, 0, 0, 0) == 0
+    assert moe.lib().moe_selftest_recurrence_waits(0, 0, 0, 0) == 0

@@ -32,7 +32,7 @@ def test_barriers_that_other_blocks_complete_are_waited_for_at_cluster_scope():
     waits = re.findall(r"(\w+)(?:<[^>]*>)?\(&\w+\.received\[", code)
     waits = [w for w in waits if "wait" in w]
     assert waits == ["wait_for_cluster"]
-    assert "mbar_wait_cluster(" in body(code, "void wait_for_cluster(")
+    assert "mbar_wait_cluster(" in body(code, "wait_for_cluster(uint64_t*")
 
 
 def test_warps_converge_before_the_clusters_barriers():

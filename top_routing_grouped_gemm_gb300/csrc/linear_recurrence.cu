@@ -304,6 +304,14 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// A warp's end: no block leaves while another may still write to it.
+__device__ __forceinline__ void leave_together(int cluster) {
+  if (cluster > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
+}
+
 // What the warps of a block and the blocks of a cluster exchange.  Step n uses the buffers n % 2
 // between the warps of a block.  A warp forms its pair of step n + 2 after it has used what the
 // joining warps gave it for step n, and they go to step n + 2 when every warp has formed its pair.
@@ -317,6 +325,7 @@ struct Exchange {
   Marks marks[2][kWarps];
   uint64_t formed[2], joined[2], received[4];
   uint64_t loaded[kStages], freed[kStages];  // tiles
+  int sent[kMaxCluster];  // pairs that each block of the cluster has sent, known from the last barrier on
   int abort;
 };
 
@@ -329,31 +338,55 @@ struct Turn {
   }
 };
 
-// Waits, with a limit.  When it runs out the rest of the launch goes on without waiting (its
-// results are then wrong, and reported).  (Trying again and again without a look at the clock
-// between takes issue slots from the warps that work: 2 to 6 % of the scans' time.)
-__device__ __forceinline__ void wait_for(uint64_t* bar, unsigned parity, int* abort,
-                                         int* dev_status) {
-  if (!mbar_wait(bar, parity, abort)) {
+// How long a launch waits.  (drill_*: in the self-test, that warp of the blocks of that rank leaves
+// at that step as if a wait of its own had run out.)
+struct Waits {
+  uint64_t limit_ns = kWaitTimeoutNs;
+  int* dev_status = nullptr;
+  int drill_rank = -1, drill_warp = -1, drill_step = 0;
+
+  __device__ __forceinline__ int steps_of(int rank, int warp, int steps) const {
+    return rank == drill_rank && warp == drill_warp ? min(steps, drill_step) : steps;
+  }
+  __device__ __forceinline__ void give_up(int* abort) const {
     *reinterpret_cast<volatile int*>(abort) = 1;
     report_status(dev_status, MOE_ERR_TIMEOUT);
   }
+};
+
+// Waits, with a limit.  A warp whose wait runs out arrives nowhere and starts no copy any more, so
+// nobody who depends on it goes on either, and no buffer is written again before it has been read.
+// What is under way then is waited for at the end (drain, drain_pairs).  A joining warp, whose lanes
+// all send, leaves at once, its lanes deciding together; a working warp, one lane of which arrives for
+// it, goes through its rows in vain, 8 us a step (deciding together at every wait takes 1 % of the
+// scans' time, and looking at `abort` once a step as much).
+// (Trying again and again without a look at the clock between takes issue slots from the warps that
+// work: 2 to 6 %.)
+[[nodiscard]] __device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity, int* abort,
+                                                       const Waits& w) {
+  return __all_sync(~0u, mbar_wait(bar, parity, abort, w.limit_ns));
 }
 
 // The same for a barrier that other blocks of the cluster complete: what they wrote is acquired at
 // their scope.
-__device__ __forceinline__ void wait_for_cluster(uint64_t* bar, unsigned parity, int* abort,
-                                                 int* dev_status) {
-  if (!mbar_wait_cluster(bar, parity, abort)) {
-    *reinterpret_cast<volatile int*>(abort) = 1;
-    report_status(dev_status, MOE_ERR_TIMEOUT);
+[[nodiscard]] __device__ __forceinline__ bool wait_for_cluster(uint64_t* bar, unsigned parity,
+                                                               int* abort, const Waits& w) {
+  return __all_sync(~0u, mbar_wait_cluster(bar, parity, abort, w.limit_ns));
+}
+
+// A working warp's lane waits; `alive` becomes false when that runs out.
+__device__ __forceinline__ void wait_alive(bool& alive, uint64_t* bar, unsigned parity, int* abort,
+                                           const Waits& w) {
+  if (!mbar_wait(bar, parity, abort, w.limit_ns)) {
+    w.give_up(abort);
+    alive = false;
   }
 }
 
 // One lane's arrival for its warp.
-__device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
+__device__ __forceinline__ void arrive_warp(uint64_t* bar, bool arrives) {
   __syncwarp();
-  if (lane == 0) mbar_arrive(bar);
+  if (arrives) mbar_arrive(bar);
 }
 
 template <int CH, int PAIRS>
@@ -397,7 +430,7 @@ __device__ __forceinline__ void join_warps(Exchange<CH, PAIRS>& x, Pair<CH>* blo
   uint64_t* received = &x.received[it & 3];
   if (cluster == 1) {
     *slot = sum;
-    arrive_warp(received, lane);
+    arrive_warp(received, lane == 0);
   } else {
     if (lane == 0) mbar_arrive_expect_tx(received, cluster * 32 * sizeof(Pair<CH>));
     for (int q = 0; q < cluster; ++q) {
@@ -416,16 +449,17 @@ __device__ __forceinline__ void join_warps(Exchange<CH, PAIRS>& x, Pair<CH>* blo
             : "memory");
     }
   }
-  arrive_warp(&x.joined[it & 1], lane);
+  arrive_warp(&x.joined[it & 1], lane == 0);
 }
 
 // The second one's: the state in front of this block's tile, from `state` in front of the step's
 // first tile, which moves on over the whole step.
 template <int CH, int PAIRS>
-__device__ __forceinline__ void join_blocks(Exchange<CH, PAIRS>& x, const Pair<CH>* blocks, int it,
-                                            int rank, int cluster, int lane, Vec<CH>& state,
-                                            int* dev_status) {
-  wait_for_cluster(&x.received[it & 3], it >> 2 & 1, &x.abort, dev_status);
+[[nodiscard]] __device__ __forceinline__ bool join_blocks(Exchange<CH, PAIRS>& x,
+                                                          const Pair<CH>* blocks, int it, int rank,
+                                                          int cluster, int lane, Vec<CH>& state,
+                                                          const Waits& waits) {
+  if (!wait_for_cluster(&x.received[it & 3], it >> 2 & 1, &x.abort, waits)) return false;
   Vec<CH> mine = state;
   const Pair<CH>* pairs = &blocks[(it & 3) * cluster * 32 + lane];
 #pragma unroll 4
@@ -434,7 +468,40 @@ __device__ __forceinline__ void join_blocks(Exchange<CH, PAIRS>& x, const Pair<C
     follow(state, pairs[q * 32]);
   }
   x.state[it & 1][lane] = mine;
-  arrive_warp(&x.joined[it & 1], lane);
+  arrive_warp(&x.joined[it & 1], lane == 0);
+  return true;
+}
+
+// Before the last barrier of the cluster, the first joining warp's part: tells every block how many
+// pairs this one has sent.
+template <int CH, int PAIRS>
+__device__ __forceinline__ void publish_sent(Exchange<CH, PAIRS>& x, int sent, int rank, int cluster,
+                                             int lane) {
+  if (lane < cluster) st_cluster(cluster_addr(&x.sent[rank], lane), sent);
+  fence_cluster();  // (the barrier itself orders nothing)
+}
+
+// After it, the second one's in a block that has seen the pairs of `got` steps only: waits, again with
+// a limit, for those that are still under way to it, so that none comes when the block has gone.  They
+// belong to the four steps from `got` on, as no block sends its pair of step n + 4 before all have used
+// step n; the barrier of a step then counts the blocks that did send theirs.
+template <int CH, int PAIRS>
+__device__ __forceinline__ void drain_pairs(Exchange<CH, PAIRS>& x, int got, int steps, int rank,
+                                            int cluster, int lane) {
+  if (lane) return;
+  constexpr int kBytes = 32 * sizeof(Pair<CH>);
+  for (int n = got; n < min(steps, got + 4); ++n) {
+    int senders = 0;
+    for (int q = 0; q < cluster; ++q) senders += x.sent[q] > n;
+    if (senders == 0) continue;
+    uint64_t* received = &x.received[n & 3];
+    if (x.sent[rank] <= n)
+      mbar_arrive_expect_tx(received, senders * kBytes);
+    else if (senders < cluster)  // it expects all of them
+      mbar_complete_tx(received, (cluster - senders) * kBytes);
+    int never = 0;
+    mbar_wait_cluster(received, n >> 2 & 1, &never);
+  }
 }
 
 // ------------------------------------------------------------------ tiles in shared memory
@@ -458,11 +525,11 @@ __device__ __forceinline__ void load_tile(uint32_t* ring, uint64_t* loaded, cons
     tma_load_2d(tile_at<ARRAYS>(ring, stage, i), &maps[i], &loaded[stage], d0, t0, policy);
 }
 
-// The same thread at the end: no copy is in flight when the block goes, not even in a launch that
-// gave up (again with a limit).
-__device__ __forceinline__ void drain(uint64_t* loaded, int steps) {
+// The same thread at the end, after the copies of the first `issued` steps: none is in flight when the
+// block goes, not even in a launch that gave up (again with a limit).
+__device__ __forceinline__ void drain(uint64_t* loaded, int issued) {
   int never = 0;
-  for (int it = max(0, steps - kStages); it < steps; ++it)
+  for (int it = max(0, issued - kStages); it < issued; ++it)
     mbar_wait(&loaded[it % kStages], it / kStages & 1, &never);
 }
 
@@ -530,7 +597,7 @@ struct ForwardArgs {
   const float* h0;  // may be h_T
   T* h;
   float *h_T, *h_chunks;
-  int* dev_status;
+  Waits waits;
 };
 
 template <typename T, int CH, bool MIX, bool ASYNC>
@@ -545,43 +612,51 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = blockIdx.x % p.cluster, part = blockIdx.x / p.cluster;
   const int d = (blockIdx.y * 32 + lane) * CH;
-  const bool on = d < p.D;
+  bool on = d < p.D;  // (of a working warp's first lane: and it has waited for everything)
   const long long D = p.D;
   exchange_init(xch);
   if (p.cluster > 1) cluster_arrive();  // (its way there and back, while the bounds come)
   after_previous();
   const Packed seq = near(p.seq, bounds);
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(seq, p.dev_status);
+  if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(seq, p.waits.dev_status);
   const Cut from = part_begin(seq, part, p.parts);
   const int lo = from.row, hi = part_begin(seq, part + 1, p.parts).row;
   const int base = lo / kTile * kTile, step = kTile * p.cluster;
   const int steps = hi > lo ? (hi - base + step - 1) / step : 0;
   const auto tile_row = [&](int it) { return base + (it * p.cluster + rank) * kTile; };
+  int issued = 0;  // tiles (the loading warp's)
   const auto load = [&](int it) {
-    if (ASYNC && lane == 0 && it < steps)
+    if (!ASYNC || it >= steps) return;
+    if (lane == 0)
       load_tile<2>(ring, xch.loaded, p.maps, it, blockIdx.y * 32 * CH, tile_row(it));
+    issued = it + 1;
   };
+  // a warp that ends before the last step has given up
+  const int own_steps = p.waits.steps_of(rank, warp, steps);
+  int done = 0;
   if (warp == kWarps)
     for (int it = 0; it < kStages; ++it) load(it);
   if (p.cluster > 1) cluster_wait();  // every block runs, its barriers set, before one sends
 
   if (warp == kWarps) {  // joins the warps, and has the tiles loaded
-    for (int it = 0; it < steps; ++it) {
-      wait_for(&xch.formed[it & 1], it >> 1 & 1, &xch.abort, p.dev_status);
-      join_warps<false>(xch, blocks, it, rank, p.cluster, lane);
-      load(it + kStages);  // over the tile that every warp has read
+    for (; done < own_steps; ++done) {
+      if (!wait_for(&xch.formed[done & 1], done >> 1 & 1, &xch.abort, p.waits)) break;
+      join_warps<false>(xch, blocks, done, rank, p.cluster, lane);
+      load(done + kStages);  // over the tile that every warp has read
     }
-    if (ASYNC && lane == 0) drain(xch.loaded, steps);
+    if (p.cluster > 1) publish_sent(xch, done, rank, p.cluster, lane);
   } else if (warp > kWarps) {  // joins the blocks
     Vec<CH> state = all<CH>(0.f);
-    for (int it = 0; it < steps; ++it)
-      join_blocks(xch, blocks, it, rank, p.cluster, lane, state, p.dev_status);
+    while (done < own_steps &&
+           join_blocks(xch, blocks, done, rank, p.cluster, lane, state, p.waits))
+      ++done;
   } else {
     if (seq.off && p.h_T && on) hand_on_empty<CH>(seq, p.h0, p.h_T, D, d, warp);
     struct Span {
       Vec<CH> a[kRows], b[kRows];  // the rows' decays and inputs
       unsigned firsts, lasts;
     };
+    if (own_steps < steps) report_status(p.waits.dev_status, MOE_ERR_TIMEOUT);
     Walker<false> walk;
     walk.start(from);
 
@@ -593,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       uint32_t* g = tile_at<2>(ring, it % kStages, 0) + warp * kRows * 32 + lane;
       uint32_t* x = tile_at<2>(ring, it % kStages, 1) + warp * kRows * 32 + lane;
       if (ASYNC) {
-        wait_for(&xch.loaded[it % kStages], it / kStages & 1, &xch.abort, p.dev_status);
+        wait_alive(on, &xch.loaded[it % kStages], it / kStages & 1, &xch.abort, p.waits);
         if (t0 < lo || t0 + kRows > hi) {  // rows of others and padding: the state goes through
 #pragma unroll
           for (int r = 0; r < kRows; ++r)
@@ -625,14 +700,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         pair.A = all<CH>(-1.f);
       }
       xch.warps[buf][0][warp][lane] = pair;
-      arrive_warp(&xch.formed[buf], lane);
+      arrive_warp(&xch.formed[buf], on && lane == 0);
     };
 
     // the rows of step `it` from the state in front of them
     const auto finish = [&](int it, int buf, Span& s) {
       const int t0 = tile_row(it) + warp * kRows;
       const Marks& m = xch.marks[buf][warp];
-      wait_for(&xch.joined[buf], it >> 1 & 1, &xch.abort, p.dev_status);
+      wait_alive(on, &xch.joined[buf], it >> 1 & 1, &xch.abort, p.waits);
       Vec<CH> h = xch.state[buf][lane];
       follow(h, xch.warps[buf][0][warp][lane]);
       if (warp == 0 && p.h_chunks && on && t0 >= lo && t0 < hi)  // kTile == kChunk
@@ -659,16 +734,19 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     // always one step's pairs ahead of the states
     Span even, odd;
-    for (int it = -1; it < steps; it += 2) {
-      if (it + 1 < steps) form(it + 1, 0, even);
+    for (int it = -1; it < own_steps; it += 2) {
+      if (it + 1 < own_steps) form(it + 1, 0, even);
       if (it >= 0) finish(it, 1, odd);
-      if (it + 2 < steps) form(it + 2, 1, odd);
-      if (it + 1 < steps) finish(it + 1, 0, even);
+      if (it + 2 < own_steps) form(it + 2, 1, odd);
+      if (it + 1 < own_steps) finish(it + 1, 0, even);
     }
   }
+  if (warp >= kWarps && done < steps) p.waits.give_up(&xch.abort);
+  if (ASYNC && warp == kWarps && lane == 0) drain(xch.loaded, issued);
   if (p.cluster > 1) {  // no block leaves while another may still write to it
     cluster_arrive();
     cluster_wait();
+    if (warp > kWarps && done < steps) drain_pairs(xch, done, steps, rank, p.cluster, lane);
   }
 }
 
@@ -695,7 +773,7 @@ struct BackwardArgs {
   const float *h0, *h_chunks, *dh_T;
   T *dg, *dx;
   float* dh0;
-  int* dev_status;
+  Waits waits;
 };
 
 template <typename T, int CH, bool MIX, bool ASYNC>
@@ -717,30 +795,40 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (p.cluster > 1) cluster_arrive();  // (its way there and back, while the bounds come)
   after_previous();
   const Packed seq = near(p.seq, bounds);
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(seq, p.dev_status);
+  if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(seq, p.waits.dev_status);
   const Cut until = part_begin(seq, part + 1, p.parts);
   const int lo = part_begin(seq, part, p.parts).row, hi = until.row;
   const int top = (hi + kTile - 1) / kTile * kTile, step = kTile * p.cluster;
   const int steps = hi > lo ? (top - lo / kTile * kTile + step - 1) / step : 0;
   const auto tile_row = [&](int it) { return top - (it * p.cluster + rank + 1) * kTile; };
+  int issued = 0;  // tiles (the loading warp's)
   const auto load = [&](int it) {
-    if (ASYNC && lane == 0 && it < steps)
+    if (!ASYNC || it >= steps) return;
+    if (lane == 0)
       load_tile<3>(ring, xch.loaded, p.maps, it, blockIdx.y * 32 * CH, tile_row(it));
+    issued = it + 1;
   };
+  // a warp that ends before the last step has given up
+  const int own_steps = p.waits.steps_of(rank, warp, steps);
+  int done = 0;
   if (warp == kWarps)
     for (int it = 0; it < kStages; ++it) load(it);
   if (p.cluster > 1) cluster_wait();  // every block runs, its barriers set, before one sends
 
   if (warp == kWarps) {  // joins the gradient's pairs of the warps, and has the tiles loaded
-    for (int it = 0; it < steps; ++it) {
-      wait_for(&xch.formed[it & 1], it >> 1 & 1, &xch.abort, p.dev_status);
-      join_warps<true>(xch, blocks, it, rank, p.cluster, lane);
-      if (ASYNC && it > 0) {  // the step before has been read for the second time
-        wait_for(&xch.freed[(it - 1) % kStages], (it - 1) / kStages & 1, &xch.abort, p.dev_status);
-        load(it - 1 + kStages);
+    while (done < own_steps) {
+      if (!wait_for(&xch.formed[done & 1], done >> 1 & 1, &xch.abort, p.waits)) break;
+      join_warps<true>(xch, blocks, done, rank, p.cluster, lane);
+      const int before = done++ - 1;
+      if (ASYNC && before >= 0) {  // that step has been read for the second time
+        if (!wait_for(&xch.freed[before % kStages], before / kStages & 1, &xch.abort, p.waits)) break;
+        load(before + kStages);
       }
     }
-    if (ASYNC && lane == 0) drain(xch.loaded, steps);
+    if (done < steps) p.waits.give_up(&xch.abort);
+    if (p.cluster > 1) publish_sent(xch, done, rank, p.cluster, lane);
+    if (ASYNC && lane == 0) drain(xch.loaded, issued);
+    leave_together(p.cluster);
   } else if (warp > kWarps) {  // joins the state's pairs of the warps, and the blocks
     const auto kept_state = [&](int it) {
       const int tile = tile_row(it);
@@ -748,19 +836,24 @@ __global__ void __launch_bounds__(kThreads, 2)
                                            : all<CH>(0.f);
     };
     Vec<CH> state = all<CH>(0.f), kept = kept_state(0);
-    for (int it = 0; it < steps; ++it) {
-      wait_for(&xch.formed[it & 1], it >> 1 & 1, &xch.abort, p.dev_status);
+    for (; done < own_steps; ++done) {
+      if (!wait_for(&xch.formed[done & 1], done >> 1 & 1, &xch.abort, p.waits)) break;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {  // the state in front of each warp's rows, as A
-        const Pair<CH> pair = xch.warps[it & 1][1][w][lane];
-        xch.warps[it & 1][1][w][lane].A = kept;
+        const Pair<CH> pair = xch.warps[done & 1][1][w][lane];
+        xch.warps[done & 1][1][w][lane].A = kept;
         follow(kept, pair);
       }
-      kept = kept_state(it + 1);
-      join_blocks(xch, blocks, it, rank, p.cluster, lane, state, p.dev_status);
+      kept = kept_state(done + 1);
+      if (!join_blocks(xch, blocks, done, rank, p.cluster, lane, state, p.waits)) break;
     }
+    if (done < steps) p.waits.give_up(&xch.abort);
+    leave_together(p.cluster);
+    if (p.cluster > 1 && done < steps) drain_pairs(xch, done, steps, rank, p.cluster, lane);
   } else {
     if (seq.off && p.dh0 && on) hand_on_empty<CH>(seq, p.dh_T, p.dh0, D, d, warp);
+    if (own_steps < steps) report_status(p.waits.dev_status, MOE_ERR_TIMEOUT);
+    bool arrives = lane == 0;
     Walker<true> walk;
     walk.start(until);
     const auto state_before = [&](const Marks& m, int r) {  // where a sequence begins
@@ -795,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                *x = tile_at<3>(ring, form_tile.at, 1) + warp * kRows * 32 + lane,
                *dh = tile_at<3>(ring, form_tile.at, 2) + warp * kRows * 32 + lane;
       if (ASYNC) {
-        wait_for(&xch.loaded[form_tile.at], form_tile.use, &xch.abort, p.dev_status);
+        wait_alive(arrives, &xch.loaded[form_tile.at], form_tile.use, &xch.abort, p.waits);
         if (t0 < lo || t0 + kRows > hi) {  // rows of others and padding: all goes through
 #pragma unroll
           for (int r = 0; r < kRows; ++r)
@@ -843,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       xch.warps[buf][0][warp][lane] = rev;
       xch.warps[buf][1][warp][lane] = fwd;
-      arrive_warp(&xch.formed[buf], lane);
+      arrive_warp(&xch.formed[buf], arrives);
       form_tile.next();
     };
 
@@ -857,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                      *dh = tile_at<3>(ring, tile.at, 2) + warp * kRows * 32 + lane;
       Vec<CH> a[kRows], om[MIX ? kRows : 1];
       gates(g, a, om);
-      wait_for(&xch.joined[buf], it >> 1 & 1, &xch.abort, p.dev_status);
+      wait_alive(arrives, &xch.joined[buf], it >> 1 & 1, &xch.abort, p.waits);
       Vec<CH> back = xch.state[buf][lane], h = xch.warps[buf][1][warp][lane].A;
       follow(back, xch.warps[buf][0][warp][lane]);
       Vec<CH> before[kRows], o_g, o_x;
@@ -908,22 +1001,19 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
       }
-      if (ASYNC) arrive_warp(&xch.freed[tile.at], lane);
+      if (ASYNC) arrive_warp(&xch.freed[tile.at], arrives);
       tile.next();
     };
 
     // always one step's pairs ahead of the states (one copy of the code: with two, it no longer
     // fits the instruction cache)
     Masks now{}, next{};
-    for (int it = -1; it < steps; ++it) {
-      if (it + 1 < steps) form(it + 1, (it + 1) & 1, next);
+    for (int it = -1; it < own_steps; ++it) {
+      if (it + 1 < own_steps) form(it + 1, (it + 1) & 1, next);
       if (it >= 0) finish(it, it & 1, now);
       now = next;
     }
-  }
-  if (p.cluster > 1) {  // no block leaves while another may still write to it
-    cluster_arrive();
-    cluster_wait();
+    leave_together(p.cluster);
   }
 }
 
@@ -990,6 +1080,15 @@ __global__ void __launch_bounds__(kStepThreads)
 }
 
 // ------------------------------------------------------------------------ host side
+
+// The self-test's settings, of the calling thread.
+thread_local Waits test_waits;
+
+Waits waits_of(int* dev_status) {
+  Waits w = test_waits;
+  w.dev_status = dev_status;
+  return w;
+}
 
 bool misaligned(const void* p, int size) {
   return reinterpret_cast<uintptr_t>(p) & static_cast<unsigned>(size - 1);
@@ -1132,7 +1231,7 @@ int moe_glr_forward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off,
         constexpr int CH = decltype(ch)::value;
         constexpr bool ASYNC = decltype(async)::value, F32 = sizeof(T) == 4;
         ForwardArgs<T> a{{}, seq, D, 1, 1, static_cast<const T*>(g), static_cast<const T*>(x), ld_g, ld_x, h0, static_cast<T*>(h), h_T,
-                         h_chunks, dev_status};
+                         h_chunks, waits_of(dev_status)};
         if (ASYNC) {
           if (int err = encode_map_rows(&a.maps[0], g, F32, D, N, ld_g, 32 * CH, kTile)) return err;
           if (int err = encode_map_rows(&a.maps[1], x, F32, D, N, ld_x, 32 * CH, kTile)) return err;
@@ -1164,7 +1263,7 @@ int moe_glr_backward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off
         BackwardArgs<T> a{{}, seq, D, 1, 1, static_cast<const T*>(g),
                           static_cast<const T*>(x), static_cast<const T*>(dh), ld_g, ld_x, h0,
                           h_chunks, dh_T, static_cast<T*>(dg), static_cast<T*>(dx), dh0,
-                          dev_status};
+                          waits_of(dev_status)};
         if (ASYNC) {
           const void* in[3] = {g, x, dh};
           const long long ld[3] = {ld_g, ld_x, D};
@@ -1220,6 +1319,18 @@ int moe_glr_step(int32_t B, int32_t D, int32_t mode, int32_t dtype, const void* 
   mark_after(MOE_KERNEL_GLR_STEP, stream);
   count_launches(1);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int moe_selftest_recurrence_waits(int32_t limit_ms, int32_t rank, int32_t warp, int32_t step) {
+  if (limit_ms < 0 || limit_ms > 2000 || (limit_ms && step < 0)) return MOE_ERR_INVALID_ARG;
+  test_waits = Waits{};
+  if (limit_ms) {
+    test_waits.limit_ns = limit_ms * 1000000ull;
+    test_waits.drill_rank = rank;
+    test_waits.drill_warp = warp;
+    test_waits.drill_step = step;
+  }
+  return MOE_OK;
 }
 
 }  // extern "C"

@@ -147,6 +147,7 @@ _SIGS = {
     "moe_set_kernel_events": (ctypes.c_int, [ctypes.c_int, c_vp, c_vp]),
     "moe_launch_count": (ctypes.c_longlong, []),
     "moe_selftest_wait_timeout": (ctypes.c_int, [c_vp, c_i32, c_vp]),
+    "moe_selftest_recurrence_waits": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32]),
 }
 
 KERNEL_IDS = {"router_gemm": 0, "topk": 1, "dispatch": 2, "gateup_gemm": 3, "down_gemm": 4,
@@ -723,6 +724,12 @@ def moe_launch_count() -> int:
 def moe_selftest_wait_timeout(dev_status, timeout_ms, stream=None):
     _check("moe_selftest_wait_timeout",
            lib().moe_selftest_wait_timeout(_ptr(dev_status), timeout_ms, _stream(stream)))
+
+
+def moe_selftest_recurrence_waits(limit_ms, rank=0, warp=0, step=0):
+    """Launches of the recurrence's scans by this thread give up by themselves (0: no longer)."""
+    _check("moe_selftest_recurrence_waits",
+           lib().moe_selftest_recurrence_waits(limit_ms, rank, warp, step))
 
 
 # ----------------------------------------------------------------------------- layer helpers
