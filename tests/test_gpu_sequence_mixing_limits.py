@@ -127,3 +127,54 @@ def test_scans_that_give_up_end_by_themselves_and_harm_nobody(N, D, dtype, n_seq
     torch.cuda.synchronize()
     assert int(status) == 0
     assert all(torch.equal(out[n], want[n]) for n in want)
+
+
+@pytest.mark.parametrize("n_seq", [511, 512, 5000, 1 << 24])
+def test_few_rows_among_millions_of_empty_sequences(n_seq):
+    """However many sequences are empty, no wait runs out: rows have the bits of a call without the
+    empty ones, and these hand their states on (h_T over h0 too)."""
+    D, lengths = 2, [3, 1, 40, 8, 1, 30, 9]
+    N = sum(lengths)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    g, x, dh = -r(N + 3, D).abs(), r(N + 3, D), r(N + 3, D)
+    where = sorted([0, 1, n_seq // 3, n_seq // 3 + 200, n_seq // 2 + 70, n_seq - 2, n_seq - 1])
+    counts = torch.zeros(n_seq, dtype=torch.int64, device="cuda")
+    counts[where] = torch.tensor(lengths, device="cuda")
+    off = torch.zeros(n_seq + 1, dtype=torch.int32, device="cuda")
+    off[1:] = counts.cumsum(0)
+    few_off = torch.tensor([0] + lengths, device="cuda").cumsum(0).to(torch.int32)
+    h0, dh_T = r(n_seq, D), r(n_seq, D)
+
+    def run(n, offsets, h0, dh_T, in_place=False):
+        h, dg, dx = (torch.full((N + 3, D), 7.0, device="cuda") for _ in range(3))
+        h_T = h0.clone() if in_place else torch.full_like(h0, 7.0)
+        dh0, chunks = torch.full_like(h0, 7.0), torch.zeros((2, D), device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        head = (N + 3, D, n, offsets, moe.MOE_GLR_MIX, moe.MOE_F32, g, x)
+        moe.moe_glr_forward(*head, h_T if in_place else h0, h, h_T, chunks, status)
+        moe.moe_glr_backward(*head, h0, chunks, dh, dh_T, dg, dx, dh0, status)
+        torch.cuda.synchronize()
+        assert int(status) == 0
+        return h, dg, dx, h_T, dh0
+
+    want = run(len(lengths), few_off, h0[where].contiguous(), dh_T[where].contiguous())
+    for in_place in (False, True):
+        got = run(n_seq, off, h0, dh_T, in_place)
+        for a, b in zip(got[:3], want[:3]):
+            assert torch.equal(a, b)
+        for a, b, kept in zip(got[3:], want[3:], (h0, dh_T)):
+            assert torch.equal(a[where], b)
+            a[where] = kept[where]
+            assert torch.equal(a, kept)
+
+
+def test_empty_sequences_without_states_end_in_zeros():
+    """h0 NULL: an empty sequence's final state is zero, whoever writes it."""
+    for n_seq in (100, 3000):
+        off = torch.zeros(n_seq + 1, dtype=torch.int32, device="cuda")
+        off[7:] = 2
+        g = torch.zeros((2, 40), device="cuda")
+        h, h_T = torch.empty_like(g), torch.full((n_seq, 40), 7.0, device="cuda")
+        moe.moe_glr_forward(2, 40, n_seq, off, 0, moe.MOE_F32, g, g + 1, None, h, h_T, None)
+        assert (h_T[6] == 2).all() and h_T.sum() == 80

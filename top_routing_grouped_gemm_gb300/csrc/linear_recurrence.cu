@@ -201,7 +201,8 @@ struct Marks {
 };
 
 // Walks the bounds of the sequences beside a warp's rows, which come in ascending (DOWN:
-// descending) order.  The state is the same in all lanes.
+// descending) order.  The state is the same in all lanes.  (Others wait meanwhile, for 2 s at most: 2^24
+// empty sequences beside the same rows, the most there can be, take 0.18 s.)
 template <bool DOWN>
 struct Walker {
   int cursor;  // bounds passed (DOWN: bounds left)
@@ -569,13 +570,35 @@ __device__ __forceinline__ Packed near(const Packed& q, int* bounds) {
   return {q.N, q.n_seq, bounds, q.len};
 }
 
-// to = from for the sequences without rows, from null: zero (a part of them for each warp).
+// to = from for the sequences without rows, from null: zero.  32 of every 32 `groups` sequences; called
+// by whole warps.
 template <int CH>
 __device__ __forceinline__ void hand_on_empty(const Packed& q, const float* from, float* to,
-                                              long long D, int d, int warp) {
-  for (int s = blockIdx.x * kWarps + warp; s < q.n_seq; s += gridDim.x * kWarps)
-    if (bound_of(q, s) >= bound_of(q, s + 1))
-      write(to + s * D + d, from ? read<CH>(from + s * D + d) : all<CH>(0.f));
+                                              long long D, int d, bool on, int lane, int group,
+                                              int groups) {
+  for (int s = group * 32; s < q.n_seq; s += groups * 32) {
+    const int mine = s + lane;
+    unsigned empty =
+        __ballot_sync(~0u, mine < q.n_seq && bound_of(q, mine) >= bound_of(q, mine + 1));
+    for (; empty; empty &= empty - 1) {
+      const long long at = (s + __ffs(empty) - 1) * D + d;
+      if (on) write(to + at, from ? read<CH>(from + at) : all<CH>(0.f));
+    }
+  }
+}
+
+// The scans do that when their rows are done (nobody waits for it then), if there are so few sequences
+// that their bounds lie in shared memory; else this kernel does it behind them, which has blocks by the
+// number of sequences.
+constexpr int kEmptyThreads = 256;
+
+__global__ void __launch_bounds__(kEmptyThreads)
+    glr_empty_kernel(const Packed q, const float* from, float* to, int D) {
+  after_previous();
+  const int lane = threadIdx.x & 31, warps = kEmptyThreads / 32;
+  const int d = blockIdx.y * 32 + lane;
+  hand_on_empty<1>(q, from, to, D, d, d < D, lane, blockIdx.x * warps + threadIdx.x / 32,
+                   gridDim.x * warps);
 }
 
 // ------------------------------------------------------------------ forward
@@ -636,6 +659,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   int done = 0;
   if (warp == kWarps)
     for (int it = 0; it < kStages; ++it) load(it);
+  const auto hand_on = [&](int group, int groups) {
+    if (seq.off && p.h_T && seq.n_seq < kBounds)
+      hand_on_empty<CH>(seq, p.h0, p.h_T, D, d, on, lane, group, groups);
+  };
   if (p.cluster > 1) cluster_wait();  // every block runs, its barriers set, before one sends
 
   if (warp == kWarps) {  // joins the warps, and has the tiles loaded
@@ -650,8 +677,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     while (done < own_steps &&
            join_blocks(xch, blocks, done, rank, p.cluster, lane, state, p.waits))
       ++done;
+    // (without TMA the working warps are short of registers: 8191 x 2046 bf16 38.8 us there, 33.9 here)
+    if (!ASYNC) hand_on(blockIdx.x, gridDim.x);
   } else {
-    if (seq.off && p.h_T && on) hand_on_empty<CH>(seq, p.h0, p.h_T, D, d, warp);
     struct Span {
       Vec<CH> a[kRows], b[kRows];  // the rows' decays and inputs
       unsigned firsts, lasts;
@@ -740,6 +768,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (it + 2 < own_steps) form(it + 2, 1, odd);
       if (it + 1 < own_steps) finish(it + 1, 0, even);
     }
+    if (ASYNC) hand_on(blockIdx.x * kWarps + warp, gridDim.x * kWarps);
   }
   if (warp >= kWarps && done < steps) p.waits.give_up(&xch.abort);
   if (ASYNC && warp == kWarps && lane == 0) drain(xch.loaded, issued);
@@ -851,7 +880,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     leave_together(p.cluster);
     if (p.cluster > 1 && done < steps) drain_pairs(xch, done, steps, rank, p.cluster, lane);
   } else {
-    if (seq.off && p.dh0 && on) hand_on_empty<CH>(seq, p.dh_T, p.dh0, D, d, warp);
     if (own_steps < steps) report_status(p.waits.dev_status, MOE_ERR_TIMEOUT);
     bool arrives = lane == 0;
     Walker<true> walk;
@@ -1013,6 +1041,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (it >= 0) finish(it, it & 1, now);
       now = next;
     }
+    if (seq.off && p.dh0 && seq.n_seq < kBounds)
+      hand_on_empty<CH>(seq, p.dh_T, p.dh0, D, d, on, lane, blockIdx.x * kWarps + warp,
+                        gridDim.x * kWarps);
     leave_together(p.cluster);
   }
 }
@@ -1186,6 +1217,18 @@ int launch(int N, int D, int n_seq, Args& args, cudaStream_t stream) {
   return launched(cudaLaunchKernelEx(&cfg, KERNEL, args)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// What the scans leave to a kernel of its own: MOE_OK, and 1 more in `launches`, where there is any.
+int launch_empty(const Packed& seq, const float* from, float* to, int D, cudaStream_t stream,
+                 int* launches) {
+  if (!seq.off || !to || seq.n_seq < kBounds) return MOE_OK;
+  ++*launches;
+  const dim3 grid((seq.n_seq + kEmptyThreads - 1) / kEmptyThreads, (D + 31) / 32);
+  return launch_behind(glr_empty_kernel, grid, kEmptyThreads, 0, stream, seq, from, to, D) ==
+                 cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
 // Calls f(T{}, channels per lane, mode, ASYNC) for the call's type.  Tensors whose rows all begin
 // on 16-byte boundaries (and do not share one row) are copied by TMA; a lane has two bf16 where they
 // all begin on 4-byte boundaries (8191 x 2046, forward: 62 us with one, 37 us with two).
@@ -1225,7 +1268,8 @@ int moe_glr_forward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off,
   if (int e = check_rows(N, D, n_seq, seq_off, mode, dtype, g, ld_g, x, ld_x, h, false)) return e;
   const Packed seq{N, n_seq, seq_off, seq_off ? 0 : N / n_seq};
   mark_before(MOE_KERNEL_GLR_FWD, stream);
-  const int e = dispatch(
+  int launches = 1;
+  int e = dispatch(
       mode, dtype, {g, x, h}, {ld_g, ld_x, D}, [&](auto type, auto ch, auto mix, auto async) {
         using T = decltype(type);
         constexpr int CH = decltype(ch)::value;
@@ -1239,8 +1283,9 @@ int moe_glr_forward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off,
         return launch<glr_forward_kernel<T, CH, decltype(mix)::value, ASYNC>, CH, 2>(N, D, n_seq, a,
                                                                                       stream);
       });
+  if (e == MOE_OK) e = launch_empty(seq, h0, h_T, D, stream, &launches);
   mark_after(MOE_KERNEL_GLR_FWD, stream);
-  count_launches(1);
+  count_launches(launches);
   return e;
 }
 
@@ -1254,7 +1299,8 @@ int moe_glr_backward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off
   if (misaligned(dh, size) || misaligned(dx, size)) return MOE_ERR_UNSUPPORTED;
   const Packed seq{N, n_seq, seq_off, seq_off ? 0 : N / n_seq};
   mark_before(MOE_KERNEL_GLR_BWD, stream);
-  const int e = dispatch(
+  int launches = 1;
+  int e = dispatch(
       mode, dtype, {g, x, dh, dg, dx}, {ld_g, ld_x, D},
       [&](auto type, auto ch, auto mix, auto async) {
         using T = decltype(type);
@@ -1274,8 +1320,9 @@ int moe_glr_backward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off
         return launch<glr_backward_kernel<T, CH, decltype(mix)::value, ASYNC>, CH, 3>(N, D, n_seq, a,
                                                                                        stream);
       });
+  if (e == MOE_OK) e = launch_empty(seq, dh_T, dh0, D, stream, &launches);
   mark_after(MOE_KERNEL_GLR_BWD, stream);
-  count_launches(1);
+  count_launches(launches);
   return e;
 }
 
