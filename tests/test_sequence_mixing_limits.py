@@ -1,6 +1,7 @@
 """CPU checks of the limits of the operators beside the gated delta rule: sizes and addresses that a
 call refuses before anything reaches a GPU."""
 
+import os
 import subprocess
 import sys
 
@@ -35,3 +36,29 @@ def test_selftest_of_the_recurrences_waits_refuses():
         assert moe.lib().moe_selftest_recurrence_waits(*args) == 1
     assert moe.lib().moe_selftest_recurrence_waits(5, 0, 0, 0) == 0
     assert moe.lib().moe_selftest_recurrence_waits(0, 0, 0, 0) == 0
+
+
+FAKE = 0x10000  # never dereferenced: every call below fails its host checks first
+INVALID, UNSUPPORTED = 1, 2
+
+
+def gdr_step(B=4, H=2, dk=64, dv=64, q=FAKE, k=FAKE, v=FAKE, beta=FAKE, g=FAKE, slot=FAKE,
+             n_slots=1 << 24, S=FAKE, o=FAKE, status=None):
+    return moe.lib().moe_gdr_step(B, H, dk, dv, q, k, v, beta, g, slot, n_slots, 0.1, S, o, status,
+                                  None)
+
+
+def test_steps_refuse_batches_whose_slots_take_too_long_to_compare():
+    """Every request looks for its slot among those before it, which grows with the square of the
+    batch."""
+    assert gdr_step(B=65536, H=1) == UNSUPPORTED
+    assert gdr_step(B=1 << 24, H=1) == UNSUPPORTED
+    assert gdr_step(B=1 << 13, H=(1 << 11) + 1, slot=None) == UNSUPPORTED
+    assert moe.lib().moe_glr_step(65536, 8, 0, 0, FAKE, 8, FAKE, 8, FAKE, 1 << 24, FAKE, FAKE, None,
+                                  None) == UNSUPPORTED
+
+
+def test_limits_of_the_steps_are_documented():
+    with open(os.path.join(B.ROOT, "include", "linear_attention.h")) as f:
+        text = " ".join(f.read().split())
+    assert "B * H up to 2^24" in text and "B up to 65535" in text

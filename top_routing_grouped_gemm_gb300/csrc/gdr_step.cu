@@ -126,6 +126,7 @@ extern "C" int moe_gdr_step(int32_t B, int32_t H, int32_t dk, int32_t dv, const 
   if (!slot && B > n_slots) return MOE_ERR_INVALID_ARG;
   if (!((dk == 64 || dk == 128) && (dv == 64 || dv == 128))) return MOE_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * H > (1ll << 24)) return MOE_ERR_UNSUPPORTED;
+  if (slot && B > kMaxSlots) return MOE_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) |
        reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(S) |
        reinterpret_cast<uintptr_t>(o)) & 15u)

@@ -1331,7 +1331,7 @@ int moe_glr_step(int32_t B, int32_t D, int32_t mode, int32_t dtype, const void* 
                  void* h, int32_t* dev_status, moe_stream_t stream) {
   if (int e = check_rows(B, D, 1, nullptr, mode, dtype, g, ld_g, x, ld_x, h, false)) return e;
   if (!state || n_slots <= 0 || (!slot && B > n_slots)) return MOE_ERR_INVALID_ARG;
-  if (B > 65535) return MOE_ERR_UNSUPPORTED;
+  if (B > kMaxSlots) return MOE_ERR_UNSUPPORTED;  // (and no more fit a grid's second dimension)
   // four channels to a thread where every row begins on the boundary of four values (64 requests x
   // 4096 channels, bf16: 4.5 us with one, 3.6 us with four; 512 requests: 12.8 and 6.9)
   const int size = dtype == MOE_BF16 ? 2 : 4;

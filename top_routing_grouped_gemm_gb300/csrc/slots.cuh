@@ -5,6 +5,11 @@
 
 namespace moe {
 
+// Requests of a batch with slots: every block of a request looks through those before it, which grows
+// with the square of the batch: the delta rule's step of 4096 x 16 heads of 128 takes 1211 us without
+// slots and 1259 us with them, 65535 x 4 heads 4.8 and 38 ms.
+constexpr int kMaxSlots = 65535;
+
 // Whether an earlier request of the batch has already named request b's row: two blocks would race
 // on its state.  That is reported.  Called by whole blocks, every thread with the same b.
 __device__ __forceinline__ bool named_before(int b, int row, const int* slot, int* dev_status) {
