@@ -35,9 +35,14 @@
  * being incomplete, and is reported as MOE_ERR_TIMEOUT in *dev_status.  Nothing of it is under way
  * any more when it has ended.
  *
- * Precision: states, products and sums are fp32; h, dg and dx are rounded once.  Sequences do
- * not see each other: infinities or NaN in one leave the others alone.  Deterministic: the
- * work is cut by sizes alone and every combination has a fixed order.
+ * Precision: states, products and sums are fp32; h, dg and dx are rounded once.  The scans form
+ * exp(g) as 2^(g log2(e)), whose rounded product costs |g| 2^-24 of it, and take less than 2^-126
+ * as zero; the step calls the library's exponential, so the two round differently.  Sequences do
+ * not see each other: infinities or NaN in one leave the others alone.  An infinity makes all
+ * that follows in its sequence and channel infinite or NaN, but not always the one that the
+ * formula gives: where the decays of up to 64 rows multiply to less than 2^-149 the scans'
+ * product is zero, and zero times an infinity is NaN.  Deterministic: the work is cut by sizes
+ * (and by what the GPU has room for) alone and every combination has a fixed order.
  */
 #ifndef MOE_LINEAR_RECURRENCE_H
 #define MOE_LINEAR_RECURRENCE_H

@@ -178,3 +178,47 @@ def test_empty_sequences_without_states_end_in_zeros():
         h, h_T = torch.empty_like(g), torch.full((n_seq, 40), 7.0, device="cuda")
         moe.moe_glr_forward(2, 40, n_seq, off, 0, moe.MOE_F32, g, g + 1, None, h, h_T, None)
         assert (h_T[6] == 2).all() and h_T.sum() == 80
+
+
+@pytest.mark.parametrize("mean", [-0.02, -2.0, -30.0])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_an_infinity_stays_in_its_sequence_and_channel(dtype, mean):
+    """What the definition makes infinite or NaN is infinite or NaN, the rest has the bits that it
+    has without the infinities: mild decays, decays whose product over 64 rows is no fp32 number, and
+    decays that are none themselves after three rows."""
+    N, D, off = 600, 70, [0, 250, 600]
+    gen = torch.Generator().manual_seed(17)
+    g = (mean * (0.5 + torch.rand((N, D), generator=gen))).to(dtype).cuda()
+    x, dh = (torch.randn((N, D), generator=gen).to(dtype).cuda() for _ in range(2))
+    h0, dh_T = (torch.randn((2, D), generator=gen).cuda() for _ in range(2))
+    arg = torch.tensor(off, dtype=torch.int32).cuda()
+    inf = float("inf")
+
+    def run(x, dh, h0, dh_T):
+        h, dg, dx = (torch.empty_like(x) for _ in range(3))
+        h_T, dh0 = torch.empty_like(h0), torch.empty_like(h0)
+        chunks = torch.empty(((N + 63) // 64, D), device="cuda")
+        moe.moe_glr_forward(N, D, 2, arg, 0, CODE[dtype], g, x, h0, h, h_T, chunks)
+        moe.moe_glr_backward(N, D, 2, arg, 0, CODE[dtype], g, x, h0, chunks, dh, dh_T, dg, dx, dh0)
+        torch.cuda.synchronize()
+        return dict(h=h, h_T=h_T, dg=dg, dx=dx, dh0=dh0)
+
+    clean = run(x, dh, h0, dh_T)
+    x2, dh2, h02, dh_T2 = x.clone(), dh.clone(), h0.clone(), dh_T.clone()
+    h02[0, 3], x2[100, 5], x2[599, 6], x2[260, 7] = inf, -inf, inf, inf  # forward
+    dh_T2[1, 10], dh2[400, 12], dh2[0, 13], dh2[249, 14] = -inf, inf, inf, -inf  # backward
+    got = run(x2, dh2, h02, dh_T2)
+    bad = {n: np.zeros(t.shape, bool) for n, t in got.items()}
+    for first, last, c in ((0, 250, 3), (100, 250, 5), (599, 600, 6), (260, 600, 7)):
+        bad["h"][first:last, c] = True
+        bad["dg"][first + (first != 0):last, c] = True  # a_t lam_t h_{t-1}
+        bad["h_T"][int(first >= 250), c] = True
+    for first, last, c in ((250, 600, 10), (250, 401, 12), (0, 1, 13), (0, 250, 14)):
+        bad["dx"][first:last, c] = True
+        bad["dg"][first:last, c] = True
+        bad["dh0"][int(first >= 250), c] = True
+    for n, t in got.items():
+        finite = np.isfinite(f64(t))
+        assert not finite[bad[n]].any(), n
+        keep = torch.from_numpy(~bad[n]).cuda()
+        assert torch.equal(t[keep], clean[n][keep]), n
