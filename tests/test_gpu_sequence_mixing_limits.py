@@ -9,7 +9,7 @@ import torch
 from oracle import sequence_mixing as SM
 from top_routing_grouped_gemm_gb300 import moe
 from parity_util import f64
-from test_gpu_sequence_mixing import BF, CODE, F32, LAST, U, close, majorants
+from test_gpu_sequence_mixing import BF, CODE, F32, close, majorants
 
 pytestmark = pytest.mark.gpu
 
@@ -222,3 +222,42 @@ def test_an_infinity_stays_in_its_sequence_and_channel(dtype, mean):
         assert not finite[bad[n]].any(), n
         keep = torch.from_numpy(~bad[n]).cuda()
         assert torch.equal(t[keep], clean[n][keep]), n
+
+
+@pytest.mark.parametrize("which", ["g", "x", "both"])
+@pytest.mark.parametrize("D", [64, 33])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_row_shared_by_all(dtype, D, which):
+    """Row stride 0: the forward and the step read one row for all of them."""
+    N, slots = 150, 200
+    gen = torch.Generator().manual_seed(41)
+    whole = dict(g=-torch.rand((N, D), generator=gen), x=torch.randn((N, D), generator=gen))
+    i = {n: t.to(dtype).cuda() for n, t in whole.items()}
+    for n in ("g", "x") if which == "both" else (which,):
+        i[n] = i[n][:1].expand(N, D)
+        assert i[n].stride(0) == 0
+    h0 = torch.randn((2, D), generator=gen).cuda()
+    off = torch.tensor([0, 70, N], dtype=torch.int32).cuda()
+    slot = torch.randperm(slots, generator=gen)[:N].to(torch.int32).cuda()
+    state = torch.randn((slots, D), generator=gen).cuda()
+    old = f64(state)[slot.cpu().numpy()]
+    h, hs = (torch.empty((N, D), dtype=dtype, device="cuda") for _ in range(2))
+    h_T = torch.empty_like(h0)
+    moe.moe_glr_forward(N, D, 2, off, 1, CODE[dtype], i["g"], i["x"], h0, h, h_T, None)
+    moe.moe_glr_step(N, D, 1, CODE[dtype], i["g"], i["x"], slot, slots, state, hs)
+    torch.cuda.synchronize()
+    g, x = f64(i["g"]), f64(i["x"])
+    ref, ref_T = SM.gated_recurrence(g, x, [0, 70, N], f64(h0), True)
+    E = majorants(g, x, [0, 70, N], f64(h0), True)[1]
+    close(h, ref, E, dtype, "h")
+    close(h_T, ref_T, E[[69, N - 1]], F32, "h_T")
+    rows = list(range(N + 1))
+    ref = SM.gated_recurrence(g, x, rows, old, True)[0]
+    close(hs, ref, majorants(g, x, rows, old, True)[1], dtype, "step")
+
+
+def test_no_row_shared_in_an_input_with_a_gradient():
+    g = torch.zeros((1, 8), device="cuda").expand(4, 8)
+    z = torch.zeros((4, 8), device="cuda")
+    with pytest.raises(moe.MoEError):
+        moe.moe_glr_backward(4, 8, 1, None, 0, moe.MOE_F32, g, z, None, z[:1], z, None, g, z + 1, None)
