@@ -261,3 +261,21 @@ def test_no_row_shared_in_an_input_with_a_gradient():
     z = torch.zeros((4, 8), device="cuda")
     with pytest.raises(moe.MoEError):
         moe.moe_glr_backward(4, 8, 1, None, 0, moe.MOE_F32, g, z, None, z[:1], z, None, g, z + 1, None)
+
+
+@pytest.mark.parametrize("stride", [4, 8, 1 << 40])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_stride_of_a_single_row_means_nothing(dtype, stride):
+    """One row: whatever its tensor says of the next one, forward and backward."""
+    D = 256
+    gen = torch.Generator().manual_seed(43)
+    g, x, dh = (torch.randn((1, D), generator=gen).to(dtype).cuda() for _ in range(3))
+    g = -g.abs()
+    one = lambda t: t.as_strided((1, D), (stride, 1))  # noqa: E731
+    h, dg, dx = (torch.empty((1, D), dtype=dtype, device="cuda") for _ in range(3))
+    chunks = torch.empty((1, D), device="cuda")
+    moe.moe_glr_forward(1, D, 1, None, 0, CODE[dtype], one(g), one(x), None, h, None, chunks)
+    moe.moe_glr_backward(1, D, 1, None, 0, CODE[dtype], one(g), one(x), None, chunks, dh, None,
+                         one(dg), one(dx), None)
+    torch.cuda.synchronize()
+    assert torch.equal(h, x) and torch.equal(dx, dh) and (dg == 0).all()

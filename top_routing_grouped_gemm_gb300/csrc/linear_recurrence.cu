@@ -1266,6 +1266,7 @@ int moe_glr_forward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off,
                     const float* h0, void* h, float* h_T, float* h_chunks, int32_t* dev_status,
                     moe_stream_t stream) {
   if (int e = check_rows(N, D, n_seq, seq_off, mode, dtype, g, ld_g, x, ld_x, h, false)) return e;
+  if (N == 1) ld_g = ld_x = D;  // whatever they are
   const Packed seq{N, n_seq, seq_off, seq_off ? 0 : N / n_seq};
   mark_before(MOE_KERNEL_GLR_FWD, stream);
   int launches = 1;
@@ -1297,6 +1298,7 @@ int moe_glr_backward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off
   if (!h_chunks || !dh || !dx) return MOE_ERR_INVALID_ARG;
   const int size = dtype == MOE_BF16 ? 2 : 4;
   if (misaligned(dh, size) || misaligned(dx, size)) return MOE_ERR_UNSUPPORTED;
+  if (N == 1) ld_g = ld_x = D;
   const Packed seq{N, n_seq, seq_off, seq_off ? 0 : N / n_seq};
   mark_before(MOE_KERNEL_GLR_BWD, stream);
   int launches = 1;
