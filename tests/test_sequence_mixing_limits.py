@@ -1,6 +1,7 @@
 """CPU checks of the limits of the operators beside the gated delta rule: sizes and addresses that a
 call refuses before anything reaches a GPU."""
 
+import ctypes
 import os
 import subprocess
 import sys
@@ -62,3 +63,58 @@ def test_limits_of_the_steps_are_documented():
     with open(os.path.join(B.ROOT, "include", "linear_attention.h")) as f:
         text = " ".join(f.read().split())
     assert "B * H up to 2^24" in text and "B up to 65535" in text
+
+
+CHOICE = r"""
+#include "cluster_room.h"
+extern "C" void choose(const int* fits, int strips, int tiles, int n_seq, int* out) {
+  const moe::ClusterRoom room = moe::ask_room([&](int c, int* n) {
+    *n = fits[c];
+    return fits[c] >= 0;  // negative: the driver refuses the size
+  });
+  const moe::ClusterChoice c = moe::choose_clusters(room, strips, tiles, n_seq);
+  out[0] = c.cluster;
+  out[1] = c.parts;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def choose(tmp_path_factory):
+    at = tmp_path_factory.mktemp("choice")
+    (at / "choice.cpp").write_text(CHOICE)
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I", B.CSRC, str(at / "choice.cpp"),
+                    "-o", str(at / "choice.so")], check=True)
+    f = ctypes.CDLL(str(at / "choice.so")).choose
+
+    def call(fits, strips, tiles, n_seq):
+        out = (ctypes.c_int * 2)()
+        f((ctypes.c_int * 17)(*fits), strips, tiles, n_seq, out)
+        return tuple(out)
+
+    return call
+
+
+FITS = [0] + [304 // c for c in range(1, 17)]  # two blocks to each of 152 SMs, nothing lost to size
+
+
+def test_clusters_are_as_large_as_fit(choose):
+    assert choose(FITS, 36, 1000, 1) == (8, 1)        # 36 strips: 38 clusters of 8 fit, 33 of 9
+    assert choose(FITS, 32, 1000, 1) == (9, 1)        # 32 strips: one block more for each
+    assert choose(FITS, 40, 1000, 1) == (7, 1)        # 38 clusters of 8 do not hold 40 strips
+    assert choose(FITS, 1, 1000, 1) == (16, 1)        # few channels: more blocks to work
+    assert choose(FITS, 1, 1000, 100) == (8, 38)      # with many sequences parts do that
+    assert choose(FITS, 1, 3, 1) == (3, 1)            # no more blocks than tiles
+    assert choose(FITS, 400, 1000, 5) == (1, 1)       # more strips than places
+
+
+def test_cluster_sizes_that_the_driver_refuses_are_left_out(choose):
+    """A size that cannot be launched here costs that size, not every call."""
+    few = [n if c <= 8 else -1 for c, n in enumerate(FITS)]
+    assert choose(few, 1, 1000, 1) == (8, 1)
+    holes = [-1 if c in (8, 16, 15) else n for c, n in enumerate(FITS)]
+    assert choose(holes, 36, 1000, 1) == (7, 1)
+    assert choose(holes, 32, 1000, 1) == (9, 1)
+    assert choose(holes, 1, 1000, 1) == (14, 1)
+    none = [-1] * 17
+    assert choose(none, 32, 1000, 10) == (1, 1)

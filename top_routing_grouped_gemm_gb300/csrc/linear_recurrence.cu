@@ -1,10 +1,12 @@
 // Gated linear recurrence over packed sequences, forward, backward and one token
 // (include/linear_recurrence.h has the formulas).
 #include <algorithm>
+#include <atomic>
 #include <initializer_list>
 #include <mutex>
 #include <type_traits>
 
+#include "cluster_room.h"
 #include "moe_internal.h"
 #include "overlap.cuh"
 #include "ptx.cuh"
@@ -21,7 +23,6 @@ constexpr int kThreads = 32 * (kWarps + 2);
 constexpr int kRows = 8;        // rows of a warp in a tile
 constexpr int kTile = kWarps * kRows;
 constexpr int kStages = 3;      // tiles in shared memory
-constexpr int kMaxCluster = 16;  // blocks of a cluster
 constexpr int kBounds = 512;    // bounds of sequences that a block keeps in shared memory
 
 // ------------------------------------------------------------------ what a lane works on
@@ -1156,56 +1157,45 @@ cudaLaunchAttribute cluster_of(int c) {
 
 // A cluster beyond what the GPU has room for beside the others would wait for a second round (40
 // strips of clusters of 7, where 38 fit, took half as long again as clusters of 6), so the driver
-// is asked how many clusters of each size run at once, for each kernel and device the first time.
-struct Room {
-  int clusters[kMaxCluster + 1] = {};
-  cudaError_t err = cudaErrorUnknown;
-};
-
+// is asked how many clusters of each size run at once, for each kernel and device the first time that
+// this succeeds.  Sizes that it refuses are left out.
 template <auto KERNEL, int CH, int ARRAYS>
-const Room* room_for() {
-  static Room rooms[64];
-  static std::once_flag once[64];
+const ClusterRoom* room_for() {
+  static ClusterRoom rooms[64];
+  static std::atomic<bool> known[64];
+  static std::mutex mu;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-  std::call_once(once[dev], [&] {
-    Room& r = rooms[dev];
-    r.err = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 dynamic_bytes<CH>(ARRAYS, kMaxCluster));
-    if (r.err == cudaSuccess)
-      r.err = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    for (int c = 1; c <= kMaxCluster && r.err == cudaSuccess; ++c) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(c);
-      cfg.blockDim = dim3(kThreads);
-      cfg.dynamicSmemBytes = dynamic_bytes<CH>(ARRAYS, c);
-      cudaLaunchAttribute attr = cluster_of(c);
-      cfg.attrs = &attr;
-      cfg.numAttrs = 1;
-      r.err = cudaOccupancyMaxActiveClusters(&r.clusters[c], KERNEL, &cfg);
-    }
+  if (launched(cudaGetDevice(&dev)) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  if (known[dev].load(std::memory_order_acquire)) return &rooms[dev];
+  std::lock_guard<std::mutex> lock(mu);
+  if (known[dev].load(std::memory_order_relaxed)) return &rooms[dev];
+  if (launched(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    dynamic_bytes<CH>(ARRAYS, kMaxCluster))) != cudaSuccess)
+    return nullptr;
+  launched(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+  rooms[dev] = ask_room([](int c, int* n) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = dynamic_bytes<CH>(ARRAYS, c);
+    cudaLaunchAttribute attr = cluster_of(c);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return launched(cudaOccupancyMaxActiveClusters(n, KERNEL, &cfg)) == cudaSuccess;
   });
-  return launched(rooms[dev].err) == cudaSuccess ? &rooms[dev] : nullptr;
+  known[dev].store(true, std::memory_order_release);
+  return &rooms[dev];
 }
 
-// Launches KERNEL in as large clusters as can all run at once, up to 8 blocks; where these leave
-// room, sequences are parted.  Larger clusters (whose exchanges take longer) only where they put
-// more blocks to work: few channels in few sequences (65536 x 64, one sequence: 107 us in clusters
-// of 8, 63 us of 16; 65536 x 512, 24 sequences: 51 us of 8 and 89 us of 16).
+// Launches KERNEL.
 template <auto KERNEL, int CH, int ARRAYS, typename Args>
 int launch(int N, int D, int n_seq, Args& args, cudaStream_t stream) {
-  const Room* room = room_for<KERNEL, CH, ARRAYS>();
+  const ClusterRoom* room = room_for<KERNEL, CH, ARRAYS>();
   if (!room) return MOE_ERR_CUDA;
   const int strips = (D + 32 * CH - 1) / (32 * CH), tiles = (N + kTile - 1) / kTile;
-  const auto parts = [&](int c) {
-    return std::max(1, std::min({n_seq, tiles, room->clusters[c] / strips}));
-  };
-  int cluster = 1;
-  for (int c = 2; c <= std::min(kMaxCluster, tiles); ++c)
-    if (room->clusters[c] >= strips && (c <= 8 || c * parts(c) > cluster * parts(cluster)))
-      cluster = c;
-  args.cluster = cluster;
-  args.parts = parts(cluster);
+  const ClusterChoice choice = choose_clusters(*room, strips, tiles, n_seq);
+  const int cluster = args.cluster = choice.cluster;
+  args.parts = choice.parts;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster * args.parts, strips);
   cfg.blockDim = dim3(kThreads);
