@@ -104,8 +104,9 @@ int moe_gdr_backward(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, co
  *
  * Supported (else MOE_ERR_UNSUPPORTED): D a multiple of 8, at most 256; rotary_dim a multiple
  * of 16, at most D, 0 for no rotation (positions and inv_freq may then be NULL); at most 4096
- * heads in a group and 2^30 tokens; pointers 16-byte aligned; strides multiples of 8 values.  eps > 0.  Heads are addressed by strides (in
- * values), so q and k can be parts of one fused projection row; token t's head h starts at
+ * heads in a group and 2^30 tokens; pointers 16-byte aligned (positions and inv_freq as their types
+ * want it); strides multiples of 8 values.  eps > 0.  Heads are addressed by strides (in values), so
+ * q and k can be parts of one fused projection row; token t's head h starts at
  * t * token_stride + h * head_stride.  Input strides may be 0 (broadcast); rows of an output
  * must not overlap (MOE_ERR_INVALID_ARG).  y may be x, with the same strides, and dx may be x
  * or dy (of the same type, with the same strides); other overlaps of inputs and outputs give
@@ -169,7 +170,7 @@ int moe_qk_norm_rope_backward(int32_t N, int32_t D, int32_t rotary_dim, int32_t 
  * skipped and its o left as it was.  Any other value outside [0, n_slots) and every later
  * request with an earlier one's slot is skipped the same way and reported as MOE_ERR_BAD_INDEX
  * in *dev_status (may be NULL).  The products are plain fp32; deterministic.  q, k, v, o and S
- * must be 16-byte aligned, dk and dv in {64, 128}, B * H up to 2^24 and, with slot, B up to 65535
+ * must be 16-byte aligned (the rest as their types want it), dk and dv in {64, 128}, B * H up to 2^24 and, with slot, B up to 65535
  * (a request's slot is compared with all before it), else MOE_ERR_UNSUPPORTED. */
 int moe_gdr_step(int32_t B, int32_t H, int32_t dk, int32_t dv, const moe_bf16* q,
                  const moe_bf16* k, const moe_bf16* v, const float* beta, const float* g,

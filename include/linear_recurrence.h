@@ -27,9 +27,9 @@
  *   h0, h_T, dh_T, dh0 [n_seq, D] fp32: the state before a sequence's first row and after its
  *   last, and their gradients; each may be NULL (zero, or not wanted).  h_T may be h0: the
  *   states are then updated in place.  An empty sequence hands its h0 to h_T.
- * D up to 2^20, N up to 2^30 and n_seq up to 2^24 (else MOE_ERR_UNSUPPORTED), any alignment of
- * the values' own type; where the rows of all `dtype` tensors begin on 16-byte boundaries they are
- * copied by TMA, which is faster.  Apart from h_T over h0, outputs may not overlap inputs.
+ * D up to 2^20, N up to 2^30 and n_seq up to 2^24, every array aligned as its values' type wants
+ * it (else MOE_ERR_UNSUPPORTED); where the rows of all `dtype` tensors begin on 16-byte
+ * boundaries they are copied by TMA, which is faster.  Apart from h_T over h0, outputs may not overlap inputs.
  *
  * Waits inside the kernels are bounded; one that runs out ends that launch early, its outputs then
  * being incomplete, and is reported as MOE_ERR_TIMEOUT in *dev_status.  Nothing of it is under way

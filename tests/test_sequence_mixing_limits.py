@@ -118,3 +118,40 @@ def test_cluster_sizes_that_the_driver_refuses_are_left_out(choose):
     assert choose(holes, 1, 1000, 1) == (14, 1)
     none = [-1] * 17
     assert choose(none, 32, 1000, 10) == (1, 1)
+
+
+def glr(backward=False, **over):
+    a = dict(N=8, D=5, n_seq=2, off=FAKE, mode=0, dtype=0, g=FAKE, ld_g=5, x=FAKE, ld_x=5, h0=FAKE,
+             h=FAKE, h_T=FAKE, chunks=FAKE, dh=FAKE, dh_T=FAKE, dg=FAKE, dx=FAKE, dh0=FAKE,
+             status=FAKE)
+    a.update(over)
+    names = ["N", "D", "n_seq", "off", "mode", "dtype", "g", "ld_g", "x", "ld_x", "h0"]
+    names += ["chunks", "dh", "dh_T", "dg", "dx", "dh0"] if backward else ["h", "h_T", "chunks"]
+    call = moe.lib().moe_glr_backward if backward else moe.lib().moe_glr_forward
+    return call(*[a[n] for n in names + ["status"]], None)
+
+
+def test_addresses_off_their_types_boundary_are_refused():
+    """A kernel would fault on them."""
+    for off in (1, 2, 3):
+        at = FAKE + off
+        for n in ("off", "h0", "h_T", "chunks", "status"):
+            assert glr(**{n: at}) == UNSUPPORTED, n
+        for n in ("off", "h0", "chunks", "dh_T", "dh0", "status"):
+            assert glr(backward=True, **{n: at}) == UNSUPPORTED, n
+        for n in ("beta", "g", "slot", "status"):
+            assert gdr_step(**{n: at}) == UNSUPPORTED, n
+        for slot, state, status in ((at, FAKE, None), (FAKE, at, None), (FAKE, FAKE, at)):
+            assert moe.lib().moe_glr_step(4, 5, 0, 0, FAKE, 5, FAKE, 5, slot, 4, state, FAKE, status,
+                                          None) == UNSUPPORTED
+    rows = moe.moe_qk_rows(x=FAKE, x_token_stride=256, x_head_stride=64, y=FAKE, y_token_stride=256,
+                           y_head_stride=64, heads=4)
+    grads = moe.moe_qk_grads(x=FAKE, x_token_stride=256, x_head_stride=64, dy=FAKE,
+                             dy_token_stride=256, dy_head_stride=64, dx=FAKE, dx_token_stride=256,
+                             dx_head_stride=64, heads=4)
+    for pos, freq in ((FAKE + 2, FAKE), (FAKE, FAKE + 4)):
+        assert moe.lib().moe_qk_norm_rope(8, 64, 64, 0, 0, 1e-6, pos, freq, ctypes.byref(rows), None,
+                                          None) == UNSUPPORTED
+        assert moe.lib().moe_qk_norm_rope_backward(8, 64, 64, 0, 0, 1, 1e-6, pos, freq,
+                                                   ctypes.byref(grads), None, None, 0,
+                                                   None) == UNSUPPORTED

@@ -127,10 +127,13 @@ extern "C" int moe_gdr_step(int32_t B, int32_t H, int32_t dk, int32_t dv, const 
   if (!((dk == 64 || dk == 128) && (dv == 64 || dv == 128))) return MOE_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * H > (1ll << 24)) return MOE_ERR_UNSUPPORTED;
   if (slot && B > kMaxSlots) return MOE_ERR_UNSUPPORTED;
-  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) |
-       reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(S) |
-       reinterpret_cast<uintptr_t>(o)) & 15u)
-    return MOE_ERR_UNSUPPORTED;
+  for (const void* p : {static_cast<const void*>(q), static_cast<const void*>(k),
+                        static_cast<const void*>(v), static_cast<const void*>(S),
+                        static_cast<const void*>(o)})
+    if (misaligned(p, 16)) return MOE_ERR_UNSUPPORTED;
+  for (const void* p : {static_cast<const void*>(beta), static_cast<const void*>(g),
+                        static_cast<const void*>(slot), static_cast<const void*>(dev_status)})
+    if (misaligned(p, 4)) return MOE_ERR_UNSUPPORTED;
   const auto* q_ = reinterpret_cast<const __nv_bfloat16*>(q);
   const auto* k_ = reinterpret_cast<const __nv_bfloat16*>(k);
   const auto* v_ = reinterpret_cast<const __nv_bfloat16*>(v);

@@ -1122,8 +1122,9 @@ Waits waits_of(int* dev_status) {
   return w;
 }
 
-bool misaligned(const void* p, int size) {
-  return reinterpret_cast<uintptr_t>(p) & static_cast<unsigned>(size - 1);
+// Of fp32 and int32 arrays.
+bool misaligned_words(std::initializer_list<const void*> ptrs) {
+  return std::any_of(ptrs.begin(), ptrs.end(), [](const void* p) { return misaligned(p, 4); });
 }
 
 int check_rows(int N, int D, int n_seq, const int* seq_off, int mode, int dtype, const void* g,
@@ -1256,6 +1257,7 @@ int moe_glr_forward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off,
                     const float* h0, void* h, float* h_T, float* h_chunks, int32_t* dev_status,
                     moe_stream_t stream) {
   if (int e = check_rows(N, D, n_seq, seq_off, mode, dtype, g, ld_g, x, ld_x, h, false)) return e;
+  if (misaligned_words({seq_off, h0, h_T, h_chunks, dev_status})) return MOE_ERR_UNSUPPORTED;
   if (N == 1) ld_g = ld_x = D;  // whatever they are
   const Packed seq{N, n_seq, seq_off, seq_off ? 0 : N / n_seq};
   mark_before(MOE_KERNEL_GLR_FWD, stream);
@@ -1287,7 +1289,9 @@ int moe_glr_backward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off
   if (int e = check_rows(N, D, n_seq, seq_off, mode, dtype, g, ld_g, x, ld_x, dg, true)) return e;
   if (!h_chunks || !dh || !dx) return MOE_ERR_INVALID_ARG;
   const int size = dtype == MOE_BF16 ? 2 : 4;
-  if (misaligned(dh, size) || misaligned(dx, size)) return MOE_ERR_UNSUPPORTED;
+  if (misaligned(dh, size) || misaligned(dx, size) ||
+      misaligned_words({seq_off, h0, h_chunks, dh_T, dh0, dev_status}))
+    return MOE_ERR_UNSUPPORTED;
   if (N == 1) ld_g = ld_x = D;
   const Packed seq{N, n_seq, seq_off, seq_off ? 0 : N / n_seq};
   mark_before(MOE_KERNEL_GLR_BWD, stream);
@@ -1323,6 +1327,7 @@ int moe_glr_step(int32_t B, int32_t D, int32_t mode, int32_t dtype, const void* 
                  void* h, int32_t* dev_status, moe_stream_t stream) {
   if (int e = check_rows(B, D, 1, nullptr, mode, dtype, g, ld_g, x, ld_x, h, false)) return e;
   if (!state || n_slots <= 0 || (!slot && B > n_slots)) return MOE_ERR_INVALID_ARG;
+  if (misaligned_words({slot, state, dev_status})) return MOE_ERR_UNSUPPORTED;
   if (B > kMaxSlots) return MOE_ERR_UNSUPPORTED;  // (and no more fit a grid's second dimension)
   // four channels to a thread where every row begins on the boundary of four values (64 requests x
   // 4096 channels, bf16: 4.5 us with one, 3.6 us with four; 512 requests: 12.8 and 6.9)

@@ -14,6 +14,11 @@ namespace moe {
 // Bounded device-side waits give up after this much wall time (ns).
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
 
+// Whether an address is off a boundary of `size` bytes (a power of two); NULL is not.
+inline bool misaligned(const void* p, int size) {
+  return reinterpret_cast<uintptr_t>(p) & static_cast<unsigned>(size - 1);
+}
+
 inline size_t up256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
 // Entry-point helpers shared by the files of the C ABI (defined in capi.cu).

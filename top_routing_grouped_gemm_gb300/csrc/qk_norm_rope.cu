@@ -446,7 +446,7 @@ Cuts cuts_of(int N, int D, int heads, int blocks_per_sm) {
   return c;
 }
 
-bool bad_align(const void* p) { return reinterpret_cast<uintptr_t>(p) & 15u; }
+bool bad_align(const void* p) { return misaligned(p, 16); }
 
 // Whether the rows [N, heads] of D values at these strides overlap.
 bool overlap(long long N, long long heads, long long D, long long ts, long long hs) {
@@ -463,6 +463,7 @@ int check_common(int N, int D, int rot, int dtype, float eps, const void* pos, c
   if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
   if (rot > 0 && (!pos || !freq)) return MOE_ERR_INVALID_ARG;
   if (D % 8 || D > kMaxD || rot % 16 || N > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+  if (misaligned(pos, 4) || misaligned(freq, 8)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
