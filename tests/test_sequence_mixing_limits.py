@@ -7,6 +7,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 from conftest import ROOT
 from top_routing_grouped_gemm_gb300 import build as B
@@ -155,3 +156,23 @@ def test_addresses_off_their_types_boundary_are_refused():
         assert moe.lib().moe_qk_norm_rope_backward(8, 64, 64, 0, 0, 1, 1e-6, pos, freq,
                                                    ctypes.byref(grads), None, None, 0,
                                                    None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("dtype", [7, -1, None])
+def test_binding_refuses_types_that_it_does_not_know(dtype):
+    """With the error that it raises for every other argument that is not what a call takes."""
+    z, x = torch.zeros((4, 8)), torch.zeros((4, 2, 64))
+    pos, freq = torch.arange(4, dtype=torch.int32), torch.ones(32, dtype=torch.float64)
+    q, f = dict(x=x, y=x, dy=x, dx=x), moe.MOE_F32
+    calls = [lambda: moe.moe_glr_forward(4, 8, 1, None, 0, dtype, z, z, None, z, None, None),
+             lambda: moe.moe_glr_backward(4, 8, 1, None, 0, dtype, z, z, None, z[:1], z, None, z, z,
+                                          None),
+             lambda: moe.moe_glr_step(4, 8, 0, dtype, z, z, None, 4, z, z),
+             lambda: moe.moe_qk_norm_rope(4, 64, 64, False, dtype, 1e-6, pos, freq, q, None),
+             lambda: moe.moe_qk_norm_rope_backward(4, 64, 64, False, dtype, f, 1e-6, pos, freq, q,
+                                                   None, None),
+             lambda: moe.moe_qk_norm_rope_backward(4, 64, 64, False, f, dtype, 1e-6, pos, freq, q,
+                                                   None, None)]
+    for call in calls:
+        with pytest.raises(ValueError, match="MOE_BF16 or MOE_F32"):
+            call()

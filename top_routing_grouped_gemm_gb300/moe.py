@@ -492,7 +492,12 @@ def moe_gdr_backward(B, T, H, dk, dv, q, k, v, beta, g, scale, d_o, dS_T, S_chun
                                   wp, wn, _stream(stream)))
 
 
-_DTYPES = {MOE_BF16: torch.bfloat16, MOE_F32: torch.float32}
+class _Types(dict):
+    def __missing__(self, code):
+        raise ValueError(f"dtype: MOE_BF16 or MOE_F32 is wanted, got {code!r}")
+
+
+_DTYPES = _Types({MOE_BF16: torch.bfloat16, MOE_F32: torch.float32})
 
 
 _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
