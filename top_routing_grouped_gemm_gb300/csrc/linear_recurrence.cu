@@ -138,7 +138,7 @@ __device__ __forceinline__ Vec<CH> decay_of(Vec<CH> g) {
 // the interpolation of (exp(g) - 1) / g at the five Chebyshev points of [-0.35, 0] (off by 1.4e-8
 // at most; 1.1e-7 with the roundings of fp32); beyond, the difference is off by 3.2e-7 at most.
 // One channel at a time: the packed instructions run on one of the two fp32 pipes alone, and this
-// is where they would fill it (32768 x 2048, mixed: 104 us packed, 90 us so).
+// is where they would fill it (32768 x 2048, mixed, 87 us: a sixth more time packed).
 __device__ __forceinline__ float one_minus(float g, float a) {
   float q = fmaf(-0.007211245596408844f, g, -0.04133187234401703f);
   q = fmaf(q, g, -0.16662530601024628f);
@@ -294,9 +294,9 @@ __device__ __forceinline__ void append(Pair<CH>& s, const Pair<CH>& p) {
   follow(s.H, p);
 }
 
-// The clusters' barriers wait for no memory: the first one orders the set-up of the mbarriers, which has
-// a fence of its own, the last one nothing (waiting for the copies and stores in flight there cost 1 us
-// of a launch).  A warp's threads, one of which may have copied tiles on its own, come there together.
+// The clusters' barriers wait for no memory: the first one orders the set-up of the mbarriers, the last
+// one the numbers of pairs sent, and both of these have fences of their own (waiting for the copies and
+// stores in flight there cost 1 us of a launch).  A warp's threads, one of which may have copied tiles on its own, come there together.
 __device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -604,12 +604,12 @@ __global__ void __launch_bounds__(kEmptyThreads)
 
 // ------------------------------------------------------------------ forward
 //
-// g and x are read once and h is written once.  32768 x 2048 bf16 take 70.2 us, 0.86 of the rate of
-// a plain copy (16276 x 2048 fp32 63.9 us, 0.94): what holds the bf16 form back is waiting, between
-// instructions (two channels to unpack and gate for each word) and for the other blocks, with 50 %
-// of the issue slots used.  24 sequences in as many rows take 82 us, as tiles with bounds go through
-// a path of their own.  (16 rows to a warp, without the pairs of the next tile in between, took 69.6 us
-// where this form then took 72.6, but 90 us where it took 83 with 24 sequences.)
+// g and x are read once and h is written once.  32768 x 2048 bf16 take 71.0 us, 0.85 of the rate of
+// a plain copy (16276 x 2048 fp32 64.1 us, 0.93): what holds the bf16 form back is waiting, between
+// instructions (two channels to unpack and gate for each word) and for the other blocks, with 53 %
+// of the issue slots used.  24 sequences in as many rows take 81 us, as tiles with bounds go through
+// a path of their own.  (16 rows to a warp, without the pairs of the next tile in between: 4 % less
+// time with one sequence, 8 % more with 24.)
 
 template <typename T>
 struct ForwardArgs {
@@ -788,10 +788,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 // block, by pairs of their own.
 //
 // g, x and dh are read once and dg and dx are written once.  8192 x 4096 bf16 in 6 sequences, mixed,
-// take 79 us after the forward's 45 us (123.7 us together, 0.65 of a copy's rate), bound by
-// instructions: 66 % of the issue slots, 79 % of the busiest scheduler's.  The gates are formed
+// take 79 us after the forward's 46 us (124.7 us together, 0.64 of a copy's rate), bound by
+// instructions: 65 % of the issue slots, 78 % of the busiest scheduler's.  The gates are formed
 // twice; holding them in registers until the pairs are known leaves no room for the overlap of two
-// tiles (4 us more).
+// tiles (3 % more).
 
 template <typename T>
 struct BackwardArgs {
@@ -1076,10 +1076,10 @@ __device__ __forceinline__ void set(__nv_bfloat16* p, const float (&v)[1]) {
   *p = __float2bfloat16_rn(v[0]);
 }
 
-// V channels to a thread; 64 requests x 4096 channels take 1.8 us in a graph of such steps, two
-// dependent round trips to memory, 512 requests 6.6 us (0.66 of a copy's rate).  Gates and inputs are
-// on their way while the request's row is looked up,
-// and the state while the requests before it are searched for the same row.
+// V channels to a thread; 64 requests x 4096 channels take 1.9 us in a graph of twelve steps, two
+// dependent round trips to memory; 512 requests 4.9 us (0.90 of a copy's rate; L2 holds their states).
+// Gates and inputs are on their way while the request's row is looked up, and the state while the
+// requests before it are searched for the same row.
 constexpr int kStepThreads = 128;
 
 template <typename T, bool MIX, int V>
@@ -1222,7 +1222,7 @@ int launch_empty(const Packed& seq, const float* from, float* to, int D, cudaStr
 
 // Calls f(T{}, channels per lane, mode, ASYNC) for the call's type.  Tensors whose rows all begin
 // on 16-byte boundaries (and do not share one row) are copied by TMA; a lane has two bf16 where they
-// all begin on 4-byte boundaries (8191 x 2046, forward: 62 us with one, 37 us with two).
+// all begin on 4-byte boundaries (8191 x 2046, forward: 62 us with one, 34 us with two).
 template <typename F>
 int dispatch(int mode, int dtype, std::initializer_list<const void*> ptrs,
              std::initializer_list<long long> strides, F f) {
@@ -1330,7 +1330,8 @@ int moe_glr_step(int32_t B, int32_t D, int32_t mode, int32_t dtype, const void* 
   if (misaligned_words({slot, state, dev_status})) return MOE_ERR_UNSUPPORTED;
   if (B > kMaxSlots) return MOE_ERR_UNSUPPORTED;  // (and no more fit a grid's second dimension)
   // four channels to a thread where every row begins on the boundary of four values (64 requests x
-  // 4096 channels, bf16: 4.5 us with one, 3.6 us with four; 512 requests: 12.8 and 6.9)
+  // 4096 channels, bf16, in a graph of twelve steps: 2.5 us with one, 1.9 us with four; 512 requests:
+  // 10.9 and 4.9)
   const int size = dtype == MOE_BF16 ? 2 : 4;
   const bool four = D % 4 == 0 && ld_g % 4 == 0 && ld_x % 4 == 0 && !misaligned(g, 4 * size) &&
                     !misaligned(x, 4 * size) && !misaligned(h, 4 * size) && !misaligned(state, 16);

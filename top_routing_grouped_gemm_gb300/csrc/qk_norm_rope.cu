@@ -16,7 +16,9 @@ namespace moe {
 namespace {
 
 constexpr int kMaxD = 256, kMaxHeads = 4096;
-constexpr int kSms = 152;  // of the GPU that the cuts are made for
+// Of the GPU that the cuts are made for.  (Not asked of the driver: the workspace's size follows from
+// the cuts, and has to be the same wherever and before whatever it is asked for.)
+constexpr int kSms = 152;
 
 // One group of heads (q or k) as the kernels see it.
 struct Side {
@@ -403,7 +405,8 @@ int rows_of(int D) { return kThreads / 32 * (32 / (D / 8)); }
 
 // Heads of a block: what leaves fewest lanes idle (of a block's lanes, and of the last part's
 // heads), against the angles that each part of the heads forms anew.  In instructions a row, about
-// 90 for each lane and 50 for each pair's angle.  (16 + 4 heads of 96, 16 rows to a block: two parts
+// 90 for each lane and 50 for each pair's angle, all values of a head taken as turned: the workspace's
+// size, which follows the same cut, is asked for without rotary_dim.  (16 + 4 heads of 96, 16 rows to a block: two parts
 // of 10 heads leave 3 / 8 of the lanes idle, four of 5 leave 1 / 16; the backward of 26041 tokens
 // in bf16 takes 125 and 108 us.)
 int heads_of_block(int D, int heads) {
