@@ -69,8 +69,8 @@ int moe_glr_forward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off,
                     const float* h0, void* h, float* h_T, float* h_chunks, int32_t* dev_status,
                     moe_stream_t stream);
 
-/* Backward: gradients of <dh, h> + <dh_T, h_T>.  h_chunks: the forward's (required); h_{t-1} is
- * formed again from it in fp32.  dg and dx have the strides of g and x (ld >= D).  No output may
+/* Backward: gradients of <dh, h> + <dh_T, h_T>.  h0: as the forward read it (a copy, where h_T
+ * went over it).  h_chunks: the forward's (required); h_{t-1} is formed again from it in fp32.  dg and dx have the strides of g and x (ld >= D).  No output may
  * overlap an input. */
 int moe_glr_backward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off, int32_t mode,
                      int32_t dtype, const void* g, int64_t ld_g, const void* x, int64_t ld_x,
