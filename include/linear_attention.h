@@ -170,8 +170,9 @@ int moe_qk_norm_rope_backward(int32_t N, int32_t D, int32_t rotary_dim, int32_t 
  * skipped and its o left as it was.  Any other value outside [0, n_slots) and every later
  * request with an earlier one's slot is skipped the same way and reported as MOE_ERR_BAD_INDEX
  * in *dev_status (may be NULL).  The products are plain fp32; deterministic.  q, k, v, o and S
- * must be 16-byte aligned (the rest as their types want it), dk and dv in {64, 128}, B * H up to 2^24 and, with slot, B up to 65535
- * (a request's slot is compared with all before it), else MOE_ERR_UNSUPPORTED. */
+ * must be 16-byte aligned (the rest as their types want it), dk and dv in {64, 128},
+ * B * H up to 2^24 and, with slot, B up to 65535 (a request's slot is compared with all before
+ * it), else MOE_ERR_UNSUPPORTED. */
 int moe_gdr_step(int32_t B, int32_t H, int32_t dk, int32_t dv, const moe_bf16* q,
                  const moe_bf16* k, const moe_bf16* v, const float* beta, const float* g,
                  const int32_t* slot, int32_t n_slots, float scale, float* S, moe_bf16* o,

@@ -29,7 +29,8 @@
  *   states are then updated in place.  An empty sequence hands its h0 to h_T.
  * D up to 2^20, N up to 2^30 and n_seq up to 2^24, every array aligned as its values' type wants
  * it (else MOE_ERR_UNSUPPORTED); where the rows of all `dtype` tensors begin on 16-byte
- * boundaries they are copied by TMA, which is faster.  Apart from h_T over h0, outputs may not overlap inputs.
+ * boundaries they are copied by TMA, which is faster.  Apart from h_T over h0, outputs may not
+ * overlap inputs.
  *
  * Waits inside the kernels are bounded; one that runs out ends that launch early, its outputs then
  * being incomplete, and is reported as MOE_ERR_TIMEOUT in *dev_status.  Nothing of it is under way
@@ -70,8 +71,8 @@ int moe_glr_forward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off,
                     moe_stream_t stream);
 
 /* Backward: gradients of <dh, h> + <dh_T, h_T>.  h0: as the forward read it (a copy, where h_T
- * went over it).  h_chunks: the forward's (required); h_{t-1} is formed again from it in fp32.  dg and dx have the strides of g and x (ld >= D).  No output may
- * overlap an input. */
+ * went over it).  h_chunks: the forward's (required); h_{t-1} is formed again from it in fp32.  dg
+ * and dx have the strides of g and x (ld >= D).  No output may overlap an input. */
 int moe_glr_backward(int32_t N, int32_t D, int32_t n_seq, const int32_t* seq_off, int32_t mode,
                      int32_t dtype, const void* g, int64_t ld_g, const void* x, int64_t ld_x,
                      const float* h0, const float* h_chunks, const void* dh, const float* dh_T,

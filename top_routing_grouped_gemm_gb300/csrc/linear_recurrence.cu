@@ -296,7 +296,8 @@ __device__ __forceinline__ void append(Pair<CH>& s, const Pair<CH>& p) {
 
 // The clusters' barriers wait for no memory: the first one orders the set-up of the mbarriers, the last
 // one the numbers of pairs sent, and both of these have fences of their own (waiting for the copies and
-// stores in flight there cost 1 us of a launch).  A warp's threads, one of which may have copied tiles on its own, come there together.
+// stores in flight there cost 1 us of a launch).  A warp's threads, one of which may have copied tiles
+// on its own, come there together.
 __device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
