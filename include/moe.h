@@ -417,7 +417,13 @@ enum moe_kernel_id {
   MOE_KERNEL_GLR_FWD = 19,      /* gated linear recurrence: forward               */
   MOE_KERNEL_GLR_BWD = 20,      /* gated linear recurrence: backward              */
   MOE_KERNEL_GLR_STEP = 21,     /* gated linear recurrence: one token             */
-  MOE_KERNEL_COUNT = 22
+  MOE_KERNEL_ROUTE_SELECT = 22, /* selection by scores, bias and groups           */
+  MOE_KERNEL_ROUTE_SELECT_BWD = 23, /* its gradient with respect to the logits    */
+  MOE_KERNEL_BLOCK_NORM = 24,   /* norms around a block, gate, residual sum       */
+  MOE_KERNEL_BLOCK_NORM_BWD = 25, /* their backward (with the weight gradients)   */
+  MOE_KERNEL_W4_GATEUP = 26,    /* 4-bit experts: slots by expert, gate/up, SwiGLU */
+  MOE_KERNEL_W4_DOWN = 27,      /* 4-bit experts: down, sum over a token's experts */
+  MOE_KERNEL_COUNT = 28
 };
 int moe_set_kernel_events(int kernel_id, void* event_before, void* event_after);
 long long moe_launch_count(void);

@@ -9,6 +9,8 @@
 #include "moe_internal.h"
 #include "route.h"
 
+#include "../../include/moe_block.h"
+
 using namespace moe;
 
 namespace moe {
@@ -203,13 +205,19 @@ int moe_route_from_logits(const moe_problem* p, const float* logits, int32_t* to
 
 namespace {
 
+// What follows the logits: the top-k kernel, its form fused with the product, or nothing.
+enum RouteTail { kRouteTopk, kRouteFused, kRouteLogits };
+
 int route_impl(const moe_problem* p, const moe_bf16* x, const float* w_router, const float* bias,
                int32_t* topk_idx, float* topk_gate, float* prob_partials, float* logits,
                void* workspace, size_t workspace_bytes, int32_t* dev_status,
-               moe_stream_t stream, bool fused) {
+               moe_stream_t stream, RouteTail tail) {
+  const bool fused = tail == kRouteFused;
   MOE_TRY(check_problem(p));
   if (fused && p->k > kRouteTileK) return MOE_ERR_UNSUPPORTED;
-  if (!x || !w_router || !topk_idx || !topk_gate || !prob_partials) return MOE_ERR_INVALID_ARG;
+  if (!x || !w_router) return MOE_ERR_INVALID_ARG;
+  if (tail == kRouteLogits ? !logits : (!topk_idx || !topk_gate || !prob_partials))
+    return MOE_ERR_INVALID_ARG;
   if (!al16(x) || !al16(w_router) || (logits && !al16(logits))) return MOE_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < route_ws(p)) return MOE_ERR_WORKSPACE;
   const int T = p->T, d = p->d, E = p->E;
@@ -249,6 +257,10 @@ int route_impl(const moe_problem* p, const moe_bf16* x, const float* w_router, c
   mark_before(MOE_KERNEL_ROUTER_GEMM, stream);
   MOE_CUDA(fused ? launch_gemm_router_topk(P, bn, stream) : launch_gemm_router(P, bn, stream));
   mark_after(MOE_KERNEL_ROUTER_GEMM, stream);
+  if (tail == kRouteLogits) {
+    count_launches(2);
+    return MOE_OK;
+  }
   mark_before(MOE_KERNEL_TOPK, stream);
   if (fused) {
     MOE_CUDA(launch_route_merge(L, cand, tile_max, T, E, p->k, nt, topk_idx, topk_gate,
@@ -268,7 +280,7 @@ int moe_route(const moe_problem* p, const moe_bf16* x, const float* w_router, co
               void* workspace, size_t workspace_bytes, int32_t* dev_status,
               moe_stream_t stream) {
   return route_impl(p, x, w_router, bias, topk_idx, topk_gate, prob_partials, logits, workspace,
-                    workspace_bytes, dev_status, stream, false);
+                    workspace_bytes, dev_status, stream, kRouteTopk);
 }
 
 int moe_route_fused_topk(const moe_problem* p, const moe_bf16* x, const float* w_router,
@@ -276,7 +288,14 @@ int moe_route_fused_topk(const moe_problem* p, const moe_bf16* x, const float* w
                          float* prob_partials, float* logits, void* workspace,
                          size_t workspace_bytes, int32_t* dev_status, moe_stream_t stream) {
   return route_impl(p, x, w_router, bias, topk_idx, topk_gate, prob_partials, logits, workspace,
-                    workspace_bytes, dev_status, stream, true);
+                    workspace_bytes, dev_status, stream, kRouteFused);
+}
+
+int moe_route_logits(const moe_problem* p, const moe_bf16* x, const float* w_router,
+                     const float* bias, float* logits, void* workspace, size_t workspace_bytes,
+                     int32_t* dev_status, moe_stream_t stream) {
+  return route_impl(p, x, w_router, bias, nullptr, nullptr, nullptr, logits, workspace,
+                    workspace_bytes, dev_status, stream, kRouteLogits);
 }
 
 // ------------------------------------------------------------------------ dispatch
@@ -942,6 +961,23 @@ int moe_dispatch_route_bwd(const moe_problem* p, const moe_bf16* dx_perm,
   mark_before(MOE_KERNEL_DISPATCH_ROUTE_BWD, stream);
   const int st = cuda_status(launch_dispatch_route_bwd(
       reinterpret_cast<const __nv_bfloat16*>(dx_perm), slot_row, topk_idx, topk_gate, dgate,
+      w_router, p->T, p->d, p->E, p->k, dx, stream));
+  mark_after(MOE_KERNEL_DISPATCH_ROUTE_BWD, stream);
+  return st;
+}
+
+int moe_dispatch_logits_bwd(const moe_problem* p, const moe_bf16* dx_perm,
+                            const int32_t* slot_row, const int32_t* topk_idx,
+                            const float* dlogits_topk, const float* w_router, float* dx,
+                            moe_stream_t stream) {
+  MOE_TRY(check_problem(p));
+  if (!dx_perm || !slot_row || !topk_idx || !dlogits_topk || !w_router || !dx)
+    return MOE_ERR_INVALID_ARG;
+  if (!al16(dx_perm) || !al16(w_router) || !al16(dx)) return MOE_ERR_UNSUPPORTED;
+  count_launches(1);
+  mark_before(MOE_KERNEL_DISPATCH_ROUTE_BWD, stream);
+  const int st = cuda_status(launch_dispatch_route_bwd(
+      reinterpret_cast<const __nv_bfloat16*>(dx_perm), slot_row, topk_idx, nullptr, dlogits_topk,
       w_router, p->T, p->d, p->E, p->k, dx, stream));
   mark_after(MOE_KERNEL_DISPATCH_ROUTE_BWD, stream);
   return st;

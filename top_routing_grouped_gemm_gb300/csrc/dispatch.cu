@@ -379,14 +379,14 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_route_bwd_kernel(
     if (lane < k) {
       const size_t slot = static_cast<size_t>(t) * k + lane;
       r = slot_row[slot];
-      g = gate[slot];
+      g = gate ? gate[slot] : 1.f;
       dg = dgate[slot];
       e = idx[slot];
       if (e < 0 || e >= E) { e = 0; g = 0.f; }
     }
     const float sgd = warp_sum_f(g * dg);
     rows[lane] = r;
-    cs[lane] = g * (dg - sgd);
+    cs[lane] = gate ? g * (dg - sgd) : (g != 0.f ? dg : 0.f);
     es[lane] = e;
   }
   __syncthreads();

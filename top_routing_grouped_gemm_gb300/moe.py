@@ -29,6 +29,8 @@ c_sz = ctypes.c_size_t
 
 MOE_BF16, MOE_F32 = 0, 1          # moe_dtype
 MOE_GLR_ADD, MOE_GLR_MIX = 0, 1   # moe_glr_mode
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1  # moe_score
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_VALUE = 0, 1, 2, 3  # moe_gate
 
 MOE_OK = 0
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
@@ -72,6 +74,30 @@ class moe_qk_grads(ctypes.Structure):
                 ("dx", c_vp), ("dx_token_stride", c_i64), ("dx_head_stride", c_i64),
                 ("weight", c_vp), ("dweight", c_vp), ("weight_per_head", c_i32),
                 ("heads", c_i32)]
+
+
+class moe_route_rule(ctypes.Structure):
+    _fields_ = [("score", c_i32), ("groups", c_i32), ("groups_kept", c_i32),
+                ("group_best", c_i32), ("renormalise", c_i32), ("scale", ctypes.c_float)]
+
+
+class moe_block_in(ctypes.Structure):
+    _fields_ = [("N", c_i32), ("D", c_i32), ("stream_dtype", c_i32), ("dtype", c_i32),
+                ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("gate_kind", c_i32),
+                ("gate_sigmoid", c_i32), ("post_norm", c_i32), ("x", c_vp), ("ld_x", c_i64),
+                ("y", c_vp), ("ld_y", c_i64), ("gate", c_vp), ("ld_gate", c_i64),
+                ("w_post", c_vp), ("w_pre", c_vp)]
+
+
+class moe_block_grads(ctypes.Structure):
+    _fields_ = [("dz", c_vp), ("ld_dz", c_i64), ("dn", c_vp), ("ld_dn", c_i64),
+                ("dn_dtype", c_i32), ("dx", c_vp), ("ld_dx", c_i64), ("dy", c_vp),
+                ("ld_dy", c_i64), ("dgate", c_vp), ("ld_dgate", c_i64), ("dw_post", c_vp),
+                ("dw_pre", c_vp)]
+
+
+class moe_w4(ctypes.Structure):
+    _fields_ = [("codes", c_vp), ("scales", c_vp), ("group", c_i32), ("has_zeros", c_i32)]
 
 
 _P = ctypes.POINTER(moe_problem)
@@ -144,6 +170,19 @@ _SIGS = {
                                         c_vp, c_vp]),
     "moe_glr_step": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp,
                                     c_i32, c_vp, c_vp, c_vp, c_vp]),
+    "moe_route_select": (ctypes.c_int, [c_i32, c_i32, c_i32, c_vp, c_i32, c_vp, c_i64, c_vp, c_vp,
+                                        c_vp, c_vp, c_vp]),
+    "moe_route_select_backward": (ctypes.c_int, [c_i32, c_i32, c_i32, c_vp, c_i32, c_vp, c_i64,
+                                                 c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "moe_route_logits": (ctypes.c_int, [_P, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
+    "moe_dispatch_logits_bwd": (ctypes.c_int, [_P, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "moe_block_norm": (ctypes.c_int, [c_vp, c_vp, c_i64, c_vp, c_i64, c_vp]),
+    "moe_block_norm_backward_workspace_size": (c_sz, [c_i32, c_i32, c_i32]),
+    "moe_block_norm_backward": (ctypes.c_int, [c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "moe_w4_pack": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "moe_w4_expert_ffn_workspace_size": (c_sz, [_P]),
+    "moe_w4_expert_ffn": (ctypes.c_int, [_P, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz,
+                                         c_vp, c_vp]),
     "moe_set_kernel_events": (ctypes.c_int, [ctypes.c_int, c_vp, c_vp]),
     "moe_launch_count": (ctypes.c_longlong, []),
     "moe_selftest_wait_timeout": (ctypes.c_int, [c_vp, c_i32, c_vp]),
@@ -154,7 +193,9 @@ KERNEL_IDS = {"router_gemm": 0, "topk": 1, "dispatch": 2, "gateup_gemm": 3, "dow
               "combine": 5, "bwd_dh_gemm": 6, "bwd_dx_gemm": 7, "wgrad": 8, "gdr_chunk": 9,
               "gdr_scan": 10, "gdr_bwd": 11, "combine_bwd": 12, "dispatch_route_bwd": 13,
               "gdr_bwd_factors": 14, "gdr_bwd_scan": 15, "qk_norm_rope": 16, "qk_norm_rope_bwd": 17,
-              "gdr_step": 18, "glr_fwd": 19, "glr_bwd": 20, "glr_step": 21}
+              "gdr_step": 18, "glr_fwd": 19, "glr_bwd": 20, "glr_step": 21,
+              "route_select": 22, "route_select_bwd": 23, "block_norm": 24, "block_norm_bwd": 25,
+              "w4_gateup": 26, "w4_down": 27}
 
 _lib = None
 
@@ -709,6 +750,199 @@ def moe_glr_step(B, D, mode, dtype, g, x, slot, n_slots, state, h, dev_status=No
                               _tensor("state", state, torch.float32, (n_slots, D), dev),
                               _tensor("h", h, dt, rows, dev), _status(dev_status, dev),
                               _stream_of(stream, dev)))
+
+
+# ---- around the experts (include/moe_block.h)
+
+class RouteRule:
+    """How moe_route_select makes experts and gates of logits."""
+
+    def __init__(self, score, groups=1, groups_kept=1, group_best=1, renormalise=True, scale=1.0):
+        self.score, self.groups, self.groups_kept = score, groups, groups_kept
+        self.group_best, self.renormalise, self.scale = group_best, renormalise, scale
+        self._c = moe_route_rule(score, groups, groups_kept, group_best, 1 if renormalise else 0,
+                                 scale)
+
+    def c(self):
+        return ctypes.addressof(self._c)
+
+
+def moe_route_select(T, E, k, rule, dtype, logits, select_bias, topk_idx, topk_gate,
+                     prob_partials, stream=None):
+    """select_bias and prob_partials may be None; logits may have any row stride."""
+    f32, dev = torch.float32, _device()
+    _check("moe_route_select",
+           lib().moe_route_select(T, E, k, rule.c(), dtype,
+                                  *_rows("logits", logits, _DTYPES[dtype], (T, E), dev),
+                                  _tensor("select_bias", select_bias, f32, (E,), dev, True),
+                                  _tensor("topk_idx", topk_idx, torch.int32, (T, k), dev),
+                                  _tensor("topk_gate", topk_gate, f32, (T, k), dev),
+                                  _tensor("prob_partials", prob_partials, f32, ((T + 7) // 8, E),
+                                          dev, True), _stream_of(stream, dev)))
+
+
+def moe_route_select_backward(T, E, k, rule, dtype, logits, topk_idx, dgate, dlogits,
+                              dlogits_topk, dev_status=None, stream=None):
+    """One of dlogits [T, E] and dlogits_topk [T, k] may be None."""
+    dt, f32, dev = _DTYPES[dtype], torch.float32, _device()
+    _check("moe_route_select_backward",
+           lib().moe_route_select_backward(
+               T, E, k, rule.c(), dtype, *_rows("logits", logits, dt, (T, E), dev),
+               _tensor("topk_idx", topk_idx, torch.int32, (T, k), dev),
+               _tensor("dgate", dgate, f32, (T, k), dev),
+               _tensor("dlogits", dlogits, dt, (T, E), dev, True),
+               _tensor("dlogits_topk", dlogits_topk, f32, (T, k), dev, True),
+               _status(dev_status, dev), _stream_of(stream, dev)))
+
+
+def moe_route_logits(p, x, w_router, bias, logits, workspace, dev_status=None, stream=None):
+    bf, f32, dev = torch.bfloat16, torch.float32, _device()
+    wp, wn = _ws(workspace)
+    _check("moe_route_logits",
+           lib().moe_route_logits(p.c(), _tensor("x", x, bf, (p.T, p.d), dev),
+                                  _tensor("w_router", w_router, f32, (p.E, p.d), dev),
+                                  _tensor("bias", bias, f32, (p.E,), dev, True),
+                                  _tensor("logits", logits, f32, (p.T, p.E), dev), wp, wn,
+                                  _status(dev_status, dev), _stream_of(stream, dev)))
+
+
+def moe_dispatch_logits_bwd(p, dx_perm, slot_row, topk_idx, dlogits_topk, w_router, dx,
+                            stream=None):
+    _check("moe_dispatch_logits_bwd",
+           lib().moe_dispatch_logits_bwd(p.c(), _ptr(dx_perm), _ptr(slot_row), _ptr(topk_idx),
+                                         _ptr(dlogits_topk), _ptr(w_router), _ptr(dx),
+                                         _stream(stream)))
+
+
+_GATE_SHAPES = {MOE_GATE_NONE: lambda N, D: None, MOE_GATE_CHANNEL: lambda N, D: (D,),
+                MOE_GATE_TOKEN: lambda N, D: (N,), MOE_GATE_VALUE: lambda N, D: (N, D)}
+
+
+def _optional_rows(name, t, dtype, shape, dev):
+    return (None, 0) if t is None else _rows(name, t, dtype, shape, dev)
+
+
+def _block_gate(name, gate, kind, dtype, N, D, dev):
+    """(address, row stride) of a gate or its gradient."""
+    if kind not in _GATE_SHAPES:
+        raise ValueError(f"gate_kind: one of the MOE_GATE_ codes is wanted, got {kind!r}")
+    if gate is None:
+        return None, 0
+    if kind == MOE_GATE_VALUE:
+        return _rows(name, gate, dtype, (N, D), dev)
+    return _tensor(name, gate, torch.float32, _GATE_SHAPES[kind](N, D), dev), 0
+
+
+def _block_in(N, D, stream_dtype, dtype, eps, scale, x, y, gate_kind, gate_sigmoid, gate,
+              post_norm, w_post, w_pre, dev):
+    st, dt, f32 = _DTYPES[stream_dtype], _DTYPES[dtype], torch.float32
+    return moe_block_in(N, D, stream_dtype, dtype, eps, scale, gate_kind, 1 if gate_sigmoid else 0,
+                        1 if post_norm else 0, *_rows("x", x, st, (N, D), dev),
+                        *_optional_rows("y", y, dt, (N, D), dev),
+                        *_block_gate("gate", gate, gate_kind, dt, N, D, dev),
+                        _tensor("w_post", w_post, f32, (D,), dev, True),
+                        _tensor("w_pre", w_pre, f32, (D,), dev, True))
+
+
+def moe_block_norm(N, D, stream_dtype, dtype, eps, scale, x, y, gate_kind, gate_sigmoid, gate,
+                   post_norm, w_post, w_pre, z, n, stream=None):
+    """x, y, z, n and a gate [N, D] may have any row strides; y, gate, w_post, w_pre, z, n may be
+    None as moe_block.h says."""
+    dev = _device()
+    block = _block_in(N, D, stream_dtype, dtype, eps, scale, x, y, gate_kind, gate_sigmoid, gate,
+                      post_norm, w_post, w_pre, dev)
+    _check("moe_block_norm",
+           lib().moe_block_norm(ctypes.addressof(block),
+                                *_optional_rows("z", z, _DTYPES[stream_dtype], (N, D), dev),
+                                *_optional_rows("n", n, _DTYPES[dtype], (N, D), dev),
+                                _stream_of(stream, dev)))
+
+
+def moe_block_norm_backward_workspace_size(N, D, gate_kind) -> int:
+    return lib().moe_block_norm_backward_workspace_size(N, D, gate_kind)
+
+
+def moe_block_norm_backward(N, D, stream_dtype, dtype, eps, scale, x, y, gate_kind, gate_sigmoid,
+                            gate, post_norm, w_post, w_pre, dz, dn_dtype, dn, dx, dy, dgate,
+                            dw_post, dw_pre, workspace, stream=None):
+    """The forward's inputs, then gradients (dz, dn in; the others out, None where not wanted)."""
+    st, dt, f32, dev = _DTYPES[stream_dtype], _DTYPES[dtype], torch.float32, _device()
+    block = _block_in(N, D, stream_dtype, dtype, eps, scale, x, y, gate_kind, gate_sigmoid, gate,
+                      post_norm, w_post, w_pre, dev)
+    rows, wp_wn = (N, D), _ws(workspace)
+    grads = moe_block_grads(*_optional_rows("dz", dz, st, rows, dev),
+                            *_optional_rows("dn", dn, _DTYPES[dn_dtype], rows, dev), dn_dtype,
+                            *_rows("dx", dx, st, rows, dev),
+                            *_optional_rows("dy", dy, dt, rows, dev),
+                            *_block_gate("dgate", dgate, gate_kind, dt, N, D, dev),
+                            _tensor("dw_post", dw_post, f32, (D,), dev, True),
+                            _tensor("dw_pre", dw_pre, f32, (D,), dev, True))
+    _check("moe_block_norm_backward",
+           lib().moe_block_norm_backward(ctypes.addressof(block), ctypes.addressof(grads), *wp_wn,
+                                         _stream_of(stream, dev)))
+
+
+def moe_w4_pack(E, rows, cols, group, codes, scales, zeros, packed_codes, packed_scales,
+                stream=None):
+    """codes [E, rows, cols / 2], zeros and packed_codes uint8, scales bf16; packed_scales as many
+    uint8 as its entries take."""
+    u8, dev = torch.uint8, _device()
+    shape = (E, rows, cols // group)
+    _check("moe_w4_pack",
+           lib().moe_w4_pack(E, rows, cols, group, _tensor("codes", codes, u8, (E, rows, cols // 2),
+                                                           dev),
+                             _tensor("scales", scales, torch.bfloat16, shape, dev),
+                             _tensor("zeros", zeros, u8, shape, dev, True),
+                             _tensor("packed_codes", packed_codes, u8, (E * rows * cols // 2,),
+                                     dev),
+                             _tensor("packed_scales", packed_scales, u8,
+                                     (E * rows * (cols // group) * (2 if zeros is None else 4),),
+                                     dev), _stream_of(stream, dev)))
+
+
+class W4Weights:
+    """4-bit weights [E, rows, cols], laid out for moe_w4_expert_ffn: codes [E, rows, cols / 2] (two
+    to a byte, the lower four bits first), scales [E, rows, cols / group] bf16, zeros like scales
+    (uint8) or None (8)."""
+
+    def __init__(self, codes, scales, zeros=None, stream=None):
+        if codes.dim() != 3 or scales.dim() != 3 or scales.shape[2] == 0:
+            raise ValueError("codes [E, rows, cols / 2] and scales [E, rows, cols / group] are wanted")
+        self.E, self.rows, self.cols = codes.shape[0], codes.shape[1], codes.shape[2] * 2
+        self.group = self.cols // scales.shape[2]
+        entries = scales.numel() * (2 if zeros is None else 4)
+        self.codes = torch.empty(codes.numel(), dtype=torch.uint8, device=codes.device)
+        self.scales = torch.empty(entries, dtype=torch.uint8, device=codes.device)
+        moe_w4_pack(self.E, self.rows, self.cols, self.group, codes, scales, zeros, self.codes,
+                    self.scales, stream)
+        self._c = moe_w4(self.codes.data_ptr(), self.scales.data_ptr(), self.group,
+                         0 if zeros is None else 1)
+
+    def c(self, name, shape, dev):
+        if (self.E, self.rows, self.cols) != shape or self.codes.get_device() != dev:
+            raise ValueError(f"{name}: weights {shape} on the current device are wanted, got "
+                             f"{(self.E, self.rows, self.cols)} on {self.codes.device}")
+        return ctypes.addressof(self._c)
+
+
+def moe_w4_expert_ffn_workspace_size(p: Problem) -> int:
+    return lib().moe_w4_expert_ffn_workspace_size(p.c())
+
+
+def moe_w4_expert_ffn(p, x, topk_idx, topk_gate, w_gate, w_up, w_down, y, workspace,
+                      dev_status=None, stream=None):
+    """w_gate, w_up [E, F, d] and w_down [E, d, F]: W4Weights."""
+    bf, dev = torch.bfloat16, _device()
+    wp, wn = _ws(workspace)
+    _check("moe_w4_expert_ffn",
+           lib().moe_w4_expert_ffn(p.c(), _tensor("x", x, bf, (p.T, p.d), dev),
+                                   _tensor("topk_idx", topk_idx, torch.int32, (p.T, p.k), dev),
+                                   _tensor("topk_gate", topk_gate, torch.float32, (p.T, p.k), dev),
+                                   w_gate.c("w_gate", (p.E, p.F, p.d), dev),
+                                   w_up.c("w_up", (p.E, p.F, p.d), dev),
+                                   w_down.c("w_down", (p.E, p.d, p.F), dev),
+                                   _tensor("y", y, bf, (p.T, p.d), dev), wp, wn,
+                                   _status(dev_status, dev), _stream_of(stream, dev)))
 
 
 def moe_set_kernel_events(kernel, before, after):
