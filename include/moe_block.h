@@ -183,13 +183,16 @@ int moe_block_norm_backward(const moe_block_in* in, const moe_block_grads* grads
  *   h_j  = silu(W_gate[e_j] x_t) * (W_up[e_j] x_t),   e_j = topk_idx[t, j]
  *   y_t  = sum_j topk_gate[t, j] * W_down[e_j] h_j
  *
- * Products and sums are fp32 (each product exact: codes less zeros, as bf16, times bf16); h is kept in two bf16
- * pieces (2^-16 of it); y is rounded once.  p gives T, d, E, k and F; r has to be 0 (adapters are
+ * Sums are fp32; each product is exact: x and h are scaled by powers of two for each 64 values and
+ * taken as fp16, x in one part (bf16 values that are less than 2^-28 of the largest of their 64
+ * lose bits), h in two (to 2^-23 of it); y is rounded once.  A value of x or h that is not finite
+ * makes its token's y NaN.  p gives T, d, E, k and F; r has to be 0 (adapters are
  * not part of it) and the capacity is not used: every slot is computed.  Entries of topk_idx
  * outside [0, E) are reported as MOE_ERR_BAD_INDEX in *dev_status (may be NULL) and contribute
  * nothing; a token may name an expert twice.
- * Supported (else MOE_ERR_UNSUPPORTED): p as everywhere (d and F multiples of 64), T * k up to
- * 16384, group 32, 64 or 128 and a divisor of d and of F, packed arrays, x and y 16-byte aligned.
+ * Supported (else MOE_ERR_UNSUPPORTED): p as everywhere (d and F multiples of 64, and up to 2^20
+ * here), T * k up to 16384; group 32, 64 or 128, a divisor of d and of F; group and has_zeros the
+ * same for all three; packed arrays, x, y and the workspace 16-byte aligned.
  *
  * moe_w4_pack lays weights [E, rows, cols] out for it, once (cols: what a product sums over).
  * codes [E, rows, cols / 2]: two codes to a byte, the lower four bits first; scales

@@ -542,14 +542,24 @@ def run_w4(case, w, x, idx, gate, status=None):
 
 # Sums on the tensor cores: exact products of a group are added in group / 16 steps of a few roundings
 # each (counted as 4 of half a step, whether they round or cut off), times the scale, over cols / 512
-# or so tiles a warp and 8 warps.
+# or so tiles a warp and 8 warps.  The products may be those of 16 + code, 16 + zero times the sum of the
+# values being taken off afterwards: the sizes of both count, not that of their difference.
 def product_count(cols, group):
     return 4 * group / 16 + 2 * cols / 512 + 16
+
+
+def w4_sizes(codes, scales, zeros):
+    """(16 + code + 16 + zero) scale: what the sums of a product are made of."""
+    code = MB.w4_values(codes, np.ones(scales.shape), np.zeros(scales.shape, np.uint8))
+    group = code.shape[-1] // scales.shape[-1]
+    zero = 8.0 if zeros is None else np.repeat(zeros.astype(float), group, -1)
+    return (32 + code + zero) * np.repeat(scales, group, -1)
 
 
 def check_w4(case, w, x, idx, gate, y):
     T, d, E, k, F, group = case[:6]
     W = [MB.w4_values(m[0].numpy(), f64(m[1]), None if m[2] is None else m[2].numpy()) for m in w]
+    sizes = [w4_sizes(m[0].numpy(), f64(m[1]), None if m[2] is None else m[2].numpy()) for m in w]
     x, g, idx = f64(x), f64(gate), idx.numpy()
     value, error = np.zeros((T, d)), np.zeros((T, d))
     for t in range(T):
@@ -557,7 +567,7 @@ def check_w4(case, w, x, idx, gate, y):
             e = idx[t, j]
             if not 0 <= e < E:
                 continue
-            a, b = (Rounded(W[i][e] @ x[t], product_count(d, group) * U * (np.abs(W[i][e]) @ np.abs(x[t])))
+            a, b = (Rounded(W[i][e] @ x[t], product_count(d, group) * U * (sizes[i][e] @ np.abs(x[t])))
                     for i in (0, 1))
             h = a * a.sigmoid() * b
             h = Rounded(h.v, h.e + 2.0 ** -16 * np.abs(h.v))  # two pieces

@@ -246,7 +246,7 @@ def problem(**change):
     (dict(idx=FAKE + 2), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(ws_bytes=64), WORKSPACE),
     (dict(ws=FAKE + 8), UNSUPPORTED), (dict(p=problem(T=0)), INVALID), (dict(p=problem(d=100)), UNSUPPORTED),
     (dict(p=problem(r=8)), UNSUPPORTED), (dict(p=problem(T=4097)), UNSUPPORTED),
-    (dict(p=problem(E=1025)), UNSUPPORTED),
+    (dict(p=problem(E=1025)), UNSUPPORTED), (dict(p=problem(d=(1 << 20) + 64)), UNSUPPORTED),
 ])
 def test_w4_refuses(change, status):
     assert w4(**change) == status
@@ -291,5 +291,5 @@ def test_limits_are_documented():
     with open(B.ROOT + "/include/moe_block.h") as f:
         text = " ".join(f.read().split())
     for words in ("E <= 1024, k <= 32, groups <= 32, T up to 2^24", "D a multiple of 8, at most 16384",
-                  "T * k up to * 16384"):
+                  "T * k up to 16384"):
         assert words in text, words

@@ -1,9 +1,17 @@
 // The experts' products with 4-bit weights for few tokens (include/moe_block.h has the formulas).
 //
 // A weight w = s (c - z) is read once for all rows (tokens) of its expert, and the time is that of
-// reading.  The products run on the tensor cores with 16 weight rows against 8 tokens (m16n8k16, bf16
-// operands, fp32 sums): codes less zeros are whole numbers that bf16 holds exactly, and a group's sum
-// is multiplied by its scale in fp32 afterwards.
+// reading; what has to be small beside it is the number of instructions for each weight.  The products
+// run on the tensor cores with 16 weight rows against 8 tokens, 16 columns at a time, fp16 operands and
+// fp32 sums: a code 0 .. 15 in the lowest bits of a half-word IS the fp16 value code 2^-24 (a subnormal
+// one), and in the next four bits 16 times that, so eight codes become operands by one shift and four
+// masks.  A token's values are scaled beforehand by a power of two for each 64 of them, so that fp16
+// holds what bf16 had; those that go with the 16-fold codes are divided by 16.  Zeros are taken off the
+// sums: sum s (c - z) x = s (sum c x - z sum x), the sums of x being formed once beforehand.  (Codes made
+// 16 + code in bf16, less 16 + zero, took 71 instructions for 16 x 64 weights, where half the pipes' rate
+// holds for 40 of them.  e4m3 operands, which a code in a byte is too, are turned into others first on
+// this GPU: 108 instructions.)
+#include <cuda_fp16.h>
 #include <math.h>
 
 #include <algorithm>
@@ -21,18 +29,19 @@ namespace {
 constexpr int kStrip = 16;       // weight rows of a product
 constexpr int kTile = 64;        // weights of a row that a lane's 16 bytes are part of
 constexpr int kMaxSlots = 16384;
+constexpr int kMaxWidth = 1 << 20;
 constexpr int kMaxExperts = 1024;
-constexpr int kWarps = 8;
+constexpr int kXParts = 1, kHParts = 2;  // fp16 values for one of x, of h
+constexpr int kWarps = 8, kMaxWarps = 16;  // to a block
 
 // ---------------------------------------------------------------- layout
 // A tile of 16 rows x 64 columns takes 512 bytes, 16 to a lane: lane 4 g + t holds rows g and g + 8,
 // columns 8 t .. 8 t + 7 of each half of the tile, as the words (g, first half), (g + 8, first half),
 // (g, second half), (g + 8, second half).  Within a word column 2 p + i of its eight is nibble
-// p + 4 i, so that a shift and a mask leave two neighbouring columns in the halves of a word, as the
-// product's operands want them (the order of the columns means nothing to it, as long as the tokens'
-// operand has the same: column 8 t + j of a half is in lane t there too).  A tile's rows are those
-// of a strip; strips, then experts follow one another.  Scales: for 16 rows and a group of columns,
-// (row g, row g + 8) for each g; with zeros, each scale is followed by 128 + zero, in bf16.
+// p + 4 i.  (The order of the columns means nothing to a product, as long as the tokens' operand has the
+// same.)  A tile's rows are those of a strip; strips, then experts follow one another.  Scales: for 16
+// rows and a group of columns, 4096 times the scales of rows g and g + 8 for each g; with zeros, each
+// scale is followed by its zero, in bf16.
 
 __global__ void w4_pack_kernel(int rows, int cols, long long words, const uint8_t* codes,
                                uint32_t* out) {
@@ -48,10 +57,7 @@ __global__ void w4_pack_kernel(int rows, int cols, long long words, const uint8_
     const int col = static_cast<int>(tile % tiles) * kTile + word / 2 * 32 + lane % 4 * 8;
     const uint8_t* from = codes + (row * cols + col) / 2;
     uint32_t w = 0;
-    for (int p = 0; p < 4; ++p) {
-      const uint32_t two = from[p];
-      w |= (two & 15) << (4 * p) | (two >> 4) << (4 * p + 16);
-    }
+    for (int c = 0; c < 8; ++c) w |= (from[c / 2] >> (c % 2 * 4) & 15u) << (c / 2 * 4 + c % 2 * 16);
     out[i] = w;
   }
 }
@@ -66,25 +72,46 @@ __global__ void w4_pack_scales_kernel(int groups, long long entries, const __nv_
     const long long at = i >> 4;
     const long long row = at / groups * kStrip + in / 2 + in % 2 * 8;
     const long long from = row * groups + at % groups;
+    const __nv_bfloat16 scale = __float2bfloat16_rn(4096.f * __bfloat162float(scales[from]));
     if (zeros) {
-      out[2 * i] = scales[from];
-      out[2 * i + 1] = __float2bfloat16_rn(128.f + (zeros[from] & 15));
+      out[2 * i] = scale;
+      out[2 * i + 1] = __float2bfloat16_rn(static_cast<float>(zeros[from] & 15));
     } else {
-      out[i] = scales[from];
+      out[i] = scale;
     }
   }
 }
 
 // ---------------------------------------------------------------- the slots by expert
 // Chunks of at most `chunk` rows of one expert; a row is a slot, in the slots' order within an
-// expert.  One block.
+// expert.  With up to 8 tokens a token's slots of one expert are one row, with the sum of their gates,
+// and `row_of_token` [chunks][8] has the tokens' rows (-1 for none).
 struct Groups {
-  int* count;      // [1] chunks
-  int* expert;     // [E + slots / chunk]
-  int* first;      // [...] its first row
-  int* rows;       // [...] how many
-  int* row_slot;   // [slots]
-  int* slot_row;   // [slots], -1 for a bad expert
+  const int* idx;  // [slots] the slots' experts; a single token's slots are chunks as they are
+  const float* gate;
+  int slots, E, single;
+  int* count;     // [1] chunks
+  int* expert;    // [E + slots / chunk]
+  int* first;     // [...] its first row
+  int* rows;      // [...] how many
+  int* row_slot;  // [slots]
+  float* row_gate;
+  int* slot_row;      // [slots], -1 for a bad expert
+  int* row_of_token;
+
+  __device__ __forceinline__ bool good(int slot) const { return idx[slot] >= 0 && idx[slot] < E; }
+  __device__ __forceinline__ int chunks() const { return single ? slots : *count; }
+  // The expert of chunk c, its first row and how many there are (none for a bad expert).
+  __device__ __forceinline__ int expert_of(int c) const {
+    return single ? (good(c) ? idx[c] : 0) : expert[c];
+  }
+  __device__ __forceinline__ int first_of(int c) const { return single ? c : first[c]; }
+  __device__ __forceinline__ int rows_of(int c) const { return single ? good(c) : rows[c]; }
+  __device__ __forceinline__ int slot_of(int row) const { return single ? row : row_slot[row]; }
+  __device__ __forceinline__ float gate_of(int row) const { return single ? gate[row] : row_gate[row]; }
+  __device__ __forceinline__ int row_of(int c, int token) const {
+    return single ? (token == 0 && good(c) ? c : -1) : row_of_token[c * 8 + token];
+  }
 };
 
 __device__ __forceinline__ int block_scan(int v, int* sums) {  // exclusive, 1024 threads
@@ -112,23 +139,35 @@ __device__ __forceinline__ int block_scan(int v, int* sums) {  // exclusive, 102
   return before + in - v;
 }
 
-__global__ void __launch_bounds__(1024)
-    w4_group_kernel(const int* idx, int slots, int E, int chunk, Groups g, int* dev_status) {
-  extern __shared__ unsigned short seen[];  // [32][E]: slots of the expert in the warp's part
-  __shared__ int sums[32];
-  after_previous();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int part = (slots + 1023) / 1024 * 32;  // slots of a warp
-  for (int i = threadIdx.x; i < 32 * E; i += 1024) seen[i] = 0;
+// One block of 1024.  The first `warps` of its warps have a part of the slots each, 32 at a time.
+__device__ void group_slots(const Groups& g, int k, int chunk, int warps, int* dev_status) {
+  extern __shared__ unsigned short seen[];  // [warps][E]: slots of the expert in the warp's part
+  __shared__ int sums[32], start[kMaxExperts], at_chunk[kMaxExperts];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = g.E;
+  const bool merge = chunk == 8;
+  const int part = (g.slots + warps * 32 - 1) / (warps * 32) * 32;
+  for (int i = threadIdx.x; i < warps * E; i += 1024) seen[i] = 0;
   __syncthreads();
-  const int lo = warp * part, hi = min(lo + part, slots);
+  const int lo = warp * part, hi = warp < warps ? min(lo + part, g.slots) : 0;
   const auto pass = [&](auto put) {
     for (int at = lo; at < hi; at += 32) {
       const int slot = at + lane;
       int e = -1;
+      float gate = 0.f;
       if (slot < hi) {
-        e = idx[slot];
-        if (e < 0 || e >= E) e = -1;
+        if (g.good(slot)) e = g.idx[slot];
+        gate = g.gate[slot];
+        if (merge && e >= 0) {  // the token's other slots of this expert
+          const int token = slot / k;
+          for (int j = token * k; j < token * k + k; ++j)
+            if (j != slot && g.idx[j] == e) {
+              if (j < slot) {
+                e = -1;
+                break;
+              }
+              gate += g.gate[j];
+            }
+        }
       }
       const unsigned same = __match_any_sync(~0u, e);
       const int rank = __popc(same & ((1u << lane) - 1));
@@ -136,73 +175,197 @@ __global__ void __launch_bounds__(1024)
       __syncwarp();
       if (e >= 0 && rank == 0) seen[warp * E + e] = before + __popc(same);
       __syncwarp();
-      if (slot < hi) put(slot, e, before + rank);
+      if (slot < hi) put(slot, e, before + rank, gate);
     }
   };
-  pass([&](int, int e, int) {
-    if (e < 0) report_status(dev_status, MOE_ERR_BAD_INDEX);
+  pass([&](int slot, int, int, float) {
+    if (!g.good(slot)) report_status(dev_status, MOE_ERR_BAD_INDEX);
   });
   __syncthreads();
   int all = 0;
   const int e = threadIdx.x;
   if (e < E)
-    for (int w = 0; w < 32; ++w) {
+    for (int w = 0; w < warps; ++w) {
       const int n = seen[w * E + e];
       seen[w * E + e] = all;
       all += n;
     }
   const int chunks = (all + chunk - 1) / chunk;
-  const int row = block_scan(all, sums), at = block_scan(chunks, sums);
+  const int both = block_scan(all | chunks << 16, sums);  // (each up to 16384)
+  const int row = both & 0xffff, at = both >> 16;
   if (threadIdx.x == 1023) *g.count = at + chunks;
   for (int c = 0; c < chunks; ++c) {
     g.expert[at + c] = e;
     g.first[at + c] = row + c * chunk;
     g.rows[at + c] = min(chunk, all - c * chunk);
+    if (merge) {
+      const int4 none = make_int4(-1, -1, -1, -1);
+      reinterpret_cast<int4*>(g.row_of_token)[2 * (at + c)] = none;
+      reinterpret_cast<int4*>(g.row_of_token)[2 * (at + c) + 1] = none;
+    }
   }
-  __shared__ int start[kMaxExperts];
-  if (e < E) start[e] = row;
+  if (e < E) start[e] = row, at_chunk[e] = at;
   __syncthreads();
-  pass([&](int slot, int of, int rank) {
+  pass([&](int slot, int of, int rank, float gate) {
     const int r = of < 0 ? -1 : start[of] + rank;
     g.slot_row[slot] = r;
-    if (r >= 0) g.row_slot[r] = slot;
+    if (r < 0) return;
+    g.row_slot[r] = slot;
+    g.row_gate[r] = gate;
+    if (merge) g.row_of_token[at_chunk[of] * 8 + slot / k] = r;
   });
 }
 
-// ---------------------------------------------------------------- products
+// ---------------------------------------------------------------- the tokens' values
+// Rows of values as operands: PARTS fp16 values to each, and for every 64 columns (a tile) the factor
+// that their sum is scaled by and the sums of the values themselves.
+template <int PARTS>
+struct Rows {
+  uint8_t* parts;  // [rows][PARTS][tiles][4 lanes][2 halves of a tile][8] fp16
+  float4* info;    // [rows][tiles]: the factor; sums / 4096 over the halves and the tile
+  int tiles;
 
-__device__ __forceinline__ uint4 load_stream(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
+  __device__ __forceinline__ const uint8_t* row(int r) const {
+    return parts + static_cast<long long>(r) * (PARTS * kTile * 2) * tiles;
+  }
+  __device__ __forceinline__ const float4* info_row(int r) const {
+    return info + static_cast<long long>(r) * tiles;
+  }
 
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                    uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t less(uint32_t codes, uint32_t zero) {
-  __nv_bfloat162 v = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&codes),
-                             *reinterpret_cast<__nv_bfloat162*>(&zero));
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
-// Two codes of a word (those 2 p and 2 p + 1) as 128 + code in bf16, less 128 + zero.
-__device__ __forceinline__ uint32_t two_codes(uint32_t word, int p, uint32_t zero) {
-  return less((word >> (4 * p) & 0x000f000fu) | 0x43004300u, zero);
-}
-
-// One strip's weights, as the kernels read them.
-struct Matrix {
-  const uint4* codes;
-  const uint32_t* scales;
+  // Four neighbouring lanes (t = 0 .. 3) write a tile of a row: v[c][j] is column 32 c + 8 t + j.
+  // u = v 2^e, |u| < 2^15, divided by 16 for j = 2, 3, 6, 7, is part 0 + part 1 / 2048: fp16 has 11
+  // bits, so one part is off by at most 2^-12 of it (bf16 values not at all) and two by 2^-24; and the
+  // small ones, whose bits end at 2^-24, by 2^-25 or 2^-36 in that scale, 2^-35 or 2^-46 of the tile's
+  // largest.  Where that is not finite the factor is NaN, and so becomes all that the row's products
+  // give.
+  __device__ __forceinline__ void write(int r, int tile, const float (&v)[2][8]) const {
+    const int t = threadIdx.x & 3;
+    float most = 0.f, sum[2];
+    bool finite = true;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      sum[c] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        most = fmaxf(most, fabsf(v[c][j]));
+        finite &= fabsf(v[c][j]) <= 3.4028235e38f;
+        sum[c] += v[c][j];
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o *= 2) {
+      most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+      finite &= __shfl_xor_sync(~0u, static_cast<int>(finite), o) != 0;
+      sum[0] += __shfl_xor_sync(~0u, sum[0], o);
+      sum[1] += __shfl_xor_sync(~0u, sum[1], o);
+    }
+    const int exponent = max((__float_as_int(most) >> 23) - 127, -120);  // of the largest
+    uint8_t* to = parts + (static_cast<long long>(r) * PARTS * tiles + tile) * (kTile * 2) + t * 32;
+    float left[2][8];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) left[c][j] = ldexpf(v[c][j], (j & 2 ? 10 : 14) - exponent);
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t word[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 p = __floats2half2_rn(left[c][2 * i], left[c][2 * i + 1]);
+          left[c][2 * i] = (left[c][2 * i] - __low2float(p)) * 2048.f;
+          left[c][2 * i + 1] = (left[c][2 * i + 1] - __high2float(p)) * 2048.f;
+          word[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        *reinterpret_cast<uint4*>(to + static_cast<long long>(q) * tiles * (kTile * 2) + c * 16) =
+            make_uint4(word[0], word[1], word[2], word[3]);
+      }
+    if (t == 0)
+      info[static_cast<long long>(r) * tiles + tile] =
+          make_float4(finite ? ldexpf(1.f, exponent - 2) : NAN, sum[0] / 4096.f, sum[1] / 4096.f,
+                      (sum[0] + sum[1]) / 4096.f);
+  }
 };
+
+// The tokens' values as operands, and (the last block) the slots by expert; counters set to zero.
+__global__ void __launch_bounds__(1024)
+    w4_prepare_kernel(const __nv_bfloat16* x, int T, Rows<kXParts> rows, int* counters, int n_counters,
+                      const Groups g, int k, int chunk, int warps, int* dev_status) {
+  after_previous();
+  const int blocks = g.single ? gridDim.x : gridDim.x - 1;
+  if (blockIdx.x == blocks) {
+    group_slots(g, k, chunk, warps, dev_status);
+    return;
+  }
+  const long long step = static_cast<long long>(blocks) * 1024;
+  const long long me = blockIdx.x * 1024ll + threadIdx.x;
+  for (long long i = me; i < n_counters; i += step) counters[i] = 0;
+  if (g.single && me < g.slots && !g.good(static_cast<int>(me)))
+    report_status(dev_status, MOE_ERR_BAD_INDEX);
+  const long long all = static_cast<long long>(T) * rows.tiles;
+  for (long long i = me / 4; i - threadIdx.x % 32 / 4 < all; i += step / 4) {  // whole warps
+    const long long at = min(i, all - 1);  // (again the last one: the same values)
+    const int t = threadIdx.x & 3;
+    float v[2][8];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint4 q = *reinterpret_cast<const uint4*>(x + at * kTile + c * 32 + t * 8);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[c][2 * j] = __uint_as_float(w[j] << 16);
+        v[c][2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+    }
+    rows.write(static_cast<int>(at / rows.tiles), static_cast<int>(at % rows.tiles), v);
+  }
+}
+
+// ---------------------------------------------------------------- products
+//
+// `split` warps (1 to 8) take a strip of 16 weight rows (of both matrices, for gate and up), each every
+// split'th piece of 256 of its columns.  Pieces come by bulk copies into a ring that is the warp's own,
+// one piece or more ahead of the products and on into the warp's next strip.  (16 bytes to a lane by
+// cp.async took about as many instructions for the copies as for the products: 1738 us -> 1161 us for
+// 64 tokens, at 2.1 TB/s with 60 % of the issue slots used.)
+
+// d = a b + c
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                    float c0, float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
+        "f"(c3));
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                    bool first) {
+  if (first)
+    mma(d, a, b0, b1, 0.f, 0.f, 0.f, 0.f);
+  else
+    mma(d, a, b0, b1, d[0], d[1], d[2], d[3]);
+}
+
+// A bulk copy into shared memory; its bytes are counted at `bar`.
+__device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t bytes, uint64_t* bar,
+                                          uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
+      "[%3], %4;" ::"r"(smem_u32(to)), "l"(from), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// Whether the barrier's phase completed, for the whole warp; gives up after kWaitTimeoutNs.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!(ok = mbar_try_wait(bar, parity)) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
+    }
+  }
+  return __all_sync(~0u, ok);
+}
 
 struct Weights {
   const void* codes;
@@ -210,243 +373,597 @@ struct Weights {
   int group;
 };
 
-// Scales (and zeros) of rows g and g + 8 in a group of columns.
-template <bool ZEROS>
-struct Scale {
-  float s0, s1;
-  uint32_t z0, z1;
-  __device__ __forceinline__ void load(const uint32_t* scales, long long group, int g) {
-    if constexpr (ZEROS) {
-      const uint2 v = reinterpret_cast<const uint2*>(scales)[group * 8 + g];
-      s0 = __uint_as_float(v.x << 16), s1 = __uint_as_float(v.y << 16);
-      z0 = __byte_perm(v.x, 0, 0x3232), z1 = __byte_perm(v.y, 0, 0x3232);
-    } else {
-      const uint32_t v = scales[group * 8 + g];
-      s0 = __uint_as_float(v << 16), s1 = __uint_as_float(v & 0xffff0000u);
-      z0 = z1 = 0x43084308u;  // 136
-    }
+// Strips of MATS matrices [E, rows, cols] for the slots' chunks: task i is strip i % strips of chunk
+// i / strips.
+template <int MATS>
+struct Problem {
+  Groups g;
+  Weights w[MATS];
+  int rows, cols, split;
+  int* dev_status;
+};
+
+// The tasks of a team of warps, one after the other.
+struct Tasks {
+  int chunk, strip, strips, chunk_step, strip_step;
+  __device__ __forceinline__ Tasks(int first, int step, int strips_)
+      : chunk(first / strips_), strip(first % strips_), strips(strips_),
+        chunk_step(step / strips_), strip_step(step % strips_) {}
+  __device__ __forceinline__ void next() {
+    chunk += chunk_step, strip += strip_step;
+    if (strip >= strips) strip -= strips, ++chunk;
   }
 };
 
-// acc += W x^T over the tiles first, first + step, ... of a strip, for MATS matrices against NT x 8
-// tokens, whose values are given in PIECES parts to add.  x[i]: the row of token 8 i + g (its tile
-// begins at column 0), null for none; the second piece is `piece` values behind.
-template <int MATS, int NT, int PIECES, bool ZEROS>
-__device__ __forceinline__ void product(const Matrix (&m)[MATS], int group, int tiles, int first,
-                                        int step, const __nv_bfloat16* const (&x)[NT],
-                                        long long piece, float (&acc)[MATS][NT][4]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  constexpr int U = 2;  // tiles on their way
-  for (int tile = first; tile < tiles; tile += U * step) {
-    uint4 w[U][MATS];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < MATS; ++i)
-        if (tile + u * step < tiles)
-          w[u][i] = load_stream(m[i].codes + (tile + u * step) * 32ll + lane);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = tile + u * step;
-      if (at >= tiles) break;
-      uint4 v[2][NT][PIECES];
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int q = 0; q < PIECES; ++q) {
-            v[c][n][q] = make_uint4(0, 0, 0, 0);
-            if (x[n])
-              v[c][n][q] = *reinterpret_cast<const uint4*>(x[n] + q * piece + at * kTile + c * 32 +
-                                                           t * 8);
-          }
+constexpr int kPieceTiles = 4;
+
+// MATS matrices, NT x 8 tokens at most, whose values come in PARTS to add; ZEROS: zeros are given;
+// FINE: two groups of 32 columns to a tile.
+template <int MATS, int NT, int PARTS, bool ZEROS, bool FINE>
+struct Product {
+  static constexpr int kPlaces = MATS == 2 ? (NT == 1 ? 3 : 2) : 4;  // of the ring; one less on their way
+  static constexpr int kWords = ZEROS ? 2 : 1;       // of a group's scales, to a lane
+  static constexpr int kCodes = kPieceTiles * 512;   // bytes of a piece and matrix
+  static constexpr int kPlace = kCodes + kPieceTiles * (FINE ? 2 : 1) * 32 * kWords;
+  static constexpr int kRing = kPlaces * MATS * kPlace;
+  static constexpr int kSums = MATS * NT * 4;  // to a lane
+  static constexpr int kWarpBytes = kRing + kSums * 128 + kPlaces * 8, kBytes = kWarps * kWarpBytes;
+  static constexpr int kBlocks = 2;  // to an SM, where they fit
+
+  // Issues the copies of pieces; by a warp's first lane.
+  struct Copies {
+    uint8_t* ring;
+    uint64_t* bars;
+    int place, group_shift;
+    uint64_t policy;
+
+    __device__ __forceinline__ Copies(const Problem<MATS>& p, uint8_t* ring_, uint64_t* bars_)
+        : ring(ring_), bars(bars_), place(0), group_shift(31 - __clz(p.w[0].group)),
+          policy(l2_policy_evict_first()) {}
+    // Bytes of the scales of n tiles.
+    __device__ __forceinline__ int of_scales(int n) const { return n * (2048 * kWords) >> group_shift; }
+    __device__ __forceinline__ void issue(const uint8_t* const (&codes)[MATS],
+                                          const uint8_t* const (&scales)[MATS], int n) {
+      uint8_t* to = ring + place * (MATS * kPlace);
+      const int bytes = of_scales(n);
+      mbar_arrive_expect_tx(bars + place, MATS * (n * 512 + bytes));
 #pragma unroll
       for (int i = 0; i < MATS; ++i) {
-        Scale<ZEROS> s;
-        float part[NT][4];
+        bulk_load(to + i * kPlace, codes[i], n * 512, bars + place, policy);
+        bulk_load(to + i * kPlace + kCodes, scales[i], bytes, bars + place, policy);
+      }
+      if (++place == kPlaces) place = 0;
+    }
+  };
+
+  // The pieces of a team's strips, one warp's share, ahead of the products.
+  struct Ahead : Copies {
+    const Problem<MATS>& p;
+    Tasks at;
+    int chunks, tiles, left, skip;  // tiles from the piece on; tiles of the team's pieces before
+    const uint8_t* codes[MATS];
+    const uint8_t* scales[MATS];
+
+    __device__ __forceinline__ Ahead(const Problem<MATS>& p_, uint8_t* ring_, uint64_t* bars_,
+                                     const Tasks& at_, int chunks_, int first)
+        : Copies(p_, ring_, bars_), p(p_), at(at_), chunks(chunks_), tiles(p_.cols / kTile),
+          skip(first * kPieceTiles) {
+      begin();
+    }
+    __device__ __forceinline__ void begin() {
+      if (at.chunk >= chunks) return;
+      const long long strip =
+          static_cast<long long>(p.g.expert_of(at.chunk)) * at.strips + at.strip;
+      left = tiles - skip;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (c == 0 || group == 32) {
-            s.load(m[i].scales, group == 32 ? at * 2 + c : group == 64 ? at : at >> 1, g);
+      for (int i = 0; i < MATS; ++i) {
+        codes[i] = static_cast<const uint8_t*>(p.w[i].codes) + (strip * tiles + skip) * 512;
+        scales[i] = static_cast<const uint8_t*>(p.w[i].scales) + strip * this->of_scales(tiles) +
+                    this->of_scales(skip);
+      }
+    }
+    __device__ __forceinline__ void next() {
+      if (at.chunk >= chunks) return;
+      this->issue(codes, scales, min(kPieceTiles, left));
+      const int step = p.split * kPieceTiles;
+      left -= step;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+      for (int i = 0; i < MATS; ++i) codes[i] += step * 512, scales[i] += this->of_scales(step);
+      if (left <= 0) {
+        at.next();
+        begin();
+      }
+    }
+  };
+
+  // A warp's share of the pieces of one strip of all chunks after one another, and of the block's next
+  // strips.
+  struct Pieces {
+    int chunk, piece, pieces, chunk_step, piece_step;
+    __device__ __forceinline__ Pieces(int first, int step, int pieces_)
+        : chunk(first / pieces_), piece(first % pieces_), pieces(pieces_),
+          chunk_step(step / pieces_), piece_step(step % pieces_) {}
+    __device__ __forceinline__ void next() {
+      chunk += chunk_step, piece += piece_step;
+      if (piece >= pieces) piece -= pieces, ++chunk;
+    }
+  };
+  struct AheadInStrips : Copies {
+    const Problem<MATS>& p;
+    Pieces start, at;
+    int chunks, tiles, strip, strips, expert;
+
+    __device__ __forceinline__ AheadInStrips(const Problem<MATS>& p_, uint8_t* ring_, uint64_t* bars_,
+                                             const Pieces& at_, int chunks_)
+        : Copies(p_, ring_, bars_), p(p_), start(at_), at(at_), chunks(chunks_),
+          tiles(p_.cols / kTile), strip(blockIdx.x), strips(p_.rows / kStrip) {
+      if (at.chunk >= chunks) strip = strips;  // more warps than pieces
+      if (strip < strips) expert = p.g.expert_of(at.chunk);
+    }
+    __device__ __forceinline__ void next() {
+      if (strip >= strips) return;
+      const long long of = static_cast<long long>(expert) * strips + strip;
+      const int skip = at.piece * kPieceTiles;
+      const uint8_t *codes[MATS], *scales[MATS];
 #pragma unroll
-              for (int r = 0; r < 4; ++r) part[n][r] = 0.f;
-          }
-          const uint32_t w0 = c ? w[u][i].z : w[u][i].x, w1 = c ? w[u][i].w : w[u][i].y;
+      for (int i = 0; i < MATS; ++i) {
+        codes[i] = static_cast<const uint8_t*>(p.w[i].codes) + (of * tiles + skip) * 512;
+        scales[i] = static_cast<const uint8_t*>(p.w[i].scales) + of * this->of_scales(tiles) +
+                    this->of_scales(skip);
+      }
+      this->issue(codes, scales, min(kPieceTiles, tiles - skip));
+      at.next();
+      if (at.chunk >= chunks) at = start, strip += gridDim.x;
+      if (strip < strips) expert = p.g.expert_of(at.chunk);  // (wanted at the next call)
+    }
+  };
+
+  struct Scale {
+    float s[2], z[2];  // of rows g and g + 8
+    __device__ __forceinline__ void load(const uint32_t* from) {
+      if constexpr (ZEROS) {
+        const uint2 v = *reinterpret_cast<const uint2*>(from);
+        s[0] = __uint_as_float(v.x << 16), s[1] = __uint_as_float(v.y << 16);
+        z[0] = __uint_as_float(v.x & 0xffff0000u), z[1] = __uint_as_float(v.y & 0xffff0000u);
+      } else {
+        const uint32_t v = *from;
+        s[0] = __uint_as_float(v << 16), s[1] = __uint_as_float(v & 0xffff0000u);
+        z[0] = z[1] = 8.f;
+      }
+    }
+  };
+
+  // A tile's weights as operands, for each 16 of its columns.
+  struct Operands {
+    uint32_t a[4][4];
+    Scale s[FINE ? 2 : 1];
+    __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales) {
+      const int lane = threadIdx.x & 31;
+      const uint4 w = *reinterpret_cast<const uint4*>(codes + lane * 16);
+      const uint32_t* of = reinterpret_cast<const uint32_t*>(scales) + lane / 4 * kWords;
+      s[0].load(of);
+      if (FINE) s[FINE].load(of + 8 * kWords);
+      const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t a0 = two_codes(w0, 2 * h, s.z0), a1 = two_codes(w1, 2 * h, s.z1);
-            const uint32_t a2 = two_codes(w0, 2 * h + 1, s.z0), a3 = two_codes(w1, 2 * h + 1, s.z1);
+      for (int i = 0; i < 4; ++i) {  // row g + i % 2 * 8, half i / 2
+        const uint32_t next = words[i] >> 8;
+        a[i / 2 * 2][i % 2] = words[i] & 0x000f000fu, a[i / 2 * 2][i % 2 + 2] = words[i] & 0x00f000f0u;
+        a[i / 2 * 2 + 1][i % 2] = next & 0x000f000fu, a[i / 2 * 2 + 1][i % 2 + 2] = next & 0x00f000f0u;
+      }
+    }
+  };
+
+  // Where a lane finds the values of eight tokens: the parts of token lane / 4, and what goes with the
+  // sums of tokens lane % 4 * 2 and the one after.
+  struct From {
+    const uint8_t* parts;
+    const float4* info[2];
+  };
+  // Those values, for a tile; with SOME, null rows are zero.
+  struct Values {
+    uint4 v[PARTS][2];
+    float4 info[2];
+    template <bool SOME>
+    __device__ __forceinline__ void load(const From& x, int tile, int tiles) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+      for (int q = 0; q < PARTS; ++q)
 #pragma unroll
-              for (int q = 0; q < PIECES; ++q)
-                mma(part[n], a0, a1, a2, a3, h ? v[c][n][q].z : v[c][n][q].x,
-                    h ? v[c][n][q].w : v[c][n][q].y);
-          }
-          if (c == 1 || group == 32) {
+        for (int c = 0; c < 2; ++c)
+          if (!SOME || x.parts)
+            v[q][c] = reinterpret_cast<const uint4*>(x.parts + (q * tiles + tile) * (kTile * 2))[c];
+          else
+            v[q][c] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              acc[i][n][0] = fmaf(s.s0, part[n][0], acc[i][n][0]);
-              acc[i][n][1] = fmaf(s.s0, part[n][1], acc[i][n][1]);
-              acc[i][n][2] = fmaf(s.s1, part[n][2], acc[i][n][2]);
-              acc[i][n][3] = fmaf(s.s1, part[n][3], acc[i][n][3]);
-            }
-          }
+      for (int i = 0; i < 2; ++i)
+        if (!SOME || x.info[i])
+          info[i] = x.info[i][tile];
+        else
+          info[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+
+  static __device__ __forceinline__ void multiply(const Operands& w, const Values& x,
+                                                  float (&acc)[4]) {
+    float part[PARTS][4];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q) {
+        mma(part[q], w.a[2 * c], x.v[q][c].x, x.v[q][c].y, c == 0 || FINE);
+        mma(part[q], w.a[2 * c + 1], x.v[q][c].z, x.v[q][c].w, false);
+      }
+      if (c == 1 || FINE) {
+        const Scale& s = w.s[FINE ? c : 0];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float4& info = x.info[r % 2];
+          const float sum = FINE ? (c ? info.z : info.y) : info.w;
+          float v = part[PARTS - 1][r];
+#pragma unroll
+          for (int q = PARTS - 2; q >= 0; --q) v = fmaf(v, 1.f / 2048.f, part[q][r]);
+          acc[r] = fmaf(s.s[r / 2], fmaf(info.x, v, -s.z[r / 2] * sum), acc[r]);
         }
       }
     }
   }
-}
 
-template <int MATS, bool ZEROS>
-__device__ __forceinline__ Matrix strip_of(const Weights& w, int e, int rows, int cols, int strip) {
-  const long long strips = rows / kStrip, at = e * strips + strip;
-  return {static_cast<const uint4*>(w.codes) + at * (cols / kTile) * 32,
-          static_cast<const uint32_t*>(w.scales) + at * (cols / w.group) * (ZEROS ? 16 : 8)};
-}
-
-// The warps of a block share a strip's tiles; their sums are added in the warps' order.
-// put(i, row, token, sums of the MATS matrices) for all 16 x 8 NT of them.
-template <int MATS, int NT, int PIECES, bool ZEROS, typename Put>
-__device__ __forceinline__ void strip_product(const Matrix (&m)[MATS], int group, int cols,
-                                              const __nv_bfloat16* const (&x)[NT],
-                                              long long piece, float* sums, Put put) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float acc[MATS][NT][4] = {};
-  product<MATS, NT, PIECES, ZEROS>(m, group, cols / kTile, warp, kWarps, x, piece, acc);
-  __syncthreads();  // (the last strip's readers are done)
+  // N tiles of a piece from its tile u0 on (u0 + at of the row's).  Of a single eight of tokens, `now`
+  // has the values of the first one, and is left with those of the tile after the last if there is
+  // `more` to come.
+  template <int N, bool SOME>
+  static __device__ __forceinline__ void tiles_of(const uint8_t* from, int at, int u0, int coarse,
+                                                  const From (&x)[NT], int tiles, int rows,
+                                                  bool more, Values& now,
+                                                  float (&acc)[MATS][NT][4]) {
 #pragma unroll
-  for (int i = 0; i < MATS; ++i)
+    for (int k = 0; k < N; ++k) {
+      const int u = u0 + k;
+      Operands w[MATS];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int i = 0; i < MATS; ++i)
+        w[i].load(from + i * kPlace + u * 512,
+                  from + i * kPlace + kCodes + (FINE ? 2 * u : u >> coarse) * (32 * kWords));
+      if (NT == 1) {
+        const Values mine = now;
+        if (k + 1 < N || more) now.template load<SOME>(x[0], at + u + 1, tiles);
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        sums[(((warp * MATS + i) * NT + n) * 4 + r) * 32 + lane] = acc[i][n][r];
-  __syncthreads();
-  // place (n, r, lane) is row lane / 4 + r / 2 * 8, token 8 n + lane % 4 * 2 + r % 2
-  for (int p = threadIdx.x; p < NT * 128; p += kWarps * 32) {
-    float v[MATS] = {};
+        for (int i = 0; i < MATS; ++i) multiply(w[i], mine, acc[i][0]);
+      } else {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
+        for (int n = 0; n < NT; ++n)
+          if (n * 8 < rows) {
+            now.template load<false>(x[n], at + u, tiles);
 #pragma unroll
-      for (int i = 0; i < MATS; ++i) v[i] += sums[(w * MATS + i) * NT * 128 + p];
-    const int l = p & 31, r = p >> 5 & 3, n = p >> 7;
-    put(l / 4 + r / 2 * 8, n * 8 + l % 4 * 2 + r % 2, v);
+            for (int i = 0; i < MATS; ++i) multiply(w[i], now, acc[i][n]);
+          }
+      }
+    }
   }
-}
 
-struct GateUp {
-  Groups g;
-  Weights gate, up;
-  const __nv_bfloat16* x;
-  __nv_bfloat16* h;  // [2][slots][F]: two pieces
-  int d, F, k, slots;
+  // All of the warp's strips.  value_row(r) is the row of x of a chunk's row r; put(chunk,
+  // first, rows, strip, sums) gets the sums: places (n, r) of a lane are row lane / 4 + r / 2 * 8 of the
+  // strip, token 8 n + lane % 4 * 2 + r % 2 of the chunk.  (Columns of tokens that there are not repeat
+  // the first one's; a product's columns have nothing to do with each other.)
+  template <typename RowOf, typename Put>
+  static __device__ __forceinline__ void run(const Problem<MATS>& p, const Rows<PARTS>& values,
+                                             uint8_t* shared, RowOf value_row, Put put) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, split = p.split;
+    const int team = warp / split, me = warp % split, teams = kWarps / split;
+    uint8_t* ring = shared + warp * kRing;
+    float* sums = reinterpret_cast<float*>(shared + kWarps * kRing);  // [warp][kSums][32]
+    uint64_t* bars =
+        reinterpret_cast<uint64_t*>(shared + kWarps * (kRing + kSums * 128)) + warp * kPlaces;
+    if (lane == 0) {
+      for (int i = 0; i < kPlaces; ++i) mbar_init(bars + i, 1);
+      fence_barrier_init();
+    }
+    __syncwarp();
+    after_previous();
+    const int strips = p.rows / kStrip, tiles = p.cols / kTile, chunks = p.g.chunks();
+    const int coarse = p.w[0].group == 128;
+    Tasks task(blockIdx.x * teams + team, gridDim.x * teams, strips);
+    Ahead ahead(p, ring, bars, task, chunks, me);
+    if (lane == 0)
+      for (int i = 0; i < kPlaces - 1; ++i) ahead.next();
+    int place = 0;
+    uint32_t parity = 0;
+    bool ok = true;
+    for (; task.chunk < chunks; task.next()) {
+      const int first = p.g.first_of(task.chunk), rows = p.g.rows_of(task.chunk);
+      From x[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const auto row = [&](int token) {
+          return value_row(first + (n * 8 + token < rows ? n * 8 + token : 0));
+        };
+        x[n].parts = values.row(row(lane / 4)) + lane % 4 * 32;
+        x[n].info[0] = values.info_row(row(lane % 4 * 2));
+        x[n].info[1] = values.info_row(row(lane % 4 * 2 + 1));
+      }
+      float acc[MATS][NT][4] = {};
+      for (int at = me * kPieceTiles; at < tiles && ok; at += split * kPieceTiles) {
+        Values now;
+        if (NT == 1) now.template load<false>(x[0], at, tiles);
+        if (!wait_for(bars + place, parity)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) ahead.next();
+        __syncwarp();
+        const uint8_t* from = ring + place * (MATS * kPlace);
+        const int left = tiles - at;
+        if (left >= kPieceTiles)
+          tiles_of<kPieceTiles, false>(from, at, 0, coarse, x, tiles, rows, false, now, acc);
+        else
+#pragma unroll 1
+          for (int u = 0; u < left; ++u)
+            tiles_of<1, false>(from, at, u, coarse, x, tiles, rows, u + 1 < left, now, acc);
+        if (++place == kPlaces) place = 0, parity ^= 1;
+        __syncwarp();  // the place is read before it is copied into again
+      }
+      if (split > 1) {  // the team's sums, added in its order by its first warp
+        const auto sync = [&] {
+          asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(split * 32) : "memory");
+        };
+        if (me)
+#pragma unroll
+          for (int i = 0; i < MATS * NT; ++i)
+            if (i % NT * 8 < rows)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                sums[(warp * kSums + i * 4 + r) * 32 + lane] = acc[i / NT][i % NT][r];
+        sync();
+        if (!me)
+#pragma unroll
+          for (int i = 0; i < MATS * NT; ++i)
+            if (i % NT * 8 < rows)
+              for (int o = 1; o < split; ++o)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  acc[i / NT][i % NT][r] += sums[((warp + o) * kSums + i * 4 + r) * 32 + lane];
+        sync();
+      }
+      if (!me) put(task.chunk, first, rows, task.strip, acc);
+    }
+    drain(p, ok, ahead.place, bars, place, parity);
+  }
+
+  // All of the block's strips, for up to 8 tokens, whose columns are the same in all chunks: the sums
+  // over a token's experts stay in the products' sums.  Tokens that a chunk has not are zero there.
+  // put(strip, row, token, sum).
+  template <typename Put>
+  static __device__ __forceinline__ void run_strips(const Problem<MATS>& p,
+                                                    const Rows<PARTS>& values, uint8_t* shared,
+                                                    Put put) {
+    static_assert(MATS == 1 && NT == 1, "one matrix, 8 tokens");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
+    uint8_t* ring = shared + warp * kRing;
+    float* sums = reinterpret_cast<float*>(shared + warps * kRing);  // [warp][4][32]
+    uint64_t* bars =
+        reinterpret_cast<uint64_t*>(shared + warps * (kRing + kSums * 128)) + warp * kPlaces;
+    if (lane == 0) {
+      for (int i = 0; i < kPlaces; ++i) mbar_init(bars + i, 1);
+      fence_barrier_init();
+    }
+    __syncwarp();
+    after_previous();
+    const int strips = p.rows / kStrip, tiles = p.cols / kTile, chunks = p.g.chunks();
+    const int coarse = p.w[0].group == 128;
+    const Pieces start(warp, warps, (tiles + kPieceTiles - 1) / kPieceTiles);
+    AheadInStrips ahead(p, ring, bars, start, chunks);
+    if (lane == 0)
+      for (int i = 0; i < kPlaces - 1; ++i) ahead.next();
+    int place = 0;
+    uint32_t parity = 0;
+    bool ok = true;
+    for (int strip = blockIdx.x; strip < strips; strip += gridDim.x) {
+      float acc[1][1][4] = {};
+      Pieces at = start;
+      int row = at.chunk < chunks ? p.g.row_of(at.chunk, lane / 4) : -1;
+      while (at.chunk < chunks && ok) {
+        From x[1] = {};
+        if (row >= 0) x[0].parts = values.row(row) + lane % 4 * 32;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = __shfl_sync(~0u, row, (lane % 4 * 2 + i) * 4);
+          if (r >= 0) x[0].info[i] = values.info_row(r);
+        }
+        const int first = at.piece * kPieceTiles, left = tiles - first;
+        Values now;
+        now.template load<true>(x[0], first, tiles);
+        at.next();
+        if (at.chunk < chunks) row = p.g.row_of(at.chunk, lane / 4);
+        if (!wait_for(bars + place, parity)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) ahead.next();
+        __syncwarp();
+        const uint8_t* from = ring + place * kPlace;
+        if (left >= kPieceTiles)
+          tiles_of<kPieceTiles, true>(from, first, 0, coarse, x, tiles, 8, false, now, acc);
+        else
+#pragma unroll 1
+          for (int u = 0; u < left; ++u)
+            tiles_of<1, true>(from, first, u, coarse, x, tiles, 8, u + 1 < left, now, acc);
+        if (++place == kPlaces) place = 0, parity ^= 1;
+        __syncwarp();  // the place is read before it is copied into again
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sums[(warp * 4 + r) * 32 + lane] = acc[0][0][r];
+      __syncthreads();
+      if (threadIdx.x < 128) {
+        float sum = 0.f;
+        for (int w = 0; w < warps; ++w) sum += sums[w * 128 + threadIdx.x];
+        const int r = threadIdx.x >> 5;
+        put(strip, lane / 4 + r / 2 * 8, lane % 4 * 2 + r % 2, sum);
+      }
+      __syncthreads();
+    }
+    drain(p, ok, ahead.place, bars, place, parity);
+  }
+
+  // After a wait that ran out: what is on its way arrives before the block's memory is given up.
+  static __device__ __forceinline__ void drain(const Problem<MATS>& p, bool ok, int issued,
+                                               uint64_t* bars, int place, uint32_t parity) {
+    if (ok) return;
+    if ((threadIdx.x & 31) == 0) report_status(p.dev_status, MOE_ERR_TIMEOUT);
+    const int end = __shfl_sync(~0u, issued, 0);
+    while (place != end) {
+      wait_for(bars + place, parity);
+      if (++place == kPlaces) place = 0, parity ^= 1;
+    }
+  }
 };
 
-template <int NT, bool ZEROS>
-__device__ __forceinline__ void gateup_task(const GateUp& p, int c, int strip, float* sums) {
-  const int e = p.g.expert[c], first = p.g.first[c], rows = p.g.rows[c];
-  const int g = (threadIdx.x & 31) >> 2;
-  const Matrix m[2] = {strip_of<2, ZEROS>(p.gate, e, p.F, p.d, strip),
-                       strip_of<2, ZEROS>(p.up, e, p.F, p.d, strip)};
-  const __nv_bfloat16* x[NT];
+struct GateUp {
+  Problem<2> p;
+  Rows<kXParts> x;
+  float* h;       // [slots][F], times the gate
+  Rows<kHParts> parts;  // the same as operands
+  int* counters;  // [chunks][F / 64]: strips of a tile that are done
+  int k;
+};
+
+// h goes to memory in fp32; the warp that brings the last of a tile's four strips makes operands of it.
+template <int NT, bool ZEROS, bool FINE>
+__global__ void __launch_bounds__(kWarps * 32, Product<2, NT, kXParts, ZEROS, FINE>::kBlocks) w4_gateup_kernel(const GateUp a) {
+  using Of = Product<2, NT, kXParts, ZEROS, FINE>;
+  extern __shared__ __align__(16) uint8_t shared[];
+  const int F = a.p.rows, lane = threadIdx.x & 31;
+  Of::run(
+      a.p, a.x, shared, [&](int r) { return a.p.g.slot_of(r) / a.k; },
+      [&](int chunk, int first, int rows, int strip, const float (&acc)[2][NT][4]) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int r = n * 8 + g;
-    x[n] = r < rows ? p.x + static_cast<long long>(p.g.row_slot[first + r] / p.k) * p.d : nullptr;
-  }
-  strip_product<2, NT, 1, ZEROS>(
-      m, p.gate.group, p.d, x, 0, sums, [&](int row, int token, const float (&v)[2]) {
-        if (token >= rows) return;
-        const float a = v[0], h = a / (1.f + expf(-a)) * v[1];
-        const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-        __nv_bfloat16* to = p.h + (first + token) * static_cast<long long>(p.F) + strip * kStrip + row;
-        to[0] = hi;
-        to[static_cast<long long>(p.slots) * p.F] = __float2bfloat16_rn(h - __bfloat162float(hi));
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int token = n * 8 + lane % 4 * 2 + r % 2;
+            if (token >= rows) continue;
+            const float v = acc[0][n][r];
+            const float h = a.p.g.gate_of(first + token) * (v / (1.f + expf(-v)) * acc[1][n][r]);
+            __stcg(a.h + (first + token) * static_cast<long long>(F) + strip * kStrip + lane / 4 +
+                       r / 2 * 8, h);
+          }
+        const int tile = strip / 4;
+        __threadfence();
+        __syncwarp();
+        int before = 0;
+        if (lane == 0) before = atomicAdd(a.counters + static_cast<long long>(chunk) * (F / kTile) + tile, 1);
+        if (__shfl_sync(~0u, before, 0) != 3) return;
+        __threadfence();
+        for (int r0 = 0; r0 < rows; r0 += 8) {
+          const int r = first + min(r0 + lane / 4, rows - 1);  // (the last one again)
+          float v[2][8];
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+              const float4 q = __ldcg(reinterpret_cast<const float4*>(
+                  a.h + r * static_cast<long long>(F) + tile * kTile + c * 32 + lane % 4 * 8 + j));
+              v[c][j] = q.x, v[c][j + 1] = q.y, v[c][j + 2] = q.z, v[c][j + 3] = q.w;
+            }
+          a.parts.write(r, tile, v);
+        }
       });
 }
 
-template <int NT, bool ZEROS>
-__global__ void __launch_bounds__(kWarps * 32) w4_gateup_kernel(const GateUp p) {
-  __shared__ float sums[kWarps * 2 * NT * 128];
-  after_previous();
-  const int strips = p.F / kStrip;
-  const long long tasks = static_cast<long long>(*p.g.count) * strips;
-  for (long long task = blockIdx.x; task < tasks; task += gridDim.x) {
-    const int c = static_cast<int>(task / strips), strip = static_cast<int>(task % strips);
-    gateup_task<NT, ZEROS>(p, c, strip, sums);
-  }
-}
-
 struct Down {
-  Groups g;
-  Weights down;
-  const __nv_bfloat16* h;
-  float* out;  // [slots][d], a row to a slot, before the gates
-  int d, F, slots;
+  Problem<1> p;
+  Rows<kHParts> h;
+  float* out;  // [slots][d], a row to a slot
+  __nv_bfloat16* y;
+  int T;
 };
 
-template <int NT, bool ZEROS>
-__global__ void __launch_bounds__(kWarps * 32) w4_down_kernel(const Down p) {
-  __shared__ float sums[kWarps * NT * 128];
-  after_previous();
-  const int strips = p.d / kStrip;
-  const long long tasks = static_cast<long long>(*p.g.count) * strips;
-  const int g = (threadIdx.x & 31) >> 2;
-  for (long long task = blockIdx.x; task < tasks; task += gridDim.x) {
-    const int c = static_cast<int>(task / strips), strip = static_cast<int>(task % strips);
-    const int e = p.g.expert[c], first = p.g.first[c], rows = p.g.rows[c];
-    const Matrix m[1] = {strip_of<1, ZEROS>(p.down, e, p.d, p.F, strip)};
-    const __nv_bfloat16* x[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      x[n] = n * 8 + g < rows ? p.h + (first + n * 8 + g) * static_cast<long long>(p.F) : nullptr;
-    strip_product<1, NT, 2, ZEROS>(
-        m, p.down.group, p.F, x, static_cast<long long>(p.slots) * p.F, sums,
-        [&](int row, int token, const float (&v)[1]) {
-          if (token < rows)
-            p.out[(first + token) * static_cast<long long>(p.d) + strip * kStrip + row] = v[0];
-        });
-  }
+// Up to 8 tokens: y at once.
+template <bool ZEROS, bool FINE>
+__global__ void __launch_bounds__(kMaxWarps * 32) w4_down_kernel(const Down a) {
+  using Of = Product<1, 1, kHParts, ZEROS, FINE>;
+  extern __shared__ __align__(16) uint8_t shared[];
+  const int d = a.p.rows;
+  Of::run_strips(a.p, a.h, shared, [&](int strip, int row, int token, float sum) {
+    if (token < a.T)
+      a.y[static_cast<long long>(token) * d + strip * kStrip + row] = __float2bfloat16_rn(sum);
+  });
 }
 
-// y_t = sum_j gate_j out[row of slot (t, j)], in the slots' order.
-__global__ void __launch_bounds__(256)
-    w4_combine_kernel(const float* out, const int* slot_row, const float* gate, int T, int d, int k,
-                      __nv_bfloat16* y) {
+// More tokens: the rows' parts of it, which w4_combine_kernel adds.
+template <bool ZEROS, bool FINE>
+__global__ void __launch_bounds__(kWarps * 32, Product<1, 4, kHParts, ZEROS, FINE>::kBlocks)
+    w4_down_rows_kernel(const Down a) {
+  using Of = Product<1, 4, kHParts, ZEROS, FINE>;
+  extern __shared__ __align__(16) uint8_t shared[];
+  const int d = a.p.rows, lane = threadIdx.x & 31;
+  Of::run(a.p, a.h, shared, [&](int r) { return r; },
+          [&](int, int first, int rows, int strip, const float (&acc)[1][4][4]) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int token = n * 8 + lane % 4 * 2 + r % 2;
+                if (token < rows)
+                  a.out[(first + token) * static_cast<long long>(d) + strip * kStrip + lane / 4 +
+                        r / 2 * 8] = acc[0][n][r];
+              }
+          });
+}
+
+// y_t = sum_j out[row of slot (t, j)], in the slots' order: 4 columns to a thread.
+__global__ void __launch_bounds__(128)
+    w4_combine_kernel(const int* slot_row, const float* out, int d, int k, __nv_bfloat16* y) {
+  __shared__ int rows[32];
   after_previous();
-  const long long pairs = static_cast<long long>(T) * d / 2;
-  const long long step = gridDim.x * 256ll;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < pairs; i += step) {
-    const int t = static_cast<int>(i / (d / 2)), c = static_cast<int>(i % (d / 2)) * 2;
-    float2 sum = make_float2(0.f, 0.f);
-    for (int j = 0; j < k; ++j) {
-      const int r = slot_row[t * k + j];
-      if (r < 0) continue;
-      const float w = gate[t * k + j];
-      const float2 v = *reinterpret_cast<const float2*>(out + static_cast<long long>(r) * d + c);
-      sum.x = fmaf(w, v.x, sum.x);
-      sum.y = fmaf(w, v.y, sum.y);
+  const long long t = blockIdx.x;
+  if (threadIdx.x < 32) rows[threadIdx.x] = threadIdx.x < k ? slot_row[t * k + threadIdx.x] : -1;
+  __syncthreads();
+  for (int c = (blockIdx.y * 128 + threadIdx.x) * 4; c < d; c += gridDim.y * 512) {
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < k; j0 += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (rows[j0 + j] >= 0)
+          v[j] = *reinterpret_cast<const float4*>(out + static_cast<long long>(rows[j0 + j]) * d + c);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        sum.x += v[j].x, sum.y += v[j].y, sum.z += v[j].z, sum.w += v[j].w;
     }
-    *reinterpret_cast<uint32_t*>(y + static_cast<long long>(t) * d + c) =
-        pack_bf16x2(sum.x, sum.y);
+    *reinterpret_cast<uint2*>(y + t * d + c) =
+        make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
   }
 }
 
 // ------------------------------------------------------------------------ host side
 
 constexpr int kSms = 152;
-constexpr int kBlocks = 4;  // to an SM
-
 // Rows of an expert that its weights are read once for; more of them are taken in several chunks.
-int chunk_of(int T) { return T <= 8 ? 8 : T <= 16 ? 16 : 32; }
+int chunk_of(int T) { return T <= 8 ? 8 : 32; }
+
+constexpr int kSharedPerSm = 228 * 1024;
+
+// Warps to a strip: what takes least time, in pieces, with one more for each strip's beginning and end;
+// the strips are taken in rounds.
+int split_of(long long strips, int pieces, int warps) {
+  int best = 1;
+  long long least = -1;
+  for (int split = 1; split <= kWarps && split <= pieces; split *= 2) {
+    const long long teams = warps / split, rounds = (strips + teams - 1) / teams;
+    const long long cost = rounds * ((pieces + split - 1) / split + 1);
+    if (least < 0 || cost < least) least = cost, best = split;
+  }
+  return best;
+}
 
 struct Workspace {
   Groups g;
-  __nv_bfloat16* h;
+  Rows<kXParts> x;
+  Rows<kHParts> parts;
+  int* counters;
+  int n_counters;
+  float* h;
   float* out;
   size_t bytes;
 };
@@ -466,15 +983,26 @@ Workspace carve(const moe_problem* p, void* base) {
   w.g.first = reinterpret_cast<int*>(take(chunks * 4));
   w.g.rows = reinterpret_cast<int*>(take(chunks * 4));
   w.g.row_slot = reinterpret_cast<int*>(take(slots * 4));
+  w.g.row_gate = reinterpret_cast<float*>(take(slots * 4));
   w.g.slot_row = reinterpret_cast<int*>(take(slots * 4));
-  w.h = reinterpret_cast<__nv_bfloat16*>(take(slots * p->F * 4));
-  w.out = reinterpret_cast<float*>(take(slots * p->d * 4));
+  w.g.row_of_token = reinterpret_cast<int*>(take(chunk == 8 ? chunks * 32 : 0));
+  const size_t x_tiles = p->d / kTile, h_tiles = p->F / kTile;
+  w.x.tiles = p->d / kTile, w.parts.tiles = p->F / kTile;
+  w.x.parts = take(p->T * x_tiles * (kXParts * kTile * 2));
+  w.x.info = reinterpret_cast<float4*>(take(p->T * x_tiles * 16));
+  w.parts.parts = take(slots * h_tiles * (kHParts * kTile * 2));
+  w.parts.info = reinterpret_cast<float4*>(take(slots * h_tiles * 16));
+  w.n_counters = static_cast<int>((p->T == 1 ? slots : chunks) * h_tiles);
+  w.counters = reinterpret_cast<int*>(take(w.n_counters * 4));
+  w.h = reinterpret_cast<float*>(take(slots * p->F * 4));
+  w.out = reinterpret_cast<float*>(take(chunk == 8 ? 0 : slots * p->d * 4));
   return w;
 }
 
 int check_w4(const moe_problem* p) {
   if (int e = check_problem(p)) return e;
   if (p->r || static_cast<long long>(p->T) * p->k > kMaxSlots) return MOE_ERR_UNSUPPORTED;
+  if (std::max(p->d, p->F) > kMaxWidth) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -533,7 +1061,7 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
   if (int e = check_weights(w_up, p->d)) return e;
   if (int e = check_weights(w_down, p->F)) return e;
   const bool zeros = w_gate->has_zeros != 0;
-  if (w_gate->group != w_up->group || zeros != (w_up->has_zeros != 0) ||
+  if (w_gate->group != w_up->group || w_gate->group != w_down->group || zeros != (w_up->has_zeros != 0) ||
       zeros != (w_down->has_zeros != 0))
     return MOE_ERR_UNSUPPORTED;
   if (misaligned(x, 16) || misaligned(y, 16) || misaligned(topk_idx, 4) ||
@@ -544,47 +1072,69 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
   const Workspace ws = carve(p, workspace);
   const int slots = p->T * p->k, chunk = chunk_of(p->T);
   const auto of = [](const moe_w4* w) { return Weights{w->codes, w->scales, w->group}; };
-  const GateUp up{ws.g, of(w_gate), of(w_up), reinterpret_cast<const __nv_bfloat16*>(x), ws.h,
-                  p->d, p->F, p->k, slots};
-  const Down down{ws.g, of(w_down), ws.h, ws.out, p->d, p->F, slots};
-  const int smem = 32 * p->E * 2;
-  cudaError_t err = launched(cudaFuncSetAttribute(
-      w4_group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 32 * kMaxExperts * 2));
-  mark_before(MOE_KERNEL_W4_GATEUP, stream);
-  if (err == cudaSuccess)
-    err = launch_behind(w4_group_kernel, 1, 1024, smem, stream, topk_idx, slots, p->E, chunk, ws.g,
-                        dev_status);
-  const auto run = [&](auto nt, auto z) {
-    constexpr int NT = decltype(nt)::value;
-    constexpr bool Z = decltype(z)::value;
+  Groups g = ws.g;
+  g.idx = topk_idx, g.gate = topk_gate, g.slots = slots, g.E = p->E, g.single = p->T == 1;
+  const int chunks = std::min(p->E, slots);
+  GateUp up{{g, {of(w_gate), of(w_up)}, p->F, p->d, 1, dev_status}, ws.x, ws.h, ws.parts,
+            ws.counters, p->k};
+  Down down{{g, {of(w_down)}, p->d, p->F, 1, dev_status}, ws.parts, ws.out,
+            reinterpret_cast<__nv_bfloat16*>(y), p->T};
+  cudaError_t err = cudaSuccess;
+  const auto launch = [&](auto kernel, int blocks, int warps, int bytes, auto& args) {
     if (err == cudaSuccess)
-      err = launch_behind(w4_gateup_kernel<NT, Z>, kBlocks * kSms, kWarps * 32, 0, stream, up);
+      err = launched(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    if (err == cudaSuccess) err = launch_behind(kernel, blocks, warps * 32, bytes, stream, args);
+  };
+  const auto by_strips = [&](auto kernel, auto product, auto& args) {
+    using Of = decltype(product);
+    const int blocks = std::min(Of::kBlocks, kSharedPerSm / (Of::kBytes + 1024)) * kSms;
+    args.p.split = split_of(chunks * static_cast<long long>(args.p.rows / kStrip),
+                            (args.p.cols / kTile + kPieceTiles - 1) / kPieceTiles, blocks * kWarps);
+    launch(kernel, blocks, kWarps, Of::kBytes, args);
+  };
+  mark_before(MOE_KERNEL_W4_GATEUP, stream);
+  {
+    const int warps = std::min(32, (slots + 31) / 32);
+    const long long lanes = static_cast<long long>(p->T) * ws.x.tiles * 4;
+    const int blocks = static_cast<int>(std::min<long long>((lanes + 1023) / 1024, 2 * kSms));
+    err = launched(cudaFuncSetAttribute(
+        w4_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 32 * kMaxExperts * 2));
+    if (err == cudaSuccess)
+      err = launch_behind(w4_prepare_kernel, blocks + !g.single, 1024, g.single ? 0 : warps * p->E * 2,
+                          stream, reinterpret_cast<const __nv_bfloat16*>(x), p->T, ws.x, ws.counters,
+                          ws.n_counters, g, p->k, chunk, warps, dev_status);
+  }
+  const auto with = [&](auto z, auto f) {
+    constexpr bool Z = decltype(z)::value, FINE = decltype(f)::value;
+    const bool few = chunk == 8;
+    if (few)
+      by_strips(w4_gateup_kernel<1, Z, FINE>, Product<2, 1, kXParts, Z, FINE>{}, up);
+    else
+      by_strips(w4_gateup_kernel<4, Z, FINE>, Product<2, 4, kXParts, Z, FINE>{}, up);
     mark_after(MOE_KERNEL_W4_GATEUP, stream);
     mark_before(MOE_KERNEL_W4_DOWN, stream);
-    if (err == cudaSuccess)
-      err = launch_behind(w4_down_kernel<NT, Z>, kBlocks * kSms, kWarps * 32, 0, stream, down);
+    if (few) {
+      using Of = Product<1, 1, kHParts, Z, FINE>;
+      const int strips = p->d / kStrip, warps = strips > kSms ? kWarps : kMaxWarps;
+      launch(w4_down_kernel<Z, FINE>, std::min(strips, 2 * kSms * kWarps / warps), warps,
+             warps * Of::kWarpBytes, down);
+    } else {
+      by_strips(w4_down_rows_kernel<Z, FINE>, Product<1, 4, kHParts, Z, FINE>{}, down);
+      if (err == cudaSuccess)
+        err = launch_behind(w4_combine_kernel, dim3(p->T, std::min(64, (p->d + 511) / 512)), 128, 0,
+                            stream, ws.g.slot_row, ws.out, p->d, p->k, down.y);
+    }
   };
-  const auto with_chunk = [&](auto z) {
-    if (chunk == 8)
-      run(std::integral_constant<int, 1>{}, z);
-    else if (chunk == 16)
-      run(std::integral_constant<int, 2>{}, z);
-    else
-      run(std::integral_constant<int, 4>{}, z);
-  };
-  if (zeros)
-    with_chunk(std::true_type{});
+  if (zeros && w_gate->group == 32)
+    with(std::true_type{}, std::true_type{});
+  else if (zeros)
+    with(std::true_type{}, std::false_type{});
+  else if (w_gate->group == 32)
+    with(std::false_type{}, std::true_type{});
   else
-    with_chunk(std::false_type{});
-  if (err == cudaSuccess) {
-    const long long pairs = static_cast<long long>(p->T) * p->d / 2;
-    err = launch_behind(w4_combine_kernel,
-                        static_cast<int>(std::min<long long>((pairs + 255) / 256, 8ll * kSms)), 256, 0, stream,
-                        ws.out, ws.g.slot_row, topk_gate, p->T, p->d, p->k,
-                        reinterpret_cast<__nv_bfloat16*>(y));
-  }
+    with(std::false_type{}, std::false_type{});
   mark_after(MOE_KERNEL_W4_DOWN, stream);
-  count_launches(4);
+  count_launches(3 + (chunk != 8));
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
