@@ -19,7 +19,8 @@ constexpr int kWarps = 8;  // a token to each: the 8 tokens of a row of prob_par
 constexpr int kMaxE = 1024;
 
 struct Select {
-  int T, E, k, groups, kept, best, group_size, lanes;  // lanes of a group: 32 / (groups, up to 2^n)
+  int T, E, k, groups, kept, best, group_size;
+  int lanes, lanes_log2;  // of a group: 32 / (groups, up to 2^n)
   int sigmoid, renormalise;
   float scale;
   const void* logits;
@@ -50,13 +51,18 @@ __device__ __forceinline__ Two warp_sum(Two v) {
 // A logit; what is not a number counts as -inf.
 template <typename T>
 __device__ __forceinline__ float logit(const T* row, int e) {
-  const float v = static_cast<float>(row[e]);
-  return v == v ? v : -INFINITY;
+  return fmaxf(static_cast<float>(row[e]), -INFINITY);
 }
 
 __device__ __forceinline__ float sigmoid(float l) {
   const float e = expf(-fabsf(l)), t = e / (1.f + e);
   return l < 0.f ? t : 1.f / (1.f + e);
+}
+// The same by the hardware's approximations.  exp(-|l|) is off by (|l| + 4) 2^-24 of it, the reciprocal
+// by 2^-23, which leaves the score off by 8 x 2^-24 at most (|l| e^-|l| < 0.4).
+__device__ __forceinline__ float quick_sigmoid(float l) {
+  const float e = __expf(-fabsf(l)), r = __fdividef(1.f, 1.f + e);
+  return l < 0.f ? e * r : r;
 }
 
 // A score, where only its share in a sum is wanted: softmax scores without their sum, and sigmoid
@@ -68,6 +74,33 @@ __device__ __forceinline__ float unscaled(float l, float most, bool sigmoid_scor
   return expf(l - most);
 }
 
+template <int VEC>
+__device__ __forceinline__ void load_logits(const float* p, float (&v)[VEC]) {
+  if constexpr (VEC == 4) {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+  } else {
+    v[0] = *p;
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void store_scores(float* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 4)
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *p = v[0];
+}
+template <int VEC>
+__device__ __forceinline__ void load_logits(const __nv_bfloat16* p, float (&v)[VEC]) {
+  if constexpr (VEC == 4) {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xffff0000u);
+    v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xffff0000u);
+  } else {
+    v[0] = static_cast<float>(*p);
+  }
+}
+
 // The scores of a row's selected experts over their sum, one to a lane (0 for lanes that hold none: l
 // = -inf), and 0 where that sum is.
 __device__ __forceinline__ float share(float l, bool sigmoid_scores) {
@@ -76,150 +109,460 @@ __device__ __forceinline__ float share(float l, bool sigmoid_scores) {
   return sum == 0.f ? 0.f : v / sum;  // (a NaN stays one)
 }
 
-// One warp to a token.  Its lanes are parted among the groups; lane i of a group has every
-// lanes'th of its experts from i on, VPL of them at most.
-template <typename T, int VPL>
-__global__ void __launch_bounds__(kWarps * 32) route_select_kernel(const Select s) {
-  extern __shared__ float shares[];  // [kWarps][E]
+// What a lane of a token's warp holds: the lanes are parted among the groups, and a group's lanes take
+// `vec` neighbouring ones of its experts in turn.
+struct Share {
+  int group, first, step, vec, count;  // its first expert, from one of its vecs to the next, how many
+  bool have;
+  __device__ __forceinline__ Share(const Select& s, int vec_) : vec(vec_) {
+    const int lane = threadIdx.x & 31;
+    group = lane >> s.lanes_log2;
+    have = group < s.groups;
+    const int sub = (lane & (s.lanes - 1)) * vec;
+    first = group * s.group_size + sub;
+    step = s.lanes * vec;
+    count = have && sub < s.group_size ? ((s.group_size - sub + step - 1) / vec >> s.lanes_log2) * vec : 0;
+  }
+  __device__ __forceinline__ int expert(int j) const { return first + j / vec * step + j % vec; }
+};
+
+// Whether the lane's group is among those kept, `worth` being the key of its value.
+__device__ __forceinline__ bool group_kept(const Select& s, uint64_t worth, int group) {
+  int before = 0;
+  for (int g = 0; g < s.groups; ++g) {
+    const uint64_t other = __shfl_sync(~0u, worth, g * s.lanes);
+    before += other > worth || (other == worth && g < group);
+  }
+  return group < s.groups && before < s.kept;
+}
+
+__device__ __forceinline__ uint64_t warp_most(uint64_t v) {
+  const uint32_t hi = __reduce_max_sync(~0u, static_cast<uint32_t>(v >> 32));
+  const uint32_t lo =
+      __reduce_max_sync(~0u, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+// Scores (and biases) as two floats.  What follows up to the kernel runs for few tokens, on an SM
+// whose instruction cache has not got it: short code and loops that are not unrolled matter more than
+// the number of instructions.  (Unrolled, three tokens of 16384 that came here took 50 us.)
+__device__ __noinline__ Two exact_score(float l, float most, bool sigmoid, Two total, float bias) {
+  const float shift = most == -INFINITY ? 0.f : most;
+  const Two e = two_exp(sigmoid ? Two{-fabsf(l), 0.f} : two_sum(l, -shift));
+  // sigmoid: e / (1 + e), or what that lacks to 1, which keeps its own precision; softmax: e / total
+  const Two one = quick_sum(1.f, e.hi);
+  Two c = e / (sigmoid ? quick_sum(one.hi, __fadd_rn(one.lo, e.lo)) : total);
+  if (sigmoid && l >= 0.f) {
+    const Two rest = quick_sum(1.f, -c.hi);
+    c = quick_sum(rest.hi, __fsub_rn(rest.lo, c.lo));
+  }
+  if (!sigmoid && most == INFINITY) c = {NAN, 0.f};
+  const Two w = two_sum(c.hi, bias);
+  c = quick_sum(w.hi, __fadd_rn(w.lo, c.lo));
+  if (isinf(w.hi)) c = {w.hi, 0.f};
+  return w.hi != w.hi ? Two{-INFINITY, 0.f} : c;
+}
+
+struct Exact {
+  Two total;  // of softmax's exponentials
+  float most;
+  const float* bias;
+  bool sigmoid;
+  template <typename T>
+  __device__ __forceinline__ Exact(const Select& s, const Share& mine, const T* row, float most_)
+      : total{0.f, 0.f}, most(most_), bias(s.bias), sigmoid(s.sigmoid) {
+    if (sigmoid) return;
+    const float shift = most == -INFINITY ? 0.f : most;
+#pragma unroll 1
+    for (int j = 0; j < mine.count; ++j)
+      total = total + two_exp(two_sum(logit(row, mine.expert(j)), -shift));
+#pragma unroll 1
+    for (int o = 16; o; o >>= 1)
+      total = total + Two{__shfl_xor_sync(~0u, total.hi, o), __shfl_xor_sync(~0u, total.lo, o)};
+    if (total.hi == 0.f) total.hi = 1.f;
+  }
+  __device__ __forceinline__ Two score(float l, int e) const {
+    return exact_score(l, most, sigmoid, total, bias ? bias[e] : 0.f);
+  }
+};
+
+// The selection by such scores: lane r gets the r-th expert.  Rarely called: short code and few
+// registers (its keys are in local memory) matter more than its time, several times that of the
+// selection in fp32.
+template <typename T>
+__device__ __noinline__ int select_exactly(const Select& s, const T* row, float most, int vec) {
+  Share mine(s, vec);
+  const int lane = threadIdx.x & 31;
+  const Exact exact(s, mine, row, most);
+  uint64_t key[64];
+  uint64_t top[2] = {0, 0};  // the lane's largest two, of the group's then
+  Two value[2] = {{-INFINITY, 0.f}, {-INFINITY, 0.f}};
+  const auto put = [&](uint64_t of, Two c) {
+    if (of > top[0]) {
+      top[1] = top[0], value[1] = value[0];
+      top[0] = of, value[0] = c;
+    } else if (of > top[1]) {
+      top[1] = of, value[1] = c;
+    }
+  };
+#pragma unroll 1
+  for (int j = 0; j < mine.count; ++j) {
+    const float l = logit(row, mine.expert(j));
+    const Two c = exact.score(l, mine.expert(j));
+    const uint64_t of = two_key(c);
+    key[j] = s.bias ? of : two_key({l, 0.f});
+    put(of, c);
+  }
+  if (s.groups > 1) {
+#pragma unroll 1
+    for (int o = s.lanes / 2; o; o >>= 1) {
+      const uint64_t k0 = __shfl_xor_sync(~0u, top[0], o), k1 = __shfl_xor_sync(~0u, top[1], o);
+      const Two v0{__shfl_xor_sync(~0u, value[0].hi, o), __shfl_xor_sync(~0u, value[0].lo, o)};
+      const Two v1{__shfl_xor_sync(~0u, value[1].hi, o), __shfl_xor_sync(~0u, value[1].lo, o)};
+      put(k0, v0);
+      put(k1, v1);
+    }
+    Two worth = value[0];
+    if (s.best == 2)
+      worth = isinf(value[0].hi) || isinf(value[1].hi) ? Two{value[0].hi + value[1].hi, 0.f}
+                                                       : value[0] + value[1];
+    if (!group_kept(s, two_key(worth), mine.group)) mine.count = 0;
+  }
+  // k rounds: the lane whose first it was (of equal ones the lowest expert) looks for its next
+  uint64_t head = ~0ull;
+  int expert = -1, chosen = 0;
+  const auto next = [&] {
+    const uint64_t below = head;
+    const int after = expert;
+    head = 0, expert = kMaxE;
+#pragma unroll 1
+    for (int j = 0; j < mine.count; ++j)
+      if ((key[j] < below || (key[j] == below && mine.expert(j) > after)) && key[j] > head)
+        head = key[j], expert = mine.expert(j);
+  };
+  next();
+#pragma unroll 1
+  for (int r = 0; r < s.k; ++r) {
+    const uint64_t best = warp_most(head);
+    const int e = __reduce_min_sync(~0u, head == best ? expert : kMaxE);
+    if (lane == r) chosen = e;
+    if (expert == e) next();
+  }
+  return chosen;
+}
+
+// Whether the lane's group is among those kept, by exact values: those of the experts from `least` on
+// (of their scores in fp32, times `scale`, and biases), which are in `list` then, 64 at most: -1 for
+// more.  One to a lane and turn.
+template <typename T>
+__device__ __noinline__ int keep_exactly(const Select& s, const T* row, const float* row_scores,
+                                         float scale, float most, float least, int vec, int* list,
+                                         Two* values) {
+  const Share mine(s, vec);
+  const Exact exact(s, mine, row, most);
+  const int lane = threadIdx.x & 31;
+  const auto wanted = [&](int j) {
+    const int e = mine.expert(j);
+    return fmaxf(row_scores[e] * scale + (s.bias ? s.bias[e] : 0.f), -INFINITY) >= least;
+  };
+  int to = 0;
+#pragma unroll 1
+  for (int j = 0; j < mine.count; ++j) to += wanted(j);
+  const int own = to;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int before = __shfl_up_sync(~0u, to, o);
+    if (lane >= o) to += before;
+  }
+  const int n = __shfl_sync(~0u, to, 31);
+  if (n > 64) return -1;
+  to -= own;
+#pragma unroll 1
+  for (int j = 0; j < mine.count; ++j)
+    if (wanted(j)) list[to++] = mine.expert(j);
+  __syncwarp();
+#pragma unroll 1
+  for (int i = lane; i < n; i += 32)
+    values[i] = exact.score(logit(row, list[i]), list[i]);
+  __syncwarp();
+  Two top[2] = {{-INFINITY, 0.f}, {-INFINITY, 0.f}};
+#pragma unroll 1
+  for (int i = 0; i < n; ++i)
+    if (static_cast<unsigned>(list[i] - mine.group * s.group_size) < static_cast<unsigned>(s.group_size)) {
+      const Two c = values[i];
+      if (two_key(c) > two_key(top[0]))
+        top[1] = top[0], top[0] = c;
+      else if (two_key(c) > two_key(top[1]))
+        top[1] = c;
+    }
+  __syncwarp();  // (the list is used again)
+  Two worth = top[0];
+  if (s.best == 2)
+    worth = isinf(top[0].hi) || isinf(top[1].hi) ? Two{top[0].hi + top[1].hi, 0.f} : top[0] + top[1];
+  return group_kept(s, two_key(worth), mine.group);
+}
+
+// The selection from candidates, up to two to a lane (kMaxE: none), which hold all that can be chosen.
+template <typename T>
+__device__ __noinline__ int order_exactly(const Select& s, const T* row, float most, int vec,
+                                          int expert0, int expert1) {
+  const Exact exact(s, Share(s, vec), row, most);
+  uint64_t key0 = 0, key1 = 0;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    key1 = key0;
+    const int e = i ? expert0 : expert1;
+    if (__any_sync(~0u, e < kMaxE)) {
+      const int at = min(e, s.E - 1);
+      key0 = two_key(exact.score(logit(row, at), at));
+    }
+    if (e >= kMaxE) key0 = 0;
+  }
+  if (key1 > key0 || (key1 == key0 && expert1 < expert0)) {
+    const uint64_t key = key0;
+    const int expert = expert0;
+    key0 = key1, expert0 = expert1;
+    key1 = key, expert1 = expert;
+  }
+  int chosen = 0;
+#pragma unroll 1
+  for (int r = 0; r < s.k; ++r) {
+    const uint64_t best = warp_most(key0);
+    const int e = __reduce_min_sync(~0u, key0 == best ? expert0 : kMaxE);
+    if (static_cast<int>(threadIdx.x & 31) == r) chosen = e;
+    if (expert0 == e) key0 = key1, expert0 = expert1, key1 = 0, expert1 = kMaxE;
+  }
+  return chosen;
+}
+
+// One warp to a token, VPL experts to a lane at most.  The scores are formed in fp32 and selected by;
+// where two that stand next to each other in the order (or the last group kept and the first one left
+// out) are nearer than their rounding, the token is selected again with scores as two floats.  Equal
+// logits with equal biases have equal scores and need that not.
+template <typename T, int VPL, int VEC, bool SIGMOID>
+__global__ void __launch_bounds__(kWarps * 32, VPL <= 16 ? 4 : VPL <= 32 ? 3 : 2)
+    route_select_kernel(const __grid_constant__ Select s) {
+  extern __shared__ __align__(16) float scores[];  // [kWarps][E], as they are formed
+  __shared__ uint2 candidates[kWarps][96];
+  __shared__ float share_of[kWarps];  // 1 / their sum
   after_previous();
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const long long t = static_cast<long long>(blockIdx.x) * kWarps + warp;
-  float* mine = shares + warp * s.E;
   if (t < s.T) {
     const T* row = static_cast<const T*>(s.logits) + t * s.ld;
-    const int group = lane / s.lanes, sub = lane % s.lanes;
-    const bool have = group < s.groups;
-    const auto in = [&](int j) { return have && sub + j * s.lanes < s.group_size; };
-    const auto expert = [&](int j) { return group * s.group_size + sub + j * s.lanes; };
-    float l[VPL], lo[VPL];
-    float most = -INFINITY, sum = 0.f;
+    float* row_scores = scores + warp * s.E;
+    const Share mine(s, VEC);
+    float v[VPL];  // logits, then what is compared; NaN: none
+    float most = -INFINITY, sum = 0.f, inv = 1.f;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      l[j] = in(j) ? logit(row, expert(j)) : -INFINITY;
-      most = fmaxf(most, l[j]);
+    for (int j = 0; j < VPL; j += VEC) {
+      float q[VEC];
+      if (j < mine.count) load_logits<VEC>(row + mine.expert(j), q);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[j + i] = j < mine.count ? fmaxf(q[i], -INFINITY) : NAN;
     }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) most = fmaxf(most, v[j]);
     most = warp_max(most);
-    // scores for the sums over tokens, in fp32
-    const float shift = most == -INFINITY ? 0.f : most;
+    bool exact = true;
+    const bool small = SIGMOID && !(most > -40.f);  // scores below 2^-57
+    const bool by_score = s.bias || s.groups > 1;
+    if (s.partials || by_score || (!SIGMOID && !s.renormalise)) {
+      const float shift = most == -INFINITY ? 0.f : most;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (in(j)) sum += unscaled(l[j], most, s.sigmoid);
-    sum = warp_sum(sum);
-    if (s.partials) {
+      for (int j = 0; j < VPL; j += VEC) {
+        if (j >= mine.count) continue;
+        float q[VEC];
 #pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if (in(j)) {
-          const float v = unscaled(l[j], most, s.sigmoid);
-          mine[expert(j)] = sum == 0.f ? 0.f : v / sum;
+        for (int i = 0; i < VEC; ++i) {
+          q[i] = SIGMOID ? quick_sigmoid(v[j + i]) : __expf(v[j + i] - shift);
+          sum += q[i];
         }
-    }
-    // what is compared: scores (+ bias) as two floats, in l and lo
-    Two total{0.f, 0.f};
-    const bool by_logit = !s.bias;
-    const auto score = [&](int j) -> Two {
-      if (s.sigmoid) return two_sigmoid(l[j]);
-      const Two e = two_exp(two_sum(l[j], -shift));
-      return most == INFINITY ? Two{NAN, 0.f} : e / total;
-    };
-    if (!s.sigmoid && (s.bias || s.groups > 1)) {
+        store_scores<VEC>(row_scores + mine.expert(j), q);
+      }
+      if (small) {  // what is added up over tokens is their shares
+        sum = 0.f;
 #pragma unroll 1
-      for (int j = 0; j < VPL; ++j)
-        if (in(j)) total = total + two_exp(two_sum(l[j], -shift));
-      total = warp_sum(total);
-      if (total.hi == 0.f) total.hi = 1.f;
-    }
-    uint64_t key[VPL];
-    uint64_t top[2] = {0, 0};  // the lane's largest two, of the group's then
-    Two value[2] = {{-INFINITY, 0.f}, {-INFINITY, 0.f}};
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      key[j] = 0;
-      if (!in(j)) continue;
-      Two c{l[j], 0.f};
-      if (s.bias || s.groups > 1) c = score(j);
-      if (s.bias) {
-        const float b = s.bias[expert(j)];
-        const Two w = two_sum(c.hi, b);
-        c = quick_sum(w.hi, __fadd_rn(w.lo, c.lo));
-        if (isinf(w.hi) || w.hi != w.hi) c = {w.hi == w.hi ? w.hi : -INFINITY, 0.f};
-      }
-      const uint64_t of = two_key(c);
-      key[j] = by_logit ? two_key({l[j], 0.f}) : of;
-      if (s.groups > 1) {
-        if (c.hi != c.hi) c = {-INFINITY, 0.f};
-        if (of > top[0]) {
-          top[1] = top[0], value[1] = value[0];
-          top[0] = of, value[0] = c;
-        } else if (of > top[1]) {
-          top[1] = of, value[1] = c;
+        for (int j = 0; j < mine.count; ++j) {
+          const float q = unscaled(logit(row, mine.expert(j)), most, true);
+          sum += q;
+          row_scores[mine.expert(j)] = q;
         }
+        if (s.bias) exact = false;  // they need more than fp32 beside it
       }
+      sum = warp_sum(sum);
+      inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
+      if (lane == 0) share_of[warp] = inv;
     }
-    bool in_kept = have;
-    if (s.groups > 1) {
-      for (int o = s.lanes / 2; o; o >>= 1) {
-        uint64_t other[2];
-        Two theirs[2];
+    // Errors of scores are at most `step` of their size: 8 halves of an fp32 step of sigmoid's, and
+    // for softmax |l - most| + VPL + 20 of them; of the sum with a bias one more.
+    const float step = SIGMOID ? 0x1p-21f : 0x1p-17f;
+    const float largest = SIGMOID ? 1.f : inv;  // what no score is above
+    bool kept = true;
+    if (by_score) {
+      float top[2] = {-INFINITY, -INFINITY};
+      const bool by_logit = !s.bias && s.best == 1;  // the order of the largest scores
+      if (!by_logit) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          other[i] = __shfl_xor_sync(~0u, top[i], o);
-          theirs[i].hi = __shfl_xor_sync(~0u, value[i].hi, o);
-          theirs[i].lo = __shfl_xor_sync(~0u, value[i].lo, o);
-        }
+        for (int j = 0; j < VPL; j += VEC) {
+          if (j >= mine.count) continue;
+          float q[VEC], b[VEC];
+          load_logits<VEC>(row_scores + mine.expert(j), q);
+          if (s.bias) load_logits<VEC>(s.bias + mine.expert(j), b);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (other[i] > top[0]) {
-            top[1] = top[0], value[1] = value[0];
-            top[0] = other[i], value[0] = theirs[i];
-          } else if (other[i] > top[1]) {
-            top[1] = other[i], value[1] = theirs[i];
+          for (int i = 0; i < VEC; ++i) {
+            float c = SIGMOID ? q[i] : q[i] * inv;
+            if (s.bias) v[j + i] = c = fmaxf(c + b[i], -INFINITY);
+            if (s.groups > 1) {
+              top[1] = fmaxf(top[1], fminf(top[0], c));
+              top[0] = fmaxf(top[0], c);
+            }
           }
+        }
       }
-      Two worth = value[0];
-      if (s.best == 2) {
-        worth = isinf(value[0].hi) || isinf(value[1].hi)
-                    ? Two{value[0].hi + value[1].hi, 0.f}
-                    : value[0] + value[1];
+      if (s.groups > 1) {
+        if (by_logit)
+#pragma unroll
+          for (int j = 0; j < VPL; ++j) top[0] = fmaxf(top[0], v[j]);
+        for (int o = s.lanes / 2; o; o >>= 1) {
+          const float a = __shfl_xor_sync(~0u, top[0], o), b = __shfl_xor_sync(~0u, top[1], o);
+          top[1] = fmaxf(fmaxf(top[1], b), fminf(top[0], a));
+          top[0] = fmaxf(top[0], a);
+        }
+        const float worth = fmaxf(s.best == 2 ? top[0] + top[1] : top[0], -INFINITY);
+        kept = group_kept(s, ordered_bits(worth), mine.group);
+        if (!by_logit && s.kept < s.groups) {
+          const float last = -warp_max(kept ? -worth : -INFINITY);
+          const float next = warp_max(mine.have && !kept ? worth : -INFINITY);
+          // two sums of one or two scores (and biases)
+          const float size = 2.f * s.best * largest + fabsf(last) + fabsf(next);
+          if (!(last - next > size * step)) {
+            // experts that may be among the largest of their group
+            const float least = s.best == 2 ? top[1] : top[0];
+            const int by_value = keep_exactly(
+                s, row, row_scores, SIGMOID ? 1.f : inv, most,
+                least - (2.f * largest + 0.5f * fabsf(least)) * step, VEC,
+                reinterpret_cast<int*>(candidates[warp]),
+                reinterpret_cast<Two*>(candidates[warp] + 32));
+            if (__any_sync(~0u, by_value < 0))
+              exact = false;
+            else
+              kept = by_value;
+          }
+        }
+        if (!kept)
+#pragma unroll
+          for (int j = 0; j < VPL; ++j) v[j] = NAN;
       }
-      const uint64_t v = two_key(worth);
-      int before = 0;
-      for (int g = 0; g < s.groups; ++g) {
-        const uint64_t other = __shfl_sync(~0u, v, g * s.lanes);
-        before += other > v || (other == v && g < group);
-      }
-      in_kept = have && before < s.kept;
     }
-    // k rounds: the warp's largest key (of equal ones the lowest expert) goes to lane r
-    uint64_t head = 0;
-    int head_expert = kMaxE;
-    const auto next = [&](uint64_t below, int after) {
-      head = 0, head_expert = kMaxE;
+    // Candidates: all from a threshold on that leaves k + 1 of them at least, and 64 at most.  At
+    // least as many are above it as there are lanes' halves whose largest is: bisected until those
+    // are few.  (As keys in the values' order; 0: none.)
+    float half[2] = {NAN, NAN};
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) half[j >= VPL / 2] = fmaxf(half[j >= VPL / 2], v[j]);
+    const uint32_t key0 = half[0] == half[0] ? ordered_bits(half[0]) : 0;
+    const uint32_t key1 = half[1] == half[1] ? ordered_bits(half[1]) : 0;
+    const auto above = [&](uint32_t from) {
+      return __popc(__ballot_sync(~0u, key0 >= from)) + __popc(__ballot_sync(~0u, key1 >= from));
+    };
+    const uint32_t low = min(key0, key1);
+    uint32_t over = __reduce_max_sync(~0u, max(key0, key1));
+    uint32_t least = __reduce_min_sync(~0u, low ? low : ~0u);
+    constexpr uint32_t kLowest = 0x007fffffu;  // of -inf
+    if (above(least) <= s.k) least = kLowest;
+    for (int i = 0; i < 12 && least < over; ++i) {
+      const uint32_t middle = least + (over - least + 1) / 2;
+      const int n = above(middle);
+      if (n <= s.k) {
+        over = middle - 1;
+      } else {
+        least = middle;
+        if (n <= s.k + 8) break;
+      }
+    }
+    float from;
+    int own, n;
+    // Counted; and, where they are more than 64 (rare), bisected on by their own number.
+    uint32_t under = least, most_key = __reduce_max_sync(~0u, max(key0, key1));
+    for (;;) {
+      from = ordered_value(least);
+      own = 0;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) own += v[j] >= from;
+      n = __reduce_add_sync(~0u, own);
+      if (n > 64)
+        under = least;
+      else if (n <= s.k && least > under)
+        most_key = least - 1;
+      else
+        break;
+      if (under >= most_key) break;
+      least = under + (most_key - under + 1) / 2;
+    }
+    int to = own;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int before = __shfl_up_sync(~0u, to, o);
+      if (lane >= o) to += before;
+    }
+    to -= own;
+    int chosen = 0;
+    if (n > 64 || (n <= s.k && least > kLowest)) {  // (equal ones are not parted)
+      exact = false;
+    } else if (exact) {
+      uint2* list = candidates[warp];
 #pragma unroll
       for (int j = 0; j < VPL; ++j)
-        if (in_kept && key[j] && (key[j] < below || (key[j] == below && expert(j) > after)) &&
-            key[j] > head)
-          head = key[j], head_expert = expert(j);
-    };
-    next(~0ull, -1);
-    int chosen = 0;
-    for (int r = 0; r < s.k; ++r) {
-      const uint32_t hi = __reduce_max_sync(~0u, static_cast<uint32_t>(head >> 32));
-      const uint32_t low = __reduce_max_sync(
-          ~0u, static_cast<uint32_t>(head >> 32) == hi ? static_cast<uint32_t>(head) : 0u);
-      const uint64_t best = static_cast<uint64_t>(hi) << 32 | low;
-      const int e = __reduce_min_sync(~0u, head == best ? head_expert : kMaxE);
-      if (lane == r) chosen = e;
-      if (head_expert == e) next(best, e);
+        if (v[j] >= from)
+          list[to++] = make_uint2(ordered_bits(v[j]), static_cast<uint32_t>(mine.expert(j)));
+      __syncwarp();
+      // two to a lane, the larger one (of equal ones the lower expert) first
+      uint2 first = make_uint2(0, kMaxE), second = first;
+      if (lane < n) first = list[lane];
+      if (lane + 32 < n) second = list[lane + 32];
+      const int expert0 = first.y, expert1 = second.y;
+      if (second.x > first.x || (second.x == first.x && second.y < first.y)) {
+        const uint2 swap = first;
+        first = second, second = swap;
+      }
+      // k rounds: the warp's first goes to lane r; and one more, whose key goes to all
+      uint32_t of = 0, after = 0;
+      for (int r = 0; r <= s.k; ++r) {
+        const uint32_t best = __reduce_max_sync(~0u, first.x);
+        const int e = __reduce_min_sync(~0u, first.x == best ? first.y : kMaxE);
+        if (lane == r && r < s.k) chosen = e, of = best;
+        if (lane == r - 1) after = best;
+        if (r == s.k) break;
+        if (static_cast<int>(first.y) == e) first = second, second = make_uint2(0, kMaxE);
+      }
+      if (s.bias) {
+        bool near = false, edge = false;
+        if (lane < s.k && after) {
+          const float a = ordered_value(of), b = ordered_value(after);
+          const float size = 2.f * largest + (fabsf(a) + fabsf(b)) * 0.25f;
+          near = !(a - b > size * step);
+          // candidates end too near to the last one chosen
+          edge = lane == s.k - 1 && !(a - from > size * step);
+        }
+        if (__any_sync(~0u, near)) {
+          if (__any_sync(~0u, edge))
+            exact = false;
+          else
+            chosen = order_exactly(s, row, most, VEC, expert0, expert1);
+        }
+      }
     }
+    if (!exact) chosen = select_exactly(s, row, most, VEC);
     const bool slot = lane < s.k;
-    const float of = slot ? logit(row, chosen) : -INFINITY;
+    const float l = slot ? logit(row, chosen) : -INFINITY;
     float g;
     if (s.renormalise)
-      g = share(of, s.sigmoid);
-    else if (s.sigmoid)
-      g = sigmoid(of);
+      g = share(l, SIGMOID);
+    else if (SIGMOID)
+      g = sigmoid(l);
     else
-      g = sum == 0.f ? 0.f : unscaled(of, most, false) / sum;
+      g = sum == 0.f ? 0.f : unscaled(l, most, false) / sum;
     if (slot) {
       s.idx[t * s.k + lane] = chosen;
       s.gate[t * s.k + lane] = s.scale * g;
@@ -231,7 +574,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_select_kernel(const Select 
                                           s.T - static_cast<long long>(blockIdx.x) * kWarps));
   for (int e = threadIdx.x; e < s.E; e += kWarps * 32) {
     float sum = 0.f;
-    for (int w = 0; w < tokens; ++w) sum += shares[w * s.E + e];
+    for (int w = 0; w < tokens; ++w) sum = fmaf(scores[w * s.E + e], share_of[w], sum);
     s.partials[static_cast<long long>(blockIdx.x) * s.E + e] = sum;
   }
 }
@@ -334,22 +677,27 @@ int check(int T, int E, int k, const moe_route_rule* r, int dtype, const void* l
 
 int blocks_of(int T) { return route_num_partials(T); }
 
-// Calls f(VPL) for what a lane holds.
+// Calls f(VPL, VEC) for what a lane holds.
 template <typename F>
-void with_values(int per_lane, F f) {
-  using std::integral_constant;
+void with_values(int per_lane, bool fours, F f) {
+  const auto with = [&](auto v) {
+    if (fours)
+      f(v, std::integral_constant<int, 4>{});
+    else
+      f(v, std::integral_constant<int, 1>{});
+  };
   if (per_lane <= 4)
-    f(integral_constant<int, 4>{});
+    with(std::integral_constant<int, 4>{});
   else if (per_lane <= 8)
-    f(integral_constant<int, 8>{});
+    with(std::integral_constant<int, 8>{});
   else if (per_lane <= 16)
-    f(integral_constant<int, 16>{});
+    with(std::integral_constant<int, 16>{});
   else if (per_lane <= 28)
-    f(integral_constant<int, 28>{});
+    with(std::integral_constant<int, 28>{});
   else if (per_lane <= 32)
-    f(integral_constant<int, 32>{});
+    with(std::integral_constant<int, 32>{});
   else
-    f(integral_constant<int, 64>{});
+    with(std::integral_constant<int, 64>{});
 }
 
 }  // namespace
@@ -373,7 +721,8 @@ int moe_route_select(int32_t T, int32_t E, int32_t k, const moe_route_rule* rule
   s.groups = rule->groups, s.kept = rule->groups_kept, s.best = rule->group_best;
   s.group_size = E / s.groups;
   s.lanes = 32;
-  for (int g = 1; g < s.groups; g *= 2) s.lanes /= 2;
+  s.lanes_log2 = 5;
+  for (int g = 1; g < s.groups; g *= 2) s.lanes /= 2, --s.lanes_log2;
   s.sigmoid = rule->score == MOE_SCORE_SIGMOID;
   s.renormalise = rule->renormalise != 0;
   s.scale = rule->scale;
@@ -381,14 +730,29 @@ int moe_route_select(int32_t T, int32_t E, int32_t k, const moe_route_rule* rule
   s.idx = topk_idx, s.gate = topk_gate, s.partials = prob_partials;
   mark_before(MOE_KERNEL_ROUTE_SELECT, stream);
   cudaError_t err = cudaSuccess;
-  with_values((s.group_size + s.lanes - 1) / s.lanes, [&](auto v) {
-    constexpr int VPL = decltype(v)::value;
-    const int smem = prob_partials ? kWarps * E * 4 : 0;
+  // four neighbours to a load where rows and groups begin on such boundaries
+  const int bytes = dtype == MOE_F32 ? 16 : 8;
+  const bool fours = s.group_size % 4 == 0 && s.ld % 4 == 0 && !misaligned(logits, bytes) &&
+                     !misaligned(select_bias, 16);
+  const int vec = fours ? 4 : 1, per = s.lanes * vec;
+  with_values((s.group_size + per - 1) / per * vec, fours, [&](auto v, auto c) {
+    constexpr int VPL = decltype(v)::value, VEC = decltype(c)::value;
+    const bool stored = prob_partials || s.bias || s.groups > 1 || (!s.sigmoid && !s.renormalise);
+    const int smem = stored ? kWarps * E * 4 : 0;
+    const auto launch = [&](auto kernel) {
+      err = launch_behind(kernel, blocks_of(T), kWarps * 32, smem, stream, s);
+    };
+    const auto with = [&](auto type) {
+      using L = decltype(type);
+      if (s.sigmoid)
+        launch(route_select_kernel<L, VPL, VEC, true>);
+      else
+        launch(route_select_kernel<L, VPL, VEC, false>);
+    };
     if (dtype == MOE_F32)
-      err = launch_behind(route_select_kernel<float, VPL>, blocks_of(T), kWarps * 32, smem, stream, s);
+      with(float{});
     else
-      err = launch_behind(route_select_kernel<__nv_bfloat16, VPL>, blocks_of(T), kWarps * 32, smem,
-                          stream, s);
+      with(__nv_bfloat16{});
   });
   mark_after(MOE_KERNEL_ROUTE_SELECT, stream);
   count_launches(1);

@@ -85,20 +85,13 @@ __device__ __forceinline__ Two two_exp(Two x) {
   return {e.hi * scale, e.lo * scale};
 }
 
-// 1 / (1 + exp(-l)); what it lacks to 1 keeps its own precision.
-__device__ __forceinline__ Two two_sigmoid(float l) {
-  const Two e = two_exp({-fabsf(l), 0.f});
-  const Two one = quick_sum(1.f, e.hi);
-  const Two t = e / quick_sum(one.hi, __fadd_rn(one.lo, e.lo));
-  if (l < 0.f) return t;
-  const Two s = quick_sum(1.f, -t.hi);
-  return quick_sum(s.hi, __fsub_rn(s.lo, t.lo));
-}
-
 // A 64-bit key in the numbers' order.  What is not a number comes with -inf.
 __device__ __forceinline__ uint32_t ordered_bits(float v) {
   const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float ordered_value(uint32_t u) {
+  return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
 }
 __device__ __forceinline__ uint64_t two_key(Two v) {
   if (v.hi != v.hi) v.hi = -INFINITY;
