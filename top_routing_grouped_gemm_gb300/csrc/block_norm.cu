@@ -33,45 +33,56 @@ struct Grads {
   const void *dz, *dn;
   void *dx, *dy, *dgate;
   long long ld_dz, ld_dn, ld_dx, ld_dy, ld_dgate;
-  float* partial;  // [blocks][3][D]: dw_pre, dw_post, dgate of a gate [D]; null: none wanted
+  float* partial;  // [blocks][2][D]: sums of the blocks' rows; null: none wanted
 };
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+// V neighbouring values: 8, or 4 where the residual stream is fp32, so that 16 bytes of it follow 16
+// bytes of the next lane (8 values to a lane, in two pieces 32 bytes apart, leave half of every
+// 32-byte sector to another instruction: 8192 x 4096 forward 86 us at 4.0 TB/s).
+__device__ __forceinline__ void unpack(uint32_t w, float& a, float& b) {
+  a = __uint_as_float(w << 16), b = __uint_as_float(w & 0xffff0000u);
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 q = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+template <int V>
+__device__ __forceinline__ void load(const float* p, float (&v)[V]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  for (int i = 0; i < V; i += 4) {
+    const float4 q = reinterpret_cast<const float4*>(p)[i / 4];
+    v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
   }
 }
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-}
-__device__ __forceinline__ void weight8(const float* w, int at, float (&v)[8]) {
-  if (w)
-    load8(w + at, v);
-  else
+template <int V>
+__device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[V]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 1.f;
+  for (int i = 0; i < V; i += 4) {
+    const uint2 q = reinterpret_cast<const uint2*>(p)[i / 4];
+    unpack(q.x, v[i], v[i + 1]);
+    unpack(q.y, v[i + 2], v[i + 3]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void store(float* p, const float (&v)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += 4)
+    reinterpret_cast<float4*>(p)[i / 4] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+template <int V>
+__device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[V]) {
+  if constexpr (V == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  else
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + __expf(-v)); }
+__device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + expf(-v)); }
 
-// A row is held by WARPS warps, C pieces of 8 values to a lane: piece c of thread i has values
-// (c * 32 * WARPS + i) * 8 on.  Rows of up to 512 values take one warp.
-template <int WARPS, int C>
+// A row is held by WARPS warps, C pieces of V values to a lane: piece c of thread i has values
+// (c * 32 * WARPS + i) * V on.  Rows of up to 512 values take one warp.
+// FULL: the rows have just as many, and no piece is beyond their end.
+template <int WARPS, int C, int V, bool FULL>
 struct Lanes {
-  static constexpr int kRowThreads = WARPS * 32;
+  static constexpr int kRowThreads = WARPS * 32, kPieces = C, kValues = V;
+  static constexpr bool kFull = FULL;
   static constexpr int kThreads = kRowThreads > 256 ? kRowThreads : 256;
   static constexpr int kGroups = kThreads / kRowThreads;  // rows that a block has at once
 
@@ -79,45 +90,103 @@ struct Lanes {
 
   __device__ __forceinline__ Lanes()
       : thread(threadIdx.x % kRowThreads), group(threadIdx.x / kRowThreads) {}
-  __device__ __forceinline__ int at(int c) const { return (c * kRowThreads + thread) * 8; }
+  __device__ __forceinline__ int at(int c) const { return (c * kRowThreads + thread) * V; }
+  __device__ __forceinline__ bool in(int c, int D) const { return FULL || at(c) < D; }
 
   // Sums over the row's threads, the same in all of them.  `sums` is the group's, of the call's
   // own: three in turn are enough, as nobody is two barriers ahead.
-  __device__ __forceinline__ float2 sum(float2 v, float2* sums) const {
+  template <int N>
+  __device__ __forceinline__ void sum(float (&v)[N], float (*sums)[WARPS]) const {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      v.x += __shfl_xor_sync(~0u, v.x, o);
-      v.y += __shfl_xor_sync(~0u, v.y, o);
-    }
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(~0u, v[i], o);
     if constexpr (WARPS > 1) {
-      if (thread % 32 == 0) sums[thread / 32] = v;
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kRowThreads) : "memory");
-      v = make_float2(0.f, 0.f);
+      if (thread % 32 == 0)
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) v.x += sums[w].x, v.y += sums[w].y;
+        for (int i = 0; i < N; ++i) sums[i][thread / 32] = v[i];
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kRowThreads) : "memory");
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        v[i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) v[i] += sums[i][w];
+      }
     }
-    return v;
   }
-  __device__ __forceinline__ float sum(float v, float2* sums) const {
-    return sum(make_float2(v, 0.f), sums).x;
+  __device__ __forceinline__ float sum(float v, float (*sums)[WARPS]) const {
+    float one[1] = {v};
+    sum(one, sums);
+    return one[0];
   }
 };
 
-// a(gate) of 8 values; of a gate [N] the same for all.
-template <typename T>
-__device__ __forceinline__ void gate8(const Block& b, long long row, int at, float token,
-                                      float (&a)[8]) {
-  if (b.gate_kind == MOE_GATE_VALUE)
-    load8(static_cast<const T*>(b.gate) + row * b.ld_gate + at, a);
-  else if (b.gate_kind == MOE_GATE_CHANNEL)
-    load8(static_cast<const float*>(b.gate) + at, a);
+// Rows on their way: every thread copies the 16-byte pieces that it will read itself into places of
+// its own in shared memory, some rows ahead, so that nothing but its own wait stands between.
+// (Loaded when they were wanted, 2 blocks of 256 threads to an SM had too few bytes under way:
+// 16384 x 4096 bf16 169 us.)  V values of type X take V * sizeof(X) bytes of each of THREADS threads,
+// in pieces of 8 or 16 bytes; piece i of all threads follows piece i - 1 of all.
+template <int THREADS, int V, typename X>
+struct Piece {
+  static constexpr int kBytes = V * sizeof(X) < 16 ? 8 : 16, kCount = V * sizeof(X) / kBytes;
+  static constexpr int kAll = THREADS * V * sizeof(X);  // bytes of a piece of V values of all threads
+
+  static __device__ __forceinline__ void copy(uint32_t to, const X* from) {
+    to += threadIdx.x * kBytes;
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+      const X* at = from + i * (V / kCount);
+      if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * (THREADS * 16)), "l"(at)
+                     : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(at) : "memory");
+    }
+  }
+  static __device__ __forceinline__ void read(uint32_t from, float (&v)[V]) {
+    from += threadIdx.x * kBytes;
+    uint32_t w[V * sizeof(X) / 4];
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+      uint32_t(&q)[V * sizeof(X) / 4] = w;
+      if constexpr (kBytes == 16)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(q[4 * i]), "=r"(q[4 * i + 1]), "=r"(q[4 * i + 2]), "=r"(q[4 * i + 3])
+                     : "r"(from + i * (THREADS * 16))
+                     : "memory");
+      else
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q[0]), "=r"(q[1]) : "r"(from) : "memory");
+    }
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(V * sizeof(X) / 4); ++i)
+      if constexpr (sizeof(X) == 4)
+        v[i] = __uint_as_float(w[i]);
+      else
+        unpack(w[i], v[2 * i], v[2 * i + 1]);
+  }
+};
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_copies(int but) {
+  if (but == 3)
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (but == 2)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (but == 1)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
   else
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a[e] = token;
-  if (b.gate_sigmoid && b.gate_kind >= MOE_GATE_CHANNEL && b.gate_kind != MOE_GATE_TOKEN)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a[e] = sigmoid(a[e]);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
+
+// Where the pieces of a row are, in bytes: x, y, a gate [N, D], then dz and dn.
+template <typename S, typename T, typename G, int THREADS, int C, int V, bool BACKWARD>
+struct Places {
+  static constexpr int kS = Piece<THREADS, V, S>::kAll, kT = Piece<THREADS, V, T>::kAll;
+  static constexpr int kG = Piece<THREADS, V, G>::kAll;
+  static constexpr int kY = C * kS, kGate = kY + C * kT;
+  static constexpr int dz(bool gates) { return kGate + (gates ? C * kT : 0); }
+  static constexpr int dn(bool gates) { return dz(gates) + (BACKWARD ? C * kS : 0); }
+  static constexpr int all(bool gates) { return dn(gates) + (BACKWARD ? C * kG : 0); }
+};
 
 // a(gate) of a gate [N], 1 without a gate.
 __device__ __forceinline__ float token_gate(const Block& b, long long row) {
@@ -126,69 +195,187 @@ __device__ __forceinline__ float token_gate(const Block& b, long long row) {
   return b.gate_sigmoid ? sigmoid(g) : g;
 }
 
-template <typename S, typename T, int WARPS, int C>
-__global__ void __launch_bounds__(Lanes<WARPS, C>::kThreads)
-    block_norm_kernel(const Block b, void* z_, long long ld_z, void* n_, long long ld_n) {
-  using L = Lanes<WARPS, C>;
-  __shared__ float2 sums[3][L::kGroups][WARPS];
+// Rows of more than 8192 values are read where they are, again for each time that they are wanted.
+template <int WARPS>
+constexpr bool kDirect = WARPS == 32;
+
+// A row in shared memory (or, kDirect, in its matrices), as one thread sees it.
+template <typename S, typename T, typename G, int WARPS, int C, int V, bool FULL, bool BACKWARD>
+struct Row {
+  using L = Lanes<WARPS, C, V, FULL>;
+  using P = Places<S, T, G, L::kThreads, C, V, BACKWARD>;
+  uint32_t at;
+  long long r;
+  int first, gates;  // the thread's first column
+
+  __device__ __forceinline__ int col(int c) const { return first + c * (L::kRowThreads * V); }
+  template <typename X>
+  __device__ __forceinline__ void get(int place, const void* p, long long ld, int c,
+                                      float (&v)[V]) const {
+    if constexpr (kDirect<WARPS>)
+      load(static_cast<const X*>(p) + r * ld + col(c), v);
+    else
+      Piece<L::kThreads, V, X>::read(at + place + c * Piece<L::kThreads, V, X>::kAll, v);
+  }
+  template <typename X>
+  __device__ __forceinline__ void put(int place, const void* p, long long ld, int c) const {
+    Piece<L::kThreads, V, X>::copy(at + place + c * Piece<L::kThreads, V, X>::kAll,
+                                   static_cast<const X*>(p) + r * ld + col(c));
+  }
+  __device__ __forceinline__ void x(const Block& b, int c, float (&v)[V]) const {
+    get<S>(0, b.x, b.ld_x, c, v);
+  }
+  __device__ __forceinline__ void y(const Block& b, int c, float (&v)[V]) const {
+    get<T>(P::kY, b.y, b.ld_y, c, v);
+  }
+  __device__ __forceinline__ void dz(const Grads& g, int c, float (&v)[V]) const {
+    get<S>(P::dz(gates), g.dz, g.ld_dz, c, v);
+  }
+  __device__ __forceinline__ void dn(const Grads& g, int c, float (&v)[V]) const {
+    get<G>(P::dn(gates), g.dn, g.ld_dn, c, v);
+  }
+  // a(gate) of a gate [N, D].
+  __device__ __forceinline__ void gate(const Block& b, int c, float (&a)[V]) const {
+    get<T>(P::kGate, b.gate, b.ld_gate, c, a);
+    if (b.gate_sigmoid)
+#pragma unroll
+      for (int e = 0; e < V; ++e) a[e] = sigmoid(a[e]);
+  }
+  __device__ __forceinline__ void copy_block(const Block& b) const {
+    if constexpr (kDirect<WARPS>) return;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (!FULL && col(c) >= b.D) continue;
+      put<S>(0, b.x, b.ld_x, c);
+      if (b.y) put<T>(P::kY, b.y, b.ld_y, c);
+      if (gates) put<T>(P::kGate, b.gate, b.ld_gate, c);
+    }
+  }
+  __device__ __forceinline__ void copy_grads(const Block& b, const Grads& g) const {
+    if constexpr (kDirect<WARPS>) return;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (!FULL && col(c) >= b.D) continue;
+      if (g.dz) put<S>(P::dz(gates), g.dz, g.ld_dz, c);
+      if (g.dn) put<G>(P::dn(gates), g.dn, g.ld_dn, c);
+    }
+  }
+};
+
+// What the thread's columns have in all rows: scale w_post a (of a gate [D]), and w_pre.
+template <int WARPS, int C, int V, bool FULL>
+struct Columns {
+  float post[C][V], pre[C][V];
+  __device__ __forceinline__ Columns(const Block& b, const Lanes<WARPS, C, V, FULL>& me) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) post[c][e] = b.scale, pre[c][e] = 1.f;
+      if (!me.in(c, b.D)) continue;
+      float a[V];
+      if (b.w_post) times(static_cast<const float*>(b.w_post), me.at(c), post[c]);
+      if (b.gate_kind == MOE_GATE_CHANNEL) {
+        load(static_cast<const float*>(b.gate) + me.at(c), a);
+#pragma unroll
+        for (int e = 0; e < V; ++e) post[c][e] *= b.gate_sigmoid ? sigmoid(a[e]) : a[e];
+      }
+      if (b.w_pre) times(static_cast<const float*>(b.w_pre), me.at(c), pre[c]);
+    }
+  }
+  static __device__ __forceinline__ void times(const float* w, int at, float (&v)[V]) {
+    float f[V];
+    load(w + at, f);
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] *= f[e];
+  }
+};
+
+// The weights of the thread's columns stay in registers over the block's rows, and everything that
+// is one number for a row is multiplied together first: two fused products to a value of z, and one
+// product less for the norms than for weights and factors one by one (515 instructions for a warp's
+// part of a row of 4096 then).
+template <typename S, typename T, int WARPS, int C, int V, bool FULL>
+__global__ void __launch_bounds__(Lanes<WARPS, C, V, FULL>::kThreads, Lanes<WARPS, C, V, FULL>::kThreads > 256 ? 1 : 2)
+    block_norm_kernel(const Block b, void* z_, long long ld_z, void* n_, long long ld_n, int ahead) {
+  using L = Lanes<WARPS, C, V, FULL>;
+  using R = Row<S, T, T, WARPS, C, V, FULL, false>;
+  __shared__ float sums[2][L::kGroups][1][WARPS];
+  extern __shared__ __align__(16) uint8_t shared[];
   after_previous();
   const L me;
+  const int gates = b.gate_kind == MOE_GATE_VALUE;
+  const uint32_t ring = smem_u32(shared);
+  const int row_bytes = R::P::all(gates);
   const float inv_D = 1.f / b.D;
   const long long step = static_cast<long long>(gridDim.x) * L::kGroups;
-  for (long long row = static_cast<long long>(blockIdx.x) * L::kGroups + me.group; row < b.N;
-       row += step) {
-    const S* x = static_cast<const S*>(b.x) + row * b.ld_x;
-    const T* y = static_cast<const T*>(b.y) + row * b.ld_y;
-    float z[C][8], u[C][8];
+  const long long first = static_cast<long long>(blockIdx.x) * L::kGroups + me.group;
+  for (int i = 0; i < ahead; ++i) {
+    if (first + i * step < b.N) {
+      const R row{ring + i * row_bytes, first + i * step, me.at(0), gates};
+      row.copy_block(b);
+    }
+    commit_copies();
+  }
+  const Columns<WARPS, C, V, FULL> columns(b, me);
+  int now = 0, next = ahead;
+  for (long long r = first; r < b.N; r += step) {
+    if (r + ahead * step < b.N) {
+      const R coming{ring + next * row_bytes, r + ahead * step, me.at(0), gates};
+      coming.copy_block(b);
+    }
+    commit_copies();
+    const float token = b.y ? token_gate(b, r) : 0.f;
+    wait_for_copies(ahead);
+    const R row{ring + now * row_bytes, r, me.at(0), gates};
+    if (++now > ahead) now = 0;
+    if (++next > ahead) next = 0;
+    float z[C][V], y[C][V];
+    float s = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      if (me.at(c) < b.D) {
-        load8(x + me.at(c), z[c]);
-        if (b.y) load8(y + me.at(c), u[c]);
+      if (me.in(c, b.D)) {
+        row.x(b, c, z[c]);
+        if (b.y) {
+          row.y(b, c, y[c]);
+#pragma unroll
+          for (int e = 0; e < V; ++e) s = fmaf(y[c][e], y[c][e], s);
+        }
       }
     if (b.y) {
-      const float token = token_gate(b, row);
-      float ry = 1.f;
-      if (b.post_norm) {
-        float s = 0.f;
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-          if (me.at(c) < b.D)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s = fmaf(u[c][e], u[c][e], s);
-        ry = rsqrtf(fmaf(me.sum(s, sums[0][me.group]), inv_D, b.eps));
-      }
+      float by = token;
+      if (b.post_norm) by *= rsqrtf(fmaf(me.sum(s, sums[0][me.group]), inv_D, b.eps));
+      s = 0.f;
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        if (me.at(c) < b.D) {
-          float w[8], a[8];
-          weight8(b.post_norm ? b.w_post : nullptr, me.at(c), w);
-          gate8<T>(b, row, me.at(c), token, a);
+        if (me.in(c, b.D)) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            z[c][e] = fmaf(b.scale * a[e], w[e] * (u[c][e] * ry), z[c][e]);
+          for (int e = 0; e < V; ++e) y[c][e] *= by;
+          if (gates) {
+            float a[V];
+            row.gate(b, c, a);
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[c][e] *= a[e];
+          }
+#pragma unroll
+          for (int e = 0; e < V; ++e) z[c][e] = fmaf(columns.post[c][e], y[c][e], z[c][e]);
         }
     }
-    if (z_)
+    s = 0.f;
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (me.at(c) < b.D) store8(static_cast<S*>(z_) + row * ld_z + me.at(c), z[c]);
+    for (int c = 0; c < C; ++c)
+      if (me.in(c, b.D)) {
+        if (z_) store(static_cast<S*>(z_) + r * ld_z + me.at(c), z[c]);
+#pragma unroll
+        for (int e = 0; e < V; ++e) s = fmaf(z[c][e], z[c][e], s);
+      }
     if (n_) {
-      float s = 0.f;
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (me.at(c) < b.D)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s = fmaf(z[c][e], z[c][e], s);
       const float rz = rsqrtf(fmaf(me.sum(s, sums[1][me.group]), inv_D, b.eps));
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        if (me.at(c) < b.D) {
-          float w[8];
-          weight8(b.w_pre, me.at(c), w);
+        if (me.in(c, b.D)) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] *= z[c][e] * rz;
-          store8(static_cast<T*>(n_) + row * ld_n + me.at(c), w);
+          for (int e = 0; e < V; ++e) z[c][e] *= rz * columns.pre[c][e];
+          store(static_cast<T*>(n_) + r * ld_n + me.at(c), z[c]);
         }
     }
     // the next row's first sums go where this row's readers may still be: one more barrier's worth
@@ -197,215 +384,291 @@ __global__ void __launch_bounds__(Lanes<WARPS, C>::kThreads)
   }
 }
 
-// z is formed again.  With z^ = z / rms(z) and y^ = y / rms(y),
+// z is formed again.  With z^ = z / rms(z), y^ = y / rms(y), p = scale w_post a (of a gate [D]) and a
+// gate [N]'s a apart,
 //   dz' = dz + (w_pre dn - z^ mean(w_pre dn z^)) / rms(z) = dx
-//   t   = scale a dz',   da = scale dz' u
-//   dy  = (w_post t - y^ mean(w_post t y^)) / rms(y), or t
-// The sums over rows (of dn z^, t y^, da) stay in shared memory, each thread's values in places of
-// its own, over all rows of a block.
-template <typename S, typename T, typename G, int WARPS, int C>
-__global__ void __launch_bounds__(Lanes<WARPS, C>::kThreads)
-    block_norm_backward_kernel(const Block b, const Grads g) {
-  using L = Lanes<WARPS, C>;
-  __shared__ float2 sums[3][L::kGroups][WARPS];
-  extern __shared__ float acc[];  // [3][C][8][threads]
+//   dy  = (a p dz' - y^ mean(a p dz' y^)) / rms(y), or a p dz'
+// and with Q = sum over rows of a dz' y^, what the gradients of w_post and of a gate [D] are made of
+// (scale a Q and scale w_post a' Q), and sum(p dz' y^) the gradient of a gate [N] before a'.  The sums
+// over rows stay in registers over all rows of a block.
+template <typename S, typename T, typename G, int WARPS, int C, int V, bool FULL>
+__global__ void __launch_bounds__(Lanes<WARPS, C, V, FULL>::kThreads, Lanes<WARPS, C, V, FULL>::kThreads > 256 ? 1 : 2)
+    block_norm_backward_kernel(const Block b, const Grads g, int ahead) {
+  using L = Lanes<WARPS, C, V, FULL>;
+  using R = Row<S, T, G, WARPS, C, V, FULL, true>;
+  __shared__ float sums[3][L::kGroups][2][WARPS];
+  extern __shared__ __align__(16) uint8_t shared[];
   after_previous();
   const L me;
+  const int gates = b.gate_kind == MOE_GATE_VALUE;
+  const uint32_t ring = smem_u32(shared);
+  const int row_bytes = R::P::all(gates);
   const float inv_D = 1.f / b.D;
-  const auto place = [&](int which, int c, int e) -> float& {
-    return acc[((which * C + c) * 8 + e) * L::kThreads + threadIdx.x];
-  };
-  if (g.partial)
-    for (int i = 0; i < 3 * C * 8; ++i) acc[i * L::kThreads + threadIdx.x] = 0.f;
   const long long step = static_cast<long long>(gridDim.x) * L::kGroups;
-  for (long long row = static_cast<long long>(blockIdx.x) * L::kGroups + me.group; row < b.N;
-       row += step) {
-    const S* x = static_cast<const S*>(b.x) + row * b.ld_x;
-    const T* y = static_cast<const T*>(b.y) + row * b.ld_y;
-    const S* dz_row = static_cast<const S*>(g.dz) + row * g.ld_dz;
-    const G* dn_row = static_cast<const G*>(g.dn) + row * g.ld_dn;
-    float z[C][8], v[C][8], dz[C][8], dn[C][8];
+  const long long first = static_cast<long long>(blockIdx.x) * L::kGroups + me.group;
+  for (int i = 0; i < ahead; ++i) {
+    if (first + i * step < b.N) {
+      const R row{ring + i * row_bytes, first + i * step, me.at(0), gates};
+      row.copy_block(b);
+      row.copy_grads(b, g);
+    }
+    commit_copies();
+  }
+  const Columns<WARPS, C, V, FULL> columns(b, me);
+  float of_pre[C][V] = {}, of_post[C][V] = {};  // sums of dn z^, and Q
+  int now = 0, next = ahead;
+  for (long long r = first; r < b.N; r += step) {
+    if (r + ahead * step < b.N) {
+      const R coming{ring + next * row_bytes, r + ahead * step, me.at(0), gates};
+      coming.copy_block(b);
+      coming.copy_grads(b, g);
+    }
+    commit_copies();
+    const float token = b.y ? token_gate(b, r) : 0.f;
+    wait_for_copies(ahead);
+    const R row{ring + now * row_bytes, r, me.at(0), gates};
+    if (++now > ahead) now = 0;
+    if (++next > ahead) next = 0;
+    float ry = 1.f;
+    if (b.y && b.post_norm) {
+      float s = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (me.in(c, b.D)) {
+          float y[V];
+          row.y(b, c, y);
+#pragma unroll
+          for (int e = 0; e < V; ++e) s = fmaf(y[e], y[e], s);
+        }
+      ry = rsqrtf(fmaf(me.sum(s, sums[0][me.group]), inv_D, b.eps));
+    }
+    const float by = ry * token;
+    float z[C][V];
+    float s[2] = {0.f, 0.f};  // of z z, and of w_pre dn z
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      if (me.at(c) < b.D) {
-        load8(x + me.at(c), z[c]);
-        if (b.y) load8(y + me.at(c), v[c]);
+      if (me.in(c, b.D)) {
+        row.x(b, c, z[c]);
+        if (b.y) {
+          float y[V];
+          row.y(b, c, y);
+#pragma unroll
+          for (int e = 0; e < V; ++e) y[e] *= by;
+          if (gates) {
+            float a[V];
+            row.gate(b, c, a);
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e] *= a[e];
+          }
+#pragma unroll
+          for (int e = 0; e < V; ++e) z[c][e] = fmaf(columns.post[c][e], y[e], z[c][e]);
+        }
+        if (g.dn) {
+          float dn[V];
+          row.dn(g, c, dn);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            s[0] = fmaf(z[c][e], z[c][e], s[0]);
+            s[1] = fmaf(columns.pre[c][e] * dn[e], z[c][e], s[1]);
+          }
+        }
+      }
+    float rz = 0.f, m = 0.f;
+    if (g.dn) {
+      me.sum(s, sums[1][me.group]);
+      rz = rsqrtf(fmaf(s[0], inv_D, b.eps));
+      m = s[1] * inv_D * rz * rz * rz;
+    }
+    float sum = 0.f;  // of p dz' y (with a gate [N, D]'s a)
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (me.in(c, b.D)) {
+        float dz[V];
         if (g.dz) {
-          load8(dz_row + me.at(c), dz[c]);
+          row.dz(g, c, dz);
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dz[c][e] = 0.f;
+          for (int e = 0; e < V; ++e) dz[e] = 0.f;
         }
-        if (g.dn) load8(dn_row + me.at(c), dn[c]);
+        if (g.dn) {
+          float dn[V];
+          row.dn(g, c, dn);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            of_pre[c][e] = fmaf(dn[e] * rz, z[c][e], of_pre[c][e]);
+            dz[e] = fmaf(columns.pre[c][e] * dn[e], rz, fmaf(-m, z[c][e], dz[e]));
+          }
+        }
+        store(static_cast<S*>(g.dx) + r * g.ld_dx + me.at(c), dz);
+        if (!b.y) continue;
+        float y[V];
+        row.y(b, c, y);
+        if (gates) {
+          float a[V], da[V];
+          row.gate(b, c, a);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            da[e] = columns.post[c][e] * dz[e] * (y[e] * ry);
+            if (b.gate_sigmoid) da[e] *= a[e] * (1.f - a[e]);
+            dz[e] *= a[e];
+          }
+          if (g.dgate) store(static_cast<T*>(g.dgate) + r * g.ld_dgate + me.at(c), da);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          of_post[c][e] = fmaf(dz[e], y[e] * by, of_post[c][e]);
+          z[c][e] = columns.post[c][e] * dz[e];  // what dy is made of
+          sum = fmaf(z[c][e], y[e], sum);
+        }
       }
-    const float token = b.y ? token_gate(b, row) : 0.f;
-    float ry = 1.f;
     if (b.y) {
-      if (b.post_norm) {
-        float s = 0.f;
+      sum = me.sum(sum, sums[2][me.group]);
+      if (b.gate_kind == MOE_GATE_TOKEN && g.dgate && me.thread == 0)
+        static_cast<float*>(g.dgate)[r] = sum * ry * (b.gate_sigmoid ? token * (1.f - token) : 1.f);
+      if (g.dy) {
+        const float my = b.post_norm ? sum * token * inv_D * ry * ry * ry : 0.f;
 #pragma unroll
         for (int c = 0; c < C; ++c)
-          if (me.at(c) < b.D)
+          if (me.in(c, b.D)) {
+            float y[V];
+            row.y(b, c, y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s = fmaf(v[c][e], v[c][e], s);
-        ry = rsqrtf(fmaf(me.sum(s, sums[0][me.group]), inv_D, b.eps));
-      }
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (me.at(c) < b.D) {
-          float w[8], a[8];
-          weight8(b.post_norm ? b.w_post : nullptr, me.at(c), w);
-          gate8<T>(b, row, me.at(c), token, a);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            z[c][e] = fmaf(b.scale * a[e], w[e] * (v[c][e] * ry), z[c][e]);
-        }
-    }
-    if (g.dn) {
-      float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (me.at(c) < b.D) {
-          float w[8];
-          weight8(b.w_pre, me.at(c), w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            s.x = fmaf(z[c][e], z[c][e], s.x);
-            s.y = fmaf(w[e] * dn[c][e], z[c][e], s.y);
+            for (int e = 0; e < V; ++e) z[c][e] = fmaf(by, z[c][e], -my * y[e]);
+            store(static_cast<T*>(g.dy) + r * g.ld_dy + me.at(c), z[c]);
           }
-        }
-      s = me.sum(s, sums[1][me.group]);
-      const float rz = rsqrtf(fmaf(s.x, inv_D, b.eps));
-      const float m = s.y * inv_D * rz * rz;
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (me.at(c) < b.D) {
-          float w[8];
-          weight8(b.w_pre, me.at(c), w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (g.partial) place(0, c, e) += dn[c][e] * (z[c][e] * rz);
-            dz[c][e] += rz * fmaf(-m, z[c][e], w[e] * dn[c][e]);
-          }
-        }
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (me.at(c) < b.D) store8(static_cast<S*>(g.dx) + row * g.ld_dx + me.at(c), dz[c]);
-    if (!b.y) {
-      if (WARPS > 1 && g.dn)
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + me.group), "n"(L::kRowThreads) : "memory");
-      continue;
-    }
-    float2 s = make_float2(0.f, 0.f);  // of w_post t y, and of dz' u
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (me.at(c) < b.D) {
-        float w[8], a[8], da[8];
-        weight8(b.post_norm ? b.w_post : nullptr, me.at(c), w);
-        gate8<T>(b, row, me.at(c), token, a);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float d = b.scale * dz[c][e], u = w[e] * (v[c][e] * ry);
-          da[e] = d * u;
-          s.y += da[e];
-          const float t = d * a[e];
-          s.x = fmaf(t * w[e], v[c][e], s.x);
-          if (g.partial) place(1, c, e) += t * (v[c][e] * ry);
-          dz[c][e] = t * w[e];
-          if (b.gate_sigmoid) da[e] *= a[e] * (1.f - a[e]);
-          if (g.partial && b.gate_kind == MOE_GATE_CHANNEL) place(2, c, e) += da[e];
-        }
-        if (b.gate_kind == MOE_GATE_VALUE && g.dgate)
-          store8(static_cast<T*>(g.dgate) + row * g.ld_dgate + me.at(c), da);
       }
-    s = me.sum(s, sums[2][me.group]);
-    if (b.gate_kind == MOE_GATE_TOKEN && g.dgate && me.thread == 0)
-      static_cast<float*>(g.dgate)[row] = s.y * (b.gate_sigmoid ? token * (1.f - token) : 1.f);
-    if (g.dy) {
-      const float m = b.post_norm ? s.x * inv_D * ry * ry : 0.f;
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (me.at(c) < b.D) {
-          float d[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] = ry * fmaf(-m, v[c][e], dz[c][e]);
-          store8(static_cast<T*>(g.dy) + row * g.ld_dy + me.at(c), d);
-        }
     }
-    // without a sum before it the next row's could meet this one's readers
-    if (WARPS > 1 && !b.post_norm && !g.dn)
+    // with one sum to a row the next one's could meet this one's readers
+    if (WARPS > 1 && (!b.y || (!b.post_norm && !g.dn)))
       asm volatile("bar.sync %0, %1;" ::"r"(1 + me.group), "n"(L::kRowThreads) : "memory");
   }
   if (!g.partial) return;
+  // The row groups' sums, added in their order.
+  wait_for_copies(0);
   __syncthreads();
-  for (int i = threadIdx.x; i < 3 * b.D; i += L::kThreads) {
-    const int which = i / b.D, col = i % b.D;
-    const int piece = col / 8, c = piece / L::kRowThreads, thread = piece % L::kRowThreads;
-    float sum = 0.f;
-    for (int group = 0; group < L::kGroups; ++group)
-      sum += acc[((which * C + c) * 8 + col % 8) * L::kThreads + group * L::kRowThreads + thread];
-    g.partial[static_cast<long long>(blockIdx.x) * 3 * b.D + i] = sum;
+  float* all = reinterpret_cast<float*>(shared);  // [groups][values of a row's places] of one of both
+  constexpr int kValues = C * L::kRowThreads * V;
+  float* to = g.partial + static_cast<long long>(blockIdx.x) * 2 * b.D;
+  if (L::kGroups == 1) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (me.in(c, b.D)) {
+        store(to + me.at(c), of_pre[c]);
+        store(to + b.D + me.at(c), of_post[c]);
+      }
+    return;
+  }
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      store(all + me.group * kValues + me.at(c), which ? of_post[c] : of_pre[c]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < b.D; i += L::kThreads) {
+      float sum = 0.f;
+#pragma unroll
+      for (int group = 0; group < L::kGroups; ++group) sum += all[group * kValues + i];
+      to[which * b.D + i] = sum;
+    }
+    __syncthreads();
   }
 }
 
-// The blocks' sums added: 32 columns to a block, whose 32 warps take every 32nd of the rows each and
-// are then added in order.
+// The blocks' sums added, 64 columns to a block, whose 32 warps take every 32nd of the rows each and
+// are then added in order; y = 1: Q, of which the gradients of w_post and of a gate [D] are made.
 __global__ void __launch_bounds__(1024)
-    block_norm_sums_kernel(const float* partial, int blocks, int D, float* out0, float* out1,
-                           float* out2) {
-  __shared__ float sums[32][33];
+    block_norm_sums_kernel(const Block b, const float* partial, int blocks, float* dw_pre,
+                           float* dw_post, float* dgate) {
+  __shared__ float2 sums[32][32];
   after_previous();
-  float* out = blockIdx.y == 0 ? out0 : blockIdx.y == 1 ? out1 : out2;
-  if (!out) return;
+  if (blockIdx.y == 0 ? !dw_pre : !dw_post && !dgate) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + lane;
-  float sum = 0.f;
-  if (col < D)
-#pragma unroll 4
-    for (int r = warp; r < blocks; r += 32)
-      sum += partial[(static_cast<long long>(r) * 3 + blockIdx.y) * D + col];
+  const int col = blockIdx.x * 64 + lane * 2;
+  float2 sum = make_float2(0.f, 0.f);
+  if (col < b.D)
+#pragma unroll 5
+    for (int r = warp; r < blocks; r += 32) {
+      const float2 v = *reinterpret_cast<const float2*>(
+          partial + (static_cast<long long>(r) * 2 + blockIdx.y) * b.D + col);
+      sum.x += v.x, sum.y += v.y;
+    }
   sums[warp][lane] = sum;
   __syncthreads();
-  if (warp) return;
+  if (warp || col >= b.D) return;
 #pragma unroll
-  for (int w = 1; w < 32; ++w) sum += sums[w][lane];
-  if (col < D) out[col] = sum;
+  for (int w = 1; w < 32; ++w) sum.x += sums[w][lane].x, sum.y += sums[w][lane].y;
+  const float q[2] = {sum.x, sum.y};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (blockIdx.y == 0) {
+      dw_pre[col + i] = q[i];
+      continue;
+    }
+    float a = 1.f, da = 1.f;
+    if (b.gate_kind == MOE_GATE_CHANNEL) {
+      a = static_cast<const float*>(b.gate)[col + i];
+      if (b.gate_sigmoid) a = sigmoid(a), da = a * (1.f - a);
+    }
+    if (dgate) dgate[col + i] = b.scale * (b.w_post ? b.w_post[col + i] : 1.f) * da * q[i];
+    if (dw_post) dw_post[col + i] = b.scale * a * q[i];
+  }
 }
 
 // ------------------------------------------------------------------------ host side
 
-// Calls f(WARPS, C) for the warps of a row and the pieces of a lane.
-template <typename F>
+template <typename P>
+using LanesOf = std::remove_pointer_t<typename P::value_type>;
+
+// Calls f(a Lanes) for rows of D values, V to a piece.
+template <int V, typename F>
 auto with_lanes(int D, F f) {
-  using std::integral_constant;
-  if (D <= 256) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-  if (D <= 512) return f(integral_constant<int, 1>{}, integral_constant<int, 2>{});
-  if (D <= 1024) return f(integral_constant<int, 2>{}, integral_constant<int, 2>{});
-  if (D <= 2048) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
-  if (D <= 4096) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
-  if (D <= 8192) return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
-  return f(integral_constant<int, 32>{}, integral_constant<int, 2>{});
+  const auto with = [&](auto warps, auto eights) {
+    constexpr int W = decltype(warps)::value, E = decltype(eights)::value;
+    return D == W * 32 * E * 8 ? f(std::integral_constant<Lanes<W, E * 8 / V, V, true>*, nullptr>{})
+                               : f(std::integral_constant<Lanes<W, E * 8 / V, V, false>*, nullptr>{});
+  };
+  const std::integral_constant<int, 1> one;
+  const std::integral_constant<int, 2> two;
+  if (D <= 256) return with(one, one);
+  if (D <= 512) return with(one, two);
+  if (D <= 1024) return with(two, two);
+  if (D <= 2048) return with(std::integral_constant<int, 4>{}, two);
+  if (D <= 4096) return with(std::integral_constant<int, 8>{}, two);
+  if (D <= 8192) return with(std::integral_constant<int, 16>{}, two);
+  return with(std::integral_constant<int, 32>{}, two);
 }
 
 // Blocks of a launch: the rows in turn over what the GPU holds at once.
-template <int WARPS, int C>
-int blocks_of(int N, int threads_per_sm) {
-  using L = Lanes<WARPS, C>;
-  const long long most = static_cast<long long>(kSms) * std::max(1, threads_per_sm / L::kThreads);
-  return static_cast<int>(std::min<long long>(most, (N + L::kGroups - 1ll) / L::kGroups));
+int blocks_of(int N, int groups, int per_sm) {
+  return static_cast<int>(std::min<long long>(static_cast<long long>(kSms) * per_sm, (N + groups - 1ll) / groups));
 }
 
-constexpr int kForwardThreads = 1024, kBackwardThreads = 512;  // to an SM
+constexpr int kSharedPerSm = 228 * 1024;
 
+// Rows under way beside the one at work, and the shared memory of a block for them.
+struct Ahead {
+  int rows, bytes;
+};
+// At most `most`, and so many that `blocks` of them fit an SM, or one if not even two rows do.
+template <int WARPS>
+Ahead ahead_of(int row_bytes, int most, int blocks) {
+  if (kDirect<WARPS>) return {0, 0};
+  int rows = most;
+  while (rows > 1 && (row_bytes * (rows + 1) + 2048) * blocks > kSharedPerSm) --rows;
+  while (rows && row_bytes * (rows + 1) > 224 * 1024) --rows;
+  return {rows, row_bytes * (rows + 1)};
+}
+
+// (The backward's blocks write partial sums, so their number is the same for all types.)
 int backward_blocks(int N, int D) {
-  return with_lanes(D, [&](auto warps, auto c) {
-    return blocks_of<decltype(warps)::value, decltype(c)::value>(N, kBackwardThreads);
+  return with_lanes<8>(D, [&](auto lanes) {
+    using L = LanesOf<decltype(lanes)>;
+    return blocks_of(N, L::kGroups, L::kThreads > 256 ? 1 : 2);
   });
 }
 
 size_t backward_ws(int N, int D) {
-  return up256(static_cast<size_t>(backward_blocks(N, D)) * 3 * D * 4);
+  return up256(static_cast<size_t>(backward_blocks(N, D)) * 2 * D * 4);
 }
 
 bool finite(float v) { return v == v && fabsf(v) <= 3.4028235e38f; }
@@ -487,11 +750,21 @@ int moe_block_norm(const moe_block_in* in, void* z, int64_t ld_z, void* n, int64
   mark_before(MOE_KERNEL_BLOCK_NORM, stream);
   cudaError_t err = cudaSuccess;
   with_types(in->stream_dtype, in->dtype, [&](auto s, auto t) {
-    with_lanes(b.D, [&](auto warps, auto c) {
-      constexpr int W = decltype(warps)::value, C = decltype(c)::value;
-      err = launch_behind(block_norm_kernel<decltype(s), decltype(t), W, C>,
-                          blocks_of<W, C>(b.N, kForwardThreads), Lanes<W, C>::kThreads, 0, stream,
-                          b, z, lz, n, ln);
+    using S = decltype(s);
+    using T = decltype(t);
+    with_lanes<sizeof(S) == 4 ? 4 : 8>(b.D, [&](auto lanes) {
+      using L = LanesOf<decltype(lanes)>;
+      constexpr int W = L::kRowThreads / 32, C = L::kPieces, V = L::kValues, threads = L::kThreads;
+      constexpr bool FULL = L::kFull;
+      const Ahead ahead = ahead_of<W>(
+          Places<S, T, T, threads, C, V, false>::all(b.gate_kind == MOE_GATE_VALUE), 3,
+          threads > 256 ? 1 : 2);
+      const int blocks = threads > 256 ? 1 : std::max(1, std::min(2, kSharedPerSm / (ahead.bytes + 2048)));
+      err = launched(cudaFuncSetAttribute(block_norm_kernel<S, T, W, C, V, FULL>,
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize, ahead.bytes));
+      if (err == cudaSuccess)
+        err = launch_behind(block_norm_kernel<S, T, W, C, V, FULL>, blocks_of(b.N, L::kGroups, blocks), threads,
+                            ahead.bytes, stream, b, z, lz, n, ln, ahead.rows);
     });
   });
   mark_after(MOE_KERNEL_BLOCK_NORM, stream);
@@ -536,25 +809,29 @@ int moe_block_norm_backward(const moe_block_in* in, const moe_block_grads* grads
   mark_before(MOE_KERNEL_BLOCK_NORM_BWD, stream);
   cudaError_t err = cudaSuccess;
   with_types(in->stream_dtype, in->dtype, [&](auto s, auto t) {
-    with_lanes(b.D, [&](auto warps, auto c) {
-      constexpr int W = decltype(warps)::value, C = decltype(c)::value;
-      using S = decltype(s);
-      using T = decltype(t);
-      const int threads = Lanes<W, C>::kThreads, smem = partial ? 3 * C * 8 * threads * 4 : 0;
-      const auto launch = [&](auto kernel) {
-        err = launched(cudaFuncSetAttribute(
-            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * C * 8 * threads * 4));
-        if (err == cudaSuccess) err = launch_behind(kernel, blocks, threads, smem, stream, b, g);
+    using S = decltype(s);
+    using T = decltype(t);
+    with_lanes<sizeof(S) == 4 ? 4 : 8>(b.D, [&](auto lanes) {
+      using L = LanesOf<decltype(lanes)>;
+      constexpr int W = L::kRowThreads / 32, C = L::kPieces, V = L::kValues, threads = L::kThreads;
+      constexpr bool FULL = L::kFull;
+      const auto launch = [&](auto kernel, auto dn) {
+        using P = Places<S, T, decltype(dn), threads, C, V, true>;
+        const Ahead ahead = ahead_of<W>(P::all(b.gate_kind == MOE_GATE_VALUE), 3, threads > 256 ? 1 : 2);
+        err = launched(
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ahead.bytes));
+        if (err == cudaSuccess)
+          err = launch_behind(kernel, blocks, threads, ahead.bytes, stream, b, g, ahead.rows);
       };
       if (std::is_same<T, float>::value || r->dn_dtype == MOE_F32)
-        launch(block_norm_backward_kernel<S, T, float, W, C>);
+        launch(block_norm_backward_kernel<S, T, float, W, C, V, FULL>, float{});
       else
-        launch(block_norm_backward_kernel<S, T, T, W, C>);
+        launch(block_norm_backward_kernel<S, T, T, W, C, V, FULL>, T{});
     });
   });
   if (partial && err == cudaSuccess)
-    err = launch_behind(block_norm_sums_kernel, dim3((b.D + 31) / 32, 3), 1024, 0, stream,
-                        g.partial, blocks, b.D, r->dw_pre, r->dw_post,
+    err = launch_behind(block_norm_sums_kernel, dim3((b.D + 63) / 64, 2), 1024, 0, stream, b, g.partial,
+                        blocks, r->dw_pre, r->dw_post,
                         channel ? static_cast<float*>(r->dgate) : nullptr);
   mark_after(MOE_KERNEL_BLOCK_NORM_BWD, stream);
   count_launches(partial ? 2 : 1);
