@@ -5,9 +5,9 @@
 // run on the tensor cores with 16 weight rows against 8 tokens, 16 columns at a time, fp16 operands and
 // fp32 sums: a code 0 .. 15 in the lowest bits of a half-word IS the fp16 value code 2^-24 (a subnormal
 // one), and in the next four bits 16 times that, so eight codes become operands by one shift and four
-// masks.  A token's values are scaled beforehand by a power of two for each 64 of them, so that fp16
-// holds what bf16 had; those that go with the 16-fold codes are divided by 16.  Zeros are taken off the
-// sums: sum s (c - z) x = s (sum c x - z sum x), the sums of x being formed once beforehand.  (Codes made
+// masks.  A token's values are scaled beforehand by a power of two (x by one for its row, h by one for
+// each 64 values), so that fp16 holds what bf16 had; those that go with the 16-fold codes are divided by
+// 16.  Zeros are taken off the sums: sum s (c - z) x = s (sum c x - z sum x), the sums of x being formed once beforehand.  (Codes made
 // 16 + code in bf16, less 16 + zero, took 71 instructions for 16 x 64 weights, where half the pipes' rate
 // holds for 40 of them.  e4m3 operands, which a code in a byte is too, are turned into others first on
 // this GPU: 108 instructions.)
@@ -140,11 +140,11 @@ __device__ __forceinline__ int block_scan(int v, int* sums) {  // exclusive, 102
 }
 
 // One block of 1024.  The first `warps` of its warps have a part of the slots each, 32 at a time.
-__device__ void group_slots(const Groups& g, int k, int chunk, int warps, int* dev_status) {
+__device__ void group_slots(const Groups& g, int k, int chunk, bool merge, int warps,
+                            int* dev_status) {
   extern __shared__ unsigned short seen[];  // [warps][E]: slots of the expert in the warp's part
   __shared__ int sums[32], start[kMaxExperts], at_chunk[kMaxExperts];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = g.E;
-  const bool merge = chunk == 8;
   const int part = (g.slots + warps * 32 - 1) / (warps * 32) * 32;
   for (int i = threadIdx.x; i < warps * E; i += 1024) seen[i] = 0;
   __syncthreads();
@@ -217,8 +217,9 @@ __device__ void group_slots(const Groups& g, int k, int chunk, int warps, int* d
 }
 
 // ---------------------------------------------------------------- the tokens' values
-// Rows of values as operands: PARTS fp16 values to each, and for every 64 columns (a tile) the factor
-// that their sum is scaled by and the sums of the values themselves.
+// Rows of values as operands: PARTS fp16 values to each, and for every 64 columns (a tile) the sums of
+// the values themselves and the factor that the products' sums are scaled by, which x has one of for a
+// whole row.
 template <int PARTS>
 struct Rows {
   uint8_t* parts;  // [rows][PARTS][tiles][4 lanes][2 halves of a tile][8] fp16
@@ -232,40 +233,31 @@ struct Rows {
     return info + static_cast<long long>(r) * tiles;
   }
 
-  // Four neighbouring lanes (t = 0 .. 3) write a tile of a row: v[c][j] is column 32 c + 8 t + j.
-  // u = v 2^e, |u| < 2^15, divided by 16 for j = 2, 3, 6, 7, is part 0 + part 1 / 2048: fp16 has 11
-  // bits, so one part is off by at most 2^-12 of it (bf16 values not at all) and two by 2^-24; and the
-  // small ones, whose bits end at 2^-24, by 2^-25 or 2^-36 in that scale, 2^-35 or 2^-46 of the tile's
-  // largest.  Where that is not finite the factor is NaN, and so becomes all that the row's products
-  // give.
-  __device__ __forceinline__ void write(int r, int tile, const float (&v)[2][8]) const {
+  // Four neighbouring lanes (t = 0 .. 3) write a tile of a row: v[c][j] is column 32 c + 8 t + j, and
+  // `most` the largest of what shares the factor.  u = v 2^e, |u| < 2^15, divided by 16 for j = 2, 3, 6,
+  // 7, is part 0 + part 1 / 2048: fp16 has 11 bits, so one part is off by at most 2^-12 of it (bf16
+  // values not at all) and two by 2^-24; and the small ones, whose bits end at 2^-24, by 2^-25 or 2^-36
+  // in that scale, 2^-35 or 2^-46 of the largest.  Where that is not finite the factor is NaN, and so
+  // becomes all that it scales.
+  __device__ __forceinline__ void write(int r, int tile, const float (&v)[2][8], float most,
+                                        bool whole_row) const {
     const int t = threadIdx.x & 3;
-    float most = 0.f, sum[2];
-    bool finite = true;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      sum[c] = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        most = fmaxf(most, fabsf(v[c][j]));
-        finite &= fabsf(v[c][j]) <= 3.4028235e38f;
-        sum[c] += v[c][j];
-      }
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o *= 2) {
-      most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
-      finite &= __shfl_xor_sync(~0u, static_cast<int>(finite), o) != 0;
-      sum[0] += __shfl_xor_sync(~0u, sum[0], o);
-      sum[1] += __shfl_xor_sync(~0u, sum[1], o);
-    }
     const int exponent = max((__float_as_int(most) >> 23) - 127, -120);  // of the largest
-    uint8_t* to = parts + (static_cast<long long>(r) * PARTS * tiles + tile) * (kTile * 2) + t * 32;
-    float left[2][8];
+    float left[2][8], sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) left[c][j] = ldexpf(v[c][j], (j & 2 ? 10 : 14) - exponent);
+      for (int j = 0; j < 8; ++j) {
+        const float u = ldexpf(v[c][j], 14 - exponent);
+        sum[c] += u;
+        left[c][j] = j & 2 ? u * 0.0625f : u;
+      }
+#pragma unroll
+    for (int o = 1; o < 4; o *= 2) {
+      sum[0] += __shfl_xor_sync(~0u, sum[0], o);
+      sum[1] += __shfl_xor_sync(~0u, sum[1], o);
+    }
+    uint8_t* to = parts + (static_cast<long long>(r) * PARTS * tiles + tile) * (kTile * 2) + t * 32;
 #pragma unroll
     for (int q = 0; q < PARTS; ++q)
 #pragma unroll
@@ -281,44 +273,85 @@ struct Rows {
         *reinterpret_cast<uint4*>(to + static_cast<long long>(q) * tiles * (kTile * 2) + c * 16) =
             make_uint4(word[0], word[1], word[2], word[3]);
       }
-    if (t == 0)
-      info[static_cast<long long>(r) * tiles + tile] =
-          make_float4(finite ? ldexpf(1.f, exponent - 2) : NAN, sum[0] / 4096.f, sum[1] / 4096.f,
-                      (sum[0] + sum[1]) / 4096.f);
+    if (t == 0) {
+      const float factor = most <= 3.4028235e38f ? ldexpf(1.f, exponent - 2) : NAN;
+      // the sums are of 4096ths; a whole row's are less its factor, which the results are multiplied by
+      const int scale = whole_row ? -24 : exponent - 26;
+      const float lo = ldexpf(sum[0], scale), hi = ldexpf(sum[1], scale);
+      info[static_cast<long long>(r) * tiles + tile] = make_float4(factor, lo, hi, lo + hi);
+    }
+  }
+  // Of 16 values; infinity if one is not a number.
+  static __device__ __forceinline__ float largest(const float (&v)[2][8]) {
+    float most = 0.f;
+    bool good = true;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        most = fmaxf(most, fabsf(v[c][j]));
+        good &= v[c][j] == v[c][j];
+      }
+    return good ? most : INFINITY;
   }
 };
 
-// The tokens' values as operands, and (the last block) the slots by expert; counters set to zero.
+__device__ __forceinline__ void load16(const __nv_bfloat16* x, float (&v)[2][8]) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const uint4 q = *reinterpret_cast<const uint4*>(x + c * 32);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[c][2 * j] = __uint_as_float(w[j] << 16);
+      v[c][2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  }
+}
+
+// The tokens' values as operands, 256 threads to a row, and (the last block) the slots by expert;
+// counters set to zero, and with them a row of h's operands that is all zeros, for tokens that a chunk
+// has not.
 __global__ void __launch_bounds__(1024)
-    w4_prepare_kernel(const __nv_bfloat16* x, int T, Rows<kXParts> rows, int* counters, int n_counters,
-                      const Groups g, int k, int chunk, int warps, int* dev_status) {
+    w4_prepare_kernel(const __nv_bfloat16* x, int T, Rows<kXParts> rows, Rows<kHParts> h, int zero_row,
+                      int* counters, int n_counters, const Groups g, int k, int chunk, bool merge,
+                      int warps, int* dev_status) {
+  __shared__ float largest[4][8];
   after_previous();
+  let_next_start();  // (which waits for this kernel's end before it reads what is written here)
   const int blocks = g.single ? gridDim.x : gridDim.x - 1;
   if (blockIdx.x == blocks) {
-    group_slots(g, k, chunk, warps, dev_status);
+    group_slots(g, k, chunk, merge, warps, dev_status);
     return;
   }
-  const long long step = static_cast<long long>(blocks) * 1024;
-  const long long me = blockIdx.x * 1024ll + threadIdx.x;
-  for (long long i = me; i < n_counters; i += step) counters[i] = 0;
-  if (g.single && me < g.slots && !g.good(static_cast<int>(me)))
-    report_status(dev_status, MOE_ERR_BAD_INDEX);
-  const long long all = static_cast<long long>(T) * rows.tiles;
-  for (long long i = me / 4; i - threadIdx.x % 32 / 4 < all; i += step / 4) {  // whole warps
-    const long long at = min(i, all - 1);  // (again the last one: the same values)
-    const int t = threadIdx.x & 3;
-    float v[2][8];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const uint4 q = *reinterpret_cast<const uint4*>(x + at * kTile + c * 32 + t * 8);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[c][2 * j] = __uint_as_float(w[j] << 16);
-        v[c][2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      }
+  const int me = blockIdx.x * 1024 + threadIdx.x, all = blocks * 1024;
+  for (int i = me; i < n_counters; i += all) counters[i] = 0;
+  uint4* zeros = reinterpret_cast<uint4*>(const_cast<uint8_t*>(h.row(zero_row)));
+  for (int i = me; i < h.tiles * (kHParts * kTile * 2 / 16); i += all) zeros[i] = make_uint4(0, 0, 0, 0);
+  float4* infos = const_cast<float4*>(h.info_row(zero_row));
+  for (int i = me; i < h.tiles; i += all) infos[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (g.single && me < g.slots && !g.good(me)) report_status(dev_status, MOE_ERR_BAD_INDEX);
+  const int team = threadIdx.x / 256, lane = threadIdx.x % 256;
+  for (int r = blockIdx.x * 4 + team; r < T; r += blocks * 4) {
+    const __nv_bfloat16* from = x + static_cast<long long>(r) * rows.tiles * kTile + lane % 4 * 8;
+    float v[2][8], most = 0.f;
+    for (int tile = lane / 4; tile < rows.tiles; tile += 64) {
+      load16(from + tile * kTile, v);
+      most = fmaxf(most, Rows<kXParts>::largest(v));
     }
-    rows.write(static_cast<int>(at / rows.tiles), static_cast<int>(at % rows.tiles), v);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+    if (lane % 32 == 0) largest[team][lane / 32] = most;
+    asm volatile("bar.sync %0, 256;" ::"r"(1 + team) : "memory");
+#pragma unroll
+    for (int w = 0; w < 8; ++w) most = fmaxf(most, largest[team][w]);
+    asm volatile("bar.sync %0, 256;" ::"r"(1 + team) : "memory");
+    // whole warps: lanes behind the row's end write its last tile again
+    for (int tile = lane / 4; tile - lane % 32 / 4 < rows.tiles; tile += 64) {
+      const int at = min(tile, rows.tiles - 1);
+      load16(from + at * kTile, v);
+      rows.write(r, at, v, most, true);
+    }
   }
 }
 
@@ -395,33 +428,34 @@ struct Tasks {
   }
 };
 
-constexpr int kPieceTiles = 4;
-
-// MATS matrices, NT x 8 tokens at most, whose values come in PARTS to add; ZEROS: zeros are given;
-// FINE: two groups of 32 columns to a tile.
-template <int MATS, int NT, int PARTS, bool ZEROS, bool FINE>
+// MATS matrices, NT x 8 tokens at most; ZEROS: zeros are given; GROUP columns to a scale.  Gate and up
+// (MATS 2) take x, whose rows have one factor, down takes h, which has one for each tile.
+template <int MATS, int NT, bool ZEROS, int GROUP>
 struct Product {
-  static constexpr int kPlaces = MATS == 2 ? (NT == 1 ? 3 : 2) : 4;  // of the ring; one less on their way
-  static constexpr int kWords = ZEROS ? 2 : 1;       // of a group's scales, to a lane
-  static constexpr int kCodes = kPieceTiles * 512;   // bytes of a piece and matrix
-  static constexpr int kPlace = kCodes + kPieceTiles * (FINE ? 2 : 1) * 32 * kWords;
+  static constexpr bool kFactors = MATS == 1, FINE = GROUP == 32;
+  static constexpr int PARTS = MATS == 2 ? kXParts : kHParts;
+  static constexpr int kPieceTiles = MATS == 2 ? 4 : 8;
+  static constexpr int kPlaces = MATS == 2 && NT == 1 ? 3 : 2;  // of the ring; one less on their way
+  static constexpr int kWords = ZEROS ? 2 : 1;                  // of a group's scales, to a lane
+  static constexpr int kCodes = kPieceTiles * 512;              // bytes of a piece and matrix
+  static constexpr int of_scales(int tiles) { return tiles * (2048 * kWords / GROUP); }
+  static constexpr int kPlace = kCodes + of_scales(kPieceTiles);
   static constexpr int kRing = kPlaces * MATS * kPlace;
   static constexpr int kSums = MATS * NT * 4;  // to a lane
-  static constexpr int kWarpBytes = kRing + kSums * 128 + kPlaces * 8, kBytes = kWarps * kWarpBytes;
+  static constexpr int kWarpBytes = kRing + kSums * 128 + 32, kBytes = kWarps * kWarpBytes;
   static constexpr int kBlocks = 2;  // to an SM, where they fit
+  // Tiles that one scale is multiplied with at once: two where their sums can wait for it.
+  static constexpr int kTogether = GROUP == 128 && !kFactors && NT == 1 ? 2 : 1;
 
   // Issues the copies of pieces; by a warp's first lane.
   struct Copies {
     uint8_t* ring;
     uint64_t* bars;
-    int place, group_shift;
+    int place;
     uint64_t policy;
 
-    __device__ __forceinline__ Copies(const Problem<MATS>& p, uint8_t* ring_, uint64_t* bars_)
-        : ring(ring_), bars(bars_), place(0), group_shift(31 - __clz(p.w[0].group)),
-          policy(l2_policy_evict_first()) {}
-    // Bytes of the scales of n tiles.
-    __device__ __forceinline__ int of_scales(int n) const { return n * (2048 * kWords) >> group_shift; }
+    __device__ __forceinline__ Copies(uint8_t* ring_, uint64_t* bars_)
+        : ring(ring_), bars(bars_), place(0), policy(l2_policy_evict_first()) {}
     __device__ __forceinline__ void issue(const uint8_t* const (&codes)[MATS],
                                           const uint8_t* const (&scales)[MATS], int n) {
       uint8_t* to = ring + place * (MATS * kPlace);
@@ -446,7 +480,7 @@ struct Product {
 
     __device__ __forceinline__ Ahead(const Problem<MATS>& p_, uint8_t* ring_, uint64_t* bars_,
                                      const Tasks& at_, int chunks_, int first)
-        : Copies(p_, ring_, bars_), p(p_), at(at_), chunks(chunks_), tiles(p_.cols / kTile),
+        : Copies(ring_, bars_), p(p_), at(at_), chunks(chunks_), tiles(p_.cols / kTile),
           skip(first * kPieceTiles) {
       begin();
     }
@@ -458,8 +492,8 @@ struct Product {
 #pragma unroll
       for (int i = 0; i < MATS; ++i) {
         codes[i] = static_cast<const uint8_t*>(p.w[i].codes) + (strip * tiles + skip) * 512;
-        scales[i] = static_cast<const uint8_t*>(p.w[i].scales) + strip * this->of_scales(tiles) +
-                    this->of_scales(skip);
+        scales[i] = static_cast<const uint8_t*>(p.w[i].scales) + strip * of_scales(tiles) +
+                    of_scales(skip);
       }
     }
     __device__ __forceinline__ void next() {
@@ -468,7 +502,7 @@ struct Product {
       const int step = p.split * kPieceTiles;
       left -= step;
 #pragma unroll
-      for (int i = 0; i < MATS; ++i) codes[i] += step * 512, scales[i] += this->of_scales(step);
+      for (int i = 0; i < MATS; ++i) codes[i] += step * 512, scales[i] += of_scales(step);
       if (left <= 0) {
         at.next();
         begin();
@@ -495,7 +529,7 @@ struct Product {
 
     __device__ __forceinline__ AheadInStrips(const Problem<MATS>& p_, uint8_t* ring_, uint64_t* bars_,
                                              const Pieces& at_, int chunks_)
-        : Copies(p_, ring_, bars_), p(p_), start(at_), at(at_), chunks(chunks_),
+        : Copies(ring_, bars_), p(p_), start(at_), at(at_), chunks(chunks_),
           tiles(p_.cols / kTile), strip(blockIdx.x), strips(p_.rows / kStrip) {
       if (at.chunk >= chunks) strip = strips;  // more warps than pieces
       if (strip < strips) expert = p.g.expert_of(at.chunk);
@@ -508,8 +542,8 @@ struct Product {
 #pragma unroll
       for (int i = 0; i < MATS; ++i) {
         codes[i] = static_cast<const uint8_t*>(p.w[i].codes) + (of * tiles + skip) * 512;
-        scales[i] = static_cast<const uint8_t*>(p.w[i].scales) + of * this->of_scales(tiles) +
-                    this->of_scales(skip);
+        scales[i] = static_cast<const uint8_t*>(p.w[i].scales) + of * of_scales(tiles) +
+                    of_scales(skip);
       }
       this->issue(codes, scales, min(kPieceTiles, tiles - skip));
       at.next();
@@ -536,13 +570,8 @@ struct Product {
   // A tile's weights as operands, for each 16 of its columns.
   struct Operands {
     uint32_t a[4][4];
-    Scale s[FINE ? 2 : 1];
-    __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales) {
-      const int lane = threadIdx.x & 31;
-      const uint4 w = *reinterpret_cast<const uint4*>(codes + lane * 16);
-      const uint32_t* of = reinterpret_cast<const uint32_t*>(scales) + lane / 4 * kWords;
-      s[0].load(of);
-      if (FINE) s[FINE].load(of + 8 * kWords);
+    __device__ __forceinline__ void load(const uint8_t* codes) {
+      const uint4 w = *reinterpret_cast<const uint4*>(codes + (threadIdx.x & 31) * 16);
       const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // row g + i % 2 * 8, half i / 2
@@ -559,85 +588,122 @@ struct Product {
     const uint8_t* parts;
     const float4* info[2];
   };
-  // Those values, for a tile; with SOME, null rows are zero.
+  // Those values, for a tile.
   struct Values {
     uint4 v[PARTS][2];
-    float4 info[2];
-    template <bool SOME>
+    float factor[2], sum[FINE ? 2 : 1][2];
     __device__ __forceinline__ void load(const From& x, int tile, int tiles) {
 #pragma unroll
       for (int q = 0; q < PARTS; ++q)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          if (!SOME || x.parts)
-            v[q][c] = reinterpret_cast<const uint4*>(x.parts + (q * tiles + tile) * (kTile * 2))[c];
-          else
-            v[q][c] = make_uint4(0, 0, 0, 0);
+          v[q][c] = reinterpret_cast<const uint4*>(x.parts + (q * tiles + tile) * (kTile * 2))[c];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (!SOME || x.info[i])
-          info[i] = x.info[i][tile];
-        else
-          info[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < 2; ++i) {
+        const float4* info = x.info[i] + tile;
+        if (kFactors) {
+          const float4 all = *info;
+          factor[i] = all.x, sum[0][i] = FINE ? all.y : all.w;
+          if (FINE) sum[FINE][i] = all.z;
+        } else if (FINE) {
+          sum[0][i] = info->y, sum[FINE][i] = info->z;
+        } else {
+          sum[0][i] = info->w;
+        }
+      }
     }
   };
 
+  // acc += s (part - z sum), for what `part` and `sum` have of a group's columns.
+  static __device__ __forceinline__ void add(const uint8_t* scales, int group, const float (&part)[PARTS][4],
+                                             const float (&factor)[2], const float (&sum)[2],
+                                             float (&acc)[4]) {
+    Scale s;
+    s.load(reinterpret_cast<const uint32_t*>(scales + group * (32 * kWords)) +
+           (threadIdx.x & 31) / 4 * kWords);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float v = part[PARTS - 1][r];
+#pragma unroll
+      for (int q = PARTS - 2; q >= 0; --q) v = fmaf(v, 1.f / 2048.f, part[q][r]);
+      if (kFactors)
+        v = fmaf(factor[r % 2], v, -s.z[r / 2] * sum[r % 2]);
+      else
+        v = fmaf(-s.z[r / 2], sum[r % 2], v);
+      acc[r] = fmaf(s.s[r / 2], v, acc[r]);
+    }
+  }
+
+  // Tile u of a piece (`at` in `from`), the i-th of kTogether.
   static __device__ __forceinline__ void multiply(const Operands& w, const Values& x,
+                                                  const uint8_t* scales, int u, int i,
+                                                  float (&part)[PARTS][4], float (&before)[2],
                                                   float (&acc)[4]) {
-    float part[PARTS][4];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
       for (int q = 0; q < PARTS; ++q) {
-        mma(part[q], w.a[2 * c], x.v[q][c].x, x.v[q][c].y, c == 0 || FINE);
+        mma(part[q], w.a[2 * c], x.v[q][c].x, x.v[q][c].y, (c == 0 && i == 0) || FINE);
         mma(part[q], w.a[2 * c + 1], x.v[q][c].z, x.v[q][c].w, false);
       }
-      if (c == 1 || FINE) {
-        const Scale& s = w.s[FINE ? c : 0];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float4& info = x.info[r % 2];
-          const float sum = FINE ? (c ? info.z : info.y) : info.w;
-          float v = part[PARTS - 1][r];
-#pragma unroll
-          for (int q = PARTS - 2; q >= 0; --q) v = fmaf(v, 1.f / 2048.f, part[q][r]);
-          acc[r] = fmaf(s.s[r / 2], fmaf(info.x, v, -s.z[r / 2] * sum), acc[r]);
-        }
-      }
+      if (FINE) add(scales, 2 * u + c, part, x.factor, x.sum[FINE ? c : 0], acc);
     }
+    if (FINE) return;
+    const float sum[2] = {i ? before[0] + x.sum[0][0] : x.sum[0][0],
+                          i ? before[1] + x.sum[0][1] : x.sum[0][1]};
+    if (i + 1 == kTogether)
+      add(scales, GROUP == 128 ? u / 2 : u, part, x.factor, sum, acc);
+    else
+      before[0] = sum[0], before[1] = sum[1];
   }
 
-  // N tiles of a piece from its tile u0 on (u0 + at of the row's).  Of a single eight of tokens, `now`
-  // has the values of the first one, and is left with those of the tile after the last if there is
-  // `more` to come.
-  template <int N, bool SOME>
-  static __device__ __forceinline__ void tiles_of(const uint8_t* from, int at, int u0, int coarse,
+  // N tiles of a piece from its tile u0 on, which is tile `at` + u0 of the rows.  Of a single eight of
+  // tokens, `now` has the values of the first one, and is left with those of the tile after the last if
+  // there is `more` to come.
+  template <int N>
+  static __device__ __forceinline__ void tiles_of(const uint8_t* from, int at, int u0,
                                                   const From (&x)[NT], int tiles, int rows,
                                                   bool more, Values& now,
                                                   float (&acc)[MATS][NT][4]) {
+    static_assert(N % kTogether == 0, "whole groups");
+    float part[MATS][PARTS][4], before[2];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const int u = u0 + k;
       Operands w[MATS];
 #pragma unroll
-      for (int i = 0; i < MATS; ++i)
-        w[i].load(from + i * kPlace + u * 512,
-                  from + i * kPlace + kCodes + (FINE ? 2 * u : u >> coarse) * (32 * kWords));
+      for (int i = 0; i < MATS; ++i) w[i].load(from + i * kPlace + u * 512);
       if (NT == 1) {
         const Values mine = now;
-        if (k + 1 < N || more) now.template load<SOME>(x[0], at + u + 1, tiles);
+        if (k + 1 < N || more) now.load(x[0], at + u + 1, tiles);
 #pragma unroll
-        for (int i = 0; i < MATS; ++i) multiply(w[i], mine, acc[i][0]);
+        for (int i = 0; i < MATS; ++i) {
+          float sums[2] = {before[0], before[1]};
+          multiply(w[i], mine, from + i * kPlace + kCodes, u, k % kTogether, part[i], sums, acc[i][0]);
+          if (i + 1 == MATS) before[0] = sums[0], before[1] = sums[1];
+        }
       } else {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
           if (n * 8 < rows) {
-            now.template load<false>(x[n], at + u, tiles);
+            now.load(x[n], at + u, tiles);
 #pragma unroll
-            for (int i = 0; i < MATS; ++i) multiply(w[i], now, acc[i][n]);
+            for (int i = 0; i < MATS; ++i)
+              multiply(w[i], now, from + i * kPlace + kCodes, u, 0, part[i], before, acc[i][n]);
           }
       }
     }
+  }
+  // All tiles of a piece: `left` of the rows' from tile `at` on.
+  static __device__ __forceinline__ void piece(const uint8_t* from, int at, int left, const From (&x)[NT],
+                                               int tiles, int rows, Values& now,
+                                               float (&acc)[MATS][NT][4]) {
+    const int n = min(left, kPieceTiles);
+    int u = 0;
+    for (; u + 4 <= n; u += 4) tiles_of<4>(from, at, u, x, tiles, rows, u + 4 < n, now, acc);
+#pragma unroll 1
+    for (; u < n; u += kTogether)
+      tiles_of<kTogether>(from, at, u, x, tiles, rows, u + kTogether < n, now, acc);
   }
 
   // All of the warp's strips.  value_row(r) is the row of x of a chunk's row r; put(chunk,
@@ -658,13 +724,14 @@ struct Product {
       fence_barrier_init();
     }
     __syncwarp();
-    after_previous();
+    // a single token's experts were there before the preparing kernel began
+    if (!p.g.single || MATS == 1) after_previous();
     const int strips = p.rows / kStrip, tiles = p.cols / kTile, chunks = p.g.chunks();
-    const int coarse = p.w[0].group == 128;
     Tasks task(blockIdx.x * teams + team, gridDim.x * teams, strips);
     Ahead ahead(p, ring, bars, task, chunks, me);
     if (lane == 0)
       for (int i = 0; i < kPlaces - 1; ++i) ahead.next();
+    if (p.g.single && MATS == 2) after_previous();
     int place = 0;
     uint32_t parity = 0;
     bool ok = true;
@@ -683,21 +750,14 @@ struct Product {
       float acc[MATS][NT][4] = {};
       for (int at = me * kPieceTiles; at < tiles && ok; at += split * kPieceTiles) {
         Values now;
-        if (NT == 1) now.template load<false>(x[0], at, tiles);
+        if (NT == 1) now.load(x[0], at, tiles);
         if (!wait_for(bars + place, parity)) {
           ok = false;
           break;
         }
         if (lane == 0) ahead.next();
         __syncwarp();
-        const uint8_t* from = ring + place * (MATS * kPlace);
-        const int left = tiles - at;
-        if (left >= kPieceTiles)
-          tiles_of<kPieceTiles, false>(from, at, 0, coarse, x, tiles, rows, false, now, acc);
-        else
-#pragma unroll 1
-          for (int u = 0; u < left; ++u)
-            tiles_of<1, false>(from, at, u, coarse, x, tiles, rows, u + 1 < left, now, acc);
+        piece(ring + place * (MATS * kPlace), at, tiles - at, x, tiles, rows, now, acc);
         if (++place == kPlaces) place = 0, parity ^= 1;
         __syncwarp();  // the place is read before it is copied into again
       }
@@ -729,12 +789,12 @@ struct Product {
   }
 
   // All of the block's strips, for up to 8 tokens, whose columns are the same in all chunks: the sums
-  // over a token's experts stay in the products' sums.  Tokens that a chunk has not are zero there.
+  // over a token's experts stay in the products' sums.  Tokens that a chunk has not take `zero_row`.
   // put(strip, row, token, sum).
   template <typename Put>
   static __device__ __forceinline__ void run_strips(const Problem<MATS>& p,
-                                                    const Rows<PARTS>& values, uint8_t* shared,
-                                                    Put put) {
+                                                    const Rows<PARTS>& values, int zero_row,
+                                                    uint8_t* shared, Put put) {
     static_assert(MATS == 1 && NT == 1, "one matrix, 8 tokens");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
     uint8_t* ring = shared + warp * kRing;
@@ -748,7 +808,6 @@ struct Product {
     __syncwarp();
     after_previous();
     const int strips = p.rows / kStrip, tiles = p.cols / kTile, chunks = p.g.chunks();
-    const int coarse = p.w[0].group == 128;
     const Pieces start(warp, warps, (tiles + kPieceTiles - 1) / kPieceTiles);
     AheadInStrips ahead(p, ring, bars, start, chunks);
     if (lane == 0)
@@ -759,33 +818,29 @@ struct Product {
     for (int strip = blockIdx.x; strip < strips; strip += gridDim.x) {
       float acc[1][1][4] = {};
       Pieces at = start;
-      int row = at.chunk < chunks ? p.g.row_of(at.chunk, lane / 4) : -1;
+      const auto row_of = [&](int chunk) {
+        const int r = p.g.row_of(chunk, lane / 4);
+        return r < 0 ? zero_row : r;
+      };
+      int row = at.chunk < chunks ? row_of(at.chunk) : zero_row;
       while (at.chunk < chunks && ok) {
-        From x[1] = {};
-        if (row >= 0) x[0].parts = values.row(row) + lane % 4 * 32;
+        From x[1];
+        x[0].parts = values.row(row) + lane % 4 * 32;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = __shfl_sync(~0u, row, (lane % 4 * 2 + i) * 4);
-          if (r >= 0) x[0].info[i] = values.info_row(r);
-        }
+        for (int i = 0; i < 2; ++i)
+          x[0].info[i] = values.info_row(__shfl_sync(~0u, row, (lane % 4 * 2 + i) * 4));
         const int first = at.piece * kPieceTiles, left = tiles - first;
         Values now;
-        now.template load<true>(x[0], first, tiles);
+        now.load(x[0], first, tiles);
         at.next();
-        if (at.chunk < chunks) row = p.g.row_of(at.chunk, lane / 4);
+        if (at.chunk < chunks) row = row_of(at.chunk);
         if (!wait_for(bars + place, parity)) {
           ok = false;
           break;
         }
         if (lane == 0) ahead.next();
         __syncwarp();
-        const uint8_t* from = ring + place * kPlace;
-        if (left >= kPieceTiles)
-          tiles_of<kPieceTiles, true>(from, first, 0, coarse, x, tiles, 8, false, now, acc);
-        else
-#pragma unroll 1
-          for (int u = 0; u < left; ++u)
-            tiles_of<1, true>(from, first, u, coarse, x, tiles, 8, u + 1 < left, now, acc);
+        piece(ring + place * kPlace, first, left, x, tiles, 8, now, acc);
         if (++place == kPlaces) place = 0, parity ^= 1;
         __syncwarp();  // the place is read before it is copied into again
       }
@@ -826,9 +881,9 @@ struct GateUp {
 };
 
 // h goes to memory in fp32; the warp that brings the last of a tile's four strips makes operands of it.
-template <int NT, bool ZEROS, bool FINE>
-__global__ void __launch_bounds__(kWarps * 32, Product<2, NT, kXParts, ZEROS, FINE>::kBlocks) w4_gateup_kernel(const GateUp a) {
-  using Of = Product<2, NT, kXParts, ZEROS, FINE>;
+template <int NT, bool ZEROS, int GROUP>
+__global__ void __launch_bounds__(kWarps * 32, Product<2, NT, ZEROS, GROUP>::kBlocks) w4_gateup_kernel(const GateUp a) {
+  using Of = Product<2, NT, ZEROS, GROUP>;
   extern __shared__ __align__(16) uint8_t shared[];
   const int F = a.p.rows, lane = threadIdx.x & 31;
   Of::run(
@@ -840,8 +895,10 @@ __global__ void __launch_bounds__(kWarps * 32, Product<2, NT, kXParts, ZEROS, FI
           for (int r = 0; r < 4; ++r) {
             const int token = n * 8 + lane % 4 * 2 + r % 2;
             if (token >= rows) continue;
-            const float v = acc[0][n][r];
-            const float h = a.p.g.gate_of(first + token) * (v / (1.f + expf(-v)) * acc[1][n][r]);
+            // (a factor of the whole row of x)
+            const float f = a.x.info_row(a.p.g.slot_of(first + token) / a.k)->x;
+            const float v = f * acc[0][n][r];
+            const float h = a.p.g.gate_of(first + token) * (v / (1.f + expf(-v)) * (f * acc[1][n][r]));
             __stcg(a.h + (first + token) * static_cast<long long>(F) + strip * kStrip + lane / 4 +
                        r / 2 * 8, h);
           }
@@ -863,7 +920,10 @@ __global__ void __launch_bounds__(kWarps * 32, Product<2, NT, kXParts, ZEROS, FI
                   a.h + r * static_cast<long long>(F) + tile * kTile + c * 32 + lane % 4 * 8 + j));
               v[c][j] = q.x, v[c][j + 1] = q.y, v[c][j + 2] = q.z, v[c][j + 3] = q.w;
             }
-          a.parts.write(r, tile, v);
+          float most = Rows<kHParts>::largest(v);
+          most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
+          most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
+          a.parts.write(r, tile, v, most, false);
         }
       });
 }
@@ -873,32 +933,32 @@ struct Down {
   Rows<kHParts> h;
   float* out;  // [slots][d], a row to a slot
   __nv_bfloat16* y;
-  int T;
+  int T, zero_row;
 };
 
 // Up to 8 tokens: y at once.
-template <bool ZEROS, bool FINE>
+template <bool ZEROS, int GROUP>
 __global__ void __launch_bounds__(kMaxWarps * 32) w4_down_kernel(const Down a) {
-  using Of = Product<1, 1, kHParts, ZEROS, FINE>;
+  using Of = Product<1, 1, ZEROS, GROUP>;
   extern __shared__ __align__(16) uint8_t shared[];
   const int d = a.p.rows;
-  Of::run_strips(a.p, a.h, shared, [&](int strip, int row, int token, float sum) {
+  Of::run_strips(a.p, a.h, a.zero_row, shared, [&](int strip, int row, int token, float sum) {
     if (token < a.T)
       a.y[static_cast<long long>(token) * d + strip * kStrip + row] = __float2bfloat16_rn(sum);
   });
 }
 
 // More tokens: the rows' parts of it, which w4_combine_kernel adds.
-template <bool ZEROS, bool FINE>
-__global__ void __launch_bounds__(kWarps * 32, Product<1, 4, kHParts, ZEROS, FINE>::kBlocks)
+template <int NT, bool ZEROS, int GROUP>
+__global__ void __launch_bounds__(kWarps * 32, Product<1, NT, ZEROS, GROUP>::kBlocks)
     w4_down_rows_kernel(const Down a) {
-  using Of = Product<1, 4, kHParts, ZEROS, FINE>;
+  using Of = Product<1, NT, ZEROS, GROUP>;
   extern __shared__ __align__(16) uint8_t shared[];
   const int d = a.p.rows, lane = threadIdx.x & 31;
   Of::run(a.p, a.h, shared, [&](int r) { return r; },
-          [&](int, int first, int rows, int strip, const float (&acc)[1][4][4]) {
+          [&](int, int first, int rows, int strip, const float (&acc)[1][NT][4]) {
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 const int token = n * 8 + lane % 4 * 2 + r % 2;
@@ -940,7 +1000,11 @@ __global__ void __launch_bounds__(128)
 
 constexpr int kSms = 152;
 // Rows of an expert that its weights are read once for; more of them are taken in several chunks.
-int chunk_of(int T) { return T <= 8 ? 8 : 32; }
+// (8 to a product where experts have few rows: more would be empty columns, whose values cost registers
+// and loads: 64 tokens x 16 of 896 experts, 4096 x 1024, take 590 us in chunks of 8, 965 us of 32.)
+int chunk_of(const moe_problem* p) {
+  return p->T <= 8 || static_cast<long long>(p->T) * p->k <= 4ll * p->E ? 8 : 32;
+}
 
 constexpr int kSharedPerSm = 228 * 1024;
 
@@ -969,7 +1033,7 @@ struct Workspace {
 };
 
 Workspace carve(const moe_problem* p, void* base) {
-  const size_t slots = static_cast<size_t>(p->T) * p->k, chunk = chunk_of(p->T);
+  const size_t slots = static_cast<size_t>(p->T) * p->k, chunk = chunk_of(p);
   const size_t chunks = std::min<size_t>(p->E, slots) + slots / chunk;
   Workspace w{};
   uint8_t* at = static_cast<uint8_t*>(base);
@@ -985,17 +1049,17 @@ Workspace carve(const moe_problem* p, void* base) {
   w.g.row_slot = reinterpret_cast<int*>(take(slots * 4));
   w.g.row_gate = reinterpret_cast<float*>(take(slots * 4));
   w.g.slot_row = reinterpret_cast<int*>(take(slots * 4));
-  w.g.row_of_token = reinterpret_cast<int*>(take(chunk == 8 ? chunks * 32 : 0));
+  w.g.row_of_token = reinterpret_cast<int*>(take(p->T <= 8 ? chunks * 32 : 0));
   const size_t x_tiles = p->d / kTile, h_tiles = p->F / kTile;
   w.x.tiles = p->d / kTile, w.parts.tiles = p->F / kTile;
   w.x.parts = take(p->T * x_tiles * (kXParts * kTile * 2));
   w.x.info = reinterpret_cast<float4*>(take(p->T * x_tiles * 16));
-  w.parts.parts = take(slots * h_tiles * (kHParts * kTile * 2));
-  w.parts.info = reinterpret_cast<float4*>(take(slots * h_tiles * 16));
+  w.parts.parts = take((slots + 1) * h_tiles * (kHParts * kTile * 2));
+  w.parts.info = reinterpret_cast<float4*>(take((slots + 1) * h_tiles * 16));
   w.n_counters = static_cast<int>((p->T == 1 ? slots : chunks) * h_tiles);
   w.counters = reinterpret_cast<int*>(take(w.n_counters * 4));
   w.h = reinterpret_cast<float*>(take(slots * p->F * 4));
-  w.out = reinterpret_cast<float*>(take(chunk == 8 ? 0 : slots * p->d * 4));
+  w.out = reinterpret_cast<float*>(take(p->T <= 8 ? 0 : slots * p->d * 4));
   return w;
 }
 
@@ -1070,15 +1134,16 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
   if (!workspace || workspace_bytes < carve(p, nullptr).bytes) return MOE_ERR_WORKSPACE;
   if (misaligned(workspace, 16)) return MOE_ERR_UNSUPPORTED;
   const Workspace ws = carve(p, workspace);
-  const int slots = p->T * p->k, chunk = chunk_of(p->T);
+  const int slots = p->T * p->k, chunk = chunk_of(p);
   const auto of = [](const moe_w4* w) { return Weights{w->codes, w->scales, w->group}; };
   Groups g = ws.g;
   g.idx = topk_idx, g.gate = topk_gate, g.slots = slots, g.E = p->E, g.single = p->T == 1;
   const int chunks = std::min(p->E, slots);
+  const bool few = p->T <= 8;
   GateUp up{{g, {of(w_gate), of(w_up)}, p->F, p->d, 1, dev_status}, ws.x, ws.h, ws.parts,
             ws.counters, p->k};
   Down down{{g, {of(w_down)}, p->d, p->F, 1, dev_status}, ws.parts, ws.out,
-            reinterpret_cast<__nv_bfloat16*>(y), p->T};
+            reinterpret_cast<__nv_bfloat16*>(y), p->T, slots};
   cudaError_t err = cudaSuccess;
   const auto launch = [&](auto kernel, int blocks, int warps, int bytes, auto& args) {
     if (err == cudaSuccess)
@@ -1089,52 +1154,57 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
     using Of = decltype(product);
     const int blocks = std::min(Of::kBlocks, kSharedPerSm / (Of::kBytes + 1024)) * kSms;
     args.p.split = split_of(chunks * static_cast<long long>(args.p.rows / kStrip),
-                            (args.p.cols / kTile + kPieceTiles - 1) / kPieceTiles, blocks * kWarps);
+                            (args.p.cols / kTile + Of::kPieceTiles - 1) / Of::kPieceTiles, blocks * kWarps);
     launch(kernel, blocks, kWarps, Of::kBytes, args);
   };
   mark_before(MOE_KERNEL_W4_GATEUP, stream);
   {
     const int warps = std::min(32, (slots + 31) / 32);
-    const long long lanes = static_cast<long long>(p->T) * ws.x.tiles * 4;
-    const int blocks = static_cast<int>(std::min<long long>((lanes + 1023) / 1024, 2 * kSms));
+    const int blocks = std::min((p->T + 3) / 4, kSms - 1);
     err = launched(cudaFuncSetAttribute(
         w4_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 32 * kMaxExperts * 2));
     if (err == cudaSuccess)
       err = launch_behind(w4_prepare_kernel, blocks + !g.single, 1024, g.single ? 0 : warps * p->E * 2,
-                          stream, reinterpret_cast<const __nv_bfloat16*>(x), p->T, ws.x, ws.counters,
-                          ws.n_counters, g, p->k, chunk, warps, dev_status);
+                          stream, reinterpret_cast<const __nv_bfloat16*>(x), p->T, ws.x, ws.parts, slots,
+                          ws.counters, ws.n_counters, g, p->k, chunk, few, warps, dev_status);
   }
-  const auto with = [&](auto z, auto f) {
-    constexpr bool Z = decltype(z)::value, FINE = decltype(f)::value;
-    const bool few = chunk == 8;
-    if (few)
-      by_strips(w4_gateup_kernel<1, Z, FINE>, Product<2, 1, kXParts, Z, FINE>{}, up);
+  const auto with = [&](auto z, auto of_group) {
+    constexpr bool Z = decltype(z)::value;
+    constexpr int GROUP = decltype(of_group)::value;
+    if (chunk == 8)
+      by_strips(w4_gateup_kernel<1, Z, GROUP>, Product<2, 1, Z, GROUP>{}, up);
     else
-      by_strips(w4_gateup_kernel<4, Z, FINE>, Product<2, 4, kXParts, Z, FINE>{}, up);
+      by_strips(w4_gateup_kernel<4, Z, GROUP>, Product<2, 4, Z, GROUP>{}, up);
     mark_after(MOE_KERNEL_W4_GATEUP, stream);
     mark_before(MOE_KERNEL_W4_DOWN, stream);
     if (few) {
-      using Of = Product<1, 1, kHParts, Z, FINE>;
+      using Of = Product<1, 1, Z, GROUP>;
       const int strips = p->d / kStrip, warps = strips > kSms ? kWarps : kMaxWarps;
-      launch(w4_down_kernel<Z, FINE>, std::min(strips, 2 * kSms * kWarps / warps), warps,
+      launch(w4_down_kernel<Z, GROUP>, std::min(strips, 2 * kSms * kWarps / warps), warps,
              warps * Of::kWarpBytes, down);
+    } else if (chunk == 8) {
+      by_strips(w4_down_rows_kernel<1, Z, GROUP>, Product<1, 1, Z, GROUP>{}, down);
     } else {
-      by_strips(w4_down_rows_kernel<Z, FINE>, Product<1, 4, kHParts, Z, FINE>{}, down);
-      if (err == cudaSuccess)
-        err = launch_behind(w4_combine_kernel, dim3(p->T, std::min(64, (p->d + 511) / 512)), 128, 0,
-                            stream, ws.g.slot_row, ws.out, p->d, p->k, down.y);
+      by_strips(w4_down_rows_kernel<4, Z, GROUP>, Product<1, 4, Z, GROUP>{}, down);
     }
+    if (!few && err == cudaSuccess)
+      err = launch_behind(w4_combine_kernel, dim3(p->T, std::min(64, (p->d + 511) / 512)), 128, 0,
+                          stream, ws.g.slot_row, ws.out, p->d, p->k, down.y);
   };
-  if (zeros && w_gate->group == 32)
-    with(std::true_type{}, std::true_type{});
-  else if (zeros)
-    with(std::true_type{}, std::false_type{});
-  else if (w_gate->group == 32)
-    with(std::false_type{}, std::true_type{});
+  const auto with_group = [&](auto z) {
+    if (w_gate->group == 32)
+      with(z, std::integral_constant<int, 32>{});
+    else if (w_gate->group == 64)
+      with(z, std::integral_constant<int, 64>{});
+    else
+      with(z, std::integral_constant<int, 128>{});
+  };
+  if (zeros)
+    with_group(std::true_type{});
   else
-    with(std::false_type{}, std::false_type{});
+    with_group(std::false_type{});
   mark_after(MOE_KERNEL_W4_DOWN, stream);
-  count_launches(3 + (chunk != 8));
+  count_launches(3 + !few);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
