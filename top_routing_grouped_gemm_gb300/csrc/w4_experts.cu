@@ -7,10 +7,15 @@
 // one), and in the next four bits 16 times that, so eight codes become operands by one shift and four
 // masks.  A token's values are scaled beforehand by a power of two (x by one for its row, h by one for
 // each 64 values), so that fp16 holds what bf16 had; those that go with the 16-fold codes are divided by
-// 16.  Zeros are taken off the sums: sum s (c - z) x = s (sum c x - z sum x), the sums of x being formed once beforehand.  (Codes made
-// 16 + code in bf16, less 16 + zero, took 71 instructions for 16 x 64 weights, where half the pipes' rate
-// holds for 40 of them.  e4m3 operands, which a code in a byte is too, are turned into others first on
-// this GPU: 108 instructions.)
+// 16.  Zeros are taken off the sums: sum s (c - z) x = s (sum c x - z sum x), the sums of x being formed
+// once beforehand.  (Codes made 16 + code in bf16, less 16 + zero, took 71 instructions for 16 x 64
+// weights, where half the pipes' rate holds for 40 of them.  e4m3 operands, which a code in a byte is too,
+// are turned into others first on this GPU: 108 instructions.)
+//
+// Now it is 56 for gate and up, 82 (one token) to 90 for down, whose operand has two parts.  One token
+// through 16 of 896 experts of 4096 x 1024 takes 30 us (100 MB, 15 us of reading), 64 tokens that crowd
+// on few experts 555 us (358), 32 tokens through experts of 2048 x 512 with zeros 207 us (96): warps
+// are issuing, in turn with what they wait for, half of the time.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -222,12 +227,12 @@ __device__ void group_slots(const Groups& g, int k, int chunk, bool merge, int w
 // whole row.
 template <int PARTS>
 struct Rows {
-  uint8_t* parts;  // [rows][PARTS][tiles][4 lanes][2 halves of a tile][8] fp16
+  uint8_t* parts;  // [rows][tiles][PARTS][4 lanes][2 halves of a tile][8] fp16
   float4* info;    // [rows][tiles]: the factor; sums / 4096 over the halves and the tile
   int tiles;
 
   __device__ __forceinline__ const uint8_t* row(int r) const {
-    return parts + static_cast<long long>(r) * (PARTS * kTile * 2) * tiles;
+    return parts + static_cast<long long>(r) * (PARTS * kTile * 2 * tiles);
   }
   __device__ __forceinline__ const float4* info_row(int r) const {
     return info + static_cast<long long>(r) * tiles;
@@ -257,7 +262,7 @@ struct Rows {
       sum[0] += __shfl_xor_sync(~0u, sum[0], o);
       sum[1] += __shfl_xor_sync(~0u, sum[1], o);
     }
-    uint8_t* to = parts + (static_cast<long long>(r) * PARTS * tiles + tile) * (kTile * 2) + t * 32;
+    uint8_t* to = parts + (static_cast<long long>(r) * tiles + tile) * (PARTS * kTile * 2) + t * 32;
 #pragma unroll
     for (int q = 0; q < PARTS; ++q)
 #pragma unroll
@@ -270,7 +275,7 @@ struct Rows {
           left[c][2 * i + 1] = (left[c][2 * i + 1] - __high2float(p)) * 2048.f;
           word[i] = *reinterpret_cast<const uint32_t*>(&p);
         }
-        *reinterpret_cast<uint4*>(to + static_cast<long long>(q) * tiles * (kTile * 2) + c * 16) =
+        *reinterpret_cast<uint4*>(to + q * (kTile * 2) + c * 16) =
             make_uint4(word[0], word[1], word[2], word[3]);
       }
     if (t == 0) {
@@ -380,13 +385,31 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
     mma(d, a, b0, b1, d[0], d[1], d[2], d[3]);
 }
 
+// True for one lane of a whole warp.  (Of a lane that the compiler knows to be one, operands of a bulk
+// copy go to the uniform registers at once; `lane == 0` made a loop over the lanes of each copy.)
+__device__ __forceinline__ bool one_lane() {
+  uint32_t one;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "elect.sync _|p, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(one));
+  return one != 0;
+}
+
 // A bulk copy into shared memory; its bytes are counted at `bar`.
-__device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t bytes, uint64_t* bar,
+__device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_t bytes, uint32_t bar,
                                           uint64_t policy) {
   asm volatile(
       "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
-      "[%3], %4;" ::"r"(smem_u32(to)), "l"(from), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      "[%3], %4;" ::"r"(to), "l"(from), "r"(bytes), "r"(bar), "l"(policy)
       : "memory");
+}
+__device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
 }
 
 // Whether the barrier's phase completed, for the whole warp; gives up after kWaitTimeoutNs.
@@ -429,8 +452,10 @@ struct Tasks {
 };
 
 // MATS matrices, NT x 8 tokens at most; ZEROS: zeros are given; GROUP columns to a scale.  Gate and up
-// (MATS 2) take x, whose rows have one factor, down takes h, which has one for each tile.
-template <int MATS, int NT, bool ZEROS, int GROUP>
+// (MATS 2) take x, whose rows have one factor, down takes h, which has one for each tile.  ONE: a single
+// token, whose values come with the weights' pieces and stand in all columns.  (Read from the L2 by each
+// lane, a tile ahead, they were what down waited for.)
+template <int MATS, int NT, bool ZEROS, int GROUP, bool ONE = false>
 struct Product {
   static constexpr bool kFactors = MATS == 1, FINE = GROUP == 32;
   static constexpr int PARTS = MATS == 2 ? kXParts : kHParts;
@@ -439,7 +464,9 @@ struct Product {
   static constexpr int kWords = ZEROS ? 2 : 1;                  // of a group's scales, to a lane
   static constexpr int kCodes = kPieceTiles * 512;              // bytes of a piece and matrix
   static constexpr int of_scales(int tiles) { return tiles * (2048 * kWords / GROUP); }
-  static constexpr int kPlace = kCodes + of_scales(kPieceTiles);
+  static constexpr int kValues = kCodes + of_scales(kPieceTiles);  // where ONE's values are in a place
+  static constexpr int kInfo = kValues + kPieceTiles * (PARTS * kTile * 2);
+  static constexpr int kPlace = ONE ? kInfo + kPieceTiles * 16 : kValues;
   static constexpr int kRing = kPlaces * MATS * kPlace;
   static constexpr int kSums = MATS * NT * 4;  // to a lane
   static constexpr int kWarpBytes = kRing + kSums * 128 + 32, kBytes = kWarps * kWarpBytes;
@@ -447,24 +474,36 @@ struct Product {
   // Tiles that one scale is multiplied with at once: two where their sums can wait for it.
   static constexpr int kTogether = GROUP == 128 && !kFactors && NT == 1 ? 2 : 1;
 
-  // Issues the copies of pieces; by a warp's first lane.
+  // Issues the copies of pieces; all of a warp's lanes know where it stands, one issues them.
   struct Copies {
-    uint8_t* ring;
-    uint64_t* bars;
+    const Problem<MATS>& p;
+    uint32_t ring, bars;
     int place;
     uint64_t policy;
 
-    __device__ __forceinline__ Copies(uint8_t* ring_, uint64_t* bars_)
-        : ring(ring_), bars(bars_), place(0), policy(l2_policy_evict_first()) {}
-    __device__ __forceinline__ void issue(const uint8_t* const (&codes)[MATS],
-                                          const uint8_t* const (&scales)[MATS], int n) {
-      uint8_t* to = ring + place * (MATS * kPlace);
-      const int bytes = of_scales(n);
-      mbar_arrive_expect_tx(bars + place, MATS * (n * 512 + bytes));
+    __device__ __forceinline__ Copies(const Problem<MATS>& p_, uint8_t* ring_, uint64_t* bars_)
+        : p(p_), ring(smem_u32(ring_)), bars(smem_u32(bars_)), place(0),
+          policy(l2_policy_evict_first()) {}
+    // n tiles from `tile` on of all that a matrix has (fewer than 2^31).
+    __device__ __forceinline__ void issue(int tile, int n, const void* values = nullptr,
+                                          const void* infos = nullptr) {
+      const uint32_t to = ring + place * (MATS * kPlace), bar = bars + place * 8;
+      const uint32_t bytes = n * 512, of = of_scales(n);
+      const uint32_t parts = n * (PARTS * kTile * 2), info = n * 16;
+      if (one_lane()) {
+        expect(bar, MATS * (bytes + of) + (ONE ? parts + info : 0));
+        if (ONE) {
+          bulk_load(to + kValues, values, parts, bar, policy);
+          bulk_load(to + kInfo, infos, info, bar, policy);
+        }
 #pragma unroll
-      for (int i = 0; i < MATS; ++i) {
-        bulk_load(to + i * kPlace, codes[i], n * 512, bars + place, policy);
-        bulk_load(to + i * kPlace + kCodes, scales[i], bytes, bars + place, policy);
+        for (int i = 0; i < MATS; ++i) {
+          bulk_load(to + i * kPlace, static_cast<const uint8_t*>(p.w[i].codes) + tile * 512ll, bytes,
+                    bar, policy);
+          bulk_load(to + i * kPlace + kCodes,
+                    static_cast<const uint8_t*>(p.w[i].scales) +
+                        tile * static_cast<long long>(of_scales(1)), of, bar, policy);
+        }
       }
       if (++place == kPlaces) place = 0;
     }
@@ -472,37 +511,25 @@ struct Product {
 
   // The pieces of a team's strips, one warp's share, ahead of the products.
   struct Ahead : Copies {
-    const Problem<MATS>& p;
     Tasks at;
-    int chunks, tiles, left, skip;  // tiles from the piece on; tiles of the team's pieces before
-    const uint8_t* codes[MATS];
-    const uint8_t* scales[MATS];
+    int chunks, tiles, tile, left, skip;  // tiles from the piece on; tiles of the team's pieces before
 
     __device__ __forceinline__ Ahead(const Problem<MATS>& p_, uint8_t* ring_, uint64_t* bars_,
                                      const Tasks& at_, int chunks_, int first)
-        : Copies(ring_, bars_), p(p_), at(at_), chunks(chunks_), tiles(p_.cols / kTile),
+        : Copies(p_, ring_, bars_), at(at_), chunks(chunks_), tiles(p_.cols / kTile),
           skip(first * kPieceTiles) {
       begin();
     }
     __device__ __forceinline__ void begin() {
       if (at.chunk >= chunks) return;
-      const long long strip =
-          static_cast<long long>(p.g.expert_of(at.chunk)) * at.strips + at.strip;
+      tile = (this->p.g.expert_of(at.chunk) * at.strips + at.strip) * tiles + skip;
       left = tiles - skip;
-#pragma unroll
-      for (int i = 0; i < MATS; ++i) {
-        codes[i] = static_cast<const uint8_t*>(p.w[i].codes) + (strip * tiles + skip) * 512;
-        scales[i] = static_cast<const uint8_t*>(p.w[i].scales) + strip * of_scales(tiles) +
-                    of_scales(skip);
-      }
     }
     __device__ __forceinline__ void next() {
       if (at.chunk >= chunks) return;
-      this->issue(codes, scales, min(kPieceTiles, left));
-      const int step = p.split * kPieceTiles;
-      left -= step;
-#pragma unroll
-      for (int i = 0; i < MATS; ++i) codes[i] += step * 512, scales[i] += of_scales(step);
+      this->issue(tile, min(kPieceTiles, left));
+      const int step = this->p.split * kPieceTiles;
+      tile += step, left -= step;
       if (left <= 0) {
         at.next();
         begin();
@@ -523,32 +550,32 @@ struct Product {
     }
   };
   struct AheadInStrips : Copies {
-    const Problem<MATS>& p;
     Pieces start, at;
     int chunks, tiles, strip, strips, expert;
+    const Rows<PARTS>& values;
+    int zero_row;
 
-    __device__ __forceinline__ AheadInStrips(const Problem<MATS>& p_, uint8_t* ring_, uint64_t* bars_,
+    __device__ __forceinline__ AheadInStrips(const Problem<MATS>& p_, const Rows<PARTS>& values_,
+                                             int zero_row_, uint8_t* ring_, uint64_t* bars_,
                                              const Pieces& at_, int chunks_)
-        : Copies(ring_, bars_), p(p_), start(at_), at(at_), chunks(chunks_),
-          tiles(p_.cols / kTile), strip(blockIdx.x), strips(p_.rows / kStrip) {
+        : Copies(p_, ring_, bars_), start(at_), at(at_), chunks(chunks_), tiles(p_.cols / kTile),
+          strip(blockIdx.x), strips(p_.rows / kStrip), values(values_), zero_row(zero_row_) {
       if (at.chunk >= chunks) strip = strips;  // more warps than pieces
-      if (strip < strips) expert = p.g.expert_of(at.chunk);
+      if (strip < strips) expert = p_.g.expert_of(at.chunk);
     }
     __device__ __forceinline__ void next() {
       if (strip >= strips) return;
-      const long long of = static_cast<long long>(expert) * strips + strip;
       const int skip = at.piece * kPieceTiles;
-      const uint8_t *codes[MATS], *scales[MATS];
-#pragma unroll
-      for (int i = 0; i < MATS; ++i) {
-        codes[i] = static_cast<const uint8_t*>(p.w[i].codes) + (of * tiles + skip) * 512;
-        scales[i] = static_cast<const uint8_t*>(p.w[i].scales) + of * of_scales(tiles) +
-                    of_scales(skip);
+      const int tile = (expert * strips + strip) * tiles + skip, n = min(kPieceTiles, tiles - skip);
+      if (ONE) {
+        const int row = this->p.g.good(at.chunk) ? at.chunk : zero_row;
+        this->issue(tile, n, values.row(row) + skip * (PARTS * kTile * 2), values.info_row(row) + skip);
+      } else {
+        this->issue(tile, n);
       }
-      this->issue(codes, scales, min(kPieceTiles, tiles - skip));
       at.next();
       if (at.chunk >= chunks) at = start, strip += gridDim.x;
-      if (strip < strips) expert = p.g.expert_of(at.chunk);  // (wanted at the next call)
+      if (strip < strips) expert = this->p.g.expert_of(at.chunk);  // (wanted at the next call)
     }
   };
 
@@ -587,17 +614,20 @@ struct Product {
   struct From {
     const uint8_t* parts;
     const float4* info[2];
+    __device__ __forceinline__ void advance(int n) {
+      parts += n * (PARTS * kTile * 2), info[0] += n, info[1] += n;
+    }
   };
   // Those values, for a tile.
   struct Values {
     uint4 v[PARTS][2];
     float factor[2], sum[FINE ? 2 : 1][2];
-    __device__ __forceinline__ void load(const From& x, int tile, int tiles) {
+    __device__ __forceinline__ void load(const From& x, int tile) {
 #pragma unroll
       for (int q = 0; q < PARTS; ++q)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          v[q][c] = reinterpret_cast<const uint4*>(x.parts + (q * tiles + tile) * (kTile * 2))[c];
+          v[q][c] = reinterpret_cast<const uint4*>(x.parts + (tile * PARTS + q) * (kTile * 2))[c];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float4* info = x.info[i] + tile;
@@ -657,12 +687,11 @@ struct Product {
       before[0] = sum[0], before[1] = sum[1];
   }
 
-  // N tiles of a piece from its tile u0 on, which is tile `at` + u0 of the rows.  Of a single eight of
+  // N tiles of a piece from its tile u0 on, for which x stands at the values.  Of a single eight of
   // tokens, `now` has the values of the first one, and is left with those of the tile after the last if
   // there is `more` to come.
   template <int N>
-  static __device__ __forceinline__ void tiles_of(const uint8_t* from, int at, int u0,
-                                                  const From (&x)[NT], int tiles, int rows,
+  static __device__ __forceinline__ void tiles_of(const uint8_t* from, int u0, From (&x)[NT], int rows,
                                                   bool more, Values& now,
                                                   float (&acc)[MATS][NT][4]) {
     static_assert(N % kTogether == 0, "whole groups");
@@ -675,7 +704,7 @@ struct Product {
       for (int i = 0; i < MATS; ++i) w[i].load(from + i * kPlace + u * 512);
       if (NT == 1) {
         const Values mine = now;
-        if (k + 1 < N || more) now.load(x[0], at + u + 1, tiles);
+        if (k + 1 < N || more) now.load(x[0], k + 1);
 #pragma unroll
         for (int i = 0; i < MATS; ++i) {
           float sums[2] = {before[0], before[1]};
@@ -686,24 +715,27 @@ struct Product {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
           if (n * 8 < rows) {
-            now.load(x[n], at + u, tiles);
+            now.load(x[n], k);
 #pragma unroll
             for (int i = 0; i < MATS; ++i)
               multiply(w[i], now, from + i * kPlace + kCodes, u, 0, part[i], before, acc[i][n]);
           }
       }
     }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) x[n].advance(N);
   }
-  // All tiles of a piece: `left` of the rows' from tile `at` on.
-  static __device__ __forceinline__ void piece(const uint8_t* from, int at, int left, const From (&x)[NT],
-                                               int tiles, int rows, Values& now,
-                                               float (&acc)[MATS][NT][4]) {
-    const int n = min(left, kPieceTiles);
-    int u = 0;
-    for (; u + 4 <= n; u += 4) tiles_of<4>(from, at, u, x, tiles, rows, u + 4 < n, now, acc);
+  // The n tiles of a piece, for which x stands at the values.
+  static __device__ __forceinline__ void piece(const uint8_t* from, int n, From (&x)[NT], int rows,
+                                               Values& now, float (&acc)[MATS][NT][4]) {
+    if (n == kPieceTiles) {
 #pragma unroll 1
-    for (; u < n; u += kTogether)
-      tiles_of<kTogether>(from, at, u, x, tiles, rows, u + kTogether < n, now, acc);
+      for (int u = 0; u < kPieceTiles; u += 4)
+        tiles_of<4>(from, u, x, rows, u + 4 < kPieceTiles, now, acc);
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < n; u += kTogether) tiles_of<kTogether>(from, u, x, rows, u + kTogether < n, now, acc);
+    }
   }
 
   // All of the warp's strips.  value_row(r) is the row of x of a chunk's row r; put(chunk,
@@ -729,8 +761,7 @@ struct Product {
     const int strips = p.rows / kStrip, tiles = p.cols / kTile, chunks = p.g.chunks();
     Tasks task(blockIdx.x * teams + team, gridDim.x * teams, strips);
     Ahead ahead(p, ring, bars, task, chunks, me);
-    if (lane == 0)
-      for (int i = 0; i < kPlaces - 1; ++i) ahead.next();
+    for (int i = 0; i < kPlaces - 1; ++i) ahead.next();
     if (p.g.single && MATS == 2) after_previous();
     int place = 0;
     uint32_t parity = 0;
@@ -748,16 +779,22 @@ struct Product {
         x[n].info[1] = values.info_row(row(lane % 4 * 2 + 1));
       }
       float acc[MATS][NT][4] = {};
-      for (int at = me * kPieceTiles; at < tiles && ok; at += split * kPieceTiles) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) x[n].advance(me * kPieceTiles);
+      for (int left = tiles - me * kPieceTiles; left > 0 && ok; left -= split * kPieceTiles) {
         Values now;
-        if (NT == 1) now.load(x[0], at, tiles);
+        if (NT == 1) now.load(x[0], 0);
         if (!wait_for(bars + place, parity)) {
           ok = false;
           break;
         }
-        if (lane == 0) ahead.next();
+        ahead.next();
         __syncwarp();
-        piece(ring + place * (MATS * kPlace), at, tiles - at, x, tiles, rows, now, acc);
+        piece(ring + place * (MATS * kPlace), min(left, kPieceTiles), x, rows, now, acc);
+        if (split > 1) {  // (past the others' pieces; not read behind the end)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) x[n].advance((split - 1) * kPieceTiles);
+        }
         if (++place == kPlaces) place = 0, parity ^= 1;
         __syncwarp();  // the place is read before it is copied into again
       }
@@ -809,9 +846,8 @@ struct Product {
     after_previous();
     const int strips = p.rows / kStrip, tiles = p.cols / kTile, chunks = p.g.chunks();
     const Pieces start(warp, warps, (tiles + kPieceTiles - 1) / kPieceTiles);
-    AheadInStrips ahead(p, ring, bars, start, chunks);
-    if (lane == 0)
-      for (int i = 0; i < kPlaces - 1; ++i) ahead.next();
+    AheadInStrips ahead(p, values, zero_row, ring, bars, start, chunks);
+    for (int i = 0; i < kPlaces - 1; ++i) ahead.next();
     int place = 0;
     uint32_t parity = 0;
     bool ok = true;
@@ -822,25 +858,33 @@ struct Product {
         const int r = p.g.row_of(chunk, lane / 4);
         return r < 0 ? zero_row : r;
       };
-      int row = at.chunk < chunks ? row_of(at.chunk) : zero_row;
+      int row = !ONE && at.chunk < chunks ? row_of(at.chunk) : zero_row;
       while (at.chunk < chunks && ok) {
+        const uint8_t* from = ring + place * kPlace;
+        const int first = at.piece * kPieceTiles, n = min(tiles - first, kPieceTiles);
         From x[1];
-        x[0].parts = values.row(row) + lane % 4 * 32;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          x[0].info[i] = values.info_row(__shfl_sync(~0u, row, (lane % 4 * 2 + i) * 4));
-        const int first = at.piece * kPieceTiles, left = tiles - first;
         Values now;
-        now.load(x[0], first, tiles);
+        if (ONE) {
+          x[0].parts = from + kValues + lane % 4 * 32;
+          x[0].info[0] = x[0].info[1] = reinterpret_cast<const float4*>(from + kInfo);
+        } else {
+          x[0].parts = values.row(row) + lane % 4 * 32;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            x[0].info[i] = values.info_row(__shfl_sync(~0u, row, (lane % 4 * 2 + i) * 4));
+          x[0].advance(first);
+          now.load(x[0], 0);
+        }
         at.next();
-        if (at.chunk < chunks) row = row_of(at.chunk);
+        if (!ONE && at.chunk < chunks) row = row_of(at.chunk);
         if (!wait_for(bars + place, parity)) {
           ok = false;
           break;
         }
-        if (lane == 0) ahead.next();
+        ahead.next();
+        if (ONE) now.load(x[0], 0);
         __syncwarp();
-        piece(ring + place * kPlace, first, left, x, tiles, 8, now, acc);
+        piece(from, n, x, 8, now, acc);
         if (++place == kPlaces) place = 0, parity ^= 1;
         __syncwarp();  // the place is read before it is copied into again
       }
@@ -863,8 +907,7 @@ struct Product {
                                                uint64_t* bars, int place, uint32_t parity) {
     if (ok) return;
     if ((threadIdx.x & 31) == 0) report_status(p.dev_status, MOE_ERR_TIMEOUT);
-    const int end = __shfl_sync(~0u, issued, 0);
-    while (place != end) {
+    while (place != issued) {
       wait_for(bars + place, parity);
       if (++place == kPlaces) place = 0, parity ^= 1;
     }
@@ -937,9 +980,9 @@ struct Down {
 };
 
 // Up to 8 tokens: y at once.
-template <bool ZEROS, int GROUP>
+template <bool ZEROS, int GROUP, bool ONE>
 __global__ void __launch_bounds__(kMaxWarps * 32) w4_down_kernel(const Down a) {
-  using Of = Product<1, 1, ZEROS, GROUP>;
+  using Of = Product<1, 1, ZEROS, GROUP, ONE>;
   extern __shared__ __align__(16) uint8_t shared[];
   const int d = a.p.rows;
   Of::run_strips(a.p, a.h, a.zero_row, shared, [&](int strip, int row, int token, float sum) {
@@ -1001,12 +1044,12 @@ __global__ void __launch_bounds__(128)
 constexpr int kSms = 152;
 // Rows of an expert that its weights are read once for; more of them are taken in several chunks.
 // (8 to a product where experts have few rows: more would be empty columns, whose values cost registers
-// and loads: 64 tokens x 16 of 896 experts, 4096 x 1024, take 590 us in chunks of 8, 965 us of 32.)
+// and loads: 64 tokens x 16 of 896 experts, 4096 x 1024, took 590 us in chunks of 8, 965 us of 32.)
 int chunk_of(const moe_problem* p) {
   return p->T <= 8 || static_cast<long long>(p->T) * p->k <= 4ll * p->E ? 8 : 32;
 }
 
-constexpr int kSharedPerSm = 228 * 1024;
+constexpr int kSharedPerSm = 228 * 1024, kSharedPerBlock = 227 * 1024;
 
 // Warps to a strip: what takes least time, in pieces, with one more for each strip's beginning and end;
 // the strips are taken in rounds.
@@ -1063,10 +1106,13 @@ Workspace carve(const moe_problem* p, void* base) {
   return w;
 }
 
+// 2^40 weights of a matrix, whose tiles are counted in 31 bits.
+bool too_many(long long E, long long rows, long long cols) { return E * rows > (1ll << 40) / cols; }
+
 int check_w4(const moe_problem* p) {
   if (int e = check_problem(p)) return e;
   if (p->r || static_cast<long long>(p->T) * p->k > kMaxSlots) return MOE_ERR_UNSUPPORTED;
-  if (std::max(p->d, p->F) > kMaxWidth) return MOE_ERR_UNSUPPORTED;
+  if (std::max(p->d, p->F) > kMaxWidth || too_many(p->E, p->d, p->F)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -1097,7 +1143,7 @@ int moe_w4_pack(int32_t E, int32_t rows, int32_t cols, int32_t group, const uint
   if (misaligned(scales, 2) || misaligned(packed_codes, 16) || misaligned(packed_scales, 16))
     return MOE_ERR_UNSUPPORTED;
   const long long weights = static_cast<long long>(E) * rows * cols;
-  if (static_cast<long long>(E) * rows > (1ll << 40) / cols) return MOE_ERR_UNSUPPORTED;
+  if (too_many(E, rows, cols)) return MOE_ERR_UNSUPPORTED;
   const auto grid = [](long long n) {
     return static_cast<int>(std::min<long long>((n + 255) / 256, 8ll * kSms));
   };
@@ -1178,10 +1224,17 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
     mark_after(MOE_KERNEL_W4_GATEUP, stream);
     mark_before(MOE_KERNEL_W4_DOWN, stream);
     if (few) {
-      using Of = Product<1, 1, Z, GROUP>;
-      const int strips = p->d / kStrip, warps = strips > kSms ? kWarps : kMaxWarps;
-      launch(w4_down_kernel<Z, GROUP>, std::min(strips, 2 * kSms * kWarps / warps), warps,
-             warps * Of::kWarpBytes, down);
+      const auto down_of = [&](auto one) {
+        using Of = Product<1, 1, Z, GROUP, decltype(one)::value>;
+        constexpr int kMost = std::min(kMaxWarps, kSharedPerBlock / Of::kWarpBytes);
+        const int strips = p->d / kStrip, warps = strips > kSms ? kWarps : kMost;
+        launch(w4_down_kernel<Z, GROUP, decltype(one)::value>,
+               std::min(strips, 2 * kSms * kWarps / warps), warps, warps * Of::kWarpBytes, down);
+      };
+      if (g.single)
+        down_of(std::true_type{});
+      else
+        down_of(std::false_type{});
     } else if (chunk == 8) {
       by_strips(w4_down_rows_kernel<1, Z, GROUP>, Product<1, 1, Z, GROUP>{}, down);
     } else {
