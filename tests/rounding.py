@@ -65,7 +65,13 @@ class Rounded:
         return self._new(v, v * self.e, LIBRARY)
 
     def sigmoid(self):
-        return 1.0 / (1.0 + (-self).exp())
+        """1 / (1 + exp(-v)).  Below -80, where exp(-v) may be infinite in fp32 and this 0: off by its own
+        size at most, which an error e of v makes exp(e) times as large."""
+        low = self.v < -80
+        r = 1.0 / (1.0 + (-Rounded(np.where(low, 0.0, self.v), np.where(low, 0.0, self.e))).exp())
+        own = np.exp(np.where(low, self.v, 0.0))
+        return Rounded(np.where(low, own, r.v),
+                       np.where(low, own * np.exp(np.minimum(self.e, 600.0)), r.e))
 
     def close(self, got, last=U, what=""):
         """|got - value| within the bound and a last rounding of relative size `last`."""

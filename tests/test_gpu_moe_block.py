@@ -542,8 +542,8 @@ def run_w4(case, w, x, idx, gate, status=None):
 
 # Sums on the tensor cores: exact products of a group are added in group / 16 steps of a few roundings
 # each (counted as 4 of half a step, whether they round or cut off), times the scale, over cols / 512
-# or so tiles a warp and 8 warps.  The products may be those of 16 + code, 16 + zero times the sum of the
-# values being taken off afterwards: the sizes of both count, not that of their difference.
+# or so tiles a warp and 8 warps.  The products are those of the codes, zero times the sum of the values
+# being taken off afterwards: the sizes of both count, not that of their difference.
 def product_count(cols, group):
     return 4 * group / 16 + 2 * cols / 512 + 16
 

@@ -1033,6 +1033,7 @@ class LayerBuffers:
                     self.saved[n] = _empty((N, r), torch.bfloat16, dev)
             self.dz_perm = _empty((N, d), torch.bfloat16, dev)
             self.dgate = _empty((T, k), torch.float32, dev)
+            self.dlogits_topk = _empty((T, k), torch.float32, dev)   # where a rule routes
             self.dx_perm = _empty((N, d), torch.bfloat16, dev)
             self.dx = _empty((T, d), torch.float32, dev)
             self.ws_bwd = _bytes(moe_expert_ffn_bwd_workspace_size(p, N), dev)
@@ -1056,8 +1057,12 @@ def fused_permute_default(p: Problem, train: bool) -> bool:
 
 
 def layer_forward(buf: LayerBuffers, x, w_router, bias, w_gate, w_up, w_down, lora=None,
-                  stream=None, gather=None, fuse_combine=False):
+                  stream=None, gather=None, fuse_combine=False, rule=None, select_bias=None):
     """route -> dispatch -> experts -> combine -> aux, all enqueued on one stream.
+
+    rule: a RouteRule by which moe_route_select takes experts and gates (with select_bias [E], the
+    balance bias, or None) from the logits that moe_route would have taken them from; it wants the
+    buffers' logits and has no remapping of overflowing slots.
 
     gather=True fuses the permute into the expert GEMMs (moe_expert_ffn_gather: dispatch
     writes only the index maps and the GEMM copies token rows of x into its operand tiles);
@@ -1066,8 +1071,17 @@ def layer_forward(buf: LayerBuffers, x, w_router, bias, w_gate, w_up, w_down, lo
     p = buf.p
     if gather is None:
         gather = fused_permute_default(p, buf.train)
-    moe_route(p, x, w_router, bias, buf.topk_idx, buf.topk_gate, buf.partials, buf.logits,
-              buf.ws_route, buf.dev_status, stream)
+    if rule is None:
+        if select_bias is not None:
+            raise ValueError("layer_forward: select_bias wants a rule")
+        moe_route(p, x, w_router, bias, buf.topk_idx, buf.topk_gate, buf.partials, buf.logits,
+                  buf.ws_route, buf.dev_status, stream)
+    else:
+        if buf.logits is None or buf.remap_rounds:
+            raise ValueError("layer_forward: a rule wants buffers with logits and without remapping")
+        moe_route_logits(p, x, w_router, bias, buf.logits, buf.ws_route, buf.dev_status, stream)
+        moe_route_select(p.T, p.E, p.k, rule, MOE_F32, buf.logits, select_bias, buf.topk_idx,
+                         buf.topk_gate, buf.partials, stream)
     if buf.remap_rounds:
         # overflowing slots move to the token's next preferences instead of being dropped
         R = buf.remap_rounds
@@ -1097,18 +1111,30 @@ def layer_forward(buf: LayerBuffers, x, w_router, bias, w_gate, w_up, w_down, lo
 
 
 def layer_backward(buf: LayerBuffers, dy, x, w_router, w_gate, w_up, w_down, lora=None,
-                   stream=None):
+                   stream=None, rule=None):
     """Gradient of <dy, y> for the forward last run on ``buf`` (which must have been built
-    with train=True): combine backward (dz_perm) -> expert backward (dx_perm, LoRA grads, and
+    with train=True; rule: the forward's, whose scale has to be above 0 and whose gates have to
+    depend on the selected logits alone): combine backward (dz_perm) -> expert backward (dx_perm, LoRA grads, and
     the gate gradients from its dh product) -> dispatch and router backward in one pass (the
     expert path and the gate path of dx)."""
     p = buf.p
     assert buf.train, "LayerBuffers(train=True) keeps what the backward needs"
+    if rule is not None and not rule.scale > 0:
+        # gradients of gates are formed by a division by them, of positive ones
+        raise ValueError("layer_backward: a rule's scale has to be above 0")
+    if rule is not None and rule.score == MOE_SCORE_SOFTMAX and not rule.renormalise:
+        raise ValueError("layer_backward: softmax scores have to be renormalised")
     moe_combine_bwd(p, dy, None, buf.slot_row, buf.topk_gate, buf.dz_perm, buf.dgate, stream)
     moe_expert_ffn_bwd(p, buf.rows_max, buf.x_perm, buf.offsets, w_gate, w_up, w_down, lora,
                        buf.saved, buf.h, buf.dz_perm, buf.dx_perm, buf.grads, buf.ws_bwd,
                        buf.dev_status, stream, row_slot=buf.row_slot, topk_gate=buf.topk_gate,
                        dgate=buf.dgate)
-    moe_dispatch_route_bwd(p, buf.dx_perm, buf.slot_row, buf.topk_idx, buf.topk_gate,
-                           buf.dgate, w_router, buf.dx, stream)
+    if rule is None:
+        moe_dispatch_route_bwd(p, buf.dx_perm, buf.slot_row, buf.topk_idx, buf.topk_gate,
+                               buf.dgate, w_router, buf.dx, stream)
+    else:
+        moe_route_select_backward(p.T, p.E, p.k, rule, MOE_F32, buf.logits, buf.topk_idx,
+                                  buf.dgate, None, buf.dlogits_topk, buf.dev_status, stream)
+        moe_dispatch_logits_bwd(p, buf.dx_perm, buf.slot_row, buf.topk_idx, buf.dlogits_topk,
+                                w_router, buf.dx, stream)
     return buf.dx
