@@ -343,7 +343,7 @@ template <typename T, int VPL, int VEC, bool SIGMOID>
 __global__ void __launch_bounds__(kWarps * 32, VPL <= 16 ? 4 : VPL <= 32 ? 3 : 2)
     route_select_kernel(const __grid_constant__ Select s) {
   extern __shared__ __align__(16) float scores[];  // [kWarps][E], as they are formed
-  __shared__ uint2 candidates[kWarps][96];
+  __shared__ uint2 candidates[kWarps][68 + 33];
   __shared__ float share_of[kWarps];  // 1 / their sum
   after_previous();
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -398,6 +398,9 @@ __global__ void __launch_bounds__(kWarps * 32, VPL <= 16 ? 4 : VPL <= 32 ? 3 : 2
     // for softmax |l - most| + VPL + 20 of them; of the sum with a bias one more.
     const float step = SIGMOID ? 0x1p-21f : 0x1p-17f;
     const float largest = SIGMOID ? 1.f : inv;  // what no score is above
+    const auto compared = [&](float q, float b) {
+      return fmaxf(SIGMOID ? q + b : fmaf(q, inv, b), -INFINITY);
+    };
     bool kept = true;
     if (by_score) {
       float top[2] = {-INFINITY, -INFINITY};
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(kWarps * 32, VPL <= 16 ? 4 : VPL <= 32 ? 3 : 2
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
             float c = SIGMOID ? q[i] : q[i] * inv;
-            if (s.bias) v[j + i] = c = fmaxf(c + b[i], -INFINITY);
+            if (s.bias) v[j + i] = c = compared(q[i], b[i]);
             if (s.groups > 1) {
               top[1] = fmaxf(top[1], fminf(top[0], c));
               top[0] = fmaxf(top[0], c);
@@ -482,15 +485,18 @@ __global__ void __launch_bounds__(kWarps * 32, VPL <= 16 ? 4 : VPL <= 32 ? 3 : 2
       }
     }
     float from;
-    int own, n;
+    uint64_t own;  // the lane's values from there on, a bit to each
+    int n;
     // Counted; and, where they are more than 64 (rare), bisected on by their own number.
     uint32_t under = least, most_key = __reduce_max_sync(~0u, max(key0, key1));
     for (;;) {
       from = ordered_value(least);
-      own = 0;
+      uint32_t low_bits = 0, high_bits = 0;
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) own += v[j] >= from;
-      n = __reduce_add_sync(~0u, own);
+      for (int j = 0; j < VPL; ++j)
+        if (v[j] >= from) (j < 32 ? low_bits : high_bits) |= 1u << (j & 31);
+      own = low_bits | static_cast<uint64_t>(high_bits) << 32;
+      n = __reduce_add_sync(~0u, __popc(low_bits) + __popc(high_bits));
       if (n > 64)
         under = least;
       else if (n <= s.k && least > under)
@@ -500,42 +506,55 @@ __global__ void __launch_bounds__(kWarps * 32, VPL <= 16 ? 4 : VPL <= 32 ? 3 : 2
       if (under >= most_key) break;
       least = under + (most_key - under + 1) / 2;
     }
-    int to = own;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int before = __shfl_up_sync(~0u, to, o);
-      if (lane >= o) to += before;
-    }
-    to -= own;
     int chosen = 0;
     if (n > 64 || (n <= s.k && least > kLowest)) {  // (equal ones are not parted)
       exact = false;
     } else if (exact) {
-      uint2* list = candidates[warp];
+      const int count = __popcll(own);
+      int to = count;
 #pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if (v[j] >= from)
-          list[to++] = make_uint2(ordered_bits(v[j]), static_cast<uint32_t>(mine.expert(j)));
+      for (int o = 1; o < 32; o *= 2) {
+        const int before = __shfl_up_sync(~0u, to, o);
+        if (lane >= o) to += before;
+      }
+      to -= count;
+      // as (the expert's complement, key), which as 64 bits are in the order wanted; read again, since
+      // which of v they are is not known to the compiler (28 conditional stores took more)
+      uint2* list = candidates[warp];
+      for (; own; own &= own - 1) {
+        const int e = mine.expert(__ffsll(own) - 1);
+        float c;
+        if (s.bias)
+          c = compared(row_scores[e], s.bias[e]);
+        else
+          c = fmaxf(logit(row, e), -INFINITY);
+        list[to++] = make_uint2(~static_cast<uint32_t>(e), ordered_bits(c));
+      }
+      if (lane < 4) list[n + lane] = make_uint2(0, 0);
+      uint2* sorted = list + 68;
+      sorted[lane] = make_uint2(~static_cast<uint32_t>(kMaxE), 0);
+      if (lane == 0) sorted[32] = sorted[0];
       __syncwarp();
-      // two to a lane, the larger one (of equal ones the lower expert) first
-      uint2 first = make_uint2(0, kMaxE), second = first;
-      if (lane < n) first = list[lane];
-      if (lane + 32 < n) second = list[lane + 32];
-      const int expert0 = first.y, expert1 = second.y;
-      if (second.x > first.x || (second.x == first.x && second.y < first.y)) {
-        const uint2 swap = first;
-        first = second, second = swap;
+      // Up to two to a lane; each one's place is the number of those before it.
+      const uint2 first = lane < n ? list[lane] : make_uint2(~static_cast<uint32_t>(kMaxE), 0);
+      const uint2 second = lane + 32 < n ? list[lane + 32] : make_uint2(~static_cast<uint32_t>(kMaxE), 0);
+      const auto both = [](uint2 c) { return c.x | static_cast<uint64_t>(c.y) << 32; };
+      const uint64_t mine0 = both(first), mine1 = both(second);
+      int place0 = 0, place1 = 0;
+      for (int i = 0; i < n; i += 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t other = both(list[i + j]);
+          place0 += other > mine0;
+          if (n > 32) place1 += other > mine1;
+        }
       }
-      // k rounds: the warp's first goes to lane r; and one more, whose key goes to all
-      uint32_t of = 0, after = 0;
-      for (int r = 0; r <= s.k; ++r) {
-        const uint32_t best = __reduce_max_sync(~0u, first.x);
-        const int e = __reduce_min_sync(~0u, first.x == best ? first.y : kMaxE);
-        if (lane == r && r < s.k) chosen = e, of = best;
-        if (lane == r - 1) after = best;
-        if (r == s.k) break;
-        if (static_cast<int>(first.y) == e) first = second, second = make_uint2(0, kMaxE);
-      }
+      if (lane < n && place0 <= s.k) sorted[place0] = first;
+      if (lane + 32 < n && place1 <= s.k) sorted[place1] = second;
+      __syncwarp();
+      const int expert0 = static_cast<int>(~first.x), expert1 = static_cast<int>(~second.x);
+      chosen = static_cast<int>(~sorted[lane].x);
+      const uint32_t of = sorted[lane].y, after = lane < s.k ? sorted[lane + 1].y : 0;
       if (s.bias) {
         bool near = false, edge = false;
         if (lane < s.k && after) {
