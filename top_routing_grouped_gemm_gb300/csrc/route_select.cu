@@ -357,9 +357,12 @@ __global__ void __launch_bounds__(kWarps * 32, VPL <= 16 ? 4 : VPL <= 32 ? 3 : 2
 #pragma unroll
     for (int j = 0; j < VPL; j += VEC) {
       float q[VEC];
-      if (j < mine.count) load_logits<VEC>(row + mine.expert(j), q);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) v[j + i] = j < mine.count ? fmaxf(q[i], -INFINITY) : NAN;
+      for (int i = 0; i < VEC; ++i) q[i] = NAN;
+      if (j < mine.count) load_logits<VEC>(row + mine.expert(j), q);
+      const float floor = j < mine.count ? -INFINITY : NAN;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[j + i] = fmaxf(q[i], floor);
     }
 #pragma unroll
     for (int j = 0; j < VPL; ++j) most = fmaxf(most, v[j]);
@@ -371,14 +374,16 @@ __global__ void __launch_bounds__(kWarps * 32, VPL <= 16 ? 4 : VPL <= 32 ? 3 : 2
       const float shift = most == -INFINITY ? 0.f : most;
 #pragma unroll
       for (int j = 0; j < VPL; j += VEC) {
-        if (j >= mine.count) continue;
-        float q[VEC];
+        float q[VEC], of = 0.f;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           q[i] = SIGMOID ? quick_sigmoid(v[j + i]) : __expf(v[j + i] - shift);
-          sum += q[i];
+          of += q[i];
         }
-        store_scores<VEC>(row_scores + mine.expert(j), q);
+        if (j < mine.count) {  // (short, so that it takes no branches)
+          sum += of;
+          store_scores<VEC>(row_scores + mine.expert(j), q);
+        }
       }
       if (small) {  // what is added up over tokens is their shares
         sum = 0.f;
@@ -398,8 +403,8 @@ __global__ void __launch_bounds__(kWarps * 32, VPL <= 16 ? 4 : VPL <= 32 ? 3 : 2
     // for softmax |l - most| + VPL + 20 of them; of the sum with a bias one more.
     const float step = SIGMOID ? 0x1p-21f : 0x1p-17f;
     const float largest = SIGMOID ? 1.f : inv;  // what no score is above
-    const auto compared = [&](float q, float b) {
-      return fmaxf(SIGMOID ? q + b : fmaf(q, inv, b), -INFINITY);
+    const auto compared = [&](float q, float b, float floor) {
+      return fmaxf(SIGMOID ? q + b : fmaf(q, inv, b), floor);
     };
     bool kept = true;
     if (by_score) {
@@ -408,15 +413,18 @@ __global__ void __launch_bounds__(kWarps * 32, VPL <= 16 ? 4 : VPL <= 32 ? 3 : 2
       if (!by_logit) {
 #pragma unroll
         for (int j = 0; j < VPL; j += VEC) {
-          if (j >= mine.count) continue;
           float q[VEC], b[VEC];
-          load_logits<VEC>(row_scores + mine.expert(j), q);
-          if (s.bias) load_logits<VEC>(s.bias + mine.expert(j), b);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) q[i] = NAN, b[i] = 0.f;
+          if (j < mine.count) load_logits<VEC>(row_scores + mine.expert(j), q);
+          if (s.bias && j < mine.count) load_logits<VEC>(s.bias + mine.expert(j), b);
+          const float floor = j < mine.count ? -INFINITY : NAN;
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
             float c = SIGMOID ? q[i] : q[i] * inv;
-            if (s.bias) v[j + i] = c = compared(q[i], b[i]);
+            if (s.bias) v[j + i] = c = compared(q[i], b[i], floor);
             if (s.groups > 1) {
+              c = fmaxf(c, -INFINITY);  // (none there)
               top[1] = fmaxf(top[1], fminf(top[0], c));
               top[0] = fmaxf(top[0], c);
             }
@@ -525,7 +533,7 @@ __global__ void __launch_bounds__(kWarps * 32, VPL <= 16 ? 4 : VPL <= 32 ? 3 : 2
         const int e = mine.expert(__ffsll(own) - 1);
         float c;
         if (s.bias)
-          c = compared(row_scores[e], s.bias[e]);
+          c = compared(row_scores[e], s.bias[e], -INFINITY);
         else
           c = fmaxf(logit(row, e), -INFINITY);
         list[to++] = make_uint2(~static_cast<uint32_t>(e), ordered_bits(c));
@@ -593,7 +601,13 @@ __global__ void __launch_bounds__(kWarps * 32, VPL <= 16 ? 4 : VPL <= 32 ? 3 : 2
                                           s.T - static_cast<long long>(blockIdx.x) * kWarps));
   for (int e = threadIdx.x; e < s.E; e += kWarps * 32) {
     float sum = 0.f;
-    for (int w = 0; w < tokens; ++w) sum = fmaf(scores[w * s.E + e], share_of[w], sum);
+    if (tokens == kWarps) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum = fmaf(scores[w * s.E + e], share_of[w], sum);
+    } else {
+#pragma unroll 1
+      for (int w = 0; w < tokens; ++w) sum = fmaf(scores[w * s.E + e], share_of[w], sum);
+    }
     s.partials[static_cast<long long>(blockIdx.x) * s.E + e] = sum;
   }
 }
