@@ -58,11 +58,18 @@ __device__ __forceinline__ float sigmoid(float l) {
   const float e = expf(-fabsf(l)), t = e / (1.f + e);
   return l < 0.f ? t : 1.f / (1.f + e);
 }
-// The same by the hardware's approximations.  exp(-|l|) is off by (|l| + 4) 2^-24 of it, the reciprocal
-// by 2^-23, which leaves the score off by 8 x 2^-24 at most (|l| e^-|l| < 0.4).
+// The same by the hardware's approximations, 2^x off by 2^-22 of it and 1 / x by 2^-23: exp(l) is off by
+// (|l| + 4) 2^-24 of it, which leaves the score off by 8 x 2^-24 at most (|l| e^-|l| < 0.4).  What would
+// be subnormal is 0.
+__device__ __forceinline__ float quick_exp(float l) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * 1.44269504f));
+  return e;
+}
 __device__ __forceinline__ float quick_sigmoid(float l) {
-  const float e = __expf(-fabsf(l)), r = __fdividef(1.f, 1.f + e);
-  return l < 0.f ? e * r : r;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + quick_exp(-l)));
+  return r;
 }
 
 // A score, where only its share in a sum is wanted: softmax scores without their sum, and sigmoid
@@ -377,7 +384,7 @@ __global__ void __launch_bounds__(kWarps * 32, VPL <= 16 ? 4 : VPL <= 32 ? 3 : 2
         float q[VEC], of = 0.f;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          q[i] = SIGMOID ? quick_sigmoid(v[j + i]) : __expf(v[j + i] - shift);
+          q[i] = SIGMOID ? quick_sigmoid(v[j + i]) : quick_exp(v[j + i] - shift);
           of += q[i];
         }
         if (j < mine.count) {  // (short, so that it takes no branches)
