@@ -41,13 +41,6 @@ __device__ __forceinline__ float warp_max(float v) {
   for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
   return v;
 }
-__device__ __forceinline__ Two warp_sum(Two v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1)
-    v = v + Two{__shfl_xor_sync(~0u, v.hi, o), __shfl_xor_sync(~0u, v.lo, o)};
-  return v;
-}
-
 // A logit; what is not a number counts as -inf.
 template <typename T>
 __device__ __forceinline__ float logit(const T* row, int e) {
@@ -622,6 +615,7 @@ __global__ void __launch_bounds__(kWarps * 32, VPL <= 16 ? 4 : VPL <= 32 ? 3 : 2
 struct SelectGrad {
   int T, E, k;
   int sigmoid, renormalise;
+  int wide;  // 16 bytes of dlogits to a store
   float scale;
   const void* logits;
   long long ld;
@@ -680,15 +674,24 @@ __global__ void __launch_bounds__(kWarps * 32) route_select_backward_kernel(cons
   if (!s.dlogits) return;
   T* out = static_cast<T*>(s.dlogits) + t * s.E;
   const bool dense = !s.renormalise && !s.sigmoid;
-  for (int i = lane; i < s.E; i += 32)
-    out[i] = static_cast<T>(dense ? -dot * (expf(logit(row, i) - most) * inv) : 0.f);
+  if (dense)
+    for (int i = lane; i < s.E; i += 32)
+      out[i] = static_cast<T>(-dot * (expf(logit(row, i) - most) * inv));
+  else if (s.wide)
+    for (int i = lane; i < s.E * static_cast<int>(sizeof(T)) / 16; i += 32)
+      reinterpret_cast<uint4*>(out)[i] = make_uint4(0, 0, 0, 0);
+  else
+    for (int i = lane; i < s.E; i += 32) out[i] = static_cast<T>(0.f);
   __syncwarp();
   // the parts of an expert that is named twice are added in the slots' order by the first of them
   const unsigned same = __match_any_sync(~0u, e);
-  float sum = 0.f;
-  for (int j = 0; j < s.k; ++j) {
-    const float other = __shfl_sync(~0u, v, j);
-    if (same >> j & 1) sum += other;
+  float sum = v;
+  if (__any_sync(~0u, e >= 0 && (same & (same - 1)))) {
+    sum = 0.f;
+    for (int j = 0; j < s.k; ++j) {
+      const float other = __shfl_sync(~0u, v, j);
+      if (same >> j & 1) sum += other;
+    }
   }
   if (e < 0 || (same & ((1u << lane) - 1))) return;
   if (dense) sum = fmaf(-dot, expf(l - most) * inv, sum);
@@ -818,6 +821,7 @@ int moe_route_select_backward(int32_t T, int32_t E, int32_t k, const moe_route_r
   s.logits = logits, s.ld = T == 1 ? 0 : ld_logits;
   s.idx = topk_idx, s.dgate = dgate, s.dlogits = dlogits, s.dlogits_topk = dlogits_topk;
   s.dev_status = dev_status;
+  s.wide = !misaligned(dlogits, 16) && E * (dtype == MOE_F32 ? 4 : 2) % 16 == 0;
   mark_before(MOE_KERNEL_ROUTE_SELECT_BWD, stream);
   const cudaError_t err =
       dtype == MOE_F32

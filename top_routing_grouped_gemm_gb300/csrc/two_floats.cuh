@@ -37,7 +37,6 @@ __device__ __forceinline__ Two operator/(Two a, Two b) {
   const float r = __fadd_rn(__fmaf_rn(-q, b.hi, a.hi), __fmaf_rn(-q, b.lo, a.lo));
   return quick_sum(q, __fdiv_rn(r, b.hi));
 }
-__device__ __forceinline__ Two operator-(Two a) { return {-a.hi, -a.lo}; }
 
 // 2^(j / 32), from its definition in 60 digits.
 __device__ const Two kPowers[32] = {
