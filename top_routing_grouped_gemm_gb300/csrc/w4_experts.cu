@@ -145,10 +145,9 @@ __device__ __forceinline__ int block_scan(int v, int* sums) {  // exclusive, 102
 }
 
 // One block of 1024.  The first `warps` of its warps have a part of the slots each, 32 at a time.
-__device__ void group_slots(const Groups& g, int k, int chunk, bool merge, int warps,
-                            int* dev_status) {
+__device__ void group_slots(const Groups& g, int chunk, int warps, int* dev_status) {
   extern __shared__ unsigned short seen[];  // [warps][E]: slots of the expert in the warp's part
-  __shared__ int sums[32], start[kMaxExperts], at_chunk[kMaxExperts];
+  __shared__ int sums[32], start[kMaxExperts];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = g.E;
   const int part = (g.slots + warps * 32 - 1) / (warps * 32) * 32;
   for (int i = threadIdx.x; i < warps * E; i += 1024) seen[i] = 0;
@@ -157,33 +156,17 @@ __device__ void group_slots(const Groups& g, int k, int chunk, bool merge, int w
   const auto pass = [&](auto put) {
     for (int at = lo; at < hi; at += 32) {
       const int slot = at + lane;
-      int e = -1;
-      float gate = 0.f;
-      if (slot < hi) {
-        if (g.good(slot)) e = g.idx[slot];
-        gate = g.gate[slot];
-        if (merge && e >= 0) {  // the token's other slots of this expert
-          const int token = slot / k;
-          for (int j = token * k; j < token * k + k; ++j)
-            if (j != slot && g.idx[j] == e) {
-              if (j < slot) {
-                e = -1;
-                break;
-              }
-              gate += g.gate[j];
-            }
-        }
-      }
+      const int e = slot < hi && g.good(slot) ? g.idx[slot] : -1;
       const unsigned same = __match_any_sync(~0u, e);
       const int rank = __popc(same & ((1u << lane) - 1));
       const int before = e >= 0 ? seen[warp * E + e] : 0;
       __syncwarp();
       if (e >= 0 && rank == 0) seen[warp * E + e] = before + __popc(same);
       __syncwarp();
-      if (slot < hi) put(slot, e, before + rank, gate);
+      if (slot < hi) put(slot, e, before + rank);
     }
   };
-  pass([&](int slot, int, int, float) {
+  pass([&](int slot, int, int) {
     if (!g.good(slot)) report_status(dev_status, MOE_ERR_BAD_INDEX);
   });
   __syncthreads();
@@ -203,22 +186,78 @@ __device__ void group_slots(const Groups& g, int k, int chunk, bool merge, int w
     g.expert[at + c] = e;
     g.first[at + c] = row + c * chunk;
     g.rows[at + c] = min(chunk, all - c * chunk);
-    if (merge) {
-      const int4 none = make_int4(-1, -1, -1, -1);
-      reinterpret_cast<int4*>(g.row_of_token)[2 * (at + c)] = none;
-      reinterpret_cast<int4*>(g.row_of_token)[2 * (at + c) + 1] = none;
-    }
   }
-  if (e < E) start[e] = row, at_chunk[e] = at;
+  if (e < E) start[e] = row;
   __syncthreads();
-  pass([&](int slot, int of, int rank, float gate) {
+  pass([&](int slot, int of, int rank) {
     const int r = of < 0 ? -1 : start[of] + rank;
     g.slot_row[slot] = r;
     if (r < 0) return;
     g.row_slot[r] = slot;
-    g.row_gate[r] = gate;
-    if (merge) g.row_of_token[at_chunk[of] * 8 + slot / k] = r;
+    g.row_gate[r] = g.gate[slot];
   });
+}
+
+// The same for up to 8 tokens, chunks in the order of their first slots: every slot looks at all others
+// (256 at most), which has three barriers where the above has ten.  One block of 1024.
+__device__ void group_few_slots(const Groups& g, int k, int* dev_status) {
+  __shared__ __align__(16) int expert[256], first_slot[256];  // (of rows' slots: the first of their expert)
+  const int i = threadIdx.x, slots = g.slots, token = i / k;
+  int e = -1;
+  float gate = 0.f;
+  if (i < slots) {
+    gate = g.gate[i];
+    if (g.good(i))
+      e = g.idx[i];
+    else
+      report_status(dev_status, MOE_ERR_BAD_INDEX);
+  }
+  if (i < 256) expert[i] = e;
+  const int4 none = make_int4(-1, -1, -1, -1);
+  if (i < 2 * min(g.E, slots)) reinterpret_cast<int4*>(g.row_of_token)[i] = none;  // as many chunks
+  __syncthreads();
+  int mine = -1;  // the first slot of the expert, if this is the token's first one
+  if (e >= 0) {
+    bool row = true;
+    for (int j = token * k; j < token * k + k; ++j)
+      if (j != i && expert[j] == e) {
+        row &= j > i;
+        gate += g.gate[j];
+      }
+    if (row) {
+      mine = i;
+      for (int j = 0; j < i; j += 4) {
+        const int4 other = reinterpret_cast<const int4*>(expert)[j / 4];
+        if (other.w == e) mine = min(mine, j + 3);
+        if (other.z == e) mine = min(mine, j + 2);
+        if (other.y == e) mine = min(mine, j + 1);
+        if (other.x == e) mine = min(mine, j);
+      }
+    }
+  }
+  if (i < 256) first_slot[i] = mine;
+  const int chunks = __syncthreads_count(mine == i);
+  if (i == 0) *g.count = chunks;
+  if (mine < 0) return;
+  int chunk = 0, before = 0, rows = 0, row = 0;
+  for (int j = 0; j < slots; j += 4) {
+    const int4 all = reinterpret_cast<const int4*>(first_slot)[j / 4];
+    const int others[4] = {all.x, all.y, all.z, all.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int other = others[q];
+      if (other < 0) continue;
+      chunk += other == j + q && other < mine;
+      before += other < mine;
+      rows += other == mine;
+      row += other == mine && j + q < i;
+    }
+  }
+  row += before;
+  g.row_slot[row] = i;
+  g.row_gate[row] = gate;
+  g.row_of_token[chunk * 8 + token] = row;
+  if (mine == i) g.expert[chunk] = e, g.first[chunk] = before, g.rows[chunk] = rows;
 }
 
 // ---------------------------------------------------------------- the tokens' values
@@ -319,14 +358,17 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* x, float (&v)[2][8])
 // has not.
 __global__ void __launch_bounds__(1024)
     w4_prepare_kernel(const __nv_bfloat16* x, int T, Rows<kXParts> rows, Rows<kHParts> h, int zero_row,
-                      int* counters, int n_counters, const Groups g, int k, int chunk, bool merge,
-                      int warps, int* dev_status) {
+                      int* counters, int n_counters, const Groups g, int k, int chunk, int warps,
+                      int* dev_status) {
   __shared__ float largest[4][8];
   after_previous();
   let_next_start();  // (which waits for this kernel's end before it reads what is written here)
   const int blocks = g.single ? gridDim.x : gridDim.x - 1;
   if (blockIdx.x == blocks) {
-    group_slots(g, k, chunk, merge, warps, dev_status);
+    if (T <= 8)
+      group_few_slots(g, k, dev_status);
+    else
+      group_slots(g, chunk, warps, dev_status);
     return;
   }
   const int me = blockIdx.x * 1024 + threadIdx.x, all = blocks * 1024;
@@ -1210,9 +1252,9 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
     err = launched(cudaFuncSetAttribute(
         w4_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 32 * kMaxExperts * 2));
     if (err == cudaSuccess)
-      err = launch_behind(w4_prepare_kernel, blocks + !g.single, 1024, g.single ? 0 : warps * p->E * 2,
+      err = launch_behind(w4_prepare_kernel, blocks + !g.single, 1024, few ? 0 : warps * p->E * 2,
                           stream, reinterpret_cast<const __nv_bfloat16*>(x), p->T, ws.x, ws.parts, slots,
-                          ws.counters, ws.n_counters, g, p->k, chunk, few, warps, dev_status);
+                          ws.counters, ws.n_counters, g, p->k, chunk, warps, dev_status);
   }
   const auto with = [&](auto z, auto of_group) {
     constexpr bool Z = decltype(z)::value;
