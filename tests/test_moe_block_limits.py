@@ -293,3 +293,13 @@ def test_limits_are_documented():
     for words in ("E <= 1024, k <= 32, groups <= 32, T up to 2^24", "D a multiple of 8, at most 16384",
                   "T * k up to 16384"):
         assert words in text, words
+
+
+@pytest.mark.parametrize("packed, structure", [("_BLOCK_IN", "moe_block_in"),
+                                               ("_BLOCK_GRADS", "moe_block_grads")])
+def test_structures_as_bytes(packed, structure):
+    packed, structure = getattr(moe, packed), getattr(moe, structure)
+    values = list(range(1, len(structure._fields_) + 1))
+    assert packed.size == ctypes.sizeof(structure)
+    read = structure.from_buffer_copy(packed.pack(*values))
+    assert [getattr(read, name) for name, _ in structure._fields_] == values

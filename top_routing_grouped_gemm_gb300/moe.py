@@ -693,7 +693,7 @@ def moe_gdr_step(B, H, dk, dv, q, k, v, beta, g, slot, n_slots, scale, S, o, dev
 
 def _rows(name, t, dtype, shape, dev):
     """(address, row stride) of rows dense in themselves."""
-    if not _is_rows(t, dtype, shape, dev):
+    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _refuse(name, t, f"a {dtype} tensor {shape}")
     by_row, by_value = t.stride()
     if by_value != 1 and shape[1] > 1:
@@ -818,8 +818,18 @@ _GATE_SHAPES = {MOE_GATE_NONE: lambda N, D: None, MOE_GATE_CHANNEL: lambda N, D:
                 MOE_GATE_TOKEN: lambda N, D: (N,), MOE_GATE_VALUE: lambda N, D: (N, D)}
 
 
+# moe_block_in and moe_block_grads as bytes, like those of the norm with the rotation
+_BLOCK_IN = struct.Struct("iiiiffiiiPqPqPqPP")
+_BLOCK_GRADS = struct.Struct("PqPqiPqPqPqPP")
+
+
 def _optional_rows(name, t, dtype, shape, dev):
-    return (None, 0) if t is None else _rows(name, t, dtype, shape, dev)
+    return (0, 0) if t is None else _rows(name, t, dtype, shape, dev)
+
+
+def _optional_row(name, t, D, dev):
+    """Address of a dense fp32 tensor [D], 0 for None."""
+    return 0 if t is None else _tensor(name, t, torch.float32, (D,), dev)
 
 
 def _block_gate(name, gate, kind, dtype, N, D, dev):
@@ -827,7 +837,7 @@ def _block_gate(name, gate, kind, dtype, N, D, dev):
     if kind not in _GATE_SHAPES:
         raise ValueError(f"gate_kind: one of the MOE_GATE_ codes is wanted, got {kind!r}")
     if gate is None:
-        return None, 0
+        return 0, 0
     if kind == MOE_GATE_VALUE:
         return _rows(name, gate, dtype, (N, D), dev)
     return _tensor(name, gate, torch.float32, _GATE_SHAPES[kind](N, D), dev), 0
@@ -835,13 +845,13 @@ def _block_gate(name, gate, kind, dtype, N, D, dev):
 
 def _block_in(N, D, stream_dtype, dtype, eps, scale, x, y, gate_kind, gate_sigmoid, gate,
               post_norm, w_post, w_pre, dev):
-    st, dt, f32 = _DTYPES[stream_dtype], _DTYPES[dtype], torch.float32
-    return moe_block_in(N, D, stream_dtype, dtype, eps, scale, gate_kind, 1 if gate_sigmoid else 0,
-                        1 if post_norm else 0, *_rows("x", x, st, (N, D), dev),
-                        *_optional_rows("y", y, dt, (N, D), dev),
-                        *_block_gate("gate", gate, gate_kind, dt, N, D, dev),
-                        _tensor("w_post", w_post, f32, (D,), dev, True),
-                        _tensor("w_pre", w_pre, f32, (D,), dev, True))
+    st, dt = _DTYPES[stream_dtype], _DTYPES[dtype]
+    return _BLOCK_IN.pack(N, D, stream_dtype, dtype, eps, scale, gate_kind, 1 if gate_sigmoid else 0,
+                          1 if post_norm else 0, *_rows("x", x, st, (N, D), dev),
+                          *_optional_rows("y", y, dt, (N, D), dev),
+                          *_block_gate("gate", gate, gate_kind, dt, N, D, dev),
+                          _optional_row("w_post", w_post, D, dev),
+                          _optional_row("w_pre", w_pre, D, dev))
 
 
 def moe_block_norm(N, D, stream_dtype, dtype, eps, scale, x, y, gate_kind, gate_sigmoid, gate,
@@ -852,7 +862,7 @@ def moe_block_norm(N, D, stream_dtype, dtype, eps, scale, x, y, gate_kind, gate_
     block = _block_in(N, D, stream_dtype, dtype, eps, scale, x, y, gate_kind, gate_sigmoid, gate,
                       post_norm, w_post, w_pre, dev)
     _check("moe_block_norm",
-           lib().moe_block_norm(ctypes.addressof(block),
+           lib().moe_block_norm(block,
                                 *_optional_rows("z", z, _DTYPES[stream_dtype], (N, D), dev),
                                 *_optional_rows("n", n, _DTYPES[dtype], (N, D), dev),
                                 _stream_of(stream, dev)))
@@ -866,20 +876,19 @@ def moe_block_norm_backward(N, D, stream_dtype, dtype, eps, scale, x, y, gate_ki
                             gate, post_norm, w_post, w_pre, dz, dn_dtype, dn, dx, dy, dgate,
                             dw_post, dw_pre, workspace, stream=None):
     """The forward's inputs, then gradients (dz, dn in; the others out, None where not wanted)."""
-    st, dt, f32, dev = _DTYPES[stream_dtype], _DTYPES[dtype], torch.float32, _device()
+    st, dt, dev = _DTYPES[stream_dtype], _DTYPES[dtype], _device()
     block = _block_in(N, D, stream_dtype, dtype, eps, scale, x, y, gate_kind, gate_sigmoid, gate,
                       post_norm, w_post, w_pre, dev)
     rows, wp_wn = (N, D), _ws(workspace)
-    grads = moe_block_grads(*_optional_rows("dz", dz, st, rows, dev),
-                            *_optional_rows("dn", dn, _DTYPES[dn_dtype], rows, dev), dn_dtype,
-                            *_rows("dx", dx, st, rows, dev),
-                            *_optional_rows("dy", dy, dt, rows, dev),
-                            *_block_gate("dgate", dgate, gate_kind, dt, N, D, dev),
-                            _tensor("dw_post", dw_post, f32, (D,), dev, True),
-                            _tensor("dw_pre", dw_pre, f32, (D,), dev, True))
+    grads = _BLOCK_GRADS.pack(*_optional_rows("dz", dz, st, rows, dev),
+                              *_optional_rows("dn", dn, _DTYPES[dn_dtype], rows, dev), dn_dtype,
+                              *_rows("dx", dx, st, rows, dev),
+                              *_optional_rows("dy", dy, dt, rows, dev),
+                              *_block_gate("dgate", dgate, gate_kind, dt, N, D, dev),
+                              _optional_row("dw_post", dw_post, D, dev),
+                              _optional_row("dw_pre", dw_pre, D, dev))
     _check("moe_block_norm_backward",
-           lib().moe_block_norm_backward(ctypes.addressof(block), ctypes.addressof(grads), *wp_wn,
-                                         _stream_of(stream, dev)))
+           lib().moe_block_norm_backward(block, grads, *wp_wn, _stream_of(stream, dev)))
 
 
 def moe_w4_pack(E, rows, cols, group, codes, scales, zeros, packed_codes, packed_scales,
@@ -903,7 +912,8 @@ def moe_w4_pack(E, rows, cols, group, codes, scales, zeros, packed_codes, packed
 class W4Weights:
     """4-bit weights [E, rows, cols], laid out for moe_w4_expert_ffn: codes [E, rows, cols / 2] (two
     to a byte, the lower four bits first), scales [E, rows, cols / group] bf16, zeros like scales
-    (uint8) or None (8)."""
+    (uint8) or None (8).  The arrays are allocated on the current stream: another ``stream`` has to
+    have waited for it."""
 
     def __init__(self, codes, scales, zeros=None, stream=None):
         if codes.dim() != 3 or scales.dim() != 3 or scales.shape[2] == 0:
