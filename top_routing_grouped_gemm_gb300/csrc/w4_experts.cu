@@ -38,6 +38,7 @@ constexpr int kMaxWidth = 1 << 20;
 constexpr int kMaxExperts = 1024;
 constexpr int kXParts = 1, kHParts = 2;  // fp16 values for one of x, of h
 constexpr int kWarps = 8, kMaxWarps = 16;  // to a block
+constexpr int kSharedPerSm = 228 * 1024, kSharedPerBlock = 227 * 1024;
 
 // ---------------------------------------------------------------- layout
 // A tile of 16 rows x 64 columns takes 512 bytes, 16 to a lane: lane 4 g + t holds rows g and g + 8,
@@ -502,17 +503,21 @@ struct Product {
   static constexpr bool kFactors = MATS == 1, FINE = GROUP == 32;
   static constexpr int PARTS = MATS == 2 ? kXParts : kHParts;
   static constexpr int kPieceTiles = MATS == 2 ? 4 : 8;
-  static constexpr int kPlaces = MATS == 2 && NT == 1 ? 3 : 2;  // of the ring; one less on their way
   static constexpr int kWords = ZEROS ? 2 : 1;                  // of a group's scales, to a lane
   static constexpr int kCodes = kPieceTiles * 512;              // bytes of a piece and matrix
   static constexpr int of_scales(int tiles) { return tiles * (2048 * kWords / GROUP); }
   static constexpr int kValues = kCodes + of_scales(kPieceTiles);  // where ONE's values are in a place
   static constexpr int kInfo = kValues + kPieceTiles * (PARTS * kTile * 2);
   static constexpr int kPlace = ONE ? kInfo + kPieceTiles * 16 : kValues;
-  static constexpr int kRing = kPlaces * MATS * kPlace;
   static constexpr int kSums = MATS * NT * 4;  // to a lane
-  static constexpr int kWarpBytes = kRing + kSums * 128 + 32, kBytes = kWarps * kWarpBytes;
-  static constexpr int kBlocks = 2;  // to an SM, where they fit
+  static constexpr int with_places(int n) { return n * MATS * kPlace + kSums * 128 + 32; }
+  static constexpr int kBlocks = 2;  // to an SM
+  // Of the ring, one less of them on their way: three for the shorter pieces of gate and up, if two
+  // blocks still fit (with one, 32 tokens with zeros and groups of 64 took 81 us there instead of 66).
+  static constexpr int kPlaces =
+      MATS == 2 && NT == 1 && kBlocks * (kWarps * with_places(3) + 1024) <= kSharedPerSm ? 3 : 2;
+  static constexpr int kRing = kPlaces * MATS * kPlace;
+  static constexpr int kWarpBytes = with_places(kPlaces), kBytes = kWarps * kWarpBytes;
   // Tiles that one scale is multiplied with at once: two where their sums can wait for it.
   static constexpr int kTogether = GROUP == 128 && !kFactors && NT == 1 ? 2 : 1;
 
@@ -1091,7 +1096,6 @@ int chunk_of(const moe_problem* p) {
   return p->T <= 8 || static_cast<long long>(p->T) * p->k <= 4ll * p->E ? 8 : 32;
 }
 
-constexpr int kSharedPerSm = 228 * 1024, kSharedPerBlock = 227 * 1024;
 
 // Warps to a strip: what takes least time, in pieces, with one more for each strip's beginning and end;
 // the strips are taken in rounds.
