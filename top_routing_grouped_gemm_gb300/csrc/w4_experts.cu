@@ -472,17 +472,15 @@ struct Weights {
   int group;
 };
 
-// Strips of MATS matrices [E, rows, cols] for the slots' chunks: task i is strip i % strips of chunk
-// i / strips.
-template <int MATS>
+// Strips of one or two matrices [E, rows, cols] for the slots' chunks.
 struct Problem {
   Groups g;
-  Weights w[MATS];
+  Weights w[2];
   int rows, cols, split;
   int* dev_status;
 };
 
-// The tasks of a team of warps, one after the other.
+// The tasks of a team of warps, one after the other: task i is strip i % strips of chunk i / strips.
 struct Tasks {
   int chunk, strip, strips, chunk_step, strip_step;
   __device__ __forceinline__ Tasks(int first, int step, int strips_)
@@ -494,15 +492,17 @@ struct Tasks {
   }
 };
 
-// MATS matrices, NT x 8 tokens at most; ZEROS: zeros are given; GROUP columns to a scale.  Gate and up
-// (MATS 2) take x, whose rows have one factor, down takes h, which has one for each tile.  ONE: a single
-// token, whose values come with the weights' pieces and stand in all columns.  (Read from the L2 by each
-// lane, a tile ahead, they were what down waited for.)
-template <int MATS, int NT, bool ZEROS, int GROUP, bool ONE = false>
+// MATS strips of weights with NT x 8 tokens at most; ZEROS: zeros are given; GROUP columns to a scale.
+// Gate and up take x, whose rows have one factor, and a strip of each.  DOWN takes h, which has a factor
+// for each tile, and one strip or two neighbouring ones (which share the loads of h and wait for them
+// half as often: 32 tokens, 2048 x 512: 170 -> 158 us).  ONE: a single token, whose values come with the weights' pieces and stand in
+// all columns.  (Read from the L2 by each lane, a tile ahead, they were what down waited for.)
+template <bool DOWN, int MATS, int NT, bool ZEROS, int GROUP, bool ONE = false>
 struct Product {
-  static constexpr bool kFactors = MATS == 1, FINE = GROUP == 32;
-  static constexpr int PARTS = MATS == 2 ? kXParts : kHParts;
+  static constexpr bool kFactors = DOWN, FINE = GROUP == 32;
+  static constexpr int PARTS = DOWN ? kHParts : kXParts;
   static constexpr int kPieceTiles = MATS == 2 ? 4 : 8;
+  static constexpr int kRows = DOWN ? MATS * kStrip : kStrip;  // of a matrix, to a task
   static constexpr int kWords = ZEROS ? 2 : 1;                  // of a group's scales, to a lane
   static constexpr int kCodes = kPieceTiles * 512;              // bytes of a piece and matrix
   static constexpr int of_scales(int tiles) { return tiles * (2048 * kWords / GROUP); }
@@ -523,13 +523,13 @@ struct Product {
 
   // Issues the copies of pieces; all of a warp's lanes know where it stands, one issues them.
   struct Copies {
-    const Problem<MATS>& p;
+    const Problem& p;
     uint32_t ring, bars;
-    int place;
+    int tiles, place;  // tiles: of a strip
     uint64_t policy;
 
-    __device__ __forceinline__ Copies(const Problem<MATS>& p_, uint8_t* ring_, uint64_t* bars_)
-        : p(p_), ring(smem_u32(ring_)), bars(smem_u32(bars_)), place(0),
+    __device__ __forceinline__ Copies(const Problem& p_, uint8_t* ring_, uint64_t* bars_)
+        : p(p_), ring(smem_u32(ring_)), bars(smem_u32(bars_)), tiles(p_.cols / kTile), place(0),
           policy(l2_policy_evict_first()) {}
     // n tiles from `tile` on of all that a matrix has (fewer than 2^31).
     __device__ __forceinline__ void issue(int tile, int n, const void* values = nullptr,
@@ -545,11 +545,11 @@ struct Product {
         }
 #pragma unroll
         for (int i = 0; i < MATS; ++i) {
-          bulk_load(to + i * kPlace, static_cast<const uint8_t*>(p.w[i].codes) + tile * 512ll, bytes,
-                    bar, policy);
-          bulk_load(to + i * kPlace + kCodes,
-                    static_cast<const uint8_t*>(p.w[i].scales) +
-                        tile * static_cast<long long>(of_scales(1)), of, bar, policy);
+          const Weights& w = p.w[DOWN ? 0 : i];
+          const long long at = tile + (DOWN ? i * tiles : 0);
+          bulk_load(to + i * kPlace, static_cast<const uint8_t*>(w.codes) + at * 512, bytes, bar, policy);
+          bulk_load(to + i * kPlace + kCodes, static_cast<const uint8_t*>(w.scales) + at * of_scales(1),
+                    of, bar, policy);
         }
       }
       if (++place == kPlaces) place = 0;
@@ -559,18 +559,17 @@ struct Product {
   // The pieces of a team's strips, one warp's share, ahead of the products.
   struct Ahead : Copies {
     Tasks at;
-    int chunks, tiles, tile, left, skip;  // tiles from the piece on; tiles of the team's pieces before
+    int chunks, tile, left, skip;  // tiles from the piece on; tiles of the team's pieces before
 
-    __device__ __forceinline__ Ahead(const Problem<MATS>& p_, uint8_t* ring_, uint64_t* bars_,
+    __device__ __forceinline__ Ahead(const Problem& p_, uint8_t* ring_, uint64_t* bars_,
                                      const Tasks& at_, int chunks_, int first)
-        : Copies(p_, ring_, bars_), at(at_), chunks(chunks_), tiles(p_.cols / kTile),
-          skip(first * kPieceTiles) {
+        : Copies(p_, ring_, bars_), at(at_), chunks(chunks_), skip(first * kPieceTiles) {
       begin();
     }
     __device__ __forceinline__ void begin() {
       if (at.chunk >= chunks) return;
-      tile = (this->p.g.expert_of(at.chunk) * at.strips + at.strip) * tiles + skip;
-      left = tiles - skip;
+      tile = (this->p.g.expert_of(at.chunk) * at.strips + at.strip) * (kRows / kStrip * this->tiles) + skip;
+      left = this->tiles - skip;
     }
     __device__ __forceinline__ void next() {
       if (at.chunk >= chunks) return;
@@ -598,14 +597,14 @@ struct Product {
   };
   struct AheadInStrips : Copies {
     Pieces start, at;
-    int chunks, tiles, strip, strips, expert;
+    int chunks, strip, strips, expert;
     const Rows<PARTS>& values;
     int zero_row;
 
-    __device__ __forceinline__ AheadInStrips(const Problem<MATS>& p_, const Rows<PARTS>& values_,
+    __device__ __forceinline__ AheadInStrips(const Problem& p_, const Rows<PARTS>& values_,
                                              int zero_row_, uint8_t* ring_, uint64_t* bars_,
                                              const Pieces& at_, int chunks_)
-        : Copies(p_, ring_, bars_), start(at_), at(at_), chunks(chunks_), tiles(p_.cols / kTile),
+        : Copies(p_, ring_, bars_), start(at_), at(at_), chunks(chunks_),
           strip(blockIdx.x), strips(p_.rows / kStrip), values(values_), zero_row(zero_row_) {
       if (at.chunk >= chunks) strip = strips;  // more warps than pieces
       if (strip < strips) expert = p_.g.expert_of(at.chunk);
@@ -613,7 +612,8 @@ struct Product {
     __device__ __forceinline__ void next() {
       if (strip >= strips) return;
       const int skip = at.piece * kPieceTiles;
-      const int tile = (expert * strips + strip) * tiles + skip, n = min(kPieceTiles, tiles - skip);
+      const int tile = (expert * strips + strip) * this->tiles + skip;
+      const int n = min(kPieceTiles, this->tiles - skip);
       if (ONE) {
         const int row = this->p.g.good(at.chunk) ? at.chunk : zero_row;
         this->issue(tile, n, values.row(row) + skip * (PARTS * kTile * 2), values.info_row(row) + skip);
@@ -790,7 +790,7 @@ struct Product {
   // strip, token 8 n + lane % 4 * 2 + r % 2 of the chunk.  (Columns of tokens that there are not repeat
   // the first one's; a product's columns have nothing to do with each other.)
   template <typename RowOf, typename Put>
-  static __device__ __forceinline__ void run(const Problem<MATS>& p, const Rows<PARTS>& values,
+  static __device__ __forceinline__ void run(const Problem& p, const Rows<PARTS>& values,
                                              uint8_t* shared, RowOf value_row, Put put) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, split = p.split;
     const int team = warp / split, me = warp % split, teams = kWarps / split;
@@ -804,12 +804,12 @@ struct Product {
     }
     __syncwarp();
     // a single token's experts were there before the preparing kernel began
-    if (!p.g.single || MATS == 1) after_previous();
-    const int strips = p.rows / kStrip, tiles = p.cols / kTile, chunks = p.g.chunks();
+    if (!p.g.single || DOWN) after_previous();
+    const int strips = p.rows / kRows, tiles = p.cols / kTile, chunks = p.g.chunks();
     Tasks task(blockIdx.x * teams + team, gridDim.x * teams, strips);
     Ahead ahead(p, ring, bars, task, chunks, me);
     for (int i = 0; i < kPlaces - 1; ++i) ahead.next();
-    if (p.g.single && MATS == 2) after_previous();
+    if (p.g.single && !DOWN) after_previous();
     int place = 0;
     uint32_t parity = 0;
     bool ok = true;
@@ -876,7 +876,7 @@ struct Product {
   // over a token's experts stay in the products' sums.  Tokens that a chunk has not take `zero_row`.
   // put(strip, row, token, sum).
   template <typename Put>
-  static __device__ __forceinline__ void run_strips(const Problem<MATS>& p,
+  static __device__ __forceinline__ void run_strips(const Problem& p,
                                                     const Rows<PARTS>& values, int zero_row,
                                                     uint8_t* shared, Put put) {
     static_assert(MATS == 1 && NT == 1, "one matrix, 8 tokens");
@@ -950,7 +950,7 @@ struct Product {
   }
 
   // After a wait that ran out: what is on its way arrives before the block's memory is given up.
-  static __device__ __forceinline__ void drain(const Problem<MATS>& p, bool ok, int issued,
+  static __device__ __forceinline__ void drain(const Problem& p, bool ok, int issued,
                                                uint64_t* bars, int place, uint32_t parity) {
     if (ok) return;
     if ((threadIdx.x & 31) == 0) report_status(p.dev_status, MOE_ERR_TIMEOUT);
@@ -962,7 +962,7 @@ struct Product {
 };
 
 struct GateUp {
-  Problem<2> p;
+  Problem p;
   Rows<kXParts> x;
   float* h;       // [slots][F], times the gate
   Rows<kHParts> parts;  // the same as operands
@@ -972,8 +972,8 @@ struct GateUp {
 
 // h goes to memory in fp32; the warp that brings the last of a tile's four strips makes operands of it.
 template <int NT, bool ZEROS, int GROUP>
-__global__ void __launch_bounds__(kWarps * 32, Product<2, NT, ZEROS, GROUP>::kBlocks) w4_gateup_kernel(const GateUp a) {
-  using Of = Product<2, NT, ZEROS, GROUP>;
+__global__ void __launch_bounds__(kWarps * 32, Product<false, 2, NT, ZEROS, GROUP>::kBlocks) w4_gateup_kernel(const GateUp a) {
+  using Of = Product<false, 2, NT, ZEROS, GROUP>;
   extern __shared__ __align__(16) uint8_t shared[];
   const int F = a.p.rows, lane = threadIdx.x & 31;
   Of::run(
@@ -1019,7 +1019,7 @@ __global__ void __launch_bounds__(kWarps * 32, Product<2, NT, ZEROS, GROUP>::kBl
 }
 
 struct Down {
-  Problem<1> p;
+  Problem p;
   Rows<kHParts> h;
   float* out;  // [slots][d], a row to a slot
   __nv_bfloat16* y;
@@ -1029,7 +1029,7 @@ struct Down {
 // Up to 8 tokens: y at once.
 template <bool ZEROS, int GROUP, bool ONE>
 __global__ void __launch_bounds__(kMaxWarps * 32) w4_down_kernel(const Down a) {
-  using Of = Product<1, 1, ZEROS, GROUP, ONE>;
+  using Of = Product<true, 1, 1, ZEROS, GROUP, ONE>;
   extern __shared__ __align__(16) uint8_t shared[];
   const int d = a.p.rows;
   Of::run_strips(a.p, a.h, a.zero_row, shared, [&](int strip, int row, int token, float sum) {
@@ -1039,22 +1039,24 @@ __global__ void __launch_bounds__(kMaxWarps * 32) w4_down_kernel(const Down a) {
 }
 
 // More tokens: the rows' parts of it, which w4_combine_kernel adds.
-template <int NT, bool ZEROS, int GROUP>
-__global__ void __launch_bounds__(kWarps * 32, Product<1, NT, ZEROS, GROUP>::kBlocks)
+template <int MATS, int NT, bool ZEROS, int GROUP>
+__global__ void __launch_bounds__(kWarps * 32, Product<true, MATS, NT, ZEROS, GROUP>::kBlocks)
     w4_down_rows_kernel(const Down a) {
-  using Of = Product<1, NT, ZEROS, GROUP>;
+  using Of = Product<true, MATS, NT, ZEROS, GROUP>;
   extern __shared__ __align__(16) uint8_t shared[];
   const int d = a.p.rows, lane = threadIdx.x & 31;
   Of::run(a.p, a.h, shared, [&](int r) { return r; },
-          [&](int, int first, int rows, int strip, const float (&acc)[1][NT][4]) {
+          [&](int, int first, int rows, int strip, const float (&acc)[MATS][NT][4]) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 const int token = n * 8 + lane % 4 * 2 + r % 2;
                 if (token < rows)
-                  a.out[(first + token) * static_cast<long long>(d) + strip * kStrip + lane / 4 +
-                        r / 2 * 8] = acc[0][n][r];
+#pragma unroll
+                  for (int i = 0; i < MATS; ++i)
+                    a.out[(first + token) * static_cast<long long>(d) + (strip * MATS + i) * kStrip +
+                          lane / 4 + r / 2 * 8] = acc[i][n][r];
               }
           });
 }
@@ -1234,7 +1236,7 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
   const bool few = p->T <= 8;
   GateUp up{{g, {of(w_gate), of(w_up)}, p->F, p->d, 1, dev_status}, ws.x, ws.h, ws.parts,
             ws.counters, p->k};
-  Down down{{g, {of(w_down)}, p->d, p->F, 1, dev_status}, ws.parts, ws.out,
+  Down down{{g, {of(w_down), {}}, p->d, p->F, 1, dev_status}, ws.parts, ws.out,
             reinterpret_cast<__nv_bfloat16*>(y), p->T, slots};
   cudaError_t err = cudaSuccess;
   const auto launch = [&](auto kernel, int blocks, int warps, int bytes, auto& args) {
@@ -1245,7 +1247,7 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
   const auto by_strips = [&](auto kernel, auto product, auto& args) {
     using Of = decltype(product);
     const int blocks = std::min(Of::kBlocks, kSharedPerSm / (Of::kBytes + 1024)) * kSms;
-    args.p.split = split_of(chunks * static_cast<long long>(args.p.rows / kStrip),
+    args.p.split = split_of(chunks * static_cast<long long>(args.p.rows / Of::kRows),
                             (args.p.cols / kTile + Of::kPieceTiles - 1) / Of::kPieceTiles, blocks * kWarps);
     launch(kernel, blocks, kWarps, Of::kBytes, args);
   };
@@ -1264,14 +1266,14 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
     constexpr bool Z = decltype(z)::value;
     constexpr int GROUP = decltype(of_group)::value;
     if (chunk == 8)
-      by_strips(w4_gateup_kernel<1, Z, GROUP>, Product<2, 1, Z, GROUP>{}, up);
+      by_strips(w4_gateup_kernel<1, Z, GROUP>, Product<false, 2, 1, Z, GROUP>{}, up);
     else
-      by_strips(w4_gateup_kernel<4, Z, GROUP>, Product<2, 4, Z, GROUP>{}, up);
+      by_strips(w4_gateup_kernel<4, Z, GROUP>, Product<false, 2, 4, Z, GROUP>{}, up);
     mark_after(MOE_KERNEL_W4_GATEUP, stream);
     mark_before(MOE_KERNEL_W4_DOWN, stream);
     if (few) {
       const auto down_of = [&](auto one) {
-        using Of = Product<1, 1, Z, GROUP, decltype(one)::value>;
+        using Of = Product<true, 1, 1, Z, GROUP, decltype(one)::value>;
         constexpr int kMost = std::min(kMaxWarps, kSharedPerBlock / Of::kWarpBytes);
         const int strips = p->d / kStrip, warps = strips > kSms ? kWarps : kMost;
         launch(w4_down_kernel<Z, GROUP, decltype(one)::value>,
@@ -1282,9 +1284,9 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
       else
         down_of(std::false_type{});
     } else if (chunk == 8) {
-      by_strips(w4_down_rows_kernel<1, Z, GROUP>, Product<1, 1, Z, GROUP>{}, down);
+      by_strips(w4_down_rows_kernel<2, 1, Z, GROUP>, Product<true, 2, 1, Z, GROUP>{}, down);
     } else {
-      by_strips(w4_down_rows_kernel<4, Z, GROUP>, Product<1, 4, Z, GROUP>{}, down);
+      by_strips(w4_down_rows_kernel<1, 4, Z, GROUP>, Product<true, 1, 4, Z, GROUP>{}, down);
     }
     if (!few && err == cudaSuccess)
       err = launch_behind(w4_combine_kernel, dim3(p->T, std::min(64, (p->d + 511) / 512)), 128, 0,
