@@ -12,10 +12,10 @@
 // weights, where half the pipes' rate holds for 40 of them.  e4m3 operands, which a code in a byte is too,
 // are turned into others first on this GPU: 108 instructions.)
 //
-// Now it is 56 for gate and up, 82 (one token) to 90 for down, whose operand has two parts.  One token
-// through 16 of 896 experts of 4096 x 1024 takes 30 us (100 MB, 15 us of reading), 64 tokens that crowd
-// on few experts 555 us (358), 32 tokens through experts of 2048 x 512 with zeros 207 us (96): warps
-// are issuing, in turn with what they wait for, half of the time.
+// Now it is 56 for gate and up, 80 for down, whose operand has two parts.  One token through 16 of 896
+// experts of 4096 x 1024 takes 30 us (104 MB, 15 us of reading), 64 tokens that crowd on few experts
+// 503 us (358), 32 tokens through experts of 2048 x 512 with zeros 158 us (97): warps are issuing half of
+// the time, in turn with what they wait for.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -89,9 +89,7 @@ __global__ void w4_pack_scales_kernel(int groups, long long entries, const __nv_
 }
 
 // ---------------------------------------------------------------- the slots by expert
-// Chunks of at most `chunk` rows of one expert; a row is a slot, in the slots' order within an
-// expert.  With up to 8 tokens a token's slots of one expert are one row, with the sum of their gates,
-// and `row_of_token` [chunks][8] has the tokens' rows (-1 for none).
+// Chunks of at most `chunk` rows of one expert; a row is a slot, in the slots' order within an expert.
 struct Groups {
   const int* idx;  // [slots] the slots' experts; a single token's slots are chunks as they are
   const float* gate;
@@ -102,8 +100,7 @@ struct Groups {
   int* rows;      // [...] how many
   int* row_slot;  // [slots]
   float* row_gate;
-  int* slot_row;      // [slots], -1 for a bad expert
-  int* row_of_token;
+  int* slot_row;  // [slots], -1 for a bad expert
 
   __device__ __forceinline__ bool good(int slot) const { return idx[slot] >= 0 && idx[slot] < E; }
   __device__ __forceinline__ int chunks() const { return single ? slots : *count; }
@@ -115,9 +112,6 @@ struct Groups {
   __device__ __forceinline__ int rows_of(int c) const { return single ? good(c) : rows[c]; }
   __device__ __forceinline__ int slot_of(int row) const { return single ? row : row_slot[row]; }
   __device__ __forceinline__ float gate_of(int row) const { return single ? gate[row] : row_gate[row]; }
-  __device__ __forceinline__ int row_of(int c, int token) const {
-    return single ? (token == 0 && good(c) ? c : -1) : row_of_token[c * 8 + token];
-  }
 };
 
 __device__ __forceinline__ int block_scan(int v, int* sums) {  // exclusive, 1024 threads
@@ -199,66 +193,57 @@ __device__ void group_slots(const Groups& g, int chunk, int warps, int* dev_stat
   });
 }
 
-// The same for up to 8 tokens, chunks in the order of their first slots: every slot looks at all others
-// (256 at most), which has three barriers where the above has ten.  One block of 1024.
-__device__ void group_few_slots(const Groups& g, int k, int* dev_status) {
-  __shared__ __align__(16) int expert[256], first_slot[256];  // (of rows' slots: the first of their expert)
-  const int i = threadIdx.x, slots = g.slots, token = i / k;
+// The same for few slots: every slot looks at all others, which has two barriers where the above has
+// ten (7 tokens x 4 of 64 experts, 512 x 256: 17.1 -> 15.7 us).  Experts in the order of their first
+// slots.  One block of 1024.
+constexpr int kFewSlots = 256;
+__device__ void group_few_slots(const Groups& g, int chunk, int* dev_status) {
+  __shared__ __align__(16) int expert[kFewSlots], rows_of[kFewSlots];  // (of an expert's first slots)
+  const int i = threadIdx.x, slots = g.slots;
   int e = -1;
-  float gate = 0.f;
   if (i < slots) {
-    gate = g.gate[i];
     if (g.good(i))
       e = g.idx[i];
     else
       report_status(dev_status, MOE_ERR_BAD_INDEX);
   }
-  if (i < 256) expert[i] = e;
-  const int4 none = make_int4(-1, -1, -1, -1);
-  if (i < 2 * min(g.E, slots)) reinterpret_cast<int4*>(g.row_of_token)[i] = none;  // as many chunks
+  if (i < kFewSlots) expert[i] = e;
   __syncthreads();
-  int mine = -1;  // the first slot of the expert, if this is the token's first one
-  if (e >= 0) {
-    bool row = true;
-    for (int j = token * k; j < token * k + k; ++j)
-      if (j != i && expert[j] == e) {
-        row &= j > i;
-        gate += g.gate[j];
-      }
-    if (row) {
-      mine = i;
-      for (int j = 0; j < i; j += 4) {
-        const int4 other = reinterpret_cast<const int4*>(expert)[j / 4];
-        if (other.w == e) mine = min(mine, j + 3);
-        if (other.z == e) mine = min(mine, j + 2);
-        if (other.y == e) mine = min(mine, j + 1);
-        if (other.x == e) mine = min(mine, j);
-      }
-    }
-  }
-  if (i < 256) first_slot[i] = mine;
-  const int chunks = __syncthreads_count(mine == i);
-  if (i == 0) *g.count = chunks;
-  if (mine < 0) return;
-  int chunk = 0, before = 0, rows = 0, row = 0;
-  for (int j = 0; j < slots; j += 4) {
-    const int4 all = reinterpret_cast<const int4*>(first_slot)[j / 4];
-    const int others[4] = {all.x, all.y, all.z, all.w};
+  int first = i, rank = 0, rows = 0;  // of the slots of this expert
+  if (e >= 0)
+    for (int j = 0; j < slots; j += 4) {
+      const int4 q = reinterpret_cast<const int4*>(expert)[j / 4];
+      const int others[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int other = others[q];
-      if (other < 0) continue;
-      chunk += other == j + q && other < mine;
-      before += other < mine;
-      rows += other == mine;
-      row += other == mine && j + q < i;
+      for (int c = 0; c < 4; ++c) {
+        const bool same = others[c] == e;
+        if (same && rows == 0) first = j + c;
+        rows += same;
+        rank += same && j + c < i;
+      }
+    }
+  if (i < kFewSlots) rows_of[i] = e >= 0 && first == i ? rows : 0;
+  __syncthreads();
+  if (i >= slots) return;
+  int row = rank, at = 0, all = 0;  // chunks before the expert's, and of all
+  for (int j = 0; j < slots; j += 4) {
+    const int4 q = reinterpret_cast<const int4*>(rows_of)[j / 4];
+    const int others[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int chunks = (others[c] + chunk - 1) / chunk;
+      all += chunks;
+      if (j + c < first) row += others[c], at += chunks;
     }
   }
-  row += before;
+  if (i == 0) *g.count = all;
+  g.slot_row[i] = e >= 0 ? row : -1;
+  if (e < 0) return;
   g.row_slot[row] = i;
-  g.row_gate[row] = gate;
-  g.row_of_token[chunk * 8 + token] = row;
-  if (mine == i) g.expert[chunk] = e, g.first[chunk] = before, g.rows[chunk] = rows;
+  g.row_gate[row] = g.gate[i];
+  if (rank % chunk) return;
+  at += rank / chunk;
+  g.expert[at] = e, g.first[at] = row, g.rows[at] = min(chunk, rows - rank);
 }
 
 // ---------------------------------------------------------------- the tokens' values
@@ -355,19 +340,18 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* x, float (&v)[2][8])
 }
 
 // The tokens' values as operands, 256 threads to a row, and (the last block) the slots by expert;
-// counters set to zero, and with them a row of h's operands that is all zeros, for tokens that a chunk
-// has not.
+// counters set to zero, and with them a row of h's operands that is all zeros, for a single token's bad
+// experts.
 __global__ void __launch_bounds__(1024)
     w4_prepare_kernel(const __nv_bfloat16* x, int T, Rows<kXParts> rows, Rows<kHParts> h, int zero_row,
-                      int* counters, int n_counters, const Groups g, int k, int chunk, int warps,
-                      int* dev_status) {
+                      int* counters, int n_counters, const Groups g, int chunk, int warps, int* dev_status) {
   __shared__ float largest[4][8];
   after_previous();
   let_next_start();  // (which waits for this kernel's end before it reads what is written here)
   const int blocks = g.single ? gridDim.x : gridDim.x - 1;
   if (blockIdx.x == blocks) {
-    if (T <= 8)
-      group_few_slots(g, k, dev_status);
+    if (g.slots <= kFewSlots)
+      group_few_slots(g, chunk, dev_status);
     else
       group_slots(g, chunk, warps, dev_status);
     return;
@@ -614,12 +598,8 @@ struct Product {
       const int skip = at.piece * kPieceTiles;
       const int tile = (expert * strips + strip) * this->tiles + skip;
       const int n = min(kPieceTiles, this->tiles - skip);
-      if (ONE) {
-        const int row = this->p.g.good(at.chunk) ? at.chunk : zero_row;
-        this->issue(tile, n, values.row(row) + skip * (PARTS * kTile * 2), values.info_row(row) + skip);
-      } else {
-        this->issue(tile, n);
-      }
+      const int row = this->p.g.good(at.chunk) ? at.chunk : zero_row;
+      this->issue(tile, n, values.row(row) + skip * (PARTS * kTile * 2), values.info_row(row) + skip);
       at.next();
       if (at.chunk >= chunks) at = start, strip += gridDim.x;
       if (strip < strips) expert = this->p.g.expert_of(at.chunk);  // (wanted at the next call)
@@ -872,14 +852,12 @@ struct Product {
     drain(p, ok, ahead.place, bars, place, parity);
   }
 
-  // All of the block's strips, for up to 8 tokens, whose columns are the same in all chunks: the sums
-  // over a token's experts stay in the products' sums.  Tokens that a chunk has not take `zero_row`.
-  // put(strip, row, token, sum).
+  // All of the block's strips, for a single token: the sums over its experts stay in the products' sums.
+  // A bad expert takes `zero_row`.  put(strip, row, sum).
   template <typename Put>
-  static __device__ __forceinline__ void run_strips(const Problem& p,
-                                                    const Rows<PARTS>& values, int zero_row,
-                                                    uint8_t* shared, Put put) {
-    static_assert(MATS == 1 && NT == 1, "one matrix, 8 tokens");
+  static __device__ __forceinline__ void run_strips(const Problem& p, const Rows<PARTS>& values,
+                                                    int zero_row, uint8_t* shared, Put put) {
+    static_assert(ONE && MATS == 1 && NT == 1, "one strip, one token");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
     uint8_t* ring = shared + warp * kRing;
     float* sums = reinterpret_cast<float*>(shared + warps * kRing);  // [warp][4][32]
@@ -900,49 +878,29 @@ struct Product {
     bool ok = true;
     for (int strip = blockIdx.x; strip < strips; strip += gridDim.x) {
       float acc[1][1][4] = {};
-      Pieces at = start;
-      const auto row_of = [&](int chunk) {
-        const int r = p.g.row_of(chunk, lane / 4);
-        return r < 0 ? zero_row : r;
-      };
-      int row = !ONE && at.chunk < chunks ? row_of(at.chunk) : zero_row;
-      while (at.chunk < chunks && ok) {
-        const uint8_t* from = ring + place * kPlace;
-        const int first = at.piece * kPieceTiles, n = min(tiles - first, kPieceTiles);
-        From x[1];
-        Values now;
-        if (ONE) {
-          x[0].parts = from + kValues + lane % 4 * 32;
-          x[0].info[0] = x[0].info[1] = reinterpret_cast<const float4*>(from + kInfo);
-        } else {
-          x[0].parts = values.row(row) + lane % 4 * 32;
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            x[0].info[i] = values.info_row(__shfl_sync(~0u, row, (lane % 4 * 2 + i) * 4));
-          x[0].advance(first);
-          now.load(x[0], 0);
-        }
-        at.next();
-        if (!ONE && at.chunk < chunks) row = row_of(at.chunk);
+      for (Pieces at = start; at.chunk < chunks && ok; at.next()) {
         if (!wait_for(bars + place, parity)) {
           ok = false;
           break;
         }
         ahead.next();
-        if (ONE) now.load(x[0], 0);
+        const uint8_t* from = ring + place * kPlace;
+        const float4* infos = reinterpret_cast<const float4*>(from + kInfo);
+        From x[1] = {{from + kValues + lane % 4 * 32, {infos, infos}}};
+        Values now;
+        now.load(x[0], 0);
         __syncwarp();
-        piece(from, n, x, 8, now, acc);
+        piece(from, min(tiles - at.piece * kPieceTiles, kPieceTiles), x, 8, now, acc);
         if (++place == kPlaces) place = 0, parity ^= 1;
         __syncwarp();  // the place is read before it is copied into again
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) sums[(warp * 4 + r) * 32 + lane] = acc[0][0][r];
       __syncthreads();
-      if (threadIdx.x < 128) {
+      if (threadIdx.x < 128 && lane % 4 == 0 && warp % 2 == 0) {  // (all columns are the same)
         float sum = 0.f;
         for (int w = 0; w < warps; ++w) sum += sums[w * 128 + threadIdx.x];
-        const int r = threadIdx.x >> 5;
-        put(strip, lane / 4 + r / 2 * 8, lane % 4 * 2 + r % 2, sum);
+        put(strip, lane / 4 + warp / 2 * 8, sum);
       }
       __syncthreads();
     }
@@ -1023,18 +981,16 @@ struct Down {
   Rows<kHParts> h;
   float* out;  // [slots][d], a row to a slot
   __nv_bfloat16* y;
-  int T, zero_row;
+  int zero_row;
 };
 
-// Up to 8 tokens: y at once.
-template <bool ZEROS, int GROUP, bool ONE>
+// A single token: y at once.
+template <bool ZEROS, int GROUP>
 __global__ void __launch_bounds__(kMaxWarps * 32) w4_down_kernel(const Down a) {
-  using Of = Product<true, 1, 1, ZEROS, GROUP, ONE>;
+  using Of = Product<true, 1, 1, ZEROS, GROUP, true>;
   extern __shared__ __align__(16) uint8_t shared[];
-  const int d = a.p.rows;
-  Of::run_strips(a.p, a.h, a.zero_row, shared, [&](int strip, int row, int token, float sum) {
-    if (token < a.T)
-      a.y[static_cast<long long>(token) * d + strip * kStrip + row] = __float2bfloat16_rn(sum);
+  Of::run_strips(a.p, a.h, a.zero_row, shared, [&](int strip, int row, float sum) {
+    a.y[strip * kStrip + row] = __float2bfloat16_rn(sum);
   });
 }
 
@@ -1098,7 +1054,6 @@ int chunk_of(const moe_problem* p) {
   return p->T <= 8 || static_cast<long long>(p->T) * p->k <= 4ll * p->E ? 8 : 32;
 }
 
-
 // Warps to a strip: what takes least time, in pieces, with one more for each strip's beginning and end;
 // the strips are taken in rounds.
 int split_of(long long strips, int pieces, int warps) {
@@ -1140,7 +1095,6 @@ Workspace carve(const moe_problem* p, void* base) {
   w.g.row_slot = reinterpret_cast<int*>(take(slots * 4));
   w.g.row_gate = reinterpret_cast<float*>(take(slots * 4));
   w.g.slot_row = reinterpret_cast<int*>(take(slots * 4));
-  w.g.row_of_token = reinterpret_cast<int*>(take(p->T <= 8 ? chunks * 32 : 0));
   const size_t x_tiles = p->d / kTile, h_tiles = p->F / kTile;
   w.x.tiles = p->d / kTile, w.parts.tiles = p->F / kTile;
   w.x.parts = take(p->T * x_tiles * (kXParts * kTile * 2));
@@ -1150,7 +1104,7 @@ Workspace carve(const moe_problem* p, void* base) {
   w.n_counters = static_cast<int>((p->T == 1 ? slots : chunks) * h_tiles);
   w.counters = reinterpret_cast<int*>(take(w.n_counters * 4));
   w.h = reinterpret_cast<float*>(take(slots * p->F * 4));
-  w.out = reinterpret_cast<float*>(take(p->T <= 8 ? 0 : slots * p->d * 4));
+  w.out = reinterpret_cast<float*>(take(p->T == 1 ? 0 : slots * p->d * 4));
   return w;
 }
 
@@ -1233,11 +1187,10 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
   Groups g = ws.g;
   g.idx = topk_idx, g.gate = topk_gate, g.slots = slots, g.E = p->E, g.single = p->T == 1;
   const int chunks = std::min(p->E, slots);
-  const bool few = p->T <= 8;
   GateUp up{{g, {of(w_gate), of(w_up)}, p->F, p->d, 1, dev_status}, ws.x, ws.h, ws.parts,
             ws.counters, p->k};
   Down down{{g, {of(w_down), {}}, p->d, p->F, 1, dev_status}, ws.parts, ws.out,
-            reinterpret_cast<__nv_bfloat16*>(y), p->T, slots};
+            reinterpret_cast<__nv_bfloat16*>(y), slots};
   cudaError_t err = cudaSuccess;
   const auto launch = [&](auto kernel, int blocks, int warps, int bytes, auto& args) {
     if (err == cudaSuccess)
@@ -1258,9 +1211,9 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
     err = launched(cudaFuncSetAttribute(
         w4_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 32 * kMaxExperts * 2));
     if (err == cudaSuccess)
-      err = launch_behind(w4_prepare_kernel, blocks + !g.single, 1024, few ? 0 : warps * p->E * 2,
+      err = launch_behind(w4_prepare_kernel, blocks + !g.single, 1024, slots <= kFewSlots ? 0 : warps * p->E * 2,
                           stream, reinterpret_cast<const __nv_bfloat16*>(x), p->T, ws.x, ws.parts, slots,
-                          ws.counters, ws.n_counters, g, p->k, chunk, warps, dev_status);
+                          ws.counters, ws.n_counters, g, chunk, warps, dev_status);
   }
   const auto with = [&](auto z, auto of_group) {
     constexpr bool Z = decltype(z)::value;
@@ -1271,24 +1224,18 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
       by_strips(w4_gateup_kernel<4, Z, GROUP>, Product<false, 2, 4, Z, GROUP>{}, up);
     mark_after(MOE_KERNEL_W4_GATEUP, stream);
     mark_before(MOE_KERNEL_W4_DOWN, stream);
-    if (few) {
-      const auto down_of = [&](auto one) {
-        using Of = Product<true, 1, 1, Z, GROUP, decltype(one)::value>;
-        constexpr int kMost = std::min(kMaxWarps, kSharedPerBlock / Of::kWarpBytes);
-        const int strips = p->d / kStrip, warps = strips > kSms ? kWarps : kMost;
-        launch(w4_down_kernel<Z, GROUP, decltype(one)::value>,
-               std::min(strips, 2 * kSms * kWarps / warps), warps, warps * Of::kWarpBytes, down);
-      };
-      if (g.single)
-        down_of(std::true_type{});
-      else
-        down_of(std::false_type{});
+    if (g.single) {
+      using Of = Product<true, 1, 1, Z, GROUP, true>;
+      constexpr int kMost = std::min(kMaxWarps, kSharedPerBlock / Of::kWarpBytes);
+      const int strips = p->d / kStrip, warps = strips > kSms ? kWarps : kMost;
+      launch(w4_down_kernel<Z, GROUP>, std::min(strips, 2 * kSms * kWarps / warps), warps,
+             warps * Of::kWarpBytes, down);
     } else if (chunk == 8) {
       by_strips(w4_down_rows_kernel<2, 1, Z, GROUP>, Product<true, 2, 1, Z, GROUP>{}, down);
     } else {
       by_strips(w4_down_rows_kernel<1, 4, Z, GROUP>, Product<true, 1, 4, Z, GROUP>{}, down);
     }
-    if (!few && err == cudaSuccess)
+    if (!g.single && err == cudaSuccess)
       err = launch_behind(w4_combine_kernel, dim3(p->T, std::min(64, (p->d + 511) / 512)), 128, 0,
                           stream, ws.g.slot_row, ws.out, p->d, p->k, down.y);
   };
@@ -1305,7 +1252,7 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
   else
     with_group(std::false_type{});
   mark_after(MOE_KERNEL_W4_DOWN, stream);
-  count_launches(3 + !few);
+  count_launches(3 + !g.single);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
