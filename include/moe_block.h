@@ -147,8 +147,9 @@ int moe_block_norm(const moe_block_in* in, void* z, int64_t ld_z, void* n, int64
 /* Backward: gradients of <dz, z> + <dn, n>.  `in` as the forward read it: z is formed again from
  * it.  dz, dx of type stream_dtype; dn of type dn_dtype (MOE_F32, as layers' backward passes write
  * it, or dtype); dy of type dtype.  dz or dn may be NULL (zero).  dy, dgate, dw_post and dw_pre
- * may each be NULL (not wanted); dgate is shaped and typed as gate.  Without dn, dw_pre is zero.  dx may
- * be dz, dy may be y or dn of the same type, a gate's [N, D] gradient may be the gate (each with the same strides).
+ * may each be NULL (not wanted); dgate is shaped and typed as gate.  Without dn, dw_pre is zero.
+ * dx may be dz, dy may be y or dn of the same type, a gate's [N, D] gradient may be the gate (each
+ * with the same strides).
  * Workspace: for dw_post, dw_pre and the gradient of a gate [D] (else it may be NULL), 16-byte
  * aligned; its size is 0 for sizes that are not supported. */
 typedef struct moe_block_grads {
@@ -191,8 +192,8 @@ int moe_block_norm_backward(const moe_block_in* in, const moe_block_grads* grads
  * of topk_idx outside [0, E) are reported as MOE_ERR_BAD_INDEX in *dev_status (may be NULL) and
  * contribute nothing; a token may name an expert twice.
  * Supported (else MOE_ERR_UNSUPPORTED): p as everywhere (d and F multiples of 64, and up to 2^20
- * here; a matrix of up to 2^40 weights), T * k up to 16384; group 32, 64 or 128, a divisor of d and of F; group and has_zeros the
- * same for all three; packed arrays, x, y and the workspace 16-byte aligned.
+ * here; a matrix of up to 2^40 weights), T * k up to 16384; group 32, 64 or 128, a divisor of d and
+ * of F; group and has_zeros the same for all three; packed arrays, x, y and the workspace 16-byte aligned.
  *
  * moe_w4_pack lays weights [E, rows, cols] out for it, once (cols: what a product sums over).
  * codes [E, rows, cols / 2]: two codes to a byte, the lower four bits first; scales

@@ -255,8 +255,8 @@ def test_w4_most_slots():
 
 @pytest.mark.parametrize("T", [1, 5, 20, 100])
 def test_w4_values_of_all_sizes(T):
-    """Rows of zeros, of the smallest and of the largest values, and single large ones among small; a row
-    with a value that is not finite leaves the others as they are."""
+    """Rows of zeros, of small values and of all sizes, and single large ones among small; a row with a
+    value that is not finite leaves the others as they are."""
     case = (T, 256, 6, 2, 128, 64, True, None)
     w, x, idx, gate = w4_case(case)
     for t in range(T):

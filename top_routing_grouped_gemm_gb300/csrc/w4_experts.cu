@@ -477,10 +477,11 @@ struct Tasks {
 };
 
 // MATS strips of weights with NT x 8 tokens at most; ZEROS: zeros are given; GROUP columns to a scale.
-// Gate and up take x, whose rows have one factor, and a strip of each.  DOWN takes h, which has a factor
-// for each tile, and one strip or two neighbouring ones (which share the loads of h and wait for them
-// half as often: 32 tokens, 2048 x 512: 170 -> 158 us).  ONE: a single token, whose values come with the weights' pieces and stand in
-// all columns.  (Read from the L2 by each lane, a tile ahead, they were what down waited for.)
+// Gate and up take x, whose rows have one factor, and a strip of each.  DOWN takes h, which has a
+// factor for each tile, and one strip or two neighbouring ones (which share the loads of h and wait for
+// them half as often: 32 tokens, 2048 x 512: 170 -> 158 us).  ONE: a single token, whose values come
+// with the weights' pieces and stand in all columns.  (Read from the L2 by each lane, a tile ahead, they
+// were what down waited for: 34 -> 30 us.)
 template <bool DOWN, int MATS, int NT, bool ZEROS, int GROUP, bool ONE = false>
 struct Product {
   static constexpr bool kFactors = DOWN, FINE = GROUP == 32;
@@ -552,7 +553,7 @@ struct Product {
     }
     __device__ __forceinline__ void begin() {
       if (at.chunk >= chunks) return;
-      tile = (this->p.g.expert_of(at.chunk) * at.strips + at.strip) * (kRows / kStrip * this->tiles) + skip;
+      tile = (this->p.g.expert_of(at.chunk) * at.strips + at.strip) * (kRows / kStrip) * this->tiles + skip;
       left = this->tiles - skip;
     }
     __device__ __forceinline__ void next() {
@@ -672,9 +673,9 @@ struct Product {
   };
 
   // acc += s (part - z sum), for what `part` and `sum` have of a group's columns.
-  static __device__ __forceinline__ void add(const uint8_t* scales, int group, const float (&part)[PARTS][4],
-                                             const float (&factor)[2], const float (&sum)[2],
-                                             float (&acc)[4]) {
+  static __device__ __forceinline__ void add(const uint8_t* scales, int group,
+                                             const float (&part)[PARTS][4], const float (&factor)[2],
+                                             const float (&sum)[2], float (&acc)[4]) {
     Scale s;
     s.load(reinterpret_cast<const uint32_t*>(scales + group * (32 * kWords)) +
            (threadIdx.x & 31) / 4 * kWords);
@@ -761,7 +762,8 @@ struct Product {
         tiles_of<4>(from, u, x, rows, u + 4 < kPieceTiles, now, acc);
     } else {
 #pragma unroll 1
-      for (int u = 0; u < n; u += kTogether) tiles_of<kTogether>(from, u, x, rows, u + kTogether < n, now, acc);
+      for (int u = 0; u < n; u += kTogether)
+        tiles_of<kTogether>(from, u, x, rows, u + kTogether < n, now, acc);
     }
   }
 
@@ -930,7 +932,8 @@ struct GateUp {
 
 // h goes to memory in fp32; the warp that brings the last of a tile's four strips makes operands of it.
 template <int NT, bool ZEROS, int GROUP>
-__global__ void __launch_bounds__(kWarps * 32, Product<false, 2, NT, ZEROS, GROUP>::kBlocks) w4_gateup_kernel(const GateUp a) {
+__global__ void __launch_bounds__(kWarps * 32, Product<false, 2, NT, ZEROS, GROUP>::kBlocks)
+    w4_gateup_kernel(const GateUp a) {
   using Of = Product<false, 2, NT, ZEROS, GROUP>;
   extern __shared__ __align__(16) uint8_t shared[];
   const int F = a.p.rows, lane = threadIdx.x & 31;
@@ -954,7 +957,8 @@ __global__ void __launch_bounds__(kWarps * 32, Product<false, 2, NT, ZEROS, GROU
         __threadfence();
         __syncwarp();
         int before = 0;
-        if (lane == 0) before = atomicAdd(a.counters + static_cast<long long>(chunk) * (F / kTile) + tile, 1);
+        if (lane == 0)
+          before = atomicAdd(a.counters + static_cast<long long>(chunk) * (F / kTile) + tile, 1);
         if (__shfl_sync(~0u, before, 0) != 3) return;
         __threadfence();
         for (int r0 = 0; r0 < rows; r0 += 8) {
@@ -1173,8 +1177,8 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
   if (int e = check_weights(w_up, p->d)) return e;
   if (int e = check_weights(w_down, p->F)) return e;
   const bool zeros = w_gate->has_zeros != 0;
-  if (w_gate->group != w_up->group || w_gate->group != w_down->group || zeros != (w_up->has_zeros != 0) ||
-      zeros != (w_down->has_zeros != 0))
+  if (w_gate->group != w_up->group || w_gate->group != w_down->group ||
+      zeros != (w_up->has_zeros != 0) || zeros != (w_down->has_zeros != 0))
     return MOE_ERR_UNSUPPORTED;
   if (misaligned(x, 16) || misaligned(y, 16) || misaligned(topk_idx, 4) ||
       misaligned(topk_gate, 4) || misaligned(dev_status, 4))
@@ -1201,7 +1205,8 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
     using Of = decltype(product);
     const int blocks = std::min(Of::kBlocks, kSharedPerSm / (Of::kBytes + 1024)) * kSms;
     args.p.split = split_of(chunks * static_cast<long long>(args.p.rows / Of::kRows),
-                            (args.p.cols / kTile + Of::kPieceTiles - 1) / Of::kPieceTiles, blocks * kWarps);
+                            (args.p.cols / kTile + Of::kPieceTiles - 1) / Of::kPieceTiles,
+                            blocks * kWarps);
     launch(kernel, blocks, kWarps, Of::kBytes, args);
   };
   mark_before(MOE_KERNEL_W4_GATEUP, stream);
@@ -1211,9 +1216,9 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
     err = launched(cudaFuncSetAttribute(
         w4_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 32 * kMaxExperts * 2));
     if (err == cudaSuccess)
-      err = launch_behind(w4_prepare_kernel, blocks + !g.single, 1024, slots <= kFewSlots ? 0 : warps * p->E * 2,
-                          stream, reinterpret_cast<const __nv_bfloat16*>(x), p->T, ws.x, ws.parts, slots,
-                          ws.counters, ws.n_counters, g, chunk, warps, dev_status);
+      err = launch_behind(w4_prepare_kernel, blocks + !g.single, 1024,
+                          slots <= kFewSlots ? 0 : warps * p->E * 2, stream,
+                          reinterpret_cast<const __nv_bfloat16*>(x), p->T, ws.x, ws.parts, slots, ws.counters, ws.n_counters, g, chunk, warps, dev_status);
   }
   const auto with = [&](auto z, auto of_group) {
     constexpr bool Z = decltype(z)::value;
