@@ -294,6 +294,9 @@ NORMS = [
     (1300, 1024, BF, BF, "token", True, True, True, True, "columns"),
     (7, 4104, F32, BF, "channel", True, True, True, True, "dense"),
     (6, 8192, BF, BF, "token", True, True, True, True, "dense"),
+    (300, 5000, F32, BF, "value", True, True, True, True, "columns"),
+    (310, 6144, BF, BF, "channel", True, True, True, True, "dense"),
+    (2, 6152, F32, F32, "token", True, True, True, True, "dense"),
     (3, 8200, F32, F32, "value", True, True, True, True, "dense"),
     (5, 16384, F32, BF, "channel", True, True, True, True, "columns"),
     (400, 4096, F32, BF, "token", True, True, True, True, "shared"),
