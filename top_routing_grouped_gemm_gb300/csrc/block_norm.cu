@@ -74,7 +74,14 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[V]) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + expf(-v)); }
+// 1 / (1 + exp(-v)): the hardware's reciprocal and one step of Newton's, which leaves the last rounding
+// (and no branch, which a division has for what does not occur here).
+__device__ __forceinline__ float sigmoid(float v) {
+  const float x = 1.f + expf(-v);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return x < 1e38f ? fmaf(r, fmaf(-x, r, 1.f), r) : r;  // (infinite: 0)
+}
 
 // A row is held by WARPS warps, C pieces of V values to a lane: piece c of thread i has values
 // (c * 32 * WARPS + i) * V on.  Rows of up to 512 values take one warp.
