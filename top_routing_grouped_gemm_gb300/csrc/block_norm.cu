@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(Lanes<WARPS, C, V, FULL>::kThreads,
 //   dy  = (a p dz' - y^ mean(a p dz' y^)) / rms(y), or a p dz'
 // and with Q = sum over rows of a dz' y^, what the gradients of w_post and of a gate [D] are made of
 // (scale a Q and scale w_post a' Q), and sum(p dz' y^) the gradient of a gate [N] before a'.  The sums
-// over rows stay in registers over all rows of a block.  8192 x 4096 as above 132 us (604 MB: 89).
+// over rows stay in registers over all rows of a block.  8192 x 4096 as above 127 us (604 MB: 89).
 template <typename S, typename T, typename G, int WARPS, int C, int V, bool FULL>
 __global__ void __launch_bounds__(Lanes<WARPS, C, V, FULL>::kThreads,
                                   Lanes<WARPS, C, V, FULL>::kThreads > 256 ? 1 : 2)
