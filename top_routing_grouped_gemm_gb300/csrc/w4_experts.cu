@@ -14,7 +14,7 @@
 //
 // Now it is 56 for gate and up, 80 for down, whose operand has two parts.  One token through 16 of 896
 // experts of 4096 x 1024 takes 30 us (104 MB, 15 us of reading), 64 tokens that crowd on few experts
-// 503 us (358), 32 tokens through experts of 2048 x 512 with zeros 158 us (97): warps are issuing half of
+// 496 us (358), 32 tokens through experts of 2048 x 512 with zeros 158 us (97): warps are issuing half of
 // the time, in turn with what they wait for.
 #include <cuda_fp16.h>
 #include <math.h>
@@ -36,6 +36,11 @@ constexpr int kTile = 64;        // weights of a row that a lane's 16 bytes are 
 constexpr int kMaxSlots = 16384;
 constexpr int kMaxWidth = 1 << 20;
 constexpr int kMaxExperts = 1024;
+// Rows of an expert that its weights are read once for; more of them are taken in several chunks.  (Where
+// experts have many rows the second reading is of the L2: 32 rows to a chunk, with as many values to
+// wait for as a lane then has, took 160 us instead of 94 for 16 tokens x 8 of 64 experts, 4096 x 1024,
+// 252 instead of 138 for 64 and 4153 instead of 2654 for 2048.)
+constexpr int kChunk = 8;
 constexpr int kXParts = 1, kHParts = 2;  // fp16 values for one of x, of h
 constexpr int kWarps = 8, kMaxWarps = 16;  // to a block
 constexpr int kSharedPerSm = 228 * 1024, kSharedPerBlock = 227 * 1024;
@@ -89,13 +94,13 @@ __global__ void w4_pack_scales_kernel(int groups, long long entries, const __nv_
 }
 
 // ---------------------------------------------------------------- the slots by expert
-// Chunks of at most `chunk` rows of one expert; a row is a slot, in the slots' order within an expert.
+// Chunks of at most kChunk rows of one expert; a row is a slot, in the slots' order within an expert.
 struct Groups {
   const int* idx;  // [slots] the slots' experts; a single token's slots are chunks as they are
   const float* gate;
   int slots, E, single;
   int* count;     // [1] chunks
-  int* expert;    // [E + slots / chunk]
+  int* expert;    // [E + slots / kChunk]
   int* first;     // [...] its first row
   int* rows;      // [...] how many
   int* row_slot;  // [slots]
@@ -140,7 +145,7 @@ __device__ __forceinline__ int block_scan(int v, int* sums) {  // exclusive, 102
 }
 
 // One block of 1024.  The first `warps` of its warps have a part of the slots each, 32 at a time.
-__device__ void group_slots(const Groups& g, int chunk, int warps, int* dev_status) {
+__device__ void group_slots(const Groups& g, int warps, int* dev_status) {
   extern __shared__ unsigned short seen[];  // [warps][E]: slots of the expert in the warp's part
   __shared__ int sums[32], start[kMaxExperts];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = g.E;
@@ -173,14 +178,14 @@ __device__ void group_slots(const Groups& g, int chunk, int warps, int* dev_stat
       seen[w * E + e] = all;
       all += n;
     }
-  const int chunks = (all + chunk - 1) / chunk;
+  const int chunks = (all + kChunk - 1) / kChunk;
   const int both = block_scan(all | chunks << 16, sums);  // (each up to 16384)
   const int row = both & 0xffff, at = both >> 16;
   if (threadIdx.x == 1023) *g.count = at + chunks;
   for (int c = 0; c < chunks; ++c) {
     g.expert[at + c] = e;
-    g.first[at + c] = row + c * chunk;
-    g.rows[at + c] = min(chunk, all - c * chunk);
+    g.first[at + c] = row + c * kChunk;
+    g.rows[at + c] = min(kChunk, all - c * kChunk);
   }
   if (e < E) start[e] = row;
   __syncthreads();
@@ -197,7 +202,7 @@ __device__ void group_slots(const Groups& g, int chunk, int warps, int* dev_stat
 // ten (7 tokens x 4 of 64 experts, 512 x 256: 17.1 -> 15.7 us).  Experts in the order of their first
 // slots.  One block of 1024.
 constexpr int kFewSlots = 256;
-__device__ void group_few_slots(const Groups& g, int chunk, int* dev_status) {
+__device__ void group_few_slots(const Groups& g, int* dev_status) {
   __shared__ __align__(16) int expert[kFewSlots], rows_of[kFewSlots];  // (of an expert's first slots)
   const int i = threadIdx.x, slots = g.slots;
   int e = -1;
@@ -231,7 +236,7 @@ __device__ void group_few_slots(const Groups& g, int chunk, int* dev_status) {
     const int others[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const int chunks = (others[c] + chunk - 1) / chunk;
+      const int chunks = (others[c] + kChunk - 1) / kChunk;
       all += chunks;
       if (j + c < first) row += others[c], at += chunks;
     }
@@ -241,9 +246,9 @@ __device__ void group_few_slots(const Groups& g, int chunk, int* dev_status) {
   if (e < 0) return;
   g.row_slot[row] = i;
   g.row_gate[row] = g.gate[i];
-  if (rank % chunk) return;
-  at += rank / chunk;
-  g.expert[at] = e, g.first[at] = row, g.rows[at] = min(chunk, rows - rank);
+  if (rank % kChunk) return;
+  at += rank / kChunk;
+  g.expert[at] = e, g.first[at] = row, g.rows[at] = min(kChunk, rows - rank);
 }
 
 // ---------------------------------------------------------------- the tokens' values
@@ -344,16 +349,16 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* x, float (&v)[2][8])
 // experts.
 __global__ void __launch_bounds__(1024)
     w4_prepare_kernel(const __nv_bfloat16* x, int T, Rows<kXParts> rows, Rows<kHParts> h, int zero_row,
-                      int* counters, int n_counters, const Groups g, int chunk, int warps, int* dev_status) {
+                      int* counters, int n_counters, const Groups g, int warps, int* dev_status) {
   __shared__ float largest[4][8];
   after_previous();
   let_next_start();  // (which waits for this kernel's end before it reads what is written here)
   const int blocks = g.single ? gridDim.x : gridDim.x - 1;
   if (blockIdx.x == blocks) {
     if (g.slots <= kFewSlots)
-      group_few_slots(g, chunk, dev_status);
+      group_few_slots(g, dev_status);
     else
-      group_slots(g, chunk, warps, dev_status);
+      group_slots(g, warps, dev_status);
     return;
   }
   const int me = blockIdx.x * 1024 + threadIdx.x, all = blocks * 1024;
@@ -476,13 +481,13 @@ struct Tasks {
   }
 };
 
-// MATS strips of weights with NT x 8 tokens at most; ZEROS: zeros are given; GROUP columns to a scale.
+// MATS strips of weights with 8 tokens at most; ZEROS: zeros are given; GROUP columns to a scale.
 // Gate and up take x, whose rows have one factor, and a strip of each.  DOWN takes h, which has a
 // factor for each tile, and one strip or two neighbouring ones (which share the loads of h and wait for
 // them half as often: 32 tokens, 2048 x 512: 170 -> 158 us).  ONE: a single token, whose values come
 // with the weights' pieces and stand in all columns.  (Read from the L2 by each lane, a tile ahead, they
 // were what down waited for: 34 -> 30 us.)
-template <bool DOWN, int MATS, int NT, bool ZEROS, int GROUP, bool ONE = false>
+template <bool DOWN, int MATS, bool ZEROS, int GROUP, bool ONE = false>
 struct Product {
   static constexpr bool kFactors = DOWN, FINE = GROUP == 32;
   static constexpr int PARTS = DOWN ? kHParts : kXParts;
@@ -494,17 +499,17 @@ struct Product {
   static constexpr int kValues = kCodes + of_scales(kPieceTiles);  // where ONE's values are in a place
   static constexpr int kInfo = kValues + kPieceTiles * (PARTS * kTile * 2);
   static constexpr int kPlace = ONE ? kInfo + kPieceTiles * 16 : kValues;
-  static constexpr int kSums = MATS * NT * 4;  // to a lane
+  static constexpr int kSums = MATS * 4;  // to a lane
   static constexpr int with_places(int n) { return n * MATS * kPlace + kSums * 128 + 32; }
   static constexpr int kBlocks = 2;  // to an SM
   // Of the ring, one less of them on their way: three for the shorter pieces of gate and up, if two
   // blocks still fit (with one, 32 tokens with zeros and groups of 64 took 81 us there instead of 66).
   static constexpr int kPlaces =
-      MATS == 2 && NT == 1 && kBlocks * (kWarps * with_places(3) + 1024) <= kSharedPerSm ? 3 : 2;
+      MATS == 2 && kBlocks * (kWarps * with_places(3) + 1024) <= kSharedPerSm ? 3 : 2;
   static constexpr int kRing = kPlaces * MATS * kPlace;
   static constexpr int kWarpBytes = with_places(kPlaces), kBytes = kWarps * kWarpBytes;
   // Tiles that one scale is multiplied with at once: two where their sums can wait for it.
-  static constexpr int kTogether = GROUP == 128 && !kFactors && NT == 1 ? 2 : 1;
+  static constexpr int kTogether = GROUP == 128 && !kFactors ? 2 : 1;
 
   // Issues the copies of pieces; all of a warp's lanes know where it stands, one issues them.
   struct Copies {
@@ -715,13 +720,11 @@ struct Product {
       before[0] = sum[0], before[1] = sum[1];
   }
 
-  // N tiles of a piece from its tile u0 on, for which x stands at the values.  Of a single eight of
-  // tokens, `now` has the values of the first one, and is left with those of the tile after the last if
-  // there is `more` to come.
+  // N tiles of a piece from its tile u0 on, for which x stands at the values.  `now` has those of the
+  // first one, and is left with those of the tile after the last if there is `more` to come.
   template <int N>
-  static __device__ __forceinline__ void tiles_of(const uint8_t* from, int u0, From (&x)[NT], int rows,
-                                                  bool more, Values& now,
-                                                  float (&acc)[MATS][NT][4]) {
+  static __device__ __forceinline__ void tiles_of(const uint8_t* from, int u0, From& x, bool more,
+                                                  Values& now, float (&acc)[MATS][4]) {
     static_assert(N % kTogether == 0, "whole groups");
     float part[MATS][PARTS][4], before[2];
 #pragma unroll
@@ -730,47 +733,35 @@ struct Product {
       Operands w[MATS];
 #pragma unroll
       for (int i = 0; i < MATS; ++i) w[i].load(from + i * kPlace + u * 512);
-      if (NT == 1) {
-        const Values mine = now;
-        if (k + 1 < N || more) now.load(x[0], k + 1);
+      const Values mine = now;
+      if (k + 1 < N || more) now.load(x, k + 1);
 #pragma unroll
-        for (int i = 0; i < MATS; ++i) {
-          float sums[2] = {before[0], before[1]};
-          multiply(w[i], mine, from + i * kPlace + kCodes, u, k % kTogether, part[i], sums, acc[i][0]);
-          if (i + 1 == MATS) before[0] = sums[0], before[1] = sums[1];
-        }
-      } else {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          if (n * 8 < rows) {
-            now.load(x[n], k);
-#pragma unroll
-            for (int i = 0; i < MATS; ++i)
-              multiply(w[i], now, from + i * kPlace + kCodes, u, 0, part[i], before, acc[i][n]);
-          }
+      for (int i = 0; i < MATS; ++i) {
+        float sums[2] = {before[0], before[1]};
+        multiply(w[i], mine, from + i * kPlace + kCodes, u, k % kTogether, part[i], sums, acc[i]);
+        if (i + 1 == MATS) before[0] = sums[0], before[1] = sums[1];
       }
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) x[n].advance(N);
+    x.advance(N);
   }
-  // The n tiles of a piece, for which x stands at the values.
-  static __device__ __forceinline__ void piece(const uint8_t* from, int n, From (&x)[NT], int rows,
-                                               Values& now, float (&acc)[MATS][NT][4]) {
+  // The n tiles of a piece, for which x stands at the values and `now` has those of the first.
+  static __device__ __forceinline__ void piece(const uint8_t* from, int n, From& x, Values& now,
+                                               float (&acc)[MATS][4]) {
     if (n == kPieceTiles) {
 #pragma unroll 1
       for (int u = 0; u < kPieceTiles; u += 4)
-        tiles_of<4>(from, u, x, rows, u + 4 < kPieceTiles, now, acc);
+        tiles_of<4>(from, u, x, u + 4 < kPieceTiles, now, acc);
     } else {
 #pragma unroll 1
       for (int u = 0; u < n; u += kTogether)
-        tiles_of<kTogether>(from, u, x, rows, u + kTogether < n, now, acc);
+        tiles_of<kTogether>(from, u, x, u + kTogether < n, now, acc);
     }
   }
 
-  // All of the warp's strips.  value_row(r) is the row of x of a chunk's row r; put(chunk,
-  // first, rows, strip, sums) gets the sums: places (n, r) of a lane are row lane / 4 + r / 2 * 8 of the
-  // strip, token 8 n + lane % 4 * 2 + r % 2 of the chunk.  (Columns of tokens that there are not repeat
-  // the first one's; a product's columns have nothing to do with each other.)
+  // All of the warp's strips.  value_row(r) is the row of x of a chunk's row r; put(chunk, first, rows,
+  // strip, sums) gets the sums: place r of a lane is row lane / 4 + r / 2 * 8 of the strip, token
+  // lane % 4 * 2 + r % 2 of the chunk.  (Columns of tokens that there are not repeat the first one's; a
+  // product's columns have nothing to do with each other.)
   template <typename RowOf, typename Put>
   static __device__ __forceinline__ void run(const Problem& p, const Rows<PARTS>& values,
                                              uint8_t* shared, RowOf value_row, Put put) {
@@ -797,33 +788,22 @@ struct Product {
     bool ok = true;
     for (; task.chunk < chunks; task.next()) {
       const int first = p.g.first_of(task.chunk), rows = p.g.rows_of(task.chunk);
-      From x[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const auto row = [&](int token) {
-          return value_row(first + (n * 8 + token < rows ? n * 8 + token : 0));
-        };
-        x[n].parts = values.row(row(lane / 4)) + lane % 4 * 32;
-        x[n].info[0] = values.info_row(row(lane % 4 * 2));
-        x[n].info[1] = values.info_row(row(lane % 4 * 2 + 1));
-      }
-      float acc[MATS][NT][4] = {};
-#pragma unroll
-      for (int n = 0; n < NT; ++n) x[n].advance(me * kPieceTiles);
+      const auto row = [&](int token) { return value_row(first + (token < rows ? token : 0)); };
+      From x{values.row(row(lane / 4)) + lane % 4 * 32,
+             {values.info_row(row(lane % 4 * 2)), values.info_row(row(lane % 4 * 2 + 1))}};
+      float acc[MATS][4] = {};
+      x.advance(me * kPieceTiles);
       for (int left = tiles - me * kPieceTiles; left > 0 && ok; left -= split * kPieceTiles) {
         Values now;
-        if (NT == 1) now.load(x[0], 0);
+        now.load(x, 0);
         if (!wait_for(bars + place, parity)) {
           ok = false;
           break;
         }
         ahead.next();
         __syncwarp();
-        piece(ring + place * (MATS * kPlace), min(left, kPieceTiles), x, rows, now, acc);
-        if (split > 1) {  // (past the others' pieces; not read behind the end)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) x[n].advance((split - 1) * kPieceTiles);
-        }
+        piece(ring + place * (MATS * kPlace), min(left, kPieceTiles), x, now, acc);
+        if (split > 1) x.advance((split - 1) * kPieceTiles);  // (not read behind the end)
         if (++place == kPlaces) place = 0, parity ^= 1;
         __syncwarp();  // the place is read before it is copied into again
       }
@@ -833,20 +813,14 @@ struct Product {
         };
         if (me)
 #pragma unroll
-          for (int i = 0; i < MATS * NT; ++i)
-            if (i % NT * 8 < rows)
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                sums[(warp * kSums + i * 4 + r) * 32 + lane] = acc[i / NT][i % NT][r];
+          for (int i = 0; i < kSums; ++i)
+            sums[(warp * kSums + i) * 32 + lane] = acc[i / 4][i % 4];
         sync();
         if (!me)
 #pragma unroll
-          for (int i = 0; i < MATS * NT; ++i)
-            if (i % NT * 8 < rows)
-              for (int o = 1; o < split; ++o)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  acc[i / NT][i % NT][r] += sums[((warp + o) * kSums + i * 4 + r) * 32 + lane];
+          for (int i = 0; i < kSums; ++i)
+            for (int o = 1; o < split; ++o)
+              acc[i / 4][i % 4] += sums[((warp + o) * kSums + i) * 32 + lane];
         sync();
       }
       if (!me) put(task.chunk, first, rows, task.strip, acc);
@@ -859,7 +833,7 @@ struct Product {
   template <typename Put>
   static __device__ __forceinline__ void run_strips(const Problem& p, const Rows<PARTS>& values,
                                                     int zero_row, uint8_t* shared, Put put) {
-    static_assert(ONE && MATS == 1 && NT == 1, "one strip, one token");
+    static_assert(ONE && MATS == 1, "one strip, one token");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
     uint8_t* ring = shared + warp * kRing;
     float* sums = reinterpret_cast<float*>(shared + warps * kRing);  // [warp][4][32]
@@ -879,7 +853,7 @@ struct Product {
     uint32_t parity = 0;
     bool ok = true;
     for (int strip = blockIdx.x; strip < strips; strip += gridDim.x) {
-      float acc[1][1][4] = {};
+      float acc[1][4] = {};
       for (Pieces at = start; at.chunk < chunks && ok; at.next()) {
         if (!wait_for(bars + place, parity)) {
           ok = false;
@@ -888,16 +862,16 @@ struct Product {
         ahead.next();
         const uint8_t* from = ring + place * kPlace;
         const float4* infos = reinterpret_cast<const float4*>(from + kInfo);
-        From x[1] = {{from + kValues + lane % 4 * 32, {infos, infos}}};
+        From x{from + kValues + lane % 4 * 32, {infos, infos}};
         Values now;
-        now.load(x[0], 0);
+        now.load(x, 0);
         __syncwarp();
-        piece(from, min(tiles - at.piece * kPieceTiles, kPieceTiles), x, 8, now, acc);
+        piece(from, min(tiles - at.piece * kPieceTiles, kPieceTiles), x, now, acc);
         if (++place == kPlaces) place = 0, parity ^= 1;
         __syncwarp();  // the place is read before it is copied into again
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) sums[(warp * 4 + r) * 32 + lane] = acc[0][0][r];
+      for (int r = 0; r < 4; ++r) sums[(warp * 4 + r) * 32 + lane] = acc[0][r];
       __syncthreads();
       if (threadIdx.x < 128 && lane % 4 == 0 && warp % 2 == 0) {  // (all columns are the same)
         float sum = 0.f;
@@ -931,28 +905,26 @@ struct GateUp {
 };
 
 // h goes to memory in fp32; the warp that brings the last of a tile's four strips makes operands of it.
-template <int NT, bool ZEROS, int GROUP>
-__global__ void __launch_bounds__(kWarps * 32, Product<false, 2, NT, ZEROS, GROUP>::kBlocks)
+template <bool ZEROS, int GROUP>
+__global__ void __launch_bounds__(kWarps * 32, Product<false, 2, ZEROS, GROUP>::kBlocks)
     w4_gateup_kernel(const GateUp a) {
-  using Of = Product<false, 2, NT, ZEROS, GROUP>;
+  using Of = Product<false, 2, ZEROS, GROUP>;
   extern __shared__ __align__(16) uint8_t shared[];
   const int F = a.p.rows, lane = threadIdx.x & 31;
   Of::run(
       a.p, a.x, shared, [&](int r) { return a.p.g.slot_of(r) / a.k; },
-      [&](int chunk, int first, int rows, int strip, const float (&acc)[2][NT][4]) {
+      [&](int chunk, int first, int rows, int strip, const float (&acc)[2][4]) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int token = n * 8 + lane % 4 * 2 + r % 2;
-            if (token >= rows) continue;
-            // (a factor of the whole row of x)
-            const float f = a.x.info_row(a.p.g.slot_of(first + token) / a.k)->x;
-            const float v = f * acc[0][n][r];
-            const float h = a.p.g.gate_of(first + token) * (v / (1.f + expf(-v)) * (f * acc[1][n][r]));
-            __stcg(a.h + (first + token) * static_cast<long long>(F) + strip * kStrip + lane / 4 +
-                       r / 2 * 8, h);
-          }
+        for (int r = 0; r < 4; ++r) {
+          const int token = lane % 4 * 2 + r % 2;
+          if (token >= rows) continue;
+          // (a factor of the whole row of x)
+          const float f = a.x.info_row(a.p.g.slot_of(first + token) / a.k)->x;
+          const float v = f * acc[0][r];
+          const float h = a.p.g.gate_of(first + token) * (v / (1.f + expf(-v)) * (f * acc[1][r]));
+          __stcg(a.h + (first + token) * static_cast<long long>(F) + strip * kStrip + lane / 4 +
+                     r / 2 * 8, h);
+        }
         const int tile = strip / 4;
         __threadfence();
         __syncwarp();
@@ -961,22 +933,20 @@ __global__ void __launch_bounds__(kWarps * 32, Product<false, 2, NT, ZEROS, GROU
           before = atomicAdd(a.counters + static_cast<long long>(chunk) * (F / kTile) + tile, 1);
         if (__shfl_sync(~0u, before, 0) != 3) return;
         __threadfence();
-        for (int r0 = 0; r0 < rows; r0 += 8) {
-          const int r = first + min(r0 + lane / 4, rows - 1);  // (the last one again)
-          float v[2][8];
+        const int r = first + min(lane / 4, rows - 1);  // (the last one again)
+        float v[2][8];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-              const float4 q = __ldcg(reinterpret_cast<const float4*>(
-                  a.h + r * static_cast<long long>(F) + tile * kTile + c * 32 + lane % 4 * 8 + j));
-              v[c][j] = q.x, v[c][j + 1] = q.y, v[c][j + 2] = q.z, v[c][j + 3] = q.w;
-            }
-          float most = Rows<kHParts>::largest(v);
-          most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
-          most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
-          a.parts.write(r, tile, v, most, false);
-        }
+          for (int j = 0; j < 8; j += 4) {
+            const float4 q = __ldcg(reinterpret_cast<const float4*>(
+                a.h + r * static_cast<long long>(F) + tile * kTile + c * 32 + lane % 4 * 8 + j));
+            v[c][j] = q.x, v[c][j + 1] = q.y, v[c][j + 2] = q.z, v[c][j + 3] = q.w;
+          }
+        float most = Rows<kHParts>::largest(v);
+        most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
+        a.parts.write(r, tile, v, most, false);
       });
 }
 
@@ -991,7 +961,7 @@ struct Down {
 // A single token: y at once.
 template <bool ZEROS, int GROUP>
 __global__ void __launch_bounds__(kMaxWarps * 32) w4_down_kernel(const Down a) {
-  using Of = Product<true, 1, 1, ZEROS, GROUP, true>;
+  using Of = Product<true, 1, ZEROS, GROUP, true>;
   extern __shared__ __align__(16) uint8_t shared[];
   Of::run_strips(a.p, a.h, a.zero_row, shared, [&](int strip, int row, float sum) {
     a.y[strip * kStrip + row] = __float2bfloat16_rn(sum);
@@ -999,26 +969,24 @@ __global__ void __launch_bounds__(kMaxWarps * 32) w4_down_kernel(const Down a) {
 }
 
 // More tokens: the rows' parts of it, which w4_combine_kernel adds.
-template <int MATS, int NT, bool ZEROS, int GROUP>
-__global__ void __launch_bounds__(kWarps * 32, Product<true, MATS, NT, ZEROS, GROUP>::kBlocks)
+template <bool ZEROS, int GROUP>
+__global__ void __launch_bounds__(kWarps * 32, Product<true, 2, ZEROS, GROUP>::kBlocks)
     w4_down_rows_kernel(const Down a) {
-  using Of = Product<true, MATS, NT, ZEROS, GROUP>;
   extern __shared__ __align__(16) uint8_t shared[];
   const int d = a.p.rows, lane = threadIdx.x & 31;
-  Of::run(a.p, a.h, shared, [&](int r) { return r; },
-          [&](int, int first, int rows, int strip, const float (&acc)[MATS][NT][4]) {
+  Product<true, 2, ZEROS, GROUP>::run(
+      a.p, a.h, shared, [&](int r) { return r; },
+      [&](int, int first, int rows, int strip, const float (&acc)[2][4]) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+        for (int r = 0; r < 4; ++r) {
+          const int token = lane % 4 * 2 + r % 2;
+          if (token < rows)
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const int token = n * 8 + lane % 4 * 2 + r % 2;
-                if (token < rows)
-#pragma unroll
-                  for (int i = 0; i < MATS; ++i)
-                    a.out[(first + token) * static_cast<long long>(d) + (strip * MATS + i) * kStrip +
-                          lane / 4 + r / 2 * 8] = acc[i][n][r];
-              }
-          });
+            for (int i = 0; i < 2; ++i)
+              a.out[(first + token) * static_cast<long long>(d) + (strip * 2 + i) * kStrip + lane / 4 +
+                    r / 2 * 8] = acc[i][r];
+        }
+      });
 }
 
 // y_t = sum_j out[row of slot (t, j)], in the slots' order: 4 columns to a thread.
@@ -1051,13 +1019,6 @@ __global__ void __launch_bounds__(128)
 // ------------------------------------------------------------------------ host side
 
 constexpr int kSms = 152;
-// Rows of an expert that its weights are read once for; more of them are taken in several chunks.
-// (8 to a product where experts have few rows: more would be empty columns, whose values cost registers
-// and loads: 64 tokens x 16 of 896 experts, 4096 x 1024, took 590 us in chunks of 8, 965 us of 32.)
-int chunk_of(const moe_problem* p) {
-  return p->T <= 8 || static_cast<long long>(p->T) * p->k <= 4ll * p->E ? 8 : 32;
-}
-
 // Warps to a strip: what takes least time, in pieces, with one more for each strip's beginning and end;
 // the strips are taken in rounds.
 int split_of(long long strips, int pieces, int warps) {
@@ -1083,8 +1044,8 @@ struct Workspace {
 };
 
 Workspace carve(const moe_problem* p, void* base) {
-  const size_t slots = static_cast<size_t>(p->T) * p->k, chunk = chunk_of(p);
-  const size_t chunks = std::min<size_t>(p->E, slots) + slots / chunk;
+  const size_t slots = static_cast<size_t>(p->T) * p->k;
+  const size_t chunks = std::min<size_t>(p->E, slots) + slots / kChunk;
   Workspace w{};
   uint8_t* at = static_cast<uint8_t*>(base);
   const auto take = [&](size_t bytes) {
@@ -1186,11 +1147,11 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
   if (!workspace || workspace_bytes < carve(p, nullptr).bytes) return MOE_ERR_WORKSPACE;
   if (misaligned(workspace, 16)) return MOE_ERR_UNSUPPORTED;
   const Workspace ws = carve(p, workspace);
-  const int slots = p->T * p->k, chunk = chunk_of(p);
+  const int slots = p->T * p->k;
   const auto of = [](const moe_w4* w) { return Weights{w->codes, w->scales, w->group}; };
   Groups g = ws.g;
   g.idx = topk_idx, g.gate = topk_gate, g.slots = slots, g.E = p->E, g.single = p->T == 1;
-  const int chunks = std::min(p->E, slots);
+  const int chunks = std::max(std::min(p->E, slots), slots / kChunk);  // about
   GateUp up{{g, {of(w_gate), of(w_up)}, p->F, p->d, 1, dev_status}, ws.x, ws.h, ws.parts,
             ws.counters, p->k};
   Down down{{g, {of(w_down), {}}, p->d, p->F, 1, dev_status}, ws.parts, ws.out,
@@ -1218,27 +1179,22 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
     if (err == cudaSuccess)
       err = launch_behind(w4_prepare_kernel, blocks + !g.single, 1024,
                           slots <= kFewSlots ? 0 : warps * p->E * 2, stream,
-                          reinterpret_cast<const __nv_bfloat16*>(x), p->T, ws.x, ws.parts, slots, ws.counters, ws.n_counters, g, chunk, warps, dev_status);
+                          reinterpret_cast<const __nv_bfloat16*>(x), p->T, ws.x, ws.parts, slots, ws.counters, ws.n_counters, g, warps, dev_status);
   }
   const auto with = [&](auto z, auto of_group) {
     constexpr bool Z = decltype(z)::value;
     constexpr int GROUP = decltype(of_group)::value;
-    if (chunk == 8)
-      by_strips(w4_gateup_kernel<1, Z, GROUP>, Product<false, 2, 1, Z, GROUP>{}, up);
-    else
-      by_strips(w4_gateup_kernel<4, Z, GROUP>, Product<false, 2, 4, Z, GROUP>{}, up);
+    by_strips(w4_gateup_kernel<Z, GROUP>, Product<false, 2, Z, GROUP>{}, up);
     mark_after(MOE_KERNEL_W4_GATEUP, stream);
     mark_before(MOE_KERNEL_W4_DOWN, stream);
     if (g.single) {
-      using Of = Product<true, 1, 1, Z, GROUP, true>;
+      using Of = Product<true, 1, Z, GROUP, true>;
       constexpr int kMost = std::min(kMaxWarps, kSharedPerBlock / Of::kWarpBytes);
       const int strips = p->d / kStrip, warps = strips > kSms ? kWarps : kMost;
       launch(w4_down_kernel<Z, GROUP>, std::min(strips, 2 * kSms * kWarps / warps), warps,
              warps * Of::kWarpBytes, down);
-    } else if (chunk == 8) {
-      by_strips(w4_down_rows_kernel<2, 1, Z, GROUP>, Product<true, 2, 1, Z, GROUP>{}, down);
     } else {
-      by_strips(w4_down_rows_kernel<1, 4, Z, GROUP>, Product<true, 1, 4, Z, GROUP>{}, down);
+      by_strips(w4_down_rows_kernel<Z, GROUP>, Product<true, 2, Z, GROUP>{}, down);
     }
     if (!g.single && err == cudaSuccess)
       err = launch_behind(w4_combine_kernel, dim3(p->T, std::min(64, (p->d + 511) / 512)), 128, 0,
