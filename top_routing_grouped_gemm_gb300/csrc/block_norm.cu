@@ -784,8 +784,8 @@ int moe_block_norm(const moe_block_in* in, void* z, int64_t ld_z, void* n, int64
       err = launched(cudaFuncSetAttribute(block_norm_kernel<S, T, W, C, V, FULL>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize, ahead.bytes));
       if (err == cudaSuccess)
-        err = launch_behind(block_norm_kernel<S, T, W, C, V, FULL>, blocks_of(b.N, L::kGroups, blocks), threads,
-                            ahead.bytes, stream, b, z, lz, n, ln, ahead.rows);
+        err = launch_behind(block_norm_kernel<S, T, W, C, V, FULL>, blocks_of(b.N, L::kGroups, blocks),
+                            threads, ahead.bytes, stream, b, z, lz, n, ln, ahead.rows);
     });
   });
   mark_after(MOE_KERNEL_BLOCK_NORM, stream);

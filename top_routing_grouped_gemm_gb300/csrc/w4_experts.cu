@@ -1179,7 +1179,8 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
     if (err == cudaSuccess)
       err = launch_behind(w4_prepare_kernel, blocks + !g.single, 1024,
                           slots <= kFewSlots ? 0 : warps * p->E * 2, stream,
-                          reinterpret_cast<const __nv_bfloat16*>(x), p->T, ws.x, ws.parts, slots, ws.counters, ws.n_counters, g, warps, dev_status);
+                          reinterpret_cast<const __nv_bfloat16*>(x), p->T, ws.x, ws.parts, slots,
+                          ws.counters, ws.n_counters, g, warps, dev_status);
   }
   const auto with = [&](auto z, auto of_group) {
     constexpr bool Z = decltype(z)::value;
