@@ -14,7 +14,7 @@
 //
 // Now it is 56 for gate and up, 80 for down, whose operand has two parts.  One token through 16 of 896
 // experts of 4096 x 1024 takes 30 us (104 MB, 15 us of reading), 64 tokens that crowd on few experts
-// 496 us (358), 32 tokens through experts of 2048 x 512 with zeros 158 us (97): warps are issuing half of
+// 498 us (358), 32 tokens through experts of 2048 x 512 with zeros 158 us (97): warps are issuing half of
 // the time, in turn with what they wait for.
 #include <cuda_fp16.h>
 #include <math.h>
@@ -817,9 +817,9 @@ struct Product {
             sums[(warp * kSums + i) * 32 + lane] = acc[i / 4][i % 4];
         sync();
         if (!me)
+          for (int o = 1; o < split; ++o)
 #pragma unroll
-          for (int i = 0; i < kSums; ++i)
-            for (int o = 1; o < split; ++o)
+            for (int i = 0; i < kSums; ++i)
               acc[i / 4][i % 4] += sums[((warp + o) * kSums + i) * 32 + lane];
         sync();
       }
