@@ -914,6 +914,7 @@ __global__ void __launch_bounds__(kWarps * 32, Product<false, 2, ZEROS, GROUP>::
   Of::run(
       a.p, a.x, shared, [&](int r) { return a.p.g.slot_of(r) / a.k; },
       [&](int chunk, int first, int rows, int strip, const float (&acc)[2][4]) {
+        if (rows == 0) return;  // a single token's bad expert: it has no row, and down none of h to read
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int token = lane % 4 * 2 + r % 2;
