@@ -9,7 +9,7 @@ import torch
 
 from oracle import moe_block as MB
 from parity_util import f64
-from test_gpu_moe_block import BF, F32, check_w4, randn, w4_case
+from test_gpu_moe_block import BF, check_w4, w4_case
 from top_routing_grouped_gemm_gb300 import moe
 
 pytestmark = pytest.mark.gpu
@@ -62,3 +62,18 @@ def test_w4_one_token_with_experts_out_of_range(case, where):
         assert not y.any()
     for _ in range(10):
         assert torch.equal(run_w4_guarded(case, w, x, idx, gate), y)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("T", [1, 3])
+def test_w4_experts_out_of_range_read_nobodys_weights(T, value):
+    """What the experts that nobody names have for scales means nothing."""
+    case = (T, 512, 6, 4, 256, 64, True, None)
+    w, x, idx, gate = w4_case(case)
+    idx[idx == 0] = 5
+    idx[:, 1] = -1
+    want = run_w4_guarded(case, w, x, idx, gate)
+    for m in w:
+        m[1][0] = value
+    assert torch.equal(run_w4_guarded(case, w, x, idx, gate), want)
+    assert not want.isnan().any()

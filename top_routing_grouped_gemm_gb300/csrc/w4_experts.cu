@@ -345,11 +345,10 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* x, float (&v)[2][8])
 }
 
 // The tokens' values as operands, 256 threads to a row, and (the last block) the slots by expert;
-// counters set to zero, and with them a row of h's operands that is all zeros, for a single token's bad
-// experts.
+// counters set to zero.
 __global__ void __launch_bounds__(1024)
-    w4_prepare_kernel(const __nv_bfloat16* x, int T, Rows<kXParts> rows, Rows<kHParts> h, int zero_row,
-                      int* counters, int n_counters, const Groups g, int warps, int* dev_status) {
+    w4_prepare_kernel(const __nv_bfloat16* x, int T, Rows<kXParts> rows, int* counters,
+                      int n_counters, const Groups g, int warps, int* dev_status) {
   __shared__ float largest[4][8];
   after_previous();
   let_next_start();  // (which waits for this kernel's end before it reads what is written here)
@@ -363,10 +362,6 @@ __global__ void __launch_bounds__(1024)
   }
   const int me = blockIdx.x * 1024 + threadIdx.x, all = blocks * 1024;
   for (int i = me; i < n_counters; i += all) counters[i] = 0;
-  uint4* zeros = reinterpret_cast<uint4*>(const_cast<uint8_t*>(h.row(zero_row)));
-  for (int i = me; i < h.tiles * (kHParts * kTile * 2 / 16); i += all) zeros[i] = make_uint4(0, 0, 0, 0);
-  float4* infos = const_cast<float4*>(h.info_row(zero_row));
-  for (int i = me; i < h.tiles; i += all) infos[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (g.single && me < g.slots && !g.good(me)) report_status(dev_status, MOE_ERR_BAD_INDEX);
   const int team = threadIdx.x / 256, lane = threadIdx.x % 256;
   for (int r = blockIdx.x * 4 + team; r < T; r += blocks * 4) {
@@ -573,30 +568,39 @@ struct Product {
     }
   };
 
-  // A warp's share of the pieces of one strip of all chunks after one another, and of the block's next
-  // strips.
+  // A warp's share of the pieces of one strip of a single token's slots after one another, those of bad
+  // experts left out; the same in the block's next strips.
   struct Pieces {
     int chunk, piece, pieces, chunk_step, piece_step;
-    __device__ __forceinline__ Pieces(int first, int step, int pieces_)
+    uint32_t good;  // slots, a bit to each (32 at most)
+    __device__ __forceinline__ Pieces(int first, int step, int pieces_, uint32_t good_)
         : chunk(first / pieces_), piece(first % pieces_), pieces(pieces_),
-          chunk_step(step / pieces_), piece_step(step % pieces_) {}
+          chunk_step(step / pieces_), piece_step(step % pieces_), good(good_) {
+      while (bad()) step_on();
+    }
     __device__ __forceinline__ void next() {
+      do step_on();
+      while (bad());
+    }
+    __device__ __forceinline__ bool left() const { return chunk < 32 && good >> chunk; }
+
+   private:
+    __device__ __forceinline__ bool bad() const { return left() && !(good >> chunk & 1); }
+    __device__ __forceinline__ void step_on() {
       chunk += chunk_step, piece += piece_step;
       if (piece >= pieces) piece -= pieces, ++chunk;
     }
   };
   struct AheadInStrips : Copies {
     Pieces start, at;
-    int chunks, strip, strips, expert;
+    int strip, strips, expert;
     const Rows<PARTS>& values;
-    int zero_row;
 
     __device__ __forceinline__ AheadInStrips(const Problem& p_, const Rows<PARTS>& values_,
-                                             int zero_row_, uint8_t* ring_, uint64_t* bars_,
-                                             const Pieces& at_, int chunks_)
-        : Copies(p_, ring_, bars_), start(at_), at(at_), chunks(chunks_),
-          strip(blockIdx.x), strips(p_.rows / kStrip), values(values_), zero_row(zero_row_) {
-      if (at.chunk >= chunks) strip = strips;  // more warps than pieces
+                                             uint8_t* ring_, uint64_t* bars_, const Pieces& at_)
+        : Copies(p_, ring_, bars_), start(at_), at(at_), strip(blockIdx.x), strips(p_.rows / kStrip),
+          values(values_) {
+      if (!at.left()) strip = strips;  // more warps than pieces
       if (strip < strips) expert = p_.g.expert_of(at.chunk);
     }
     __device__ __forceinline__ void next() {
@@ -604,10 +608,10 @@ struct Product {
       const int skip = at.piece * kPieceTiles;
       const int tile = (expert * strips + strip) * this->tiles + skip;
       const int n = min(kPieceTiles, this->tiles - skip);
-      const int row = this->p.g.good(at.chunk) ? at.chunk : zero_row;
-      this->issue(tile, n, values.row(row) + skip * (PARTS * kTile * 2), values.info_row(row) + skip);
+      this->issue(tile, n, values.row(at.chunk) + skip * (PARTS * kTile * 2),
+                  values.info_row(at.chunk) + skip);
       at.next();
-      if (at.chunk >= chunks) at = start, strip += gridDim.x;
+      if (!at.left()) at = start, strip += gridDim.x;
       if (strip < strips) expert = this->p.g.expert_of(at.chunk);  // (wanted at the next call)
     }
   };
@@ -829,10 +833,10 @@ struct Product {
   }
 
   // All of the block's strips, for a single token: the sums over its experts stay in the products' sums.
-  // A bad expert takes `zero_row`.  put(strip, row, sum).
+  // put(strip, row, sum).
   template <typename Put>
   static __device__ __forceinline__ void run_strips(const Problem& p, const Rows<PARTS>& values,
-                                                    int zero_row, uint8_t* shared, Put put) {
+                                                    uint8_t* shared, Put put) {
     static_assert(ONE && MATS == 1, "one strip, one token");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
     uint8_t* ring = shared + warp * kRing;
@@ -845,16 +849,17 @@ struct Product {
     }
     __syncwarp();
     after_previous();
-    const int strips = p.rows / kStrip, tiles = p.cols / kTile, chunks = p.g.chunks();
-    const Pieces start(warp, warps, (tiles + kPieceTiles - 1) / kPieceTiles);
-    AheadInStrips ahead(p, values, zero_row, ring, bars, start, chunks);
+    const int strips = p.rows / kStrip, tiles = p.cols / kTile;
+    const uint32_t good = __ballot_sync(~0u, lane < p.g.slots && p.g.good(lane));
+    const Pieces start(warp, warps, (tiles + kPieceTiles - 1) / kPieceTiles, good);
+    AheadInStrips ahead(p, values, ring, bars, start);
     for (int i = 0; i < kPlaces - 1; ++i) ahead.next();
     int place = 0;
     uint32_t parity = 0;
     bool ok = true;
     for (int strip = blockIdx.x; strip < strips; strip += gridDim.x) {
       float acc[1][4] = {};
-      for (Pieces at = start; at.chunk < chunks && ok; at.next()) {
+      for (Pieces at = start; at.left() && ok; at.next()) {
         if (!wait_for(bars + place, parity)) {
           ok = false;
           break;
@@ -956,7 +961,6 @@ struct Down {
   Rows<kHParts> h;
   float* out;  // [slots][d], a row to a slot
   __nv_bfloat16* y;
-  int zero_row;
 };
 
 // A single token: y at once.
@@ -964,7 +968,7 @@ template <bool ZEROS, int GROUP>
 __global__ void __launch_bounds__(kMaxWarps * 32) w4_down_kernel(const Down a) {
   using Of = Product<true, 1, ZEROS, GROUP, true>;
   extern __shared__ __align__(16) uint8_t shared[];
-  Of::run_strips(a.p, a.h, a.zero_row, shared, [&](int strip, int row, float sum) {
+  Of::run_strips(a.p, a.h, shared, [&](int strip, int row, float sum) {
     a.y[strip * kStrip + row] = __float2bfloat16_rn(sum);
   });
 }
@@ -1065,8 +1069,8 @@ Workspace carve(const moe_problem* p, void* base) {
   w.x.tiles = p->d / kTile, w.parts.tiles = p->F / kTile;
   w.x.parts = take(p->T * x_tiles * (kXParts * kTile * 2));
   w.x.info = reinterpret_cast<float4*>(take(p->T * x_tiles * 16));
-  w.parts.parts = take((slots + 1) * h_tiles * (kHParts * kTile * 2));
-  w.parts.info = reinterpret_cast<float4*>(take((slots + 1) * h_tiles * 16));
+  w.parts.parts = take(slots * h_tiles * (kHParts * kTile * 2));
+  w.parts.info = reinterpret_cast<float4*>(take(slots * h_tiles * 16));
   w.n_counters = static_cast<int>((p->T == 1 ? slots : chunks) * h_tiles);
   w.counters = reinterpret_cast<int*>(take(w.n_counters * 4));
   w.h = reinterpret_cast<float*>(take(slots * p->F * 4));
@@ -1156,7 +1160,7 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
   GateUp up{{g, {of(w_gate), of(w_up)}, p->F, p->d, 1, dev_status}, ws.x, ws.h, ws.parts,
             ws.counters, p->k};
   Down down{{g, {of(w_down), {}}, p->d, p->F, 1, dev_status}, ws.parts, ws.out,
-            reinterpret_cast<__nv_bfloat16*>(y), slots};
+            reinterpret_cast<__nv_bfloat16*>(y)};
   cudaError_t err = cudaSuccess;
   const auto launch = [&](auto kernel, int blocks, int warps, int bytes, auto& args) {
     if (err == cudaSuccess)
@@ -1180,8 +1184,8 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
     if (err == cudaSuccess)
       err = launch_behind(w4_prepare_kernel, blocks + !g.single, 1024,
                           slots <= kFewSlots ? 0 : warps * p->E * 2, stream,
-                          reinterpret_cast<const __nv_bfloat16*>(x), p->T, ws.x, ws.parts, slots,
-                          ws.counters, ws.n_counters, g, warps, dev_status);
+                          reinterpret_cast<const __nv_bfloat16*>(x), p->T, ws.x, ws.counters,
+                          ws.n_counters, g, warps, dev_status);
   }
   const auto with = [&](auto z, auto of_group) {
     constexpr bool Z = decltype(z)::value;
