@@ -9,7 +9,7 @@ import torch
 
 from oracle import moe_block as MB
 from parity_util import f64
-from test_gpu_moe_block import BF, check_w4, w4_case
+from test_gpu_moe_block import BF, F32, SIG, SOFT, U, check_w4, randn, run_select, w4_case
 from top_routing_grouped_gemm_gb300 import moe
 
 pytestmark = pytest.mark.gpu
@@ -77,3 +77,48 @@ def test_w4_experts_out_of_range_read_nobodys_weights(T, value):
         m[1][0] = value
     assert torch.equal(run_w4_guarded(case, w, x, idx, gate), want)
     assert not want.isnan().any()
+
+
+# ------------------------------------------------------------------------ routing
+
+INF, NAN = float("inf"), float("nan")
+
+# what a bias has, by group and expert of the group
+BIASES = {
+    "one +inf": {(5, 2): INF},
+    "two +inf in a group": {(6, 0): INF, (6, 3): INF},
+    "+inf in two groups": {(2, 1): INF, (7, 2): INF},
+    "+inf and two of them": {(1, 1): INF, (4, 0): INF, (4, 3): INF},
+    "three +inf in a group": {(3, 0): INF, (3, 1): INF, (3, 3): INF},
+    "-inf here and there": {(0, 0): -INF, (3, 2): -INF, (3, 3): -INF},
+    "groups of -inf": {(g, e): -INF for g in (0, 1, 2, 4, 5) for e in range(4)},
+    "all groups but one of -inf": {(g, e): -INF for g in range(8) if g != 6 for e in range(4)},
+    "nothing but -inf": {(g, e): -INF for g in range(8) for e in range(4)},
+    "one of a group left": {(g, e): -INF for g in range(8) for e in range(4) if e != g % 4},
+    "NaN": {(0, 1): NAN, (4, 0): NAN, (4, 1): NAN},
+    "+inf, -inf and NaN": {(0, 1): -INF, (2, 0): INF, (4, 1): NAN, (7, 3): INF, (7, 1): -INF},
+}
+
+
+@pytest.mark.parametrize("kept", [1, 2, 3, 7])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("score", [SIG, SOFT])
+@pytest.mark.parametrize("size", [4, 5, 32])
+@pytest.mark.parametrize("what", BIASES)
+def test_route_select_with_groups_and_infinite_biases(what, size, score, best, kept):
+    """+inf puts an expert, and its group with it, first, -inf and NaN last; equal ones by index."""
+    T, groups, k = 20, 8, 3
+    case = (T, groups * size, k, score, groups, kept, best, True, True, F32)
+    gen = torch.Generator().manual_seed(size)
+    logits = randn(gen, *case[:2])
+    bias = randn(gen, case[1]) * (0.05 if score == SIG else 0.3 / case[1])
+    for (group, expert), value in BIASES[what].items():
+        bias[group * size + expert] = value
+    if "one of a group left" in what:
+        bias.view(groups, size)[:, 4:] = -INF
+    if "-inf" in what and "here" not in what and "+" not in what:
+        bias.view(groups, size)[:, 4:] = bias.view(groups, size)[:, :1]
+    idx, gate, _ = run_select(case, logits.cuda(), bias.cuda())
+    want, ref, _ = MB.select(f64(logits), f64(bias), k, score == SIG, groups, kept, best, True, 2.5)
+    assert np.array_equal(idx, want)
+    assert np.allclose(gate, ref, rtol=64 * U, atol=0)

@@ -452,10 +452,11 @@ __global__ void __launch_bounds__(kWarps * 32, VPL <= 16 ? 4 : VPL <= 32 ? 3 : 2
           const float size = 2.f * s.best * largest + fabsf(last) + fabsf(next);
           if (!(last - next > size * step)) {
             // experts that may be among the largest of their group
+            // (an infinite one as it is: inf - inf would leave out all of them)
             const float least = s.best == 2 ? top[1] : top[0];
+            const float margin = isinf(least) ? 0.f : (2.f * largest + 0.5f * fabsf(least)) * step;
             const int by_value = keep_exactly(
-                s, row, row_scores, SIGMOID ? 1.f : inv, most,
-                least - (2.f * largest + 0.5f * fabsf(least)) * step, VEC,
+                s, row, row_scores, SIGMOID ? 1.f : inv, most, least - margin, VEC,
                 reinterpret_cast<int*>(candidates[warp]),
                 reinterpret_cast<Two*>(candidates[warp] + 32));
             if (__any_sync(~0u, by_value < 0))
