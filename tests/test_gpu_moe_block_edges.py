@@ -3,6 +3,9 @@ threads, outputs over inputs, orders and values next to a rounding.
 
 Tolerances as in test_gpu_moe_block.py."""
 
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -122,3 +125,52 @@ def test_route_select_with_groups_and_infinite_biases(what, size, score, best, k
     want, ref, _ = MB.select(f64(logits), f64(bias), k, score == SIG, groups, kept, best, True, 2.5)
     assert np.array_equal(idx, want)
     assert np.allclose(gate, ref, rtol=64 * U, atol=0)
+
+
+# ------------------------------------------------------------------------ calls from several threads
+
+def together(calls, times):
+    """Each call `times` times in a thread and on a stream of its own, all at once; its statuses."""
+    start, statuses = threading.Barrier(len(calls)), [set() for _ in calls]
+
+    def run(call, seen):
+        stream = torch.cuda.Stream()
+        start.wait()
+        for i in range(times):
+            seen.add(call(stream.cuda_stream))
+            if i % 256 == 255:
+                stream.synchronize()
+
+    threads = [threading.Thread(target=run, args=a) for a in zip(calls, statuses)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return set().union(*statuses)
+
+
+def ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def test_norms_with_and_without_gates_at_once():
+    """Calls whose blocks want different amounts of shared memory, in threads beside each other."""
+    N, D = 3, 256
+    gen = torch.Generator().manual_seed(0)
+    x, y, gate, dz = (randn(gen, N, D).cuda() for _ in range(4))
+    calls, backs, outs, lib = [], [], [], moe.lib()
+    for kind, a in ((moe.MOE_GATE_NONE, None), (moe.MOE_GATE_VALUE, gate)) * 2:
+        z, n, dx, dy = (torch.empty_like(x) for _ in range(4))
+        block = moe.moe_block_in(N, D, 1, 1, 1e-6, 0.5, kind, 1, 1, ptr(x), D, ptr(y), D, ptr(a), D, None, None)
+        grads = moe.moe_block_grads(ptr(dz), D, ptr(dz), D, 1, ptr(dx), D, ptr(dy), D, None, 0, None, None)
+        b, g = (ctypes.addressof(c) for c in (block, grads))
+        calls.append(lambda s, b=b, z=ptr(z), n=ptr(n), keep=block: lib.moe_block_norm(b, z, D, n, D, s))
+        backs.append(lambda s, b=b, g=g, keep=(block, grads): lib.moe_block_norm_backward(b, g, None, 0, s))
+        outs.append((z, n, dx, dy))
+    assert [c(None) for c in calls + backs] == [0] * 8
+    torch.cuda.synchronize()
+    want = [[t.clone() for t in o] for o in outs]
+    assert together(calls, 30000) == {0}
+    assert together(backs, 30000) == {0}
+    assert all(torch.equal(a, b) for o, w in zip(outs, want) for a, b in zip(o, w))

@@ -680,6 +680,21 @@ Ahead ahead_of(int row_bytes, int most, int blocks) {
   return {rows, row_bytes * (rows + 1)};
 }
 
+// Three rows at most, of places P with a gate [N, D] or without.
+template <typename L, typename P>
+Ahead ahead_with(bool gates) {
+  return ahead_of<L::kRowThreads / 32>(P::all(gates), 3, L::kThreads > 256 ? 1 : 2);
+}
+
+// How much shared memory a kernel may be launched with.  That is the kernel's, for all threads of the
+// process: what any call wants, so that no call takes it down while another one is about to launch.
+template <typename L, typename P>
+cudaError_t allow_shared(const void* kernel) {
+  return launched(
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           std::max(ahead_with<L, P>(false).bytes, ahead_with<L, P>(true).bytes)));
+}
+
 // (The backward's blocks write partial sums, so their number is the same for all types.)
 int backward_blocks(int N, int D) {
   return with_lanes<8>(D, [&](auto lanes) {
@@ -777,15 +792,14 @@ int moe_block_norm(const moe_block_in* in, void* z, int64_t ld_z, void* n, int64
       using L = LanesOf<decltype(lanes)>;
       constexpr int W = L::kRowThreads / 32, C = L::kPieces, V = L::kValues, threads = L::kThreads;
       constexpr bool FULL = L::kFull;
-      const Ahead ahead = ahead_of<W>(
-          Places<S, T, T, threads, C, V, false>::all(b.gate_kind == MOE_GATE_VALUE), 3,
-          threads > 256 ? 1 : 2);
+      using P = Places<S, T, T, threads, C, V, false>;
+      const Ahead ahead = ahead_with<L, P>(b.gate_kind == MOE_GATE_VALUE);
       const int blocks = threads > 256 ? 1 : std::max(1, std::min(2, kSharedPerSm / (ahead.bytes + 2048)));
-      err = launched(cudaFuncSetAttribute(block_norm_kernel<S, T, W, C, V, FULL>,
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize, ahead.bytes));
+      const auto kernel = block_norm_kernel<S, T, W, C, V, FULL>;
+      err = allow_shared<L, P>(reinterpret_cast<const void*>(kernel));
       if (err == cudaSuccess)
-        err = launch_behind(block_norm_kernel<S, T, W, C, V, FULL>, blocks_of(b.N, L::kGroups, blocks),
-                            threads, ahead.bytes, stream, b, z, lz, n, ln, ahead.rows);
+        err = launch_behind(kernel, blocks_of(b.N, L::kGroups, blocks), threads, ahead.bytes, stream, b,
+                            z, lz, n, ln, ahead.rows);
     });
   });
   mark_after(MOE_KERNEL_BLOCK_NORM, stream);
@@ -838,9 +852,8 @@ int moe_block_norm_backward(const moe_block_in* in, const moe_block_grads* grads
       constexpr bool FULL = L::kFull;
       const auto launch = [&](auto kernel, auto dn) {
         using P = Places<S, T, decltype(dn), threads, C, V, true>;
-        const Ahead ahead = ahead_of<W>(P::all(b.gate_kind == MOE_GATE_VALUE), 3, threads > 256 ? 1 : 2);
-        err = launched(
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ahead.bytes));
+        const Ahead ahead = ahead_with<L, P>(b.gate_kind == MOE_GATE_VALUE);
+        err = allow_shared<L, P>(reinterpret_cast<const void*>(kernel));
         if (err == cudaSuccess)
           err = launch_behind(kernel, blocks, threads, ahead.bytes, stream, b, g, ahead.rows);
       };
