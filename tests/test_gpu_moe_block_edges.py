@@ -174,3 +174,24 @@ def test_norms_with_and_without_gates_at_once():
     assert together(calls, 30000) == {0}
     assert together(backs, 30000) == {0}
     assert all(torch.equal(a, b) for o, w in zip(outs, want) for a, b in zip(o, w))
+
+
+def test_w4_of_two_models_at_once():
+    """One token through models of few and of many columns."""
+    calls, ys, lib = [], [], moe.lib()
+    for d in (64, 2560) * 2:
+        case = (1, d, 4, 2, 64, 32, True, None)
+        w, x, idx, gate = w4_case(case)
+        p = moe.Problem(*case[:5])
+        packed = [moe.W4Weights(*(t.cuda() for t in m)) for m in w]
+        ws = torch.empty(moe.moe_w4_expert_ffn_workspace_size(p), dtype=torch.uint8, device="cuda")
+        x, idx, gate, y = x.cuda(), idx.cuda(), gate.cuda(), torch.empty((1, d), dtype=BF, device="cuda")
+        mats = [ctypes.addressof(m._c) for m in packed]
+        args = (p.c(), ptr(x), ptr(idx), ptr(gate), *mats, ptr(y), ptr(ws), ws.numel(), None)
+        calls.append(lambda s, args=args, keep=(p, packed, ws, x, idx, gate): lib.moe_w4_expert_ffn(*args, s))
+        ys.append(y)
+    assert [c(None) for c in calls] == [0] * 4
+    torch.cuda.synchronize()
+    want = [y.clone() for y in ys]
+    assert together(calls, 20000) == {0}
+    assert all(torch.equal(a, b) for a, b in zip(ys, want))

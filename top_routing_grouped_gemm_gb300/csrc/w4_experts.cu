@@ -1162,9 +1162,11 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
   Down down{{g, {of(w_down), {}}, p->d, p->F, 1, dev_status}, ws.parts, ws.out,
             reinterpret_cast<__nv_bfloat16*>(y)};
   cudaError_t err = cudaSuccess;
-  const auto launch = [&](auto kernel, int blocks, int warps, int bytes, auto& args) {
+  // (The limit is the kernel's, for all threads of the process: the most that any call wants, so that
+  // no call takes it down while another one is about to launch.)
+  const auto launch = [&](auto kernel, int blocks, int warps, int bytes, int limit, auto& args) {
     if (err == cudaSuccess)
-      err = launched(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+      err = launched(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, limit));
     if (err == cudaSuccess) err = launch_behind(kernel, blocks, warps * 32, bytes, stream, args);
   };
   const auto by_strips = [&](auto kernel, auto product, auto& args) {
@@ -1173,7 +1175,7 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
     args.p.split = split_of(chunks * static_cast<long long>(args.p.rows / Of::kRows),
                             (args.p.cols / kTile + Of::kPieceTiles - 1) / Of::kPieceTiles,
                             blocks * kWarps);
-    launch(kernel, blocks, kWarps, Of::kBytes, args);
+    launch(kernel, blocks, kWarps, Of::kBytes, Of::kBytes, args);
   };
   mark_before(MOE_KERNEL_W4_GATEUP, stream);
   {
@@ -1198,7 +1200,7 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
       constexpr int kMost = std::min(kMaxWarps, kSharedPerBlock / Of::kWarpBytes);
       const int strips = p->d / kStrip, warps = strips > kSms ? kWarps : kMost;
       launch(w4_down_kernel<Z, GROUP>, std::min(strips, 2 * kSms * kWarps / warps), warps,
-             warps * Of::kWarpBytes, down);
+             warps * Of::kWarpBytes, kMost * Of::kWarpBytes, down);
     } else {
       by_strips(w4_down_rows_kernel<Z, GROUP>, Product<true, 2, Z, GROUP>{}, down);
     }
