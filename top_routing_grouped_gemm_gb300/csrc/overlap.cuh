@@ -5,9 +5,9 @@
 // holds as ever, for plain loads (what is read-only for a kernel's whole life is another matter: no
 // __ldg and no restricted pointers here).  What is saved is the launch itself (0.4 us of a one-token
 // step of 2.3 us in a graph; calls one after the other: 8192 x 4096 recurrence forward + backward
-// 129 -> 124 us, norm + rotation's backward of 32768 x 32 x 128 185 -> 174 us).  No kernel lets the
-// next one in before its own blocks end: those took the first places that came free, unevenly
-// (124 -> 128 us).
+// 129 -> 124 us, norm + rotation's backward of 32768 x 32 x 128 185 -> 174 us).  Kernels of more blocks
+// than the GPU has room for let nobody in before their own blocks end: the next one's took the first
+// places that came free, unevenly (124 -> 128 us).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -19,8 +19,8 @@ __device__ __forceinline__ void after_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Lets the next kernel of the stream be set up now: for one of a few blocks, which leaves room for all
-// of the next one's.
+// Lets the next kernel of the stream be set up as soon as all blocks have come here, for a kernel of no
+// more blocks than SMs that leaves room beside them.  The next one still begins with after_previous().
 __device__ __forceinline__ void let_next_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -351,7 +351,8 @@ __global__ void __launch_bounds__(1024)
                       int n_counters, const Groups g, int warps, int* dev_status) {
   __shared__ float largest[4][8];
   after_previous();
-  let_next_start();  // (which waits for this kernel's end before it reads what is written here)
+  // (gate and up are set up beside this: one token 32.1 -> 31.9 us, 32 tokens 161 -> 157, 64 499 -> 500)
+  let_next_start();
   const int blocks = g.single ? gridDim.x : gridDim.x - 1;
   if (blockIdx.x == blocks) {
     if (g.slots <= kFewSlots)
@@ -780,13 +781,11 @@ struct Product {
       fence_barrier_init();
     }
     __syncwarp();
-    // a single token's experts were there before the preparing kernel began
-    if (!p.g.single || DOWN) after_previous();
+    after_previous();
     const int strips = p.rows / kRows, tiles = p.cols / kTile, chunks = p.g.chunks();
     Tasks task(blockIdx.x * teams + team, gridDim.x * teams, strips);
     Ahead ahead(p, ring, bars, task, chunks, me);
     for (int i = 0; i < kPlaces - 1; ++i) ahead.next();
-    if (p.g.single && !DOWN) after_previous();
     int place = 0;
     uint32_t parity = 0;
     bool ok = true;
