@@ -1,0 +1,24 @@
+"""CPU checks of the binding of what stands around the experts: what it hands on is what its objects say."""
+
+import ctypes
+
+import pytest
+
+from top_routing_grouped_gemm_gb300 import moe
+
+
+@pytest.mark.parametrize("field, value", [("score", moe.MOE_SCORE_SOFTMAX), ("groups", 8), ("groups_kept", 4),
+                                          ("group_best", 2), ("renormalise", False), ("scale", 2.5)])
+def test_a_rule_that_is_changed_is_what_the_library_reads(field, value):
+    rule = moe.RouteRule(moe.MOE_SCORE_SIGMOID)
+    before = moe.moe_route_rule.from_address(rule.c())
+    assert [getattr(before, n) for n, _ in before._fields_] == [1, 1, 1, 1, 1, 1.0]
+    setattr(rule, field, value)
+    assert getattr(rule, field) == value
+    assert getattr(moe.moe_route_rule.from_address(rule.c()), field) == value
+
+
+def test_a_rule_by_position():
+    rule = moe.RouteRule(moe.MOE_SCORE_SIGMOID, 8, 4, 2, False, 2.5)
+    assert [getattr(rule, n) for n, _ in moe.moe_route_rule._fields_] == [1, 8, 4, 2, 0, 2.5]
+    assert ctypes.sizeof(rule) == ctypes.sizeof(moe.moe_route_rule)

@@ -754,17 +754,15 @@ def moe_glr_step(B, D, mode, dtype, g, x, slot, n_slots, state, h, dev_status=No
 
 # ---- around the experts (include/moe_block.h)
 
-class RouteRule:
-    """How moe_route_select makes experts and gates of logits."""
+class RouteRule(moe_route_rule):
+    """How moe_route_select makes experts and gates of logits: score, groups, groups_kept, group_best,
+    renormalise and scale, which may be changed between calls."""
 
     def __init__(self, score, groups=1, groups_kept=1, group_best=1, renormalise=True, scale=1.0):
-        self.score, self.groups, self.groups_kept = score, groups, groups_kept
-        self.group_best, self.renormalise, self.scale = group_best, renormalise, scale
-        self._c = moe_route_rule(score, groups, groups_kept, group_best, 1 if renormalise else 0,
-                                 scale)
+        super().__init__(score, groups, groups_kept, group_best, 1 if renormalise else 0, scale)
 
     def c(self):
-        return ctypes.addressof(self._c)
+        return ctypes.addressof(self)
 
 
 def moe_route_select(T, E, k, rule, dtype, logits, select_bias, topk_idx, topk_gate,
