@@ -3,6 +3,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from top_routing_grouped_gemm_gb300 import moe
 
@@ -22,3 +23,12 @@ def test_a_rule_by_position():
     rule = moe.RouteRule(moe.MOE_SCORE_SIGMOID, 8, 4, 2, False, 2.5)
     assert [getattr(rule, n) for n, _ in moe.moe_route_rule._fields_] == [1, 8, 4, 2, 0, 2.5]
     assert ctypes.sizeof(rule) == ctypes.sizeof(moe.moe_route_rule)
+
+
+@pytest.mark.parametrize("group", [0, -32])
+def test_packing_refuses_groups_of_nothing(group):
+    codes, scales = torch.zeros(1, 16, 32, dtype=torch.uint8), torch.zeros(1, 16, 1, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="codes|scales"):
+        moe.moe_w4_pack(1, 16, 64, group, codes, scales, None, codes, codes)
+    with pytest.raises(ValueError, match="codes|scales"):
+        moe.W4Weights(torch.zeros(1, 16, 0, dtype=torch.uint8), scales)

@@ -894,7 +894,8 @@ def moe_w4_pack(E, rows, cols, group, codes, scales, zeros, packed_codes, packed
     """codes [E, rows, cols / 2], zeros and packed_codes uint8, scales bf16; packed_scales as many
     uint8 as its entries take."""
     u8, dev = torch.uint8, _device()
-    shape = (E, rows, cols // group)
+    groups = cols // group if group > 0 else 0
+    shape = (E, rows, groups)
     _check("moe_w4_pack",
            lib().moe_w4_pack(E, rows, cols, group, _tensor("codes", codes, u8, (E, rows, cols // 2),
                                                            dev),
@@ -903,7 +904,7 @@ def moe_w4_pack(E, rows, cols, group, codes, scales, zeros, packed_codes, packed
                              _tensor("packed_codes", packed_codes, u8, (E * rows * cols // 2,),
                                      dev),
                              _tensor("packed_scales", packed_scales, u8,
-                                     (E * rows * (cols // group) * (2 if zeros is None else 4),),
+                                     (E * rows * groups * (2 if zeros is None else 4),),
                                      dev), _stream_of(stream, dev)))
 
 
