@@ -186,7 +186,8 @@ def test_w4_of_two_models_at_once():
         packed = [moe.W4Weights(*(t.cuda() for t in m)) for m in w]
         ws = torch.empty(moe.moe_w4_expert_ffn_workspace_size(p), dtype=torch.uint8, device="cuda")
         x, idx, gate, y = x.cuda(), idx.cuda(), gate.cuda(), torch.empty((1, d), dtype=BF, device="cuda")
-        mats = [ctypes.addressof(m._c) for m in packed]
+        shapes = (4, 64, d), (4, 64, d), (4, d, 64)
+        mats = [m.c("w", s, 0) for m, s in zip(packed, shapes)]
         args = (p.c(), ptr(x), ptr(idx), ptr(gate), *mats, ptr(y), ptr(ws), ws.numel(), None)
         calls.append(lambda s, args=args, keep=(p, packed, ws, x, idx, gate): lib.moe_w4_expert_ffn(*args, s))
         ys.append(y)

@@ -32,3 +32,15 @@ def test_packing_refuses_groups_of_nothing(group):
         moe.moe_w4_pack(1, 16, 64, group, codes, scales, None, codes, codes)
     with pytest.raises(ValueError, match="codes|scales"):
         moe.W4Weights(torch.zeros(1, 16, 0, dtype=torch.uint8), scales)
+
+
+def test_weights_whose_arrays_are_replaced_are_what_the_library_reads():
+    """A copy made elsewhere, say, of arrays that are then given up."""
+    w = object.__new__(moe.W4Weights)
+    w.E, w.rows, w.cols, w.group, w.has_zeros = 2, 16, 64, 32, True
+    w.codes, w.scales = (torch.zeros(n, dtype=torch.uint8) for n in (1024, 256))
+    for _ in range(2):
+        read = moe.moe_w4.from_buffer_copy(w.c("w", (2, 16, 64), -1))
+        assert [getattr(read, n) for n, _ in read._fields_] == [w.codes.data_ptr(), w.scales.data_ptr(), 32, 1]
+        w.codes, w.scales = w.codes.clone(), w.scales.clone()
+    assert ctypes.sizeof(moe.moe_w4) == moe._W4.size

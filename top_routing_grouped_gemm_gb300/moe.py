@@ -908,6 +908,9 @@ def moe_w4_pack(E, rows, cols, group, codes, scales, zeros, packed_codes, packed
                                      dev), _stream_of(stream, dev)))
 
 
+_W4 = struct.Struct("PPii")  # moe_w4 as bytes
+
+
 class W4Weights:
     """4-bit weights [E, rows, cols], laid out for moe_w4_expert_ffn: codes [E, rows, cols / 2] (two
     to a byte, the lower four bits first), scales [E, rows, cols / group] bf16, zeros like scales
@@ -924,14 +927,13 @@ class W4Weights:
         self.scales = torch.empty(entries, dtype=torch.uint8, device=codes.device)
         moe_w4_pack(self.E, self.rows, self.cols, self.group, codes, scales, zeros, self.codes,
                     self.scales, stream)
-        self._c = moe_w4(self.codes.data_ptr(), self.scales.data_ptr(), self.group,
-                         0 if zeros is None else 1)
+        self.has_zeros = zeros is not None
 
     def c(self, name, shape, dev):
         if (self.E, self.rows, self.cols) != shape or self.codes.get_device() != dev:
             raise ValueError(f"{name}: weights {shape} on the current device are wanted, got "
                              f"{(self.E, self.rows, self.cols)} on {self.codes.device}")
-        return ctypes.addressof(self._c)
+        return _W4.pack(self.codes.data_ptr(), self.scales.data_ptr(), self.group, self.has_zeros)
 
 
 def moe_w4_expert_ffn_workspace_size(p: Problem) -> int:
