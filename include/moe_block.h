@@ -186,7 +186,7 @@ int moe_block_norm_backward(const moe_block_in* in, const moe_block_grads* grads
  *
  * Sums are fp32; each product is exact: x and h are scaled by powers of two, one for a row of x and
  * one for each 64 values of h, and taken as fp16, x in one part (bf16 values that are less than
- * 2^-28 of the largest of their row lose bits), h in two (to 2^-23 of it); y is rounded once.  A
+ * 2^-27 of the largest of their row may lose bits), h in two (to 2^-23 of it); y is rounded once.  A
  * value of x or h that is not finite makes its token's y NaN.  p gives T, d, E, k and F; r has to
  * be 0 (adapters are not part of it) and the capacity is not used: every slot is computed.  Entries
  * of topk_idx outside [0, E) are reported as MOE_ERR_BAD_INDEX in *dev_status (may be NULL) and

@@ -12,7 +12,8 @@ import torch
 
 from oracle import moe_block as MB
 from parity_util import f64
-from test_gpu_moe_block import BF, F32, SIG, SOFT, U, check_w4, randn, run_select, w4_case
+from rounding import Rounded
+from test_gpu_moe_block import BF, F32, SIG, SOFT, U, check_w4, randn, run_select, w4_case, LAST
 from top_routing_grouped_gemm_gb300 import moe
 
 pytestmark = pytest.mark.gpu
@@ -196,3 +197,79 @@ def test_w4_of_two_models_at_once():
     want = [y.clone() for y in ys]
     assert together(calls, 20000) == {0}
     assert all(torch.equal(a, b) for a, b in zip(ys, want))
+
+
+# ------------------------------------------------------------------------ 4-bit experts: roundings
+
+# Sums over the codes times the values, less the zero times the sum of the values: both parts' sizes count.
+# 16 products and a sum are added at once, each cut off at 2^-24 of the largest (18 halves of a step to 16
+# columns of a group); a group's sum is corrected, scaled and added to the others (cols / group); the sums
+# of the values, the joins of 8 warps and the last factors are 40 more.
+def tight(cols, group):
+    return (18 * group / 16 + cols / group + 40) * U
+
+
+def code_and_zero(m):
+    codes, scales, zeros = m[0].numpy(), f64(m[1]), None if m[2] is None else m[2].numpy()
+    code = MB.w4_values(codes, np.ones(scales.shape), np.zeros(scales.shape, np.uint8))
+    zero = np.repeat(np.full(scales.shape, 8.0) if zeros is None else zeros.astype(float),
+                     code.shape[-1] // scales.shape[-1], -1)
+    scale = np.repeat(scales, code.shape[-1] // scales.shape[-1], -1)
+    return (code - zero) * scale, (code + zero) * scale
+
+
+@pytest.mark.parametrize("small_codes", [False, True])
+@pytest.mark.parametrize("case", [(1, 512, 6, 4, 256, 64, True, None), (1, 256, 3, 2, 1152, 128, False, None),
+                                  (8, 384, 4, 3, 192, 32, True, None), (40, 256, 6, 2, 512, 128, True, None),
+                                  (70, 192, 5, 3, 320, 64, False, None)], ids=str)
+def test_w4_within_the_roundings_of_its_sums(case, small_codes):
+    """The sizes of code and zero, and h in two parts (off by 2^-23, and by 2^-45 of its tile's largest)."""
+    T, d, E, k, F, group, zeros = case[:7]
+    w, x, idx, gate = w4_case(case, 3)
+    if small_codes:  # 0 to 3, zeros 0 to 2
+        w = [(m[0] & 0x33, m[1], torch.clamp(m[2], max=2) if zeros else None) for m in w]
+    got = run_w4_guarded(case, w, x, idx, gate)
+    W, size = zip(*(code_and_zero(m) for m in w))
+    x, g, idx = f64(x), f64(gate), idx.numpy()
+    value, error = np.zeros((T, d)), np.zeros((T, d))
+    for t in range(T):
+        for j in range(k):
+            e = idx[t, j]
+            a, b = (Rounded(W[i][e] @ x[t], tight(d, group) * (size[i][e] @ np.abs(x[t]))) for i in (0, 1))
+            h = a / (1.0 + (-a).exp()) * b * g[t, j]
+            most = np.repeat(np.abs(h.v).reshape(-1, 64).max(-1), 64)
+            parts = 2.0 ** -23 * np.abs(h.v) + 2.0 ** -45 * most
+            value[t] += W[2][e] @ h.v
+            error[t] += np.abs(W[2][e]) @ h.e + size[2][e] @ (
+                parts + (tight(F, group) + k * F / group * U) * np.abs(h.v))
+    Rounded(value, error).close(f64(got), LAST[BF], "y")
+
+
+def one_weight(E, rows, cols, group, row, col, scale):
+    """Weights of which one row, or all (None), has code 15 at a column; zeros 0."""
+    codes = torch.zeros((E, rows, cols // 2), dtype=torch.uint8)
+    codes[:, slice(None) if row is None else row, col // 2] = 15 << col % 2 * 4
+    scales = torch.full((E, rows, cols // group), scale).to(BF)
+    return codes, scales, torch.zeros(scales.shape, dtype=torch.uint8)
+
+
+def through_one_weight(T, col, x, scale):
+    """(y, what it has to be): x's column through gate and up, h's column 70 through all rows of down."""
+    d, F, group = 128, 128, 32
+    case = (T, d, 2, 1, F, group, True, None)
+    w = [one_weight(2, F, d, group, 70, col, scale)] * 2 + [one_weight(2, d, F, group, None, 70, 0.125)]
+    y = run_w4_guarded(case, w, x, torch.ones((T, 1), dtype=torch.int32), torch.ones((T, 1)))
+    a = 15 * float(torch.tensor(scale).to(BF)) * f64(x)[:, col]
+    return f64(y), (a / (1 + np.exp(-a)) * a * 15 * 0.125)[:, None]
+
+
+@pytest.mark.parametrize("T", [1, 3, 20])
+@pytest.mark.parametrize("col", [2, 3, 38, 71, 127])
+@pytest.mark.parametrize("small", [1 + 2 ** -7, 2 - 2 ** -7])
+def test_w4_values_from_2_to_the_minus_27_of_a_rows_largest_on_keep_their_bits(T, col, small):
+    """In columns that meet the 16-fold codes, which have the fewest bits.  A lost last bit (2^-7 of x) would
+    show twice over; what is allowed is the last rounding, and 64 of fp32's."""
+    x = torch.zeros((T, 128), dtype=BF)
+    x[:, 0], x[:, col] = 2.0 ** 27, small
+    y, want = through_one_weight(T, col, x, 1 / 16)
+    assert (np.abs(y - want) <= (2.0 ** -8 / 2 + 2.0 ** -8 / 2 * 2.0 ** -7 + 64 * U) * np.abs(want)).all()
