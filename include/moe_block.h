@@ -178,8 +178,8 @@ int moe_block_norm_backward(const moe_block_in* in, const moe_block_grads* grads
  *
  *   w = scale * (code - zero),   code 0 .. 15,
  *
- * with one scale (bf16) and zero (0 .. 15; 8 if there are none) for `group` neighbouring weights of
- * a row, and for every token t
+ * with one scale (bf16, less than 2^116 in size: larger ones become infinite) and zero (0 .. 15; 8
+ * if there are none) for `group` neighbouring weights of a row, and for every token t
  *
  *   h_j  = silu(W_gate[e_j] x_t) * (W_up[e_j] x_t),   e_j = topk_idx[t, j]
  *   y_t  = sum_j topk_gate[t, j] * W_down[e_j] h_j

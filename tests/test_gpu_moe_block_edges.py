@@ -273,3 +273,13 @@ def test_w4_values_from_2_to_the_minus_27_of_a_rows_largest_on_keep_their_bits(T
     x[:, 0], x[:, col] = 2.0 ** 27, small
     y, want = through_one_weight(T, col, x, 1 / 16)
     assert (np.abs(y - want) <= (2.0 ** -8 / 2 + 2.0 ** -8 / 2 * 2.0 ** -7 + 64 * U) * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("T", [1, 20])
+@pytest.mark.parametrize("scale, value", [(2.0 ** 115, 2.0 ** -118), (2.0 ** -126, 2.0 ** 123),
+                                          (2.0 ** -133, 2.0 ** 126)])
+def test_w4_scales_from_the_smallest_to_2_to_the_115(T, scale, value):
+    x = torch.zeros((T, 128), dtype=BF)
+    x[:, 5] = value
+    y, want = through_one_weight(T, 5, x, scale)
+    assert want.all() and (np.abs(y - want) <= (2.0 ** -8 + 64 * U) * np.abs(want)).all()
