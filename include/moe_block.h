@@ -42,8 +42,8 @@ extern "C" {
  * A logit of -inf has the score 0 (NaN counts as -inf).  Where all selected scores are 0 the gates
  * are 0, as are the softmax scores of a row of -inf alone; experts of score 0 are selected, by
  * index, where fewer than k others are left.  A logit of +inf has the sigmoid score 1; it makes
- * the softmax scores of its row NaN.  A bias of -inf or +inf puts an expert last or first; NaN
- * counts as -inf.
+ * the softmax scores of its row NaN.  A bias of -inf or +inf puts an expert last or first, and a
+ * group by the values that it is compared by (of +inf and -inf added: last); NaN counts as -inf.
  *
  * logits [T, E], of type `dtype` (a moe_dtype), their rows ld_logits values apart (>= E; 0: one
  * row that all tokens share); select_bias [E] fp32 or NULL; topk_idx [T, k] int32, topk_gate

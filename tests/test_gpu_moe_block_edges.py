@@ -13,7 +13,8 @@ import torch
 from oracle import moe_block as MB
 from parity_util import f64
 from rounding import Rounded
-from test_gpu_moe_block import BF, F32, SIG, SOFT, U, check_w4, randn, run_select, w4_case, LAST
+from test_gpu_moe_block import (BF, F32, LAST, SIG, SOFT, U, check_w4, randn, run_select,
+                                w4_case)
 from top_routing_grouped_gemm_gb300 import moe
 
 pytestmark = pytest.mark.gpu
@@ -126,6 +127,23 @@ def test_route_select_with_groups_and_infinite_biases(what, size, score, best, k
     want, ref, _ = MB.select(f64(logits), f64(bias), k, score == SIG, groups, kept, best, True, 2.5)
     assert np.array_equal(idx, want)
     assert np.allclose(gate, ref, rtol=64 * U, atol=0)
+
+
+@pytest.mark.parametrize("score", [SIG, SOFT])
+@pytest.mark.parametrize("size", [2, 4])
+def test_route_select_of_groups_of_both_infinities(size, score):
+    """The best two of a group are +inf and -inf: last, whatever else there is."""
+    E, T, k = 4 * size, 9, 2
+    logits = randn(torch.Generator().manual_seed(size), T, E)
+    bias = torch.zeros(E)
+    bias[size:2 * size] = -INF
+    bias[size + 1], bias[0] = INF, -0.5
+    case = (T, E, k, score, 4, 3, 2, True, True, F32)
+    idx, _, _ = run_select(case, logits.cuda(), bias.cuda())
+    without = torch.cat([logits[:, :size], logits[:, size:2 * size] * 0 - 100, logits[:, 2 * size:]], 1)
+    s = torch.sigmoid(without.double()) if score == SIG else torch.softmax(logits.double(), -1)
+    c = s + torch.where(bias.isinf(), -9.0, bias.double())
+    assert np.array_equal(idx, c.sort(-1, descending=True).indices[:, :k].numpy())
 
 
 # ------------------------------------------------------------------------ calls from several threads
