@@ -4,6 +4,7 @@ threads, outputs over inputs, orders and values next to a rounding.
 Tolerances as in test_gpu_moe_block.py."""
 
 import ctypes
+import decimal
 import threading
 
 import numpy as np
@@ -13,7 +14,7 @@ import torch
 from oracle import moe_block as MB
 from parity_util import f64
 from rounding import Rounded
-from test_gpu_moe_block import (BF, F32, LAST, SIG, SOFT, U, check_w4, randn, run_select,
+from test_gpu_moe_block import (BF, CODE, EPS, F32, LAST, SCALE, SIG, SOFT, U, check_w4, randn, run_select,
                                 w4_case)
 from top_routing_grouped_gemm_gb300 import moe
 
@@ -301,3 +302,147 @@ def test_w4_scales_from_the_smallest_to_2_to_the_115(T, scale, value):
     x[:, 5] = value
     y, want = through_one_weight(T, 5, x, scale)
     assert want.all() and (np.abs(y - want) <= (2.0 ** -8 + 64 * U) * np.abs(want)).all()
+
+
+# ------------------------------------------------------------------------ outputs over inputs
+
+# N, D, stream, type; the longest rows are read from memory each time that they are wanted
+IN_PLACE = [(9, 72, F32, F32), (700, 1000, BF, BF), (40, 4096, F32, BF), (30, 6152, BF, BF),
+            (200, 8192, F32, BF), (5, 8200, F32, F32), (400, 8200, F32, BF), (7, 16384, BF, BF)]
+
+
+def in_place_inputs(case, post):
+    N, D, st, dt = case
+    gen = torch.Generator().manual_seed(N + D)
+    x, dz = (randn(gen, N, D).to(st).cuda() for _ in range(2))
+    y, a, dn = (randn(gen, N, D).to(dt).cuda() for _ in range(3))
+    wp, wn = ((1 + 0.2 * randn(gen, D)).cuda() for _ in range(2))
+    return x, y, a, dz, dn, wp if post else None, wn
+
+
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("case", IN_PLACE, ids=str)
+def test_block_norm_over_its_inputs(case, post):
+    """z over x; n over y, and over a gate of each value."""
+    N, D, st, dt = case
+    x, y, a, _, _, wp, wn = in_place_inputs(case, post)
+    head = (N, D, CODE[st], CODE[dt], EPS, SCALE)
+    rest = (moe.MOE_GATE_VALUE, True)
+    z, n = torch.empty_like(x), torch.empty_like(y)
+    moe.moe_block_norm(*head, x, y, *rest, a, post, wp, wn, z, n)
+    for over in ("y", "gate"):
+        x2, y2, a2 = x.clone(), y.clone(), a.clone()
+        n2 = y2 if over == "y" else a2
+        moe.moe_block_norm(*head, x2, y2, *rest, a2, post, wp, wn, x2, n2)
+        assert torch.equal(x2, z) and torch.equal(n2, n), over
+
+
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("case", IN_PLACE, ids=str)
+def test_block_norm_backward_over_its_inputs(case, post):
+    """dx over dz; dy over y, and over dn; a gate's gradient over the gate."""
+    N, D, st, dt = case
+    x, y, a, dz, dn, wp, wn = in_place_inputs(case, post)
+    ws = torch.empty(moe.moe_block_norm_backward_workspace_size(N, D, 3), dtype=torch.uint8, device="cuda")
+
+    def back(y, a, dz, dn, dx, dy, da):
+        dwp, dwn = torch.empty(D, device="cuda") if post else None, torch.empty(D, device="cuda")
+        moe.moe_block_norm_backward(N, D, CODE[st], CODE[dt], EPS, SCALE, x, y, moe.MOE_GATE_VALUE, True, a,
+                                    post, wp, wn, dz, CODE[dt], dn, dx, dy, da, dwp, dwn, ws)
+        return [dx, dy, da, dwn] + [dwp] * post
+
+    want = back(y, a, dz, dn, torch.empty_like(x), torch.empty_like(y), torch.empty_like(a))
+    for over in ("y", "dn"):
+        y2, a2, dz2, dn2 = (t.clone() for t in (y, a, dz, dn))
+        got = back(y2, a2, dz2, dn2, dz2, y2 if over == "y" else dn2, a2)
+        assert all(torch.equal(g, w) for g, w in zip(got, want)), over
+
+
+# ------------------------------------------------------------------------ nearly equal scores
+
+def ulps(l, most, gen):
+    """Logits moved by up to `most` steps of fp32."""
+    step = torch.randint(-most, most + 1, l.shape, generator=gen, dtype=torch.int32)
+    return (l.contiguous().view(torch.int32) + step).view(torch.float32)
+
+
+def near_equal(score, T, E, near, gen):
+    """Logits and a bias: the scores and biases of `near` experts of a row add up to nearly one value, the
+    others' to far less."""
+    value = 0.6 if score == SIG else 1 / 64
+    bias = randn(gen, E) * 0.05 * value
+    order = torch.rand((T, E), generator=gen).argsort(1)
+    s = (value - bias.double()).repeat(T, 1)
+    if score == SIG:
+        l, rest = torch.logit(s), torch.full((T, 1), -1.0, dtype=torch.float64)
+    else:  # shares; the others have what is left, or all of them that much more
+        left = 1 - (s * (order < near)).sum(-1, keepdim=True)
+        s = s + left / E if near == E else s
+        l, rest = s.log(), (left / max(1, E - near)).clamp(min=1e-9).log()
+    return torch.where(order < near, ulps(l.float(), 8, gen), rest.float().expand(T, E)), bias
+
+
+def near_pairs(score, T, groups, size, gen):
+    """Logits: the best two scores of every group have nearly one sum."""
+    a = torch.rand((T, groups), generator=gen).double() - 0.5
+    if score == SIG:
+        b = torch.logit(1.2 - torch.sigmoid(a.float().double()))
+    else:
+        b = torch.log(2.0 - torch.exp(a.float().double()))
+    l = torch.full((T, groups, size), -6.0) - torch.rand((T, groups, size), generator=gen)
+    l[..., 1], l[..., size - 1] = a.float(), ulps(b.float(), 4, gen)
+    return l.view(T, -1)
+
+
+def check_order(l, bias, idx, score, groups, kept, best, k):
+    """Against sums in 40 digits.  What is closer than 2^-40 may be in either order: such rows are left out,
+    and there are few."""
+    D, skipped = decimal.Decimal, 0
+    with decimal.localcontext() as context:
+        context.prec = 40
+        tie = D(2) ** -40
+        for t, row in enumerate(l.tolist()):
+            if score == SIG:
+                c = [1 / (1 + (-D(v)).exp()) for v in row]
+            else:
+                e = [D(v).exp() for v in row]
+                total = sum(e)
+                c = [v / total for v in e]
+            c = c if bias is None else [v + D(b) for v, b in zip(c, bias.tolist())]
+            size = len(row) // groups
+            worth = [sum(sorted(c[g * size:(g + 1) * size])[::-1][:best]) for g in range(groups)]
+            order = sorted(range(groups), key=lambda g: (-worth[g], g))
+            near = kept < groups and worth[order[kept - 1]] - worth[order[kept]] < tie
+            key = row if bias is None else c
+            want = sorted((e for e in range(len(row)) if e // size in order[:kept]), key=lambda e: (-key[e], e))
+            if bias is not None:
+                near |= any(0 < c[a] - c[b] < tie for a, b in zip(want[:k], want[1:k + 1]))
+            if near:
+                skipped += 1
+            else:
+                assert idx[t].tolist() == want[:k], t
+    assert skipped <= len(l) // 8
+
+
+# experts, near ones: all of them, more than a list of 64 holds (of sigmoid scores), fewer
+@pytest.mark.parametrize("E, near", [(64, 64), (512, 200), (512, 40), (300, 50)])
+@pytest.mark.parametrize("groups, kept, best", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
+@pytest.mark.parametrize("score", [SIG, SOFT])
+def test_route_select_of_some_nearly_equal_scores(score, groups, kept, best, E, near):
+    T, k = 24, 8
+    if score == SOFT:
+        near = min(near, 50) if E > 64 else near
+    case = (T, E, k, score, groups, kept, best, True, True, F32)
+    l, bias = near_equal(score, T, E, near, torch.Generator().manual_seed(E + near))
+    idx, _, _ = run_select(case, l.cuda(), bias.cuda())
+    check_order(l, bias, idx, score, groups, kept, best, k)
+
+
+@pytest.mark.parametrize("groups, size, kept", [(16, 4, 5), (8, 5, 3), (30, 32, 11), (32, 4, 31)])
+@pytest.mark.parametrize("score", [SIG, SOFT])
+def test_route_select_of_groups_whose_best_two_add_up_to_nearly_the_same(score, groups, size, kept):
+    T, k = 24, 5
+    case = (T, groups * size, k, score, groups, kept, 2, True, False, F32)
+    l = near_pairs(score, T, groups, size, torch.Generator().manual_seed(groups))
+    idx, _, _ = run_select(case, l.cuda(), None)
+    check_order(l, None, idx, score, groups, kept, 2, k)
