@@ -217,6 +217,14 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
                       const moe_w4* w_down, moe_bf16* y, void* workspace,
                       size_t workspace_bytes, int32_t* dev_status, moe_stream_t stream);
 
+/* Self-test of the waits for copies of weights, which give up after 2 s.  After it, launches of
+ * moe_w4_expert_ffn by the calling thread (group 32, no zeros; else MOE_ERR_UNSUPPORTED) wait
+ * limit_ms (1..2000) at most, and copy `copy` of warp `warp` of block `block` of the product with
+ * w_gate and w_up (down 0) or w_down (1) never arrives whole.  Such a launch ends on its own, reports
+ * MOE_ERR_TIMEOUT where there is such a copy, and leaves y undefined.  limit_ms = 0 ends the
+ * self-test. */
+int moe_selftest_w4_waits(int32_t limit_ms, int32_t down, int32_t block, int32_t warp, int32_t copy);
+
 #ifdef __cplusplus
 }
 #endif

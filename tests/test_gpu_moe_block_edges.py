@@ -446,3 +446,53 @@ def test_route_select_of_groups_whose_best_two_add_up_to_nearly_the_same(score, 
     l = near_pairs(score, T, groups, size, torch.Generator().manual_seed(groups))
     idx, _, _ = run_select(case, l.cuda(), None)
     check_order(l, None, idx, score, groups, kept, 2, k)
+
+
+# ------------------------------------------------------------------------ 4-bit experts: waits that run out
+
+@pytest.fixture
+def impatient():
+    """Ends the self-test of the waits whatever the test does."""
+    yield
+    moe.moe_selftest_w4_waits(0)
+
+
+# in one strip of a team and in several, by one warp of a team and by all, with pieces at a row's end
+@pytest.mark.parametrize("case", [(1, 2048, 5, 4, 1152, 32, False, None), (1, 64, 2, 1, 64, 32, False, None),
+                                  (1, 2560, 3, 3, 320, 32, False, None), (3, 1152, 4, 2, 2048, 32, False, None),
+                                  (40, 512, 8, 4, 640, 32, False, None)], ids=str)
+def test_w4_copies_that_never_arrive_end_by_themselves_and_harm_nobody(case, impatient):
+    """One copy of one warp is missing, early and late, in each product.  The launch ends and says so; what
+    runs beside it and after it has its bits."""
+    w, x, idx, gate = w4_case(case)
+    p = moe.Problem(*case[:5])
+    packed = [moe.W4Weights(m[0].cuda(), m[1].cuda()) for m in w]
+    x, idx, gate = x.cuda(), idx.cuda(), gate.cuda()
+    status, o_status = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
+    y, o_y = (torch.empty(case[:2], dtype=BF, device="cuda") for _ in range(2))
+    ws, o_ws = (torch.empty(moe.moe_w4_expert_ffn_workspace_size(p), dtype=torch.uint8, device="cuda")
+                for _ in range(2))
+    call = lambda: moe.moe_w4_expert_ffn(p, x, idx, gate, *packed, y, ws, status)  # noqa: E731
+    other = lambda: moe.moe_w4_expert_ffn(p, x, idx, gate, *packed, o_y, o_ws, o_status)  # noqa: E731
+    call()
+    want = y.clone()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for down in (False, True):
+        gave_up = 0
+        for block, warp, copy in [(0, 0, 0), (1, 0, 0), (0, 3, 0), (2, 7, 1), (0, 0, 2), (3, 1, 3), (0, 1, 5)]:
+            status.zero_()
+            torch.cuda.synchronize()
+            moe.moe_selftest_w4_waits(4, down, block, warp, copy)
+            call()
+            moe.moe_selftest_w4_waits(0)
+            with torch.cuda.stream(side):
+                other()
+            torch.cuda.synchronize()
+            assert int(status) in (0, 5) and int(o_status) == 0  # MOE_ERR_TIMEOUT where there is such a copy
+            gave_up += int(status) == 5
+            assert torch.equal(o_y, want) and (int(status) == 5 or torch.equal(y, want))
+        assert gave_up > 0, down
+    status.zero_()
+    call()
+    assert torch.equal(y, want) and int(status) == 0

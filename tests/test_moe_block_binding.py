@@ -44,3 +44,19 @@ def test_weights_whose_arrays_are_replaced_are_what_the_library_reads():
         assert [getattr(read, n) for n, _ in read._fields_] == [w.codes.data_ptr(), w.scales.data_ptr(), 32, 1]
         w.codes, w.scales = w.codes.clone(), w.scales.clone()
     assert ctypes.sizeof(moe.moe_w4) == moe._W4.size
+
+
+def test_selftest_of_the_4_bit_experts_waits_refuses():
+    lib = moe.lib()
+    for args in ((2001, 0, 0, 0, 0), (-1, 0, 0, 0, 0), (5, 0, -1, 0, 0), (5, 0, 0, -1, 0), (5, 1, 0, 0, -1)):
+        assert lib.moe_selftest_w4_waits(*args) == 1
+    p = moe.Problem(T=4, d=64, E=4, k=2, F=64)
+    try:
+        moe.moe_selftest_w4_waits(5)
+        for group, zeros in ((64, 0), (32, 1)):  # (addresses that nothing reads)
+            w4 = moe.moe_w4(0x10000, 0x10000, group, zeros)
+            m = ctypes.addressof(w4)
+            assert lib.moe_w4_expert_ffn(p.c(), *[0x10000] * 3, m, m, m, 0x10000, 0x10000, 1 << 40, None,
+                                         None) == 2
+    finally:
+        moe.moe_selftest_w4_waits(0)

@@ -44,6 +44,7 @@ constexpr int kChunk = 8;
 constexpr int kXParts = 1, kHParts = 2;  // fp16 values for one of x, of h
 constexpr int kWarps = 8, kMaxWarps = 16;  // to a block
 constexpr int kSharedPerSm = 228 * 1024, kSharedPerBlock = 227 * 1024;
+constexpr int kDrillGroup = 32;  // of the weights (without zeros) that the waits are tested with
 
 // ---------------------------------------------------------------- layout
 // A tile of 16 rows x 64 columns takes 512 bytes, 16 to a lane: lane 4 g + t holds rows g and g + 8,
@@ -440,16 +441,24 @@ __device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
                : "memory");
 }
 
-// Whether the barrier's phase completed, for the whole warp; gives up after kWaitTimeoutNs.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+// Whether the barrier's phase completed, for the whole warp; gives up after a limit.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   bool ok = mbar_try_wait(bar, parity);
   if (!ok) {
     const uint64_t t0 = globaltimer_ns();
-    while (!(ok = mbar_try_wait(bar, parity)) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
+    while (!(ok = mbar_try_wait(bar, parity)) && globaltimer_ns() - t0 < limit_ns) {
     }
   }
   return __all_sync(~0u, ok);
 }
+
+// Self-test of those waits, of launches by the thread that asks for it: they wait this long at most, and
+// one copy of one warp is expected to be longer than it is, so that its wait runs out.
+struct Drill {
+  uint64_t limit_ns;  // 0: none
+  int block, warp, copy;
+};
+thread_local Drill drill_of_gateup, drill_of_down;
 
 struct Weights {
   const void* codes;
@@ -463,6 +472,7 @@ struct Problem {
   Weights w[2];
   int rows, cols, split;
   int* dev_status;
+  Drill drill;
 };
 
 // The tasks of a team of warps, one after the other: task i is strip i % strips of chunk i / strips.
@@ -481,9 +491,9 @@ struct Tasks {
 // Gate and up take x, whose rows have one factor, and a strip of each.  DOWN takes h, which has a
 // factor for each tile, and one strip or two neighbouring ones (which share the loads of h and wait for
 // them half as often: 32 tokens, 2048 x 512: 170 -> 158 us).  ONE: a single token, whose values come
-// with the weights' pieces and stand in all columns.  (Read from the L2 by each lane, a tile ahead, they
+// with the weights' pieces and stand in all columns.  DRILL: the waits' self-test.  (Read from the L2 by each lane, a tile ahead, they
 // were what down waited for: 34 -> 30 us.)
-template <bool DOWN, int MATS, bool ZEROS, int GROUP, bool ONE = false>
+template <bool DOWN, int MATS, bool ZEROS, int GROUP, bool ONE = false, bool DRILL = false>
 struct Product {
   static constexpr bool kFactors = DOWN, FINE = GROUP == 32;
   static constexpr int PARTS = DOWN ? kHParts : kXParts;
@@ -513,6 +523,7 @@ struct Product {
     uint32_t ring, bars;
     int tiles, place;  // tiles: of a strip
     uint64_t policy;
+    int copies = 0;  // (DRILL)
 
     __device__ __forceinline__ Copies(const Problem& p_, uint8_t* ring_, uint64_t* bars_)
         : p(p_), ring(smem_u32(ring_)), bars(smem_u32(bars_)), tiles(p_.cols / kTile), place(0),
@@ -523,8 +534,12 @@ struct Product {
       const uint32_t to = ring + place * (MATS * kPlace), bar = bars + place * 8;
       const uint32_t bytes = n * 512, of = of_scales(n);
       const uint32_t parts = n * (PARTS * kTile * 2), info = n * 16;
+      uint32_t more = 0;
+      if (DRILL && blockIdx.x == p.drill.block && threadIdx.x / 32 == p.drill.warp &&
+          copies++ == p.drill.copy)
+        more = 16;
       if (one_lane()) {
-        expect(bar, MATS * (bytes + of) + (ONE ? parts + info : 0));
+        expect(bar, MATS * (bytes + of) + (ONE ? parts + info : 0) + more);
         if (ONE) {
           bulk_load(to + kValues, values, parts, bar, policy);
           bulk_load(to + kInfo, infos, info, bar, policy);
@@ -799,7 +814,7 @@ struct Product {
       for (int left = tiles - me * kPieceTiles; left > 0 && ok; left -= split * kPieceTiles) {
         Values now;
         now.load(x, 0);
-        if (!wait_for(bars + place, parity)) {
+        if (!wait_for(bars + place, parity, limit(p))) {
           ok = false;
           break;
         }
@@ -859,7 +874,7 @@ struct Product {
     for (int strip = blockIdx.x; strip < strips; strip += gridDim.x) {
       float acc[1][4] = {};
       for (Pieces at = start; at.left() && ok; at.next()) {
-        if (!wait_for(bars + place, parity)) {
+        if (!wait_for(bars + place, parity, limit(p))) {
           ok = false;
           break;
         }
@@ -887,13 +902,16 @@ struct Product {
     drain(p, ok, ahead.place, bars, place, parity);
   }
 
+  static __device__ __forceinline__ uint64_t limit(const Problem& p) {
+    return DRILL ? p.drill.limit_ns : kWaitTimeoutNs;
+  }
   // After a wait that ran out: what is on its way arrives before the block's memory is given up.
   static __device__ __forceinline__ void drain(const Problem& p, bool ok, int issued,
                                                uint64_t* bars, int place, uint32_t parity) {
     if (ok) return;
     if ((threadIdx.x & 31) == 0) report_status(p.dev_status, MOE_ERR_TIMEOUT);
     while (place != issued) {
-      wait_for(bars + place, parity);
+      wait_for(bars + place, parity, limit(p));
       if (++place == kPlaces) place = 0, parity ^= 1;
     }
   }
@@ -909,10 +927,10 @@ struct GateUp {
 };
 
 // h goes to memory in fp32; the warp that brings the last of a tile's four strips makes operands of it.
-template <bool ZEROS, int GROUP>
+template <bool ZEROS, int GROUP, bool DRILL>
 __global__ void __launch_bounds__(kWarps * 32, Product<false, 2, ZEROS, GROUP>::kBlocks)
     w4_gateup_kernel(const GateUp a) {
-  using Of = Product<false, 2, ZEROS, GROUP>;
+  using Of = Product<false, 2, ZEROS, GROUP, false, DRILL>;
   extern __shared__ __align__(16) uint8_t shared[];
   const int F = a.p.rows, lane = threadIdx.x & 31;
   Of::run(
@@ -963,9 +981,9 @@ struct Down {
 };
 
 // A single token: y at once.
-template <bool ZEROS, int GROUP>
+template <bool ZEROS, int GROUP, bool DRILL>
 __global__ void __launch_bounds__(kMaxWarps * 32) w4_down_kernel(const Down a) {
-  using Of = Product<true, 1, ZEROS, GROUP, true>;
+  using Of = Product<true, 1, ZEROS, GROUP, true, DRILL>;
   extern __shared__ __align__(16) uint8_t shared[];
   Of::run_strips(a.p, a.h, shared, [&](int strip, int row, float sum) {
     a.y[strip * kStrip + row] = __float2bfloat16_rn(sum);
@@ -973,12 +991,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32) w4_down_kernel(const Down a) {
 }
 
 // More tokens: the rows' parts of it, which w4_combine_kernel adds.
-template <bool ZEROS, int GROUP>
+template <bool ZEROS, int GROUP, bool DRILL>
 __global__ void __launch_bounds__(kWarps * 32, Product<true, 2, ZEROS, GROUP>::kBlocks)
     w4_down_rows_kernel(const Down a) {
   extern __shared__ __align__(16) uint8_t shared[];
   const int d = a.p.rows, lane = threadIdx.x & 31;
-  Product<true, 2, ZEROS, GROUP>::run(
+  Product<true, 2, ZEROS, GROUP, false, DRILL>::run(
       a.p, a.h, shared, [&](int r) { return r; },
       [&](int, int first, int rows, int strip, const float (&acc)[2][4]) {
 #pragma unroll
@@ -1156,9 +1174,12 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
   Groups g = ws.g;
   g.idx = topk_idx, g.gate = topk_gate, g.slots = slots, g.E = p->E, g.single = p->T == 1;
   const int chunks = std::max(std::min(p->E, slots), slots / kChunk);  // about
-  GateUp up{{g, {of(w_gate), of(w_up)}, p->F, p->d, 1, dev_status}, ws.x, ws.h, ws.parts,
+  const Drill drill_up = drill_of_gateup, drill_down = drill_of_down;
+  const bool drill = drill_up.limit_ns || drill_down.limit_ns;
+  if (drill && (zeros || w_gate->group != kDrillGroup)) return MOE_ERR_UNSUPPORTED;
+  GateUp up{{g, {of(w_gate), of(w_up)}, p->F, p->d, 1, dev_status, drill_up}, ws.x, ws.h, ws.parts,
             ws.counters, p->k};
-  Down down{{g, {of(w_down), {}}, p->d, p->F, 1, dev_status}, ws.parts, ws.out,
+  Down down{{g, {of(w_down), {}}, p->d, p->F, 1, dev_status, drill_down}, ws.parts, ws.out,
             reinterpret_cast<__nv_bfloat16*>(y)};
   cudaError_t err = cudaSuccess;
   // (The limit is the kernel's, for all threads of the process: the most that any call wants, so that
@@ -1188,20 +1209,20 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
                           reinterpret_cast<const __nv_bfloat16*>(x), p->T, ws.x, ws.counters,
                           ws.n_counters, g, warps, dev_status);
   }
-  const auto with = [&](auto z, auto of_group) {
-    constexpr bool Z = decltype(z)::value;
+  const auto with = [&](auto z, auto of_group, auto drilled) {
+    constexpr bool Z = decltype(z)::value, DRILL = decltype(drilled)::value;
     constexpr int GROUP = decltype(of_group)::value;
-    by_strips(w4_gateup_kernel<Z, GROUP>, Product<false, 2, Z, GROUP>{}, up);
+    by_strips(w4_gateup_kernel<Z, GROUP, DRILL>, Product<false, 2, Z, GROUP>{}, up);
     mark_after(MOE_KERNEL_W4_GATEUP, stream);
     mark_before(MOE_KERNEL_W4_DOWN, stream);
     if (g.single) {
       using Of = Product<true, 1, Z, GROUP, true>;
       constexpr int kMost = std::min(kMaxWarps, kSharedPerBlock / Of::kWarpBytes);
       const int strips = p->d / kStrip, warps = strips > kSms ? kWarps : kMost;
-      launch(w4_down_kernel<Z, GROUP>, std::min(strips, 2 * kSms * kWarps / warps), warps,
+      launch(w4_down_kernel<Z, GROUP, DRILL>, std::min(strips, 2 * kSms * kWarps / warps), warps,
              warps * Of::kWarpBytes, kMost * Of::kWarpBytes, down);
     } else {
-      by_strips(w4_down_rows_kernel<Z, GROUP>, Product<true, 2, Z, GROUP>{}, down);
+      by_strips(w4_down_rows_kernel<Z, GROUP, DRILL>, Product<true, 2, Z, GROUP>{}, down);
     }
     if (!g.single && err == cudaSuccess)
       err = launch_behind(w4_combine_kernel, dim3(p->T, std::min(64, (p->d + 511) / 512)), 128, 0,
@@ -1209,19 +1230,32 @@ int moe_w4_expert_ffn(const moe_problem* p, const moe_bf16* x, const int32_t* to
   };
   const auto with_group = [&](auto z) {
     if (w_gate->group == 32)
-      with(z, std::integral_constant<int, 32>{});
+      with(z, std::integral_constant<int, 32>{}, std::false_type{});
     else if (w_gate->group == 64)
-      with(z, std::integral_constant<int, 64>{});
+      with(z, std::integral_constant<int, 64>{}, std::false_type{});
     else
-      with(z, std::integral_constant<int, 128>{});
+      with(z, std::integral_constant<int, 128>{}, std::false_type{});
   };
-  if (zeros)
+  if (drill)
+    with(std::false_type{}, std::integral_constant<int, kDrillGroup>{}, std::true_type{});
+  else if (zeros)
     with_group(std::true_type{});
   else
     with_group(std::false_type{});
   mark_after(MOE_KERNEL_W4_DOWN, stream);
   count_launches(3 + !g.single);
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int moe_selftest_w4_waits(int32_t limit_ms, int32_t down, int32_t block, int32_t warp, int32_t copy) {
+  if (limit_ms < 0 || limit_ms > 2000 || (limit_ms && (block < 0 || warp < 0 || copy < 0)))
+    return MOE_ERR_INVALID_ARG;
+  drill_of_gateup = drill_of_down = Drill{};
+  if (!limit_ms) return MOE_OK;
+  const uint64_t limit_ns = limit_ms * 1000000ull;
+  drill_of_gateup = {limit_ns, down ? -1 : block, warp, copy};
+  drill_of_down = {limit_ns, down ? block : -1, warp, copy};
+  return MOE_OK;
 }
 
 }  // extern "C"

@@ -187,6 +187,7 @@ _SIGS = {
     "moe_launch_count": (ctypes.c_longlong, []),
     "moe_selftest_wait_timeout": (ctypes.c_int, [c_vp, c_i32, c_vp]),
     "moe_selftest_recurrence_waits": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32]),
+    "moe_selftest_w4_waits": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32, c_i32]),
 }
 
 KERNEL_IDS = {"router_gemm": 0, "topk": 1, "dispatch": 2, "gateup_gemm": 3, "down_gemm": 4,
@@ -980,6 +981,12 @@ def moe_selftest_recurrence_waits(limit_ms, rank=0, warp=0, step=0):
     """Launches of the recurrence's scans by this thread give up by themselves (0: no longer)."""
     _check("moe_selftest_recurrence_waits",
            lib().moe_selftest_recurrence_waits(limit_ms, rank, warp, step))
+
+
+def moe_selftest_w4_waits(limit_ms, down=False, block=0, warp=0, copy=0):
+    """Calls of moe_w4_expert_ffn by this thread lose a copy and give up by themselves (0: no longer)."""
+    _check("moe_selftest_w4_waits",
+           lib().moe_selftest_w4_waits(limit_ms, 1 if down else 0, block, warp, copy))
 
 
 # ----------------------------------------------------------------------------- layer helpers
