@@ -930,11 +930,18 @@ class W4Weights:
                     self.scales, stream)
         self.has_zeros = zeros is not None
 
+    _packed = None, None, None  # arrays, and a moe_w4 of their addresses
+
     def c(self, name, shape, dev):
         if (self.E, self.rows, self.cols) != shape or self.codes.get_device() != dev:
             raise ValueError(f"{name}: weights {shape} on the current device are wanted, got "
                              f"{(self.E, self.rows, self.cols)} on {self.codes.device}")
-        return _W4.pack(self.codes.data_ptr(), self.scales.data_ptr(), self.group, self.has_zeros)
+        codes, scales, packed = self._packed
+        if codes is not self.codes or scales is not self.scales:  # (others were put in their place)
+            codes, scales = self.codes, self.scales
+            packed = _W4.pack(codes.data_ptr(), scales.data_ptr(), self.group, self.has_zeros)
+            self._packed = codes, scales, packed
+        return packed
 
 
 def moe_w4_expert_ffn_workspace_size(p: Problem) -> int:
