@@ -13,8 +13,8 @@
 // are turned into others first on this GPU: 108 instructions.)
 //
 // Now it is 56 for gate and up, 80 for down, whose operand has two parts.  One token through 16 of 896
-// experts of 4096 x 1024 takes 30 us (104 MB, 15 us of reading), 64 tokens that crowd on few experts
-// 498 us (358), 32 tokens through experts of 2048 x 512 with zeros 158 us (97): warps are issuing half of
+// experts of 4096 x 1024 takes 31.5 us (104 MB, 15 us of reading), 64 tokens that crowd on few experts
+// 500 us (358), 32 tokens through experts of 2048 x 512 with zeros 157 us (97): warps are issuing half of
 // the time, in turn with what they wait for.
 #include <cuda_fp16.h>
 #include <math.h>
