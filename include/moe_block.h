@@ -195,9 +195,9 @@ int moe_block_norm_backward(const moe_block_in* in, const moe_block_grads* grads
  * here; a matrix of up to 2^40 weights), T * k up to 16384; group 32, 64 or 128, a divisor of d and
  * of F; group and has_zeros the same for all three; packed arrays, x, y and the workspace 16-byte aligned.
  * An expert's weights are read and converted for every 8 of its rows.  Up to about 20 rows to an
- * expert that takes less time than moe_dispatch, moe_expert_ffn and moe_combine with weights in bf16 (8
- * of 64 experts, 4096 x 1024: 64 tokens 141 us and 293, 256 tokens 379 and 306, 2048 tokens 2689 and 506); beyond, what it
- * saves is memory.
+ * expert that takes less time than moe_dispatch, moe_expert_ffn and moe_combine with weights in
+ * bf16 (8 of 64 experts, 4096 x 1024: 64 tokens 141 us and 293, 256 tokens 379 and 306, 2048 tokens
+ * 2689 and 506); beyond, what it saves is memory.
  *
  * moe_w4_pack lays weights [E, rows, cols] out for it, once (cols: what a product sums over).
  * codes [E, rows, cols / 2]: two codes to a byte, the lower four bits first; scales
